@@ -11,7 +11,10 @@ include/mslkb.h).  This module only marshals arguments:
 
 * ``mslkb_*`` functions mirror the C entry points one to one (raw integer pointers);
 * ``f8f8bf16_rowwise_grouped_stacked`` / ``..._dynamic`` take torch CUDA tensors and
-  call the same entry points on the current stream.
+  call the same entry points on the current stream;
+* ``moe`` holds both forms of the operators around the product in a mixture-of-experts
+  block (norm with an e4m3 output, expert routing, dispatch and combine, SwiGLU with an
+  e4m3 output and checkpoint, and their gradients), re-exported here.
 
 There is no fallback: if libmslkb.so is missing or cannot be loaded, every call raises.
 """
@@ -27,6 +30,8 @@ CHECKED_LIB_PATH = os.path.join(_PKG, "libmslkb_checked.so")
 
 MSLKB_OK, MSLKB_ERR_NULL, MSLKB_ERR_SHAPE, MSLKB_ERR_ALIGN, MSLKB_ERR_DEVICE, MSLKB_ERR_CUDA = range(6)
 MSLKB_ERR_TOO_LARGE = 6
+MSLKB_ERR_DTYPE = 7
+MSLKB_ERR_WORKSPACE = 8
 NOALLOC_SCRATCH_BYTES = 8 << 20
 MSLKB_DEV_TIMEOUT = 0x1
 MSLKB_DEV_MSIZES_CLAMPED = 0x2
@@ -128,7 +133,8 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.mslkb_workspace_count.restype = ctypes.c_int32
     L.mslkb_version.argtypes = []
     L.mslkb_version.restype = ctypes.c_int32
-    return L
+    from . import moe
+    return moe.declare(L)
 
 
 def lib() -> ctypes.CDLL:
@@ -632,3 +638,14 @@ def f8f8bf16_groupwise_grouped_batched(XQ, WQ, x_scale, w_scale, out=None, strea
 def device_status(stream=None) -> int:
     """Read and clear the device status word (MSLKB_DEV_* bits)."""
     return mslkb_get_device_status(_stream_ptr(stream))
+
+
+from .moe import (  # noqa: E402 - needs the definitions above
+    Dispatch, NormQuant, Routing, SwigluQuant,
+    add_rms_norm_quant, add_rms_norm_quant_backward, moe_combine, moe_combine_backward,
+    moe_dispatch, mslkb_add_rms_norm_quant, mslkb_add_rms_norm_quant_backward,
+    mslkb_add_rms_norm_quant_backward_workspace_bytes, mslkb_moe_combine,
+    mslkb_moe_combine_backward, mslkb_moe_dispatch, mslkb_moe_dispatch_workspace_bytes,
+    mslkb_route_experts, mslkb_route_experts_backward, mslkb_swiglu_quant,
+    mslkb_swiglu_quant_backward, route_experts, route_experts_backward, swiglu_quant,
+    swiglu_quant_backward)

@@ -32,7 +32,8 @@ BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmslkb_checked.so")
 SOURCES = ["mslkb.cu", "mslkb_noalloc.cu", "variants_stacked_tma.cu",
            "variants_dynamic_tma.cu", "variants_cpasync.cu", "variants_ragged_n.cu",
-           "variants_ragged_k.cu", "variants_blockscale.cu", "variants_blockscale_dynamic.cu"]
+           "variants_ragged_k.cu", "variants_blockscale.cu", "variants_blockscale_dynamic.cu",
+           "norm_quant.cu", "route.cu", "dispatch.cu", "swiglu_quant.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,58 @@
+// host.h -- internal: what the entry points outside mslkb.cu share on the host side (device
+// set-up, error record, profiler ranges, launches with programmatic dependence).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mslkb.h"
+
+namespace mslkb {
+
+// Defined in mslkb.cu.
+void record_cuda_error(cudaError_t e);
+
+// Checks the current device (MSLKB_ERR_DEVICE unless sm_103) and returns its SM count.
+mslkb_status device_sms(int* sm_count);
+
+// NVTX push/pop range of the domain "mslkb" around a launch: `name` and the call's rows.
+struct TraceRange {
+  TraceRange(const char* name, int64_t rows);
+  ~TraceRange();
+};
+
+inline mslkb_status launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return MSLKB_OK;
+  record_cuda_error(e);
+  return MSLKB_ERR_CUDA;
+}
+
+// Launches `kernel` with programmatic dependent launch: it may start while the stream's
+// previous kernel ends, and waits (griddepcontrol.wait) before its first global access.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                             void* stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+inline bool aligned_to(const void* p, size_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
+
+inline int dtype_bytes(int32_t dtype) { return dtype == MSLKB_FP32 ? 4 : 2; }
+inline bool dtype_ok(int32_t dtype) {
+  return dtype == MSLKB_BF16 || dtype == MSLKB_FP16 || dtype == MSLKB_FP32;
+}
+
+}  // namespace mslkb

@@ -18,6 +18,7 @@
 #include <mutex>
 #include <utility>
 
+#include "host.h"
 #include "launch.h"
 #include "mslkb.h"
 #include "mslkb_tuning.h"
@@ -101,12 +102,16 @@ nvtxDomainHandle_t g_nvtx_domain = nullptr;
 nvtxStringHandle_t g_nvtx_names[kMaxTracedVariants] = {};
 std::once_flag g_nvtx_once;
 
-cudaError_t launch_traced(int vi, const LaunchArgs& la, int64_t rows) {
+void nvtx_init() {
   std::call_once(g_nvtx_once, [] {
     g_nvtx_domain = nvtxDomainCreateA("mslkb");
     for (int i = 0; i < num_variants() && i < kMaxTracedVariants; ++i)
       g_nvtx_names[i] = nvtxDomainRegisterStringA(g_nvtx_domain, variant(i)->name);
   });
+}
+
+cudaError_t launch_traced(int vi, const LaunchArgs& la, int64_t rows) {
+  nvtx_init();
   nvtxEventAttributes_t a = {};
   a.version = NVTX_VERSION;
   a.size = NVTX_EVENT_ATTRIB_STRUCT_SIZE;
@@ -792,6 +797,27 @@ mslkb_status run_stacked_with_scratch(const void* A, const void* B, const float*
 
 void record_cuda_error(cudaError_t e) { t_last_cuda_error = static_cast<int>(e); }
 
+mslkb_status device_sms(int* sm_count) {
+  DeviceState* st = nullptr;
+  const mslkb_status s = device_state(&st);
+  if (s == MSLKB_OK) *sm_count = st->sm_count;
+  return s;
+}
+
+TraceRange::TraceRange(const char* name, int64_t rows) {
+  nvtx_init();
+  nvtxEventAttributes_t a = {};
+  a.version = NVTX_VERSION;
+  a.size = NVTX_EVENT_ATTRIB_STRUCT_SIZE;
+  a.messageType = NVTX_MESSAGE_TYPE_ASCII;
+  a.message.ascii = name;
+  a.payloadType = NVTX_PAYLOAD_TYPE_INT64;
+  a.payload.llValue = rows;
+  nvtxDomainRangePushEx(g_nvtx_domain, &a);
+}
+
+TraceRange::~TraceRange() { nvtxDomainRangePop(g_nvtx_domain); }
+
 }  // namespace mslkb
 
 extern "C" {
@@ -915,6 +941,8 @@ const char* mslkb_status_string(mslkb_status status) {
     case MSLKB_ERR_TOO_LARGE:
       return "the problem needs more split-tile scratch than the allocation-free entry "
              "point holds (MSLKB_NOALLOC_SCRATCH_BYTES)";
+    case MSLKB_ERR_DTYPE: return "an element type that the call does not take";
+    case MSLKB_ERR_WORKSPACE: return "the workspace is NULL, misaligned or too small";
   }
   return "unknown status";
 }

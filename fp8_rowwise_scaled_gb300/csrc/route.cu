@@ -1,0 +1,379 @@
+// route.cu -- the choice of each token's experts from the router's logits, and its gradient.
+//
+// One warp per token.  A lane holds kPer consecutive experts in registers, as integer keys
+// that order like their choice values (0: masked), so that the largest key of the warp is
+// one redux instruction and ties fall to the lowest lane, then to its lowest expert: the
+// lowest expert index.
+#include "host.h"
+#include "rows.cuh"
+
+namespace mslkb {
+namespace {
+
+constexpr int kWarps = 4;  // tokens per CTA
+constexpr float kMasked = -__builtin_huge_valf();
+
+struct RouteParams {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int64_t T, ld;
+  int32_t E, top_k;
+  int32_t sigmoid;
+  int32_t groups, top_groups, group_top;
+  int32_t by_logits;  // softmax whose order is that of the logits
+  int32_t renormalize;
+  float scale;
+};
+
+// An integer that orders as the float does: NaN above all, -inf (masked) 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  if (v == kMasked) return 0;
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 orders as +0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (k == 0) return kMasked;
+  if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+__device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
+
+// What a group is worth: its best choice, and with group_top = 2 the second as well.
+__device__ __forceinline__ uint32_t worth_key(uint32_t best, uint32_t second, int group_top) {
+  if (group_top == 1 || second == 0) return best;
+  return order_key(key_value(best) + key_value(second));
+}
+
+template <class T, int kPer>
+__global__ void __launch_bounds__(kWarps * 32)
+    route_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ uint32_t shared_keys[];  // [kWarps][E], groups that lanes do not hold whole
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (t >= p.T) return;
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  const int first = lane * kPer;
+
+  float x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    x[i] = first + i < p.E ? to_float(row[first + i]) : kMasked;
+
+  // softmax over all experts: its maximum and sum
+  float top = 0.f, total = 1.f;
+  if (!p.sigmoid && !(p.by_logits && p.renormalize)) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (first + i < p.E) s += expf(x[i] - m);  // a NaN logit makes the sum NaN
+    top = m;
+    total = warp_sum(s);
+  }
+
+  uint32_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    float c = x[i];
+    if (!p.by_logits && c != kMasked) {
+      c = p.sigmoid ? sigmoid_of(c) : expf(c - top) / total;
+      if (p.bias != nullptr) c += p.bias[first + i];
+    }
+    key[i] = order_key(c);
+  }
+
+  if (p.groups > 1) {
+    const int per = p.E / p.groups;
+    const int lanes = per / kPer;  // lanes of a group, where a group is whole lanes
+    if (per % kPer == 0 && (lanes & (lanes - 1)) == 0) {
+      uint32_t best = 0, second = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        second = max(second, min(best, key[i]));
+        best = max(best, key[i]);
+      }
+      for (int d = 1; d < lanes; d <<= 1) {
+        const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+        const uint32_t s = __shfl_xor_sync(0xFFFFFFFFu, second, d);
+        second = max(max(second, s), min(best, b));
+        best = max(best, b);
+      }
+      const uint32_t mine = worth_key(best, second, p.group_top);
+      const int group = lane / lanes;
+      int better = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, g * lanes);
+        better += other > mine || (other == mine && g < group);
+      }
+      if (better >= p.top_groups) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) key[i] = 0;
+      }
+    } else {
+      uint32_t* keys = shared_keys + warp * p.E;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (first + i < p.E) keys[first + i] = key[i];
+      __syncwarp();
+      uint32_t best = 0, second = 0;
+      if (lane < p.groups) {
+        for (int i = 0; i < per; ++i) {
+          const uint32_t k = keys[lane * per + i];
+          second = max(second, min(best, k));
+          best = max(best, k);
+        }
+      }
+      const uint32_t mine = worth_key(best, second, p.group_top);
+      int better = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, g);
+        better += other > mine || (other == mine && g < lane);
+      }
+      const uint32_t kept = __ballot_sync(0xFFFFFFFFu, better < p.top_groups);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (first + i < p.E && !((kept >> ((first + i) / per)) & 1u)) key[i] = 0;
+    }
+  }
+
+  // the best key of the lane, and where it is
+  uint32_t best = key[0];
+  int at = 0;
+#pragma unroll
+  for (int i = 1; i < kPer; ++i)
+    if (key[i] > best) best = key[i], at = i;
+  int id = -1;  // lane j: the j-th choice
+  for (int j = 0; j < p.top_k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (m == 0) break;
+    const int winner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+    const int chosen = __shfl_sync(0xFFFFFFFFu, first + at, winner);
+    if (lane == j) id = chosen;
+    if (lane == winner) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == at) key[i] = 0;
+      best = key[0];
+      at = 0;
+#pragma unroll
+      for (int i = 1; i < kPer; ++i)
+        if (key[i] > best) best = key[i], at = i;
+    }
+  }
+
+  // weights, one choice per lane (the logit is read again: an L1 hit)
+  const float logit = id >= 0 ? to_float(row[id]) : kMasked;
+  float w = 0.f;
+  if (p.sigmoid) {
+    if (id >= 0) w = sigmoid_of(logit);
+    if (p.renormalize) w /= warp_sum(w) + 1e-20f;
+  } else if (p.renormalize) {
+    float m = logit;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (id >= 0) w = expf(logit - m);
+    w /= warp_sum(w);
+  } else if (id >= 0) {
+    w = expf(logit - top) / total;
+  }
+  if (lane < p.top_k) {
+    p.ids[t * p.top_k + lane] = id;
+    p.weights[t * p.top_k + lane] = id >= 0 ? w * p.scale : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------------
+struct RouteBackwardParams {
+  const float* dweights;
+  const void* logits;
+  const int32_t* ids;
+  void* dlogits;
+  int64_t T, ld;
+  int32_t E, top_k;
+  int32_t sigmoid;
+  int32_t renormalize;
+  float scale;
+};
+
+// One warp per token; the row of gradients is built in shared memory (zeros, or the full
+// softmax's part), the chosen experts' parts are added, and it leaves in one coalesced pass.
+template <class T>
+__global__ void __launch_bounds__(kWarps * 32)
+    route_backward_kernel(const __grid_constant__ RouteBackwardParams p) {
+  extern __shared__ float grads[];  // [kWarps][E]
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (t >= p.T) return;
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  float* d = grads + warp * p.E;
+
+  int id = -1;
+  float g = 0.f;
+  if (lane < p.top_k) {
+    id = p.ids[t * p.top_k + lane];
+    if (id < 0 || id >= p.E) id = -1;
+    if (id >= 0) g = p.dweights[t * p.top_k + lane] * p.scale;
+  }
+  const float logit = id >= 0 ? to_float(row[id]) : kMasked;
+  float mine = 0.f;  // what the chosen expert's logit gets
+  if (!p.sigmoid && !p.renormalize) {
+    float m = kMasked;
+    for (int e = lane; e < p.E; e += 32) {
+      const float x = to_float(row[e]);
+      d[e] = x;
+      m = fmaxf(m, x);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    float sum = 0.f;
+    for (int e = lane; e < p.E; e += 32) {
+      const float v = d[e] == kMasked ? 0.f : expf(d[e] - m);
+      d[e] = v;
+      sum += v;
+    }
+    sum = warp_sum(sum);
+    const float chosen = logit != kMasked ? expf(logit - m) / sum : 0.f;
+    mine = chosen * g;
+    const float along = warp_sum(mine);
+    const float factor = sum > 0.f || sum != sum ? along / sum : 0.f;  // all masked: no gradient
+    for (int e = lane; e < p.E; e += 32) d[e] = -d[e] * factor;
+  } else {
+    if (p.sigmoid) {
+      const float s = id >= 0 ? sigmoid_of(logit) : 0.f;
+      if (p.renormalize) {
+        const float total = warp_sum(s) + 1e-20f;
+        g = (g - warp_sum(g * s) / total) / total;
+      }
+      mine = g * s * (1.f - s);
+    } else {
+      float m = logit;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+      float w = logit != kMasked ? expf(logit - m) : 0.f;
+      const float total = warp_sum(w);
+      w = logit != kMasked ? w / total : 0.f;
+      mine = w * (g - warp_sum(w * g));
+    }
+    for (int e = lane; e < p.E; e += 32) d[e] = 0.f;
+  }
+  __syncwarp();
+  // experts named twice (ids of another origin) add up, in the order of the slots
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, id >= 0 ? id : -1 - lane);
+  if (__all_sync(0xFFFFFFFFu, same == 1u << lane)) {
+    if (id >= 0) d[id] += mine;
+  } else {
+    for (int j = 0; j < p.top_k; ++j) {
+      if (lane == j && id >= 0) d[id] += mine;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  T* out = static_cast<T*>(p.dlogits) + t * p.E;
+  for (int e = lane; e < p.E; e += 32) out[e] = from_float<T>(d[e]);
+}
+
+template <class T>
+cudaError_t launch_route(const RouteParams& p, void* stream) {
+  const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
+  const size_t smem = p.groups > 1 ? sizeof(uint32_t) * kWarps * p.E : 0;
+  if (p.E <= 32) return launch_dependent(route_kernel<T, 1>, grid, block, smem, stream, p);
+  if (p.E <= 64) return launch_dependent(route_kernel<T, 2>, grid, block, smem, stream, p);
+  if (p.E <= 128) return launch_dependent(route_kernel<T, 4>, grid, block, smem, stream, p);
+  if (p.E <= 256) return launch_dependent(route_kernel<T, 8>, grid, block, smem, stream, p);
+  if (p.E <= 512) return launch_dependent(route_kernel<T, 16>, grid, block, smem, stream, p);
+  return launch_dependent(route_kernel<T, 32>, grid, block, smem, stream, p);
+}
+
+mslkb_status check_route(int64_t T, int64_t E, int64_t ld, int64_t top_k, int32_t score,
+                         double scale, int32_t dtype) {
+  if (T < 0 || E < 0 || T > MSLKB_MAX_DIM || E > MSLKB_MAX_EXPERTS) return MSLKB_ERR_SHAPE;
+  if (top_k < 0 || top_k > E || top_k > MSLKB_MAX_TOPK) return MSLKB_ERR_SHAPE;
+  if (ld < E || ld > MSLKB_MAX_DIM || T * top_k > MSLKB_MAX_DIM) return MSLKB_ERR_SHAPE;
+  if (score != MSLKB_SOFTMAX && score != MSLKB_SIGMOID) return MSLKB_ERR_SHAPE;
+  if (!(scale > -1e30 && scale < 1e30)) return MSLKB_ERR_SHAPE;
+  return dtype_ok(dtype) ? MSLKB_OK : MSLKB_ERR_DTYPE;
+}
+
+}  // namespace
+}  // namespace mslkb
+
+extern "C" {
+
+mslkb_status mslkb_route_experts(const void* logits, const float* bias, int32_t* ids,
+                                 float* weights, int64_t T, int64_t E, int64_t ld, int64_t top_k,
+                                 int32_t score, int64_t num_groups, int64_t topk_groups,
+                                 int32_t group_top, int32_t renormalize, double scale,
+                                 int32_t dtype, void* stream) {
+  using namespace mslkb;
+  mslkb_status s = check_route(T, E, ld, top_k, score, scale, dtype);
+  if (s != MSLKB_OK) return s;
+  if (num_groups < 1 || num_groups > 32 || E % num_groups != 0) return MSLKB_ERR_SHAPE;
+  if (topk_groups < 1 || topk_groups > num_groups) return MSLKB_ERR_SHAPE;
+  if (top_k > E / num_groups * topk_groups) return MSLKB_ERR_SHAPE;
+  if (group_top != 1 && group_top != 2) return MSLKB_ERR_SHAPE;
+  if (T == 0 || top_k == 0) return MSLKB_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return MSLKB_ERR_NULL;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != MSLKB_OK) return s;
+  const bool by_logits = score == MSLKB_SOFTMAX && bias == nullptr &&
+                         (group_top == 1 || num_groups == 1);
+  const RouteParams p{logits, bias, ids, weights, T, ld, static_cast<int32_t>(E),
+                      static_cast<int32_t>(top_k), score == MSLKB_SIGMOID,
+                      static_cast<int32_t>(num_groups), static_cast<int32_t>(topk_groups),
+                      group_top, by_logits, renormalize, static_cast<float>(scale)};
+  TraceRange range("route_experts", T);
+  cudaError_t e;
+  if (dtype == MSLKB_BF16)
+    e = launch_route<__nv_bfloat16>(p, stream);
+  else if (dtype == MSLKB_FP16)
+    e = launch_route<__half>(p, stream);
+  else
+    e = launch_route<float>(p, stream);
+  return launch_status(e);
+}
+
+mslkb_status mslkb_route_experts_backward(const float* dweights, const void* logits,
+                                          const int32_t* ids, void* dlogits, int64_t T, int64_t E,
+                                          int64_t ld, int64_t top_k, int32_t score,
+                                          int32_t renormalize, double scale, int32_t dtype,
+                                          void* stream) {
+  using namespace mslkb;
+  mslkb_status s = check_route(T, E, ld, top_k, score, scale, dtype);
+  if (s != MSLKB_OK) return s;
+  if (T == 0 || E == 0) return MSLKB_OK;
+  if (logits == nullptr || dlogits == nullptr ||
+      (top_k > 0 && (dweights == nullptr || ids == nullptr)))
+    return MSLKB_ERR_NULL;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != MSLKB_OK) return s;
+  const RouteBackwardParams p{dweights, logits, ids, dlogits, T, ld, static_cast<int32_t>(E),
+                              static_cast<int32_t>(top_k), score == MSLKB_SIGMOID, renormalize,
+                              static_cast<float>(scale)};
+  const dim3 grid(static_cast<unsigned>((T + kWarps - 1) / kWarps)), block(kWarps * 32);
+  const size_t smem = sizeof(float) * kWarps * static_cast<size_t>(E);
+  TraceRange range("route_experts_backward", T);
+  cudaError_t e;
+  if (dtype == MSLKB_BF16)
+    e = launch_dependent(route_backward_kernel<__nv_bfloat16>, grid, block, smem, stream, p);
+  else if (dtype == MSLKB_FP16)
+    e = launch_dependent(route_backward_kernel<__half>, grid, block, smem, stream, p);
+  else
+    e = launch_dependent(route_backward_kernel<float>, grid, block, smem, stream, p);
+  return launch_status(e);
+}
+
+}  // extern "C"

@@ -73,7 +73,9 @@ typedef enum mslkb_status {
                            16-byte aligned, or their row length not a multiple of 16) */
   MSLKB_ERR_DEVICE = 4, /* the current device is not sm_103 (GB300 / B300) */
   MSLKB_ERR_CUDA = 5,   /* a CUDA runtime or driver call failed; see mslkb_last_cuda_error */
-  MSLKB_ERR_TOO_LARGE = 6 /* needs more scratch than the allocation-free entry point holds */
+  MSLKB_ERR_TOO_LARGE = 6, /* needs more scratch than the allocation-free entry point holds */
+  MSLKB_ERR_DTYPE = 7,     /* an element type that the call does not take */
+  MSLKB_ERR_WORKSPACE = 8  /* the workspace is NULL, misaligned or too small */
 } mslkb_status;
 
 /* Bits of the device status word (mslkb_get_device_status). */
@@ -319,6 +321,176 @@ MSLKB_API mslkb_status mslkb_f8f8bf16_rowwise_grouped_stacked_noalloc(
     const void *A, const void *B, const float *scale_a, const float *scale_b,
     const int64_t *m_sizes, void *out, int64_t total_M, int64_t G, int64_t N, int64_t K,
     void *stream);
+
+/*
+ * Operators around the grouped product in a mixture-of-experts block (additions of this
+ * library).  They make the product's operands and use its results:
+ *
+ *   add_rms_norm_quant -> (router's logits) -> route_experts -> moe_dispatch
+ *     -> grouped gate/up product -> swiglu_quant -> grouped down product -> moe_combine
+ *
+ * Conventions beside those above: `dtype` is the element type of the 16- or 32-bit float
+ * tensors of a call (MSLKB_BF16 / FP16 / FP32; MSLKB_ERR_DTYPE otherwise).  Sums, norms and
+ * softmax statistics are fp32; every output is rounded once, to nearest even.  Any base
+ * alignment that suits the element type is accepted; 16-byte aligned rows take the wide
+ * path.  Inputs named with an `ld` argument may be slices of wider rows (ld elements from
+ * row to row, ld >= the row's length); everything else is dense.  An output may be the same
+ * buffer as an input only where that is said.  Nothing is allocated: the two calls that
+ * need scratch take it as `workspace` (16-byte aligned, contents need not be initialised,
+ * not shared by calls that may run at the same time) of at least the bytes that the
+ * matching *_workspace_bytes function returns.  Sums are made in a fixed order: equal
+ * inputs give equal bits.
+ *
+ * e4m3 outputs: one scale per row (groupwise = 0) or per 128 columns (groupwise = 1; the
+ * row length must be a multiple of 128).  scale = amax / 448 over the row or block and
+ * code = e4m3_rne(value / scale); where amax < 2^-80 the codes are 0 and the scale 1.  A
+ * NaN, or an infinity that the formula makes NaN, gives its row or block a NaN scale.
+ */
+typedef enum mslkb_dtype { MSLKB_BF16 = 0, MSLKB_FP16 = 1, MSLKB_FP32 = 2 } mslkb_dtype;
+
+#define MSLKB_MAX_HIDDEN 32768 /* longest row of the norm and SwiGLU calls */
+#define MSLKB_MAX_TOPK 32      /* experts per token */
+#define MSLKB_MAX_EXPERTS 1024 /* experts of the routing and dispatch calls */
+
+/*
+ * Residual addition, root-mean-square norm and quantisation of T rows of H elements:
+ *
+ *   h = x + residual (residual NULL: h = x),   rstd = (mean(h^2) + eps)^(-1/2),
+ *   y = h * rstd * weight,                     q, scale = e4m3(y)
+ *
+ *   x, residual   device, dtype [T, H], rows ldx / ldr elements apart
+ *   weight        device, [H], dtype, or fp32 if weight_fp32 is not 0
+ *   q             device, e4m3 [T, H];  scale  device, fp32 [T] or [T, H / 128]
+ *   residual_out  device, dtype [T, H]: h; NULL: not written.  May be residual itself
+ *   y             device, dtype [T, H], for readers of the unquantised norm; NULL: none
+ *   rstd          device, fp32 [T], for the gradient; NULL: none
+ *
+ * The norm is that of the fp32 sum, before residual_out's rounding.  1e-12 <= eps < 1.
+ */
+MSLKB_API mslkb_status mslkb_add_rms_norm_quant(
+    const void *x, const void *residual, const void *weight, void *q, float *scale,
+    void *residual_out, void *y, float *rstd, int64_t T, int64_t H, int64_t ldx, int64_t ldr,
+    double eps, int32_t dtype, int32_t weight_fp32, int32_t groupwise, void *stream);
+
+/*
+ * Gradient of the norm (the quantisation passes the gradient through):
+ *
+ *   xhat = h * rstd,  g = dy * weight,
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dresidual,   dweight = sum over rows of dy * xhat
+ *
+ * dx is the gradient of x and of residual alike; dresidual is the gradient that arrives on
+ * residual_out (NULL: none).  dy, h, dresidual, dx are dense dtype [T, H] (dx may be dy or
+ * dresidual), rstd fp32 [T], dweight fp32 [H].
+ */
+MSLKB_API int64_t mslkb_add_rms_norm_quant_backward_workspace_bytes(int64_t T, int64_t H);
+MSLKB_API mslkb_status mslkb_add_rms_norm_quant_backward(
+    const void *dy, const void *h, const void *weight, const float *rstd, const void *dresidual,
+    void *dx, float *dweight, void *workspace, int64_t workspace_bytes, int64_t T, int64_t H,
+    int32_t dtype, int32_t weight_fp32, void *stream);
+
+/*
+ * Each token's experts and weights from the router's logits:
+ *
+ *   score  = softmax(logits) or 1 / (1 + exp(-logits))       (MSLKB_SOFTMAX, MSLKB_SIGMOID)
+ *   choice = score + bias                                    (bias fp32 [E], or NULL)
+ *
+ * The E experts form num_groups equal groups (1: none).  A group is worth the sum of its
+ * group_top (1 or 2) best choices; the experts of the topk_groups best groups stay, and the
+ * top_k best choices among them are taken, best first, the lowest index first among equals.
+ * (Softmax without bias and with group_top = 1 orders by the logits themselves.)
+ *
+ *   ids      device, int32 [T, top_k]
+ *   weights  device, fp32 [T, top_k]: scale * score, with renormalize scale * score / (sum of
+ *            the taken scores, + 1e-20 for the sigmoid)
+ *
+ * An expert whose logit is -infinity (or whose choice is) is masked: it is never taken, and
+ * a token with fewer than top_k experts left gets id -1 and weight 0 in the rest.  A NaN
+ * choice counts as the largest and gives NaN weights.  logits: dtype [T, E], rows ld apart.
+ */
+#define MSLKB_SOFTMAX 0
+#define MSLKB_SIGMOID 1
+MSLKB_API mslkb_status mslkb_route_experts(
+    const void *logits, const float *bias, int32_t *ids, float *weights, int64_t T, int64_t E,
+    int64_t ld, int64_t top_k, int32_t score, int64_t num_groups, int64_t topk_groups,
+    int32_t group_top, int32_t renormalize, double scale, int32_t dtype, void *stream);
+
+/*
+ * Gradient of the routing weights for the choice that was made (ids; an id outside [0, E)
+ * has none): dlogits dtype [T, E], every element written, dense.  The choice itself and the
+ * bias have no gradient.
+ */
+MSLKB_API mslkb_status mslkb_route_experts_backward(
+    const float *dweights, const void *logits, const int32_t *ids, void *dlogits, int64_t T,
+    int64_t E, int64_t ld, int64_t top_k, int32_t score, int32_t renormalize, double scale,
+    int32_t dtype, void *stream);
+
+/*
+ * Packs the tokens' rows by expert into the stacked layout.  The choices (t, j) with
+ * 0 <= ids[t, j] < E are ordered by expert, then by t * top_k + j; choice number r becomes
+ * row r of xq_out.  Choices with another id (a masked slot, an expert of another device) are
+ * left out, and rows past the last choice are not written.
+ *
+ *   x           device, [T, row_bytes] bytes (e4m3 codes, or any other row); rows dense
+ *   x_scale     device, fp32 [T, scale_cols]; NULL with scale_cols = 0
+ *   ids         device, int32 [T, top_k]
+ *   x_out       device, [T * top_k, row_bytes];  scale_out  fp32 [T * top_k, scale_cols]
+ *   m_sizes     device, int64 [E]: rows per expert, as the stacked products take them
+ *   dest        device, int32 [T, top_k]: the choice's row, -1 if left out
+ *
+ * T * top_k is limited to MSLKB_MAX_DIM / 2.
+ */
+MSLKB_API int64_t mslkb_moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
+MSLKB_API mslkb_status mslkb_moe_dispatch(
+    const void *x, const float *x_scale, const int32_t *ids, void *x_out, float *scale_out,
+    int64_t *m_sizes, int32_t *dest, void *workspace, int64_t workspace_bytes, int64_t T,
+    int64_t top_k, int64_t E, int64_t row_bytes, int64_t scale_cols, void *stream);
+
+/*
+ * The weighted sum of a token's rows:
+ *
+ *   out[t] = sum over j of weights[t, j] * rows[dest[t, j]]
+ *
+ * rows dtype [R, H], dest int32 [T, top_k] (outside [0, R): the choice adds nothing and its
+ * row is not read), weights fp32 [T, top_k] (NULL: ones, which makes this the gradient of
+ * the dispatch), out dtype [T, H].
+ */
+MSLKB_API mslkb_status mslkb_moe_combine(const void *rows, const int32_t *dest,
+                                         const float *weights, void *out, int64_t T,
+                                         int64_t top_k, int64_t H, int64_t R, int32_t dtype,
+                                         void *stream);
+
+/*
+ * Gradient of the combination: drows[dest[t, j]] = weights[t, j] * dout[t], dweights[t, j] =
+ * the dot product of dout[t] and rows[dest[t, j]] (0 where the choice has no row).  Rows of
+ * drows that no choice names are not written; two choices must not name one row.
+ */
+MSLKB_API mslkb_status mslkb_moe_combine_backward(
+    const void *dout, const void *rows, const int32_t *dest, const float *weights, void *drows,
+    float *dweights, int64_t T, int64_t top_k, int64_t H, int64_t R, int32_t dtype, void *stream);
+
+/*
+ * The experts' activation: x dtype [R, 2 * W], rows ldx apart, holds gate and up side by side;
+ *
+ *   a = gate * sigmoid(gate) * up,    q, scale = e4m3(a)     q [R, W], scale [R] or [R, W / 128]
+ *
+ * With saved not NULL the input is kept in 8 bits for the gradient: saved e4m3 [R, 2 * W] and
+ * saved_scale fp32 [R, 2 * W / 128] (one scale per 128 columns; W a multiple of 128).
+ */
+MSLKB_API mslkb_status mslkb_swiglu_quant(
+    const void *x, void *q, float *scale, void *saved, float *saved_scale, int64_t R, int64_t W,
+    int64_t ldx, int32_t dtype, int32_t groupwise, void *stream);
+
+/*
+ * Gradient of the activation, dx dtype [R, 2 * W], from dy dtype [R, W] and the kept input:
+ *
+ *   dgate = dy * up * s * (1 + gate * (1 - s)),   dup = dy * gate * s,   s = sigmoid(gate)
+ *
+ * saved is the checkpoint with its scales, or the input itself (dtype [R, 2 * W], dense) with
+ * saved_scale NULL.
+ */
+MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *saved,
+                                                   const float *saved_scale, void *dx, int64_t R,
+                                                   int64_t W, int32_t dtype, void *stream);
 
 /* Static description of a status code.  Never NULL. */
 MSLKB_API const char *mslkb_status_string(mslkb_status status);
