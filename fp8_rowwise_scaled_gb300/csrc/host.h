@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "mslkb.h"
@@ -44,6 +45,25 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Dynamic shared memory that one CTA can have beside a few KB of its own (227 KB in all), and
+// what the CTAs of an SM have together.
+constexpr int kMaxCtaSmem = 224 * 1024;
+constexpr int kMaxSmSmem = 228 * 1024;
+
+// Lets `kKernel` use up to kMaxCtaSmem of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCtaSmem);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 inline bool aligned_to(const void* p, size_t bytes) {

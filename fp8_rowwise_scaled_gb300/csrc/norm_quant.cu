@@ -1,10 +1,17 @@
 // norm_quant.cu -- residual addition + root-mean-square norm + e4m3 output, and the gradient.
 //
-// Forward, one CTA per row, the row in registers between its one read and its one write:
+// Forward, the row in registers between its one read and its one write:
 //   h = x + residual, u = h * weight, and in one pass sum(h^2) and max|u|.
 // The codes need no rstd: y / scale = h rstd w * 448 / (rstd max|h w|) = u * (448 / max|u|).
 // So one exchange over the CTA gives both rstd and the row's scale (block scales need only
 // the 16 lanes that hold a block), where norm-then-quantise would need two.
+//
+// Both directions read every input once and write every output once and are bound by HBM.
+// With a row per CTA, the CTA's loads wait while it reduces and stores; so for many rows the
+// kernels are persistent, and each thread copies its own columns of the next rows into a ring
+// of stages in shared memory (cp.async, 16 bytes) while it works on this one.  A thread reads
+// back only what it copied itself: its own cp.async.wait_group is all the synchronisation
+// that the ring needs.
 #include "host.h"
 #include "rows.cuh"
 
@@ -22,10 +29,10 @@ struct NormParams {
   void* residual_out;
   void* y;
   float* rstd;
-  int64_t ldx, ldr;
+  int64_t T, ldx, ldr;
   int32_t H;
   int32_t weight_fp32;
-  float eps;
+  float eps, inv_h;
 };
 
 // weight elements [c, c + 8): fp32 or T
@@ -51,6 +58,65 @@ __device__ __forceinline__ void cta_sum_max(float& sum, uint32_t& largest, float
   largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mine.y));
 }
 
+// A thread's columns [c, c + 8), c = (i * blockDim.x + threadIdx.x) * 8, of one row that is
+// h in registers: everything from there to the outputs.
+template <class T, int kVecs, bool kWide, bool kBlocks, class Weight>
+__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, float (&h)[kVecs][8],
+                                           Weight weight, float2* slot) {
+  const int n = p.H;
+  T* residual_out = static_cast<T*>(p.residual_out) + row * n;
+  float sum = 0.f;
+  uint32_t largest = 0, block_largest[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * 8;
+    if (p.residual_out != nullptr) store8<T, kWide>(residual_out, c, n, h[i]);
+    float w[8];
+    weight(i, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum = fmaf(h[i][j], h[i][j], sum);
+      w[j] *= h[i][j];
+    }
+    block_largest[i] = abs_max(w);
+    if constexpr (kBlocks)
+      block_largest[i] = block_max<16>(block_largest[i]);
+    else
+      largest = max(largest, block_largest[i]);
+  }
+  cta_sum_max(sum, largest, slot);
+  const float rstd = rsqrtf(fmaf(sum, p.inv_h, p.eps));  // 2 ulp
+  if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  QuantScale s;
+  if constexpr (!kBlocks) {
+    const float m = __uint_as_float(largest);
+    s = quant_scale(m * rstd, m);
+    if (threadIdx.x == 0) p.scale[row] = s.scale;
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * 8;
+    if constexpr (kBlocks) {
+      const float m = __uint_as_float(block_largest[i]);
+      s = quant_scale(m * rstd, m);
+      if (c < n && c % kScaleBlock == 0)
+        p.scale[row * (n / kScaleBlock) + c / kScaleBlock] = s.scale;
+    }
+    float w[8], v[8];
+    weight(i, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h[i][j] * w[j];
+    store_codes8<kWide>(p.q + row * n, c, n, quantize8(v, s.inv));
+    if (p.y != nullptr) {
+      // (h * rstd) * weight: h * weight alone may fall among the subnormals
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * rstd * w[j];
+      store8<T, kWide>(static_cast<T*>(p.y) + row * n, c, n, v);
+    }
+  }
+}
+
+// One CTA per row, straight from global memory.
 template <class T, int kVecs, bool kWide, bool kBlocks>
 __global__ void __launch_bounds__(kMaxThreads)
     norm_quant_kernel(const __grid_constant__ NormParams p) {
@@ -61,9 +127,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int n = p.H;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* residual = static_cast<const T*>(p.residual) + row * p.ldr;
-  T* residual_out = static_cast<T*>(p.residual_out) + row * n;
-
-  float u[kVecs][8];  // h
+  float h[kVecs][8];
   {
     Raw8<T> rx[kVecs], rr[kVecs];
 #pragma unroll
@@ -76,65 +140,115 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      unpack8(rx[i], u[i]);
+      unpack8(rx[i], h[i]);
       if (p.residual != nullptr) {
         float r[8];
         unpack8(rr[i], r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[i][j] += r[j];
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
       }
     }
   }
-  float sum = 0.f;
-  uint32_t largest = 0, block_largest[kVecs];
+  finish_row<T, kVecs, kWide, kBlocks>(
+      p, row, h,
+      [&](int i, float (&w)[8]) {
+        load_weight8<T, kWide>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w);
+      },
+      slot);
+}
+
+// ---------------------------------------------------------------------------------
+// the ring of rows
+// ---------------------------------------------------------------------------------
+// Where a thread finds chunk k of its columns c = (i * blockDim.x + threadIdx.x) * 8 of input
+// `stream` in a stage: 16 bytes per thread side by side, free of bank conflicts.
+template <class T, int kVecs>
+__device__ __forceinline__ uint32_t ring_offset(int stream, int i, int k) {
+  constexpr int kChunks = sizeof(T) / 2;  // 16-byte chunks of eight elements
+  return (((stream * kVecs + i) * kChunks + k) * blockDim.x + threadIdx.x) * 16;
+}
+
+template <class T, int kVecs>
+__device__ __forceinline__ void ring_fetch(uint32_t stage, int stream, const T* row, int n) {
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int c = (i * blockDim.x + threadIdx.x) * 8;
-    if (p.residual_out != nullptr) store8<T, kWide>(residual_out, c, n, u[i]);
-    float w[8];
-    load_weight8<T, kWide>(p.weight, p.weight_fp32, c, n, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sum = fmaf(u[i][j], u[i][j], sum);
-      w[j] *= u[i][j];
-    }
-    block_largest[i] = abs_max8(w);
-    if constexpr (kBlocks)
-      block_largest[i] = block16_max(block_largest[i]);
-    else
-      largest = max(largest, block_largest[i]);
+    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k)
+      // past the row's end nothing is read and zeros are written
+      ptx::cp_async<16>(stage + ring_offset<T, kVecs>(stream, i, k),
+                        c < n ? row + c + k * (16 / sizeof(T)) : row, c < n ? 16 : 0);
   }
-  cta_sum_max(sum, largest, slot);
-  const float rstd = 1.f / sqrtf(sum / static_cast<float>(n) + p.eps);
-  if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-  float inv = 0.f;
-  if constexpr (!kBlocks) {
-    const float m = __uint_as_float(largest), amax = m * rstd;
-    const bool zero = amax < kQuantTiny;
-    inv = zero ? 0.f : kE4m3Max / m;
-    if (threadIdx.x == 0) p.scale[row] = zero ? 1.f : amax / kE4m3Max;
-  }
+}
+
+template <class T, int kVecs>
+__device__ __forceinline__ void ring_read(const uint8_t* stage, int stream, int i,
+                                          float (&v)[8]) {
+  Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * 8;
-    if constexpr (kBlocks) {
-      const float m = __uint_as_float(block_largest[i]), amax = m * rstd;
-      const bool zero = amax < kQuantTiny;
-      inv = zero ? 0.f : kE4m3Max / m;
-      if (c < n && c % kScaleBlock == 0)
-        p.scale[row * (n / kScaleBlock) + c / kScaleBlock] = zero ? 1.f : amax / kE4m3Max;
+  for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k)
+    r.w[k] = load16(stage + ring_offset<T, kVecs>(stream, i, k));
+  unpack8(r, v);
+}
+
+template <class T, int kVecs>
+int ring_stage_bytes(int streams, int threads) {
+  return streams * kVecs * static_cast<int>(sizeof(T) / 2) * threads * 16;
+}
+
+template <class T, int kVecs, int kStages, bool kBlocks>
+__global__ void __launch_bounds__(512, 2)
+    norm_ring_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 slot[2][32];
+  const int n = p.H;
+  const bool add = p.residual != nullptr;
+  const int stage_bytes = (add ? 2 : 1) * kVecs * static_cast<int>(sizeof(T) / 2) *
+                          static_cast<int>(blockDim.x) * 16;
+  const uint32_t base = ptx::smem_addr(ring);
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.T) {
+      const uint32_t at = base + stage * stage_bytes;
+      ring_fetch<T, kVecs>(at, 0, static_cast<const T*>(p.x) + row * p.ldx, n);
+      if (add) ring_fetch<T, kVecs>(at, 1, static_cast<const T*>(p.residual) + row * p.ldr, n);
     }
-    float w[8], v[8];
-    load_weight8<T, kWide>(p.weight, p.weight_fp32, c, n, w);
+    ptx::cp_async_commit();
+  };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = u[i][j] * w[j];
-    store_codes8<kWide>(p.q + row * n, c, n, quantize8(v, inv));
-    if (p.y != nullptr) {
-      // (h * rstd) * weight: h * weight alone may fall among the subnormals
+  for (int s = 0; s < kStages - 1; ++s)
+    fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  float w[kVecs][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = u[i][j] * rstd * w[j];
-      store8<T, kWide>(static_cast<T*>(p.y) + row * n, c, n, v);
+  for (int i = 0; i < kVecs; ++i)
+    load_weight8<T, true>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w[i]);
+  int stage = 0, turn = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    fetch(row + static_cast<int64_t>(kStages - 1) * gridDim.x,
+          stage == 0 ? kStages - 1 : stage - 1);
+    ptx::cp_async_wait<kStages - 1>();
+    const uint8_t* at = ring + stage * stage_bytes;
+    float h[kVecs][8];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      ring_read<T, kVecs>(at, 0, i, h[i]);
+      if (add) {
+        float r[8];
+        ring_read<T, kVecs>(at, 1, i, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+      }
     }
+    finish_row<T, kVecs, true, kBlocks>(
+        p, row, h,
+        [&](int i, float (&v)[8]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = w[i][j];
+        },
+        slot[turn]);
+    turn ^= 1;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
 }
 
@@ -155,6 +269,7 @@ struct NormBackwardParams {
   int64_t T;
   int32_t H;
   int32_t weight_fp32;
+  float inv_h;
 };
 
 __device__ __forceinline__ float cta_sum(float sum, float* slot) {
@@ -166,8 +281,43 @@ __device__ __forceinline__ float cta_sum(float sum, float* slot) {
   return warp_sum(lane < warps ? slot[lane] : 0.f);
 }
 
-// A thread keeps its columns over the CTA's rows, so the weight gradient stays in registers
-// and is written once per CTA.
+// One row of the gradient; `inputs` gives a thread's eight columns i of dy and h, `weight` and
+// `residual` those of the others.  dy and h are taken twice (from the ring or L1), before and
+// after the row's mean, rather than kept: with the weight gradient in registers over all the
+// CTA's rows, that is what lets two CTAs share an SM.
+template <class T, int kVecs, bool kWide, class Inputs, class Weight, class Residual>
+__device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_t row, float rstd,
+                                             float (&dw)[kVecs][8], Inputs inputs, Weight weight,
+                                             Residual residual, float* slot) {
+  const int n = p.H;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    float g[8], xhat[8], w[8];
+    inputs(i, g, xhat);
+    weight(i, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      xhat[j] *= rstd;
+      dw[i][j] = fmaf(g[j], xhat[j], dw[i][j]);
+      sum = fmaf(g[j] * w[j], xhat[j], sum);
+    }
+  }
+  const float mean = cta_sum(sum, slot) * p.inv_h;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    float g[8], xhat[8], w[8], d[8];
+    inputs(i, g, xhat);
+    weight(i, w);
+    residual(i, d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      d[j] = fmaf(rstd, g[j] * w[j] - xhat[j] * rstd * mean, d[j]);
+    store8<T, kWide>(static_cast<T*>(p.dx) + row * n, (i * blockDim.x + threadIdx.x) * 8, n, d);
+  }
+}
+
+// Straight from global memory.
 template <class T, int kVecs, bool kWide>
 __global__ void __launch_bounds__(kMaxThreads)
     norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
@@ -175,54 +325,97 @@ __global__ void __launch_bounds__(kMaxThreads)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int n = p.H;
-  float dw[kVecs][8];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  float dw[kVecs][8] = {};
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-    const float rstd = p.rstd[row];
-    float g[kVecs][8], xhat[kVecs][8];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * 8;
-      unpack8(load8<T, kWide>(static_cast<const T*>(p.dy) + row * n, c, n), g[i]);
-      unpack8(load8<T, kWide>(static_cast<const T*>(p.h) + row * n, c, n), xhat[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float w[8];
-      load_weight8<T, kWide>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xhat[i][j] *= rstd;
-        dw[i][j] = fmaf(g[i][j], xhat[i][j], dw[i][j]);
-        g[i][j] *= w[j];
-        sum = fmaf(g[i][j], xhat[i][j], sum);
-      }
-    }
-    const float mean = cta_sum(sum, slot[turn]) / static_cast<float>(n);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * 8;
-      float d[8];
-      if (p.dresidual != nullptr) {
-        unpack8(load8<T, kWide>(static_cast<const T*>(p.dresidual) + row * n, c, n), d);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, g[i][j] - xhat[i][j] * mean, d[j]);
-      store8<T, kWide>(static_cast<T*>(p.dx) + row * n, c, n, d);
-    }
+    backward_row<T, kVecs, kWide>(
+        p, row, p.rstd[row], dw,
+        [&](int i, float (&g)[8], float (&h)[8]) {
+          const int c = (i * blockDim.x + threadIdx.x) * 8;
+          unpack8(load8<T, kWide>(static_cast<const T*>(p.dy) + row * n, c, n), g);
+          unpack8(load8<T, kWide>(static_cast<const T*>(p.h) + row * n, c, n), h);
+        },
+        [&](int i, float (&w)[8]) {
+          load_weight8<T, kWide>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n,
+                                 w);
+        },
+        [&](int i, float (&d)[8]) {
+          const T* from = static_cast<const T*>(p.dresidual) + row * n;
+          unpack8(load8<T, kWide>(from, (i * blockDim.x + threadIdx.x) * 8,
+                                  p.dresidual != nullptr ? n : 0),
+                  d);
+        },
+        slot[turn]);
   }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
     store8<float, kWide>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
                          (i * blockDim.x + threadIdx.x) * 8, n, dw[i]);
+}
+
+template <class T, int kVecs, int kStages>
+__global__ void __launch_bounds__(512, 2)
+    norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float slot[2][32];
+  const int n = p.H;
+  const bool add = p.dresidual != nullptr;
+  const int stage_bytes = (add ? 3 : 2) * kVecs * static_cast<int>(sizeof(T) / 2) *
+                          static_cast<int>(blockDim.x) * 16;
+  const uint32_t base = ptx::smem_addr(ring);
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.T) {
+      const uint32_t at = base + stage * stage_bytes;
+      ring_fetch<T, kVecs>(at, 0, static_cast<const T*>(p.dy) + row * n, n);
+      ring_fetch<T, kVecs>(at, 1, static_cast<const T*>(p.h) + row * n, n);
+      if (add) ring_fetch<T, kVecs>(at, 2, static_cast<const T*>(p.dresidual) + row * n, n);
+    }
+    ptx::cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s)
+    fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  float w[kVecs][8], dw[kVecs][8] = {};
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    load_weight8<T, true>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w[i]);
+  int stage = 0, turn = 0;
+  float rstd = p.rstd[blockIdx.x];  // the grid is no larger than T
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    fetch(row + static_cast<int64_t>(kStages - 1) * gridDim.x,
+          stage == 0 ? kStages - 1 : stage - 1);
+    const float next_rstd = row + gridDim.x < p.T ? p.rstd[row + gridDim.x] : 0.f;
+    ptx::cp_async_wait<kStages - 1>();
+    const uint8_t* at = ring + stage * stage_bytes;
+    backward_row<T, kVecs, true>(
+        p, row, rstd, dw,
+        [&](int i, float (&g)[8], float (&h)[8]) {
+          ring_read<T, kVecs>(at, 0, i, g);
+          ring_read<T, kVecs>(at, 1, i, h);
+        },
+        [&](int i, float (&v)[8]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = w[i][j];
+        },
+        [&](int i, float (&d)[8]) {
+          if (add) {
+            ring_read<T, kVecs>(at, 2, i, d);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = 0.f;
+          }
+        },
+        slot[turn]);
+    rstd = next_rstd;
+    turn ^= 1;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    store8<float, true>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
+                        (i * blockDim.x + threadIdx.x) * 8, n, dw[i]);
 }
 
 // Column sums of parts [rows, H], in a fixed order: 8 threads per column.
@@ -255,36 +448,80 @@ int threads_for(int64_t n, int vecs) {
 }
 
 template <class T, int kVecs, bool kWide>
-cudaError_t launch_norm(const NormParams& p, int64_t rows, bool blocks, void* stream) {
-  const dim3 grid(static_cast<unsigned>(rows)), block(threads_for(p.H, kVecs));
+cudaError_t launch_norm(const NormParams& p, bool blocks, void* stream) {
+  const dim3 grid(static_cast<unsigned>(p.T)), block(threads_for(p.H, kVecs));
   return blocks ? launch_dependent(norm_quant_kernel<T, kVecs, kWide, true>, grid, block, 0,
                                    stream, p)
                 : launch_dependent(norm_quant_kernel<T, kVecs, kWide, false>, grid, block, 0,
                                    stream, p);
 }
 
-template <class T>
-cudaError_t launch_norm(const NormParams& p, int64_t rows, bool wide, bool blocks,
-                        void* stream) {
-  const int64_t n = p.H;
-  if (!wide) return launch_norm<T, 4, false>(p, rows, blocks, stream);
-  if (n <= 8 * kMaxThreads) return launch_norm<T, 1, true>(p, rows, blocks, stream);
-  if (n <= 16 * kMaxThreads) return launch_norm<T, 2, true>(p, rows, blocks, stream);
-  return launch_norm<T, 4, true>(p, rows, blocks, stream);
+// CTAs of a ring kernel that an SM holds: by shared memory, threads and 64 registers each.
+int ring_ctas(int smem, int threads) {
+  int c = kMaxSmSmem / (smem + 1024);
+  if (c > 65536 / 64 / threads) c = 65536 / 64 / threads;
+  return c < 1 ? 1 : c;
 }
 
+template <class T, int kVecs, int kStages>
+cudaError_t launch_norm_ring(const NormParams& p, int sms, bool blocks, void* stream) {
+  const int threads = threads_for(p.H, kVecs);
+  const int smem = kStages * ring_stage_bytes<T, kVecs>(p.residual != nullptr ? 2 : 1, threads);
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads);
+  const dim3 grid(static_cast<unsigned>(p.T < most ? p.T : most));
+  cudaError_t e = blocks ? allow_smem<norm_ring_kernel<T, kVecs, kStages, true>>()
+                         : allow_smem<norm_ring_kernel<T, kVecs, kStages, false>>();
+  if (e != cudaSuccess) return e;
+  return blocks ? launch_dependent(norm_ring_kernel<T, kVecs, kStages, true>, grid, dim3(threads),
+                                   smem, stream, p)
+                : launch_dependent(norm_ring_kernel<T, kVecs, kStages, false>, grid,
+                                   dim3(threads), smem, stream, p);
+}
+
+template <class T>
+cudaError_t launch_norm(const NormParams& p, int sms, bool wide, bool blocks, void* stream) {
+  const int64_t n = p.H;
+  if (!wide) return launch_norm<T, 4, false>(p, blocks, stream);
+  if (p.T > 4 * sms && n <= 8192) {
+    constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
+    if (n <= 4096) return launch_norm_ring<T, 1, kStages>(p, sms, blocks, stream);
+    return launch_norm_ring<T, 2, kStages>(p, sms, blocks, stream);
+  }
+  if (n <= 8 * kMaxThreads) return launch_norm<T, 1, true>(p, blocks, stream);
+  if (n <= 16 * kMaxThreads) return launch_norm<T, 2, true>(p, blocks, stream);
+  return launch_norm<T, 4, true>(p, blocks, stream);
+}
+
+// The gradient's first kernel; *parts: the rows of partial weight gradients that it writes.
 template <class T, int kVecs, bool kWide>
-cudaError_t launch_backward(const NormBackwardParams& p, int64_t parts, void* stream) {
+cudaError_t launch_backward(const NormBackwardParams& p, int64_t* parts, void* stream) {
   return launch_dependent(norm_backward_kernel<T, kVecs, kWide>,
-                          dim3(static_cast<unsigned>(parts)), dim3(threads_for(p.H, kVecs)), 0,
+                          dim3(static_cast<unsigned>(*parts)), dim3(threads_for(p.H, kVecs)), 0,
                           stream, p);
 }
 
+template <class T, int kVecs, int kStages>
+cudaError_t launch_backward_ring(const NormBackwardParams& p, int sms, int64_t* parts,
+                                 void* stream) {
+  const int threads = threads_for(p.H, kVecs);
+  const int smem = kStages * ring_stage_bytes<T, kVecs>(p.dresidual != nullptr ? 3 : 2, threads);
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads);
+  if (*parts > most) *parts = most;
+  cudaError_t e = allow_smem<norm_backward_ring_kernel<T, kVecs, kStages>>();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(norm_backward_ring_kernel<T, kVecs, kStages>,
+                          dim3(static_cast<unsigned>(*parts)), dim3(threads), smem, stream, p);
+}
+
 template <class T>
-cudaError_t launch_backward(const NormBackwardParams& p, bool wide, int64_t parts,
+cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int64_t* parts,
                             void* stream) {
   const int64_t n = p.H;
   if (!wide) return launch_backward<T, 4, false>(p, parts, stream);
+  if (n <= 8192 && p.T > 2 * sms) {
+    if (n <= 4096) return launch_backward_ring<T, 1, 2>(p, sms, parts, stream);
+    return launch_backward_ring<T, 2, 2>(p, sms, parts, stream);
+  }
   if (n <= 16 * kMaxThreads) return launch_backward<T, 2, true>(p, parts, stream);
   return launch_backward<T, 4, true>(p, parts, stream);
 }
@@ -324,16 +561,17 @@ mslkb_status mslkb_add_rms_norm_quant(const void* x, const void* residual, const
                     aligned_to(weight, 16) && aligned_to(q, 8) && aligned_to(residual_out, 16) &&
                     aligned_to(y, 16);
   NormParams p{x,    residual, weight, static_cast<uint8_t*>(q),
-               scale, residual_out, y, rstd, ldx, ldr,
-               static_cast<int32_t>(H), weight_fp32, static_cast<float>(eps)};
+               scale, residual_out, y, rstd, T, ldx, ldr,
+               static_cast<int32_t>(H), weight_fp32, static_cast<float>(eps),
+               1.f / static_cast<float>(H)};
   TraceRange range("add_rms_norm_quant", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_norm<__nv_bfloat16>(p, T, wide, groupwise != 0, stream);
+    e = launch_norm<__nv_bfloat16>(p, sms, wide, groupwise != 0, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_norm<__half>(p, T, wide, groupwise != 0, stream);
+    e = launch_norm<__half>(p, sms, wide, groupwise != 0, stream);
   else
-    e = launch_norm<float>(p, T, wide, groupwise != 0, stream);
+    e = launch_norm<float>(p, sms, wide, groupwise != 0, stream);
   return launch_status(e);
 }
 
@@ -364,19 +602,18 @@ mslkb_status mslkb_add_rms_norm_quant_backward(const void* dy, const void* h, co
   const bool wide = H % 8 == 0 && aligned_to(dy, 16) && aligned_to(h, 16) &&
                     aligned_to(weight, 16) && aligned_to(dresidual, 16) && aligned_to(dx, 16);
   int64_t parts = backward_parts(T);
-  if (parts > 4 * static_cast<int64_t>(sms)) parts = 4 * static_cast<int64_t>(sms);
   float* partial = static_cast<float*>(workspace);
   NormBackwardParams p{dy, h, weight, rstd, dresidual, dx, partial, T,
-                       static_cast<int32_t>(H), weight_fp32};
+                       static_cast<int32_t>(H), weight_fp32, 1.f / static_cast<float>(H)};
   TraceRange range("add_rms_norm_quant_backward", T);
   cudaError_t e = cudaSuccess;
   if (T > 0) {
     if (dtype == MSLKB_BF16)
-      e = launch_backward<__nv_bfloat16>(p, wide, parts, stream);
+      e = launch_backward<__nv_bfloat16>(p, sms, wide, &parts, stream);
     else if (dtype == MSLKB_FP16)
-      e = launch_backward<__half>(p, wide, parts, stream);
+      e = launch_backward<__half>(p, sms, wide, &parts, stream);
     else
-      e = launch_backward<float>(p, wide, parts, stream);
+      e = launch_backward<float>(p, sms, wide, &parts, stream);
   }
   if (e == cudaSuccess)
     e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(256),

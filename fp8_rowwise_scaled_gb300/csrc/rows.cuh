@@ -152,16 +152,6 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t codes) {
   return unpack2(h, __half());
 }
 
-__device__ __forceinline__ void unpack_e4m3x8(uint2 codes, float (&v)[8]) {
-  const uint32_t w[2] = {codes.x, codes.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_e4m3x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
 // Codes [c, c + 8) of a row of n codes (kWide: 8-byte aligned rows, n a multiple of 8).
 template <bool kWide>
 __device__ __forceinline__ void store_codes8(uint8_t* row, int c, int n, uint2 codes) {
@@ -175,15 +165,25 @@ __device__ __forceinline__ void store_codes8(uint8_t* row, int c, int n, uint2 c
   }
 }
 
-// Magnitudes are compared as the bit patterns of |v|: the order of the floats, with NaN
+// Largest magnitude, as the bit pattern of |v|: integers in the order of the floats with NaN
 // above infinity, so that a NaN is never lost in a maximum.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ uint32_t abs_max8(const float (&v)[8]) {
-  uint32_t m = abs_bits(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max(m, abs_bits(v[i]));
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
   return m;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+template <int kN>
+__device__ __forceinline__ uint32_t abs_max(const float (&v)[kN]) {
+  static_assert(kN % 2 == 0, "pairs");
+  float m = max_nan(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+  for (int i = 2; i < kN; i += 2) m = max_nan(m, fabsf(v[i]), fabsf(v[i + 1]));
+  return __float_as_uint(m);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -192,29 +192,154 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// over the 16 lanes that share a block of 128 columns (eight per lane)
-__device__ __forceinline__ uint32_t block16_max(uint32_t m) {
+// over the kLanes lanes that share a block of 128 columns
+template <int kLanes>
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  for (int d = kLanes / 2; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
   return m;
 }
 
-// The scale of a row or block whose largest magnitude is `amax`, and the factor from values
-// to codes; zeros below kQuantTiny (a NaN amax is not below it and stays).
+// 1 / x to one ulp for 2^-126 <= x <= 2^126 (0 and NaN as IEEE), one instruction
+__device__ __forceinline__ float recip(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The scale of values whose largest magnitude is `amax`, and the factor from `u` to codes,
+// where u are the values divided by a common factor and `u_max` their largest magnitude
+// (values that are not scaled: u_max = amax).  Zeros below kQuantTiny; a NaN amax is not
+// below it and stays.  Two roundings and recip's ulp: 4 u in all; the 1/16 keeps recip's
+// argument and result normal up to the largest float.
 struct QuantScale {
   float scale, inv;
 };
-__device__ __forceinline__ QuantScale quant_scale(float amax) {
+__device__ __forceinline__ QuantScale quant_scale(float amax, float u_max) {
   QuantScale q;
   const bool zero = amax < kQuantTiny;
-  q.scale = zero ? 1.f : amax / kE4m3Max;
-  q.inv = zero ? 0.f : kE4m3Max / amax;
+  q.scale = zero ? 1.f : amax * (1.f / kE4m3Max);
+  q.inv = zero ? 0.f : (kE4m3Max / 16) * recip(u_max * 0.0625f);
   return q;
 }
 
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float inv) {
   return make_uint2(pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// ---------------------------------------------------------------------------------
+// kCols columns per thread, by the widest access that the buffers allow
+// ---------------------------------------------------------------------------------
+enum class Access { kElement, k16, k32 };  // element by element, 16 bytes, 32 bytes
+
+struct Words8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Words8 load32(const void* p) {
+  Words8 r;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                 "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void store32(void* p, const Words8& r) {
+  asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r.w[0]),
+               "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]),
+               "r"(r.w[7]), "l"(p)
+               : "memory");
+}
+
+// Columns [c, c + kCols) of a row of n; past its end zeros, nothing read.  k32: kCols 16, 32-byte
+// aligned rows, n a multiple of 16; k16: kCols 8, 16-byte aligned rows, n a multiple of 8.
+template <class T, int kCols, Access kAccess>
+__device__ __forceinline__ void load_cols(const T* row, int c, int n, float (&v)[kCols]) {
+  if constexpr (kAccess == Access::k32) {
+    static_assert(kCols == 16, "32-byte accesses take 16 columns");
+    constexpr int kEach = 32 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < kCols / kEach; ++k) {
+      Words8 r = {};
+      if (c < n) r = load32(row + c + k * kEach);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          v[k * kEach + i] = __uint_as_float(r.w[i]);
+        } else {
+          const float2 f = unpack2(r.w[i], T());
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        }
+      }
+    }
+  } else {
+    static_assert(kCols == 8, "narrower accesses take 8 columns");
+    unpack8(load8<T, kAccess == Access::k16>(row, c, n), v);
+  }
+}
+
+template <class T, int kCols, Access kAccess>
+__device__ __forceinline__ void store_cols(T* row, int c, int n, const float (&v)[kCols]) {
+  if constexpr (kAccess == Access::k32) {
+    constexpr int kEach = 32 / sizeof(T);
+    if (c < n) {
+#pragma unroll
+      for (int k = 0; k < kCols / kEach; ++k) {
+        Words8 r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (sizeof(T) == 4)
+            r.w[i] = __float_as_uint(v[k * kEach + i]);
+          else
+            r.w[i] = pack2(v[2 * i], v[2 * i + 1], T());
+        }
+        store32(row + c + k * kEach, r);
+      }
+    }
+  } else {
+    store8<T, kAccess == Access::k16>(row, c, n, v);
+  }
+}
+
+// e4m3 codes of v * inv.
+template <int kCols, Access kAccess>
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, const float (&v)[kCols],
+                                            float inv) {
+  if constexpr (kAccess == Access::k32) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                         v[4 * i + 3] * inv);
+    if (c < n) store16(row + c, make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+    store_codes8<kAccess == Access::k16>(row, c, n, quantize8(v, inv));
+  }
+}
+
+// e4m3 codes of columns that are all in the row.
+template <int kCols, Access kAccess>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int c, float (&v)[kCols]) {
+  uint32_t w[kCols / 4] = {};
+  if constexpr (kAccess == Access::k32) {
+    const uint4 r = load16(row + c);
+    w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+  } else if constexpr (kAccess == Access::k16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(row + c);
+    w[0] = r.x, w[1] = r.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      w[i / 4] |= static_cast<uint32_t>(row[c + i]) << (8 * (i & 3));
+  }
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) {
+    const float2 f = unpack_e4m3x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 }  // namespace mslkb

@@ -1,6 +1,11 @@
 // swiglu_quant.cu -- silu(gate) * up between the two expert products: e4m3 output with its
 // scales, optionally an e4m3 checkpoint of the input, and the gradient from the input or its
 // checkpoint.
+//
+// Every input is read once and every output written once; the floor is HBM's, but with a
+// sigmoid, two or three block maxima and as many roundings per element the instructions come
+// close to it.  Hence 16 columns per thread: a block of 128 columns is eight lanes (three
+// shuffles), a scale's division is shared by 16 elements, and accesses are 32 bytes wide.
 #include "host.h"
 #include "rows.cuh"
 
@@ -17,50 +22,56 @@ struct SwigluParams {
   int32_t W;
 };
 
-__device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
-
-// e4m3 of eight columns whose block of 128 is spread over 16 lanes, and the block's scale.
-template <bool kWide>
-__device__ __forceinline__ void quantize_block(const float (&v)[8], uint8_t* codes, float* scale,
-                                               int c, int n) {
-  const QuantScale s = quant_scale(__uint_as_float(block16_max(abs_max8(v))));
-  if (c < n && c % kScaleBlock == 0) scale[c / kScaleBlock] = s.scale;
-  store_codes8<kWide>(codes, c, n, quantize8(v, s.inv));
+// 1 / (1 + e^-x) with e^-x = 2^(-x log2 e): the exponent's rounding is |x| 2^-24 of it, ex2 and
+// recip are good to 2 and 1 ulp.  Far out it is exactly 0 or 1, NaN stays NaN.
+__device__ __forceinline__ float sigmoid_of(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  return recip(1.f + e);
 }
 
-// One CTA per row (kBlocks: threadIdx.y rows per CTA).
-template <class T, int kVecs, bool kWide, bool kBlocks>
-__global__ void __launch_bounds__(1024)
+// e4m3 of a thread's kCols columns, whose block of 128 is spread over 128 / kCols lanes.
+template <int kCols, Access kAccess>
+__device__ __forceinline__ void quantize_block(const float (&v)[kCols], uint8_t* codes,
+                                               float* scale, int c, int n) {
+  const float amax = __uint_as_float(block_max<kScaleBlock / kCols>(abs_max(v)));
+  const QuantScale s = quant_scale(amax, amax);
+  if (c < n && c % kScaleBlock == 0) scale[c / kScaleBlock] = s.scale;
+  store_codes<kCols, kAccess>(codes, c, n, v, s.inv);
+}
+
+// kBlocks: threadIdx.y rows per CTA, nothing shared between threads but the lanes of a block.
+// Otherwise one CTA per row, kVecs * kCols columns per thread.
+template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks>
+__global__ void __launch_bounds__(kVecs == 1 ? 512 : 1024)
     swiglu_kernel(const __grid_constant__ SwigluParams p) {
   __shared__ uint32_t slot[32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const int n = p.W;
-  const bool there = row < p.R;
+  const int n = row < p.R ? p.W : 0;  // no columns past the last row
   const T* gate = static_cast<const T*>(p.x) + row * p.ldx;
   const T* up = gate + n;
-  float a[kVecs][8];
+  float a[kVecs][kCols];
   uint32_t largest = 0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * 8;
-    float g[8], u[8];
-    unpack8(load8<T, kWide>(gate, c, there ? n : 0), g);
-    unpack8(load8<T, kWide>(up, c, there ? n : 0), u);
+    const int c = ((blockIdx.y * kVecs + i) * blockDim.x + threadIdx.x) * kCols;
+    float g[kCols], u[kCols];
+    load_cols<T, kCols, kAccess>(gate, c, n, g);
+    load_cols<T, kCols, kAccess>(up, c, n, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[i][j] = g[j] * sigmoid_of(g[j]) * u[j];
+    for (int j = 0; j < kCols; ++j) a[i][j] = g[j] * sigmoid_of(g[j]) * u[j];
     if (p.saved != nullptr) {
       uint8_t* codes = p.saved + row * 2 * n;
       float* scale = p.saved_scale + row * (2 * n / kScaleBlock);
-      quantize_block<kWide>(g, codes, scale, c, there ? n : 0);
-      quantize_block<kWide>(u, codes + n, scale + n / kScaleBlock, c, there ? n : 0);
+      quantize_block<kCols, kAccess>(g, codes, scale, c, n);
+      quantize_block<kCols, kAccess>(u, codes + n, scale + n / kScaleBlock, c, n);
     }
     if constexpr (kBlocks)
-      quantize_block<kWide>(a[i], p.q + row * n, p.scale + row * (n / kScaleBlock), c,
-                            there ? n : 0);
+      quantize_block<kCols, kAccess>(a[i], p.q + row * n, p.scale + row * (n / kScaleBlock), c, n);
     else
-      largest = max(largest, abs_max8(a[i]));
+      largest = max(largest, abs_max(a[i]));
   }
   if constexpr (!kBlocks) {
     largest = __reduce_max_sync(0xFFFFFFFFu, largest);
@@ -70,12 +81,13 @@ __global__ void __launch_bounds__(1024)
       __syncthreads();
       largest = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? slot[lane] : 0u);
     }
-    const QuantScale s = quant_scale(__uint_as_float(largest));
+    const float amax = __uint_as_float(largest);
+    const QuantScale s = quant_scale(amax, amax);
     if (threadIdx.x == 0) p.scale[row] = s.scale;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      store_codes8<kWide>(p.q + row * n, (i * blockDim.x + threadIdx.x) * 8, n,
-                          quantize8(a[i], s.inv));
+      store_codes<kCols, kAccess>(p.q + row * n, (i * blockDim.x + threadIdx.x) * kCols, n, a[i],
+                                  s.inv);
   }
 }
 
@@ -88,100 +100,99 @@ struct SwigluBackwardParams {
   int32_t W;
 };
 
-template <class T, bool kSaved8, bool kWide>
-__global__ void __launch_bounds__(256)
+template <class T, int kCols, Access kAccess, bool kSaved8>
+__global__ void __launch_bounds__(512)
     swiglu_backward_kernel(const __grid_constant__ SwigluBackwardParams p) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (row >= p.R) return;
-  const int n = p.W;
-  T* dgate = static_cast<T*>(p.dx) + row * 2 * n;
-  for (int c = threadIdx.x * 8; c < n; c += blockDim.x * 8) {
-    float d[8], g[8], u[8];
-    unpack8(load8<T, kWide>(static_cast<const T*>(p.dy) + row * n, c, n), d);
-    if constexpr (kSaved8) {
-      const uint8_t* codes = static_cast<const uint8_t*>(p.saved) + row * 2 * n;
-      const float* scale = p.saved_scale + row * (2 * n / kScaleBlock) + c / kScaleBlock;
-      uint2 gc, uc;
-      if constexpr (kWide) {
-        gc = *reinterpret_cast<const uint2*>(codes + c);
-        uc = *reinterpret_cast<const uint2*>(codes + n + c);
-      } else {
-        uint32_t w[4] = {};
+  const int n = p.W, c = (blockIdx.y * blockDim.x + threadIdx.x) * kCols;
+  if (row >= p.R || c >= n) return;
+  float d[kCols], g[kCols], u[kCols];
+  if constexpr (kSaved8) {
+    const uint8_t* codes = static_cast<const uint8_t*>(p.saved) + row * 2 * n;
+    const float* scale = p.saved_scale + row * (2 * n / kScaleBlock) + c / kScaleBlock;
+    load_codes<kCols, kAccess>(codes, c, g);
+    load_codes<kCols, kAccess>(codes + n, c, u);
+    const float gs = scale[0], us = scale[n / kScaleBlock];
+    load_cols<T, kCols, kAccess>(static_cast<const T*>(p.dy) + row * n, c, n, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i / 4] |= static_cast<uint32_t>(codes[c + i]) << (8 * (i & 3));
-          w[2 + i / 4] |= static_cast<uint32_t>(codes[n + c + i]) << (8 * (i & 3));
-        }
-        gc = make_uint2(w[0], w[1]);
-        uc = make_uint2(w[2], w[3]);
-      }
-      unpack_e4m3x8(gc, g);
-      unpack_e4m3x8(uc, u);
-      const float gs = scale[0], us = scale[n / kScaleBlock];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] *= gs, u[j] *= us;
-    } else {
-      const T* gate = static_cast<const T*>(p.saved) + row * 2 * n;
-      unpack8(load8<T, kWide>(gate, c, n), g);
-      unpack8(load8<T, kWide>(gate + n, c, n), u);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = sigmoid_of(g[j]);
-      u[j] = d[j] * u[j] * s * (1.f + g[j] * (1.f - s));
-      g[j] = d[j] * g[j] * s;
-    }
-    store8<T, kWide>(dgate, c, n, u);
-    store8<T, kWide>(dgate + n, c, n, g);
+    for (int j = 0; j < kCols; ++j) g[j] *= gs, u[j] *= us;
+  } else {
+    const T* gate = static_cast<const T*>(p.saved) + row * 2 * n;
+    load_cols<T, kCols, kAccess>(gate, c, n, g);
+    load_cols<T, kCols, kAccess>(gate + n, c, n, u);
+    load_cols<T, kCols, kAccess>(static_cast<const T*>(p.dy) + row * n, c, n, d);
   }
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) {
+    const float s = sigmoid_of(g[j]);
+    u[j] = d[j] * u[j] * s * fmaf(g[j], 1.f - s, 1.f);
+    g[j] = d[j] * g[j] * s;
+  }
+  T* dgate = static_cast<T*>(p.dx) + row * 2 * n;
+  store_cols<T, kCols, kAccess>(dgate, c, n, u);
+  store_cols<T, kCols, kAccess>(dgate + n, c, n, g);
 }
 
-template <class T, int kVecs, bool kWide>
+// ---------------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------------
+// Threads of a CTA over rows of `lanes` steps: x along a row, y rows, 256 to 512 in all.  With
+// block_lanes > 1 (a multiple of 8): whole blocks of 128 columns along x, whole warps.
+dim3 tile_threads(int64_t lanes, int64_t block_lanes) {
+  const int64_t x = (lanes + block_lanes - 1) / block_lanes * block_lanes;
+  if (x > 128) return dim3(256);
+  const int64_t y = (256 / x + 3) / 4 * 4;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+}
+
+template <class T, int kCols, Access kAccess>
 cudaError_t launch_swiglu(const SwigluParams& p, bool blocks, void* stream) {
-  int64_t x = ((p.W + 7) / 8 + kVecs - 1) / kVecs;
-  if (blocks) {  // rows of 16-lane blocks: several narrow rows per CTA
-    x = (x + 15) / 16 * 16;
-    int64_t y = 256 / x;
-    if (y == 0) {
-      y = 1;
-      x = (x + 31) / 32 * 32;
-    } else if (x * y % 32 != 0) {
-      ++y;  // whole warps
-    }
-    return launch_dependent(swiglu_kernel<T, kVecs, kWide, true>,
-                            dim3(static_cast<unsigned>((p.R + y - 1) / y)),
-                            dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), 0, stream,
-                            p);
+  const int64_t lanes = (p.W + kCols - 1) / kCols;
+  if (blocks) {
+    const dim3 block = tile_threads(lanes, kScaleBlock / kCols);
+    const dim3 grid(static_cast<unsigned>((p.R + block.y - 1) / block.y),
+                    static_cast<unsigned>((lanes + block.x - 1) / block.x));
+    return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, true>, grid, block, 0, stream, p);
   }
-  x = (x + 31) / 32 * 32;
-  return launch_dependent(swiglu_kernel<T, kVecs, kWide, false>,
-                          dim3(static_cast<unsigned>(p.R)), dim3(static_cast<unsigned>(x)), 0,
+  const dim3 grid(static_cast<unsigned>(p.R));
+  const auto threads = [&](int vecs) {
+    return dim3(static_cast<unsigned>(((lanes + vecs - 1) / vecs + 31) / 32 * 32));
+  };
+  if (lanes <= 512)
+    return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, false>, grid, threads(1), 0,
+                            stream, p);
+  constexpr int kMost = MSLKB_MAX_HIDDEN / kCols / 1024;
+  return launch_dependent(swiglu_kernel<T, kCols, kMost, kAccess, false>, grid, threads(kMost), 0,
                           stream, p);
 }
 
 template <class T>
-cudaError_t launch_swiglu(const SwigluParams& p, bool wide, bool blocks, void* stream) {
-  if (!wide) return launch_swiglu<T, 4, false>(p, blocks, stream);
-  if (p.W <= 8192) return launch_swiglu<T, 1, true>(p, blocks, stream);
-  return launch_swiglu<T, 4, true>(p, blocks, stream);
+cudaError_t launch_swiglu(const SwigluParams& p, Access access, bool blocks, void* stream) {
+  if (access == Access::k32) return launch_swiglu<T, 16, Access::k32>(p, blocks, stream);
+  if (access == Access::k16) return launch_swiglu<T, 8, Access::k16>(p, blocks, stream);
+  return launch_swiglu<T, 8, Access::kElement>(p, blocks, stream);
+}
+
+template <class T, int kCols, Access kAccess>
+cudaError_t launch_backward(const SwigluBackwardParams& p, void* stream) {
+  const int64_t lanes = (p.W + kCols - 1) / kCols;
+  const dim3 block = tile_threads(lanes, 1);
+  const dim3 grid(static_cast<unsigned>((p.R + block.y - 1) / block.y),
+                  static_cast<unsigned>((lanes + block.x - 1) / block.x));
+  return p.saved_scale != nullptr
+             ? launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, true>, grid, block, 0,
+                                stream, p)
+             : launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, false>, grid, block, 0,
+                                stream, p);
 }
 
 template <class T>
-cudaError_t launch_swiglu_backward(const SwigluBackwardParams& p, bool wide, void* stream) {
-  int64_t x = (p.W + 7) / 8;
-  x = x > 256 ? 256 : x;
-  const int64_t y = 256 / x;
-  const dim3 grid(static_cast<unsigned>((p.R + y - 1) / y));
-  const dim3 block(static_cast<unsigned>(x), static_cast<unsigned>(y));
-  if (p.saved_scale != nullptr)
-    return wide ? launch_dependent(swiglu_backward_kernel<T, true, true>, grid, block, 0, stream, p)
-                : launch_dependent(swiglu_backward_kernel<T, true, false>, grid, block, 0, stream,
-                                   p);
-  return wide ? launch_dependent(swiglu_backward_kernel<T, false, true>, grid, block, 0, stream, p)
-              : launch_dependent(swiglu_backward_kernel<T, false, false>, grid, block, 0, stream,
-                                 p);
+cudaError_t launch_backward(const SwigluBackwardParams& p, Access access, void* stream) {
+  if (access == Access::k32) return launch_backward<T, 16, Access::k32>(p, stream);
+  if (access == Access::k16) return launch_backward<T, 8, Access::k16>(p, stream);
+  return launch_backward<T, 8, Access::kElement>(p, stream);
 }
 
 mslkb_status check_swiglu(int64_t R, int64_t W, int32_t dtype) {
@@ -208,18 +219,24 @@ mslkb_status mslkb_swiglu_quant(const void* x, void* q, float* scale, void* save
     return MSLKB_ERR_NULL;
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
-  const bool wide = W % 8 == 0 && ldx * dtype_bytes(dtype) % 16 == 0 && aligned_to(x, 16) &&
-                    aligned_to(q, 8) && aligned_to(saved, 8);
+  const int64_t size = dtype_bytes(dtype);
+  Access access = Access::kElement;
+  if (W % 16 == 0 && ldx * size % 32 == 0 && aligned_to(x, 32) && aligned_to(q, 16) &&
+      aligned_to(saved, 16))
+    access = Access::k32;
+  else if (W % 8 == 0 && ldx * size % 16 == 0 && aligned_to(x, 16) && aligned_to(q, 8) &&
+           aligned_to(saved, 8))
+    access = Access::k16;
   const SwigluParams p{x, static_cast<uint8_t*>(q), scale, static_cast<uint8_t*>(saved),
                        saved_scale, R, ldx, static_cast<int32_t>(W)};
   TraceRange range("swiglu_quant", R);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_swiglu<__nv_bfloat16>(p, wide, groupwise != 0, stream);
+    e = launch_swiglu<__nv_bfloat16>(p, access, groupwise != 0, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_swiglu<__half>(p, wide, groupwise != 0, stream);
+    e = launch_swiglu<__half>(p, access, groupwise != 0, stream);
   else
-    e = launch_swiglu<float>(p, wide, groupwise != 0, stream);
+    e = launch_swiglu<float>(p, access, groupwise != 0, stream);
   return launch_status(e);
 }
 
@@ -234,17 +251,22 @@ mslkb_status mslkb_swiglu_quant_backward(const void* dy, const void* saved,
   if (dy == nullptr || saved == nullptr || dx == nullptr) return MSLKB_ERR_NULL;
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
-  const bool wide = W % 8 == 0 && aligned_to(dy, 16) && aligned_to(dx, 16) &&
-                    aligned_to(saved, saved_scale != nullptr ? 8 : 16);
+  Access access = Access::kElement;
+  if (W % 16 == 0 && aligned_to(dy, 32) && aligned_to(dx, 32) &&
+      aligned_to(saved, saved_scale != nullptr ? 16 : 32))
+    access = Access::k32;
+  else if (W % 8 == 0 && aligned_to(dy, 16) && aligned_to(dx, 16) &&
+           aligned_to(saved, saved_scale != nullptr ? 8 : 16))
+    access = Access::k16;
   const SwigluBackwardParams p{dy, saved, saved_scale, dx, R, static_cast<int32_t>(W)};
   TraceRange range("swiglu_quant_backward", R);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_swiglu_backward<__nv_bfloat16>(p, wide, stream);
+    e = launch_backward<__nv_bfloat16>(p, access, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_swiglu_backward<__half>(p, wide, stream);
+    e = launch_backward<__half>(p, access, stream);
   else
-    e = launch_swiglu_backward<float>(p, wide, stream);
+    e = launch_backward<float>(p, access, stream);
   return launch_status(e);
 }
 

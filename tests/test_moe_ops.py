@@ -71,7 +71,10 @@ def check_norm(out, x, residual, weight, groupwise, eps=EPS, want_y=True, want_r
 NORM_CASES = [  # tokens, hidden, groupwise
     (1, 1, False), (3, 7, False), (5, 128, True), (1, 7168, False), (2, 7168, True),
     (7, 1000, False), (4, 1025, False), (17, 8192, True), (3, 8200, False), (2, 16384, True),
-    (2, 16392, False), (2, 32768, True), (1, 32768, False), (2, 32767, False), (300, 256, True)]
+    (2, 16392, False), (2, 32768, True), (1, 32768, False), (2, 32767, False), (300, 256, True),
+    # many rows: the persistent kernel, CTAs with several rows and with one
+    (609, 7168, False), (1500, 8192, True), (2000, 128, True), (1300, 1000, False),
+    (700, 4096, False), (1250, 4104, False)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
@@ -166,7 +169,9 @@ def test_norm_extremes():
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("T,H,with_res", [(1, 1, True), (3, 129, False), (1, 7168, True),
                                           (700, 512, True), (50, 1000, False), (5, 16384, True),
-                                          (4, 32768, True), (3, 32767, False)])
+                                          (4, 32768, True), (3, 32767, False),
+                                          (1216, 7168, True), (900, 8192, False),
+                                          (1000, 136, True), (305, 4096, True)])
 def test_norm_backward(T, H, with_res, dtype):
     g = gen(T + H)
     dy, h = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype, scale=2.0)
@@ -597,7 +602,8 @@ SWIGLU_REL = 16 * U
 @pytest.mark.parametrize("R,W,groupwise,checkpoint", [
     (1, 2048, False, False), (1, 128, True, True), (33, 2048, True, True), (5, 384, False, True),
     (3, 1, False, False), (17, 1000, False, False), (6, 1003, False, False), (40, 640, True, False),
-    (3, 4224, True, True), (2, 8192, True, True), (2, 8320, True, True), (2, 32768, False, True),
+    (3, 4224, True, True), (9, 3968, True, True), (70, 1920, True, False), (600, 256, True, True),
+    (5, 16384, True, True), (5, 12288, False, False), (2, 8192, True, True), (2, 8320, True, True), (2, 32768, False, True),
     (1, 32767, False, False)])
 def test_swiglu(R, W, groupwise, checkpoint, dtype):
     g = gen(R + W)
@@ -651,7 +657,8 @@ def test_swiglu_extremes():
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
-@pytest.mark.parametrize("R,W", [(1, 128), (1, 2048), (70, 384), (5, 4096), (3, 33), (4, 1000)])
+@pytest.mark.parametrize("R,W", [(1, 128), (1, 2048), (70, 384), (5, 4096), (3, 33), (4, 1000),
+                                 (300, 125), (9, 3968), (130, 1), (3, 32768)])
 def test_swiglu_backward(R, W, dtype):
     g = gen(R * W)
     x, dy = randn(g, R, 2 * W, dtype=dtype, scale=2.0), randn(g, R, W, dtype=dtype)
