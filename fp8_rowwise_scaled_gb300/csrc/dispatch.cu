@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kTileWarps * 32)
     const int e = e0 + threadIdx.x;
     uint32_t before = 0, total = 0;
     if (e < E) {
+#pragma unroll 16
       for (int i = 0; i < tiles; ++i) {
         const uint32_t c = counts[static_cast<int64_t>(i) * E + e];
         if (i < tile) before += c;
@@ -168,6 +169,62 @@ __global__ void __launch_bounds__(512) copy_kernel(const __grid_constant__ CopyP
   if (threadIdx.x < p.top_k) dest[threadIdx.x] = p.dest[t * p.top_k + threadIdx.x];
   __syncthreads();
   copy_row<kWide>(p, t, dest);
+}
+
+// Few choices: one launch, no workspace.  The CTA of a token finds each of its rows by itself:
+// the row of choice i is the number of choices that come before it, those of a lower expert
+// and the earlier ones of its own.  One more CTA counts the experts' rows.
+struct DirectParams {
+  CopyParams copy;
+  const int32_t* ids;
+  int32_t* dest;
+  int64_t* m_sizes;
+  int32_t T, E;
+};
+
+template <bool kWide>
+__global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ DirectParams p) {
+  __shared__ uint32_t before[MSLKB_MAX_EXPERTS];  // a token's rows; or the experts' counts
+  __shared__ int32_t dest[MSLKB_MAX_TOPK];
+  const int k = p.copy.top_k, N = p.T * k, lane = threadIdx.x & 31;
+  const int counters = blockIdx.x == p.T ? p.E : k;
+  for (int i = threadIdx.x; i < counters; i += blockDim.x) before[i] = 0;
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  __syncthreads();
+  if (blockIdx.x == p.T) {
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+      const int e = p.ids[i];
+      if (e >= 0 && e < p.E) atomicAdd(&before[e], 1u);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.m_sizes[e] = before[e];
+    return;
+  }
+  const int first = blockIdx.x * k;
+  // a lane of each warp holds one of the token's choices; foreign ids order last and count
+  // for nobody
+  int own = lane < k ? p.ids[first + lane] : -1;
+  if (own < 0 || own >= p.E) own = -1;
+  for (int i0 = 0; i0 < N; i0 += blockDim.x) {
+    const int i = i0 + threadIdx.x;
+    int e = i < N ? p.ids[i] : -1;
+    if (e < 0 || e >= p.E) e = 0x7FFFFFFF;
+    for (int j = 0; j < k; ++j) {
+      const int mine = __shfl_sync(0xFFFFFFFFu, own, j);
+      const uint32_t earlier =
+          __ballot_sync(0xFFFFFFFFu, e < mine || (e == mine && i < first + j));
+      if (lane == 0 && earlier != 0) atomicAdd(&before[j], __popc(earlier));
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < k) {
+    const int row = own >= 0 ? static_cast<int>(before[threadIdx.x]) : -1;
+    dest[threadIdx.x] = row;
+    p.dest[first + threadIdx.x] = row;
+  }
+  __syncthreads();
+  copy_row<kWide>(p.copy, blockIdx.x, dest);
 }
 
 // ---------------------------------------------------------------------------------
@@ -311,6 +368,9 @@ int row_threads(int64_t vectors) {
 
 int64_t tiles_of(int64_t choices) { return (choices + kTile - 1) / kTile; }
 
+// Choices up to which each token's CTA finds its rows by itself.
+constexpr int64_t kDirectChoices = 2048;
+
 template <class T>
 cudaError_t launch_combine(const CombineParams& p, int64_t T_, bool wide, void* stream) {
   const dim3 grid(static_cast<unsigned>(T_)), block(row_threads((p.H + 7) / 8));
@@ -343,6 +403,7 @@ int64_t mslkb_moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E) 
   if (T <= 0 || top_k <= 0 || E <= 0 || E > MSLKB_MAX_EXPERTS || top_k > MSLKB_MAX_TOPK ||
       T > MSLKB_MAX_DIM / 2 / top_k)
     return 0;
+  if (T * top_k <= mslkb::kDirectChoices) return 0;
   return mslkb::tiles_of(T * top_k) * E * static_cast<int64_t>(sizeof(uint32_t));
 }
 
@@ -363,8 +424,9 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
     if (ids == nullptr || dest == nullptr) return MSLKB_ERR_NULL;
     if (row_bytes > 0 && (x == nullptr || x_out == nullptr)) return MSLKB_ERR_NULL;
     if (scale_cols > 0 && (x_scale == nullptr || scale_out == nullptr)) return MSLKB_ERR_NULL;
-    if (workspace_bytes < mslkb_moe_dispatch_workspace_bytes(T, top_k, E) ||
-        (E > 0 && (workspace == nullptr || !aligned_to(workspace, 16))))
+    const int64_t need = mslkb_moe_dispatch_workspace_bytes(T, top_k, E);
+    if (need > 0 &&
+        (workspace == nullptr || !aligned_to(workspace, 16) || workspace_bytes < need))
       return MSLKB_ERR_WORKSPACE;
   }
   int sms = 0;
@@ -384,6 +446,15 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
                      scale_out, row_bytes, static_cast<int32_t>(scale_cols),
                      static_cast<int32_t>(top_k)};
   TraceRange range("moe_dispatch", T);
+  const dim3 copy_block(row_threads(wide ? row_bytes / 16 : row_bytes));
+  if (N <= kDirectChoices) {
+    const DirectParams d{p, ids, dest, m_sizes, static_cast<int32_t>(T), experts};
+    const dim3 grid(static_cast<unsigned>(T) + 1);
+    const dim3 block(copy_block.x < 256 ? 256 : copy_block.x);  // they share the counting too
+    return launch_status(wide
+                             ? launch_dependent(direct_kernel<true>, grid, block, 0, stream, d)
+                             : launch_dependent(direct_kernel<false>, grid, block, 0, stream, d));
+  }
   cudaError_t e = launch_dependent(count_kernel, dim3(tiles), dim3(256),
                                    sizeof(uint32_t) * experts, stream, ids, counts, N, experts);
   if (e == cudaSuccess)
@@ -392,9 +463,8 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
                          m_sizes, N, experts, tiles);
   if (e == cudaSuccess && (row_bytes > 0 || scale_cols > 0)) {
     const dim3 grid(static_cast<unsigned>(T));
-    const dim3 block(row_threads(wide ? row_bytes / 16 : row_bytes));
-    e = wide ? launch_dependent(copy_kernel<true>, grid, block, 0, stream, p)
-             : launch_dependent(copy_kernel<false>, grid, block, 0, stream, p);
+    e = wide ? launch_dependent(copy_kernel<true>, grid, copy_block, 0, stream, p)
+             : launch_dependent(copy_kernel<false>, grid, copy_block, 0, stream, p);
   }
   return launch_status(e);
 }

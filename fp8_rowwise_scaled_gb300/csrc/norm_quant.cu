@@ -1,10 +1,11 @@
 // norm_quant.cu -- residual addition + root-mean-square norm + e4m3 output, and the gradient.
 //
 // Forward, the row in registers between its one read and its one write:
-//   h = x + residual, u = h * weight, and in one pass sum(h^2) and max|u|.
-// The codes need no rstd: y / scale = h rstd w * 448 / (rstd max|h w|) = u * (448 / max|u|).
-// So one exchange over the CTA gives both rstd and the row's scale (block scales need only
-// the 16 lanes that hold a block), where norm-then-quantise would need two.
+//   h = x + residual, u = h * weight, and in one pass sum(h^2) and max|u|;
+// rstd is the row's common factor, so max|y| = rstd max|u| and one exchange over the CTA gives
+// both rstd and the row's scale (block scales need only the 16 lanes that hold a block), where
+// norm-then-quantise would need two.  Where y is not asked for, the codes do without rstd:
+// y / scale = h rstd w * 448 / (rstd max|h w|) = u * (448 / max|u|).
 //
 // Both directions read every input once and write every output once and are bound by HBM.
 // With a row per CTA, the CTA's loads wait while it reduces and stores; so for many rows the
@@ -90,7 +91,7 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, flo
   QuantScale s;
   if constexpr (!kBlocks) {
     const float m = __uint_as_float(largest);
-    s = quant_scale(m * rstd, m);
+    s = quant_scale(m * rstd, p.y != nullptr ? m * rstd : m);
     if (threadIdx.x == 0) p.scale[row] = s.scale;
   }
 #pragma unroll
@@ -98,21 +99,22 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, flo
     const int c = (i * blockDim.x + threadIdx.x) * 8;
     if constexpr (kBlocks) {
       const float m = __uint_as_float(block_largest[i]);
-      s = quant_scale(m * rstd, m);
+      s = quant_scale(m * rstd, p.y != nullptr ? m * rstd : m);
       if (c < n && c % kScaleBlock == 0)
         p.scale[row * (n / kScaleBlock) + c / kScaleBlock] = s.scale;
     }
     float w[8], v[8];
     weight(i, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[i][j] * w[j];
-    store_codes8<kWide>(p.q + row * n, c, n, quantize8(v, s.inv));
     if (p.y != nullptr) {
       // (h * rstd) * weight: h * weight alone may fall among the subnormals
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = h[i][j] * rstd * w[j];
       store8<T, kWide>(static_cast<T*>(p.y) + row * n, c, n, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * w[j];
     }
+    store_codes8<kWide>(p.q + row * n, c, n, quantize8(v, s.inv));
   }
 }
 

@@ -1,9 +1,13 @@
 // route.cu -- the choice of each token's experts from the router's logits, and its gradient.
 //
 // One warp per token.  A lane holds kPer consecutive experts in registers, as integer keys
-// that order like their choice values (0: masked), so that the largest key of the warp is
-// one redux instruction and ties fall to the lowest lane, then to its lowest expert: the
-// lowest expert index.
+// that order like their choice values, so that the largest of the warp is one redux
+// instruction.  Bound by instructions, not by memory: 256 experts are 8 scores per lane, and
+// top_k dependent maxima.  The loop over the maxima is kept short by sorting each lane's keys
+// once, with the expert's index in place of the key's lowest bits: keys are then unique, the
+// lane that holds the maximum drops its first key, and the maximum itself names the expert.
+// Where the bits that gave way to the index might have decided (checked with the exact
+// values of the chosen), the choice is made again by exact keys.
 #include "host.h"
 #include "rows.cuh"
 
@@ -24,28 +28,46 @@ struct RouteParams {
   int32_t groups, top_groups, group_top;
   int32_t by_logits;  // softmax whose order is that of the logits
   int32_t renormalize;
+  int32_t wide;       // rows in whole, aligned 16-byte pieces
   float scale;
 };
 
-// An integer that orders as the float does: NaN above all, -inf (masked) 0.
+// An integer that orders as the float does: NaN above all; -inf, which masks, is kMaskedKey,
+// and nothing else comes that low.
+constexpr uint32_t kMaskedKey = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xFFFFFFFFu;
-  if (v == kMasked) return 0;
-  const uint32_t b = __float_as_uint(v + 0.f);  // -0 orders as +0
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 as +0, every NaN as the one above +inf
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-  if (k == 0) return kMasked;
-  if (k == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// (the IEEE forms: the choice is defined by the rounded scores)
 __device__ __forceinline__ float sigmoid_of(float x) { return 1.f / (1.f + expf(-x)); }
 
 // What a group is worth: its best choice, and with group_top = 2 the second as well.
 __device__ __forceinline__ uint32_t worth_key(uint32_t best, uint32_t second, int group_top) {
-  if (group_top == 1 || second == 0) return best;
+  if (group_top == 1 || second <= kMaskedKey) return best;
   return order_key(key_value(best) + key_value(second));
+}
+
+// Descending order of a lane's keys (odd-even merge sort; Batcher 1968).
+template <int kN>
+__device__ __forceinline__ void sort_keys(uint32_t (&s)[kN]) {
+#pragma unroll
+  for (int p = 1; p < kN; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < kN; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < kN && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = s[i + j], b = s[i + j + k];
+            s[i + j] = max(a, b);
+            s[i + j + k] = min(a, b);
+          }
 }
 
 template <class T, int kPer>
@@ -61,9 +83,34 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int first = lane * kPer;
 
   float x[kPer];
+  bool loaded = false;
+  if constexpr (kPer * sizeof(T) >= 16) {
+    if (p.wide) {
+      constexpr int kPiece = 16 / sizeof(T);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    x[i] = first + i < p.E ? to_float(row[first + i]) : kMasked;
+      for (int i = 0; i < kPer; i += kPiece) {
+        const bool in = first + i < p.E;
+        const uint4 r = in ? load16(row + first + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            x[i + j] = in ? __uint_as_float(w[j]) : kMasked;
+          } else {
+            const float2 f = unpack2(w[j], T());
+            x[i + 2 * j] = in ? f.x : kMasked;
+            x[i + 2 * j + 1] = in ? f.y : kMasked;
+          }
+        }
+      }
+      loaded = true;
+    }
+  }
+  if (!loaded) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      x[i] = first + i < p.E ? to_float(row[first + i]) : kMasked;
+  }
 
   // softmax over all experts: its maximum and sum
   float top = 0.f, total = 1.f;
@@ -80,17 +127,16 @@ __global__ void __launch_bounds__(kWarps * 32)
     top = m;
     total = warp_sum(s);
   }
-
+  // what expert e with logit v is chosen by
+  auto choice = [&](float v, int e) {
+    if (p.by_logits || v == kMasked) return v;
+    float c = p.sigmoid ? sigmoid_of(v) : expf(v - top) / total;
+    if (p.bias != nullptr) c += p.bias[e];
+    return c;
+  };
   uint32_t key[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    float c = x[i];
-    if (!p.by_logits && c != kMasked) {
-      c = p.sigmoid ? sigmoid_of(c) : expf(c - top) / total;
-      if (p.bias != nullptr) c += p.bias[first + i];
-    }
-    key[i] = order_key(c);
-  }
+  for (int i = 0; i < kPer; ++i) key[i] = order_key(choice(x[i], first + i));
 
   if (p.groups > 1) {
     const int per = p.E / p.groups;
@@ -146,33 +192,65 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
 
-  // the best key of the lane, and where it is
-  uint32_t best = key[0];
-  int at = 0;
-#pragma unroll
-  for (int i = 1; i < kPer; ++i)
-    if (key[i] > best) best = key[i], at = i;
+  // keys with the expert's index in the lowest bits, the lower index larger
+  constexpr uint32_t kIndex = 32 * kPer - 1;
   int id = -1;  // lane j: the j-th choice
-  for (int j = 0; j < p.top_k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (m == 0) break;
-    const int winner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-    const int chosen = __shfl_sync(0xFFFFFFFFu, first + at, winner);
-    if (lane == j) id = chosen;
-    if (lane == winner) {
+  float logit = kMasked;
+  {
+    uint32_t s[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == at) key[i] = 0;
-      best = key[0];
-      at = 0;
+    for (int i = 0; i < kPer; ++i) s[i] = (key[i] & ~kIndex) | (kIndex - (first + i));
+    sort_keys(s);
+    uint32_t mine = 0, last = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, s[0]);
+      if ((m | kIndex) <= kMaskedKey) break;
+      last = m;
+      if (lane == j) mine = m;
+      if (s[0] == m) {
 #pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (key[i] > best) best = key[i], at = i;
+        for (int i = 0; i + 1 < kPer; ++i) s[i] = s[i + 1];
+        s[kPer - 1] = 0;
+      }
+    }
+    if (mine != 0) {
+      id = static_cast<int>(kIndex - (mine & kIndex));
+      logit = to_float(row[id]);  // an L1 hit
+    }
+    // A logit of 16 bits has the index's bits to spare.  Otherwise the choice stands if the
+    // chosen are in the order of their exact keys, and the next one differs in the bits kept.
+    if (!(p.by_logits && sizeof(T) == 2)) {
+      const uint32_t next = __reduce_max_sync(0xFFFFFFFFu, s[0]);
+      const uint32_t exact = id >= 0 ? order_key(choice(logit, id)) : 0;
+      const uint32_t above = __shfl_up_sync(0xFFFFFFFFu, exact, 1);
+      const int above_id = __shfl_up_sync(0xFFFFFFFFu, id, 1);
+      const bool wrong = id >= 0 && lane > 0 && (above < exact || (above == exact && above_id > id));
+      const bool close = last != 0 && ((last ^ next) & ~kIndex) == 0;
+      if (__any_sync(0xFFFFFFFFu, wrong) || close) {
+        uint32_t best = 0;
+        int at = 0;
+        id = -1;
+        for (int j = 0; j < p.top_k; ++j) {
+          best = key[0];
+          at = 0;
+#pragma unroll
+          for (int i = 1; i < kPer; ++i)
+            if (key[i] > best) best = key[i], at = i;
+          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+          if (m <= kMaskedKey) break;
+          const int winner = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+          const int chosen = __shfl_sync(0xFFFFFFFFu, first + at, winner);
+          if (lane == j) id = chosen;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (first + i == chosen) key[i] = 0;
+        }
+        logit = id >= 0 ? to_float(row[id]) : kMasked;
+      }
     }
   }
 
-  // weights, one choice per lane (the logit is read again: an L1 hit)
-  const float logit = id >= 0 ? to_float(row[id]) : kMasked;
+  // weights, one choice per lane
   float w = 0.f;
   if (p.sigmoid) {
     if (id >= 0) w = sigmoid_of(logit);
@@ -331,10 +409,12 @@ mslkb_status mslkb_route_experts(const void* logits, const float* bias, int32_t*
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const bool by_logits = score == MSLKB_SOFTMAX && bias == nullptr &&
                          (group_top == 1 || num_groups == 1);
+  const int64_t size = dtype_bytes(dtype);
+  const bool wide = aligned_to(logits, 16) && ld * size % 16 == 0 && E * size % 16 == 0;
   const RouteParams p{logits, bias, ids, weights, T, ld, static_cast<int32_t>(E),
                       static_cast<int32_t>(top_k), score == MSLKB_SIGMOID,
                       static_cast<int32_t>(num_groups), static_cast<int32_t>(topk_groups),
-                      group_top, by_logits, renormalize, static_cast<float>(scale)};
+                      group_top, by_logits, renormalize, wide, static_cast<float>(scale)};
   TraceRange range("route_experts", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)

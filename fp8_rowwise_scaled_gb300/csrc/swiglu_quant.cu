@@ -43,7 +43,7 @@ __device__ __forceinline__ void quantize_block(const float (&v)[kCols], uint8_t*
 // kBlocks: threadIdx.y rows per CTA, nothing shared between threads but the lanes of a block.
 // Otherwise one CTA per row, kVecs * kCols columns per thread.
 template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks>
-__global__ void __launch_bounds__(kVecs == 1 ? 512 : 1024)
+__global__ void __launch_bounds__(kBlocks ? 256 : (kVecs == 1 ? 512 : 1024), kBlocks ? 4 : 1)
     swiglu_kernel(const __grid_constant__ SwigluParams p) {
   __shared__ uint32_t slot[32];
   ptx::griddep_wait();
@@ -101,7 +101,7 @@ struct SwigluBackwardParams {
 };
 
 template <class T, int kCols, Access kAccess, bool kSaved8>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(256)
     swiglu_backward_kernel(const __grid_constant__ SwigluBackwardParams p) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -138,12 +138,13 @@ __global__ void __launch_bounds__(512)
 // ---------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------
-// Threads of a CTA over rows of `lanes` steps: x along a row, y rows, 256 to 512 in all.  With
+// Threads of a CTA over rows of `lanes` steps: x along a row, y rows, at most 256 in all.  With
 // block_lanes > 1 (a multiple of 8): whole blocks of 128 columns along x, whole warps.
 dim3 tile_threads(int64_t lanes, int64_t block_lanes) {
-  const int64_t x = (lanes + block_lanes - 1) / block_lanes * block_lanes;
+  int64_t x = (lanes + block_lanes - 1) / block_lanes * block_lanes;
   if (x > 128) return dim3(256);
-  const int64_t y = (256 / x + 3) / 4 * 4;
+  if (x > 64) x = (x + 31) / 32 * 32;
+  const int64_t y = x > 64 ? 256 / x : 256 / x / 4 * 4;
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 

@@ -151,64 +151,75 @@ class SwigluQuant(NamedTuple):
 
 
 _torch = None
-_DTYPES = {}       # torch dtype -> mslkb_dtype
-_DEVICE = None     # the current device's index
+_DTYPES = {}            # torch dtype -> mslkb_dtype
+_F32 = _I32 = _E4M3 = None
+_device = _raw_stream = None
 
 
 def _setup():
-    """Fills the tables that need torch, which the package imports only when it is used."""
-    global _torch, _DEVICE
+    """Fills the names that need torch, which the package imports only when it is used."""
+    global _torch, _F32, _I32, _E4M3, _device, _raw_stream
     import torch
     _DTYPES.update({torch.bfloat16: MSLKB_BF16, torch.float16: MSLKB_FP16,
                     torch.float32: MSLKB_FP32})
-    _DEVICE = torch.cuda.current_device
+    _F32, _I32, _E4M3 = torch.float32, torch.int32, torch.float8_e4m3fn
+    # the index of the current device, and its current stream as a cudaStream_t: at a few
+    # microseconds per call, torch.cuda.current_stream(i).cuda_stream is 1 of them, this 0.1
+    _device = torch._C._cuda_getDevice
+    _raw_stream = torch._C._cuda_getCurrentRawStream
     _torch = torch
 
 
-def _dtype(t, name):
-    """The mslkb_dtype of a tensor that leads a call, which must be on the current device."""
+def _lead(t, name):
+    """The mslkb_dtype and device of the tensor that leads a call: on the current device."""
     if _torch is None:
         _setup()
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != _DEVICE():
-        raise ValueError(f"{name} is on another device than the current one")
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise TypeError(f"{name}: dtype {t.dtype} is not bfloat16, float16 or float32")
-    return d
+    return d, _on_device(t, name)
 
 
-def _dense(t, name, dtype, shape, device):
+def _on_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != _device():
+        raise ValueError(f"{name} is on another device than the current one")
+    return dev
+
+
+def _dense(t, name, dtype, shape, dev):
     """Checks a dense tensor of a call; returns its address."""
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype and not (dtype is _torch.float8_e4m3fn and t.dtype is _torch.uint8):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.dtype is not dtype and not (dtype is _E4M3 and t.dtype is _torch.uint8):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.get_device() != device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the same device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name, dtype, shape, device):
+def _rows(t, name, dtype, shape, dev):
     """Checks an input whose rows may be slices of wider rows; returns (address, elements from
     row to row)."""
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.is_contiguous():
+        return _dense(t, name, dtype, shape, dev), shape[1]
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.get_device() != device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the same device")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1]
     if t.stride(1) != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     ld = t.stride(0) if shape[0] > 1 else shape[1]
@@ -217,25 +228,20 @@ def _rows(t, name, dtype, shape, device):
     return t.data_ptr(), ld
 
 
-class _Stream:
-    """The raw stream of a call; `new` makes tensors that belong to it."""
+def _stream(stream, dev):
+    """The cudaStream_t of a call."""
+    return _raw_stream(dev) if stream is None else _fx._stream_ptr(stream)
 
-    def __init__(self, stream, device):
-        self.stream = stream
-        if stream is None:
-            self.raw = _torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.raw = _fx._stream_ptr(stream)
 
-    def new(self, shape, dtype, device, zero=False):
-        make = _torch.zeros if zero else _torch.empty
-        device = _torch.device("cuda", device)
-        if self.stream is None:
-            return make(shape, dtype=dtype, device=device)
-        s = self.stream if hasattr(self.stream, "cuda_stream") else \
-            _torch.cuda.ExternalStream(self.raw, device=device)
-        with _torch.cuda.stream(s):
-            return make(shape, dtype=dtype, device=device)
+def _new(stream, dev, shape, dtype, zero=False):
+    """A tensor that belongs to the stream of the call."""
+    make = _torch.zeros if zero else _torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device="cuda")
+    s = stream if hasattr(stream, "cuda_stream") else \
+        _torch.cuda.ExternalStream(int(stream), device=_torch.device("cuda", dev))
+    with _torch.cuda.stream(s):
+        return make(shape, dtype=dtype, device="cuda")
 
 
 def _matrix(t, name):
@@ -245,11 +251,14 @@ def _matrix(t, name):
 
 
 def _unpack(out, count):
-    if out is None:
-        return (None,) * count
     if len(out) != count:
         raise ValueError(f"out must hold {count} tensors (None where there is none)")
     return out
+
+
+def _same(t, name, wanted):
+    if (t is not None) != bool(wanted):
+        raise ValueError(f"out: {name} must be {'a tensor' if wanted else 'None'}")
 
 
 def _scale_shape(rows, cols, groupwise):
@@ -265,10 +274,10 @@ def _call(status, where):
         raise _fx.MslkbError(status, where)
 
 
-def _weight(weight, dtype, H, device):
+def _weight(weight, dtype, H, dev):
     """Address of a norm weight of x's type or fp32, and whether it is fp32 beside another x."""
-    fp32 = weight.dtype is _torch.float32 and dtype is not _torch.float32
-    return _dense(weight, "weight", _torch.float32 if fp32 else dtype, (H,), device), int(fp32)
+    fp32 = weight.dtype is _F32 and dtype is not _F32
+    return _dense(weight, "weight", _F32 if fp32 else dtype, (H,), dev), 1 if fp32 else 0
 
 
 def add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, groupwise=False, want_y=False,
@@ -280,32 +289,31 @@ def add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, groupwise=False, w
     residual = h where a residual was given, y with ``want_y``, rstd with ``want_rstd``).
     q and scale are XQ and x_scale of the rowwise or block-scaled products; the residual of
     ``out`` may be ``residual`` itself."""
-    dt = _dtype(x, "x")
-    T, H = _matrix(x, "x")
-    dev, xt = x.get_device(), x.dtype
-    xp, ldx = _rows(x, "x", xt, (T, H), dev)
-    rp, ldr = _rows(residual, "residual", xt, (T, H), dev) if residual is not None else (None, H)
+    dt, dev = _lead(x, "x")
+    shape = T, H = _matrix(x, "x")
+    xt = x.dtype
+    xp, ldx = _rows(x, "x", xt, shape, dev)
+    rp, ldr = (None, H) if residual is None else _rows(residual, "residual", xt, shape, dev)
     wp, fp32 = _weight(weight, xt, H, dev)
     ss = _scale_shape(T, H, groupwise)
-    s = _Stream(stream, dev)
-    q, scale, res, y, rstd = _unpack(out, 5)
     if out is None:
-        q, scale = s.new((T, H), _torch.float8_e4m3fn, dev), s.new(ss, _torch.float32, dev)
-        res = s.new((T, H), xt, dev) if residual is not None else None
-        y = s.new((T, H), xt, dev) if want_y else None
-        rstd = s.new((T,), _torch.float32, dev) if want_rstd else None
+        q, scale = _new(stream, dev, shape, _E4M3), _new(stream, dev, ss, _F32)
+        res = None if residual is None else _new(stream, dev, shape, xt)
+        y = _new(stream, dev, shape, xt) if want_y else None
+        rstd = _new(stream, dev, (T,), _F32) if want_rstd else None
         out = NormQuant(q, scale, res, y, rstd)
-    for t, name, wanted in ((res, "residual", residual is not None), (y, "y", want_y),
-                            (rstd, "rstd", want_rstd)):
-        if (t is not None) != bool(wanted):
-            raise ValueError(f"out: {name} must be {'a tensor' if wanted else 'None'}")
+    else:
+        q, scale, res, y, rstd = _unpack(out, 5)
+        _same(res, "residual", residual is not None)
+        _same(y, "y", want_y)
+        _same(rstd, "rstd", want_rstd)
     _call(_fx.lib().mslkb_add_rms_norm_quant(
-        xp, rp, wp, _dense(q, "q", _torch.float8_e4m3fn, (T, H), dev),
-        _dense(scale, "scale", _torch.float32, ss, dev),
-        None if res is None else _dense(res, "residual (out)", xt, (T, H), dev),
-        None if y is None else _dense(y, "y", xt, (T, H), dev),
-        None if rstd is None else _dense(rstd, "rstd", _torch.float32, (T,), dev),
-        T, H, ldx, ldr, eps, dt, fp32, int(bool(groupwise)), s.raw), "add_rms_norm_quant")
+        xp, rp, wp, _dense(q, "q", _E4M3, shape, dev), _dense(scale, "scale", _F32, ss, dev),
+        None if res is None else _dense(res, "residual (out)", xt, shape, dev),
+        None if y is None else _dense(y, "y", xt, shape, dev),
+        None if rstd is None else _dense(rstd, "rstd", _F32, (T,), dev),
+        T, H, ldx, ldr, eps, dt, fp32, 1 if groupwise else 0, _stream(stream, dev)),
+        "add_rms_norm_quant")
     return out
 
 
@@ -314,23 +322,24 @@ def add_rms_norm_quant_backward(dy, h, weight, rstd, dresidual=None, *, out=None
     that was normalised (NormQuant.residual, or x where there was none), rstd [T] fp32,
     dresidual [T, H] the gradient of NormQuant.residual -> (dx [T, H], the gradient of x and
     of residual alike, dweight [H] fp32)."""
-    dt = _dtype(dy, "dy")
-    T, H = _matrix(dy, "dy")
-    dev, xt = dy.get_device(), dy.dtype
+    dt, dev = _lead(dy, "dy")
+    shape = T, H = _matrix(dy, "dy")
+    xt = dy.dtype
     wp, fp32 = _weight(weight, xt, H, dev)
-    s = _Stream(stream, dev)
-    dx, dw = _unpack(out, 2)
     if out is None:
-        out = dx, dw = s.new((T, H), xt, dev), s.new((H,), _torch.float32, dev)
+        out = dx, dw = _new(stream, dev, shape, xt), _new(stream, dev, (H,), _F32)
+    else:
+        dx, dw = _unpack(out, 2)
     L = _fx.lib()
     need = L.mslkb_add_rms_norm_quant_backward_workspace_bytes(T, H)
-    ws = s.new((need,), _torch.uint8, dev)
+    ws = _new(stream, dev, (need,), _torch.uint8)
     _call(L.mslkb_add_rms_norm_quant_backward(
-        _dense(dy, "dy", xt, (T, H), dev), _dense(h, "h", xt, (T, H), dev), wp,
-        _dense(rstd, "rstd", _torch.float32, (T,), dev),
-        None if dresidual is None else _dense(dresidual, "dresidual", xt, (T, H), dev),
-        _dense(dx, "dx", xt, (T, H), dev), _dense(dw, "dweight", _torch.float32, (H,), dev),
-        ws.data_ptr(), need, T, H, dt, fp32, s.raw), "add_rms_norm_quant_backward")
+        _dense(dy, "dy", xt, shape, dev), _dense(h, "h", xt, shape, dev), wp,
+        _dense(rstd, "rstd", _F32, (T,), dev),
+        None if dresidual is None else _dense(dresidual, "dresidual", xt, shape, dev),
+        _dense(dx, "dx", xt, shape, dev), _dense(dw, "dweight", _F32, (H,), dev),
+        ws.data_ptr(), need, T, H, dt, fp32, _stream(stream, dev)),
+        "add_rms_norm_quant_backward")
     return out
 
 
@@ -354,23 +363,19 @@ def route_experts(logits, top_k, *, bias=None, score="softmax", num_groups=1, to
     ``num_groups`` > 1 only from the ``topk_groups`` groups whose ``group_top`` best choices
     sum highest.  weights = scale * score, over the sum of the taken scores if
     ``renormalize``.  Experts with logit -inf are never taken; slots left get id -1, weight 0."""
-    dt = _dtype(logits, "logits")
+    dt, dev = _lead(logits, "logits")
     T, E = _matrix(logits, "logits")
-    dev = logits.get_device()
     lp, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
     kind = _score(score)
-    s = _Stream(stream, dev)
     shape = (T, top_k)
-    ids, weights = _unpack(out, 2)
     if out is None:
-        out = ids, weights = Routing(s.new(shape, _torch.int32, dev),
-                                     s.new(shape, _torch.float32, dev))
+        out = Routing(_new(stream, dev, shape, _I32), _new(stream, dev, shape, _F32))
+    ids, weights = _unpack(out, 2)
     _call(_fx.lib().mslkb_route_experts(
-        lp, None if bias is None else _dense(bias, "bias", _torch.float32, (E,), dev),
-        _dense(ids, "ids", _torch.int32, shape, dev),
-        _dense(weights, "weights", _torch.float32, shape, dev), T, E, ld, top_k, kind,
-        num_groups, topk_groups, group_top, int(bool(renormalize)), scale, dt, s.raw),
-        "route_experts")
+        lp, None if bias is None else _dense(bias, "bias", _F32, (E,), dev),
+        _dense(ids, "ids", _I32, shape, dev), _dense(weights, "weights", _F32, shape, dev),
+        T, E, ld, top_k, kind, num_groups, topk_groups, group_top, 1 if renormalize else 0,
+        scale, dt, _stream(stream, dev)), "route_experts")
     return out
 
 
@@ -378,21 +383,18 @@ def route_experts_backward(dweights, logits, ids, *, score="softmax", renormaliz
                            scale=1.0, out=None, stream=None):
     """dlogits [T, E] (logits' type) from dweights fp32 [T, top_k] for the choice ``ids`` of
     route_experts called with the same score, renormalize and scale."""
-    dt = _dtype(logits, "logits")
+    dt, dev = _lead(logits, "logits")
     T, E = _matrix(logits, "logits")
-    dev = logits.get_device()
     lp, ld = _rows(logits, "logits", logits.dtype, (T, E), dev)
     shape = _matrix(ids, "ids")
     if shape[0] != T:
         raise ValueError("ids and logits disagree on the number of tokens")
-    s = _Stream(stream, dev)
     if out is None:
-        out = s.new((T, E), logits.dtype, dev)
+        out = _new(stream, dev, (T, E), logits.dtype)
     _call(_fx.lib().mslkb_route_experts_backward(
-        _dense(dweights, "dweights", _torch.float32, shape, dev), lp,
-        _dense(ids, "ids", _torch.int32, shape, dev),
+        _dense(dweights, "dweights", _F32, shape, dev), lp, _dense(ids, "ids", _I32, shape, dev),
         _dense(out, "out", logits.dtype, (T, E), dev), T, E, ld, shape[1], _score(score),
-        int(bool(renormalize)), scale, dt, s.raw), "route_experts_backward")
+        1 if renormalize else 0, scale, dt, _stream(stream, dev)), "route_experts_backward")
     return out
 
 
@@ -406,39 +408,35 @@ def moe_dispatch(x, x_scale, ids, num_experts, *, out=None, stream=None):
     first so that no stale memory is returned there."""
     if _torch is None:
         _setup()
+    dev = _on_device(x, "x")
     T, H = _matrix(x, "x")
-    dev = x.get_device()
-    if not x.is_cuda or dev != _DEVICE():
-        raise ValueError("x must be a CUDA tensor on the current device")
     k = _matrix(ids, "ids")[1]
     xp = _dense(x, "x", x.dtype, (T, H), dev)
-    ip = _dense(ids, "ids", _torch.int32, (T, k), dev)
+    ip = _dense(ids, "ids", _I32, (T, k), dev)
     sp, cols, tail = None, 0, ()
     if x_scale is not None:
         if x_scale.dim() not in (1, 2):
             raise ValueError(f"x_scale: expected 1 or 2 dims, got {x_scale.dim()}")
         tail = tuple(x_scale.shape[1:])
         cols = tail[0] if tail else 1
-        sp = _dense(x_scale, "x_scale", _torch.float32, (T, *tail), dev)
-    s = _Stream(stream, dev)
-    xo, so, m_sizes, dest = _unpack(out, 4)
+        sp = _dense(x_scale, "x_scale", _F32, (T, *tail), dev)
+    N = T * k
     if out is None:
-        xo = s.new((T * k, H), x.dtype, dev, zero=True)
-        so = s.new((T * k, *tail), _torch.float32, dev, zero=True) if cols else None
-        m_sizes = s.new((num_experts,), _torch.int64, dev)
-        dest = s.new((T, k), _torch.int32, dev)
-        out = Dispatch(xo, so, m_sizes, dest)
-    elif (so is None) != (x_scale is None):
-        raise ValueError("out: x_scale must be there exactly where the input has one")
+        out = Dispatch(_new(stream, dev, (N, H), x.dtype, zero=True),
+                       None if x_scale is None else _new(stream, dev, (N, *tail), _F32, zero=True),
+                       _new(stream, dev, (num_experts,), _torch.int64),
+                       _new(stream, dev, (T, k), _I32))
+    xo, so, m_sizes, dest = _unpack(out, 4)
+    _same(so, "x_scale", x_scale is not None)
     L = _fx.lib()
     need = L.mslkb_moe_dispatch_workspace_bytes(T, k, num_experts)
-    ws = s.new((need,), _torch.uint8, dev) if need else None
+    ws = _new(stream, dev, (need,), _torch.uint8) if need else None
     _call(L.mslkb_moe_dispatch(
-        xp, sp, ip, _dense(xo, "x (out)", x.dtype, (T * k, H), dev),
-        None if so is None else _dense(so, "x_scale (out)", _torch.float32, (T * k, *tail), dev),
+        xp, sp, ip, _dense(xo, "x (out)", x.dtype, (N, H), dev),
+        None if so is None else _dense(so, "x_scale (out)", _F32, (N, *tail), dev),
         _dense(m_sizes, "m_sizes", _torch.int64, (num_experts,), dev),
-        _dense(dest, "dest", _torch.int32, (T, k), dev), None if ws is None else ws.data_ptr(),
-        need, T, k, num_experts, H * x.element_size(), cols, s.raw), "moe_dispatch")
+        _dense(dest, "dest", _I32, (T, k), dev), ws.data_ptr() if need else None, need, T, k,
+        num_experts, H * x.element_size(), cols, _stream(stream, dev)), "moe_dispatch")
     return out
 
 
@@ -446,18 +444,16 @@ def moe_combine(rows, dest, weights=None, *, out=None, stream=None):
     """out[t] = sum over j of weights[t, j] * rows[dest[t, j]]: rows [R, H] bf16 / fp16 / fp32,
     dest int32 [T, top_k] (outside [0, R): left out), weights fp32 [T, top_k] or None (ones:
     the gradient of moe_dispatch) -> [T, H] of rows' type."""
-    dt = _dtype(rows, "rows")
-    R, H = _matrix(rows, "rows")
-    dev = rows.get_device()
-    T, k = _matrix(dest, "dest")
-    s = _Stream(stream, dev)
+    dt, dev = _lead(rows, "rows")
+    shape = R, H = _matrix(rows, "rows")
+    choices = T, k = _matrix(dest, "dest")
     if out is None:
-        out = s.new((T, H), rows.dtype, dev)
+        out = _new(stream, dev, (T, H), rows.dtype)
     _call(_fx.lib().mslkb_moe_combine(
-        _dense(rows, "rows", rows.dtype, (R, H), dev),
-        _dense(dest, "dest", _torch.int32, (T, k), dev),
-        None if weights is None else _dense(weights, "weights", _torch.float32, (T, k), dev),
-        _dense(out, "out", rows.dtype, (T, H), dev), T, k, H, R, dt, s.raw), "moe_combine")
+        _dense(rows, "rows", rows.dtype, shape, dev), _dense(dest, "dest", _I32, choices, dev),
+        None if weights is None else _dense(weights, "weights", _F32, choices, dev),
+        _dense(out, "out", rows.dtype, (T, H), dev), T, k, H, R, dt, _stream(stream, dev)),
+        "moe_combine")
     return out
 
 
@@ -465,24 +461,19 @@ def moe_combine_backward(dout, rows, dest, weights, *, out=None, stream=None):
     """Gradient of moe_combine: dout [T, H] -> (drows [R, H]: weights[t, j] * dout[t] at row
     dest[t, j], dweights fp32 [T, top_k]: dout[t] . rows[dest[t, j]]).  Rows that no choice
     names are not written: a drows allocated here is zeroed first."""
-    dt = _dtype(dout, "dout")
+    dt, dev = _lead(dout, "dout")
     T, H = _matrix(dout, "dout")
-    dev = dout.get_device()
     R = _matrix(rows, "rows")[0]
     k = _matrix(dest, "dest")[1]
-    s = _Stream(stream, dev)
-    drows, dw = _unpack(out, 2)
+    xt = dout.dtype
     if out is None:
-        out = drows, dw = (s.new((R, H), dout.dtype, dev, zero=True),
-                           s.new((T, k), _torch.float32, dev))
+        out = (_new(stream, dev, (R, H), xt, zero=True), _new(stream, dev, (T, k), _F32))
+    drows, dw = _unpack(out, 2)
     _call(_fx.lib().mslkb_moe_combine_backward(
-        _dense(dout, "dout", dout.dtype, (T, H), dev),
-        _dense(rows, "rows", dout.dtype, (R, H), dev),
-        _dense(dest, "dest", _torch.int32, (T, k), dev),
-        _dense(weights, "weights", _torch.float32, (T, k), dev),
-        _dense(drows, "drows", dout.dtype, (R, H), dev),
-        _dense(dw, "dweights", _torch.float32, (T, k), dev), T, k, H, R, dt, s.raw),
-        "moe_combine_backward")
+        _dense(dout, "dout", xt, (T, H), dev), _dense(rows, "rows", xt, (R, H), dev),
+        _dense(dest, "dest", _I32, (T, k), dev), _dense(weights, "weights", _F32, (T, k), dev),
+        _dense(drows, "drows", xt, (R, H), dev), _dense(dw, "dweights", _F32, (T, k), dev),
+        T, k, H, R, dt, _stream(stream, dev)), "moe_combine_backward")
     return out
 
 
@@ -491,49 +482,43 @@ def swiglu_quant(x, *, groupwise=False, checkpoint=False, out=None, stream=None)
     be strided); a = gate * sigmoid(gate) * up -> SwigluQuant(q e4m3 [R, W], scale fp32 [R] or
     [R, W/128], and with ``checkpoint`` x itself in 8 bits for the gradient: saved e4m3
     [R, 2W], saved_scale fp32 [R, 2W/128])."""
-    dt = _dtype(x, "x")
+    dt, dev = _lead(x, "x")
     R, W2 = _matrix(x, "x")
     if W2 % 2:
         raise ValueError("x holds gate and up side by side: an even number of columns")
-    W, dev = W2 // 2, x.get_device()
+    W = W2 // 2
     xp, ldx = _rows(x, "x", x.dtype, (R, W2), dev)
     ss = _scale_shape(R, W, groupwise)
-    kept = _scale_shape(R, W, True) if checkpoint else None
-    s = _Stream(stream, dev)
-    e4m3, f32 = _torch.float8_e4m3fn, _torch.float32
-    q, scale, saved, saved_scale = _unpack(out, 4)
+    kept = (R, 2 * _scale_shape(R, W, True)[1]) if checkpoint else None
     if out is None:
-        q, scale = s.new((R, W), e4m3, dev), s.new(ss, f32, dev)
-        if checkpoint:
-            saved, saved_scale = s.new((R, W2), e4m3, dev), s.new((R, 2 * kept[1]), f32, dev)
-        out = SwigluQuant(q, scale, saved, saved_scale)
-    if (saved is not None) != bool(checkpoint) or (saved_scale is not None) != bool(checkpoint):
-        raise ValueError("out: saved and saved_scale must be there exactly with checkpoint")
+        out = SwigluQuant(_new(stream, dev, (R, W), _E4M3), _new(stream, dev, ss, _F32),
+                          _new(stream, dev, (R, W2), _E4M3) if checkpoint else None,
+                          _new(stream, dev, kept, _F32) if checkpoint else None)
+    q, scale, saved, saved_scale = _unpack(out, 4)
+    _same(saved, "saved", checkpoint)
+    _same(saved_scale, "saved_scale", checkpoint)
     _call(_fx.lib().mslkb_swiglu_quant(
-        xp, _dense(q, "q", e4m3, (R, W), dev), _dense(scale, "scale", f32, ss, dev),
-        None if saved is None else _dense(saved, "saved", e4m3, (R, W2), dev),
-        None if saved is None else _dense(saved_scale, "saved_scale", f32, (R, 2 * kept[1]), dev),
-        R, W, ldx, dt, int(bool(groupwise)), s.raw), "swiglu_quant")
+        xp, _dense(q, "q", _E4M3, (R, W), dev), _dense(scale, "scale", _F32, ss, dev),
+        None if saved is None else _dense(saved, "saved", _E4M3, (R, W2), dev),
+        None if saved is None else _dense(saved_scale, "saved_scale", _F32, kept, dev),
+        R, W, ldx, dt, 1 if groupwise else 0, _stream(stream, dev)), "swiglu_quant")
     return out
 
 
 def swiglu_quant_backward(dy, saved, saved_scale=None, *, out=None, stream=None):
     """dx [R, 2W] (dy's type) from dy [R, W] and what the forward kept: the checkpoint (e4m3
     [R, 2W] with its scales) or x itself (saved_scale None)."""
-    dt = _dtype(dy, "dy")
+    dt, dev = _lead(dy, "dy")
     R, W = _matrix(dy, "dy")
-    dev = dy.get_device()
-    s = _Stream(stream, dev)
+    xt = dy.dtype
     if out is None:
-        out = s.new((R, 2 * W), dy.dtype, dev)
+        out = _new(stream, dev, (R, 2 * W), xt)
     if saved_scale is None:
-        kp, sp = _dense(saved, "saved", dy.dtype, (R, 2 * W), dev), None
+        kp, sp = _dense(saved, "saved", xt, (R, 2 * W), dev), None
     else:
-        kp = _dense(saved, "saved", _torch.float8_e4m3fn, (R, 2 * W), dev)
-        sp = _dense(saved_scale, "saved_scale", _torch.float32,
-                    (R, 2 * _scale_shape(R, W, True)[1]), dev)
+        kp = _dense(saved, "saved", _E4M3, (R, 2 * W), dev)
+        sp = _dense(saved_scale, "saved_scale", _F32, (R, 2 * _scale_shape(R, W, True)[1]), dev)
     _call(_fx.lib().mslkb_swiglu_quant_backward(
-        _dense(dy, "dy", dy.dtype, (R, W), dev), kp, sp,
-        _dense(out, "out", dy.dtype, (R, 2 * W), dev), R, W, dt, s.raw),
-        "swiglu_quant_backward")
+        _dense(dy, "dy", xt, (R, W), dev), kp, sp, _dense(out, "out", xt, (R, 2 * W), dev),
+        R, W, dt, _stream(stream, dev)), "swiglu_quant_backward")
     return out
