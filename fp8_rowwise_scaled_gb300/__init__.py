@@ -645,7 +645,7 @@ from .moe import (  # noqa: E402 - needs the definitions above
     add_rms_norm_quant, add_rms_norm_quant_backward, moe_combine, moe_combine_backward,
     moe_dispatch, mslkb_add_rms_norm_quant, mslkb_add_rms_norm_quant_backward,
     mslkb_add_rms_norm_quant_backward_workspace_bytes, mslkb_moe_combine,
-    mslkb_moe_combine_backward, mslkb_moe_dispatch, mslkb_moe_dispatch_workspace_bytes,
-    mslkb_route_experts, mslkb_route_experts_backward, mslkb_swiglu_quant,
+    mslkb_moe_combine_backward, mslkb_moe_dispatch, mslkb_route_experts,
+    mslkb_route_experts_backward, mslkb_swiglu_quant,
     mslkb_swiglu_quant_backward, route_experts, route_experts_backward, swiglu_quant,
     swiglu_quant_backward)

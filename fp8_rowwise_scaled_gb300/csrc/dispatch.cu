@@ -1,5 +1,7 @@
 // dispatch.cu -- the rows of the chosen experts: packed by expert into the stacked layout
 // (dispatch), and summed back per token with the routing weights (combine), with the gradient.
+#include <type_traits>
+
 #include "host.h"
 #include "rows.cuh"
 
@@ -7,113 +9,122 @@ namespace mslkb {
 namespace {
 
 // ---------------------------------------------------------------------------------
-// dispatch: a stable counting sort of the choices by expert, then the copies.
-//   count_kernel   tile histograms                counts[tile][E]
-//   place_kernel   row of every choice            dest, m_sizes
-//   copy_kernel    each token's row, read once, to its rows
+// dispatch: a stable counting sort of the choices by expert (place_kernel: the row of every
+// choice), then each token's row is read once and written to its rows (copy_kernel).  The
+// copies are bound by HBM's writes; the sort in front of them by latency, so it is one kernel
+// of one cluster: the eight CTAs exchange their counts through distributed shared memory.
 // ---------------------------------------------------------------------------------
-constexpr int kTile = 1024;      // choices per tile
-constexpr int kTileWarps = 8;    // a warp places kTile / kTileWarps choices, 32 at a time
-constexpr int kWarpChoices = kTile / kTileWarps;
+constexpr int kCluster = 8;
+constexpr int kPlaceWarps = 32;
 
-__global__ void __launch_bounds__(256)
-    count_kernel(const int32_t* ids, uint32_t* counts, int64_t N, int E) {
-  extern __shared__ uint32_t histogram[];
-  for (int e = threadIdx.x; e < E; e += blockDim.x) histogram[e] = 0;
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  __syncthreads();
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * kTile;
-  for (int i = threadIdx.x; i < kTile; i += blockDim.x) {
-    const int e = begin + i < N ? ids[begin + i] : -1;
-    if (e >= 0 && e < E) atomicAdd(&histogram[e], 1u);  // whole numbers: any order is the same
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    counts[static_cast<int64_t>(blockIdx.x) * E + e] = histogram[e];
+constexpr int kAhead = 8;  // loads of a warp under way together
+
+// The experts of choices [i0, i0 + 32 * kAhead) below `end`, one per lane and step; -1: not here.
+__device__ __forceinline__ void load_choices(const int32_t* ids, int64_t i0, int64_t end, int E,
+                                             int (&choice)[kAhead]) {
+  const int64_t i = i0 + (threadIdx.x & 31);
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r) choice[r] = i + r * 32 < end ? ids[i + r * 32] : -1;
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r)
+    if (choice[r] < 0 || choice[r] >= E) choice[r] = -1;
 }
 
-// Shared memory: base[E] (first row of this tile's choices of an expert), warp_count
-// [kTileWarps][E].
-__global__ void __launch_bounds__(kTileWarps * 32)
-    place_kernel(const int32_t* ids, const uint32_t* counts, int32_t* dest, int64_t* m_sizes,
-                 int64_t N, int E, int tiles) {
+// The lanes of the warp whose choice is this lane's, from one ballot per bit of the expert
+// (match.any walks through the distinct values, some thirty of them here).
+template <int kBits>
+__device__ __forceinline__ uint32_t same_expert(int choice) {
+  uint32_t same = __ballot_sync(0xFFFFFFFFu, choice >= 0);
+#pragma unroll
+  for (int b = 0; b < kBits; ++b) {
+    const bool set = choice & (1 << b);
+    const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, set);
+    same &= lanes ^ (set ? 0u : 0xFFFFFFFFu);
+  }
+  return same;
+}
+
+// The choices in contiguous chunks, one per warp of the cluster, each a multiple of 32.
+// Shared memory: first[kPlaceWarps][E]: a warp's choices per expert, then those before its next
+// choice in the CTA; cta_total[E]: this CTA's choices per expert, read by the others; base[E]:
+// the row of the CTA's first choice of an expert.  E <= 2^kBits.
+template <int kBits>
+__global__ void __launch_bounds__(kPlaceWarps * 32)
+    place_kernel(const int32_t* ids, int32_t* dest, int64_t* m_sizes, int N, int E, int chunk) {
   extern __shared__ uint32_t place_shared[];
-  uint32_t* base = place_shared;
-  uint32_t* warp_count = place_shared + E;
-  __shared__ uint32_t chunk_sum[kTileWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = kTileWarps * 32;
-  for (int i = threadIdx.x; i < kTileWarps * E; i += threads) warp_count[i] = 0;
+  uint32_t* first = place_shared;
+  uint32_t* cta_total = place_shared + kPlaceWarps * E;
+  uint32_t* base = cta_total + E;
+  __shared__ uint32_t warp_total[kPlaceWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = ptx::cluster_ctarank();
+  for (int i = threadIdx.x; i < kPlaceWarps * E; i += blockDim.x) first[i] = 0;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int tile = blockIdx.x;
-  // choices of each expert in all tiles (total) and in the tiles before this one
-  uint32_t carry = 0;  // rows of the experts before this round's
-  for (int e0 = 0; e0 < E; e0 += threads) {
-    const int e = e0 + threadIdx.x;
-    uint32_t before = 0, total = 0;
-    if (e < E) {
-#pragma unroll 16
-      for (int i = 0; i < tiles; ++i) {
-        const uint32_t c = counts[static_cast<int64_t>(i) * E + e];
-        if (i < tile) before += c;
-        total += c;
-      }
-      if (tile == 0) m_sizes[e] = total;
-    }
-    uint32_t sum = total;  // inclusive scan over the threads
+  __syncthreads();
+  uint32_t* mine = first + warp * E;
+  const int64_t begin = (static_cast<int64_t>(rank) * kPlaceWarps + warp) * chunk;
+  const int64_t end = begin + chunk < N ? begin + chunk : N;
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
+    int choice[kAhead];
+    load_choices(ids, i0, end, E, choice);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-      if (lane >= d) sum += v;
-    }
-    if (lane == 31) chunk_sum[warp] = sum;
-    __syncthreads();
-    uint32_t warps_before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kTileWarps; ++w) {
-      if (w < warp) warps_before += chunk_sum[w];
-      all += chunk_sum[w];
-    }
-    if (e < E) base[e] = carry + warps_before + sum - total + before;
-    carry += all;
-    __syncthreads();
-  }
-  // rank of each choice among its warp's choices of the same expert, in order
-  const int64_t begin = static_cast<int64_t>(tile) * kTile + warp * kWarpChoices;
-  uint32_t* mine = warp_count + warp * E;
-  int expert[kWarpChoices / 32];
-  uint32_t rank[kWarpChoices / 32];
-#pragma unroll
-  for (int r = 0; r < kWarpChoices / 32; ++r) {
-    const int64_t i = begin + r * 32 + lane;
-    int e = i < N ? ids[i] : -1;
-    if (e >= E) e = -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const uint32_t earlier = __popc(same & ((1u << lane) - 1u));
-    const uint32_t seen = e >= 0 ? mine[e] : 0;
-    __syncwarp();
-    if (e >= 0 && earlier == 0) mine[e] = seen + __popc(same);
-    __syncwarp();
-    expert[r] = e < 0 ? -1 : e;
-    rank[r] = seen + earlier;
+    for (int r = 0; r < kAhead; ++r)
+      if (choice[r] >= 0) atomicAdd(&mine[choice[r]], 1u);  // whole numbers, in any order
   }
   __syncthreads();
-  // first row of each warp's choices of an expert
-  for (int e = threadIdx.x; e < E; e += threads) {
-    uint32_t at = base[e];
+  // one expert per thread (E <= 1024): the warps' counts become offsets within the CTA
+  const int e = threadIdx.x;
+  uint32_t sum = 0;
+  if (e < E) {
 #pragma unroll
-    for (int w = 0; w < kTileWarps; ++w) {
-      const uint32_t c = warp_count[w * E + e];
-      warp_count[w * E + e] = at;
-      at += c;
+    for (int w = 0; w < kPlaceWarps; ++w) {
+      const uint32_t c = first[w * E + e];
+      first[w * E + e] = sum;
+      sum += c;
     }
+    cta_total[e] = sum;
   }
-  __syncthreads();
+  ptx::cluster_sync();
+  uint32_t before = 0, total = 0;
+  if (e < E) {
+    const uint32_t at = ptx::smem_addr(cta_total + e);
 #pragma unroll
-  for (int r = 0; r < kWarpChoices / 32; ++r) {
-    const int64_t i = begin + r * 32 + lane;
-    if (i < N) dest[i] = expert[r] < 0 ? -1 : static_cast<int32_t>(mine[expert[r]] + rank[r]);
+    for (uint32_t r = 0; r < kCluster; ++r) {
+      const uint32_t c = ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, r));
+      if (r < rank) before += c;
+      total += c;
+    }
+    if (rank == 0) m_sizes[e] = total;
+  }
+  uint32_t scan = total;  // inclusive, over the experts
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+    if (lane >= d) scan += v;
+  }
+  if (lane == 31) warp_total[warp] = scan;
+  __syncthreads();
+  uint32_t warps_before = warp_total[lane];
+  warps_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warps_before : 0u);
+  if (e < E) base[e] = warps_before + scan - total + before;
+  ptx::cluster_sync();  // rows are set; nobody reads another CTA's shared memory any more
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
+    int choice[kAhead];
+    load_choices(ids, i0, end, E, choice);
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      if (i0 + r * 32 >= end) break;
+      const int64_t i = i0 + r * 32 + lane;
+      const uint32_t same = same_expert<kBits>(choice[r]);
+      const uint32_t earlier = __popc(same & ((1u << lane) - 1u));
+      const uint32_t next = choice[r] >= 0 ? mine[choice[r]] : 0;
+      __syncwarp();
+      if (choice[r] >= 0 && earlier == 0) mine[choice[r]] = next + __popc(same);
+      __syncwarp();
+      if (i < end)
+        dest[i] = choice[r] >= 0 ? static_cast<int32_t>(base[choice[r]] + next + earlier) : -1;
+    }
   }
 }
 
@@ -128,50 +139,46 @@ struct CopyParams {
   int32_t top_k;
 };
 
-// One CTA per token: its row is read once, 16 bytes (kWide) or one byte at a time, and
-// written to each of its rows.
+// A token's row is read once, 16 bytes (kWide) or one byte at a time, and written to each of
+// its rows.  A lane of each warp holds one of them, `own` (-1: none); their load and the
+// row's are under way together.
 template <bool kWide>
-__device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, const int32_t* dest) {
-  const uint8_t* from = p.x + t * p.row_bytes;
-  if constexpr (kWide) {
-    const int n = static_cast<int>(p.row_bytes / 16);
-    for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      const uint4 v = load16(from + static_cast<int64_t>(c) * 16);
-      for (int j = 0; j < p.top_k; ++j) {
-        const int32_t d = dest[j];
-        if (d >= 0) store16(p.x_out + d * p.row_bytes + static_cast<int64_t>(c) * 16, v);
-      }
-    }
-  } else {
-    for (int64_t c = threadIdx.x; c < p.row_bytes; c += blockDim.x) {
-      const uint8_t v = from[c];
-      for (int j = 0; j < p.top_k; ++j) {
-        const int32_t d = dest[j];
-        if (d >= 0) p.x_out[d * p.row_bytes + c] = v;
-      }
+__device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, int32_t own) {
+  using Piece = std::conditional_t<kWide, uint4, uint8_t>;
+  const Piece* from = reinterpret_cast<const Piece*>(p.x + t * p.row_bytes);
+  const int n = static_cast<int>(p.row_bytes / sizeof(Piece));
+  for (int c0 = 0; c0 < n; c0 += blockDim.x) {
+    const int c = c0 + threadIdx.x;
+    Piece v{};
+    if (c < n) v = from[c];
+    for (int j = 0; j < p.top_k; ++j) {
+      const int32_t d = __shfl_sync(0xFFFFFFFFu, own, j);
+      if (d >= 0 && c < n) reinterpret_cast<Piece*>(p.x_out + d * p.row_bytes)[c] = v;
     }
   }
-  for (int c = threadIdx.x; c < p.scale_cols; c += blockDim.x) {
-    const float v = p.x_scale[t * p.scale_cols + c];
+  for (int c0 = 0; c0 < p.scale_cols; c0 += blockDim.x) {
+    const int c = c0 + threadIdx.x;
+    float v = 0.f;
+    if (c < p.scale_cols) v = p.x_scale[t * p.scale_cols + c];
     for (int j = 0; j < p.top_k; ++j) {
-      const int32_t d = dest[j];
-      if (d >= 0) p.scale_out[static_cast<int64_t>(d) * p.scale_cols + c] = v;
+      const int32_t d = __shfl_sync(0xFFFFFFFFu, own, j);
+      if (d >= 0 && c < p.scale_cols)
+        p.scale_out[static_cast<int64_t>(d) * p.scale_cols + c] = v;
     }
   }
 }
 
+// One CTA per token.
 template <bool kWide>
 __global__ void __launch_bounds__(512) copy_kernel(const __grid_constant__ CopyParams p) {
-  __shared__ int32_t dest[MSLKB_MAX_TOPK];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int64_t t = blockIdx.x;
-  if (threadIdx.x < p.top_k) dest[threadIdx.x] = p.dest[t * p.top_k + threadIdx.x];
-  __syncthreads();
-  copy_row<kWide>(p, t, dest);
+  const int lane = threadIdx.x & 31;
+  copy_row<kWide>(p, t, lane < p.top_k ? p.dest[t * p.top_k + lane] : -1);
 }
 
-// Few choices: one launch, no workspace.  The CTA of a token finds each of its rows by itself:
+// Few choices: one launch.  The CTA of a token finds each of its rows by itself:
 // the row of choice i is the number of choices that come before it, those of a lower expert
 // and the earlier ones of its own.  One more CTA counts the experts' rows.
 struct DirectParams {
@@ -185,7 +192,6 @@ struct DirectParams {
 template <bool kWide>
 __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ DirectParams p) {
   __shared__ uint32_t before[MSLKB_MAX_EXPERTS];  // a token's rows; or the experts' counts
-  __shared__ int32_t dest[MSLKB_MAX_TOPK];
   const int k = p.copy.top_k, N = p.T * k, lane = threadIdx.x & 31;
   const int counters = blockIdx.x == p.T ? p.E : k;
   for (int i = threadIdx.x; i < counters; i += blockDim.x) before[i] = 0;
@@ -206,6 +212,7 @@ __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ Dir
   // for nobody
   int own = lane < k ? p.ids[first + lane] : -1;
   if (own < 0 || own >= p.E) own = -1;
+  uint32_t count = 0;  // lane j: of the token's choice j
   for (int i0 = 0; i0 < N; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
     int e = i < N ? p.ids[i] : -1;
@@ -214,17 +221,14 @@ __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ Dir
       const int mine = __shfl_sync(0xFFFFFFFFu, own, j);
       const uint32_t earlier =
           __ballot_sync(0xFFFFFFFFu, e < mine || (e == mine && i < first + j));
-      if (lane == 0 && earlier != 0) atomicAdd(&before[j], __popc(earlier));
+      if (lane == j) count += __popc(earlier);
     }
   }
+  if (lane < k) atomicAdd(&before[lane], count);  // whole numbers: any order is the same
   __syncthreads();
-  if (threadIdx.x < k) {
-    const int row = own >= 0 ? static_cast<int>(before[threadIdx.x]) : -1;
-    dest[threadIdx.x] = row;
-    p.dest[first + threadIdx.x] = row;
-  }
-  __syncthreads();
-  copy_row<kWide>(p.copy, blockIdx.x, dest);
+  own = own >= 0 ? static_cast<int>(before[lane]) : -1;
+  if (threadIdx.x < k) p.dest[first + threadIdx.x] = own;
+  copy_row<kWide>(p.copy, blockIdx.x, own);
 }
 
 // ---------------------------------------------------------------------------------
@@ -366,8 +370,6 @@ int row_threads(int64_t vectors) {
   return static_cast<int>(t < 32 ? 32 : (t > 512 ? 512 : t));
 }
 
-int64_t tiles_of(int64_t choices) { return (choices + kTile - 1) / kTile; }
-
 // Choices up to which each token's CTA finds its rows by itself.
 constexpr int64_t kDirectChoices = 2048;
 
@@ -399,19 +401,10 @@ mslkb_status check_combine(int64_t T, int64_t top_k, int64_t H, int64_t R, int32
 
 extern "C" {
 
-int64_t mslkb_moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E) {
-  if (T <= 0 || top_k <= 0 || E <= 0 || E > MSLKB_MAX_EXPERTS || top_k > MSLKB_MAX_TOPK ||
-      T > MSLKB_MAX_DIM / 2 / top_k)
-    return 0;
-  if (T * top_k <= mslkb::kDirectChoices) return 0;
-  return mslkb::tiles_of(T * top_k) * E * static_cast<int64_t>(sizeof(uint32_t));
-}
-
 mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32_t* ids,
                                 void* x_out, float* scale_out, int64_t* m_sizes, int32_t* dest,
-                                void* workspace, int64_t workspace_bytes, int64_t T,
-                                int64_t top_k, int64_t E, int64_t row_bytes, int64_t scale_cols,
-                                void* stream) {
+                                int64_t T, int64_t top_k, int64_t E, int64_t row_bytes,
+                                int64_t scale_cols, void* stream) {
   using namespace mslkb;
   if (T < 0 || top_k < 0 || E < 0 || row_bytes < 0 || scale_cols < 0) return MSLKB_ERR_SHAPE;
   if (E > MSLKB_MAX_EXPERTS || top_k > MSLKB_MAX_TOPK || row_bytes > MSLKB_MAX_DIM ||
@@ -424,10 +417,6 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
     if (ids == nullptr || dest == nullptr) return MSLKB_ERR_NULL;
     if (row_bytes > 0 && (x == nullptr || x_out == nullptr)) return MSLKB_ERR_NULL;
     if (scale_cols > 0 && (x_scale == nullptr || scale_out == nullptr)) return MSLKB_ERR_NULL;
-    const int64_t need = mslkb_moe_dispatch_workspace_bytes(T, top_k, E);
-    if (need > 0 &&
-        (workspace == nullptr || !aligned_to(workspace, 16) || workspace_bytes < need))
-      return MSLKB_ERR_WORKSPACE;
   }
   int sms = 0;
   mslkb_status s = device_sms(&sms);
@@ -439,8 +428,7 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
     if (e == cudaSuccess && N > 0) e = cudaMemsetAsync(dest, 0xFF, sizeof(int32_t) * N, cs);
     return launch_status(e);
   }
-  uint32_t* counts = static_cast<uint32_t*>(workspace);
-  const int tiles = static_cast<int>(tiles_of(N)), experts = static_cast<int>(E);
+  const int experts = static_cast<int>(E);
   const bool wide = row_bytes % 16 == 0 && aligned_to(x, 16) && aligned_to(x_out, 16);
   const CopyParams p{static_cast<const uint8_t*>(x), x_scale, dest, static_cast<uint8_t*>(x_out),
                      scale_out, row_bytes, static_cast<int32_t>(scale_cols),
@@ -455,12 +443,14 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
                              ? launch_dependent(direct_kernel<true>, grid, block, 0, stream, d)
                              : launch_dependent(direct_kernel<false>, grid, block, 0, stream, d));
   }
-  cudaError_t e = launch_dependent(count_kernel, dim3(tiles), dim3(256),
-                                   sizeof(uint32_t) * experts, stream, ids, counts, N, experts);
+  const int64_t per_warp = (N + kCluster * kPlaceWarps - 1) / (kCluster * kPlaceWarps);
+  const auto place = experts <= 256 ? place_kernel<8> : place_kernel<10>;
+  cudaError_t e = experts <= 256 ? allow_smem<place_kernel<8>>() : allow_smem<place_kernel<10>>();
   if (e == cudaSuccess)
-    e = launch_dependent(place_kernel, dim3(tiles), dim3(kTileWarps * 32),
-                         sizeof(uint32_t) * experts * (kTileWarps + 1), stream, ids, counts, dest,
-                         m_sizes, N, experts, tiles);
+    e = launch_cluster(place, dim3(kCluster), dim3(kPlaceWarps * 32),
+                       sizeof(uint32_t) * experts * (kPlaceWarps + 2), kCluster, stream, ids, dest,
+                       m_sizes, static_cast<int>(N), experts,
+                       static_cast<int>((per_warp + 31) / 32 * 32));
   if (e == cudaSuccess && (row_bytes > 0 || scale_cols > 0)) {
     const dim3 grid(static_cast<unsigned>(T));
     e = wide ? launch_dependent(copy_kernel<true>, grid, copy_block, 0, stream, p)

@@ -9,10 +9,10 @@
 //
 // Both directions read every input once and write every output once and are bound by HBM.
 // With a row per CTA, the CTA's loads wait while it reduces and stores; so for many rows the
-// kernels are persistent, and each thread copies its own columns of the next rows into a ring
-// of stages in shared memory (cp.async, 16 bytes) while it works on this one.  A thread reads
-// back only what it copied itself: its own cp.async.wait_group is all the synchronisation
-// that the ring needs.
+// kernels are persistent, and each warp copies its own columns of the next rows into a ring of
+// stages in shared memory (cp.async, 16 bytes per lane) while it works on this one.  A warp
+// reads back only what it copied itself: cp.async.wait_group and a warp barrier are all the
+// synchronisation that the ring needs.
 #include "host.h"
 #include "rows.cuh"
 
@@ -36,14 +36,14 @@ struct NormParams {
   float eps, inv_h;
 };
 
-// weight elements [c, c + 8): fp32 or T
-template <class T, bool kWide>
-__device__ __forceinline__ void load_weight8(const void* w, int fp32, int c, int n,
-                                             float (&v)[8]) {
+// weight elements [c, c + kCols): fp32 or T
+template <class T, int kCols, Access kAccess>
+__device__ __forceinline__ void load_weight(const void* w, int fp32, int c, int n,
+                                            float (&v)[kCols]) {
   if (fp32)
-    unpack8(load8<float, kWide>(static_cast<const float*>(w), c, n), v);
+    load_cols<float, kCols, kAccess>(static_cast<const float*>(w), c, n, v);
   else
-    unpack8(load8<T, kWide>(static_cast<const T*>(w), c, n), v);
+    load_cols<T, kCols, kAccess>(static_cast<const T*>(w), c, n, v);
 }
 
 // Sum and maximum over the CTA, to every thread; `slot` holds one pair per warp.
@@ -59,29 +59,36 @@ __device__ __forceinline__ void cta_sum_max(float& sum, uint32_t& largest, float
   largest = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mine.y));
 }
 
-// A thread's columns [c, c + 8), c = (i * blockDim.x + threadIdx.x) * 8, of one row that is
-// h in registers: everything from there to the outputs.
-template <class T, int kVecs, bool kWide, bool kBlocks, class Weight>
-__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, float (&h)[kVecs][8],
-                                           Weight weight, float2* slot) {
+// The first of a thread's kCols columns, step i.
+template <int kCols>
+__device__ __forceinline__ int column(int i) {
+  return (i * blockDim.x + threadIdx.x) * kCols;
+}
+
+// One row whose h is in registers, a thread's columns [column(i), column(i) + kCols):
+// everything from there to the outputs.
+template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks, class Weight>
+__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row,
+                                           float (&h)[kVecs][kCols], Weight weight,
+                                           float2* slot) {
   const int n = p.H;
   T* residual_out = static_cast<T*>(p.residual_out) + row * n;
   float sum = 0.f;
   uint32_t largest = 0, block_largest[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * 8;
-    if (p.residual_out != nullptr) store8<T, kWide>(residual_out, c, n, h[i]);
-    float w[8];
+    if (p.residual_out != nullptr)
+      store_cols<T, kCols, kAccess>(residual_out, column<kCols>(i), n, h[i]);
+    float w[kCols];
     weight(i, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kCols; ++j) {
       sum = fmaf(h[i][j], h[i][j], sum);
       w[j] *= h[i][j];
     }
     block_largest[i] = abs_max(w);
     if constexpr (kBlocks)
-      block_largest[i] = block_max<16>(block_largest[i]);
+      block_largest[i] = block_max<kScaleBlock / kCols>(block_largest[i]);
     else
       largest = max(largest, block_largest[i]);
   }
@@ -96,31 +103,32 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, flo
   }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * 8;
+    const int c = column<kCols>(i);
     if constexpr (kBlocks) {
       const float m = __uint_as_float(block_largest[i]);
       s = quant_scale(m * rstd, p.y != nullptr ? m * rstd : m);
       if (c < n && c % kScaleBlock == 0)
         p.scale[row * (n / kScaleBlock) + c / kScaleBlock] = s.scale;
     }
-    float w[8], v[8];
+    float w[kCols], v[kCols];
     weight(i, w);
     if (p.y != nullptr) {
       // (h * rstd) * weight: h * weight alone may fall among the subnormals
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * rstd * w[j];
-      store8<T, kWide>(static_cast<T*>(p.y) + row * n, c, n, v);
+      for (int j = 0; j < kCols; ++j) v[j] = h[i][j] * rstd * w[j];
+      store_cols<T, kCols, kAccess>(static_cast<T*>(p.y) + row * n, c, n, v);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h[i][j] * w[j];
+      for (int j = 0; j < kCols; ++j) v[j] = h[i][j] * w[j];
     }
-    store_codes8<kWide>(p.q + row * n, c, n, quantize8(v, s.inv));
+    store_codes<kCols, kAccess>(p.q + row * n, c, n, v, s.inv);
   }
 }
 
-// One CTA per row, straight from global memory.
-template <class T, int kVecs, bool kWide, bool kBlocks>
-__global__ void __launch_bounds__(kMaxThreads)
+// One CTA per row, straight from global memory.  (A row's columns are spread over the threads
+// as in the ring's kernel, so its sums do not depend on the number of rows.)
+template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks>
+__global__ void __launch_bounds__(kAccess == Access::k32 ? 512 : kMaxThreads)
     norm_quant_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 slot[32];
   ptx::griddep_wait();
@@ -129,32 +137,31 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int n = p.H;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* residual = static_cast<const T*>(p.residual) + row * p.ldr;
-  float h[kVecs][8];
-  {
-    Raw8<T> rx[kVecs], rr[kVecs];
+  float h[kVecs][kCols], r[kVecs][kCols];
+  // x and residual need no more than 16-byte aligned rows, as in the ring
+  const auto input = [&](const T* from, int c, float (&v)[kCols]) {
+#pragma unroll
+    for (int j = 0; j < kCols; j += 8) {
+      float u[8];
+      unpack8(load8<T, kAccess != Access::kElement>(from, c + j, n), u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j + k] = u[k];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) input(x, column<kCols>(i), h[i]);
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) input(residual, column<kCols>(i), r[i]);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      rx[i] = load8<T, kWide>(x, (i * blockDim.x + threadIdx.x) * 8, n);
-    if (p.residual != nullptr) {
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        rr[i] = load8<T, kWide>(residual, (i * blockDim.x + threadIdx.x) * 8, n);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      unpack8(rx[i], h[i]);
-      if (p.residual != nullptr) {
-        float r[8];
-        unpack8(rr[i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
-      }
-    }
+      for (int j = 0; j < kCols; ++j) h[i][j] += r[i][j];
   }
-  finish_row<T, kVecs, kWide, kBlocks>(
+  finish_row<T, kCols, kVecs, kAccess, kBlocks>(
       p, row, h,
-      [&](int i, float (&w)[8]) {
-        load_weight8<T, kWide>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w);
+      [&](int i, float (&w)[kCols]) {
+        load_weight<T, kCols, kAccess>(p.weight, p.weight_fp32, column<kCols>(i), n, w);
       },
       slot);
 }
@@ -162,91 +169,117 @@ __global__ void __launch_bounds__(kMaxThreads)
 // ---------------------------------------------------------------------------------
 // the ring of rows
 // ---------------------------------------------------------------------------------
-// Where a thread finds chunk k of its columns c = (i * blockDim.x + threadIdx.x) * 8 of input
-// `stream` in a stage: 16 bytes per thread side by side, free of bank conflicts.
-template <class T, int kVecs>
-__device__ __forceinline__ uint32_t ring_offset(int stream, int i, int k) {
-  constexpr int kChunks = sizeof(T) / 2;  // 16-byte chunks of eight elements
-  return (((stream * kVecs + i) * kChunks + k) * blockDim.x + threadIdx.x) * 16;
+// A warp's columns of a stage, step i of input `stream`: 32 * kCols of them, in 16-byte pieces
+// that the lanes copy side by side (whole sectors of each access) and lane l reads as pieces
+// l * kPieces ...  The permutation keeps those reads free of bank conflicts.
+template <class T, int kCols, int kVecs>
+__device__ __forceinline__ uint32_t ring_piece(int stream, int i, int piece) {
+  constexpr int kPieces = kCols * sizeof(T) / 16;
+  if constexpr (kPieces == 1) return ((stream * kVecs + i) * blockDim.x + threadIdx.x) * 16;
+  const int at = piece ^ ((piece >> 3) & (kPieces - 1));
+  return (((stream * kVecs + i) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * 32 * kPieces + at) * 16;
 }
 
-template <class T, int kVecs>
+template <class T, int kCols, int kVecs>
 __device__ __forceinline__ void ring_fetch(uint32_t stage, int stream, const T* row, int n) {
+  constexpr int kPieces = kCols * sizeof(T) / 16, kEach = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * 8;
+    const int c0 = (i * static_cast<int>(blockDim.x) + (threadIdx.x & ~31)) * kCols;
 #pragma unroll
-    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k)
+    for (int k = 0; k < kPieces; ++k) {
+      const int piece = k * 32 + lane, c = c0 + piece * kEach;
       // past the row's end nothing is read and zeros are written
-      ptx::cp_async<16>(stage + ring_offset<T, kVecs>(stream, i, k),
-                        c < n ? row + c + k * (16 / sizeof(T)) : row, c < n ? 16 : 0);
+      ptx::cp_async<16>(stage + ring_piece<T, kCols, kVecs>(stream, i, piece),
+                        c < n ? row + c : row, c < n ? 16 : 0);
+    }
   }
 }
 
-template <class T, int kVecs>
+template <class T, int kCols, int kVecs>
 __device__ __forceinline__ void ring_read(const uint8_t* stage, int stream, int i,
-                                          float (&v)[8]) {
-  Raw8<T> r;
+                                          float (&v)[kCols]) {
+  constexpr int kPieces = kCols * sizeof(T) / 16, kRaw = sizeof(T) / 2;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k)
-    r.w[k] = load16(stage + ring_offset<T, kVecs>(stream, i, k));
-  unpack8(r, v);
+  for (int j = 0; j < kCols / 8; ++j) {
+    Raw8<T> r;
+#pragma unroll
+    for (int k = 0; k < kRaw; ++k)
+      r.w[k] = load16(stage + ring_piece<T, kCols, kVecs>(stream, i, lane * kPieces + j * kRaw + k));
+    float u[8];
+    unpack8(r, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[j * 8 + k] = u[k];
+  }
 }
 
-template <class T, int kVecs>
-int ring_stage_bytes(int streams, int threads) {
-  return streams * kVecs * static_cast<int>(sizeof(T) / 2) * threads * 16;
+// The calling warp's pieces of the oldest stage are in shared memory, the others' copies
+// included.  (A warp fills a stage again only after all its lanes have read it: the row's
+// reduction lies between.)
+template <int kStages, int kBytes>
+__device__ __forceinline__ void ring_wait() {
+  ptx::cp_async_wait<kStages - 1>();
+  if constexpr (kBytes > 16) __syncwarp();  // 16 bytes of columns: a lane reads its own piece
 }
 
+template <class T, int kCols, int kVecs>
+constexpr int ring_stage_bytes(int streams, int threads) {
+  return streams * kVecs * threads * kCols * static_cast<int>(sizeof(T));
+}
+
+// 16 columns per thread and step: a block of 128 columns is eight lanes, outputs leave in
+// 32-byte stores.
 template <class T, int kVecs, int kStages, bool kBlocks>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(512, kVecs == 1 ? 2 : 1)
     norm_ring_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 slot[2][32];
   const int n = p.H;
   const bool add = p.residual != nullptr;
-  const int stage_bytes = (add ? 2 : 1) * kVecs * static_cast<int>(sizeof(T) / 2) *
-                          static_cast<int>(blockDim.x) * 16;
+  const int stage_bytes =
+      (add ? 2 : 1) * kVecs * static_cast<int>(blockDim.x * 16 * sizeof(T));
   const uint32_t base = ptx::smem_addr(ring);
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.T) {
       const uint32_t at = base + stage * stage_bytes;
-      ring_fetch<T, kVecs>(at, 0, static_cast<const T*>(p.x) + row * p.ldx, n);
-      if (add) ring_fetch<T, kVecs>(at, 1, static_cast<const T*>(p.residual) + row * p.ldr, n);
+      ring_fetch<T, 16, kVecs>(at, 0, static_cast<const T*>(p.x) + row * p.ldx, n);
+      if (add) ring_fetch<T, 16, kVecs>(at, 1, static_cast<const T*>(p.residual) + row * p.ldr, n);
     }
     ptx::cp_async_commit();
   };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s)
     fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
-  float w[kVecs][8];
+  float w[kVecs][16];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    load_weight8<T, true>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w[i]);
+    load_weight<T, 16, Access::k32>(p.weight, p.weight_fp32, column<16>(i), n, w[i]);
   int stage = 0, turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     fetch(row + static_cast<int64_t>(kStages - 1) * gridDim.x,
           stage == 0 ? kStages - 1 : stage - 1);
-    ptx::cp_async_wait<kStages - 1>();
+    ring_wait<kStages, 16 * sizeof(T)>();
     const uint8_t* at = ring + stage * stage_bytes;
-    float h[kVecs][8];
+    float h[kVecs][16];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      ring_read<T, kVecs>(at, 0, i, h[i]);
+      ring_read<T, 16, kVecs>(at, 0, i, h[i]);
       if (add) {
-        float r[8];
-        ring_read<T, kVecs>(at, 1, i, r);
+        float r[16];
+        ring_read<T, 16, kVecs>(at, 1, i, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+        for (int j = 0; j < 16; ++j) h[i][j] += r[j];
       }
     }
-    finish_row<T, kVecs, true, kBlocks>(
+    finish_row<T, 16, kVecs, Access::k32, kBlocks>(
         p, row, h,
-        [&](int i, float (&v)[8]) {
+        [&](int i, float (&v)[16]) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = w[i][j];
+          for (int j = 0; j < 16; ++j) v[j] = w[i][j];
         },
         slot[turn]);
     turn ^= 1;
@@ -315,7 +348,7 @@ __device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       d[j] = fmaf(rstd, g[j] * w[j] - xhat[j] * rstd * mean, d[j]);
-    store8<T, kWide>(static_cast<T*>(p.dx) + row * n, (i * blockDim.x + threadIdx.x) * 8, n, d);
+    store8<T, kWide>(static_cast<T*>(p.dx) + row * n, column<8>(i), n, d);
   }
 }
 
@@ -333,17 +366,17 @@ __global__ void __launch_bounds__(kMaxThreads)
     backward_row<T, kVecs, kWide>(
         p, row, p.rstd[row], dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
-          const int c = (i * blockDim.x + threadIdx.x) * 8;
+          const int c = column<8>(i);
           unpack8(load8<T, kWide>(static_cast<const T*>(p.dy) + row * n, c, n), g);
           unpack8(load8<T, kWide>(static_cast<const T*>(p.h) + row * n, c, n), h);
         },
         [&](int i, float (&w)[8]) {
-          load_weight8<T, kWide>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n,
-                                 w);
+          load_weight<T, 8, kWide ? Access::k16 : Access::kElement>(p.weight, p.weight_fp32,
+                                                                    column<8>(i), n, w);
         },
         [&](int i, float (&d)[8]) {
           const T* from = static_cast<const T*>(p.dresidual) + row * n;
-          unpack8(load8<T, kWide>(from, (i * blockDim.x + threadIdx.x) * 8,
+          unpack8(load8<T, kWide>(from, column<8>(i),
                                   p.dresidual != nullptr ? n : 0),
                   d);
         },
@@ -352,7 +385,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
     store8<float, kWide>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
-                         (i * blockDim.x + threadIdx.x) * 8, n, dw[i]);
+                         column<8>(i), n, dw[i]);
 }
 
 template <class T, int kVecs, int kStages>
@@ -370,9 +403,9 @@ __global__ void __launch_bounds__(512, 2)
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.T) {
       const uint32_t at = base + stage * stage_bytes;
-      ring_fetch<T, kVecs>(at, 0, static_cast<const T*>(p.dy) + row * n, n);
-      ring_fetch<T, kVecs>(at, 1, static_cast<const T*>(p.h) + row * n, n);
-      if (add) ring_fetch<T, kVecs>(at, 2, static_cast<const T*>(p.dresidual) + row * n, n);
+      ring_fetch<T, 8, kVecs>(at, 0, static_cast<const T*>(p.dy) + row * n, n);
+      ring_fetch<T, 8, kVecs>(at, 1, static_cast<const T*>(p.h) + row * n, n);
+      if (add) ring_fetch<T, 8, kVecs>(at, 2, static_cast<const T*>(p.dresidual) + row * n, n);
     }
     ptx::cp_async_commit();
   };
@@ -382,20 +415,20 @@ __global__ void __launch_bounds__(512, 2)
   float w[kVecs][8], dw[kVecs][8] = {};
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    load_weight8<T, true>(p.weight, p.weight_fp32, (i * blockDim.x + threadIdx.x) * 8, n, w[i]);
+    load_weight<T, 8, Access::k16>(p.weight, p.weight_fp32, column<8>(i), n, w[i]);
   int stage = 0, turn = 0;
   float rstd = p.rstd[blockIdx.x];  // the grid is no larger than T
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     fetch(row + static_cast<int64_t>(kStages - 1) * gridDim.x,
           stage == 0 ? kStages - 1 : stage - 1);
     const float next_rstd = row + gridDim.x < p.T ? p.rstd[row + gridDim.x] : 0.f;
-    ptx::cp_async_wait<kStages - 1>();
+    ring_wait<kStages, 8 * sizeof(T)>();
     const uint8_t* at = ring + stage * stage_bytes;
     backward_row<T, kVecs, true>(
         p, row, rstd, dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
-          ring_read<T, kVecs>(at, 0, i, g);
-          ring_read<T, kVecs>(at, 1, i, h);
+          ring_read<T, 8, kVecs>(at, 0, i, g);
+          ring_read<T, 8, kVecs>(at, 1, i, h);
         },
         [&](int i, float (&v)[8]) {
 #pragma unroll
@@ -403,7 +436,7 @@ __global__ void __launch_bounds__(512, 2)
         },
         [&](int i, float (&d)[8]) {
           if (add) {
-            ring_read<T, kVecs>(at, 2, i, d);
+            ring_read<T, 8, kVecs>(at, 2, i, d);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = 0.f;
@@ -417,7 +450,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
     store8<float, true>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
-                        (i * blockDim.x + threadIdx.x) * 8, n, dw[i]);
+                        column<8>(i), n, dw[i]);
 }
 
 // Column sums of parts [rows, H], in a fixed order: 8 threads per column.
@@ -444,32 +477,32 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------
-int threads_for(int64_t n, int vecs) {
-  const int64_t t = ((n + 7) / 8 + vecs - 1) / vecs;
-  return static_cast<int>((t + 31) / 32 * 32);
+int threads_for(int64_t n, int cols) {  // cols: columns per thread in all
+  return static_cast<int>(((n + cols - 1) / cols + 31) / 32 * 32);
 }
 
-template <class T, int kVecs, bool kWide>
+template <class T, int kCols, int kVecs, Access kAccess>
 cudaError_t launch_norm(const NormParams& p, bool blocks, void* stream) {
-  const dim3 grid(static_cast<unsigned>(p.T)), block(threads_for(p.H, kVecs));
-  return blocks ? launch_dependent(norm_quant_kernel<T, kVecs, kWide, true>, grid, block, 0,
-                                   stream, p)
-                : launch_dependent(norm_quant_kernel<T, kVecs, kWide, false>, grid, block, 0,
-                                   stream, p);
+  const dim3 grid(static_cast<unsigned>(p.T)), block(threads_for(p.H, kCols * kVecs));
+  return blocks ? launch_dependent(norm_quant_kernel<T, kCols, kVecs, kAccess, true>, grid, block,
+                                   0, stream, p)
+                : launch_dependent(norm_quant_kernel<T, kCols, kVecs, kAccess, false>, grid, block,
+                                   0, stream, p);
 }
 
-// CTAs of a ring kernel that an SM holds: by shared memory, threads and 64 registers each.
-int ring_ctas(int smem, int threads) {
+// CTAs of a ring kernel that an SM holds, by shared memory and registers per thread.
+int ring_ctas(int smem, int threads, int registers) {
   int c = kMaxSmSmem / (smem + 1024);
-  if (c > 65536 / 64 / threads) c = 65536 / 64 / threads;
+  if (c > 65536 / registers / threads) c = 65536 / registers / threads;
   return c < 1 ? 1 : c;
 }
 
 template <class T, int kVecs, int kStages>
 cudaError_t launch_norm_ring(const NormParams& p, int sms, bool blocks, void* stream) {
-  const int threads = threads_for(p.H, kVecs);
-  const int smem = kStages * ring_stage_bytes<T, kVecs>(p.residual != nullptr ? 2 : 1, threads);
-  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads);
+  const int threads = threads_for(p.H, 16 * kVecs);
+  const int smem =
+      kStages * ring_stage_bytes<T, 16, kVecs>(p.residual != nullptr ? 2 : 1, threads);
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads, kVecs == 1 ? 64 : 128);
   const dim3 grid(static_cast<unsigned>(p.T < most ? p.T : most));
   cudaError_t e = blocks ? allow_smem<norm_ring_kernel<T, kVecs, kStages, true>>()
                          : allow_smem<norm_ring_kernel<T, kVecs, kStages, false>>();
@@ -480,34 +513,51 @@ cudaError_t launch_norm_ring(const NormParams& p, int sms, bool blocks, void* st
                                    dim3(threads), smem, stream, p);
 }
 
+// Stages of the ring: the rows under way should be about 28 KB per CTA at H = 7168.  More
+// slows the memory down (GB300, 8192 x 7168 bf16, block scales, y: with a residual, two rows
+// to a stage, 2 / 3 / 4 stages take 88.3 / 94.0 / 95.0 us), less does not cover its latency
+// (without: 52.9 / 48.0 / 47.7 us).  From memory directly, a row per CTA: 100.3 and 68.5 us.
+template <class T, int kVecs>
+cudaError_t launch_norm_ring(const NormParams& p, int sms, bool blocks, void* stream) {
+  if constexpr (sizeof(T) == 2)
+    if (p.residual == nullptr) return launch_norm_ring<T, kVecs, 3>(p, sms, blocks, stream);
+  return launch_norm_ring<T, kVecs, 2>(p, sms, blocks, stream);
+}
+
 template <class T>
-cudaError_t launch_norm(const NormParams& p, int sms, bool wide, bool blocks, void* stream) {
+cudaError_t launch_norm(const NormParams& p, int sms, Access access, bool blocks, void* stream) {
   const int64_t n = p.H;
-  if (!wide) return launch_norm<T, 4, false>(p, blocks, stream);
-  if (p.T > 4 * sms && n <= 8192) {
-    constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
-    if (n <= 4096) return launch_norm_ring<T, 1, kStages>(p, sms, blocks, stream);
-    return launch_norm_ring<T, 2, kStages>(p, sms, blocks, stream);
+  if (access == Access::k32) {
+    const bool many = p.T > 4 * sms;
+    if (n <= 8192)
+      return many ? launch_norm_ring<T, 1>(p, sms, blocks, stream)
+                  : launch_norm<T, 16, 1, Access::k32>(p, blocks, stream);
+    if (n <= 16384) {
+      if constexpr (sizeof(T) == 2)  // (stages of 32-bit rows would not fit)
+        if (many) return launch_norm_ring<T, 2>(p, sms, blocks, stream);
+      return launch_norm<T, 16, 2, Access::k32>(p, blocks, stream);
+    }
+    return launch_norm<T, 16, 4, Access::k32>(p, blocks, stream);
   }
-  if (n <= 8 * kMaxThreads) return launch_norm<T, 1, true>(p, blocks, stream);
-  if (n <= 16 * kMaxThreads) return launch_norm<T, 2, true>(p, blocks, stream);
-  return launch_norm<T, 4, true>(p, blocks, stream);
+  return access == Access::k16 ? launch_norm<T, 8, 4, Access::k16>(p, blocks, stream)
+                               : launch_norm<T, 8, 4, Access::kElement>(p, blocks, stream);
 }
 
 // The gradient's first kernel; *parts: the rows of partial weight gradients that it writes.
 template <class T, int kVecs, bool kWide>
 cudaError_t launch_backward(const NormBackwardParams& p, int64_t* parts, void* stream) {
   return launch_dependent(norm_backward_kernel<T, kVecs, kWide>,
-                          dim3(static_cast<unsigned>(*parts)), dim3(threads_for(p.H, kVecs)), 0,
+                          dim3(static_cast<unsigned>(*parts)), dim3(threads_for(p.H, 8 * kVecs)), 0,
                           stream, p);
 }
 
 template <class T, int kVecs, int kStages>
 cudaError_t launch_backward_ring(const NormBackwardParams& p, int sms, int64_t* parts,
                                  void* stream) {
-  const int threads = threads_for(p.H, kVecs);
-  const int smem = kStages * ring_stage_bytes<T, kVecs>(p.dresidual != nullptr ? 3 : 2, threads);
-  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads);
+  const int threads = threads_for(p.H, 8 * kVecs);
+  const int smem =
+      kStages * ring_stage_bytes<T, 8, kVecs>(p.dresidual != nullptr ? 3 : 2, threads);
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads, 64);
   if (*parts > most) *parts = most;
   cudaError_t e = allow_smem<norm_backward_ring_kernel<T, kVecs, kStages>>();
   if (e != cudaSuccess) return e;
@@ -520,10 +570,11 @@ cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int
                             void* stream) {
   const int64_t n = p.H;
   if (!wide) return launch_backward<T, 4, false>(p, parts, stream);
-  if (n <= 8192 && p.T > 2 * sms) {
-    if (n <= 4096) return launch_backward_ring<T, 1, 2>(p, sms, parts, stream);
-    return launch_backward_ring<T, 2, 2>(p, sms, parts, stream);
-  }
+  const bool many = p.T > 2 * sms;
+  if (n <= 4096)
+    return many ? launch_backward_ring<T, 1, 2>(p, sms, parts, stream)
+                : launch_backward<T, 1, true>(p, parts, stream);
+  if (n <= 8192 && many) return launch_backward_ring<T, 2, 2>(p, sms, parts, stream);
   if (n <= 16 * kMaxThreads) return launch_backward<T, 2, true>(p, parts, stream);
   return launch_backward<T, 4, true>(p, parts, stream);
 }
@@ -558,10 +609,17 @@ mslkb_status mslkb_add_rms_norm_quant(const void* x, const void* residual, const
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const int64_t size = dtype_bytes(dtype);
-  const bool wide = H % 8 == 0 && ldx * size % 16 == 0 && aligned_to(x, 16) &&
-                    (residual == nullptr || (ldr * size % 16 == 0 && aligned_to(residual, 16))) &&
-                    aligned_to(weight, 16) && aligned_to(q, 8) && aligned_to(residual_out, 16) &&
-                    aligned_to(y, 16);
+  const auto aligned = [&](int64_t out, int64_t in) {  // bytes of the outputs' and inputs' rows
+    return H * size % out == 0 && ldx * size % in == 0 && aligned_to(x, in) &&
+           (residual == nullptr || (ldr * size % in == 0 && aligned_to(residual, in))) &&
+           aligned_to(weight, out) && aligned_to(q, out / 2) && aligned_to(residual_out, out) &&
+           aligned_to(y, out);
+  };
+  Access access = Access::kElement;
+  if (H % 16 == 0 && aligned(32, 16))
+    access = Access::k32;
+  else if (H % 8 == 0 && aligned(16, 16))
+    access = Access::k16;
   NormParams p{x,    residual, weight, static_cast<uint8_t*>(q),
                scale, residual_out, y, rstd, T, ldx, ldr,
                static_cast<int32_t>(H), weight_fp32, static_cast<float>(eps),
@@ -569,11 +627,11 @@ mslkb_status mslkb_add_rms_norm_quant(const void* x, const void* residual, const
   TraceRange range("add_rms_norm_quant", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_norm<__nv_bfloat16>(p, sms, wide, groupwise != 0, stream);
+    e = launch_norm<__nv_bfloat16>(p, sms, access, groupwise != 0, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_norm<__half>(p, sms, wide, groupwise != 0, stream);
+    e = launch_norm<__half>(p, sms, access, groupwise != 0, stream);
   else
-    e = launch_norm<float>(p, sms, wide, groupwise != 0, stream);
+    e = launch_norm<float>(p, sms, access, groupwise != 0, stream);
   return launch_status(e);
 }
 

@@ -24,13 +24,16 @@ struct RouteParams {
   float* weights;
   int64_t T, ld;
   int32_t E, top_k;
-  int32_t sigmoid;
   int32_t groups, top_groups, group_top;
-  int32_t by_logits;  // softmax whose order is that of the logits
+  int32_t per_group;    // experts of a group
+  int32_t group_shift;  // log2 of the lanes of a group; -1: a group is not a power of two lanes
   int32_t renormalize;
-  int32_t wide;       // rows in whole, aligned 16-byte pieces
+  int32_t wide;  // rows (and the bias) in whole, aligned 16-byte pieces
   float scale;
 };
+
+// What experts are chosen by: the logits (a softmax keeps their order), or the score + bias.
+enum class Score { kLogits, kSoftmax, kSigmoid };
 
 // An integer that orders as the float does: NaN above all; -inf, which masks, is kMaskedKey,
 // and nothing else comes that low.
@@ -70,7 +73,51 @@ __device__ __forceinline__ void sort_keys(uint32_t (&s)[kN]) {
           }
 }
 
+// kPer consecutive floats from `first`, `fill` past the n-th.
 template <class T, int kPer>
+__device__ __forceinline__ void load_lane(const T* row, int first, int n, bool wide, float fill,
+                                          float (&x)[kPer]) {
+  if constexpr (kPer * sizeof(T) >= 16) {
+    if (wide) {
+      constexpr int kPiece = 16 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < kPer; i += kPiece) {
+        const bool in = first + i < n;
+        const uint4 r = in ? load16(row + first + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4) {
+            x[i + j] = in ? __uint_as_float(w[j]) : fill;
+          } else {
+            const float2 f = unpack2(w[j], T());
+            x[i + 2 * j] = in ? f.x : fill;
+            x[i + 2 * j + 1] = in ? f.y : fill;
+          }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = first + i < n ? to_float(row[first + i]) : fill;
+}
+
+// How many of the groups are worth more than this lane's, `mine`, ties to the lower group.
+// Lane g << shift holds what group g is worth; a group's lanes share the comparisons.
+__device__ __forceinline__ int better_groups(uint32_t mine, int group, int groups, int shift) {
+  const int lane = threadIdx.x & 31, lanes = 1 << shift;
+  int better = 0;
+  for (int g0 = 0; g0 < groups; g0 += lanes) {
+    const int g = g0 + (lane & (lanes - 1));
+    const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, (g << shift) & 31);
+    better += g < groups && (other > mine || (other == mine && g < group));
+  }
+  for (int d = 1; d < lanes; d <<= 1) better += __shfl_xor_sync(0xFFFFFFFFu, better, d);
+  return better;
+}
+
+template <class T, int kPer, Score kScore>
 __global__ void __launch_bounds__(kWarps * 32)
     route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ uint32_t shared_keys[];  // [kWarps][E], groups that lanes do not hold whole
@@ -83,38 +130,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int first = lane * kPer;
 
   float x[kPer];
-  bool loaded = false;
-  if constexpr (kPer * sizeof(T) >= 16) {
-    if (p.wide) {
-      constexpr int kPiece = 16 / sizeof(T);
-#pragma unroll
-      for (int i = 0; i < kPer; i += kPiece) {
-        const bool in = first + i < p.E;
-        const uint4 r = in ? load16(row + first + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(T) == 4) {
-            x[i + j] = in ? __uint_as_float(w[j]) : kMasked;
-          } else {
-            const float2 f = unpack2(w[j], T());
-            x[i + 2 * j] = in ? f.x : kMasked;
-            x[i + 2 * j + 1] = in ? f.y : kMasked;
-          }
-        }
-      }
-      loaded = true;
-    }
-  }
-  if (!loaded) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      x[i] = first + i < p.E ? to_float(row[first + i]) : kMasked;
-  }
+  load_lane<T, kPer>(row, first, p.E, p.wide, kMasked, x);
 
   // softmax over all experts: its maximum and sum
   float top = 0.f, total = 1.f;
-  if (!p.sigmoid && !(p.by_logits && p.renormalize)) {
+  if (kScore == Score::kSoftmax || (kScore == Score::kLogits && !p.renormalize)) {
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, x[i]);
@@ -127,45 +147,46 @@ __global__ void __launch_bounds__(kWarps * 32)
     top = m;
     total = warp_sum(s);
   }
-  // what expert e with logit v is chosen by
-  auto choice = [&](float v, int e) {
-    if (p.by_logits || v == kMasked) return v;
-    float c = p.sigmoid ? sigmoid_of(v) : expf(v - top) / total;
-    if (p.bias != nullptr) c += p.bias[e];
-    return c;
+  // the key of an expert with logit v and bias b (0 without): masked by its logit or its bias
+  auto choice_key = [&](float v, float b) {
+    if constexpr (kScore == Score::kLogits) return order_key(v);
+    const float c = (kScore == Score::kSigmoid ? sigmoid_of(v) : expf(v - top) / total) + b;
+    return order_key(v == kMasked ? v : c);
   };
   uint32_t key[kPer];
+  {
+    float b[kPer];
+    if (kScore != Score::kLogits && p.bias != nullptr) {
+      load_lane<float, kPer>(p.bias, first, p.E, p.wide, 0.f, b);
+    } else {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = order_key(choice(x[i], first + i));
+      for (int i = 0; i < kPer; ++i) b[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = choice_key(x[i], b[i]);
+  }
 
   if (p.groups > 1) {
-    const int per = p.E / p.groups;
-    const int lanes = per / kPer;  // lanes of a group, where a group is whole lanes
-    if (per % kPer == 0 && (lanes & (lanes - 1)) == 0) {
+    if (p.group_shift >= 0) {
       uint32_t best = 0, second = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         second = max(second, min(best, key[i]));
         best = max(best, key[i]);
       }
-      for (int d = 1; d < lanes; d <<= 1) {
+      for (int d = 1; d < 1 << p.group_shift; d <<= 1) {
         const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, d);
         const uint32_t s = __shfl_xor_sync(0xFFFFFFFFu, second, d);
         second = max(max(second, s), min(best, b));
         best = max(best, b);
       }
       const uint32_t mine = worth_key(best, second, p.group_top);
-      const int group = lane / lanes;
-      int better = 0;
-      for (int g = 0; g < p.groups; ++g) {
-        const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, g * lanes);
-        better += other > mine || (other == mine && g < group);
-      }
-      if (better >= p.top_groups) {
+      if (better_groups(mine, lane >> p.group_shift, p.groups, p.group_shift) >= p.top_groups) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) key[i] = 0;
       }
     } else {
+      const int per = p.per_group;
       uint32_t* keys = shared_keys + warp * p.E;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
@@ -180,59 +201,71 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
       }
       const uint32_t mine = worth_key(best, second, p.group_top);
-      int better = 0;
-      for (int g = 0; g < p.groups; ++g) {
-        const uint32_t other = __shfl_sync(0xFFFFFFFFu, mine, g);
-        better += other > mine || (other == mine && g < lane);
-      }
+      const int better = better_groups(mine, lane, p.groups, 0);
       const uint32_t kept = __ballot_sync(0xFFFFFFFFu, better < p.top_groups);
+      // the groups of the lane's experts, from the first one's on
+      int group = first / per, left = per - (first - group * per);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (first + i < p.E && !((kept >> ((first + i) / per)) & 1u)) key[i] = 0;
+      for (int i = 0; i < kPer; ++i) {
+        if (!((kept >> (group & 31)) & 1u)) key[i] = 0;
+        if (--left == 0) ++group, left = per;
+      }
     }
   }
 
-  // keys with the expert's index in the lowest bits, the lower index larger
+  // keys with the expert's index in the lowest bits, the lower index larger; a lane's keys as
+  // sorted lists of at most eight (sorting 8 takes 19 comparisons, 32 would take 191)
   constexpr uint32_t kIndex = 32 * kPer - 1;
+  constexpr int kList = kPer < 8 ? kPer : 8, kLists = kPer / kList;
   int id = -1;  // lane j: the j-th choice
   float logit = kMasked;
   {
-    uint32_t s[kPer];
+    uint32_t s[kLists][kList];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) s[i] = (key[i] & ~kIndex) | (kIndex - (first + i));
-    sort_keys(s);
-    uint32_t mine = 0, last = 0;
+    for (int l = 0; l < kLists; ++l) {
+#pragma unroll
+      for (int i = 0; i < kList; ++i)
+        s[l][i] = (key[l * kList + i] & ~kIndex) | (kIndex - (first + l * kList + i));
+      sort_keys(s[l]);
+    }
+    auto largest = [&] {
+      uint32_t m = s[0][0];
+#pragma unroll
+      for (int l = 1; l < kLists; ++l) m = max(m, s[l][0]);
+      return __reduce_max_sync(0xFFFFFFFFu, m);
+    };
+    uint32_t mine = 0;
     for (int j = 0; j < p.top_k; ++j) {
-      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, s[0]);
-      if ((m | kIndex) <= kMaskedKey) break;
-      last = m;
+      const uint32_t m = largest();
       if (lane == j) mine = m;
-      if (s[0] == m) {
 #pragma unroll
-        for (int i = 0; i + 1 < kPer; ++i) s[i] = s[i + 1];
-        s[kPer - 1] = 0;
+      for (int l = 0; l < kLists; ++l) {
+        if (s[l][0] == m) {  // one list of one lane, unless nothing is left
+#pragma unroll
+          for (int i = 0; i + 1 < kList; ++i) s[l][i] = s[l][i + 1];
+          s[l][kList - 1] = 0;
+        }
       }
     }
-    if (mine != 0) {
+    if ((mine | kIndex) > kMaskedKey) {
       id = static_cast<int>(kIndex - (mine & kIndex));
       logit = to_float(row[id]);  // an L1 hit
     }
     // A logit of 16 bits has the index's bits to spare.  Otherwise the choice stands if the
     // chosen are in the order of their exact keys, and the next one differs in the bits kept.
-    if (!(p.by_logits && sizeof(T) == 2)) {
-      const uint32_t next = __reduce_max_sync(0xFFFFFFFFu, s[0]);
-      const uint32_t exact = id >= 0 ? order_key(choice(logit, id)) : 0;
+    if constexpr (!(kScore == Score::kLogits && sizeof(T) == 2)) {
+      const uint32_t next = largest();
+      const float b = kScore != Score::kLogits && p.bias != nullptr && id >= 0 ? p.bias[id] : 0.f;
+      const uint32_t exact = id >= 0 ? choice_key(logit, b) : 0;
       const uint32_t above = __shfl_up_sync(0xFFFFFFFFu, exact, 1);
       const int above_id = __shfl_up_sync(0xFFFFFFFFu, id, 1);
       const bool wrong = id >= 0 && lane > 0 && (above < exact || (above == exact && above_id > id));
-      const bool close = last != 0 && ((last ^ next) & ~kIndex) == 0;
-      if (__any_sync(0xFFFFFFFFu, wrong) || close) {
-        uint32_t best = 0;
-        int at = 0;
+      const bool close = id >= 0 && lane == p.top_k - 1 && ((mine ^ next) & ~kIndex) == 0;
+      if (__any_sync(0xFFFFFFFFu, wrong || close)) {
         id = -1;
         for (int j = 0; j < p.top_k; ++j) {
-          best = key[0];
-          at = 0;
+          uint32_t best = key[0];
+          int at = 0;
 #pragma unroll
           for (int i = 1; i < kPer; ++i)
             if (key[i] > best) best = key[i], at = i;
@@ -252,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   // weights, one choice per lane
   float w = 0.f;
-  if (p.sigmoid) {
+  if (kScore == Score::kSigmoid) {
     if (id >= 0) w = sigmoid_of(logit);
     if (p.renormalize) w /= warp_sum(w) + 1e-20f;
   } else if (p.renormalize) {
@@ -364,16 +397,29 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int e = lane; e < p.E; e += 32) out[e] = from_float<T>(d[e]);
 }
 
-template <class T>
-cudaError_t launch_route(const RouteParams& p, void* stream) {
+template <class T, int kPer>
+cudaError_t launch_route(RouteParams p, Score score, void* stream) {
   const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
-  const size_t smem = p.groups > 1 ? sizeof(uint32_t) * kWarps * p.E : 0;
-  if (p.E <= 32) return launch_dependent(route_kernel<T, 1>, grid, block, smem, stream, p);
-  if (p.E <= 64) return launch_dependent(route_kernel<T, 2>, grid, block, smem, stream, p);
-  if (p.E <= 128) return launch_dependent(route_kernel<T, 4>, grid, block, smem, stream, p);
-  if (p.E <= 256) return launch_dependent(route_kernel<T, 8>, grid, block, smem, stream, p);
-  if (p.E <= 512) return launch_dependent(route_kernel<T, 16>, grid, block, smem, stream, p);
-  return launch_dependent(route_kernel<T, 32>, grid, block, smem, stream, p);
+  p.group_shift = -1;
+  for (int shift = 0; shift <= 5; ++shift)
+    if (p.per_group == kPer << shift) p.group_shift = shift;
+  const size_t smem =
+      p.groups > 1 && p.group_shift < 0 ? sizeof(uint32_t) * kWarps * p.E : 0;
+  if (score == Score::kLogits)
+    return launch_dependent(route_kernel<T, kPer, Score::kLogits>, grid, block, smem, stream, p);
+  if (score == Score::kSoftmax)
+    return launch_dependent(route_kernel<T, kPer, Score::kSoftmax>, grid, block, smem, stream, p);
+  return launch_dependent(route_kernel<T, kPer, Score::kSigmoid>, grid, block, smem, stream, p);
+}
+
+template <class T>
+cudaError_t launch_route(const RouteParams& p, Score score, void* stream) {
+  if (p.E <= 32) return launch_route<T, 1>(p, score, stream);
+  if (p.E <= 64) return launch_route<T, 2>(p, score, stream);
+  if (p.E <= 128) return launch_route<T, 4>(p, score, stream);
+  if (p.E <= 256) return launch_route<T, 8>(p, score, stream);
+  if (p.E <= 512) return launch_route<T, 16>(p, score, stream);
+  return launch_route<T, 32>(p, score, stream);
 }
 
 mslkb_status check_route(int64_t T, int64_t E, int64_t ld, int64_t top_k, int32_t score,
@@ -409,20 +455,25 @@ mslkb_status mslkb_route_experts(const void* logits, const float* bias, int32_t*
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const bool by_logits = score == MSLKB_SOFTMAX && bias == nullptr &&
                          (group_top == 1 || num_groups == 1);
+  const Score by = score == MSLKB_SIGMOID ? Score::kSigmoid
+                                          : (by_logits ? Score::kLogits : Score::kSoftmax);
   const int64_t size = dtype_bytes(dtype);
-  const bool wide = aligned_to(logits, 16) && ld * size % 16 == 0 && E * size % 16 == 0;
-  const RouteParams p{logits, bias, ids, weights, T, ld, static_cast<int32_t>(E),
-                      static_cast<int32_t>(top_k), score == MSLKB_SIGMOID,
-                      static_cast<int32_t>(num_groups), static_cast<int32_t>(topk_groups),
-                      group_top, by_logits, renormalize, wide, static_cast<float>(scale)};
+  RouteParams p{};
+  p.logits = logits, p.bias = bias, p.ids = ids, p.weights = weights;
+  p.T = T, p.ld = ld, p.E = static_cast<int32_t>(E), p.top_k = static_cast<int32_t>(top_k);
+  p.groups = static_cast<int32_t>(num_groups), p.top_groups = static_cast<int32_t>(topk_groups);
+  p.group_top = group_top, p.per_group = static_cast<int32_t>(E / num_groups);
+  p.renormalize = renormalize, p.scale = static_cast<float>(scale);
+  p.wide = aligned_to(logits, 16) && aligned_to(bias, 16) && ld * size % 16 == 0 &&
+           E * size % 16 == 0 && E % 4 == 0;
   TraceRange range("route_experts", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_route<__nv_bfloat16>(p, stream);
+    e = launch_route<__nv_bfloat16>(p, by, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_route<__half>(p, stream);
+    e = launch_route<__half>(p, by, stream);
   else
-    e = launch_route<float>(p, stream);
+    e = launch_route<float>(p, by, stream);
   return launch_status(e);
 }
 

@@ -33,17 +33,15 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
             "mslkb_add_rms_norm_quant_backward": [p] * 8 + [i64] * 3 + [i32, i32, p],
             "mslkb_route_experts": [p] * 4 + [i64] * 4 + [i32, i64, i64, i32, i32, f64, i32, p],
             "mslkb_route_experts_backward": [p] * 4 + [i64] * 4 + [i32, i32, f64, i32, p],
-            "mslkb_moe_dispatch": [p] * 8 + [i64] * 6 + [p],
+            "mslkb_moe_dispatch": [p] * 7 + [i64] * 5 + [p],
             "mslkb_moe_combine": [p] * 4 + [i64] * 4 + [i32, p],
             "mslkb_moe_combine_backward": [p] * 6 + [i64] * 4 + [i32, p],
             "mslkb_swiglu_quant": [p] * 5 + [i64] * 3 + [i32, i32, p],
             "mslkb_swiglu_quant_backward": [p] * 4 + [i64] * 2 + [i32, p]}.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
-    for name, count in (("mslkb_add_rms_norm_quant_backward_workspace_bytes", 2),
-                        ("mslkb_moe_dispatch_workspace_bytes", 3)):
-        fn = getattr(L, name)
-        fn.argtypes, fn.restype = [i64] * count, i64
+    L.mslkb_add_rms_norm_quant_backward_workspace_bytes.argtypes = [i64, i64]
+    L.mslkb_add_rms_norm_quant_backward_workspace_bytes.restype = i64
     return L
 
 
@@ -82,15 +80,10 @@ def mslkb_route_experts_backward(dweights, logits, ids, dlogits, T, E, ld, top_k
                                                   score, renormalize, scale, dtype, stream)
 
 
-def mslkb_moe_dispatch_workspace_bytes(T, top_k, E) -> int:
-    return _fx.lib().mslkb_moe_dispatch_workspace_bytes(T, top_k, E)
-
-
-def mslkb_moe_dispatch(x, x_scale, ids, x_out, scale_out, m_sizes, dest, workspace,
-                       workspace_bytes, T, top_k, E, row_bytes, scale_cols, stream=0) -> int:
-    return _fx.lib().mslkb_moe_dispatch(x, x_scale, ids, x_out, scale_out, m_sizes, dest,
-                                        workspace, workspace_bytes, T, top_k, E, row_bytes,
-                                        scale_cols, stream)
+def mslkb_moe_dispatch(x, x_scale, ids, x_out, scale_out, m_sizes, dest, T, top_k, E, row_bytes,
+                       scale_cols, stream=0) -> int:
+    return _fx.lib().mslkb_moe_dispatch(x, x_scale, ids, x_out, scale_out, m_sizes, dest, T,
+                                        top_k, E, row_bytes, scale_cols, stream)
 
 
 def mslkb_moe_combine(rows, dest, weights, out, T, top_k, H, R, dtype, stream=0) -> int:
@@ -428,15 +421,12 @@ def moe_dispatch(x, x_scale, ids, num_experts, *, out=None, stream=None):
                        _new(stream, dev, (T, k), _I32))
     xo, so, m_sizes, dest = _unpack(out, 4)
     _same(so, "x_scale", x_scale is not None)
-    L = _fx.lib()
-    need = L.mslkb_moe_dispatch_workspace_bytes(T, k, num_experts)
-    ws = _new(stream, dev, (need,), _torch.uint8) if need else None
-    _call(L.mslkb_moe_dispatch(
+    _call(_fx.lib().mslkb_moe_dispatch(
         xp, sp, ip, _dense(xo, "x (out)", x.dtype, (N, H), dev),
         None if so is None else _dense(so, "x_scale (out)", _F32, (N, *tail), dev),
         _dense(m_sizes, "m_sizes", _torch.int64, (num_experts,), dev),
-        _dense(dest, "dest", _I32, (T, k), dev), ws.data_ptr() if need else None, need, T, k,
-        num_experts, H * x.element_size(), cols, _stream(stream, dev)), "moe_dispatch")
+        _dense(dest, "dest", _I32, (T, k), dev), T, k, num_experts, H * x.element_size(), cols,
+        _stream(stream, dev)), "moe_dispatch")
     return out
 
 

@@ -335,11 +335,11 @@ MSLKB_API mslkb_status mslkb_f8f8bf16_rowwise_grouped_stacked_noalloc(
  * alignment that suits the element type is accepted; 16-byte aligned rows take the wide
  * path.  Inputs named with an `ld` argument may be slices of wider rows (ld elements from
  * row to row, ld >= the row's length); everything else is dense.  An output may be the same
- * buffer as an input only where that is said.  Nothing is allocated: the two calls that
- * need scratch take it as `workspace` (16-byte aligned, contents need not be initialised,
- * not shared by calls that may run at the same time) of at least the bytes that the
- * matching *_workspace_bytes function returns.  Sums are made in a fixed order: equal
- * inputs give equal bits.
+ * buffer as an input only where that is said.  Nothing is allocated: the one call that
+ * needs scratch takes it as `workspace` (16-byte aligned, contents need not be initialised,
+ * not shared by calls that may run at the same time) of at least the bytes that its
+ * *_workspace_bytes function returns.  Sums are made in a fixed order: equal inputs give
+ * equal bits.
  *
  * e4m3 outputs: one scale per row (groupwise = 0) or per 128 columns (groupwise = 1; the
  * row length must be a multiple of 128).  scale = amax / 448 over the row or block and
@@ -439,11 +439,10 @@ MSLKB_API mslkb_status mslkb_route_experts_backward(
  *
  * T * top_k is limited to MSLKB_MAX_DIM / 2.
  */
-MSLKB_API int64_t mslkb_moe_dispatch_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
 MSLKB_API mslkb_status mslkb_moe_dispatch(
     const void *x, const float *x_scale, const int32_t *ids, void *x_out, float *scale_out,
-    int64_t *m_sizes, int32_t *dest, void *workspace, int64_t workspace_bytes, int64_t T,
-    int64_t top_k, int64_t E, int64_t row_bytes, int64_t scale_cols, void *stream);
+    int64_t *m_sizes, int32_t *dest, int64_t T, int64_t top_k, int64_t E, int64_t row_bytes,
+    int64_t scale_cols, void *stream);
 
 /*
  * The weighted sum of a token's rows:

@@ -74,7 +74,7 @@ NORM_CASES = [  # tokens, hidden, groupwise
     (2, 16392, False), (2, 32768, True), (1, 32768, False), (2, 32767, False), (300, 256, True),
     # many rows: the persistent kernel, CTAs with several rows and with one
     (609, 7168, False), (1500, 8192, True), (2000, 128, True), (1300, 1000, False),
-    (700, 4096, False), (1250, 4104, False)]
+    (700, 4096, False), (1250, 4104, False), (620, 16384, True), (640, 12304, False)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
@@ -457,7 +457,8 @@ def random_ids(g, T, k, E, elsewhere=0.0):
 @pytest.mark.parametrize("T,k,E,H,cols,elsewhere", [
     (1, 1, 1, 16, 1, 0.0), (1, 8, 32, 7168, 1, 0.5), (3, 2, 8, 128, 1, 0.0), (129, 8, 256, 256, 2, 0.0),
     (511, 2, 16, 48, 1, 0.3), (512, 2, 16, 48, 0, 0.0), (513, 2, 16, 33, 1, 0.0),
-    (2048, 1, 1024, 16, 1, 0.2), (1500, 6, 60, 64, 3, 0.9), (5000, 8, 128, 16, 1, 0.1),
+    (2048, 1, 1024, 16, 1, 0.2), (2049, 1, 1024, 16, 1, 0.0), (300, 7, 9, 32, 1, 0.1),
+    (9000, 8, 1024, 16, 1, 0.2), (70000, 2, 4, 16, 0, 0.5), (4099, 1, 1, 16, 0, 0.0), (1500, 6, 60, 64, 3, 0.9), (5000, 8, 128, 16, 1, 0.1),
     (100, 32, 40, 80, 1, 0.0), (64, 4, 3, 1, 1, 0.0), (40, 8, 16, 100, 1, 1.0)])
 def test_dispatch(T, k, E, H, cols, elsewhere):
     g = gen(T + E)
