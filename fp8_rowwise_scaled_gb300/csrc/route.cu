@@ -315,22 +315,23 @@ struct RouteBackwardParams {
   int32_t E, top_k;
   int32_t sigmoid;
   int32_t renormalize;
+  int32_t wide;  // rows in whole, aligned 16-byte pieces
   float scale;
 };
 
-// One warp per token; the row of gradients is built in shared memory (zeros, or the full
-// softmax's part), the chosen experts' parts are added, and it leaves in one coalesced pass.
-template <class T>
+// One warp per token, kPer consecutive experts per lane; what the chosen experts get is added
+// to the row in shared memory.
+template <class T, int kPer>
 __global__ void __launch_bounds__(kWarps * 32)
     route_backward_kernel(const __grid_constant__ RouteBackwardParams p) {
-  extern __shared__ float grads[];  // [kWarps][E]
+  __shared__ float grads[kWarps][32 * kPer];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (t >= p.T) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float* d = grads + warp * p.E;
+  const int first = lane * kPer;
 
   int id = -1;
   float g = 0.f;
@@ -340,61 +341,85 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (id >= 0) g = p.dweights[t * p.top_k + lane] * p.scale;
   }
   const float logit = id >= 0 ? to_float(row[id]) : kMasked;
-  float mine = 0.f;  // what the chosen expert's logit gets
+  float mine;          // what the chosen expert's logit gets
+  float v[kPer] = {};  // what every expert's logit gets
   if (!p.sigmoid && !p.renormalize) {
-    float m = kMasked;
-    for (int e = lane; e < p.E; e += 32) {
-      const float x = to_float(row[e]);
-      d[e] = x;
-      m = fmaxf(m, x);
-    }
+    load_lane<T, kPer>(row, first, p.E, p.wide, kMasked, v);
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
     float sum = 0.f;
-    for (int e = lane; e < p.E; e += 32) {
-      const float v = d[e] == kMasked ? 0.f : expf(d[e] - m);
-      d[e] = v;
-      sum += v;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      v[i] = v[i] == kMasked ? 0.f : expf(v[i] - m);
+      sum += v[i];
     }
     sum = warp_sum(sum);
-    const float chosen = logit != kMasked ? expf(logit - m) / sum : 0.f;
-    mine = chosen * g;
+    mine = logit != kMasked ? expf(logit - m) / sum * g : 0.f;
     const float along = warp_sum(mine);
-    const float factor = sum > 0.f || sum != sum ? along / sum : 0.f;  // all masked: no gradient
-    for (int e = lane; e < p.E; e += 32) d[e] = -d[e] * factor;
-  } else {
-    if (p.sigmoid) {
-      const float s = id >= 0 ? sigmoid_of(logit) : 0.f;
-      if (p.renormalize) {
-        const float total = warp_sum(s) + 1e-20f;
-        g = (g - warp_sum(g * s) / total) / total;
-      }
-      mine = g * s * (1.f - s);
-    } else {
-      float m = logit;
+    const float factor = sum == 0.f ? 0.f : -along / sum;  // all masked: no gradient
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-      float w = logit != kMasked ? expf(logit - m) : 0.f;
-      const float total = warp_sum(w);
-      w = logit != kMasked ? w / total : 0.f;
-      mine = w * (g - warp_sum(w * g));
+    for (int i = 0; i < kPer; ++i) v[i] *= factor;
+  } else if (p.sigmoid) {
+    const float s = id >= 0 ? sigmoid_of(logit) : 0.f;
+    if (p.renormalize) {
+      const float total = warp_sum(s) + 1e-20f;
+      g = (g - warp_sum(g * s) / total) / total;
     }
-    for (int e = lane; e < p.E; e += 32) d[e] = 0.f;
-  }
-  __syncwarp();
-  // experts named twice (ids of another origin) add up, in the order of the slots
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, id >= 0 ? id : -1 - lane);
-  if (__all_sync(0xFFFFFFFFu, same == 1u << lane)) {
-    if (id >= 0) d[id] += mine;
+    mine = g * s * (1.f - s);
   } else {
+    float m = logit;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    float w = logit != kMasked ? expf(logit - m) : 0.f;
+    const float total = warp_sum(w);
+    w = logit != kMasked ? w / total : 0.f;
+    mine = w * (g - warp_sum(w * g));
+  }
+  float* d = grads[warp];
+  // experts named twice (ids of another origin): of the lanes that sign such a place, one stays
+  if (id >= 0) d[id] = __int_as_float(lane);
+  __syncwarp();
+  const bool twice = __any_sync(0xFFFFFFFFu, id >= 0 && __float_as_int(d[id]) != lane);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) d[first + i] = v[i];
+  __syncwarp();
+  if (!twice) {
+    if (id >= 0) d[id] += mine;
+  } else {  // they add up, in the order of the slots
     for (int j = 0; j < p.top_k; ++j) {
       if (lane == j && id >= 0) d[id] += mine;
       __syncwarp();
     }
   }
   __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = d[first + i];
   T* out = static_cast<T*>(p.dlogits) + t * p.E;
-  for (int e = lane; e < p.E; e += 32) out[e] = from_float<T>(d[e]);
+  if constexpr (kPer * sizeof(T) >= 16) {
+    if (p.wide) {
+      constexpr int kPiece = 16 / sizeof(T);
+#pragma unroll
+      for (int i = 0; i < kPer; i += kPiece) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (sizeof(T) == 4)
+            w[j] = __float_as_uint(v[i + j]);
+          else
+            w[j] = pack2(v[i + 2 * j], v[i + 2 * j + 1], T());
+        }
+        if (first + i < p.E) store16(out + first + i, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (first + i < p.E) out[first + i] = from_float<T>(v[i]);
 }
 
 template <class T, int kPer>
@@ -420,6 +445,17 @@ cudaError_t launch_route(const RouteParams& p, Score score, void* stream) {
   if (p.E <= 256) return launch_route<T, 8>(p, score, stream);
   if (p.E <= 512) return launch_route<T, 16>(p, score, stream);
   return launch_route<T, 32>(p, score, stream);
+}
+
+template <class T>
+cudaError_t launch_backward(const RouteBackwardParams& p, void* stream) {
+  const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
+  if (p.E <= 32) return launch_dependent(route_backward_kernel<T, 1>, grid, block, 0, stream, p);
+  if (p.E <= 64) return launch_dependent(route_backward_kernel<T, 2>, grid, block, 0, stream, p);
+  if (p.E <= 128) return launch_dependent(route_backward_kernel<T, 4>, grid, block, 0, stream, p);
+  if (p.E <= 256) return launch_dependent(route_backward_kernel<T, 8>, grid, block, 0, stream, p);
+  if (p.E <= 512) return launch_dependent(route_backward_kernel<T, 16>, grid, block, 0, stream, p);
+  return launch_dependent(route_backward_kernel<T, 32>, grid, block, 0, stream, p);
 }
 
 mslkb_status check_route(int64_t T, int64_t E, int64_t ld, int64_t top_k, int32_t score,
@@ -491,19 +527,20 @@ mslkb_status mslkb_route_experts_backward(const float* dweights, const void* log
     return MSLKB_ERR_NULL;
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
+  const int64_t size = dtype_bytes(dtype);
+  const bool wide = aligned_to(logits, 16) && aligned_to(dlogits, 16) && ld * size % 16 == 0 &&
+                    E * size % 16 == 0;
   const RouteBackwardParams p{dweights, logits, ids, dlogits, T, ld, static_cast<int32_t>(E),
                               static_cast<int32_t>(top_k), score == MSLKB_SIGMOID, renormalize,
-                              static_cast<float>(scale)};
-  const dim3 grid(static_cast<unsigned>((T + kWarps - 1) / kWarps)), block(kWarps * 32);
-  const size_t smem = sizeof(float) * kWarps * static_cast<size_t>(E);
+                              wide, static_cast<float>(scale)};
   TraceRange range("route_experts_backward", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_dependent(route_backward_kernel<__nv_bfloat16>, grid, block, smem, stream, p);
+    e = launch_backward<__nv_bfloat16>(p, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_dependent(route_backward_kernel<__half>, grid, block, smem, stream, p);
+    e = launch_backward<__half>(p, stream);
   else
-    e = launch_dependent(route_backward_kernel<float>, grid, block, smem, stream, p);
+    e = launch_backward<float>(p, stream);
   return launch_status(e);
 }
 
