@@ -10,17 +10,22 @@ making the access.  A test build (the stand-in for a memory checker); slower.
 Each translation unit in csrc/ compiles in parallel to _build/*.o, then nvcc links them
 into fp8_rowwise_scaled_gb300/libmslkb.so (CUDA runtime linked statically; the CUDA driver's
 tensor-map encoder is fetched at run time, so the library loads on a machine without a
-GPU).  Rebuilds only when a source or header is newer than the library.
+GPU).  Rebuilds only when a source or header is newer than the library.  Beside it the host
+compiler makes _binding.so, through which the torch forms of the operators around the
+product reach the library.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.machinery
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,6 +35,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmslkb.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libmslkb_checked.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["mslkb.cu", "mslkb_noalloc.cu", "variants_stacked_tma.cu",
            "variants_dynamic_tma.cu", "variants_cpasync.cu", "variants_ragged_n.cu",
            "variants_ragged_k.cu", "variants_blockscale.cu", "variants_blockscale_dynamic.cu",
@@ -77,6 +84,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     """Compile and link libmslkb.so (checked: libmslkb_checked.so); returns its path."""
     lib = LIB_CHECKED if checked else LIB
     if not force and not ptxas_verbose and up_to_date(lib):
+        if not checked:
+            build_binding()
         return lib
     os.makedirs(BUILD_CHECKED if checked else BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
@@ -92,7 +101,49 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if not checked:
+        build_binding(force)
     return lib
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so, the extension that checks torch tensors and passes them to
+    libmslkb.so, with the host compiler against this Python and torch; returns its path."""
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "mslkb.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    spec = importlib.util.find_spec("torch")   # found, not imported: seconds
+    torch_dir = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING_SOURCE, "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10", "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
+def load_binding():
+    """The loaded extension (raises if it has not been built)."""
+    if not os.path.exists(BINDING):
+        raise RuntimeError(f"{BINDING} is missing: build it with "
+                           "`python -m fp8_rowwise_scaled_gb300.build`")
+    name = __package__ + "._binding"
+    if name in sys.modules:
+        return sys.modules[name]
+    loader = importlib.machinery.ExtensionFileLoader(name, BINDING)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(module)
+    sys.modules[name] = module
+    return module
 
 
 if __name__ == "__main__":
