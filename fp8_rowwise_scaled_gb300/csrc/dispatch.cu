@@ -1,7 +1,5 @@
 // dispatch.cu -- the rows of the chosen experts: packed by expert into the stacked layout
 // (dispatch), and summed back per token with the routing weights (combine), with the gradient.
-#include <type_traits>
-
 #include "host.h"
 #include "rows.cuh"
 
@@ -134,17 +132,16 @@ struct CopyParams {
   const int32_t* dest;
   uint8_t* x_out;
   float* scale_out;
-  int64_t row_bytes;
+  int64_t row_bytes, T;
   int32_t scale_cols;
   int32_t top_k;
 };
 
-// A token's row is read once, 16 bytes (kWide) or one byte at a time, and written to each of
-// its rows.  A lane of each warp holds one of them, `own` (-1: none); their load and the
+// A token's row is read once, a Piece (16, 8, 4, 2 or 1 bytes) at a time, and written to each
+// of its rows.  A lane of each warp holds one of them, `own` (-1: none); their load and the
 // row's are under way together.
-template <bool kWide>
+template <class Piece>
 __device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, int32_t own) {
-  using Piece = std::conditional_t<kWide, uint4, uint8_t>;
   const Piece* from = reinterpret_cast<const Piece*>(p.x + t * p.row_bytes);
   const int n = static_cast<int>(p.row_bytes / sizeof(Piece));
   for (int c0 = 0; c0 < n; c0 += blockDim.x) {
@@ -168,14 +165,14 @@ __device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, int32_t
   }
 }
 
-// One CTA per token.
-template <bool kWide>
+// blockDim.y tokens per CTA, whole warps per token.
+template <class Piece>
 __global__ void __launch_bounds__(512) copy_kernel(const __grid_constant__ CopyParams p) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t t = blockIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int lane = threadIdx.x & 31;
-  copy_row<kWide>(p, t, lane < p.top_k ? p.dest[t * p.top_k + lane] : -1);
+  if (t < p.T) copy_row<Piece>(p, t, lane < p.top_k ? p.dest[t * p.top_k + lane] : -1);
 }
 
 // Few choices: one launch.  The CTA of a token finds each of its rows by itself:
@@ -189,7 +186,7 @@ struct DirectParams {
   int32_t T, E;
 };
 
-template <bool kWide>
+template <class Piece>
 __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ DirectParams p) {
   __shared__ uint32_t before[MSLKB_MAX_EXPERTS];  // a token's rows; or the experts' counts
   const int k = p.copy.top_k, N = p.T * k, lane = threadIdx.x & 31;
@@ -228,71 +225,86 @@ __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ Dir
   __syncthreads();
   own = own >= 0 ? static_cast<int>(before[lane]) : -1;
   if (threadIdx.x < k) p.dest[first + threadIdx.x] = own;
-  copy_row<kWide>(p.copy, blockIdx.x, own);
+  copy_row<Piece>(p.copy, blockIdx.x, own);
 }
 
 // ---------------------------------------------------------------------------------
-// combine and its gradient: one CTA per token, 8 columns per thread and step
+// combine and its gradient: 8 columns per thread and step
 // ---------------------------------------------------------------------------------
 struct CombineParams {
   const void* rows;
   const int32_t* dest;
   const float* weights;
   void* out;
-  int64_t H, R;
+  int64_t T, H, R;
   int32_t top_k;
 };
 
-// The token's valid rows, in slot order, with their weights; returns how many.
-__device__ __forceinline__ int gather_choices(const int32_t* dest, const float* weights,
-                                              int64_t t, int top_k, int64_t R, int32_t* row,
-                                              float* weight, int32_t* slot) {
-  __shared__ int count;
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    const int32_t d = lane < top_k ? dest[t * top_k + lane] : -1;
-    const bool here = d >= 0 && d < R;
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
-    if (here) {
-      const int at = __popc(mask & ((1u << lane) - 1u));
-      row[at] = d;
-      weight[at] = weights != nullptr ? weights[t * top_k + lane] : 1.f;
-      slot[at] = lane;
+// Every warp of a token holds its choices, one per lane: the row (-1: none) and the weight.
+struct Choice {
+  int32_t row;
+  float weight;
+};
+__device__ __forceinline__ Choice load_choice(const int32_t* dest, const float* weights,
+                                              int64_t t, int top_k, int64_t R) {
+  const int lane = threadIdx.x & 31;
+  Choice c{-1, 0.f};
+  if (lane < top_k) {
+    const int32_t d = dest[t * top_k + lane];
+    if (d >= 0 && d < R) {
+      c.row = d;
+      c.weight = weights != nullptr ? weights[t * top_k + lane] : 1.f;
     }
-    if (lane == 0) count = __popc(mask);
   }
-  __syncthreads();
-  return count;
+  return c;
 }
 
-template <class T, bool kWide>
+// The next kAhead choices that have a row, off the bits of `left`: their lanes (-1: none left).
+template <int kAhead>
+__device__ __forceinline__ void take_choices(uint32_t& left, int (&lane)[kAhead]) {
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    lane[j] = __ffs(left) - 1;
+    left &= left - 1;
+  }
+}
+
+// blockDim.y tokens per CTA, whole warps per token.
+template <class T, Access kAccess>
 __global__ void __launch_bounds__(512) combine_kernel(const __grid_constant__ CombineParams p) {
-  __shared__ int32_t row[MSLKB_MAX_TOPK], slot[MSLKB_MAX_TOPK];
-  __shared__ float weight[MSLKB_MAX_TOPK];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t t = blockIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (t >= p.T) return;
   const int n = static_cast<int>(p.H);
-  const int count = gather_choices(p.dest, p.weights, t, p.top_k, p.R, row, weight, slot);
+  const Choice own = load_choice(p.dest, p.weights, t, p.top_k, p.R);
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, own.row >= 0);
   const T* rows = static_cast<const T*>(p.rows);
-  for (int c = threadIdx.x * 8; c < n; c += blockDim.x * 8) {
+  constexpr int kRound = 4;
+  for (int c0 = 0; c0 < n; c0 += blockDim.x * 8) {
+    const int c = c0 + threadIdx.x * 8;
     float sum[8] = {};
-    for (int j0 = 0; j0 < count; j0 += 4) {
-      Raw8<T> r[4];
+    for (uint32_t left = there; left != 0;) {
+      int from[kRound];
+      take_choices(left, from);
+      Raw8<T> r[kRound];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j0 + j < count) r[j] = load8<T, kWide>(rows + row[j0 + j] * p.H, c, n);
+      for (int j = 0; j < kRound; ++j) {
+        const int32_t row = __shfl_sync(0xFFFFFFFFu, own.row, from[j] & 31);
+        if (from[j] >= 0) r[j] = load8<T, kAccess>(rows + row * p.H, c, n);
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j0 + j < count) {
+      for (int j = 0; j < kRound; ++j) {
+        const float w = __shfl_sync(0xFFFFFFFFu, own.weight, from[j] & 31);
+        if (from[j] >= 0) {
           float v[8];
           unpack8(r[j], v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = fmaf(weight[j0 + j], v[i], sum[i]);
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, v[i], sum[i]);
         }
       }
     }
-    store8<T, kWide>(static_cast<T*>(p.out) + t * p.H, c, n, sum);
+    store8<T, kAccess>(static_cast<T*>(p.out) + t * p.H, c, n, sum);
   }
 }
 
@@ -303,89 +315,149 @@ struct CombineBackwardParams {
   const float* weights;
   void* drows;
   float* dweights;
-  int64_t H, R;
+  int64_t T, H, R;
   int32_t top_k;
 };
 
-template <class T, bool kWide>
-__global__ void __launch_bounds__(512)
+// kRound rows at a time; dout is read again for each round.
+template <class T, Access kAccess, int kRound>
+__global__ void __launch_bounds__(128)
     combine_backward_kernel(const __grid_constant__ CombineBackwardParams p) {
-  __shared__ int32_t row[MSLKB_MAX_TOPK], slot[MSLKB_MAX_TOPK];
-  __shared__ float weight[MSLKB_MAX_TOPK];
-  __shared__ float partial[MSLKB_MAX_TOPK][16];  // per warp
+  __shared__ float partial[MSLKB_MAX_TOPK][4];  // per warp
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t t = blockIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int n = static_cast<int>(p.H);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int count = gather_choices(p.dest, p.weights, t, p.top_k, p.R, row, weight, slot);
+  const bool token = t < p.T;
+  const Choice own = token ? load_choice(p.dest, p.weights, t, p.top_k, p.R) : Choice{-1, 0.f};
   const T* dout = static_cast<const T*>(p.dout) + t * p.H;
-  constexpr int kRound = 4;
-  for (int j0 = 0; j0 < count; j0 += kRound) {
-    float dot[kRound] = {};
-    for (int c = threadIdx.x * 8; c < n; c += blockDim.x * 8) {
+  float mine = 0.f;  // lane j: this warp's part of the j-th choice's dot product
+  for (uint32_t left = __ballot_sync(0xFFFFFFFFu, own.row >= 0); left != 0;) {
+    int from[kRound];
+    int32_t row[kRound];
+    float w[kRound], dot[kRound] = {};
+    take_choices(left, from);
+#pragma unroll
+    for (int j = 0; j < kRound; ++j) {
+      row[j] = __shfl_sync(0xFFFFFFFFu, own.row, from[j] & 31);
+      w[j] = __shfl_sync(0xFFFFFFFFu, own.weight, from[j] & 31);
+    }
+    for (int c = threadIdx.x * 8; c - static_cast<int>(threadIdx.x) * 8 < n; c += blockDim.x * 8) {
       float d[8];
-      unpack8(load8<T, kWide>(dout, c, n), d);
+      unpack8(load8<T, kAccess>(dout, c, n), d);
       Raw8<T> r[kRound];
 #pragma unroll
       for (int j = 0; j < kRound; ++j)
-        if (j0 + j < count)
-          r[j] = load8<T, kWide>(static_cast<const T*>(p.rows) + row[j0 + j] * p.H, c, n);
+        if (from[j] >= 0)
+          r[j] = load8<T, kAccess>(static_cast<const T*>(p.rows) + row[j] * p.H, c, n);
 #pragma unroll
       for (int j = 0; j < kRound; ++j) {
-        if (j0 + j < count) {
+        if (from[j] >= 0) {
           float v[8];
           unpack8(r[j], v);
-          const float w = weight[j0 + j];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             dot[j] = fmaf(d[i], v[i], dot[j]);
-            v[i] = w * d[i];
+            v[i] = w[j] * d[i];
           }
-          store8<T, kWide>(static_cast<T*>(p.drows) + row[j0 + j] * p.H, c, n, v);
+          store8<T, kAccess>(static_cast<T*>(p.drows) + row[j] * p.H, c, n, v);
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < kRound; ++j) {
       const float s = warp_sum(dot[j]);
-      if (lane == 0 && j0 + j < count) partial[j0 + j][warp] = s;
+      if (lane == from[j]) mine = s;
     }
   }
-  __syncthreads();
-  if (threadIdx.x < p.top_k) p.dweights[t * p.top_k + threadIdx.x] = 0.f;
-  __syncthreads();
-  if (threadIdx.x < count) {
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += partial[threadIdx.x][w];
-    p.dweights[t * p.top_k + slot[threadIdx.x]] = s;
+  if (warps > 1) {  // one token per CTA
+    if (lane < p.top_k) partial[lane][warp] = mine;
+    __syncthreads();
+    if (warp > 0) return;
+    mine = 0.f;
+    if (lane < p.top_k)
+      for (int i = 0; i < warps; ++i) mine += partial[lane][i];
   }
+  if (token && lane < p.top_k) p.dweights[t * p.top_k + lane] = mine;
 }
 
 // ---------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------
-int row_threads(int64_t vectors) {
-  const int64_t t = (vectors + 31) / 32 * 32;
-  return static_cast<int>(t < 32 ? 32 : (t > 512 ? 512 : t));
+// Threads over a row of `steps`: x along the row, whole warps, in as few and even rounds as
+// `most` allow; with `tokens`, y rows per CTA, 256 threads together, where a warp is enough for
+// each.
+dim3 row_threads(int64_t steps, bool tokens, int most = 512) {
+  const int64_t rounds = (steps + most - 1) / most;
+  const int64_t each = rounds > 0 ? (steps + rounds - 1) / rounds : 0;
+  const int64_t x = each <= 32 ? 32 : (each + 31) / 32 * 32;
+  return dim3(static_cast<unsigned>(x), tokens && x == 32 ? 8 : 1);
+}
+
+dim3 token_grid(int64_t T, dim3 block) {
+  return dim3(static_cast<unsigned>((T + block.y - 1) / block.y));
 }
 
 // Choices up to which each token's CTA finds its rows by itself.
 constexpr int64_t kDirectChoices = 2048;
 
+// Threads per token (GB300, bf16, 512 / 256 / 128): 8192 tokens x 8 of 7168 149 / 153 / 153 us,
+// x 2 58.3 / 53.8 / 53.8, x 1 47.0 / 41.3 / 40.7: with few rows a thread takes more columns.
 template <class T>
-cudaError_t launch_combine(const CombineParams& p, int64_t T_, bool wide, void* stream) {
-  const dim3 grid(static_cast<unsigned>(T_)), block(row_threads((p.H + 7) / 8));
-  return wide ? launch_dependent(combine_kernel<T, true>, grid, block, 0, stream, p)
-              : launch_dependent(combine_kernel<T, false>, grid, block, 0, stream, p);
+cudaError_t launch_combine(const CombineParams& p, bool wide, void* stream) {
+  const dim3 block = row_threads((p.H + 7) / 8, true, p.top_k > 4 ? 512 : 256), grid = token_grid(p.T, block);
+  return wide ? launch_dependent(combine_kernel<T, Access::k16>, grid, block, 0, stream, p)
+              : launch_dependent(combine_kernel<T, Access::kStride>, grid, block, 0, stream, p);
+}
+
+// Rows at a time by top_k: all of up to eight, as each round reads dout again (GB300, 4096
+// tokens x 8 of 7168 bf16: 8 / 4 / 2 at a time 150 / 161 / 192 us; 8192 x 2: 102 / 101 / 94).
+// 128 threads per token: 256 take 163 us, 64 173 us on the first.
+template <class T, Access kAccess>
+cudaError_t launch_combine_backward(const CombineBackwardParams& p, void* stream) {
+  dim3 block = row_threads((p.H + 7) / 8, true, 128);
+  if (block.y > 1) block.y = 4;
+  const dim3 grid = token_grid(p.T, block);
+  if (p.top_k <= 2)
+    return launch_dependent(combine_backward_kernel<T, kAccess, 2>, grid, block, 0, stream, p);
+  if (p.top_k <= 4)
+    return launch_dependent(combine_backward_kernel<T, kAccess, 4>, grid, block, 0, stream, p);
+  return launch_dependent(combine_backward_kernel<T, kAccess, 8>, grid, block, 0, stream, p);
 }
 
 template <class T>
-cudaError_t launch_combine_backward(const CombineBackwardParams& p, int64_t T_, bool wide,
-                                    void* stream) {
-  const dim3 grid(static_cast<unsigned>(T_)), block(row_threads((p.H + 7) / 8));
-  return wide ? launch_dependent(combine_backward_kernel<T, true>, grid, block, 0, stream, p)
-              : launch_dependent(combine_backward_kernel<T, false>, grid, block, 0, stream, p);
+cudaError_t launch_combine_backward(const CombineBackwardParams& p, bool wide, void* stream) {
+  return wide ? launch_combine_backward<T, Access::k16>(p, stream)
+              : launch_combine_backward<T, Access::kStride>(p, stream);
+}
+
+// Dispatch with rows copied in Pieces.
+template <class Piece>
+cudaError_t launch_dispatch(const CopyParams& p, const int32_t* ids, int32_t* dest,
+                            int64_t* m_sizes, int64_t T, int64_t E, void* stream) {
+  const int64_t steps = p.row_bytes / static_cast<int64_t>(sizeof(Piece)), N = T * p.top_k;
+  const int experts = static_cast<int>(E);
+  if (N <= kDirectChoices) {
+    const DirectParams d{p, ids, dest, m_sizes, static_cast<int32_t>(T), experts};
+    dim3 block = row_threads(steps, false);
+    if (block.x < 256) block.x = 256;  // they share the counting too
+    return launch_dependent(direct_kernel<Piece>, dim3(static_cast<unsigned>(T) + 1), block, 0,
+                            stream, d);
+  }
+  const int64_t per_warp = (N + kCluster * kPlaceWarps - 1) / (kCluster * kPlaceWarps);
+  const auto place = experts <= 256 ? place_kernel<8> : place_kernel<10>;
+  cudaError_t e = experts <= 256 ? allow_smem<place_kernel<8>>() : allow_smem<place_kernel<10>>();
+  if (e == cudaSuccess)
+    e = launch_cluster(place, dim3(kCluster), dim3(kPlaceWarps * 32),
+                       sizeof(uint32_t) * experts * (kPlaceWarps + 2), kCluster, stream, ids, dest,
+                       m_sizes, static_cast<int>(N), experts,
+                       static_cast<int>((per_warp + 31) / 32 * 32));
+  if (e == cudaSuccess && (p.row_bytes > 0 || p.scale_cols > 0)) {
+    const dim3 block = row_threads(steps, true);
+    e = launch_dependent(copy_kernel<Piece>, token_grid(T, block), block, 0, stream, p);
+  }
+  return e;
 }
 
 mslkb_status check_combine(int64_t T, int64_t top_k, int64_t H, int64_t R, int32_t dtype) {
@@ -428,34 +500,24 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
     if (e == cudaSuccess && N > 0) e = cudaMemsetAsync(dest, 0xFF, sizeof(int32_t) * N, cs);
     return launch_status(e);
   }
-  const int experts = static_cast<int>(E);
-  const bool wide = row_bytes % 16 == 0 && aligned_to(x, 16) && aligned_to(x_out, 16);
   const CopyParams p{static_cast<const uint8_t*>(x), x_scale, dest, static_cast<uint8_t*>(x_out),
-                     scale_out, row_bytes, static_cast<int32_t>(scale_cols),
+                     scale_out, row_bytes, T, static_cast<int32_t>(scale_cols),
                      static_cast<int32_t>(top_k)};
+  const auto fits = [&](int64_t piece) {
+    return row_bytes % piece == 0 && aligned_to(x, piece) && aligned_to(x_out, piece);
+  };
   TraceRange range("moe_dispatch", T);
-  const dim3 copy_block(row_threads(wide ? row_bytes / 16 : row_bytes));
-  if (N <= kDirectChoices) {
-    const DirectParams d{p, ids, dest, m_sizes, static_cast<int32_t>(T), experts};
-    const dim3 grid(static_cast<unsigned>(T) + 1);
-    const dim3 block(copy_block.x < 256 ? 256 : copy_block.x);  // they share the counting too
-    return launch_status(wide
-                             ? launch_dependent(direct_kernel<true>, grid, block, 0, stream, d)
-                             : launch_dependent(direct_kernel<false>, grid, block, 0, stream, d));
-  }
-  const int64_t per_warp = (N + kCluster * kPlaceWarps - 1) / (kCluster * kPlaceWarps);
-  const auto place = experts <= 256 ? place_kernel<8> : place_kernel<10>;
-  cudaError_t e = experts <= 256 ? allow_smem<place_kernel<8>>() : allow_smem<place_kernel<10>>();
-  if (e == cudaSuccess)
-    e = launch_cluster(place, dim3(kCluster), dim3(kPlaceWarps * 32),
-                       sizeof(uint32_t) * experts * (kPlaceWarps + 2), kCluster, stream, ids, dest,
-                       m_sizes, static_cast<int>(N), experts,
-                       static_cast<int>((per_warp + 31) / 32 * 32));
-  if (e == cudaSuccess && (row_bytes > 0 || scale_cols > 0)) {
-    const dim3 grid(static_cast<unsigned>(T));
-    e = wide ? launch_dependent(copy_kernel<true>, grid, copy_block, 0, stream, p)
-             : launch_dependent(copy_kernel<false>, grid, copy_block, 0, stream, p);
-  }
+  cudaError_t e;
+  if (fits(16))
+    e = launch_dispatch<uint4>(p, ids, dest, m_sizes, T, E, stream);
+  else if (fits(8))
+    e = launch_dispatch<uint2>(p, ids, dest, m_sizes, T, E, stream);
+  else if (fits(4))
+    e = launch_dispatch<uint32_t>(p, ids, dest, m_sizes, T, E, stream);
+  else if (fits(2))
+    e = launch_dispatch<uint16_t>(p, ids, dest, m_sizes, T, E, stream);
+  else
+    e = launch_dispatch<uint8_t>(p, ids, dest, m_sizes, T, E, stream);
   return launch_status(e);
 }
 
@@ -471,15 +533,15 @@ mslkb_status mslkb_moe_combine(const void* rows, const int32_t* dest, const floa
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const bool wide = H % 8 == 0 && aligned_to(rows, 16) && aligned_to(out, 16);
-  const CombineParams p{rows, dest, weights, out, H, R, static_cast<int32_t>(top_k)};
+  const CombineParams p{rows, dest, weights, out, T, H, R, static_cast<int32_t>(top_k)};
   TraceRange range("moe_combine", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_combine<__nv_bfloat16>(p, T, wide, stream);
+    e = launch_combine<__nv_bfloat16>(p, wide, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_combine<__half>(p, T, wide, stream);
+    e = launch_combine<__half>(p, wide, stream);
   else
-    e = launch_combine<float>(p, T, wide, stream);
+    e = launch_combine<float>(p, wide, stream);
   return launch_status(e);
 }
 
@@ -498,16 +560,16 @@ mslkb_status mslkb_moe_combine_backward(const void* dout, const void* rows, cons
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const bool wide = H % 8 == 0 && aligned_to(dout, 16) && aligned_to(rows, 16) &&
                     aligned_to(drows, 16);
-  const CombineBackwardParams p{dout, rows, dest, weights, drows, dweights,
-                                H,    R,    static_cast<int32_t>(top_k)};
+  const CombineBackwardParams p{dout, rows, dest, weights, drows, dweights, T, H, R,
+                                static_cast<int32_t>(top_k)};
   TraceRange range("moe_combine_backward", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_combine_backward<__nv_bfloat16>(p, T, wide, stream);
+    e = launch_combine_backward<__nv_bfloat16>(p, wide, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_combine_backward<__half>(p, T, wide, stream);
+    e = launch_combine_backward<__half>(p, wide, stream);
   else
-    e = launch_combine_backward<float>(p, T, wide, stream);
+    e = launch_combine_backward<float>(p, wide, stream);
   return launch_status(e);
 }
 

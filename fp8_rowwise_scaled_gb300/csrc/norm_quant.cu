@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kAccess == Access::k32 ? 512 : kMaxThreads)
 #pragma unroll
     for (int j = 0; j < kCols; j += 8) {
       float u[8];
-      unpack8(load8<T, kAccess != Access::kElement>(from, c + j, n), u);
+      unpack8(load8<T, kAccess>(from, c + j, n), u);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[j + k] = u[k];
     }
@@ -307,53 +307,58 @@ struct NormBackwardParams {
   float inv_h;
 };
 
-__device__ __forceinline__ float cta_sum(float sum, float* slot) {
+// Sum over the threads of a row, to each of them: the CTA's, or with kRows row y's blockDim.x.
+template <bool kRows>
+__device__ __forceinline__ float row_sum(float sum, float* slot, int y) {
   sum = warp_sum(sum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (warps == 1) return sum;
-  if (lane == 0) slot[warp] = sum;
-  __syncthreads();
-  return warp_sum(lane < warps ? slot[lane] : 0.f);
+  float* mine = kRows ? slot + y * warps : slot;
+  if (lane == 0) mine[warp] = sum;
+  if constexpr (kRows)
+    ptx::named_bar_sync(1 + y, blockDim.x);
+  else
+    __syncthreads();
+  return warp_sum(lane < warps ? mine[lane] : 0.f);
 }
 
-// One row of the gradient; `inputs` gives a thread's eight columns i of dy and h, `weight` and
-// `residual` those of the others.  dy and h are taken twice (from the ring or L1), before and
-// after the row's mean, rather than kept: with the weight gradient in registers over all the
-// CTA's rows, that is what lets two CTAs share an SM.
-template <class T, int kVecs, bool kWide, class Inputs, class Weight, class Residual>
-__device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_t row, float rstd,
-                                             float (&dw)[kVecs][8], Inputs inputs, Weight weight,
-                                             Residual residual, float* slot) {
-  const int n = p.H;
+// One row of the gradient; `inputs` gives a thread's eight columns i of dy (g) and h, `weight` and
+// `residual` those of the others, `total` the row's sum.  dy and h are taken twice (from the
+// ring or L1), before and after the row's mean, rather than kept: with the weight gradient in
+// registers over all the CTA's rows, that is what leaves room for enough threads on an SM.
+template <class T, int kVecs, Access kAccess, class Inputs, class Weight, class Residual,
+          class Total>
+__device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_t row, int n,
+                                             float rstd, float (&dw)[kVecs][8], Inputs inputs,
+                                             Weight weight, Residual residual, Total total) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    float g[8], xhat[8], w[8];
-    inputs(i, g, xhat);
+    float g[8], h[8], w[8];
+    inputs(i, g, h);
     weight(i, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      xhat[j] *= rstd;
-      dw[i][j] = fmaf(g[j], xhat[j], dw[i][j]);
-      sum = fmaf(g[j] * w[j], xhat[j], sum);
+      sum = fmaf(g[j] * w[j], h[j], sum);
+      dw[i][j] = fmaf(g[j], h[j] * rstd, dw[i][j]);
     }
   }
-  const float mean = cta_sum(sum, slot) * p.inv_h;
+  // dx = rstd (g w - h rstd mean), mean = rstd sum / H (rstd^3 alone might underflow)
+  const float along = -(total(sum) * p.inv_h * rstd * rstd * rstd);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    float g[8], xhat[8], w[8], d[8];
-    inputs(i, g, xhat);
+    float g[8], h[8], w[8], d[8];
+    inputs(i, g, h);
     weight(i, w);
     residual(i, d);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      d[j] = fmaf(rstd, g[j] * w[j] - xhat[j] * rstd * mean, d[j]);
-    store8<T, kWide>(static_cast<T*>(p.dx) + row * n, column<8>(i), n, d);
+    for (int j = 0; j < 8; ++j) d[j] = fmaf(along, h[j], fmaf(rstd, g[j] * w[j], d[j]));
+    store8<T, kAccess>(static_cast<T*>(p.dx) + row * p.H, column<8>(i), n, d);
   }
 }
 
 // Straight from global memory.
-template <class T, int kVecs, bool kWide>
+template <class T, int kVecs, Access kAccess>
 __global__ void __launch_bounds__(kMaxThreads)
     norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float slot[2][32];
@@ -363,46 +368,47 @@ __global__ void __launch_bounds__(kMaxThreads)
   float dw[kVecs][8] = {};
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-    backward_row<T, kVecs, kWide>(
-        p, row, p.rstd[row], dw,
+    backward_row<T, kVecs, kAccess>(
+        p, row, n, p.rstd[row], dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
           const int c = column<8>(i);
-          unpack8(load8<T, kWide>(static_cast<const T*>(p.dy) + row * n, c, n), g);
-          unpack8(load8<T, kWide>(static_cast<const T*>(p.h) + row * n, c, n), h);
+          unpack8(load8<T, kAccess>(static_cast<const T*>(p.dy) + row * n, c, n), g);
+          unpack8(load8<T, kAccess>(static_cast<const T*>(p.h) + row * n, c, n), h);
         },
         [&](int i, float (&w)[8]) {
-          load_weight<T, 8, kWide ? Access::k16 : Access::kElement>(p.weight, p.weight_fp32,
-                                                                    column<8>(i), n, w);
+          load_weight<T, 8, kAccess>(p.weight, p.weight_fp32, column<8>(i), n, w);
         },
         [&](int i, float (&d)[8]) {
           const T* from = static_cast<const T*>(p.dresidual) + row * n;
-          unpack8(load8<T, kWide>(from, column<8>(i),
-                                  p.dresidual != nullptr ? n : 0),
-                  d);
+          unpack8(load8<T, kAccess>(from, column<8>(i), p.dresidual != nullptr ? n : 0), d);
         },
-        slot[turn]);
+        [&](float sum) { return row_sum<false>(sum, slot[turn], 0); });
   }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    store8<float, kWide>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
-                         column<8>(i), n, dw[i]);
+    store8<float, kAccess>(p.parts + static_cast<int64_t>(blockIdx.x) * n, column<8>(i), n, dw[i]);
 }
 
-template <class T, int kVecs, int kStages>
-__global__ void __launch_bounds__(512, 2)
+// From the ring.  kRows: blockDim.y narrow rows at a time, each with a barrier of its own (one
+// warp: none), whose weight gradients are added up at the end.
+template <class T, int kVecs, int kStages, bool kRows>
+__global__ void __launch_bounds__(kRows ? 512 : kMaxThreads, kRows ? 2 : 1)
     norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float slot[2][32];
-  const int n = p.H;
+  const int y = kRows ? threadIdx.y : 0, rows = kRows ? blockDim.y : 1;
   const bool add = p.dresidual != nullptr;
-  const int stage_bytes = (add ? 3 : 2) * kVecs * static_cast<int>(sizeof(T) / 2) *
-                          static_cast<int>(blockDim.x) * 16;
-  const uint32_t base = ptx::smem_addr(ring);
+  const int row_bytes = (add ? 3 : 2) * kVecs * static_cast<int>(blockDim.x * 8 * sizeof(T));
+  const int stage_bytes = rows * row_bytes;
+  const uint32_t base = ptx::smem_addr(ring) + y * row_bytes;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * rows + y;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.T) {
       const uint32_t at = base + stage * stage_bytes;
+      const int n = p.H;
       ring_fetch<T, 8, kVecs>(at, 0, static_cast<const T*>(p.dy) + row * n, n);
       ring_fetch<T, 8, kVecs>(at, 1, static_cast<const T*>(p.h) + row * n, n);
       if (add) ring_fetch<T, 8, kVecs>(at, 2, static_cast<const T*>(p.dresidual) + row * n, n);
@@ -410,22 +416,20 @@ __global__ void __launch_bounds__(512, 2)
     ptx::cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
-    fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
   float w[kVecs][8], dw[kVecs][8] = {};
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
-    load_weight<T, 8, Access::k16>(p.weight, p.weight_fp32, column<8>(i), n, w[i]);
+    load_weight<T, 8, Access::k16>(p.weight, p.weight_fp32, column<8>(i), p.H, w[i]);
   int stage = 0, turn = 0;
-  float rstd = p.rstd[blockIdx.x];  // the grid is no larger than T
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    fetch(row + static_cast<int64_t>(kStages - 1) * gridDim.x,
-          stage == 0 ? kStages - 1 : stage - 1);
-    const float next_rstd = row + gridDim.x < p.T ? p.rstd[row + gridDim.x] : 0.f;
+  float rstd = first < p.T ? p.rstd[first] : 0.f;
+  for (int64_t row = first; row < p.T; row += step) {
+    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    const float next_rstd = row + step < p.T ? p.rstd[row + step] : 0.f;
     ring_wait<kStages, 8 * sizeof(T)>();
-    const uint8_t* at = ring + stage * stage_bytes;
-    backward_row<T, kVecs, true>(
-        p, row, rstd, dw,
+    const uint8_t* at = ring + y * row_bytes + stage * stage_bytes;
+    backward_row<T, kVecs, Access::k16>(
+        p, row, p.H, rstd, dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
           ring_read<T, 8, kVecs>(at, 0, i, g);
           ring_read<T, 8, kVecs>(at, 1, i, h);
@@ -442,36 +446,53 @@ __global__ void __launch_bounds__(512, 2)
             for (int j = 0; j < 8; ++j) d[j] = 0.f;
           }
         },
-        slot[turn]);
+        [&](float sum) { return row_sum<kRows>(sum, slot[turn], y); });
     rstd = next_rstd;
     turn ^= 1;
     stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+  if constexpr (kRows) {  // through the ring, which nobody reads any more: [rows][kVecs * 8][x]
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    store8<float, true>(p.parts + static_cast<int64_t>(blockIdx.x) * n,
-                        column<8>(i), n, dw[i]);
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        sums[((y * kVecs + i) * 8 + j) * blockDim.x + threadIdx.x] = dw[i][j];
+    __syncthreads();
+    if (y >= kVecs) return;  // row y's threads add up step y of all rows
+    float total[8] = {};
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        total[j] += sums[((r * kVecs + y) * 8 + j) * blockDim.x + threadIdx.x];
+    store8<float, Access::k16>(p.parts + static_cast<int64_t>(blockIdx.x) * p.H, column<8>(y), p.H,
+                               total);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      store8<float, Access::k16>(p.parts + static_cast<int64_t>(blockIdx.x) * p.H, column<8>(i),
+                                 p.H, dw[i]);
+  }
 }
 
-// Column sums of parts [rows, H], in a fixed order: 8 threads per column.
-__global__ void __launch_bounds__(256)
+// Column sums of parts [rows, H], in a fixed order: 32 threads per column.
+__global__ void __launch_bounds__(1024)
     sum_parts_kernel(const float* parts, float* out, int rows, int n) {
-  __shared__ float slot[8][33];
+  __shared__ float slot[32][33];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < n) {
-#pragma unroll 4
-    for (int r = part; r < rows; r += 8) s += parts[static_cast<int64_t>(r) * n + c];
+#pragma unroll 10
+    for (int r = part; r < rows; r += 32) s += parts[static_cast<int64_t>(r) * n + c];
   }
-  slot[part][threadIdx.x & 31] = s;
+  slot[part][lane] = s;
   __syncthreads();
-  if (part == 0 && c < n) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += slot[i][threadIdx.x];
-    out[c] = s;
-  }
+  s = warp_sum(slot[lane][part]);  // column `part` of the 32
+  if (lane == 0 && blockIdx.x * 32 + part < n) out[blockIdx.x * 32 + part] = s;
 }
 
 // ---------------------------------------------------------------------------------
@@ -481,13 +502,17 @@ int threads_for(int64_t n, int cols) {  // cols: columns per thread in all
   return static_cast<int>(((n + cols - 1) / cols + 31) / 32 * 32);
 }
 
+template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks>
+cudaError_t launch_norm_kernel(const NormParams& p, void* stream) {
+  return launch_dependent(norm_quant_kernel<T, kCols, kVecs, kAccess, kBlocks>,
+                          dim3(static_cast<unsigned>(p.T)), dim3(threads_for(p.H, kCols * kVecs)),
+                          0, stream, p);
+}
+
 template <class T, int kCols, int kVecs, Access kAccess>
 cudaError_t launch_norm(const NormParams& p, bool blocks, void* stream) {
-  const dim3 grid(static_cast<unsigned>(p.T)), block(threads_for(p.H, kCols * kVecs));
-  return blocks ? launch_dependent(norm_quant_kernel<T, kCols, kVecs, kAccess, true>, grid, block,
-                                   0, stream, p)
-                : launch_dependent(norm_quant_kernel<T, kCols, kVecs, kAccess, false>, grid, block,
-                                   0, stream, p);
+  return blocks ? launch_norm_kernel<T, kCols, kVecs, kAccess, true>(p, stream)
+                : launch_norm_kernel<T, kCols, kVecs, kAccess, false>(p, stream);
 }
 
 // CTAs of a ring kernel that an SM holds, by shared memory and registers per thread.
@@ -539,44 +564,65 @@ cudaError_t launch_norm(const NormParams& p, int sms, Access access, bool blocks
     }
     return launch_norm<T, 16, 4, Access::k32>(p, blocks, stream);
   }
-  return access == Access::k16 ? launch_norm<T, 8, 4, Access::k16>(p, blocks, stream)
-                               : launch_norm<T, 8, 4, Access::kElement>(p, blocks, stream);
+  if (access == Access::k16) return launch_norm<T, 8, 4, Access::k16>(p, blocks, stream);
+  // whole blocks that are not aligned, or rows of any length with one scale
+  if (blocks) return launch_norm_kernel<T, 8, 4, Access::kElement, true>(p, stream);
+  return n <= 8192 ? launch_norm_kernel<T, 8, 1, Access::kStride, false>(p, stream)
+                   : launch_norm_kernel<T, 8, 4, Access::kStride, false>(p, stream);
 }
 
 // The gradient's first kernel; *parts: the rows of partial weight gradients that it writes.
-template <class T, int kVecs, bool kWide>
+template <class T, int kVecs, Access kAccess>
 cudaError_t launch_backward(const NormBackwardParams& p, int64_t* parts, void* stream) {
-  return launch_dependent(norm_backward_kernel<T, kVecs, kWide>,
-                          dim3(static_cast<unsigned>(*parts)), dim3(threads_for(p.H, 8 * kVecs)), 0,
-                          stream, p);
+  return launch_dependent(norm_backward_kernel<T, kVecs, kAccess>,
+                          dim3(static_cast<unsigned>(*parts)),
+                          dim3(threads_for(p.H, 8 * kVecs)), 0, stream, p);
 }
 
-template <class T, int kVecs, int kStages>
+template <class T, int kVecs, int kStages, bool kRows>
 cudaError_t launch_backward_ring(const NormBackwardParams& p, int sms, int64_t* parts,
                                  void* stream) {
-  const int threads = threads_for(p.H, 8 * kVecs);
-  const int smem =
-      kStages * ring_stage_bytes<T, 8, kVecs>(p.dresidual != nullptr ? 3 : 2, threads);
-  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, threads, 64);
+  const int x = threads_for(p.H, 8 * kVecs);
+  const int row = ring_stage_bytes<T, 8, kVecs>(p.dresidual != nullptr ? 3 : 2, x);
+  const int y = kRows ? 512 / x : 1;
+  const int smem = kStages * y * row;
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, x * y, 64);
+  const int64_t ctas = (p.T + y - 1) / y;
+  if (*parts > ctas) *parts = ctas;
   if (*parts > most) *parts = most;
-  cudaError_t e = allow_smem<norm_backward_ring_kernel<T, kVecs, kStages>>();
+  cudaError_t e = allow_smem<norm_backward_ring_kernel<T, kVecs, kStages, kRows>>();
   if (e != cudaSuccess) return e;
-  return launch_dependent(norm_backward_ring_kernel<T, kVecs, kStages>,
-                          dim3(static_cast<unsigned>(*parts)), dim3(threads), smem, stream, p);
+  return launch_dependent(norm_backward_ring_kernel<T, kVecs, kStages, kRows>,
+                          dim3(static_cast<unsigned>(*parts)),
+                          dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), smem, stream,
+                          p);
 }
 
 template <class T>
 cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int64_t* parts,
                             void* stream) {
   const int64_t n = p.H;
-  if (!wide) return launch_backward<T, 4, false>(p, parts, stream);
+  if (!wide)
+    return n <= 8192 ? launch_backward<T, 1, Access::kStride>(p, parts, stream)
+                     : launch_backward<T, 4, Access::kStride>(p, parts, stream);
   const bool many = p.T > 2 * sms;
-  if (n <= 4096)
-    return many ? launch_backward_ring<T, 1, 2>(p, sms, parts, stream)
-                : launch_backward<T, 1, true>(p, parts, stream);
-  if (n <= 8192 && many) return launch_backward_ring<T, 2, 2>(p, sms, parts, stream);
-  if (n <= 16 * kMaxThreads) return launch_backward<T, 2, true>(p, parts, stream);
-  return launch_backward<T, 4, true>(p, parts, stream);
+  // GB300, 16384 rows, device time.  1024 columns bf16: several rows per CTA 33 us, one 42 us;
+  // fp32 47 and 55.  2048 bf16: 58 and 55.  16384 x 6103 rows bf16: the ring 122 us, from
+  // memory directly 201 us.
+  if (n <= 1024) {
+    constexpr int kSteps = sizeof(T) == 4 ? 1 : 2;  // of eight columns per thread
+    return many ? launch_backward_ring<T, kSteps, 2, true>(p, sms, parts, stream)
+                : launch_backward<T, kSteps, Access::k16>(p, parts, stream);
+  }
+  if (n <= (sizeof(T) == 4 ? 8192 : 4096))
+    return many ? launch_backward_ring<T, 1, 2, false>(p, sms, parts, stream)
+                : launch_backward<T, 1, Access::k16>(p, parts, stream);
+  if (n <= 16384) {
+    if constexpr (sizeof(T) == 2)  // (two stages of 32-bit rows would not fit)
+      if (many) return launch_backward_ring<T, 2, 2, false>(p, sms, parts, stream);
+    return launch_backward<T, 2, Access::k16>(p, parts, stream);
+  }
+  return launch_backward<T, 4, Access::k16>(p, parts, stream);
 }
 
 int64_t backward_parts(int64_t T) { return T < kMaxParts ? T : kMaxParts; }
@@ -676,7 +722,7 @@ mslkb_status mslkb_add_rms_norm_quant_backward(const void* dy, const void* h, co
       e = launch_backward<float>(p, sms, wide, &parts, stream);
   }
   if (e == cudaSuccess)
-    e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(256),
+    e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(1024),
                          0, stream, partial, dweight, static_cast<int>(T > 0 ? parts : 0),
                          static_cast<int>(H));
   return launch_status(e);

@@ -26,7 +26,8 @@ struct RouteParams {
   int32_t E, top_k;
   int32_t groups, top_groups, group_top;
   int32_t per_group;    // experts of a group
-  int32_t group_shift;  // log2 of the lanes of a group; -1: a group is not a power of two lanes
+  int32_t whole;        // a group is a power of two lanes, with all their experts
+  int32_t group_shift;  // log2 of the lanes of a group; if not whole, of those that look through it
   int32_t renormalize;
   int32_t wide;  // rows (and the bias) in whole, aligned 16-byte pieces
   float scale;
@@ -103,6 +104,19 @@ __device__ __forceinline__ void load_lane(const T* row, int first, int n, bool w
   for (int i = 0; i < kPer; ++i) x[i] = first + i < n ? to_float(row[first + i]) : fill;
 }
 
+// Where expert e's key lies in shared memory: lanes kPer experts apart fall into other banks.
+__host__ __device__ __forceinline__ constexpr int padded(int e) { return e + (e >> 5); }
+
+// The two largest keys of each run of 2^shift lanes, from those of its lanes.
+__device__ __forceinline__ void merge_best(uint32_t& best, uint32_t& second, int shift) {
+  for (int d = 1; d < 1 << shift; d <<= 1) {
+    const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+    const uint32_t s = __shfl_xor_sync(0xFFFFFFFFu, second, d);
+    second = max(max(second, s), min(best, b));
+    best = max(best, b);
+  }
+}
+
 // How many of the groups are worth more than this lane's, `mine`, ties to the lower group.
 // Lane g << shift holds what group g is worth; a group's lanes share the comparisons.
 __device__ __forceinline__ int better_groups(uint32_t mine, int group, int groups, int shift) {
@@ -120,7 +134,7 @@ __device__ __forceinline__ int better_groups(uint32_t mine, int group, int group
 template <class T, int kPer, Score kScore>
 __global__ void __launch_bounds__(kWarps * 32)
     route_kernel(const __grid_constant__ RouteParams p) {
-  extern __shared__ uint32_t shared_keys[];  // [kWarps][E], groups that lanes do not hold whole
+  extern __shared__ uint32_t shared_keys[];  // [kWarps][padded(E)], groups that are not whole
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -167,19 +181,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 
   if (p.groups > 1) {
-    if (p.group_shift >= 0) {
+    if (p.whole) {
       uint32_t best = 0, second = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         second = max(second, min(best, key[i]));
         best = max(best, key[i]);
       }
-      for (int d = 1; d < 1 << p.group_shift; d <<= 1) {
-        const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, d);
-        const uint32_t s = __shfl_xor_sync(0xFFFFFFFFu, second, d);
-        second = max(max(second, s), min(best, b));
-        best = max(best, b);
-      }
+      merge_best(best, second, p.group_shift);
       const uint32_t mine = worth_key(best, second, p.group_top);
       if (better_groups(mine, lane >> p.group_shift, p.groups, p.group_shift) >= p.top_groups) {
 #pragma unroll
@@ -187,27 +196,29 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
     } else {
       const int per = p.per_group;
-      uint32_t* keys = shared_keys + warp * p.E;
+      uint32_t* keys = shared_keys + warp * padded(p.E);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (first + i < p.E) keys[first + i] = key[i];
+        if (first + i < p.E) keys[padded(first + i)] = key[i];
       __syncwarp();
+      const int mine_group = lane >> p.group_shift, lanes = 1 << p.group_shift;
       uint32_t best = 0, second = 0;
-      if (lane < p.groups) {
-        for (int i = 0; i < per; ++i) {
-          const uint32_t k = keys[lane * per + i];
+      if (mine_group < p.groups) {
+        for (int i = lane & (lanes - 1); i < per; i += lanes) {
+          const uint32_t k = keys[padded(mine_group * per + i)];
           second = max(second, min(best, k));
           best = max(best, k);
         }
       }
+      merge_best(best, second, p.group_shift);
       const uint32_t mine = worth_key(best, second, p.group_top);
-      const int better = better_groups(mine, lane, p.groups, 0);
+      const int better = better_groups(mine, mine_group, p.groups, p.group_shift);
       const uint32_t kept = __ballot_sync(0xFFFFFFFFu, better < p.top_groups);
       // the groups of the lane's experts, from the first one's on
       int group = first / per, left = per - (first - group * per);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (!((kept >> (group & 31)) & 1u)) key[i] = 0;
+        if (!((kept >> ((group << p.group_shift) & 31)) & 1u)) key[i] = 0;
         if (--left == 0) ++group, left = per;
       }
     }
@@ -425,11 +436,15 @@ __global__ void __launch_bounds__(kWarps * 32)
 template <class T, int kPer>
 cudaError_t launch_route(RouteParams p, Score score, void* stream) {
   const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
-  p.group_shift = -1;
-  for (int shift = 0; shift <= 5; ++shift)
-    if (p.per_group == kPer << shift) p.group_shift = shift;
-  const size_t smem =
-      p.groups > 1 && p.group_shift < 0 ? sizeof(uint32_t) * kWarps * p.E : 0;
+  p.whole = 0;
+  for (int shift = 0; shift <= 5 && !p.whole; ++shift) {
+    p.group_shift = shift;
+    p.whole = p.per_group == kPer << shift;
+  }
+  if (!p.whole)
+    for (p.group_shift = 5; p.groups > 32 >> p.group_shift; --p.group_shift) {
+    }
+  const size_t smem = p.groups > 1 && !p.whole ? sizeof(uint32_t) * kWarps * padded(p.E) : 0;
   if (score == Score::kLogits)
     return launch_dependent(route_kernel<T, kPer, Score::kLogits>, grid, block, smem, stream, p);
   if (score == Score::kSoftmax)

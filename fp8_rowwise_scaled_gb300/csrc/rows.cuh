@@ -102,27 +102,42 @@ __device__ __forceinline__ Raw8<T> pack8(const float (&v)[8]) {
   return r;
 }
 
-// Elements [c, c + 8) of a row of n elements; kWide: the row is 16-byte aligned and n a
-// multiple of 8.  Past the row's end: zeros, nothing read.
-template <class T, bool kWide>
+// How a thread reaches eight or sixteen columns of a row of n, named by c, a multiple of their
+// number; past the row's end nothing is touched and zeros are read.
+//   k32       columns [c, c + 16) in 32-byte pieces: aligned rows, n a multiple of 16
+//   k16       columns [c, c + 8) in 16-byte pieces: aligned rows, n a multiple of 8
+//   kElement  columns [c, c + 8) one by one
+//   kStride   one by one, a warp's 256 columns dealt to its lanes in turn, so that each access
+//             of the warp is one run of 32 elements (its threads name consecutive c)
+enum class Access { kElement, kStride, k16, k32 };
+
+template <Access kAccess>
+__device__ __forceinline__ int element(int c, int j) {
+  return kAccess == Access::kStride ? (c & ~255) + j * 32 + ((c >> 3) & 31) : c + j;
+}
+
+template <class T, Access kAccess>
 __device__ __forceinline__ Raw8<T> load8(const T* row, int c, int n) {
   Raw8<T> r;
-  if constexpr (kWide) {
+  if constexpr (kAccess == Access::k16 || kAccess == Access::k32) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
       r.w[i] = c < n ? load16(row + c + i * (16 / sizeof(T))) : make_uint4(0, 0, 0, 0);
   } else {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_float(row[c + i]) : 0.f;
+    for (int j = 0; j < 8; ++j) {
+      const int e = element<kAccess>(c, j);
+      v[j] = e < n ? to_float(row[e]) : 0.f;
+    }
     r = pack8<T>(v);  // exact: the values came from T
   }
   return r;
 }
 
-template <class T, bool kWide>
+template <class T, Access kAccess>
 __device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]) {
-  if constexpr (kWide) {
+  if constexpr (kAccess == Access::k16 || kAccess == Access::k32) {
     if (c < n) {
       const Raw8<T> r = pack8<T>(v);
 #pragma unroll
@@ -131,8 +146,10 @@ __device__ __forceinline__ void store8(T* row, int c, int n, const float (&v)[8]
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n) row[c + i] = from_float<T>(v[i]);
+    for (int j = 0; j < 8; ++j) {
+      const int e = element<kAccess>(c, j);
+      if (e < n) row[e] = from_float<T>(v[j]);
+    }
   }
 }
 
@@ -150,19 +167,6 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
   return unpack2(h, __half());
-}
-
-// Codes [c, c + 8) of a row of n codes (kWide: 8-byte aligned rows, n a multiple of 8).
-template <bool kWide>
-__device__ __forceinline__ void store_codes8(uint8_t* row, int c, int n, uint2 codes) {
-  if constexpr (kWide) {
-    if (c < n) *reinterpret_cast<uint2*>(row + c) = codes;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < n)
-        row[c + i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
-  }
 }
 
 // Largest magnitude, as the bit pattern of |v|: integers in the order of the floats with NaN
@@ -229,10 +233,8 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], float inv) {
 }
 
 // ---------------------------------------------------------------------------------
-// kCols columns per thread, by the widest access that the buffers allow
+// kCols columns per thread: 16 with Access::k32, else 8
 // ---------------------------------------------------------------------------------
-enum class Access { kElement, k16, k32 };  // element by element, 16 bytes, 32 bytes
-
 struct Words8 {
   uint32_t w[8];
 };
@@ -252,8 +254,6 @@ __device__ __forceinline__ void store32(void* p, const Words8& r) {
                : "memory");
 }
 
-// Columns [c, c + kCols) of a row of n; past its end zeros, nothing read.  k32: kCols 16, 32-byte
-// aligned rows, n a multiple of 16; k16: kCols 8, 16-byte aligned rows, n a multiple of 8.
 template <class T, int kCols, Access kAccess>
 __device__ __forceinline__ void load_cols(const T* row, int c, int n, float (&v)[kCols]) {
   if constexpr (kAccess == Access::k32) {
@@ -276,7 +276,7 @@ __device__ __forceinline__ void load_cols(const T* row, int c, int n, float (&v)
     }
   } else {
     static_assert(kCols == 8, "narrower accesses take 8 columns");
-    unpack8(load8<T, kAccess == Access::k16>(row, c, n), v);
+    unpack8(load8<T, kAccess>(row, c, n), v);
   }
 }
 
@@ -299,7 +299,7 @@ __device__ __forceinline__ void store_cols(T* row, int c, int n, const float (&v
       }
     }
   } else {
-    store8<T, kAccess == Access::k16>(row, c, n, v);
+    store8<T, kAccess>(row, c, n, v);
   }
 }
 
@@ -315,7 +315,16 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, const fl
                          v[4 * i + 3] * inv);
     if (c < n) store16(row + c, make_uint4(w[0], w[1], w[2], w[3]));
   } else {
-    store_codes8<kAccess == Access::k16>(row, c, n, quantize8(v, inv));
+    const uint2 codes = quantize8(v, inv);
+    if constexpr (kAccess == Access::k16) {
+      if (c < n) *reinterpret_cast<uint2*>(row + c) = codes;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = element<kAccess>(c, j);
+        if (e < n) row[e] = static_cast<uint8_t>((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
+      }
+    }
   }
 }
 

@@ -40,10 +40,12 @@ __device__ __forceinline__ void quantize_block(const float (&v)[kCols], uint8_t*
   store_codes<kCols, kAccess>(codes, c, n, v, s.inv);
 }
 
-// kBlocks: threadIdx.y rows per CTA, nothing shared between threads but the lanes of a block.
-// Otherwise one CTA per row, kVecs * kCols columns per thread.
+// blockDim.y rows per CTA.  kBlocks: nothing is shared between threads but the lanes of a
+// block.  Otherwise a row is a power of two lanes of one warp, or whole warps, with
+// kVecs * kCols columns per thread.
 template <class T, int kCols, int kVecs, Access kAccess, bool kBlocks>
-__global__ void __launch_bounds__(kBlocks ? 256 : (kVecs == 1 ? 512 : 1024), kBlocks ? 4 : 1)
+__global__ void __launch_bounds__(kVecs == 1 ? (kBlocks ? 256 : 512) : 1024,
+                                  kVecs == 1 ? (kBlocks ? 4 : 2) : 1)
     swiglu_kernel(const __grid_constant__ SwigluParams p) {
   __shared__ uint32_t slot[32];
   ptx::griddep_wait();
@@ -62,11 +64,13 @@ __global__ void __launch_bounds__(kBlocks ? 256 : (kVecs == 1 ? 512 : 1024), kBl
     load_cols<T, kCols, kAccess>(up, c, n, u);
 #pragma unroll
     for (int j = 0; j < kCols; ++j) a[i][j] = g[j] * sigmoid_of(g[j]) * u[j];
-    if (p.saved != nullptr) {
-      uint8_t* codes = p.saved + row * 2 * n;
-      float* scale = p.saved_scale + row * (2 * n / kScaleBlock);
-      quantize_block<kCols, kAccess>(g, codes, scale, c, n);
-      quantize_block<kCols, kAccess>(u, codes + n, scale + n / kScaleBlock, c, n);
+    if constexpr (kAccess != Access::kStride) {
+      if (p.saved != nullptr) {
+        uint8_t* codes = p.saved + row * 2 * n;
+        float* scale = p.saved_scale + row * (2 * n / kScaleBlock);
+        quantize_block<kCols, kAccess>(g, codes, scale, c, n);
+        quantize_block<kCols, kAccess>(u, codes + n, scale + n / kScaleBlock, c, n);
+      }
     }
     if constexpr (kBlocks)
       quantize_block<kCols, kAccess>(a[i], p.q + row * n, p.scale + row * (n / kScaleBlock), c, n);
@@ -74,16 +78,19 @@ __global__ void __launch_bounds__(kBlocks ? 256 : (kVecs == 1 ? 512 : 1024), kBl
       largest = max(largest, abs_max(a[i]));
   }
   if constexpr (!kBlocks) {
-    largest = __reduce_max_sync(0xFFFFFFFFu, largest);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lanes = blockDim.x < 32 ? blockDim.x : 32, warps = blockDim.x >> 5;
+    for (int d = lanes >> 1; d > 0; d >>= 1)
+      largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, d));
     if (warps > 1) {
-      if (lane == 0) slot[warp] = largest;
+      const int lane = threadIdx.x & 31;
+      uint32_t* mine = slot + threadIdx.y * warps;
+      if (lane == 0) mine[threadIdx.x >> 5] = largest;
       __syncthreads();
-      largest = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? slot[lane] : 0u);
+      largest = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? mine[lane] : 0u);
     }
     const float amax = __uint_as_float(largest);
     const QuantScale s = quant_scale(amax, amax);
-    if (threadIdx.x == 0) p.scale[row] = s.scale;
+    if (threadIdx.x == 0 && row < p.R) p.scale[row] = s.scale;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
       store_codes<kCols, kAccess>(p.q + row * n, (i * blockDim.x + threadIdx.x) * kCols, n, a[i],
@@ -107,7 +114,7 @@ __global__ void __launch_bounds__(256)
   ptx::griddep_launch_dependents();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int n = p.W, c = (blockIdx.y * blockDim.x + threadIdx.x) * kCols;
-  if (row >= p.R || c >= n) return;
+  if (row >= p.R || (c >= n && kAccess != Access::kStride)) return;
   float d[kCols], g[kCols], u[kCols];
   if constexpr (kSaved8) {
     const uint8_t* codes = static_cast<const uint8_t*>(p.saved) + row * 2 * n;
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(256)
 // launches
 // ---------------------------------------------------------------------------------
 // Threads of a CTA over rows of `lanes` steps: x along a row, y rows, at most 256 in all.  With
-// block_lanes > 1 (a multiple of 8): whole blocks of 128 columns along x, whole warps.
+// block_lanes > 1 (a multiple of 8): whole groups of that many along x, whole warps.
 dim3 tile_threads(int64_t lanes, int64_t block_lanes) {
   int64_t x = (lanes + block_lanes - 1) / block_lanes * block_lanes;
   if (x > 128) return dim3(256);
@@ -149,51 +156,69 @@ dim3 tile_threads(int64_t lanes, int64_t block_lanes) {
 }
 
 template <class T, int kCols, Access kAccess>
-cudaError_t launch_swiglu(const SwigluParams& p, bool blocks, void* stream) {
+cudaError_t launch_blocks(const SwigluParams& p, void* stream) {
   const int64_t lanes = (p.W + kCols - 1) / kCols;
-  if (blocks) {
-    const dim3 block = tile_threads(lanes, kScaleBlock / kCols);
-    const dim3 grid(static_cast<unsigned>((p.R + block.y - 1) / block.y),
-                    static_cast<unsigned>((lanes + block.x - 1) / block.x));
-    return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, true>, grid, block, 0, stream, p);
+  const dim3 block = tile_threads(lanes, kScaleBlock / kCols);
+  const dim3 grid(static_cast<unsigned>((p.R + block.y - 1) / block.y),
+                  static_cast<unsigned>((lanes + block.x - 1) / block.x));
+  return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, true>, grid, block, 0, stream, p);
+}
+
+template <class T, int kCols, Access kAccess>
+cudaError_t launch_rows(const SwigluParams& p, void* stream) {
+  const int64_t lanes = (p.W + kCols - 1) / kCols;
+  if (lanes <= 512) {
+    // a narrow row: a power of two lanes (whole blocks of the checkpoint; all 32 where the
+    // warp shares its columns out), several rows per CTA
+    int64_t x = kAccess == Access::kStride ? 32 : kScaleBlock / kCols;
+    while (x < 32 && x < lanes) x *= 2;
+    if (lanes > 32) x = (lanes + 31) / 32 * 32;
+    const int64_t y = x >= 128 ? 1 : 128 / x;
+    return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, false>,
+                            dim3(static_cast<unsigned>((p.R + y - 1) / y)),
+                            dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), 0, stream,
+                            p);
   }
-  const dim3 grid(static_cast<unsigned>(p.R));
-  const auto threads = [&](int vecs) {
-    return dim3(static_cast<unsigned>(((lanes + vecs - 1) / vecs + 31) / 32 * 32));
-  };
-  if (lanes <= 512)
-    return launch_dependent(swiglu_kernel<T, kCols, 1, kAccess, false>, grid, threads(1), 0,
-                            stream, p);
   constexpr int kMost = MSLKB_MAX_HIDDEN / kCols / 1024;
-  return launch_dependent(swiglu_kernel<T, kCols, kMost, kAccess, false>, grid, threads(kMost), 0,
+  const int64_t x = ((lanes + kMost - 1) / kMost + 31) / 32 * 32;
+  return launch_dependent(swiglu_kernel<T, kCols, kMost, kAccess, false>,
+                          dim3(static_cast<unsigned>(p.R)), dim3(static_cast<unsigned>(x)), 0,
                           stream, p);
 }
 
 template <class T>
 cudaError_t launch_swiglu(const SwigluParams& p, Access access, bool blocks, void* stream) {
-  if (access == Access::k32) return launch_swiglu<T, 16, Access::k32>(p, blocks, stream);
-  if (access == Access::k16) return launch_swiglu<T, 8, Access::k16>(p, blocks, stream);
-  return launch_swiglu<T, 8, Access::kElement>(p, blocks, stream);
+  if (access == Access::k32)
+    return blocks ? launch_blocks<T, 16, Access::k32>(p, stream)
+                  : launch_rows<T, 16, Access::k32>(p, stream);
+  if (access == Access::k16)
+    return blocks ? launch_blocks<T, 8, Access::k16>(p, stream)
+                  : launch_rows<T, 8, Access::k16>(p, stream);
+  if (blocks) return launch_blocks<T, 8, Access::kElement>(p, stream);
+  return p.saved != nullptr ? launch_rows<T, 8, Access::kElement>(p, stream)
+                            : launch_rows<T, 8, Access::kStride>(p, stream);
 }
 
 template <class T, int kCols, Access kAccess>
 cudaError_t launch_backward(const SwigluBackwardParams& p, void* stream) {
   const int64_t lanes = (p.W + kCols - 1) / kCols;
-  const dim3 block = tile_threads(lanes, 1);
+  const dim3 block = tile_threads(lanes, kAccess == Access::kStride ? 32 : 1);
   const dim3 grid(static_cast<unsigned>((p.R + block.y - 1) / block.y),
                   static_cast<unsigned>((lanes + block.x - 1) / block.x));
-  return p.saved_scale != nullptr
-             ? launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, true>, grid, block, 0,
-                                stream, p)
-             : launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, false>, grid, block, 0,
-                                stream, p);
+  if constexpr (kAccess != Access::kStride)
+    if (p.saved_scale != nullptr)
+      return launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, true>, grid, block, 0,
+                              stream, p);
+  return launch_dependent(swiglu_backward_kernel<T, kCols, kAccess, false>, grid, block, 0, stream,
+                          p);
 }
 
 template <class T>
 cudaError_t launch_backward(const SwigluBackwardParams& p, Access access, void* stream) {
   if (access == Access::k32) return launch_backward<T, 16, Access::k32>(p, stream);
   if (access == Access::k16) return launch_backward<T, 8, Access::k16>(p, stream);
-  return launch_backward<T, 8, Access::kElement>(p, stream);
+  return p.saved_scale != nullptr ? launch_backward<T, 8, Access::kElement>(p, stream)
+                                  : launch_backward<T, 8, Access::kStride>(p, stream);
 }
 
 mslkb_status check_swiglu(int64_t R, int64_t W, int32_t dtype) {

@@ -74,7 +74,8 @@ NORM_CASES = [  # tokens, hidden, groupwise
     (2, 16392, False), (2, 32768, True), (1, 32768, False), (2, 32767, False), (300, 256, True),
     # many rows: the persistent kernel, CTAs with several rows and with one
     (609, 7168, False), (1500, 8192, True), (2000, 128, True), (1300, 1000, False),
-    (700, 4096, False), (1250, 4104, False), (620, 16384, True), (640, 12304, False)]
+    (700, 4096, False), (1250, 4104, False), (620, 16384, True), (640, 12304, False),
+    (650, 1025, False), (300, 8, False), (700, 33, False)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
@@ -171,7 +172,10 @@ def test_norm_extremes():
                                           (700, 512, True), (50, 1000, False), (5, 16384, True),
                                           (4, 32768, True), (3, 32767, False),
                                           (1216, 7168, True), (900, 8192, False),
-                                          (1000, 136, True), (305, 4096, True)])
+                                          (1000, 136, True), (305, 4096, True),
+                                          (1300, 1025, True), (2500, 128, True),
+                                          (1501, 2048, False), (700, 16384, True),
+                                          (310, 8, False), (999, 1000, True)])
 def test_norm_backward(T, H, with_res, dtype):
     g = gen(T + H)
     dy, h = randn(g, T, H, dtype=dtype), randn(g, T, H, dtype=dtype, scale=2.0)
@@ -458,7 +462,8 @@ def random_ids(g, T, k, E, elsewhere=0.0):
     (1, 1, 1, 16, 1, 0.0), (1, 8, 32, 7168, 1, 0.5), (3, 2, 8, 128, 1, 0.0), (129, 8, 256, 256, 2, 0.0),
     (511, 2, 16, 48, 1, 0.3), (512, 2, 16, 48, 0, 0.0), (513, 2, 16, 33, 1, 0.0),
     (2048, 1, 1024, 16, 1, 0.2), (2049, 1, 1024, 16, 1, 0.0), (300, 7, 9, 32, 1, 0.1),
-    (9000, 8, 1024, 16, 1, 0.2), (70000, 2, 4, 16, 0, 0.5), (4099, 1, 1, 16, 0, 0.0), (1500, 6, 60, 64, 3, 0.9), (5000, 8, 128, 16, 1, 0.1),
+    (9000, 8, 1024, 16, 1, 0.2), (70000, 2, 4, 16, 0, 0.5), (400, 8, 16, 24, 1, 0.2),
+    (500, 6, 16, 12, 0, 0.0), (450, 5, 8, 6, 1, 0.3), (40, 2, 8, 1000, 1, 0.0), (2500, 2, 8, 1000, 1, 0.0), (4099, 1, 1, 16, 0, 0.0), (1500, 6, 60, 64, 3, 0.9), (5000, 8, 128, 16, 1, 0.1),
     (100, 32, 40, 80, 1, 0.0), (64, 4, 3, 1, 1, 0.0), (40, 8, 16, 100, 1, 1.0)])
 def test_dispatch(T, k, E, H, cols, elsewhere):
     g = gen(T + E)
@@ -515,7 +520,9 @@ def test_dispatch_nothing():
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("T,k,E,H,elsewhere", [(1, 8, 16, 7168, 0.0), (5, 2, 4, 33, 0.3),
                                                (65, 8, 32, 1000, 0.5), (40, 32, 64, 256, 0.1),
-                                               (3, 1, 2, 8, 0.0), (30, 6, 8, 4097, 1.0)])
+                                               (3, 1, 2, 8, 0.0), (30, 6, 8, 4097, 1.0),
+                                               (130, 8, 16, 64, 0.2), (21, 4, 8, 24, 0.0),
+                                               (17, 3, 4, 1, 0.3), (11, 5, 9, 4104, 0.1)])
 def test_combine(T, k, E, H, elsewhere, dtype):
     g = gen(T + H)
     ids = random_ids(g, T, k, E, elsewhere)
@@ -547,7 +554,9 @@ def test_combine_ignores_rows_outside():
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("T,k,E,H,elsewhere", [(1, 8, 16, 7168, 0.0), (5, 2, 4, 33, 0.3),
                                                (65, 8, 32, 1000, 0.5), (40, 32, 64, 256, 0.1),
-                                               (3, 1, 2, 8, 0.0), (9, 6, 8, 4097, 1.0)])
+                                               (3, 1, 2, 8, 0.0), (9, 6, 8, 4097, 1.0),
+                                               (130, 8, 16, 64, 0.2), (21, 4, 8, 24, 0.0),
+                                               (17, 3, 4, 1, 0.3), (11, 5, 9, 4104, 0.1)])
 def test_combine_backward(T, k, E, H, elsewhere, dtype):
     g = gen(T + H + 1)
     ids = random_ids(g, T, k, E, elsewhere)
@@ -604,7 +613,9 @@ SWIGLU_REL = 16 * U
     (1, 2048, False, False), (1, 128, True, True), (33, 2048, True, True), (5, 384, False, True),
     (3, 1, False, False), (17, 1000, False, False), (6, 1003, False, False), (40, 640, True, False),
     (3, 4224, True, True), (9, 3968, True, True), (70, 1920, True, False), (600, 256, True, True),
-    (5, 16384, True, True), (5, 12288, False, False), (2, 8192, True, True), (2, 8320, True, True), (2, 32768, False, True),
+    (5, 16384, True, True), (5, 12288, False, False), (300, 125, False, False),
+    (1001, 128, False, True), (41, 512, False, True), (37, 256, False, True), (3, 8208, False, False),
+    (33, 48, False, False), (70, 1536, False, True), (9, 4104, False, False), (2, 8192, True, True), (2, 8320, True, True), (2, 32768, False, True),
     (1, 32767, False, False)])
 def test_swiglu(R, W, groupwise, checkpoint, dtype):
     g = gen(R + W)
