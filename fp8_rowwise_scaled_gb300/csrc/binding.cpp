@@ -1,7 +1,8 @@
 // binding.cpp -- the Python extension _binding: checks the torch tensors of a call of the
 // operators around the grouped product and passes their addresses to libmslkb.so.  A call of
 // one token takes 3 us on the device; the checks take about 0.1 us here (with Python code and
-// ctypes they took 5).  Nothing is allocated or computed here.
+// ctypes they took 5).  Nothing is computed here, and nothing allocated but the scratch of the
+// norm's gradient.
 //
 // Every function takes positional arguments only (moe.py names them) and returns the
 // mslkb_status; wrong tensors raise TypeError or ValueError.  `out` is the tuple of results,
@@ -10,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -220,7 +222,20 @@ PyObject* add_rms_norm_quant(PyObject* const* a) {
   });
 }
 
-// dy, h, weight, rstd, dresidual, out, workspace, stream
+// Scratch of one call from torch's allocator, for the stream of the call; given back once the
+// call is enqueued, as a tensor of that stream would be.
+struct Scratch {
+  void* p;
+  Scratch(int64_t bytes, void* stream)
+      : p(bytes > 0 ? c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(
+                          static_cast<size_t>(bytes), static_cast<cudaStream_t>(stream))
+                    : nullptr) {}
+  ~Scratch() {
+    if (p != nullptr) c10::cuda::CUDACachingAllocator::raw_delete(p);
+  }
+};
+
+// dy, h, weight, rstd, dresidual, out, stream
 PyObject* add_rms_norm_quant_backward(PyObject* const* a) {
   Call c;
   const at::Tensor& lead = c.lead(a[0], "dy");
@@ -234,13 +249,13 @@ PyObject* add_rms_norm_quant_backward(PyObject* const* a) {
   const Out out(a[5], 2);
   void* dx = c.dense(out[0], "dx", c.type, {T, H});
   void* dw = c.dense(out[1], "dweight", at::kFloat, {H});
-  const int64_t bytes = tensor(a[6], "workspace").numel();
-  void* ws = c.dense(a[6], "workspace", at::kByte, {bytes});
-  void* s = c.stream(a[7]);
+  void* s = c.stream(a[6]);
+  const int64_t bytes = mslkb_add_rms_norm_quant_backward_workspace_bytes(T, H);
+  const Scratch workspace(bytes, s);
   return run([&] {
     return mslkb_add_rms_norm_quant_backward(dy, h, w, static_cast<const float*>(rstd), dres, dx,
-                                             static_cast<float*>(dw), ws, bytes, T, H, c.dtype,
-                                             fp32, s);
+                                             static_cast<float*>(dw), workspace.p, bytes, T, H,
+                                             c.dtype, fp32, s);
   });
 }
 
@@ -448,7 +463,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name, count>)), \
    METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {MSLKB_ENTRY(add_rms_norm_quant, 9),
-                           MSLKB_ENTRY(add_rms_norm_quant_backward, 8),
+                           MSLKB_ENTRY(add_rms_norm_quant_backward, 7),
                            MSLKB_ENTRY(route_experts, 11),
                            MSLKB_ENTRY(route_experts_backward, 8),
                            MSLKB_ENTRY(moe_dispatch, 6),

@@ -9,8 +9,9 @@ namespace {
 // ---------------------------------------------------------------------------------
 // dispatch: a stable counting sort of the choices by expert (place_kernel: the row of every
 // choice), then each token's row is read once and written to its rows (copy_kernel).  The
-// copies are bound by HBM's writes; the sort in front of them by latency, so it is one kernel
-// of one cluster: the eight CTAs exchange their counts through distributed shared memory.
+// copies are bound by HBM's writes (GB300, 8192 tokens x 8 rows of 7168 bytes: 81 us, 6.7 TB/s);
+// the sort in front of them, some 8 us, by latency, so it is one kernel of one cluster: the
+// eight CTAs exchange their counts through distributed shared memory.
 // ---------------------------------------------------------------------------------
 constexpr int kCluster = 8;
 constexpr int kPlaceWarps = 32;
@@ -229,7 +230,9 @@ __global__ void __launch_bounds__(512) direct_kernel(const __grid_constant__ Dir
 }
 
 // ---------------------------------------------------------------------------------
-// combine and its gradient: 8 columns per thread and step
+// combine and its gradient: 8 columns per thread and step.  Bound by HBM: GB300, bf16 rows of
+// 7168, 8111 tokens x 8 combined in 148 us (7.0 TB/s, nearly all of it reads), the gradient of
+// 4096 x 8 in 150 us (6.7 TB/s).
 // ---------------------------------------------------------------------------------
 struct CombineParams {
   const void* rows;
@@ -321,9 +324,9 @@ struct CombineBackwardParams {
 
 // kRound rows at a time; dout is read again for each round.
 template <class T, Access kAccess, int kRound>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(512)
     combine_backward_kernel(const __grid_constant__ CombineBackwardParams p) {
-  __shared__ float partial[MSLKB_MAX_TOPK][4];  // per warp
+  __shared__ float partial[MSLKB_MAX_TOPK][16];  // per warp
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -399,7 +402,9 @@ dim3 token_grid(int64_t T, dim3 block) {
   return dim3(static_cast<unsigned>((T + block.y - 1) / block.y));
 }
 
-// Choices up to which each token's CTA finds its rows by itself.
+// Choices up to which each token's CTA finds its rows by itself.  GB300, rows of 7168 bytes,
+// alone against sort and copy, us: 8 choices a token, 512 choices 3.2 / 5.5, 2048 6.3 / 7.4,
+// 4096 16.0 / 9.8; one choice a token, 1024 4.8 / 7.0, 2048 9.9 / 8.3.
 constexpr int64_t kDirectChoices = 2048;
 
 // Threads per token (GB300, bf16, 512 / 256 / 128): 8192 tokens x 8 of 7168 149 / 153 / 153 us,
@@ -413,10 +418,11 @@ cudaError_t launch_combine(const CombineParams& p, bool wide, void* stream) {
 
 // Rows at a time by top_k: all of up to eight, as each round reads dout again (GB300, 4096
 // tokens x 8 of 7168 bf16: 8 / 4 / 2 at a time 150 / 161 / 192 us; 8192 x 2: 102 / 101 / 94).
-// 128 threads per token: 256 take 163 us, 64 173 us on the first.
+// 128 threads per token: 256 take 163 us, 64 173 us on the first.  Few tokens take as many as
+// there are columns for (91 x 6 of 7168, one in ten here: 128 threads 6.2 us).
 template <class T, Access kAccess>
-cudaError_t launch_combine_backward(const CombineBackwardParams& p, void* stream) {
-  dim3 block = row_threads((p.H + 7) / 8, true, 128);
+cudaError_t launch_combine_backward(const CombineBackwardParams& p, int sms, void* stream) {
+  dim3 block = row_threads((p.H + 7) / 8, true, p.T > 4 * sms ? 128 : 512);
   if (block.y > 1) block.y = 4;
   const dim3 grid = token_grid(p.T, block);
   if (p.top_k <= 2)
@@ -427,9 +433,10 @@ cudaError_t launch_combine_backward(const CombineBackwardParams& p, void* stream
 }
 
 template <class T>
-cudaError_t launch_combine_backward(const CombineBackwardParams& p, bool wide, void* stream) {
-  return wide ? launch_combine_backward<T, Access::k16>(p, stream)
-              : launch_combine_backward<T, Access::kStride>(p, stream);
+cudaError_t launch_combine_backward(const CombineBackwardParams& p, int sms, bool wide,
+                                    void* stream) {
+  return wide ? launch_combine_backward<T, Access::k16>(p, sms, stream)
+              : launch_combine_backward<T, Access::kStride>(p, sms, stream);
 }
 
 // Dispatch with rows copied in Pieces.
@@ -565,11 +572,11 @@ mslkb_status mslkb_moe_combine_backward(const void* dout, const void* rows, cons
   TraceRange range("moe_combine_backward", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
-    e = launch_combine_backward<__nv_bfloat16>(p, wide, stream);
+    e = launch_combine_backward<__nv_bfloat16>(p, sms, wide, stream);
   else if (dtype == MSLKB_FP16)
-    e = launch_combine_backward<__half>(p, wide, stream);
+    e = launch_combine_backward<__half>(p, sms, wide, stream);
   else
-    e = launch_combine_backward<float>(p, wide, stream);
+    e = launch_combine_backward<float>(p, sms, wide, stream);
   return launch_status(e);
 }
 

@@ -7,7 +7,9 @@
 // norm-then-quantise would need two.  Where y is not asked for, the codes do without rstd:
 // y / scale = h rstd w * 448 / (rstd max|h w|) = u * (448 / max|u|).
 //
-// Both directions read every input once and write every output once and are bound by HBM.
+// Both directions read every input once and write every output once and are bound by HBM
+// (GB300, 8192 rows of 7168 bf16: with residual, block scales, y and rstd 88 us, 6.0 TB/s of
+// the 6.8 that a copy reaches; the gradient 74 us, 6.4 TB/s with the weight's sums).
 // With a row per CTA, the CTA's loads wait while it reduces and stores; so for many rows the
 // kernels are persistent, and each warp copies its own columns of the next rows into a ring of
 // stages in shared memory (cp.async, 16 bytes per lane) while it works on this one.  A warp
@@ -553,7 +555,9 @@ template <class T>
 cudaError_t launch_norm(const NormParams& p, int sms, Access access, bool blocks, void* stream) {
   const int64_t n = p.H;
   if (access == Access::k32) {
-    const bool many = p.T > 4 * sms;
+    // from memory directly against the ring, H = 7168 bf16 with everything, us: 152 rows 2.89 /
+    // 2.99, 304 3.71 / 3.92, 608 6.45 / 6.16, 1216 12.1 / 10.7, 4864 60.5 / 53.6
+    const bool many = p.T > 2 * sms;
     if (n <= 8192)
       return many ? launch_norm_ring<T, 1>(p, sms, blocks, stream)
                   : launch_norm<T, 16, 1, Access::k32>(p, blocks, stream);
@@ -605,7 +609,9 @@ cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int
   if (!wide)
     return n <= 8192 ? launch_backward<T, 1, Access::kStride>(p, parts, stream)
                      : launch_backward<T, 4, Access::kStride>(p, parts, stream);
-  const bool many = p.T > 2 * sms;
+  // from memory directly against the ring, bf16, us: H = 1024 76 rows 4.4 / 5.2, 152 5.3 / 5.2,
+  // 1216 9.1 / 6.7; H = 7168 76 rows 7.3 / 5.6, 608 14.3 / 11.4, 4864 75.7 / 47.1
+  const bool many = p.T >= sms;
   // GB300, 16384 rows, device time.  1024 columns bf16: several rows per CTA 33 us, one 42 us;
   // fp32 47 and 55.  2048 bf16: 58 and 55.  16384 x 6103 rows bf16: the ring 122 us, from
   // memory directly 201 us.
@@ -682,7 +688,7 @@ mslkb_status mslkb_add_rms_norm_quant(const void* x, const void* residual, const
 }
 
 int64_t mslkb_add_rms_norm_quant_backward_workspace_bytes(int64_t T, int64_t H) {
-  if (T <= 0 || H <= 0 || H > MSLKB_MAX_HIDDEN) return 0;
+  if (T <= 1 || H <= 0 || H > MSLKB_MAX_HIDDEN) return 0;
   return mslkb::backward_parts(T) * H * static_cast<int64_t>(sizeof(float));
 }
 
@@ -706,9 +712,11 @@ mslkb_status mslkb_add_rms_norm_quant_backward(const void* dy, const void* h, co
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
   const bool wide = H % 8 == 0 && aligned_to(dy, 16) && aligned_to(h, 16) &&
-                    aligned_to(weight, 16) && aligned_to(dresidual, 16) && aligned_to(dx, 16);
+                    aligned_to(weight, 16) && aligned_to(dresidual, 16) && aligned_to(dx, 16) &&
+                    (T != 1 || aligned_to(dweight, 16));
   int64_t parts = backward_parts(T);
-  float* partial = static_cast<float*>(workspace);
+  // one part is the gradient itself
+  float* partial = parts == 1 ? dweight : static_cast<float*>(workspace);
   NormBackwardParams p{dy, h, weight, rstd, dresidual, dx, partial, T,
                        static_cast<int32_t>(H), weight_fp32, 1.f / static_cast<float>(H)};
   TraceRange range("add_rms_norm_quant_backward", T);
@@ -721,7 +729,7 @@ mslkb_status mslkb_add_rms_norm_quant_backward(const void* dy, const void* h, co
     else
       e = launch_backward<float>(p, sms, wide, &parts, stream);
   }
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && partial != dweight)
     e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(1024),
                          0, stream, partial, dweight, static_cast<int>(T > 0 ? parts : 0),
                          static_cast<int>(H));

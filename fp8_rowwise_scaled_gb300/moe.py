@@ -221,13 +221,10 @@ def add_rms_norm_quant_backward(dy, h, weight, rstd, dresidual=None, *, out=None
     of residual alike, dweight [H] fp32)."""
     if _b is None:
         _setup()
-    T, H = _shape(dy, "dy")
     if out is None:
+        T, H = _shape(dy, "dy")
         out = _new(stream, (T, H), dy.dtype), _new(stream, (H,), _torch.float32)
-    workspace = _new(stream, (mslkb_add_rms_norm_quant_backward_workspace_bytes(T, H),),
-                     _torch.uint8)
-    s = _b.add_rms_norm_quant_backward(dy, h, weight, rstd, dresidual, out, workspace,
-                                       _raw(stream))
+    s = _b.add_rms_norm_quant_backward(dy, h, weight, rstd, dresidual, out, _raw(stream))
     if s:
         raise _fx.MslkbError(s, "add_rms_norm_quant_backward")
     return out
