@@ -487,9 +487,16 @@ __global__ void __launch_bounds__(1024)
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < n) {
-#pragma unroll 10
-    for (int r = part; r < rows; r += 32) s += parts[static_cast<int64_t>(r) * n + c];
+  constexpr int kAhead = 10;  // loads under way together
+  for (int r0 = part; c < n && r0 < rows; r0 += 32 * kAhead) {
+    float v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + 32 * i;
+      v[i] = r < rows ? parts[static_cast<int64_t>(r) * n + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) s += v[i];
   }
   slot[part][lane] = s;
   __syncthreads();
@@ -655,6 +662,8 @@ mslkb_status mslkb_add_rms_norm_quant(const void* x, const void* residual, const
   if (!(eps >= 1e-12 && eps < 1.0)) return MSLKB_ERR_SHAPE;
   if (ldx < H || ldx > MSLKB_MAX_DIM || (residual != nullptr && (ldr < H || ldr > MSLKB_MAX_DIM)))
     return MSLKB_ERR_SHAPE;
+  if (residual != nullptr && residual_out == residual && ldr != H && T > 1)
+    return MSLKB_ERR_SHAPE;  // the rows written would lie across others still to be read
   if (T == 0 || H == 0) return MSLKB_OK;
   if (x == nullptr || weight == nullptr || q == nullptr || scale == nullptr)
     return MSLKB_ERR_NULL;
