@@ -6,8 +6,8 @@
 // top_k dependent maxima.  The loop over the maxima is kept short by sorting each lane's keys
 // once, with the expert's index in place of the key's lowest bits: keys are then unique, the
 // lane that holds the maximum drops its first key, and the maximum itself names the expert.
-// Where the bits that gave way to the index might have decided (checked with the exact
-// values of the chosen), the choice is made again by exact keys.
+// Where the bits that gave way to the index decide, the chosen are put in the order of their
+// exact values, or, where another expert comes that close, chosen again by exact keys.
 // GB300, 16384 tokens x 256 experts, top 8: softmax 8 us, sigmoid + bias 12 us, with 4 of 8
 // groups 13.8 us (some 800 instructions per token at 0.8 a cycle; the logits alone are 2.6 us
 // of HBM); taking the maxima from unsorted keys took 21.9 us.
@@ -265,25 +265,42 @@ __global__ void __launch_bounds__(kWarps * 32)
       id = static_cast<int>(kIndex - (mine & kIndex));
       logit = to_float(row[id]);  // an L1 hit
     }
-    // A logit of 16 bits has the index's bits to spare.  Otherwise the choice stands if the
-    // chosen are in the order of their exact keys, and the next one differs in the bits kept
-    // from the last or, as with equal keys, nothing that is above the last was left out.
+    // A logit of 16 bits has the index's bits to spare.  Otherwise the chosen are the right ones
+    // if the next differs from the last in the bits kept, or, as with equal keys, nothing that
+    // is above the least of them was left out; then only their order may be wrong.
     if constexpr (!(kScore == Score::kLogits && sizeof(T) == 2)) {
       const uint32_t next = largest();
       const float b = kScore != Score::kLogits && p.bias != nullptr && id >= 0 ? p.bias[id] : 0.f;
       const uint32_t exact = id >= 0 ? choice_key(logit, b) : 0;
-      const uint32_t above = __shfl_up_sync(0xFFFFFFFFu, exact, 1);
-      const int above_id = __shfl_up_sync(0xFFFFFFFFu, id, 1);
-      const bool wrong = id >= 0 && lane > 0 && (above < exact || (above == exact && above_id > id));
-      bool again = __any_sync(0xFFFFFFFFu, wrong);
+      bool again = false;
       if (__any_sync(0xFFFFFFFFu,
                      id >= 0 && lane == p.top_k - 1 && ((mine ^ next) & ~kIndex) == 0)) {
-        const uint32_t last = __shfl_sync(0xFFFFFFFFu, exact, p.top_k - 1);
-        int above_last = 0;
+        const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, id >= 0 ? exact : 0xFFFFFFFFu);
+        int above = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) above_last += key[i] > last;
-        above_last = __reduce_add_sync(0xFFFFFFFFu, above_last);
-        again |= above_last != __popc(__ballot_sync(0xFFFFFFFFu, id >= 0 && exact > last));
+        for (int i = 0; i < kPer; ++i) above += key[i] > least;
+        above = __reduce_add_sync(0xFFFFFFFFu, above);
+        again = above != __popc(__ballot_sync(0xFFFFFFFFu, id >= 0 && exact > least));
+      }
+      const uint32_t above_key = __shfl_up_sync(0xFFFFFFFFu, exact, 1);
+      const int above_id = __shfl_up_sync(0xFFFFFFFFu, id, 1);
+      const bool wrong =
+          id >= 0 && lane > 0 && (above_key < exact || (above_key == exact && above_id > id));
+      if (!again && __any_sync(0xFFFFFFFFu, wrong)) {
+        int rank = 0;  // among the chosen
+        for (int j = 0; j < p.top_k; ++j) {
+          const uint32_t other = __shfl_sync(0xFFFFFFFFu, exact, j);
+          const int other_id = __shfl_sync(0xFFFFFFFFu, id, j);
+          rank += other > exact || (other == exact && other_id < id);
+        }
+        if (id < 0) rank = lane;  // those without an expert are last already
+        int from = lane;
+        for (int j = 0; j < p.top_k; ++j) {
+          const int at = __ffs(__ballot_sync(0xFFFFFFFFu, lane < p.top_k && rank == j)) - 1;
+          if (lane == j) from = at;
+        }
+        id = __shfl_sync(0xFFFFFFFFu, id, from);
+        logit = __shfl_sync(0xFFFFFFFFu, logit, from);
       }
       if (again) {
         id = -1;
@@ -393,7 +410,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const float total = warp_sum(s) + 1e-20f;
       g = (g - warp_sum(g * s) / total) / total;
     }
-    mine = g * s * (1.f - s);
+    mine = g * s * (id >= 0 ? sigmoid_of(-logit) : 0.f);  // 1 - s without cancellation
   } else {
     float m = logit;
 #pragma unroll
