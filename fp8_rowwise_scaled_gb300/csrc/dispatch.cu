@@ -10,10 +10,10 @@ namespace {
 // dispatch: a stable counting sort of the choices by expert (place_kernel: the row of every
 // choice), then each token's row is read once and written to its rows (copy_kernel).  The
 // copies are bound by HBM's writes (GB300, 8192 tokens x 8 rows of 7168 bytes: 81 us, 6.7 TB/s);
-// the sort in front of them, some 8 us, by latency, so it is one kernel of one cluster: the
-// eight CTAs exchange their counts through distributed shared memory.
+// the sort in front of them (6.5 us for 65536 choices among 256 experts, 25 us for 524288) by the
+// ballots that number a warp's choices and by latency, so it is one kernel of one cluster, whose
+// 8 or 16 CTAs exchange their counts through distributed shared memory.
 // ---------------------------------------------------------------------------------
-constexpr int kCluster = 8;
 constexpr int kPlaceWarps = 32;
 
 constexpr int kAhead = 8;  // loads of a warp under way together
@@ -43,6 +43,28 @@ __device__ __forceinline__ uint32_t same_expert(int choice) {
   return same;
 }
 
+// Numbers a warp's choices: each one's position among the warp's of its expert, of which
+// mine[expert] came before (and counts on).  Of the kAhead steps those of `left` choices.
+template <int kBits>
+__device__ __forceinline__ void number_choices(const int (&choice)[kAhead], int64_t left,
+                                               uint32_t* mine, uint32_t (&position)[kAhead]) {
+  const uint32_t lower = (1u << (threadIdx.x & 31)) - 1u;
+  uint32_t same[kAhead];
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r)
+    if (r * 32 < left) same[r] = same_expert<kBits>(choice[r]);
+#pragma unroll
+  for (int r = 0; r < kAhead; ++r) {
+    if (r * 32 >= left) break;
+    const uint32_t earlier = __popc(same[r] & lower);
+    const uint32_t next = choice[r] >= 0 ? mine[choice[r]] : 0;
+    __syncwarp();
+    if (choice[r] >= 0 && earlier == 0) mine[choice[r]] = next + __popc(same[r]);
+    __syncwarp();
+    position[r] = next + earlier;
+  }
+}
+
 // The choices in contiguous chunks, one per warp of the cluster, each a multiple of 32.
 // Shared memory: first[kPlaceWarps][E]: a warp's choices per expert, then those before its next
 // choice in the CTA; cta_total[E]: this CTA's choices per expert, read by the others; base[E]:
@@ -56,7 +78,7 @@ __global__ void __launch_bounds__(kPlaceWarps * 32)
   uint32_t* base = cta_total + E;
   __shared__ uint32_t warp_total[kPlaceWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t rank = ptx::cluster_ctarank();
+  const uint32_t rank = ptx::cluster_ctarank(), ranks = gridDim.x;  // one cluster
   for (int i = threadIdx.x; i < kPlaceWarps * E; i += blockDim.x) first[i] = 0;
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
@@ -64,12 +86,19 @@ __global__ void __launch_bounds__(kPlaceWarps * 32)
   uint32_t* mine = first + warp * E;
   const int64_t begin = (static_cast<int64_t>(rank) * kPlaceWarps + warp) * chunk;
   const int64_t end = begin + chunk < N ? begin + chunk : N;
+  // a warp with no more than these keeps their numbers
+  int choice[kAhead];
+  uint32_t position[kAhead];
+  const bool once = chunk <= 32 * kAhead;
   for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
-    int choice[kAhead];
     load_choices(ids, i0, end, E, choice);
+    if (once) {
+      number_choices<kBits>(choice, end - i0, mine, position);
+    } else {
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r)
-      if (choice[r] >= 0) atomicAdd(&mine[choice[r]], 1u);  // whole numbers, in any order
+      for (int r = 0; r < kAhead; ++r)
+        if (choice[r] >= 0) atomicAdd(&mine[choice[r]], 1u);  // whole numbers, in any order
+    }
   }
   __syncthreads();
   // one expert per thread (E <= 1024): the warps' counts become offsets within the CTA
@@ -88,8 +117,8 @@ __global__ void __launch_bounds__(kPlaceWarps * 32)
   uint32_t before = 0, total = 0;
   if (e < E) {
     const uint32_t at = ptx::smem_addr(cta_total + e);
-#pragma unroll
-    for (uint32_t r = 0; r < kCluster; ++r) {
+#pragma unroll 8
+    for (uint32_t r = 0; r < ranks; ++r) {
       const uint32_t c = ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, r));
       if (r < rank) before += c;
       total += c;
@@ -109,20 +138,17 @@ __global__ void __launch_bounds__(kPlaceWarps * 32)
   if (e < E) base[e] = warps_before + scan - total + before;
   ptx::cluster_sync();  // rows are set; nobody reads another CTA's shared memory any more
   for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
-    int choice[kAhead];
-    load_choices(ids, i0, end, E, choice);
+    if (!once) {  // mine now counts from the warps before on
+      load_choices(ids, i0, end, E, choice);
+      number_choices<kBits>(choice, end - i0, mine, position);
+    }
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
-      if (i0 + r * 32 >= end) break;
       const int64_t i = i0 + r * 32 + lane;
-      const uint32_t same = same_expert<kBits>(choice[r]);
-      const uint32_t earlier = __popc(same & ((1u << lane) - 1u));
-      const uint32_t next = choice[r] >= 0 ? mine[choice[r]] : 0;
-      __syncwarp();
-      if (choice[r] >= 0 && earlier == 0) mine[choice[r]] = next + __popc(same);
-      __syncwarp();
-      if (i < end)
-        dest[i] = choice[r] >= 0 ? static_cast<int32_t>(base[choice[r]] + next + earlier) : -1;
+      const int e = choice[r];
+      uint32_t to = 0xFFFFFFFFu;
+      if (e >= 0) to = base[e] + position[r] + (once ? mine[e] : 0);
+      if (i < end) dest[i] = static_cast<int32_t>(to);
     }
   }
 }
@@ -136,9 +162,25 @@ struct CopyParams {
   int64_t row_bytes, T;
   int32_t scale_cols;
   int32_t top_k;
+  int64_t ahead;  // tokens of the CTAs that an SM full of them starts with
 };
 
-// A token's row is read once, a Piece (16, 8, 4, 2 or 1 bytes) at a time, and written to each
+template <class Piece>
+__device__ __forceinline__ Piece load_piece(const Piece* p) {
+  if constexpr (sizeof(Piece) == 32)
+    return load32(p);
+  else
+    return *p;
+}
+template <class Piece>
+__device__ __forceinline__ void store_piece(Piece* p, const Piece& v) {
+  if constexpr (sizeof(Piece) == 32)
+    store32(p, v);
+  else
+    *p = v;
+}
+
+// A token's row is read once, a Piece (32, 16, 8, 4, 2 or 1 bytes) at a time, and written to each
 // of its rows.  A lane of each warp holds one of them, `own` (-1: none); their load and the
 // row's are under way together.
 template <class Piece>
@@ -148,10 +190,10 @@ __device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, int32_t
   for (int c0 = 0; c0 < n; c0 += blockDim.x) {
     const int c = c0 + threadIdx.x;
     Piece v{};
-    if (c < n) v = from[c];
+    if (c < n) v = load_piece(from + c);
     for (int j = 0; j < p.top_k; ++j) {
       const int32_t d = __shfl_sync(0xFFFFFFFFu, own, j);
-      if (d >= 0 && c < n) reinterpret_cast<Piece*>(p.x_out + d * p.row_bytes)[c] = v;
+      if (d >= 0 && c < n) store_piece(reinterpret_cast<Piece*>(p.x_out + d * p.row_bytes) + c, v);
     }
   }
   for (int c0 = 0; c0 < p.scale_cols; c0 += blockDim.x) {
@@ -166,14 +208,31 @@ __device__ __forceinline__ void copy_row(const CopyParams& p, int64_t t, int32_t
   }
 }
 
+// Rows per waiting CTA and token.  GB300, 0 / 1 / 2 / 4, us: 8192 tokens x 8 rows of 7168 bytes
+// 89.7 / 88.8 / 88.8 / 89.6, x 2 33.5 / 32.2 / 31.3 / 31.4, 16384 x 1 of 4096 26.9 / 25.6 / 24.8.
+constexpr int kRowsAhead = 2;
+
 // blockDim.y tokens per CTA, whole warps per token.
 template <class Piece>
 __global__ void __launch_bounds__(512) copy_kernel(const __grid_constant__ CopyParams p) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  // While the sort runs, the CTAs that wait for it have the first rows brought to L2 (x itself
+  // is there already: the sort's CTAs let this kernel start after their own wait)
+  if (t < p.ahead) {
+#pragma unroll
+    for (int r = 0; r < kRowsAhead; ++r) {
+      const int64_t row = t + r * p.ahead;
+      if (row < p.T)
+        for (int64_t c = threadIdx.x * 128; c < p.row_bytes; c += blockDim.x * 128)
+          ptx::prefetch_l2(p.x + row * p.row_bytes + c);
+    }
+  }
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int lane = threadIdx.x & 31;
-  if (t < p.T) copy_row<Piece>(p, t, lane < p.top_k ? p.dest[t * p.top_k + lane] : -1);
+  if (t >= p.T) return;
+  const int32_t own = lane < p.top_k ? p.dest[t * p.top_k + lane] : -1;
+  if (__any_sync(0xFFFFFFFFu, own >= 0)) copy_row<Piece>(p, t, own);
 }
 
 // Few choices: one launch.  The CTA of a token finds each of its rows by itself:
@@ -439,9 +498,42 @@ cudaError_t launch_combine_backward(const CombineBackwardParams& p, int sms, boo
               : launch_combine_backward<T, Access::kStride>(p, sms, stream);
 }
 
+size_t place_smem(int experts) { return sizeof(uint32_t) * experts * (kPlaceWarps + 2); }
+
+// CTAs of the sort, one cluster: 16, or the portable 8 where the device has no 16 SMs together
+// to give.  Asked once per device.
+template <auto kKernel>
+cudaError_t place_ctas(int* ctas) {
+  static std::atomic<int8_t> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int8_t>& mine = known[dev & 63];
+  if ((*ctas = mine.load()) != 0) return cudaSuccess;
+  e = allow_smem<kKernel>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kPlaceWarps * 32);
+  cfg.dynamicSmemBytes = place_smem(MSLKB_MAX_EXPERTS);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if ((e = cudaOccupancyMaxActiveClusters(&clusters, kKernel, &cfg)) != cudaSuccess) return e;
+  *ctas = clusters > 0 ? 16 : 8;
+  mine.store(static_cast<int8_t>(*ctas));
+  return cudaSuccess;
+}
+
 // Dispatch with rows copied in Pieces.
 template <class Piece>
-cudaError_t launch_dispatch(const CopyParams& p, const int32_t* ids, int32_t* dest,
+cudaError_t launch_dispatch(CopyParams p, int sms, const int32_t* ids, int32_t* dest,
                             int64_t* m_sizes, int64_t T, int64_t E, void* stream) {
   const int64_t steps = p.row_bytes / static_cast<int64_t>(sizeof(Piece)), N = T * p.top_k;
   const int experts = static_cast<int>(E);
@@ -452,16 +544,23 @@ cudaError_t launch_dispatch(const CopyParams& p, const int32_t* ids, int32_t* de
     return launch_dependent(direct_kernel<Piece>, dim3(static_cast<unsigned>(T) + 1), block, 0,
                             stream, d);
   }
-  const int64_t per_warp = (N + kCluster * kPlaceWarps - 1) / (kCluster * kPlaceWarps);
   const auto place = experts <= 256 ? place_kernel<8> : place_kernel<10>;
-  cudaError_t e = experts <= 256 ? allow_smem<place_kernel<8>>() : allow_smem<place_kernel<10>>();
-  if (e == cudaSuccess)
-    e = launch_cluster(place, dim3(kCluster), dim3(kPlaceWarps * 32),
-                       sizeof(uint32_t) * experts * (kPlaceWarps + 2), kCluster, stream, ids, dest,
-                       m_sizes, static_cast<int>(N), experts,
-                       static_cast<int>((per_warp + 31) / 32 * 32));
+  int ctas = 0;
+  cudaError_t e = experts <= 256 ? place_ctas<place_kernel<8>>(&ctas)
+                                 : place_ctas<place_kernel<10>>(&ctas);
+  if (e != cudaSuccess) return e;
+  // us: 4320 choices by 8 CTAs 4.2, by 16 4.5; 16384 4.8 and 4.9; 65536 8.0 and 6.5
+  if (N <= 16384) ctas = 8;
+  const int64_t per_warp = (N + ctas * kPlaceWarps - 1) / (ctas * kPlaceWarps);
+  e = launch_cluster(place, dim3(static_cast<unsigned>(ctas)), dim3(kPlaceWarps * 32),
+                     place_smem(experts), ctas, stream, ids, dest, m_sizes, static_cast<int>(N),
+                     experts, static_cast<int>((per_warp + 31) / 32 * 32));
   if (e == cudaSuccess && (p.row_bytes > 0 || p.scale_cols > 0)) {
-    const dim3 block = row_threads(steps, true);
+    // 32 bytes a thread against 16 and twice the threads, us: 8192 tokens x 8 of 7168, all here,
+    // 91.1 / 90.3, one in four here 36.6 / 43.3; x 2 33.3 / 39.3; 16384 x 1 of 4096 26.9 / 31.9
+    dim3 block = row_threads(steps, false);
+    if (block.x <= 128) block.y = 256 / block.x;
+    p.ahead = static_cast<int64_t>(sms) * (2048 / (block.x * block.y)) * block.y;
     e = launch_dependent(copy_kernel<Piece>, token_grid(T, block), block, 0, stream, p);
   }
   return e;
@@ -486,8 +585,8 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
                                 int64_t scale_cols, void* stream) {
   using namespace mslkb;
   if (T < 0 || top_k < 0 || E < 0 || row_bytes < 0 || scale_cols < 0) return MSLKB_ERR_SHAPE;
-  if (E > MSLKB_MAX_EXPERTS || top_k > MSLKB_MAX_TOPK || row_bytes > MSLKB_MAX_DIM ||
-      scale_cols > MSLKB_MAX_DIM || (top_k > 0 && T > MSLKB_MAX_DIM / 2 / top_k) ||
+  if (E > MSLKB_MAX_EXPERTS || top_k > MSLKB_MAX_TOPK || row_bytes > (1 << 30) ||
+      scale_cols > (1 << 30) || (top_k > 0 && T > MSLKB_MAX_DIM / 2 / top_k) ||
       T > MSLKB_MAX_DIM)
     return MSLKB_ERR_SHAPE;
   if (E > 0 && m_sizes == nullptr) return MSLKB_ERR_NULL;
@@ -509,22 +608,24 @@ mslkb_status mslkb_moe_dispatch(const void* x, const float* x_scale, const int32
   }
   const CopyParams p{static_cast<const uint8_t*>(x), x_scale, dest, static_cast<uint8_t*>(x_out),
                      scale_out, row_bytes, T, static_cast<int32_t>(scale_cols),
-                     static_cast<int32_t>(top_k)};
+                     static_cast<int32_t>(top_k), 0};
   const auto fits = [&](int64_t piece) {
     return row_bytes % piece == 0 && aligned_to(x, piece) && aligned_to(x_out, piece);
   };
   TraceRange range("moe_dispatch", T);
   cudaError_t e;
-  if (fits(16))
-    e = launch_dispatch<uint4>(p, ids, dest, m_sizes, T, E, stream);
+  if (fits(32))
+    e = launch_dispatch<Words8>(p, sms, ids, dest, m_sizes, T, E, stream);
+  else if (fits(16))
+    e = launch_dispatch<uint4>(p, sms, ids, dest, m_sizes, T, E, stream);
   else if (fits(8))
-    e = launch_dispatch<uint2>(p, ids, dest, m_sizes, T, E, stream);
+    e = launch_dispatch<uint2>(p, sms, ids, dest, m_sizes, T, E, stream);
   else if (fits(4))
-    e = launch_dispatch<uint32_t>(p, ids, dest, m_sizes, T, E, stream);
+    e = launch_dispatch<uint32_t>(p, sms, ids, dest, m_sizes, T, E, stream);
   else if (fits(2))
-    e = launch_dispatch<uint16_t>(p, ids, dest, m_sizes, T, E, stream);
+    e = launch_dispatch<uint16_t>(p, sms, ids, dest, m_sizes, T, E, stream);
   else
-    e = launch_dispatch<uint8_t>(p, ids, dest, m_sizes, T, E, stream);
+    e = launch_dispatch<uint8_t>(p, sms, ids, dest, m_sizes, T, E, stream);
   return launch_status(e);
 }
 

@@ -17,8 +17,9 @@
  * - Pointers named as device pointers must point to memory the current CUDA device
  *   can access (device or managed memory).  They are owned by the caller, are only
  *   read/written by work enqueued on `stream`, and are not retained after the call
- *   returns.  Every buffer is dense and row-major with the sizes given; strided views
- *   are not supported (the kernel addresses the output as one flat row-major buffer:
+ *   returns.  Every buffer is dense and row-major with the sizes given, but for the inputs
+ *   that have a row stride (ld...) among their arguments; other strided views are not
+ *   supported (the product's kernel addresses the output as one flat row-major buffer:
  *   MSLK #471, commit rejecting a strided output).
  * - `stream` is a cudaStream_t passed as void*; NULL means the legacy default stream.
  *   Calls are asynchronous: they enqueue work and return without synchronising.
@@ -46,7 +47,8 @@
  * - Every kernel launch is enqueued inside an NVTX push/pop range of the domain "mslkb"
  *   whose message is the kernel variant's name (mslkb_variant_name) and whose int64
  *   payload is the rows of A, so a profiler can select this library's launches (ncu:
- *   --nvtx --nvtx-include "mslkb@<variant name>/").  With no tool attached the range
+ *   --nvtx --nvtx-include "mslkb@<variant name>/").  The operators around the product have
+ *   one range per call, named as the call without "mslkb_", with its rows.  With no tool attached the range
  *   calls return at once; a launch captured in a CUDA graph replays without them.
  */
 #ifndef MSLKB_H_
@@ -362,6 +364,7 @@ typedef enum mslkb_dtype { MSLKB_BF16 = 0, MSLKB_FP16 = 1, MSLKB_FP32 = 2 } mslk
  *   weight        device, [H], dtype, or fp32 if weight_fp32 is not 0
  *   q             device, e4m3 [T, H];  scale  device, fp32 [T] or [T, H / 128]
  *   residual_out  device, dtype [T, H]: h; NULL: not written.  May be residual itself
+ *                 (rows H elements apart)
  *   y             device, dtype [T, H], for readers of the unquantised norm; NULL: none
  *   rstd          device, fp32 [T], for the gradient; NULL: none
  *
@@ -427,7 +430,7 @@ MSLKB_API mslkb_status mslkb_route_experts_backward(
 /*
  * Packs the tokens' rows by expert into the stacked layout.  The choices (t, j) with
  * 0 <= ids[t, j] < E are ordered by expert, then by t * top_k + j; choice number r becomes
- * row r of xq_out.  Choices with another id (a masked slot, an expert of another device) are
+ * row r of x_out.  Choices with another id (a masked slot, an expert of another device) are
  * left out, and rows past the last choice are not written.
  *
  *   x           device, [T, row_bytes] bytes (e4m3 codes, or any other row); rows dense
@@ -437,7 +440,7 @@ MSLKB_API mslkb_status mslkb_route_experts_backward(
  *   m_sizes     device, int64 [E]: rows per expert, as the stacked products take them
  *   dest        device, int32 [T, top_k]: the choice's row, -1 if left out
  *
- * T * top_k is limited to MSLKB_MAX_DIM / 2.
+ * T * top_k is limited to MSLKB_MAX_DIM / 2, row_bytes and scale_cols to 2^30.
  */
 MSLKB_API mslkb_status mslkb_moe_dispatch(
     const void *x, const float *x_scale, const int32_t *ids, void *x_out, float *scale_out,

@@ -119,3 +119,10 @@ def test_nothing_to_do():
 def test_new_status_strings():
     for s in (fx.MSLKB_ERR_DTYPE, fx.MSLKB_ERR_WORKSPACE):
         assert fx.mslkb_status_string(s) not in ("unknown status", "ok")
+
+
+def test_rows_too_long_and_rows_written_over():
+    refused(dispatch, fx.MSLKB_ERR_SHAPE, dict(row_bytes=(1 << 30) + 1),
+            dict(scale_cols=(1 << 30) + 1))
+    # in place, the rows of the sum have to lie where the residual's were
+    refused(norm, fx.MSLKB_ERR_SHAPE, dict(ldr=257))

@@ -448,6 +448,21 @@ def test_route_backward_masked_rows(score, renorm):
     close(got[:, 3], 0.75 * s * (1 - s), 1e-6, "an expert named twice")
 
 
+@pytest.mark.parametrize("E,top_k", [(31, 8), (64, 1), (200, 8), (256, 20), (500, 8), (1024, 32)])
+@pytest.mark.parametrize("spread", [3, 40, 5000, 1 << 20])
+def test_route_order_of_near_ties(E, top_k, spread):
+    """Logits a few steps of their last bit apart: a softmax without bias takes them in their
+    order, equal ones by index, whatever the bits that an index displaces."""
+    g = gen(E + spread)
+    steps = torch.randint(0, spread, (300, E), generator=g, device="cuda").to(torch.int32)
+    steps[200:] = -steps[200:]
+    logits = (steps + 0x3F800000).view(torch.float32)  # from 1.0 on, and below
+    got = np64(fx.route_experts(logits, top_k).ids)
+    values = np64(logits)
+    want = np.stack([np.lexsort((np.arange(E), -v))[:top_k] for v in values])
+    assert np.array_equal(got, want)
+
+
 # ---------------------------------------------------------------------------------------
 # dispatch and combine
 # ---------------------------------------------------------------------------------------
@@ -490,6 +505,27 @@ def test_dispatch(T, k, E, H, cols, elsewhere):
             assert (out.x_scale[n:] == -7.0).all()
     fresh = fx.moe_dispatch(x, scale, ids, E)
     assert torch.equal(fresh.x[:n], x[src]) and not fresh.x[n:].any()
+
+
+@pytest.mark.parametrize("T,k,E,H,cols,elsewhere", [
+    (2500, 1, 1000, 64, 1, 0.0), (2400, 8, 700, 32, 0, 0.9), (3000, 8, 256, 48, 2, 0.2),
+    (20000, 8, 256, 33, 0, 0.1), (70001, 8, 40, 16, 1, 0.5), (16500, 10, 1024, 8, 0, 0.0)])
+def test_dispatch_many_choices(T, k, E, H, cols, elsewhere):
+    """Sorts of 8 and 16 CTAs, of a warp's choices at once and in several steps."""
+    test_dispatch(T, k, E, H, cols, elsewhere)
+
+
+def test_dispatch_of_rows_off_32_bytes():
+    g = gen(77)
+    ids = random_ids(g, 2100, 2, 9, 0.4)
+    base = torch.randint(0, 256, (2100 * 64 + 16,), generator=g, device="cuda").to(torch.uint8)
+    want = fx.moe_dispatch(base[:2100 * 64].view(2100, 64).clone(), None, ids, 9)
+    x = base[16:].view(2100, 64)
+    got = fx.moe_dispatch(x, None, ids, 9)
+    n = int(got.m_sizes.sum())
+    _, dest, source = ref.dispatch(np64(ids), 9)
+    assert np.array_equal(np64(got.dest), dest) and torch.equal(got.dest, want.dest)
+    assert torch.equal(got.x[:n], x[torch.from_numpy(source).cuda()])
 
 
 def test_dispatch_foreign_ids_and_other_types():
