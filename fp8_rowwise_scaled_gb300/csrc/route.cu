@@ -1,7 +1,7 @@
 // route.cu -- the choice of each token's experts from the router's logits, and its gradient.
 //
-// One warp per token.  A lane holds kPer consecutive experts in registers, as integer keys
-// that order like their choice values, so that the largest of the warp is one redux
+// One warp per token.  A lane holds up to kPer consecutive experts in registers (of one group,
+// where the groups are a power of two: their lanes divide each evenly), as integer keys that order like their choice values, so that the largest of the warp is one redux
 // instruction.  Bound by instructions, not by memory: 256 experts are 8 scores per lane, and
 // top_k dependent maxima.  The loop over the maxima is kept short by sorting each lane's keys
 // once, with the expert's index in place of the key's lowest bits: keys are then unique, the
@@ -29,10 +29,11 @@ struct RouteParams {
   int32_t E, top_k;
   int32_t groups, top_groups, group_top;
   int32_t per_group;    // experts of a group
-  int32_t whole;        // a group is a power of two lanes, with all their experts
-  int32_t group_shift;  // log2 of the lanes of a group; if not whole, of those that look through it
+  int32_t whole;        // each group has 2^group_shift lanes of its own; no groups: all 32
+  int32_t dealt;        // those lanes have room for more than their group
+  int32_t group_shift;  // if not whole, log2 of the lanes that look through a group
   int32_t renormalize;
-  int32_t wide;  // rows (and the bias) in whole, aligned 16-byte pieces
+  int32_t wide, wide_bias;  // lanes' experts in whole, aligned pieces
   float scale;
 };
 
@@ -77,20 +78,34 @@ __device__ __forceinline__ void sort_keys(uint32_t (&s)[kN]) {
           }
 }
 
-// kPer consecutive floats from `first`, `fill` past the n-th.
+// Bytes of the pieces in which a lane reads kPer consecutive elements, where they are aligned.
 template <class T, int kPer>
-__device__ __forceinline__ void load_lane(const T* row, int first, int n, bool wide, float fill,
+__host__ __device__ constexpr int piece_bytes() {
+  constexpr int n = kPer * static_cast<int>(sizeof(T));
+  return n % 16 == 0 ? 16 : (n % 8 == 0 ? 8 : static_cast<int>(sizeof(T)));
+}
+
+// `count` (of kPer) consecutive floats, `fill` past them.
+template <class T, int kPer>
+__device__ __forceinline__ void load_lane(const T* from, int count, bool wide, float fill,
                                           float (&x)[kPer]) {
-  if constexpr (kPer * sizeof(T) >= 16) {
+  constexpr int kBytes = piece_bytes<T, kPer>();
+  if constexpr (kBytes > static_cast<int>(sizeof(T))) {
     if (wide) {
-      constexpr int kPiece = 16 / sizeof(T);
+      constexpr int kPiece = kBytes / sizeof(T);
 #pragma unroll
       for (int i = 0; i < kPer; i += kPiece) {
-        const bool in = first + i < n;
-        const uint4 r = in ? load16(row + first + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        const bool in = i < count;
+        uint32_t w[kBytes / 4] = {};
+        if constexpr (kBytes == 16) {
+          const uint4 r = in ? load16(from + i) : make_uint4(0, 0, 0, 0);
+          w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
+        } else {
+          const uint2 r = in ? *reinterpret_cast<const uint2*>(from + i) : make_uint2(0, 0);
+          w[0] = r.x, w[1] = r.y;
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kBytes / 4; ++j) {
           if constexpr (sizeof(T) == 4) {
             x[i + j] = in ? __uint_as_float(w[j]) : fill;
           } else {
@@ -104,7 +119,13 @@ __device__ __forceinline__ void load_lane(const T* row, int first, int n, bool w
     }
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = first + i < n ? to_float(row[first + i]) : fill;
+  for (int i = 0; i < kPer; ++i) x[i] = i < count ? to_float(from[i]) : fill;
+}
+
+__host__ __device__ constexpr uint32_t index_mask(int n) {  // 2^b - 1 for the least 2^b >= n
+  uint32_t m = 1;
+  while (m < static_cast<uint32_t>(n)) m *= 2;
+  return m - 1;
 }
 
 // Where expert e's key lies in shared memory: lanes kPer experts apart fall into other banks.
@@ -144,10 +165,16 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (t >= p.T) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  const int first = lane * kPer;
+  // the lane's experts, first ... first + count - 1
+  int first = lane * kPer, count = p.E - first;
+  if (p.dealt) {
+    const int within = (lane & ((1 << p.group_shift) - 1)) * kPer;
+    first = (lane >> p.group_shift) * p.per_group + within;
+    count = p.per_group - within;
+  }
 
   float x[kPer];
-  load_lane<T, kPer>(row, first, p.E, p.wide, kMasked, x);
+  load_lane<T, kPer>(row + first, count, p.wide, kMasked, x);
 
   // softmax over all experts: its maximum and sum
   float top = 0.f, total = 1.f;
@@ -160,7 +187,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (first + i < p.E) s += expf(x[i] - m);  // a NaN logit makes the sum NaN
+      if (i < count) s += expf(x[i] - m);  // a NaN logit makes the sum NaN
     top = m;
     total = warp_sum(s);
   }
@@ -174,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   {
     float b[kPer];
     if (kScore != Score::kLogits && p.bias != nullptr) {
-      load_lane<float, kPer>(p.bias, first, p.E, p.wide, 0.f, b);
+      load_lane<float, kPer>(p.bias + first, count, p.wide_bias, 0.f, b);
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) b[i] = 0.f;
@@ -202,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       uint32_t* keys = shared_keys + warp * padded(p.E);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (first + i < p.E) keys[padded(first + i)] = key[i];
+        if (i < count) keys[padded(first + i)] = key[i];
       __syncwarp();
       const int mine_group = lane >> p.group_shift, lanes = 1 << p.group_shift;
       uint32_t best = 0, second = 0;
@@ -229,8 +256,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   // keys with the expert's index in the lowest bits, the lower index larger; a lane's keys as
   // sorted lists of at most eight (sorting 8 takes 19 comparisons, 32 would take 191)
-  constexpr uint32_t kIndex = 32 * kPer - 1;
-  constexpr int kList = kPer < 8 ? kPer : 8, kLists = kPer / kList;
+  constexpr uint32_t kIndex = index_mask(32 * kPer);
+  constexpr int kLists = (kPer + 7) / 8, kList = kPer / kLists;
   int id = -1;  // lane j: the j-th choice
   float logit = kMasked;
   {
@@ -356,24 +383,42 @@ struct RouteBackwardParams {
   int32_t E, top_k;
   int32_t sigmoid;
   int32_t renormalize;
-  int32_t wide;  // rows in whole, aligned 16-byte pieces
   float scale;
 };
 
-// One warp per token, kPer consecutive experts per lane; what the chosen experts get is added
-// to the row in shared memory.  GB300, 16384 tokens x 160 experts, whole softmax: 7.05 us, by
-// instructions and latency (1.7 us of HBM).
-template <class T, int kPer>
+// One warp per token, its lanes take runs of kV experts in turn: what all experts get is written
+// first, then the lanes of the chosen write theirs again, from the same values.
+template <class T, int kV>
+__device__ __forceinline__ void store_run(T* to, const float* v) {
+  if constexpr (kV == 1) {
+    *to = from_float<T>(v[0]);
+  } else {
+    uint32_t w[kV * sizeof(T) / 4];
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(kV * sizeof(T) / 4); ++j) {
+      if constexpr (sizeof(T) == 4)
+        w[j] = __float_as_uint(v[j]);
+      else
+        w[j] = pack2(v[2 * j], v[2 * j + 1], T());
+    }
+    if constexpr (kV * sizeof(T) == 16)
+      store16(to, make_uint4(w[0], w[1], w[2], w[3]));
+    else
+      *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <class T, int kPer, int kV>
 __global__ void __launch_bounds__(kWarps * 32)
     route_backward_kernel(const __grid_constant__ RouteBackwardParams p) {
-  __shared__ float grads[kWarps][32 * kPer];
+  __shared__ int32_t sign[kWarps][32 * kPer];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (t >= p.T) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  const int first = lane * kPer;
+  T* out = static_cast<T*>(p.dlogits) + t * p.E;
 
   int id = -1;
   float g = 0.f;
@@ -383,10 +428,18 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (id >= 0) g = p.dweights[t * p.top_k + lane] * p.scale;
   }
   const float logit = id >= 0 ? to_float(row[id]) : kMasked;
-  float mine;          // what the chosen expert's logit gets
-  float v[kPer] = {};  // what every expert's logit gets
+  float mine;        // what the chosen expert's logit gets
+  float all = 0.f;   // and that it shares with every expert
   if (!p.sigmoid && !p.renormalize) {
-    load_lane<T, kPer>(row, first, p.E, p.wide, kMasked, v);
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; i += kV) {
+      const int e = lane * kV + 32 * i;
+      float run[kV];
+      load_lane<T, kV>(row + e, p.E - e, kV > 1, kMasked, run);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[i + j] = run[j];
+    }
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, v[i]);
@@ -399,83 +452,69 @@ __global__ void __launch_bounds__(kWarps * 32)
       sum += v[i];
     }
     sum = warp_sum(sum);
-    mine = logit != kMasked ? expf(logit - m) / sum * g : 0.f;
+    const float w = logit != kMasked ? expf(logit - m) : 0.f;
+    mine = logit != kMasked ? w / sum * g : 0.f;
     const float along = warp_sum(mine);
     const float factor = sum == 0.f ? 0.f : -along / sum;  // all masked: no gradient
+    all = w * factor;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] *= factor;
-  } else if (p.sigmoid) {
-    const float s = id >= 0 ? sigmoid_of(logit) : 0.f;
-    if (p.renormalize) {
-      const float total = warp_sum(s) + 1e-20f;
-      g = (g - warp_sum(g * s) / total) / total;
+#pragma unroll
+    for (int i = 0; i < kPer; i += kV) {
+      const int e = lane * kV + 32 * i;
+      if (e < p.E) store_run<T, kV>(out + e, v + i);
     }
-    mine = g * s * (id >= 0 ? sigmoid_of(-logit) : 0.f);  // 1 - s without cancellation
   } else {
-    float m = logit;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    float w = logit != kMasked ? expf(logit - m) : 0.f;
-    const float total = warp_sum(w);
-    w = logit != kMasked ? w / total : 0.f;
-    mine = w * (g - warp_sum(w * g));
-  }
-  float* d = grads[warp];
-  // experts named twice (ids of another origin): of the lanes that sign such a place, one stays
-  if (id >= 0) d[id] = __int_as_float(lane);
-  __syncwarp();
-  const bool twice = __any_sync(0xFFFFFFFFu, id >= 0 && __float_as_int(d[id]) != lane);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) d[first + i] = v[i];
-  __syncwarp();
-  if (!twice) {
-    if (id >= 0) d[id] += mine;
-  } else {  // they add up, in the order of the slots
-    for (int j = 0; j < p.top_k; ++j) {
-      if (lane == j && id >= 0) d[id] += mine;
-      __syncwarp();
-    }
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = d[first + i];
-  T* out = static_cast<T*>(p.dlogits) + t * p.E;
-  if constexpr (kPer * sizeof(T) >= 16) {
-    if (p.wide) {
-      constexpr int kPiece = 16 / sizeof(T);
-#pragma unroll
-      for (int i = 0; i < kPer; i += kPiece) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(T) == 4)
-            w[j] = __float_as_uint(v[i + j]);
-          else
-            w[j] = pack2(v[i + 2 * j], v[i + 2 * j + 1], T());
-        }
-        if (first + i < p.E) store16(out + first + i, make_uint4(w[0], w[1], w[2], w[3]));
+    if (p.sigmoid) {
+      const float s = id >= 0 ? sigmoid_of(logit) : 0.f;
+      if (p.renormalize) {
+        const float total = warp_sum(s) + 1e-20f;
+        g = (g - warp_sum(g * s) / total) / total;
       }
-      return;
+      mine = g * s * (id >= 0 ? sigmoid_of(-logit) : 0.f);  // 1 - s without cancellation
+    } else {
+      float m = logit;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+      float w = logit != kMasked ? expf(logit - m) : 0.f;
+      const float total = warp_sum(w);
+      w = logit != kMasked ? w / total : 0.f;
+      mine = w * (g - warp_sum(w * g));
+    }
+    const float zero[kV] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; i += kV) {
+      const int e = lane * kV + 32 * i;
+      if (e < p.E) store_run<T, kV>(out + e, zero);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (first + i < p.E) out[first + i] = from_float<T>(v[i]);
+  // an expert named twice (ids of another origin; of the lanes that sign its place, one stays)
+  // gets the sum, in the order of the slots, and each of its lanes writes it
+  if (id >= 0) sign[warp][id] = lane;
+  __syncwarp();
+  if (__any_sync(0xFFFFFFFFu, id >= 0 && sign[warp][id] != lane)) {
+    float sum = 0.f;
+    for (int j = 0; j < p.top_k; ++j) {
+      const int other = __shfl_sync(0xFFFFFFFFu, id, j);
+      const float part = __shfl_sync(0xFFFFFFFFu, mine, j);
+      if (other == id) sum += part;
+    }
+    mine = sum;
+  }
+  __syncwarp();  // after the stores above
+  if (id >= 0) out[id] = from_float<T>(all + mine);
 }
 
 template <class T, int kPer>
 cudaError_t launch_route(RouteParams p, Score score, void* stream) {
   const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
-  p.whole = 0;
-  for (int shift = 0; shift <= 5 && !p.whole; ++shift) {
-    p.group_shift = shift;
-    p.whole = p.per_group == kPer << shift;
-  }
-  if (!p.whole)
-    for (p.group_shift = 5; p.groups > 32 >> p.group_shift; --p.group_shift) {
-    }
-  const size_t smem = p.groups > 1 && !p.whole ? sizeof(uint32_t) * kWarps * padded(p.E) : 0;
+  constexpr int kBytes = piece_bytes<T, kPer>(), kBiasBytes = piece_bytes<float, kPer>();
+  p.dealt = p.whole && p.groups > 1 && p.per_group != kPer << p.group_shift;
+  const int64_t each = p.dealt ? p.per_group : p.E;
+  p.wide = aligned_to(p.logits, kBytes) && p.ld * sizeof(T) % kBytes == 0 &&
+           each * sizeof(T) % kBytes == 0;
+  p.wide_bias = aligned_to(p.bias, kBiasBytes) && each * sizeof(float) % kBiasBytes == 0;
+  const size_t smem = p.whole ? 0 : sizeof(uint32_t) * kWarps * padded(p.E);
   if (score == Score::kLogits)
     return launch_dependent(route_kernel<T, kPer, Score::kLogits>, grid, block, smem, stream, p);
   if (score == Score::kSoftmax)
@@ -483,25 +522,46 @@ cudaError_t launch_route(RouteParams p, Score score, void* stream) {
   return launch_dependent(route_kernel<T, kPer, Score::kSigmoid>, grid, block, smem, stream, p);
 }
 
+// The experts per lane: as few as hold them, 160 and 384 (5 and 12) included.
 template <class T>
-cudaError_t launch_route(const RouteParams& p, Score score, void* stream) {
-  if (p.E <= 32) return launch_route<T, 1>(p, score, stream);
-  if (p.E <= 64) return launch_route<T, 2>(p, score, stream);
-  if (p.E <= 128) return launch_route<T, 4>(p, score, stream);
-  if (p.E <= 256) return launch_route<T, 8>(p, score, stream);
-  if (p.E <= 512) return launch_route<T, 16>(p, score, stream);
+cudaError_t launch_route(RouteParams p, Score score, void* stream) {
+  p.group_shift = 5;
+  p.whole = (p.groups & (p.groups - 1)) == 0;
+  for (; p.groups > 32 >> p.group_shift; --p.group_shift) {
+  }
+  const int lanes = p.whole ? 1 << p.group_shift : 32, each = p.whole ? p.per_group : p.E;
+  const int per = (each + lanes - 1) / lanes;
+  if (per <= 1) return launch_route<T, 1>(p, score, stream);
+  if (per <= 2) return launch_route<T, 2>(p, score, stream);
+  if (per <= 4) return launch_route<T, 4>(p, score, stream);
+  if (per <= 5) return launch_route<T, 5>(p, score, stream);
+  if (per <= 8) return launch_route<T, 8>(p, score, stream);
+  if (per <= 12) return launch_route<T, 12>(p, score, stream);
+  if (per <= 16) return launch_route<T, 16>(p, score, stream);
   return launch_route<T, 32>(p, score, stream);
+}
+
+template <class T, int kPer>
+cudaError_t launch_backward(const RouteBackwardParams& p, void* stream) {
+  const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
+  constexpr int kBytes = piece_bytes<T, kPer>(), kV = kBytes / static_cast<int>(sizeof(T));
+  if constexpr (kV > 1)
+    if (aligned_to(p.logits, kBytes) && aligned_to(p.dlogits, kBytes) && p.E % kV == 0 &&
+        p.ld % kV == 0)
+      return launch_dependent(route_backward_kernel<T, kPer, kV>, grid, block, 0, stream, p);
+  return launch_dependent(route_backward_kernel<T, kPer, 1>, grid, block, 0, stream, p);
 }
 
 template <class T>
 cudaError_t launch_backward(const RouteBackwardParams& p, void* stream) {
-  const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps)), block(kWarps * 32);
-  if (p.E <= 32) return launch_dependent(route_backward_kernel<T, 1>, grid, block, 0, stream, p);
-  if (p.E <= 64) return launch_dependent(route_backward_kernel<T, 2>, grid, block, 0, stream, p);
-  if (p.E <= 128) return launch_dependent(route_backward_kernel<T, 4>, grid, block, 0, stream, p);
-  if (p.E <= 256) return launch_dependent(route_backward_kernel<T, 8>, grid, block, 0, stream, p);
-  if (p.E <= 512) return launch_dependent(route_backward_kernel<T, 16>, grid, block, 0, stream, p);
-  return launch_dependent(route_backward_kernel<T, 32>, grid, block, 0, stream, p);
+  if (p.E <= 32) return launch_backward<T, 1>(p, stream);
+  if (p.E <= 64) return launch_backward<T, 2>(p, stream);
+  if (p.E <= 128) return launch_backward<T, 4>(p, stream);
+  if (p.E <= 160) return launch_backward<T, 5>(p, stream);
+  if (p.E <= 256) return launch_backward<T, 8>(p, stream);
+  if (p.E <= 384) return launch_backward<T, 12>(p, stream);
+  if (p.E <= 512) return launch_backward<T, 16>(p, stream);
+  return launch_backward<T, 32>(p, stream);
 }
 
 mslkb_status check_route(int64_t T, int64_t E, int64_t ld, int64_t top_k, int32_t score,
@@ -539,15 +599,13 @@ mslkb_status mslkb_route_experts(const void* logits, const float* bias, int32_t*
                          (group_top == 1 || num_groups == 1);
   const Score by = score == MSLKB_SIGMOID ? Score::kSigmoid
                                           : (by_logits ? Score::kLogits : Score::kSoftmax);
-  const int64_t size = dtype_bytes(dtype);
+  if (topk_groups == num_groups) num_groups = topk_groups = 1;  // all of them stay
   RouteParams p{};
   p.logits = logits, p.bias = bias, p.ids = ids, p.weights = weights;
   p.T = T, p.ld = ld, p.E = static_cast<int32_t>(E), p.top_k = static_cast<int32_t>(top_k);
   p.groups = static_cast<int32_t>(num_groups), p.top_groups = static_cast<int32_t>(topk_groups);
   p.group_top = group_top, p.per_group = static_cast<int32_t>(E / num_groups);
   p.renormalize = renormalize, p.scale = static_cast<float>(scale);
-  p.wide = aligned_to(logits, 16) && aligned_to(bias, 16) && ld * size % 16 == 0 &&
-           E * size % 16 == 0 && E % 4 == 0;
   TraceRange range("route_experts", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
@@ -573,12 +631,9 @@ mslkb_status mslkb_route_experts_backward(const float* dweights, const void* log
     return MSLKB_ERR_NULL;
   int sms = 0;
   if ((s = device_sms(&sms)) != MSLKB_OK) return s;
-  const int64_t size = dtype_bytes(dtype);
-  const bool wide = aligned_to(logits, 16) && aligned_to(dlogits, 16) && ld * size % 16 == 0 &&
-                    E * size % 16 == 0;
   const RouteBackwardParams p{dweights, logits, ids, dlogits, T, ld, static_cast<int32_t>(E),
                               static_cast<int32_t>(top_k), score == MSLKB_SIGMOID, renormalize,
-                              wide, static_cast<float>(scale)};
+                              static_cast<float>(scale)};
   TraceRange range("route_experts_backward", T);
   cudaError_t e;
   if (dtype == MSLKB_BF16)
