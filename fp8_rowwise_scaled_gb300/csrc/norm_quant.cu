@@ -393,8 +393,11 @@ __global__ void __launch_bounds__(kMaxThreads)
 
 // From the ring.  kRows: blockDim.y narrow rows at a time, each with a barrier of its own (one
 // warp: none), whose weight gradients are added up at the end.
+constexpr int backward_registers(int steps) { return steps == 4 ? 128 : 64; }
+
 template <class T, int kVecs, int kStages, bool kRows>
-__global__ void __launch_bounds__(kRows ? 512 : kMaxThreads, kRows ? 2 : 1)
+__global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads),
+                                  kRows ? (kVecs == 4 ? 1 : 2) : (kVecs == 4 ? 2 : 1))
     norm_backward_ring_kernel(const __grid_constant__ NormBackwardParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float slot[2][32];
@@ -595,9 +598,10 @@ cudaError_t launch_backward_ring(const NormBackwardParams& p, int sms, int64_t* 
                                  void* stream) {
   const int x = threads_for(p.H, 8 * kVecs);
   const int row = ring_stage_bytes<T, 8, kVecs>(p.dresidual != nullptr ? 3 : 2, x);
-  const int y = kRows ? 512 / x : 1;
+  int y = kRows ? 512 / x : 1;
+  if (kRows && y > p.T / sms) y = p.T / sms > kVecs ? static_cast<int>(p.T / sms) : kVecs;
   const int smem = kStages * y * row;
-  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, x * y, 64);
+  const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, x * y, backward_registers(kVecs));
   const int64_t ctas = (p.T + y - 1) / y;
   if (*parts > ctas) *parts = ctas;
   if (*parts > most) *parts = most;
@@ -619,22 +623,37 @@ cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int
   // from memory directly against the ring, bf16, us: H = 1024 76 rows 4.4 / 5.2, 152 5.3 / 5.2,
   // 1216 9.1 / 6.7; H = 7168 76 rows 7.3 / 5.6, 608 14.3 / 11.4, 4864 75.7 / 47.1
   const bool many = p.T >= sms;
-  // GB300, 16384 rows, device time.  1024 columns bf16: several rows per CTA 33 us, one 42 us;
-  // fp32 47 and 55.  2048 bf16: 58 and 55.  16384 x 6103 rows bf16: the ring 122 us, from
-  // memory directly 201 us.
-  if (n <= 1024) {
-    constexpr int kSteps = sizeof(T) == 4 ? 1 : 2;  // of eight columns per thread
-    return many ? launch_backward_ring<T, kSteps, 2, true>(p, sms, parts, stream)
-                : launch_backward<T, kSteps, Access::k16>(p, parts, stream);
+  // Steps of eight columns per thread (few threads with many columns reduce and synchronise less,
+  // many steps leave fewer rows under way), rows per CTA and stages.  GB300, 16384 rows with a
+  // residual, device us, 1 / 2 / 4 steps:
+  //   bf16, several rows:  256 9.9 / 13.3 / 16.8   512 17.8 / 17.2 / 19.5   640 24.5 / 28.1 / 22.1
+  //                        1024 30.3 / 32.2 / 27.4   2048 (one row: 56.5 / 48.1 / 50.0) - / - / 46.9
+  //   bf16, one row:       4096 108.9 / 81.8 / 83.5   8192 rows of 7168 111.5 / 72.4 / 72.5
+  //                        2 steps, 2 / 3 stages: 4096 84.9 / 81.8, 7168 72.4 / 79.3
+  //   fp32, several rows:  512 25.9 / 32.0   1024 45.9 / 57.0      one row: 2048 84.2 / 86.1 / 83.7
+  //                        8192 rows of 5120 128.6 / 132.0 / 126.3, without a residual 125.5 /
+  //                        88.0 / 82.9
+  // A row per CTA from memory directly, 6103 x 16384 bf16: 201 us (the ring 122).
+  if constexpr (sizeof(T) == 2) {
+    if (n <= 256)
+      return many ? launch_backward_ring<T, 1, 2, true>(p, sms, parts, stream)
+                  : launch_backward<T, 1, Access::k16>(p, parts, stream);
+    if (n <= 512)
+      return many ? launch_backward_ring<T, 2, 3, true>(p, sms, parts, stream)
+                  : launch_backward<T, 1, Access::k16>(p, parts, stream);
+    if (n <= 2048)
+      return many ? launch_backward_ring<T, 4, 2, true>(p, sms, parts, stream)
+                  : launch_backward<T, 1, Access::k16>(p, parts, stream);
+    if (many && n <= 5120) return launch_backward_ring<T, 2, 3, false>(p, sms, parts, stream);
+    if (many && n <= 16384) return launch_backward_ring<T, 2, 2, false>(p, sms, parts, stream);
+  } else {
+    if (many && n <= 1024) return launch_backward_ring<T, 1, 2, true>(p, sms, parts, stream);
+    if (many && n <= 4096) return launch_backward_ring<T, 1, 2, false>(p, sms, parts, stream);
+    if (many && n <= 8192) return launch_backward_ring<T, 4, 2, false>(p, sms, parts, stream);
+    // (two stages of longer rows would not fit)
   }
-  if (n <= (sizeof(T) == 4 ? 8192 : 4096))
-    return many ? launch_backward_ring<T, 1, 2, false>(p, sms, parts, stream)
-                : launch_backward<T, 1, Access::k16>(p, parts, stream);
-  if (n <= 16384) {
-    if constexpr (sizeof(T) == 2)  // (two stages of 32-bit rows would not fit)
-      if (many) return launch_backward_ring<T, 2, 2, false>(p, sms, parts, stream);
-    return launch_backward<T, 2, Access::k16>(p, parts, stream);
-  }
+  if (n <= 4096) return launch_backward<T, 1, Access::k16>(p, parts, stream);
+  if (n <= 16384) return launch_backward<T, 2, Access::k16>(p, parts, stream);
   return launch_backward<T, 4, Access::k16>(p, parts, stream);
 }
 
