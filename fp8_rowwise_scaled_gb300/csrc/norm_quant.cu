@@ -359,17 +359,40 @@ __device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_
   }
 }
 
-// Straight from global memory.
-template <class T, int kVecs, Access kAccess>
-__global__ void __launch_bounds__(kMaxThreads)
+// Adds up the weight gradients of the CTA's rows, through shared memory [rows][kVecs * 8][x], and
+// writes them out: row y's threads those of step y.
+template <int kVecs, Access kAccess>
+__device__ __forceinline__ void store_row_sums(const NormBackwardParams& p, float* sums,
+                                               const float (&dw)[kVecs][8]) {
+  const int y = threadIdx.y, rows = blockDim.y;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      sums[((y * kVecs + i) * 8 + j) * blockDim.x + threadIdx.x] = dw[i][j];
+  __syncthreads();
+  if (y >= kVecs) return;
+  float total[8] = {};
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      total[j] += sums[((r * kVecs + y) * 8 + j) * blockDim.x + threadIdx.x];
+  store8<float, kAccess>(p.parts + static_cast<int64_t>(blockIdx.x) * p.H, column<8>(y), p.H,
+                         total);
+}
+
+// Straight from global memory.  kRows: blockDim.y narrow rows at a time, as below.
+template <class T, int kVecs, Access kAccess, bool kRows>
+__global__ void __launch_bounds__(kRows ? 512 : kMaxThreads, kRows ? 2 : 1)
     norm_backward_kernel(const __grid_constant__ NormBackwardParams p) {
   __shared__ float slot[2][32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int n = p.H;
+  const int n = p.H, y = kRows ? threadIdx.y : 0, rows = kRows ? blockDim.y : 1;
   float dw[kVecs][8] = {};
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + y; row < p.T;
+       row += static_cast<int64_t>(gridDim.x) * rows, turn ^= 1) {
     backward_row<T, kVecs, kAccess>(
         p, row, n, p.rstd[row], dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
@@ -384,11 +407,17 @@ __global__ void __launch_bounds__(kMaxThreads)
           const T* from = static_cast<const T*>(p.dresidual) + row * n;
           unpack8(load8<T, kAccess>(from, column<8>(i), p.dresidual != nullptr ? n : 0), d);
         },
-        [&](float sum) { return row_sum<false>(sum, slot[turn], 0); });
+        [&](float sum) { return row_sum<kRows>(sum, slot[turn], y); });
   }
+  if constexpr (kRows) {
+    __shared__ float sums[512 * 8 * kVecs];
+    store_row_sums<kVecs, kAccess>(p, sums, dw);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    store8<float, kAccess>(p.parts + static_cast<int64_t>(blockIdx.x) * n, column<8>(i), n, dw[i]);
+    for (int i = 0; i < kVecs; ++i)
+      store8<float, kAccess>(p.parts + static_cast<int64_t>(blockIdx.x) * n, column<8>(i), n,
+                             dw[i]);
+  }
 }
 
 // From the ring.  kRows: blockDim.y narrow rows at a time, each with a barrier of its own (one
@@ -456,24 +485,10 @@ __global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads)
     turn ^= 1;
     stage = stage == kStages - 1 ? 0 : stage + 1;
   }
-  if constexpr (kRows) {  // through the ring, which nobody reads any more: [rows][kVecs * 8][x]
+  if constexpr (kRows) {  // through the ring, which nobody reads any more
     ptx::cp_async_wait<0>();
     __syncthreads();
-    float* sums = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        sums[((y * kVecs + i) * 8 + j) * blockDim.x + threadIdx.x] = dw[i][j];
-    __syncthreads();
-    if (y >= kVecs) return;  // row y's threads add up step y of all rows
-    float total[8] = {};
-    for (int r = 0; r < rows; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        total[j] += sums[((r * kVecs + y) * 8 + j) * blockDim.x + threadIdx.x];
-    store8<float, Access::k16>(p.parts + static_cast<int64_t>(blockIdx.x) * p.H, column<8>(y), p.H,
-                               total);
+    store_row_sums<kVecs, Access::k16>(p, reinterpret_cast<float*>(ring), dw);
   } else {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
@@ -588,9 +603,27 @@ cudaError_t launch_norm(const NormParams& p, int sms, Access access, bool blocks
 // The gradient's first kernel; *parts: the rows of partial weight gradients that it writes.
 template <class T, int kVecs, Access kAccess>
 cudaError_t launch_backward(const NormBackwardParams& p, int64_t* parts, void* stream) {
-  return launch_dependent(norm_backward_kernel<T, kVecs, kAccess>,
+  return launch_dependent(norm_backward_kernel<T, kVecs, kAccess, false>,
                           dim3(static_cast<unsigned>(*parts)),
                           dim3(threads_for(p.H, 8 * kVecs)), 0, stream, p);
+}
+
+// Rows of a CTA of 512 threads with x threads each, at least `least`: fewer where the rows would
+// not reach all SMs.
+int rows_of_cta(int64_t T, int x, int sms, int least) {
+  const int64_t y = T / sms < 512 / x ? T / sms : 512 / x;
+  return y < least ? least : static_cast<int>(y);
+}
+
+template <class T>
+cudaError_t launch_backward_rows(const NormBackwardParams& p, int sms, int64_t* parts,
+                                 void* stream) {
+  const int x = threads_for(p.H, 8), y = rows_of_cta(p.T, x, sms, 1);
+  const int64_t ctas = (p.T + y - 1) / y;
+  if (*parts > ctas) *parts = ctas;
+  return launch_dependent(norm_backward_kernel<T, 1, Access::kStride, true>,
+                          dim3(static_cast<unsigned>(*parts)),
+                          dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), 0, stream, p);
 }
 
 template <class T, int kVecs, int kStages, bool kRows>
@@ -598,8 +631,7 @@ cudaError_t launch_backward_ring(const NormBackwardParams& p, int sms, int64_t* 
                                  void* stream) {
   const int x = threads_for(p.H, 8 * kVecs);
   const int row = ring_stage_bytes<T, 8, kVecs>(p.dresidual != nullptr ? 3 : 2, x);
-  int y = kRows ? 512 / x : 1;
-  if (kRows && y > p.T / sms) y = p.T / sms > kVecs ? static_cast<int>(p.T / sms) : kVecs;
+  const int y = kRows ? rows_of_cta(p.T, x, sms, kVecs) : 1;
   const int smem = kStages * y * row;
   const int64_t most = static_cast<int64_t>(sms) * ring_ctas(smem, x * y, backward_registers(kVecs));
   const int64_t ctas = (p.T + y - 1) / y;
@@ -617,6 +649,9 @@ template <class T>
 cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int64_t* parts,
                             void* stream) {
   const int64_t n = p.H;
+  // rows of any length: several per CTA against one (16384 rows, bf16): 129 16.2 / 40.4 us,
+  // 513 51.2 / 87.7, 1025 80.4 / 97.0 (fp32 81.3 / 64.4), 2047 127 / 111
+  if (!wide && n <= 768) return launch_backward_rows<T>(p, sms, parts, stream);
   if (!wide)
     return n <= 8192 ? launch_backward<T, 1, Access::kStride>(p, parts, stream)
                      : launch_backward<T, 4, Access::kStride>(p, parts, stream);

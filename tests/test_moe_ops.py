@@ -199,6 +199,17 @@ def test_norm_backward(T, H, with_res, dtype):
     assert torch.equal(out[0], dx) and torch.equal(out[1], dw)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T,H,with_res", [(1000, 256, True), (1001, 264, False), (700, 520, True),
+                                          (2600, 768, True), (170, 1024, True), (160, 2048, True),
+                                          (1300, 1536, False), (400, 2056, True),
+                                          (333, 5120, True), (333, 5128, False), (320, 6144, True),
+                                          (310, 8192, True), (153, 8192, False), (2000, 129, True),
+                                          (700, 513, False), (300, 769, True), (151, 33, True)])
+def test_norm_backward_of_many_widths(T, H, with_res, dtype):
+    test_norm_backward(T, H, with_res, dtype)
+
+
 def test_norm_backward_unaligned_and_fp32_weight():
     g = gen(3)
     T, H = 11, 512
