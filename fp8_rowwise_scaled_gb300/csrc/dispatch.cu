@@ -9,7 +9,7 @@ namespace {
 // ---------------------------------------------------------------------------------
 // dispatch: a stable counting sort of the choices by expert (place_kernel: the row of every
 // choice), then each token's row is read once and written to its rows (copy_kernel).  The
-// copies are bound by HBM's writes (GB300, 8192 tokens x 8 rows of 7168 bytes: 81 us, 6.7 TB/s);
+// copies are bound by HBM's writes (GB300, 8192 tokens x 8 rows of 7168 bytes: 82 us, 6.6 TB/s);
 // the sort in front of them (6.5 us for 65536 choices among 256 experts, 25 us for 524288) by the
 // ballots that number a warp's choices and by latency, so it is one kernel of one cluster, whose
 // 8 or 16 CTAs exchange their counts through distributed shared memory.
@@ -461,16 +461,19 @@ dim3 token_grid(int64_t T, dim3 block) {
   return dim3(static_cast<unsigned>((T + block.y - 1) / block.y));
 }
 
-// Choices up to which each token's CTA finds its rows by itself.  GB300, rows of 7168 bytes,
-// alone against sort and copy, us: 8 choices a token, 512 choices 3.2 / 5.5, 2048 6.3 / 7.4,
-// 4096 16.0 / 9.8; one choice a token, 1024 4.8 / 7.0, 2048 9.9 / 8.3.
+// Each token's CTA finds its rows by itself for up to so many choices, and up to so many
+// comparisons of one choice with another token's.  GB300, rows of 2048 bytes, alone against
+// sort and copy, us: 8 choices a token, 512 choices 3.0 / 6.2, 2048 6.3 / 7.0, 3072 9.5 / 7.3;
+// one choice a token, 1024 4.1 / 5.8, 1536 6.5 / 6.2, 2048 8.7 / 6.5.
+constexpr int64_t kDirectComparisons = 3 << 19;
 constexpr int64_t kDirectChoices = 2048;
 
 // Threads per token (GB300, bf16, 512 / 256 / 128): 8192 tokens x 8 of 7168 149 / 153 / 153 us,
 // x 2 58.3 / 53.8 / 53.8, x 1 47.0 / 41.3 / 40.7: with few rows a thread takes more columns.
 template <class T>
 cudaError_t launch_combine(const CombineParams& p, bool wide, void* stream) {
-  const dim3 block = row_threads((p.H + 7) / 8, true, p.top_k > 4 ? 512 : 256), grid = token_grid(p.T, block);
+  const dim3 block = row_threads((p.H + 7) / 8, true, p.top_k > 4 ? 512 : 256);
+  const dim3 grid = token_grid(p.T, block);
   return wide ? launch_dependent(combine_kernel<T, Access::k16>, grid, block, 0, stream, p)
               : launch_dependent(combine_kernel<T, Access::kStride>, grid, block, 0, stream, p);
 }
@@ -478,7 +481,7 @@ cudaError_t launch_combine(const CombineParams& p, bool wide, void* stream) {
 // Rows at a time by top_k: all of up to eight, as each round reads dout again (GB300, 4096
 // tokens x 8 of 7168 bf16: 8 / 4 / 2 at a time 150 / 161 / 192 us; 8192 x 2: 102 / 101 / 94).
 // 128 threads per token: 256 take 163 us, 64 173 us on the first.  Few tokens take as many as
-// there are columns for (91 x 6 of 7168, one in ten here: 128 threads 6.2 us).
+// there are columns for (91 x 6 of 7168, one in ten here: 128 threads 6.2 us, 448 3.8 us).
 template <class T, Access kAccess>
 cudaError_t launch_combine_backward(const CombineBackwardParams& p, int sms, void* stream) {
   dim3 block = row_threads((p.H + 7) / 8, true, p.T > 4 * sms ? 128 : 512);
@@ -537,7 +540,7 @@ cudaError_t launch_dispatch(CopyParams p, int sms, const int32_t* ids, int32_t* 
                             int64_t* m_sizes, int64_t T, int64_t E, void* stream) {
   const int64_t steps = p.row_bytes / static_cast<int64_t>(sizeof(Piece)), N = T * p.top_k;
   const int experts = static_cast<int>(E);
-  if (N <= kDirectChoices) {
+  if (N <= kDirectChoices && N * T <= kDirectComparisons) {
     const DirectParams d{p, ids, dest, m_sizes, static_cast<int32_t>(T), experts};
     dim3 block = row_threads(steps, false);
     if (block.x < 256) block.x = 256;  // they share the counting too

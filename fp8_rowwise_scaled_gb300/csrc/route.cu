@@ -1,13 +1,14 @@
 // route.cu -- the choice of each token's experts from the router's logits, and its gradient.
 //
 // One warp per token.  A lane holds up to kPer consecutive experts in registers (of one group,
-// where the groups are a power of two: their lanes divide each evenly), as integer keys that order like their choice values, so that the largest of the warp is one redux
-// instruction.  Bound by instructions, not by memory: 256 experts are 8 scores per lane, and
-// top_k dependent maxima.  The loop over the maxima is kept short by sorting each lane's keys
-// once, with the expert's index in place of the key's lowest bits: keys are then unique, the
-// lane that holds the maximum drops its first key, and the maximum itself names the expert.
-// Where the bits that gave way to the index decide, the chosen are put in the order of their
-// exact values, or, where another expert comes that close, chosen again by exact keys.
+// where the groups are a power of two: their lanes divide each evenly), as integer keys that
+// order like their choice values, so that the largest of the warp is one redux instruction.
+// Bound by instructions, not by memory: 256 experts are 8 scores per lane, and top_k dependent
+// maxima.  The loop over the maxima is kept short by sorting each lane's keys once, with the
+// expert's index in place of the key's lowest bits: keys are then unique, the lane that holds the
+// maximum drops its first key, and the maximum itself names the expert.  Where the bits that gave
+// way to the index decide, the chosen are put in the order of their exact values, or, where
+// another expert comes that close, chosen again by exact keys.
 // GB300, 16384 tokens x 256 experts, top 8: softmax 8 us, sigmoid + bias 12 us, with 4 of 8
 // groups 13.8 us (some 800 instructions per token at 0.8 a cycle; the logits alone are 2.6 us
 // of HBM); taking the maxima from unsorted keys took 21.9 us.

@@ -48,8 +48,8 @@
  *   whose message is the kernel variant's name (mslkb_variant_name) and whose int64
  *   payload is the rows of A, so a profiler can select this library's launches (ncu:
  *   --nvtx --nvtx-include "mslkb@<variant name>/").  The operators around the product have
- *   one range per call, named as the call without "mslkb_", with its rows.  With no tool attached the range
- *   calls return at once; a launch captured in a CUDA graph replays without them.
+ *   one range per call, named as the call without "mslkb_", with its rows.  With no tool attached
+ *   the range calls return at once; a launch captured in a CUDA graph replays without them.
  */
 #ifndef MSLKB_H_
 #define MSLKB_H_
