@@ -199,19 +199,24 @@ __device__ __forceinline__ void ring_fetch(uint32_t stage, int stream, const T* 
   }
 }
 
+template <class T, int kCols, int kVecs>  // the lane's columns 8 j ... of step i
+__device__ __forceinline__ Raw8<T> ring_raw(const uint8_t* stage, int stream, int i, int j) {
+  constexpr int kPieces = kCols * sizeof(T) / 16, kRaw = sizeof(T) / 2;
+  const int first = (threadIdx.x & 31) * kPieces + j * kRaw;
+  Raw8<T> r;
+#pragma unroll
+  for (int k = 0; k < kRaw; ++k)
+    r.w[k] = load16(stage + ring_piece<T, kCols, kVecs>(stream, i, first + k));
+  return r;
+}
+
 template <class T, int kCols, int kVecs>
 __device__ __forceinline__ void ring_read(const uint8_t* stage, int stream, int i,
                                           float (&v)[kCols]) {
-  constexpr int kPieces = kCols * sizeof(T) / 16, kRaw = sizeof(T) / 2;
-  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < kCols / 8; ++j) {
-    Raw8<T> r;
-#pragma unroll
-    for (int k = 0; k < kRaw; ++k)
-      r.w[k] = load16(stage + ring_piece<T, kCols, kVecs>(stream, i, lane * kPieces + j * kRaw + k));
     float u[8];
-    unpack8(r, u);
+    unpack8(ring_raw<T, kCols, kVecs>(stage, stream, i, j), u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[j * 8 + k] = u[k];
   }
@@ -328,12 +333,19 @@ __device__ __forceinline__ float row_sum(float sum, float* slot, int y) {
 // `residual` those of the others, `total` the row's sum.  dy and h are taken twice (from the
 // ring or L1), before and after the row's mean, rather than kept: with the weight gradient in
 // registers over all the CTA's rows, that is what leaves room for enough threads on an SM.
-template <class T, int kVecs, Access kAccess, class Inputs, class Weight, class Residual,
-          class Total>
+// kEarly: `residual` is read before the reduction (from memory, where registers allow: 16384 x
+// 1025 bf16 79 us, not 95).
+template <class T, int kVecs, Access kAccess, bool kEarly, class Inputs, class Weight,
+          class Residual, class Total>
 __device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_t row, int n,
                                              float rstd, float (&dw)[kVecs][8], Inputs inputs,
                                              Weight weight, Residual residual, Total total) {
   float sum = 0.f;
+  Raw8<T> early[kVecs];
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) early[i] = residual(i);
+  }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     float g[8], h[8], w[8];
@@ -352,7 +364,7 @@ __device__ __forceinline__ void backward_row(const NormBackwardParams& p, int64_
     float g[8], h[8], w[8], d[8];
     inputs(i, g, h);
     weight(i, w);
-    residual(i, d);
+    unpack8(kEarly ? early[i] : residual(i), d);
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = fmaf(along, h[j], fmaf(rstd, g[j] * w[j], d[j]));
     store8<T, kAccess>(static_cast<T*>(p.dx) + row * p.H, column<8>(i), n, d);
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kRows ? 512 : kMaxThreads, kRows ? 2 : 1)
   int turn = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows + y; row < p.T;
        row += static_cast<int64_t>(gridDim.x) * rows, turn ^= 1) {
-    backward_row<T, kVecs, kAccess>(
+    backward_row<T, kVecs, kAccess, kVecs * sizeof(T) <= 4>(
         p, row, n, p.rstd[row], dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
           const int c = column<8>(i);
@@ -403,9 +415,9 @@ __global__ void __launch_bounds__(kRows ? 512 : kMaxThreads, kRows ? 2 : 1)
         [&](int i, float (&w)[8]) {
           load_weight<T, 8, kAccess>(p.weight, p.weight_fp32, column<8>(i), n, w);
         },
-        [&](int i, float (&d)[8]) {
+        [&](int i) {
           const T* from = static_cast<const T*>(p.dresidual) + row * n;
-          unpack8(load8<T, kAccess>(from, column<8>(i), p.dresidual != nullptr ? n : 0), d);
+          return load8<T, kAccess>(from, column<8>(i), p.dresidual != nullptr ? n : 0);
         },
         [&](float sum) { return row_sum<kRows>(sum, slot[turn], y); });
   }
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads)
     const float next_rstd = row + step < p.T ? p.rstd[row + step] : 0.f;
     ring_wait<kStages, 8 * sizeof(T)>();
     const uint8_t* at = ring + y * row_bytes + stage * stage_bytes;
-    backward_row<T, kVecs, Access::k16>(
+    backward_row<T, kVecs, Access::k16, false>(
         p, row, p.H, rstd, dw,
         [&](int i, float (&g)[8], float (&h)[8]) {
           ring_read<T, 8, kVecs>(at, 0, i, g);
@@ -472,13 +484,8 @@ __global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = w[i][j];
         },
-        [&](int i, float (&d)[8]) {
-          if (add) {
-            ring_read<T, 8, kVecs>(at, 2, i, d);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = 0.f;
-          }
+        [&](int i) {
+          return add ? ring_raw<T, 8, kVecs>(at, 2, i, 0) : Raw8<T>{};
         },
         [&](float sum) { return row_sum<kRows>(sum, slot[turn], y); });
     rstd = next_rstd;
@@ -497,20 +504,22 @@ __global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads)
   }
 }
 
-// Column sums of parts [rows, H], in a fixed order: 32 threads per column.
+// Column sums of parts [rows, H], in a fixed order: a warp takes 32 columns of every
+// (blockDim.x / 32)-th row.
 __global__ void __launch_bounds__(1024)
     sum_parts_kernel(const float* parts, float* out, int rows, int n) {
-  __shared__ float slot[32][33];
+  __shared__ float slot[32][32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   constexpr int kAhead = 10;  // loads under way together
-  for (int r0 = part; c < n && r0 < rows; r0 += 32 * kAhead) {
+  for (int r0 = part; c < n && r0 < rows; r0 += warps * kAhead) {
     float v[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int r = r0 + 32 * i;
+      const int r = r0 + warps * i;
       v[i] = r < rows ? parts[static_cast<int64_t>(r) * n + c] : 0.f;
     }
 #pragma unroll
@@ -518,8 +527,17 @@ __global__ void __launch_bounds__(1024)
   }
   slot[part][lane] = s;
   __syncthreads();
-  s = warp_sum(slot[lane][part]);  // column `part` of the 32
-  if (lane == 0 && blockIdx.x * 32 + part < n) out[blockIdx.x * 32 + part] = s;
+  if (part > 0 || c >= n) return;
+  for (int w = 1; w < warps; ++w) s += slot[w][lane];
+  out[c] = s;
+}
+
+// Its warps: no more than ten rows each, at least four.  Few parts take small CTAs, which find
+// room beside those of the first kernel: 64 rows
+// of 8192 bf16 6.0 us in all, by 32 warps each 8.0; 8192 rows (304 parts) by 16 warps each 1 us
+// more than by 32.
+int sum_warps(int64_t parts) {
+  return parts <= 40 ? 4 : (parts <= 80 ? 8 : (parts <= 160 ? 16 : 32));
 }
 
 // ---------------------------------------------------------------------------------
@@ -655,9 +673,10 @@ cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int
   if (!wide)
     return n <= 8192 ? launch_backward<T, 1, Access::kStride>(p, parts, stream)
                      : launch_backward<T, 4, Access::kStride>(p, parts, stream);
-  // from memory directly against the ring, bf16, us: H = 1024 76 rows 4.4 / 5.2, 152 5.3 / 5.2,
-  // 1216 9.1 / 6.7; H = 7168 76 rows 7.3 / 5.6, 608 14.3 / 11.4, 4864 75.7 / 47.1
-  const bool many = p.T >= sms;
+  // From memory directly against the ring, bf16, us: 8192 columns 32 rows 5.7 / 5.6, 100 rows
+  // 7.5 / 6.8, 133 9.4 / 7.5; 16384 columns 64 rows 8.5 / 8.8, 133 11.1 / 11.5; 1024 columns,
+  // several rows per CTA, 76 4.4 / 5.2, 152 5.3 / 5.2, 1216 9.1 / 6.7.
+  const bool many = p.T >= (n > 2048 && n <= 8192 ? 32 : sms);
   // Steps of eight columns per thread (few threads with many columns reduce and synchronise less,
   // many steps leave fewer rows under way), rows per CTA and stages.  GB300, 16384 rows with a
   // residual, device us, 1 / 2 / 4 steps:
@@ -793,8 +812,8 @@ mslkb_status mslkb_add_rms_norm_quant_backward(const void* dy, const void* h, co
       e = launch_backward<float>(p, sms, wide, &parts, stream);
   }
   if (e == cudaSuccess && partial != dweight)
-    e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)), dim3(1024),
-                         0, stream, partial, dweight, static_cast<int>(T > 0 ? parts : 0),
+    e = launch_dependent(sum_parts_kernel, dim3(static_cast<unsigned>((H + 31) / 32)),
+                         dim3(32 * sum_warps(parts)), 0, stream, partial, dweight, static_cast<int>(T > 0 ? parts : 0),
                          static_cast<int>(H));
   return launch_status(e);
 }

@@ -205,7 +205,9 @@ def test_norm_backward(T, H, with_res, dtype):
                                           (1300, 1536, False), (400, 2056, True),
                                           (333, 5120, True), (333, 5128, False), (320, 6144, True),
                                           (310, 8192, True), (153, 8192, False), (2000, 129, True),
-                                          (700, 513, False), (300, 769, True), (151, 33, True)])
+                                          (700, 513, False), (300, 769, True), (151, 33, True),
+                                          (32, 4096, True), (41, 7168, False), (90, 8192, True),
+                                          (161, 2064, True), (31, 5120, True), (2, 24, True)])
 def test_norm_backward_of_many_widths(T, H, with_res, dtype):
     test_norm_backward(T, H, with_res, dtype)
 
