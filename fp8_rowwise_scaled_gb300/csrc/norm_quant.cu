@@ -13,8 +13,9 @@
 // With a row per CTA, the CTA's loads wait while it reduces and stores; so for many rows the
 // kernels are persistent, and each warp copies its own columns of the next rows into a ring of
 // stages in shared memory (cp.async, 16 bytes per lane) while it works on this one.  A warp
-// reads back only what it copied itself: cp.async.wait_group and a warp barrier are all the
-// synchronisation that the ring needs.
+// reads back only what it copied itself: cp.async.wait_group and warp barriers are all the
+// synchronisation that the ring needs (tests/test_norm_ring_lanes.py runs it on the CPU with its
+// lanes as far apart as these let them come).
 #include "host.h"
 #include "rows.cuh"
 
@@ -223,12 +224,19 @@ __device__ __forceinline__ void ring_read(const uint8_t* stage, int stream, int 
 }
 
 // The calling warp's pieces of the oldest stage are in shared memory, the others' copies
-// included.  (A warp fills a stage again only after all its lanes have read it: the row's
-// reduction lies between.)
+// included.
 template <int kStages, int kBytes>
 __device__ __forceinline__ void ring_wait() {
   ptx::cp_async_wait<kStages - 1>();
   if constexpr (kBytes > 16) __syncwarp();  // 16 bytes of columns: a lane reads its own piece
+}
+
+// All lanes of the warp have read the stage that it fills next.  For reads after the row's
+// reduction only: of what is read before it, the reduction's sum comes, which no lane has until
+// all have brought theirs.
+template <int kBytes>
+__device__ __forceinline__ void ring_release() {
+  if constexpr (kBytes > 16) __syncwarp();
 }
 
 template <class T, int kCols, int kVecs>
@@ -488,6 +496,7 @@ __global__ void __launch_bounds__(kRows ? 512 : (kVecs == 4 ? 256 : kMaxThreads)
           return add ? ring_raw<T, 8, kVecs>(at, 2, i, 0) : Raw8<T>{};
         },
         [&](float sum) { return row_sum<kRows>(sum, slot[turn], y); });
+    ring_release<8 * sizeof(T)>();  // dy, h and the residual's gradient were read after the sum
     rstd = next_rstd;
     turn ^= 1;
     stage = stage == kStages - 1 ? 0 : stage + 1;
