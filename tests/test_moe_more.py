@@ -43,3 +43,53 @@ def test_norm_backward_fp32_many_rows_per_cta(T, H, with_res):
     for _ in range(20):
         again = fx.add_rms_norm_quant_backward(dy, h, w, rstd, dres)
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw), "not the same bits again"
+
+
+# ---------------------------------------------------------------------------------------
+# SwiGLU's gradient in 32 bits
+# ---------------------------------------------------------------------------------------
+def check_swiglu_backward_fp32(dx, dy, values):
+    """Each element of an fp32 gradient to the roundings of its own formula, u = 2^-24 each: the
+    exponential 2, 1 + e and its inverse 1 each, so that sigmoid(gate) and sigmoid(-gate) are good
+    to 6 (3 and 2 with one product more); dup two products beside (8), dgate three and the sum
+    1 + gate sigmoid(-gate).  One more for the terms of second order; and the spacing of the
+    subnormals, 2^-149, in the exponential and the products."""
+    gate, up = np.split(values, 2, axis=1)
+    s, rest = ref.sigmoid(gate), ref.sigmoid(-gate)
+    factor = 1 + gate * rest
+    want = np.concatenate([dy * up * s * factor, dy * gate * s], axis=1)
+    tol = np.concatenate([np.abs(dy * up) * s * (11 * np.abs(factor) + 7 * np.abs(gate) * rest) * U,
+                          9 * U * np.abs(dy * gate) * s], axis=1)
+    small = (1 + np.abs(dy)) * (1 + np.abs(gate)) * (1 + np.abs(up)) * 2.0 ** -147
+    close(dx, want, tol + np.concatenate([small, small], axis=1), "dx")
+
+
+@pytest.mark.parametrize("R,W", [(40, 256), (7, 1000), (5, 125), (3, 8192)])
+@pytest.mark.parametrize("reach", [3.0, 20.0, 86.0, 110.0])
+def test_swiglu_backward_fp32_is_full_precision(R, W, reach):
+    """Gates over [-reach, reach], from the input and, in whole blocks, from its checkpoint."""
+    g = gen(R + W)
+    x, dy = randn(g, R, 2 * W), randn(g, R, W)
+    x[:, :W] = (2 * torch.rand((R, W), generator=g, device="cuda") - 1) * reach
+    check_swiglu_backward_fp32(fx.swiglu_quant_backward(dy, x), np64(dy), np64(x))
+    check_swiglu_backward_fp32(fx.swiglu_quant_backward(shifted(dy), x), np64(dy), np64(x))
+    if W % ref.BLOCK == 0:
+        kept = fx.swiglu_quant(x, checkpoint=True)
+        values = np64(kept.saved).reshape(R, -1, ref.BLOCK) * np64(kept.saved_scale)[..., None]
+        # (the kernel's product of code and scale is rounded to fp32)
+        values = values.reshape(R, 2 * W).astype(np.float32).astype(np.float64)
+        check_swiglu_backward_fp32(fx.swiglu_quant_backward(dy, kept.saved, kept.saved_scale),
+                                   np64(dy), values)
+
+
+def test_swiglu_backward_fp32_extremes():
+    """Infinite and NaN gates as in the formula, and gates where sigmoid is a subnormal."""
+    gate = [-104.0, -103.0, -95.0, -88.5, -87.5, 0.0, -0.0, 88.5, 104.0, 200.0, -200.0]
+    x = torch.tensor([gate + [1.0] * len(gate)], device="cuda")
+    dy = torch.ones((1, len(gate)), device="cuda")
+    check_swiglu_backward_fp32(fx.swiglu_quant_backward(dy, x), np64(dy), np64(x))
+    x[0, 0], x[0, 1] = float("nan"), float("inf")
+    dx = fx.swiglu_quant_backward(dy, x)[0]
+    n = len(gate)
+    assert torch.isnan(dx[0]) and torch.isnan(dx[n]) and torch.isinf(dx[n + 1])
+    assert torch.isfinite(dx[2:n]).all() and torch.isfinite(dx[n + 2:]).all()
