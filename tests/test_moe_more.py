@@ -8,6 +8,7 @@ import fp8_rowwise_scaled_gb300 as fx
 import moe_reference as ref
 from fp8_rowwise_scaled_gb300 import build as fxbuild
 from moe_reference import U, close, np64, rounding
+from route_tolerance import route_backward_tolerance
 from test_moe_ops import BF16, EPS, FP16, FP32, gen, randn, shifted, strided
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,37 @@ def test_swiglu_backward_fp32_extremes():
     n = len(gate)
     assert torch.isnan(dx[0]) and torch.isnan(dx[n]) and torch.isinf(dx[n + 1])
     assert torch.isfinite(dx[2:n]).all() and torch.isfinite(dx[n + 2:]).all()
+
+
+# ---------------------------------------------------------------------------------------
+# routing gradient, element by element
+# ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False),
+                                          ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("T,E,k", [(33, 8, 2), (9, 31, 6), (21, 33, 4), (21, 64, 6), (13, 100, 7),
+                                   (37, 128, 8), (21, 160, 6), (21, 161, 6), (30, 256, 8),
+                                   (11, 300, 10), (21, 384, 8), (9, 500, 10), (9, 512, 20),
+                                   (5, 777, 8), (5, 1024, 32)])
+def test_route_backward_element_by_element(T, E, k, score, renorm, dtype):
+    """Every number of experts per lane, whole and broken pieces; logits as slices of wider rows,
+    off their alignment, and the gradient off its own (which deals the experts to the lanes in
+    another order: the same bound, not the same bits)."""
+    g = gen(T + E)
+    x = randn(g, T, E, dtype=dtype, scale=1.5)
+    ids = fx.route_experts(x, k, score=score, renormalize=renorm).ids
+    ids[T // 2, 0] = -1
+    ids[0, -1] = E + 3
+    x[1, torch.randperm(E, generator=g, device="cuda")[:E // 4]] = float("-inf")
+    dw = randn(g, T, k)
+    kw = dict(score=score, renormalize=renorm, scale=1.25)
+    dx = fx.route_experts_backward(dw, x, ids, **kw)
+    args = np64(dw), np64(x), np64(ids), score == "sigmoid", renorm, 1.25
+    want = ref.route_backward(*args)
+    tol = route_backward_tolerance(*args, dtype, want)
+    close(dx, want, tol, "dlogits")
+    for v in (strided(x, 8), strided(x, 3), shifted(x)):
+        close(fx.route_experts_backward(dw, v, ids, **kw), want, tol, "dlogits of other rows")
+    out = shifted(torch.zeros_like(dx))
+    assert fx.route_experts_backward(dw, x, ids, out=out, **kw) is out
+    close(out, want, tol, "dlogits off their alignment")
