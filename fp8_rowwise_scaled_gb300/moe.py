@@ -16,6 +16,7 @@ stream of the call.  All tensors of a call are on the current device.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import NamedTuple
 
 import fp8_rowwise_scaled_gb300 as _fx
@@ -145,17 +146,23 @@ class SwigluQuant(NamedTuple):
 
 
 _torch = _b = None
+_setup_lock = threading.Lock()
 
 
 def _setup():
     """Loads the extension that checks and passes tensors (csrc/binding.cpp), and torch, which
-    the package imports only when it is used."""
+    the package imports only when it is used.  `_b` is set last: a thread that finds it set has
+    everything."""
     global _torch, _b
-    _fx.lib()
-    import torch
-    from . import build
-    _b = build.load_binding()
-    _torch = torch
+    with _setup_lock:
+        if _b is not None:
+            return
+        _fx.lib()
+        import torch
+        from . import build
+        binding = build.load_binding()
+        _torch = torch
+        _b = binding
 
 
 def _new(stream, shape, dtype, zero=False):

@@ -1,0 +1,78 @@
+"""First use of the torch forms from several host threads, on the CPU."""
+import sys
+import threading
+import time
+
+import pytest
+
+import fp8_rowwise_scaled_gb300 as fx
+from fp8_rowwise_scaled_gb300 import build as fxbuild
+from fp8_rowwise_scaled_gb300 import moe
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fxbuild.build()
+    fx.lib()
+
+
+@pytest.fixture
+def unloaded(monkeypatch):
+    """As before the first call (what is loaded now comes back afterwards)."""
+    monkeypatch.setattr(moe, "_b", None)
+    monkeypatch.setattr(moe, "_torch", None)
+
+
+def in_threads(n, call):
+    """Runs call(i) in n threads that start together; the exceptions that they raised."""
+    errors, gate = [], threading.Barrier(n)
+
+    def body(i):
+        gate.wait()
+        try:
+            call(i)
+        except BaseException as e:   # handed to the test
+            errors.append(e)
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return errors
+
+
+def test_torch_is_there_before_the_extension(unloaded):
+    """The callers look at the extension's name: at no line is it set and torch is not."""
+    seen = []
+
+    def trace(frame, event, arg):
+        if frame.f_code.co_filename != moe.__file__:
+            return None
+        seen.append((moe._b is not None, moe._torch is not None))
+        return trace
+
+    sys.settrace(trace)
+    try:
+        moe._setup()
+    finally:
+        sys.settrace(None)
+    assert seen and moe._b is not None and moe._torch is not None
+    assert (True, False) not in seen
+
+
+def test_first_calls_of_several_threads(unloaded, monkeypatch):
+    """One load for all of them, and each call gets as far as its checks."""
+    loads, load = [], fxbuild.load_binding
+
+    def slow():
+        loads.append(1)
+        time.sleep(0.05)
+        return load()
+    monkeypatch.setattr(fxbuild, "load_binding", slow)
+
+    def first(i):
+        with pytest.raises(TypeError):
+            fx.moe_combine([i], None)
+    assert in_threads(8, first) == []
+    assert len(loads) == 1
+

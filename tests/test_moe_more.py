@@ -1,5 +1,7 @@
 """More of the operators around the grouped product on the GPU: what tests/test_moe_ops.py does
 not reach, with its helpers and the same 64-bit forms."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -9,7 +11,8 @@ import moe_reference as ref
 from fp8_rowwise_scaled_gb300 import build as fxbuild
 from moe_reference import U, close, np64, rounding
 from route_tolerance import route_backward_tolerance
-from test_moe_ops import BF16, EPS, FP16, FP32, gen, randn, shifted, strided
+from test_moe_ops import (BF16, EPS, FP16, FP32, flat, gen, moe_step, randn, shifted,
+                          strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +131,41 @@ def test_route_backward_element_by_element(T, E, k, score, renorm, dtype):
     out = shifted(torch.zeros_like(dx))
     assert fx.route_experts_backward(dw, x, ids, out=out, **kw) is out
     close(out, want, tol, "dlogits off their alignment")
+
+
+def test_calls_of_several_threads():
+    """Host threads on streams and data of their own at the same time."""
+    g = gen(91)
+    E, n, cases = 32, 4, []
+    for T in (3, 65, 400, 700):
+        cases.append((randn(g, T, 512, dtype=BF16), randn(g, T, 512, dtype=BF16),
+                      randn(g, 512, dtype=BF16), randn(g, T, E)))
+    want = [flat(moe_step(*c, E)) for c in cases]
+    grads = [fx.add_rms_norm_quant_backward(c[0], c[1], c[2], torch.ones(len(c[0]), device="cuda"))
+             for c in cases]
+    torch.cuda.synchronize()
+    wrong, gate = [], threading.Barrier(n)
+
+    def body(i):
+        gate.wait()
+        try:
+            stream = torch.cuda.Stream()
+            ones = torch.ones(len(cases[i][0]), device="cuda")
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = flat(moe_step(*cases[i], E))
+                    grad = fx.add_rms_norm_quant_backward(*cases[i][:3], ones)
+                    same = [torch.equal(a, b) for a, b in zip(got + list(grad), want[i] + list(grads[i]))]
+                    if not all(same):
+                        wrong.append((i, same))
+            stream.synchronize()
+        except BaseException as e:
+            wrong.append((i, e))
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
+    assert fx.device_status() == 0
