@@ -12,7 +12,8 @@ into fp8_rowwise_scaled_gb300/libmslkb.so (CUDA runtime linked statically; the C
 tensor-map encoder is fetched at run time, so the library loads on a machine without a
 GPU).  Rebuilds only when a source or header is newer than the library.  Beside it the host
 compiler makes _binding.so, through which the torch forms of the operators around the
-product reach the library.
+product reach the library (left out where torch with CUDA is not installed: the C library does
+without).
 """
 from __future__ import annotations
 
@@ -106,15 +107,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     return lib
 
 
-def build_binding(force: bool = False) -> str:
+def torch_folder():
+    """(the folder of the installed torch, None), or (None, why the extension cannot be built)."""
+    spec = importlib.util.find_spec("torch")   # found, not imported: seconds
+    if spec is None:
+        return None, "torch is not installed"
+    folder = os.path.dirname(spec.origin)
+    if not os.path.exists(os.path.join(folder, "lib", "libc10_cuda.so")):
+        return None, f"torch in {folder} was built without CUDA"
+    return folder, None
+
+
+def build_binding(force: bool = False) -> str | None:
     """Compile _binding.so, the extension that checks torch tensors and passes them to
-    libmslkb.so, with the host compiler against this Python and torch; returns its path."""
+    libmslkb.so, with the host compiler against this Python and torch; returns its path.  Without
+    torch (or with one that has no CUDA) there is nothing that it could serve: says so and
+    returns None."""
+    torch_dir, missing = torch_folder()
+    if torch_dir is None:
+        print(f"{os.path.basename(BINDING)} left out ({missing}); libmslkb.so does not need it",
+              file=sys.stderr)
+        return None
     inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "mslkb.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(BINDING) and \
             all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
         return BINDING
-    spec = importlib.util.find_spec("torch")   # found, not imported: seconds
-    torch_dir = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
@@ -134,8 +151,10 @@ def build_binding(force: bool = False) -> str:
 def load_binding():
     """The loaded extension (raises if it has not been built)."""
     if not os.path.exists(BINDING):
-        raise RuntimeError(f"{BINDING} is missing: build it with "
-                           "`python -m fp8_rowwise_scaled_gb300.build`")
+        missing = torch_folder()[1]
+        raise RuntimeError(f"{BINDING} is missing: " + (
+            f"{missing}, and the torch forms need torch with CUDA" if missing else
+            "build it with `python -m fp8_rowwise_scaled_gb300.build`"))
     name = __package__ + "._binding"
     if name in sys.modules:
         return sys.modules[name]

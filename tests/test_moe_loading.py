@@ -1,7 +1,10 @@
-"""First use of the torch forms from several host threads, on the CPU."""
+"""First use of the torch forms from several host threads, and the build of the extension behind
+them, on the CPU."""
+import os
 import sys
 import threading
 import time
+import types
 
 import pytest
 
@@ -76,3 +79,41 @@ def test_first_calls_of_several_threads(unloaded, monkeypatch):
     assert in_threads(8, first) == []
     assert len(loads) == 1
 
+
+
+# ---------------------------------------------------------------------------------------
+# the build where torch is missing or has changed
+# ---------------------------------------------------------------------------------------
+@pytest.fixture
+def build_elsewhere(monkeypatch, tmp_path):
+    """build() of the extension into an empty folder, with what it runs recorded: the compiler
+    here writes an empty file."""
+    runs = []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+    monkeypatch.setattr(fxbuild, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(fxbuild, "subprocess", types.SimpleNamespace(run=run))
+    return runs
+
+
+@pytest.mark.parametrize("torch_is", ["missing", "without CUDA"])
+def test_build_without_torch(build_elsewhere, monkeypatch, tmp_path, capsys, torch_is):
+    """The C library needs neither torch nor the extension: build() says that it leaves the
+    extension out, and a call of the torch forms says why it is not there."""
+    folder = tmp_path / "torch"
+    folder.mkdir()
+    (folder / "__init__.py").write_text("")
+    (folder / "version.py").write_text("__version__ = '2.9.1+cpu'\n")
+    spec = types.SimpleNamespace(origin=str(folder / "__init__.py"))
+    monkeypatch.setattr(fxbuild.importlib.util, "find_spec",
+                        lambda name: None if torch_is == "missing" else spec)
+    assert fxbuild.build() == fxbuild.LIB
+    assert build_elsewhere == [] and not os.path.exists(fxbuild.BINDING)
+    said = capsys.readouterr()
+    assert "torch" in said.err + said.out
+    monkeypatch.delitem(sys.modules, fxbuild.__package__ + "._binding", raising=False)
+    with pytest.raises(RuntimeError, match="torch"):
+        fxbuild.load_binding()
