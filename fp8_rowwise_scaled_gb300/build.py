@@ -13,7 +13,8 @@ tensor-map encoder is fetched at run time, so the library loads on a machine wit
 GPU).  Rebuilds only when a source or header is newer than the library.  Beside it the host
 compiler makes _binding.so, through which the torch forms of the operators around the
 product reach the library (left out where torch with CUDA is not installed: the C library does
-without).
+without).  It is also rebuilt when Python or torch is another than the one that it was compiled
+against (_binding.so.against).
 """
 from __future__ import annotations
 
@@ -118,6 +119,18 @@ def torch_folder():
     return folder, None
 
 
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
+def built_against(torch_dir: str) -> str:
+    """The Python and the torch that an extension compiled now belongs to."""
+    return f"{sys.version}\n{torch_dir}\n{_read(os.path.join(torch_dir, 'version.py'))}"
+
+
 def build_binding(force: bool = False) -> str | None:
     """Compile _binding.so, the extension that checks torch tensors and passes them to
     libmslkb.so, with the host compiler against this Python and torch; returns its path.  Without
@@ -129,7 +142,8 @@ def build_binding(force: bool = False) -> str | None:
               file=sys.stderr)
         return None
     inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "mslkb.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and \
+    against = built_against(torch_dir)
+    if not force and os.path.exists(BINDING) and _read(BINDING + ".against") == against and \
             all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
         return BINDING
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -145,6 +159,8 @@ def build_binding(force: bool = False) -> str | None:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING + ".against", "w") as f:
+        f.write(against)
     return BINDING
 
 

@@ -117,3 +117,28 @@ def test_build_without_torch(build_elsewhere, monkeypatch, tmp_path, capsys, tor
     monkeypatch.delitem(sys.modules, fxbuild.__package__ + "._binding", raising=False)
     with pytest.raises(RuntimeError, match="torch"):
         fxbuild.load_binding()
+
+
+def test_build_again_for_another_torch_or_python(build_elsewhere, monkeypatch, tmp_path):
+    """The extension belongs to the torch and the Python that it was compiled against."""
+    fxbuild.build()
+    fxbuild.build()
+    assert len(build_elsewhere) == 1
+    folder = tmp_path / "torch"
+    (folder / "lib").mkdir(parents=True)
+    (folder / "lib" / "libc10_cuda.so").write_text("")
+    (folder / "__init__.py").write_text("")
+    (folder / "version.py").write_text("__version__ = '2.9.1+cu130'\n")
+    spec = types.SimpleNamespace(origin=str(folder / "__init__.py"))
+    monkeypatch.setattr(fxbuild.importlib.util, "find_spec", lambda name: spec)
+    fxbuild.build()
+    fxbuild.build()
+    assert len(build_elsewhere) == 2
+    (folder / "version.py").write_text("__version__ = '2.11.0+cu130'\n")
+    fxbuild.build()
+    fxbuild.build()
+    assert len(build_elsewhere) == 3
+    monkeypatch.setattr(sys, "version", "3.14.0 (another)")
+    fxbuild.build()
+    fxbuild.build()
+    assert len(build_elsewhere) == 4
