@@ -5,8 +5,8 @@
 // norm's gradient.
 //
 // Every function takes positional arguments only (moe.py names them) and returns the
-// mslkb_status; wrong tensors raise TypeError or ValueError.  `out` is the tuple of results,
-// `stream` None (the current stream) or a cudaStream_t as an integer.
+// mslkb_status, or kNoColumns; wrong tensors raise TypeError or ValueError.  `out` is the tuple
+// of results, `stream` None (the current stream) or a cudaStream_t as an integer.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -177,6 +177,18 @@ PyObject* run(F f) {
   return PyLong_FromLong(s);
 }
 
+// In place of MSLKB_OK: the rows have no columns, for which the library writes nothing, and the
+// caller fills what there is per row.
+constexpr long kNoColumns = -1;
+
+template <class F>
+PyObject* run(F f, int64_t cols) {
+  PyObject* status = run(f);
+  if (cols > 0 || status == nullptr || PyLong_AsLong(status) != MSLKB_OK) return status;
+  Py_DECREF(status);
+  return PyLong_FromLong(kNoColumns);
+}
+
 // Shape of e4m3 scales: (rows,), or (rows, cols / 128) block-scaled.
 struct ScaleShape {
   int64_t v[2];
@@ -219,7 +231,7 @@ PyObject* add_rms_norm_quant(PyObject* const* a) {
     return mslkb_add_rms_norm_quant(xp, r, w, q, static_cast<float*>(scale), ro, y,
                                     static_cast<float*>(rstd), T, H, ldx, ldr, eps, c.dtype, fp32,
                                     groupwise, s);
-  });
+  }, H);
 }
 
 // Scratch of one call from torch's allocator, for the stream of the call; given back once the
@@ -417,7 +429,7 @@ PyObject* swiglu_quant(PyObject* const* a) {
   return run([&] {
     return mslkb_swiglu_quant(x, q, static_cast<float*>(scale), saved,
                               static_cast<float*>(saved_scale), R, W, ldx, c.dtype, groupwise, s);
-  });
+  }, W);
 }
 
 // dy, saved, saved_scale, out, stream

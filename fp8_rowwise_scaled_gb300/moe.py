@@ -165,14 +165,29 @@ def _setup():
         _b = binding
 
 
+def _stream(stream):
+    """`stream` as a torch stream."""
+    return stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream))
+
+
 def _new(stream, shape, dtype, zero=False):
     """A tensor on the current device that belongs to the stream of the call."""
     make = _torch.zeros if zero else _torch.empty
     if stream is None:
         return make(shape, dtype=dtype, device="cuda")
-    s = stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(int(stream))
-    with _torch.cuda.stream(s):
+    with _torch.cuda.stream(_stream(stream)):
         return make(shape, dtype=dtype, device="cuda")
+
+
+_NO_COLUMNS = -1   # of csrc/binding.cpp: nothing was written
+
+
+def _fill(stream, *pairs):
+    """The results per row of rows without columns: (tensor or None, value)."""
+    with _torch.cuda.stream(None if stream is None else _stream(stream)):
+        for t, value in pairs:
+            if t is not None:
+                t.fill_(value)
 
 
 def _raw(stream):
@@ -216,7 +231,9 @@ def add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, groupwise=False, w
                         _new(stream, (T,), f32) if want_rstd else None)
     s = _b.add_rms_norm_quant(x, weight, residual, eps, groupwise, want_y, want_rstd, out,
                               _raw(stream))
-    if s:
+    if s == _NO_COLUMNS:
+        _fill(stream, (out[1], 1.0), (out[4], eps ** -0.5))
+    elif s:
         raise _fx.MslkbError(s, "add_rms_norm_quant")
     return out
 
@@ -352,7 +369,9 @@ def swiglu_quant(x, *, groupwise=False, checkpoint=False, out=None, stream=None)
             _new(stream, (R, W2), e4m3) if checkpoint else None,
             _new(stream, _scale_shape(R, W2, True), f32) if checkpoint else None)
     s = _b.swiglu_quant(x, groupwise, checkpoint, out, _raw(stream))
-    if s:
+    if s == _NO_COLUMNS:
+        _fill(stream, (out[1], 1.0))
+    elif s:
         raise _fx.MslkbError(s, "swiglu_quant")
     return out
 

@@ -345,7 +345,8 @@ MSLKB_API mslkb_status mslkb_f8f8bf16_rowwise_grouped_stacked_noalloc(
  *
  * e4m3 outputs: one scale per row (groupwise = 0) or per 128 columns (groupwise = 1; the
  * row length must be a multiple of 128).  scale = amax / 448 over the row or block and
- * code = e4m3_rne(value / scale); where amax < 2^-80 the codes are 0 and the scale 1.  A
+ * code = e4m3_rne(value / scale); where amax < 2^-80 the codes are 0 and the scale 1.  For
+ * rows of length 0 nothing is written (the torch forms fill in scale 1 and eps^(-1/2)).  A
  * NaN, or an infinity that the formula makes NaN, gives its row or block a NaN scale.
  */
 typedef enum mslkb_dtype { MSLKB_BF16 = 0, MSLKB_FP16 = 1, MSLKB_FP32 = 2 } mslkb_dtype;

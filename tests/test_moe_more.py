@@ -169,3 +169,33 @@ def test_calls_of_several_threads():
         t.join()
     assert not wrong, wrong[:3]
     assert fx.device_status() == 0
+
+
+@pytest.mark.parametrize("groupwise", [False, True])
+@pytest.mark.parametrize("given", [False, True])
+def test_rows_without_columns(groupwise, given):
+    """Rows of no columns have no codes, and their scales are those of zeros, 1, not what the
+    memory held; rstd is that of a sum of squares of zero."""
+    T = 300
+    x, w = torch.zeros((T, 0), dtype=BF16, device="cuda"), torch.ones(0, dtype=BF16, device="cuda")
+    scales = (T, 0) if groupwise else (T,)
+
+    def poison():
+        held = [torch.full(scales if i else (T,), float("nan"), device="cuda") for i in range(2)]
+        return (held[1], held[0]) if given else (None, None)   # else back to the allocator
+    q = torch.zeros((T, 0), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        scale, rstd = poison()
+        out = fx.NormQuant(q, scale, None, None, rstd) if given else None
+        torch.cuda.synchronize()
+        got = fx.add_rms_norm_quant(x, w, groupwise=groupwise, want_rstd=True, out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got.scale, torch.ones(scales, device="cuda"))
+        close(got.rstd, np.full(T, EPS ** -0.5), 4 * U * EPS ** -0.5, "rstd")
+        scale, _ = poison()
+        out = fx.SwigluQuant(q, scale, None, None) if given else None
+        torch.cuda.synchronize()
+        got = fx.swiglu_quant(x, groupwise=groupwise, out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got.scale, torch.ones(scales, device="cuda"))
