@@ -210,6 +210,13 @@ def _shape(t, name):
     return t.shape
 
 
+def _count(n, most, name):
+    """A number that results are allocated by."""
+    if not 0 <= n <= most:
+        raise ValueError(f"{name} must be from 0 to {most}, not {n}")
+    return n
+
+
 def add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, groupwise=False, want_y=False,
                        want_rstd=False, out=None, stream=None):
     """h = x + residual; y = h * (mean(h^2) + eps)^(-1/2) * weight; q, scale = e4m3 of y.
@@ -277,7 +284,7 @@ def route_experts(logits, top_k, *, bias=None, score="softmax", num_groups=1, to
     if _b is None:
         _setup()
     if out is None:
-        shape = (_shape(logits, "logits")[0], top_k)
+        shape = (_shape(logits, "logits")[0], _count(top_k, MAX_TOPK, "top_k"))
         out = Routing(_new(stream, shape, _torch.int32), _new(stream, shape, _torch.float32))
     s = _b.route_experts(logits, top_k, bias, _score(score), num_groups, topk_groups, group_top,
                          renormalize, scale, out, _raw(stream))
@@ -313,6 +320,10 @@ def moe_dispatch(x, x_scale, ids, num_experts, *, out=None, stream=None):
         _setup()
     if out is None:
         H, (T, k) = _shape(x, "x")[1], _shape(ids, "ids")
+        _count(k, MAX_TOPK, "experts per token")
+        _count(num_experts, MAX_EXPERTS, "num_experts")
+        if x_scale is not None and not isinstance(x_scale, _torch.Tensor):
+            raise TypeError("x_scale must be a torch.Tensor")
         out = Dispatch(_new(stream, (T * k, H), x.dtype, zero=True),
                        None if x_scale is None else
                        _new(stream, (T * k, *x_scale.shape[1:]), _torch.float32, zero=True),

@@ -199,3 +199,23 @@ def test_rows_without_columns(groupwise, given):
         got = fx.swiglu_quant(x, groupwise=groupwise, out=out, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got.scale, torch.ones(scales, device="cuda"))
+
+
+def test_sizes_are_refused_before_results_are_allocated():
+    """Numbers of experts out of range, as ValueError and with no memory taken first (the results
+    that they name would have been up to a terabyte)."""
+    x = torch.zeros((4096, 64), device="cuda")
+    ids = torch.zeros((4096, 2), dtype=torch.int32, device="cuda")
+    wide = torch.zeros((4096, 1000), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for call in (lambda: fx.route_experts(x, -1), lambda: fx.route_experts(x, 33),
+                 lambda: fx.route_experts(x, 10 ** 8), lambda: fx.moe_dispatch(x, None, ids, -1),
+                 lambda: fx.moe_dispatch(x, None, ids, 10 ** 11),
+                 lambda: fx.moe_dispatch(x, None, wide, 8)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        fx.moe_dispatch(x, [1.0], ids, 8)
+    assert torch.cuda.max_memory_allocated() == before
