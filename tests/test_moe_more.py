@@ -219,3 +219,23 @@ def test_sizes_are_refused_before_results_are_allocated():
     with pytest.raises(TypeError):
         fx.moe_dispatch(x, [1.0], ids, 8)
     assert torch.cuda.max_memory_allocated() == before
+
+
+def test_no_memory_for_the_norm_gradient():
+    """The scratch of a call raises as torch's own allocations do, and the next call is fine."""
+    T, H = 700, 16384    # 608 rows of partial sums: 40 MB
+    x, w = torch.zeros((T, H), dtype=BF16, device="cuda"), torch.ones(H, dtype=BF16, device="cuda")
+    rstd = torch.ones(T, device="cuda")
+    out = (torch.empty_like(x), torch.empty(H, device="cuda"))
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    try:
+        torch.cuda.set_per_process_memory_fraction(0.0)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            torch.empty(40 << 20, device="cuda")
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            fx.add_rms_norm_quant_backward(x, x, w, rstd, out=out)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    dx, dw = fx.add_rms_norm_quant_backward(x, x, w, rstd, out=out)
+    assert not dx.any() and not dw.any()
