@@ -30,7 +30,9 @@ inline mslkb_status launch_status(cudaError_t e) {
 }
 
 // Launches `kernel` with programmatic dependent launch: it may start while the stream's
-// previous kernel ends, and waits (griddepcontrol.wait) before its first global access.
+// previous kernel ends, and waits (griddepcontrol.wait) before its first global access.  (One
+// exception: the dispatch's copies bring rows to L2 before they wait, which changes nothing that
+// another kernel reads or writes.)
 // launch_cluster: in clusters of `cluster` CTAs.
 template <class... Params, class... Args>
 cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,

@@ -541,8 +541,8 @@ __global__ void __launch_bounds__(1024)
   out[c] = s;
 }
 
-// Its warps: no more than ten rows each, at least four.  Few parts take small CTAs, which find
-// room beside those of the first kernel: 64 rows
+// Its warps: four up to 40 parts, then one per ten rows or so, 32 at most (19 rows each of 608
+// parts).  Few parts take small CTAs, which find room beside those of the first kernel: 64 rows
 // of 8192 bf16 6.0 us in all, by 32 warps each 8.0; 8192 rows (304 parts) by 16 warps each 1 us
 // more than by 32.
 int sum_warps(int64_t parts) {
@@ -620,8 +620,14 @@ cudaError_t launch_norm(const NormParams& p, int sms, Access access, bool blocks
     }
     return launch_norm<T, 16, 4, Access::k32>(p, blocks, stream);
   }
+  // Steps per thread, with a residual and y, us at 1 / 2 / 4: bf16 8192 x 7176 105.6 / 96.4 /
+  // 91.1, 16384 x 2056 55.6 / 56.8 / 57.6, 16384 x 1000 26.8 / 26.8 / 25.7 (fp32 43.0 / 44.1 /
+  // 50.3), 4096 x 12296 - / 119.7 / 88.3; one row of 7176 2.9 / 3.2 / 3.8
   if (access == Access::k16) return launch_norm<T, 8, 4, Access::k16>(p, blocks, stream);
-  // whole blocks that are not aligned, or rows of any length with one scale
+  // whole blocks that are not aligned, or rows of any length with one scale: one step as far as
+  // 1024 threads reach (bf16, 1 / 2 / 4 steps, us: 16384 x 1025 38.2 / 48.8 / 83.4, 8192 x 8191
+  // 152.6 / 162.2 / 229.9; fp32 43.7 / 48.2 / 54.5 and 180.5 / 186.8 / 181.0), then four (4096 x
+  // 12289 fp32 - / 180.2 / 157.9, but bf16 - / 154.3 / 224.7)
   if (blocks) return launch_norm_kernel<T, 8, 4, Access::kElement, true>(p, stream);
   return n <= 8192 ? launch_norm_kernel<T, 8, 1, Access::kStride, false>(p, stream)
                    : launch_norm_kernel<T, 8, 4, Access::kStride, false>(p, stream);
@@ -692,7 +698,8 @@ cudaError_t launch_backward(const NormBackwardParams& p, int sms, bool wide, int
   //   bf16, several rows:  256 9.9 / 13.3 / 16.8   512 17.8 / 17.2 / 19.5   640 24.5 / 28.1 / 22.1
   //                        1024 30.3 / 32.2 / 27.4   2048 (one row: 56.5 / 48.1 / 50.0) - / - / 46.9
   //   bf16, one row:       4096 108.9 / 81.8 / 83.5   8192 rows of 7168 111.5 / 72.4 / 72.5
-  //                        2 steps, 2 / 3 stages: 4096 84.9 / 81.8, 7168 72.4 / 79.3
+  //                        2 steps, 2 / 3 stages: 4096 84.9 / 81.8, 8192 rows of 2560 36.1 /
+  //                        31.0, 5120 55.3 / 54.5, 5632 59.1 / 59.3, 7168 72.4 / 79.3
   //   fp32, several rows:  512 25.9 / 32.0   1024 45.9 / 57.0      one row: 2048 84.2 / 86.1 / 83.7
   //                        8192 rows of 5120 128.6 / 132.0 / 126.3, without a residual 125.5 /
   //                        88.0 / 82.9

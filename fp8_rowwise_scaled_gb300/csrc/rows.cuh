@@ -169,8 +169,7 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t codes) {
   return unpack2(h, __half());
 }
 
-// Largest magnitude, as the bit pattern of |v|: integers in the order of the floats with NaN
-// above infinity, so that a NaN is never lost in a maximum.
+// The larger of two or three, NaN if one of them is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
@@ -181,6 +180,8 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
+// Largest magnitude, as the bit pattern of |v|: integers in the order of the floats with NaN
+// above infinity, so that a NaN is never lost in a maximum.
 template <int kN>
 __device__ __forceinline__ uint32_t abs_max(const float (&v)[kN]) {
   static_assert(kN % 2 == 0, "pairs");

@@ -340,8 +340,8 @@ MSLKB_API mslkb_status mslkb_f8f8bf16_rowwise_grouped_stacked_noalloc(
  * buffer as an input only where that is said.  Nothing is allocated: the one call that
  * needs scratch takes it as `workspace` (16-byte aligned, contents need not be initialised,
  * not shared by calls that may run at the same time) of at least the bytes that its
- * *_workspace_bytes function returns.  Sums are made in a fixed order: equal inputs give
- * equal bits.
+ * *_workspace_bytes function returns.  Sums are made in a fixed order, which may depend on the
+ * sizes, row strides and alignment of a call: equal inputs in equal layouts give equal bits.
  *
  * e4m3 outputs: one scale per row (groupwise = 0) or per 128 columns (groupwise = 1; the
  * row length must be a multiple of 128).  scale = amax / 448 over the row or block and
@@ -409,7 +409,8 @@ MSLKB_API mslkb_status mslkb_add_rms_norm_quant_backward(
  *
  * An expert whose logit is -infinity (or whose choice is) is masked: it is never taken, and
  * a token with fewer than top_k experts left gets id -1 and weight 0 in the rest.  A NaN
- * choice counts as the largest and gives NaN weights.  logits: dtype [T, E], rows ld apart.
+ * choice counts as the largest; a NaN logit gives its token NaN weights (a NaN bias does not: it
+ * is not in the weights).  logits: dtype [T, E], rows ld apart.
  */
 #define MSLKB_SOFTMAX 0
 #define MSLKB_SIGMOID 1

@@ -239,3 +239,15 @@ def test_no_memory_for_the_norm_gradient():
         torch.cuda.set_per_process_memory_fraction(1.0)
     dx, dw = fx.add_rms_norm_quant_backward(x, x, w, rstd, out=out)
     assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_nan_bias(score):
+    """An expert with a NaN bias is taken first, with the weight that its logit gives."""
+    g = gen(92)
+    x, bias = randn(g, 20, 64), torch.zeros(64, device="cuda")
+    bias[11] = float("nan")
+    out = fx.route_experts(x, 4, bias=bias, score=score)
+    assert (out.ids[:, 0] == 11).all() and torch.isfinite(out.weights).all()
+    want = ref.route_weights(np64(x), np64(out.ids), score == "sigmoid", True, 1.0)
+    close(out.weights, want, 64 * U * want, "weights")   # as in tests/test_moe_ops.py
