@@ -25,8 +25,9 @@ struct SwigluParams {
 };
 
 // 1 / (1 + e^-x) with e^-x = 2^(-x log2 e): the exponent's rounding is |x| 2^-24 of it, ex2 and
-// recip are good to 2 and 1 ulp.  Far out it is exactly 0 or 1, NaN stays NaN.  For results that
-// are rounded to e4m3 or 16 bits.
+// recip are good to 2 and 1 ulp.  Far out (below -87.4, where it would be a subnormal, as well)
+// it is exactly 0 or 1, NaN stays NaN.  For results of 16 bits, and for e4m3 codes with their
+// scale (whose error, at gates of -16 2^-20 of it, is far below a code's 2^-4).
 __device__ __forceinline__ float sigmoid_of(float x) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
