@@ -14,7 +14,9 @@ include/mslkb.h).  This module only marshals arguments:
   call the same entry points on the current stream;
 * ``moe`` holds both forms of the operators around the product in a mixture-of-experts
   block (norm with an e4m3 output, expert routing, dispatch and combine, SwiGLU with an
-  e4m3 output and checkpoint, and their gradients), re-exported here.
+  e4m3 output and checkpoint, and their gradients), re-exported here;
+* ``training`` those for training the experts: their products in 16 bits and the weights'
+  gradients.
 
 There is no fallback: if libmslkb.so is missing or cannot be loaded, every call raises.
 """
@@ -133,8 +135,8 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.mslkb_workspace_count.restype = ctypes.c_int32
     L.mslkb_version.argtypes = []
     L.mslkb_version.restype = ctypes.c_int32
-    from . import moe
-    return moe.declare(L)
+    from . import moe, training
+    return training.declare(moe.declare(L))
 
 
 def lib() -> ctypes.CDLL:
@@ -649,3 +651,5 @@ from .moe import (  # noqa: E402 - needs the definitions above
     mslkb_route_experts_backward, mslkb_swiglu_quant,
     mslkb_swiglu_quant_backward, route_experts, route_experts_backward, swiglu_quant,
     swiglu_quant_backward)
+from .training import (  # noqa: E402
+    grouped_mm, grouped_mm_weight_grad, mslkb_grouped_mm, mslkb_grouped_mm_weight_grad)

@@ -454,6 +454,65 @@ PyObject* swiglu_quant_backward(PyObject* const* a) {
   });
 }
 
+// A call of the 16-bit products, led by `o`: bf16 or fp16.
+const at::Tensor& lead16(Call& c, PyObject* o, const char* name) {
+  const at::Tensor& t = c.lead(o, name);
+  if (c.type == at::kFloat)
+    raise(PyExc_TypeError, std::string(name) + ": dtype Float is not bfloat16 or float16");
+  return t;
+}
+
+const at::Tensor& stack_of(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() != 3)
+    raise(PyExc_ValueError,
+          std::string(name) + ": expected 3 dims, got " + std::to_string(t.dim()));
+  return t;
+}
+
+// x, w, m_sizes, transposed, out, stream
+PyObject* grouped_mm(PyObject* const* a) {
+  Call c;
+  const at::Tensor& x = lead16(c, a[0], "x");
+  const at::Tensor& w = stack_of(a[1], "w");
+  const bool turned = flag(a[3]);
+  const int64_t M = x.size(0), K = x.size(1), G = w.size(0), N = w.size(turned ? 2 : 1);
+  int64_t ldx = K;
+  const void* xp = c.rows(a[0], "x", {M, K}, &ldx);
+  const void* wp = turned ? c.dense(a[1], "w", c.type, {G, K, N})
+                          : c.dense(a[1], "w", c.type, {G, N, K});
+  const void* m_sizes = c.dense(a[2], "m_sizes", at::kLong, {G});
+  void* out = c.dense(a[4], "out", c.type, {M, N});
+  void* s = c.stream(a[5]);
+  return run([&] {
+    return mslkb_grouped_mm(xp, wp, static_cast<const int64_t*>(m_sizes), out, M, G, N, K, ldx,
+                            turned, c.dtype, s);
+  });
+}
+
+// dy, x, m_sizes, add, out, stream
+PyObject* grouped_mm_weight_grad(PyObject* const* a) {
+  Call c;
+  const at::Tensor& dy = lead16(c, a[0], "dy");
+  const at::Tensor& x = tensor(a[1], "x");
+  Call::matrix(x, "x");
+  const at::Tensor& to = stack_of(a[4], "out");
+  const int64_t M = dy.size(0), N = dy.size(1), K = x.size(1), G = to.size(0);
+  int64_t lddy = N, ldx = K;
+  const void* dyp = c.rows(a[0], "dy", {M, N}, &lddy);
+  const void* xp = c.rows(a[1], "x", {M, K}, &ldx);
+  const void* m_sizes = c.dense(a[2], "m_sizes", at::kLong, {G});
+  const bool fp32 = to.scalar_type() == at::kFloat;
+  const at::ScalarType type = fp32 ? at::kFloat : c.type;
+  const void* add = c.dense_or_null(a[3], "add", type, {G, N, K});
+  void* out = c.dense(a[4], "out", type, {G, N, K});
+  void* s = c.stream(a[5]);
+  return run([&] {
+    return mslkb_grouped_mm_weight_grad(dyp, xp, static_cast<const int64_t*>(m_sizes), add, out, M,
+                                        G, N, K, lddy, ldx, c.dtype, fp32, s);
+  });
+}
+
 // The number of arguments, and no C++ exception past this point.
 template <PyObject* (*kFn)(PyObject* const*), Py_ssize_t kCount>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
@@ -490,6 +549,8 @@ PyMethodDef g_methods[] = {MSLKB_ENTRY(add_rms_norm_quant, 9),
                            MSLKB_ENTRY(moe_combine_backward, 6),
                            MSLKB_ENTRY(swiglu_quant, 5),
                            MSLKB_ENTRY(swiglu_quant_backward, 5),
+                           MSLKB_ENTRY(grouped_mm, 6),
+                           MSLKB_ENTRY(grouped_mm_weight_grad, 6),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,

@@ -1,0 +1,125 @@
+// grouped_mm.cu -- 16-bit products by expert: which kernel serves a call, and the entry points.
+// (The kernel, its mathematics and layout: grouped_mm.cuh.)
+#include <cstring>
+
+#include "grouped_mm.cuh"
+#include "host.h"
+
+namespace mslkb {
+namespace {
+
+constexpr int64_t kMaxSize = 1 << 30;  // of a dimension: indices of a tile stay within 32 bits
+
+int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// More tiles than a call can have: every group's last one may be partly filled.
+template <class Cfg>
+int64_t tiles_bound(const MmParams& p) {
+  const int64_t ct = ceil_to(p.C, Cfg::kTileC);
+  if (Cfg::kGrad) return p.G * ct * ceil_to(p.R, Cfg::kTileN);
+  return ct * (p.total / Cfg::kTileN + (p.G < p.total ? p.G : p.total));
+}
+
+template <class Cfg>
+mslkb_status launch(const MmParams& p, const CUtensorMap& tp, const CUtensorMap& tq, int sms,
+                    void* stream) {
+  cudaError_t e = allow_smem<grouped_mm_kernel<Cfg>>();
+  if (e != cudaSuccess) return launch_status(e);
+  const int64_t tiles = tiles_bound<Cfg>(p);
+  if (tiles > INT32_MAX) return MSLKB_ERR_SHAPE;
+  const int64_t workers = sms / Cfg::kCtas;
+  const int64_t grid = (tiles < workers ? tiles : workers) * Cfg::kCtas;
+  return launch_status(launch_cluster(grouped_mm_kernel<Cfg>, dim3(static_cast<unsigned>(grid)),
+                                      dim3(Cfg::kThreads), Cfg::kSmemBytes, Cfg::kCtas, stream, p,
+                                      tp, tq));
+}
+
+template <Mm kMode>
+mslkb_status run(const MmParams& p, int sms, void* stream) {
+  CUtensorMap tp, tq;
+  std::memset(&tp, 0, sizeof tp);
+  std::memset(&tq, 0, sizeof tq);
+  return launch<MmCfg<kMode, false, 1, 128, 1, 4, 4>>(p, tp, tq, sms, stream);
+}
+
+bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
+  return total >= 0 && G >= 0 && N >= 0 && K >= 0 && total <= kMaxSize && N <= kMaxSize &&
+         K <= kMaxSize && G <= kMaxGroups;
+}
+
+}  // namespace
+}  // namespace mslkb
+
+extern "C" {
+
+mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_sizes, void* out,
+                              int64_t total_M, int64_t G, int64_t N, int64_t K, int64_t ldx,
+                              int32_t transposed, int32_t dtype, void* stream) {
+  using namespace mslkb;
+  if (!sizes_ok(total_M, G, N, K) || ldx < K || ldx > MSLKB_MAX_DIM) return MSLKB_ERR_SHAPE;
+  if (dtype != MSLKB_BF16 && dtype != MSLKB_FP16) return MSLKB_ERR_DTYPE;
+  if (total_M == 0 || G == 0 || N == 0) return MSLKB_OK;
+  if (m_sizes == nullptr || out == nullptr || (K > 0 && (x == nullptr || w == nullptr)))
+    return MSLKB_ERR_NULL;
+  if (!aligned_to(x, 2) || !aligned_to(w, 2) || !aligned_to(out, 2) || !aligned_to(m_sizes, 8))
+    return MSLKB_ERR_ALIGN;
+  DeviceHandles h;
+  mslkb_status s = device_handles(&h);
+  if (s != MSLKB_OK) return s;
+  MmParams p{};
+  p.P = static_cast<const uint16_t*>(w);
+  p.Q = static_cast<const uint16_t*>(x);
+  p.m_sizes = m_sizes;
+  p.out = out;
+  p.status = h.status;
+  p.timeout_ns = h.timeout_ns;
+  p.ldq = ldx;
+  p.total = static_cast<int32_t>(total_M);
+  p.G = static_cast<int32_t>(G);
+  p.C = static_cast<int32_t>(N);
+  p.K = static_cast<int32_t>(K);
+  p.bf16 = dtype == MSLKB_BF16;
+  const TraceRange range("grouped_mm", total_M);
+  return transposed ? run<Mm::kTurned>(p, h.sms, stream) : run<Mm::kRows>(p, h.sms, stream);
+}
+
+mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const int64_t* m_sizes,
+                                          const void* add, void* dw, int64_t total_M, int64_t G,
+                                          int64_t N, int64_t K, int64_t lddy, int64_t ldx,
+                                          int32_t dtype, int32_t dw_fp32, void* stream) {
+  using namespace mslkb;
+  if (!sizes_ok(total_M, G, N, K) || ldx < K || lddy < N || ldx > MSLKB_MAX_DIM ||
+      lddy > MSLKB_MAX_DIM)
+    return MSLKB_ERR_SHAPE;
+  if (dtype != MSLKB_BF16 && dtype != MSLKB_FP16) return MSLKB_ERR_DTYPE;
+  if (G == 0 || N == 0 || K == 0) return MSLKB_OK;
+  if (m_sizes == nullptr || dw == nullptr || (total_M > 0 && (x == nullptr || dy == nullptr)))
+    return MSLKB_ERR_NULL;
+  const size_t wide = dw_fp32 ? 4 : 2;
+  if (!aligned_to(x, 2) || !aligned_to(dy, 2) || !aligned_to(m_sizes, 8) ||
+      !aligned_to(dw, wide) || !aligned_to(add, wide))
+    return MSLKB_ERR_ALIGN;
+  DeviceHandles h;
+  mslkb_status s = device_handles(&h);
+  if (s != MSLKB_OK) return s;
+  MmParams p{};
+  p.P = static_cast<const uint16_t*>(x);
+  p.Q = static_cast<const uint16_t*>(dy);
+  p.m_sizes = m_sizes;
+  p.out = dw;
+  p.add = add;
+  p.status = h.status;
+  p.timeout_ns = h.timeout_ns;
+  p.ldp = ldx;
+  p.ldq = lddy;
+  p.total = static_cast<int32_t>(total_M);
+  p.G = static_cast<int32_t>(G);
+  p.C = static_cast<int32_t>(K);
+  p.R = static_cast<int32_t>(N);
+  p.bf16 = dtype == MSLKB_BF16;
+  p.out32 = dw_fp32 != 0;
+  const TraceRange range("grouped_mm_weight_grad", total_M);
+  return run<Mm::kGrad>(p, h.sms, stream);
+}
+
+}  // extern "C"

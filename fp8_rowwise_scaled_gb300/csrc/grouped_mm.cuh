@@ -1,0 +1,662 @@
+// grouped_mm.cuh -- 16-bit products by expert on the tensor cores (bf16 or fp16 operands, fp32
+// sums in tensor memory):
+//
+//   kRows   out[r, c]   = sum_k x[r, k] * w[g, c, k]              r in expert g's rows
+//   kTurned out[r, c]   = sum_k x[r, k] * w[g, k, c]              the same weights the other way
+//   kGrad   out[g, n, c] = (add[g, n, c]) + sum_r dy[r, n] * x[r, c]  over expert g's rows
+//
+// All three are D[c, r] = sum_k P[c, k] * Q[r, k] with the output's columns c on the MMA's M side
+// (TMEM lanes) and its rows r on the N side (TMEM columns).  So the rows of an expert, ragged,
+// cost the tensor core what they are, rounded up to 16 (32 on CTA pairs) and not to a tile's 128
+// or 256; and a warp reads 32 neighbouring columns of one output row from TMEM, which it stores as
+// one piece.  P is w or x, Q is x or dy; an operand whose contracted index is its rows (w turned,
+// both operands of kGrad) is read as it lies in memory, "MN-major": the tensor core takes either.
+//
+// A CTA (or a pair of CTAs on two SMs: 256 x 256 tiles, each CTA holding half of either operand)
+// is persistent and specialised by warp:
+//   warps 0-3   TMA: warp 0 loads, warp 1 issues the MMAs, warp 2 zeroes what a stage holds past
+//               the end of an expert's rows (kGrad).  Without TMA (rows that are not 16-byte
+//               aligned): all four load, through registers, and warp 4 issues the MMAs.
+//   the last 4 or 8 warps: the epilogue, from one of two accumulators while the other fills.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "kernel.cuh"
+#include "ptx.cuh"
+
+namespace mslkb {
+
+enum class Mm { kRows = 0, kTurned = 1, kGrad = 2 };
+
+struct MmParams {
+  const uint16_t* P;       // w, or x (kGrad)
+  const uint16_t* Q;       // x, or dy (kGrad)
+  const int64_t* m_sizes;  // [G]
+  void* out;
+  const void* add;         // kGrad: of out's type, or null
+  uint32_t* status;        // device status word
+  uint64_t timeout_ns;     // give-up time of one pipeline wait
+  int64_t ldp, ldq;        // elements from row to row of P (kGrad) and of Q
+  int32_t total;           // rows of x (and dy)
+  int32_t G;
+  int32_t C;               // output columns
+  int32_t R;               // kGrad: rows of each expert's output
+  int32_t K;               // contraction length (kGrad: each expert's rows instead)
+  int32_t bf16;            // 1: bf16 operands, 0: fp16
+  int32_t out32;           // 1: fp32 output, 0: the operands' type
+};
+
+template <Mm kMode_, bool kTma_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_>
+struct MmCfg {
+  static constexpr Mm kMode = kMode_;
+  static constexpr bool kGrad = kMode == Mm::kGrad;
+  static constexpr bool kPMn = kMode != Mm::kRows;  // the operand's rows are the contraction
+  static constexpr bool kQMn = kGrad;
+  static constexpr bool kTma = kTma_;
+  static constexpr int kCtas = kCtas_;
+  static constexpr bool kPair = kCtas == 2;
+  static constexpr int kTileN = kTileN_;           // output rows of a tile
+  static constexpr int kTileC = 128 * kCtas;       // output columns of a tile
+  static constexpr int kBK = 64 * kKB_;            // contraction per stage: 128-byte pieces
+  static constexpr int kKB = kKB_;
+  static constexpr int kStages = kStages_;
+  static constexpr int kQRows = kTileN / kCtas;    // of Q in one CTA
+  static constexpr int kBoxQ = kQRows < 64 ? kQRows : 64;
+  static constexpr int kPBytes = 128 * kBK * 2;
+  static constexpr int kQBytes = kQRows * kBK * 2;
+  static constexpr int kStageBytes = kPBytes + kQBytes;
+  static constexpr int kMmaWarp = kTma ? 1 : 4;
+  static constexpr int kEdgeWarp = 2;
+  static constexpr int kEpiWarp0 = kTma ? 4 : 8;
+  static constexpr int kEpiWarps = kEpiWarps_;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+  static constexpr int kRowStep = 16 * kCtas;      // a tile's rows are rounded up to these
+  static constexpr int kTmemCols = 2 * kTileN < 32 ? 32 : 2 * kTileN;
+  static constexpr int kChunk = kTileN < 32 ? kTileN : 32;  // TMEM columns read at a time
+  // rows of tiles that run next to each other: 8 x 9.5 tiles of 256 x 256 on 76 CTA pairs read
+  // the fewest bytes between them
+  static constexpr int kBand = 8;
+  // bytes between the 64-element pieces of an MN-major operand, and the step of 16 of the
+  // contraction, in the 16-byte units of a shared-memory descriptor
+  static constexpr uint32_t kMnPiece = kBK * 128;
+
+  static constexpr int kOffP = 0;
+  static constexpr int kOffQ = kStages * kPBytes;
+  static constexpr int kOffBar = kOffQ + kStages * kQBytes;
+  static constexpr int kNumBars = 3 * kStages + 4;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
+  static constexpr int kOffSched = (kOffMisc + 8 + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffSched + 2 * 4 * (kMaxGroups + 1) + 1024;
+
+  static_assert(kTileN % 16 == 0 && kTileN <= 256 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
+  static_assert(!kQMn || kQRows % 64 == 0, "MN-major pieces of 64");
+  static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(kTma || !kPair, "pairs load by TMA");
+};
+
+// A tile: its group, first output column and row, rows (h: rounded up, valid: real), and the
+// contraction [k0, k0 + len) (kGrad: rows of x and dy).
+struct MmTile {
+  int32_t g, c0, r0, h, valid, k0, len;
+};
+
+template <class Cfg>
+__device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* first,
+                                          const int32_t* tile_pre, int32_t t) {
+  const int32_t ct = (p.C + Cfg::kTileC - 1) / Cfg::kTileC;
+  MmTile o;
+  int32_t local, rows;
+  if constexpr (Cfg::kGrad) {
+    const int32_t per = ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
+    o.g = t / per;
+    local = t - o.g * per;
+    rows = p.R;
+    o.k0 = first[o.g];
+    o.len = first[o.g + 1] - o.k0;
+  } else {
+    int32_t lo = 0, hi = p.G;  // the largest g with tile_pre[g] <= t
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (tile_pre[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    o.g = lo;
+    local = t - tile_pre[lo];
+    rows = first[lo + 1] - first[lo];
+    o.k0 = 0;
+    o.len = p.K;
+  }
+  // tiles of equal height, in bands of kBand rows of tiles, column by column of tiles
+  const int32_t rt = (rows + Cfg::kTileN - 1) / Cfg::kTileN;
+  const int32_t band = local / (Cfg::kBand * ct);
+  const int32_t in = local - band * Cfg::kBand * ct;
+  const int32_t deep = min(Cfg::kBand, rt - band * Cfg::kBand);
+  const int32_t c = in / deep;
+  const int32_t r = band * Cfg::kBand + (in - c * deep);
+  const int32_t each = (rows + rt - 1) / rt;
+  const int32_t h = (each + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
+  o.c0 = c * Cfg::kTileC;
+  const int32_t off = r * h;
+  o.valid = max(0, min(h, rows - off));
+  o.h = o.valid > 0 ? (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep : 0;
+  o.r0 = off + (Cfg::kGrad ? 0 : first[o.g]);
+  return o;
+}
+
+// One warp: first[g] = rows before group g, clamped to [0, total] (G + 1 entries), and the tiles
+// before it.
+template <class Cfg>
+__device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, int32_t* tile_pre,
+                                            uint32_t lane) {
+  const int32_t G = p.G, per = (G + 31) / 32;
+  const int32_t g0 = min(G, static_cast<int32_t>(lane) * per), g1 = min(G, g0 + per);
+  const int64_t total = p.total;
+  bool clamped = false;
+  int64_t sum = 0;
+  for (int32_t g = g0; g < g1; ++g) {
+    const int64_t m = p.m_sizes[g];
+    clamped |= m < 0 || m > total;
+    const int64_t mc = m < 0 ? 0 : (m > total ? total : m);
+    first[g] = static_cast<int32_t>(mc);
+    sum += mc;
+  }
+  int64_t run = warp_incl_scan(sum, lane) - sum;
+  for (int32_t g = g0; g < g1; ++g) {
+    const int64_t mc = first[g];
+    first[g] = static_cast<int32_t>(run < total ? run : total);
+    run += mc;
+  }
+  if (lane == 31) {
+    clamped |= run > total;
+    first[G] = static_cast<int32_t>(run < total ? run : total);
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, clamped) && lane == 0 && blockIdx.x == 0)
+    atomicOr(p.status, kStatusClamped);
+  const int64_t ct = (p.C + Cfg::kTileC - 1) / Cfg::kTileC;
+  if constexpr (Cfg::kGrad) {
+    if (lane == 0)
+      tile_pre[G] = static_cast<int32_t>(G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN));
+  } else {
+    auto tiles = [&](int32_t g) {
+      return ct * ((first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN);
+    };
+    int64_t mine = 0;
+    for (int32_t g = g0; g < g1; ++g) mine += tiles(g);
+    int64_t at = warp_incl_scan(mine, lane) - mine;
+    for (int32_t g = g0; g < g1; ++g) {
+      tile_pre[g] = static_cast<int32_t>(at);
+      at += tiles(g);
+    }
+    if (lane == 31) tile_pre[G] = static_cast<int32_t>(at);
+  }
+}
+
+// Eight 16-bit elements from p on, those at or past `left` as zero.
+__device__ __forceinline__ uint4 mm_load8(const uint16_t* p, int32_t left) {
+  if (left >= 8) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+    if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+      return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+    }
+  }
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = 2 * i < left ? __ldg(p + 2 * i) : 0u;
+    const uint32_t hi = 2 * i + 1 < left ? __ldg(p + 2 * i + 1) : 0u;
+    v[i] = lo | (hi << 16);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// kind::f16 MMA, fp32 accumulator: D (+)= P * Q^T.  Instruction descriptor: bits 4-5 D format
+// (1: fp32), 7-9 and 10-12 A and B format (0: fp16, 1: bf16), 15 and 16 A and B MN-major,
+// 17-22 N >> 3, 24-28 M >> 4.
+template <class Cfg>
+__device__ __forceinline__ uint32_t mm_idesc(int32_t bf16, int32_t n) {
+  const uint32_t f = static_cast<uint32_t>(bf16);
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(Cfg::kPMn) << 15) |
+         (static_cast<uint32_t>(Cfg::kQMn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>((128 * Cfg::kCtas) >> 4) << 24);
+}
+
+// Low word of an operand's descriptor (128-byte swizzle): its address and, for an MN-major
+// operand, the bytes from one 64-element piece of M or N to the next (the high word, the 1024
+// bytes between groups of eight rows, is that of every 128-byte swizzled operand).
+template <bool kMn, uint32_t kPiece>
+__device__ __forceinline__ uint32_t mm_desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((kMn ? (kPiece >> 4) : 1u) << 16);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mm_mma(uint32_t d, uint32_t p_lo, uint32_t q_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
+        "r"(p_lo), "r"(q_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kSw128DescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
+        "r"(p_lo), "r"(q_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kSw128DescHi)
+        : "memory");
+}
+
+// Arrive, expecting `bytes`, on a barrier of another CTA of the cluster.
+__device__ __forceinline__ void mbar_expect_cluster(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                   cluster_bar),
+               "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ uint16_t mm_round16(float v, bool bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ float mm_widen(uint16_t v, bool bf16) {
+  return bf16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
+    grouped_mm_kernel(const __grid_constant__ MmParams p, const __grid_constant__ CUtensorMap tmP,
+                      const __grid_constant__ CUtensorMap tmQ) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t s_p = ptx::smem_addr(smem + Cfg::kOffP);
+  const uint32_t s_q = ptx::smem_addr(smem + Cfg::kOffQ);
+  const uint32_t s_bar = ptx::smem_addr(smem + Cfg::kOffBar);
+  auto full_bar = [&](int s) { return s_bar + 8u * s; };
+  auto empty_bar = [&](int s) { return s_bar + 8u * (Cfg::kStages + s); };
+  auto tfull_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + b); };
+  auto tempty_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + 2 + b); };
+  auto edge_bar = [&](int s) { return s_bar + 8u * (2 * Cfg::kStages + 4 + s); };
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 4);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + Cfg::kOffSched);
+  int32_t* tile_pre = first + (kMaxGroups + 1);
+
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+  const uint32_t crank = Cfg::kPair ? ptx::cluster_ctarank() : 0u;
+  const int32_t worker = static_cast<int32_t>(blockIdx.x) / Cfg::kCtas;
+  const int32_t workers = static_cast<int32_t>(gridDim.x) / Cfg::kCtas;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      // TMA: one arrival of each CTA with its bytes; else the loader's threads
+      ptx::mbar_init(full_bar(s), Cfg::kTma ? static_cast<uint32_t>(Cfg::kCtas) : 128u);
+      ptx::mbar_init(empty_bar(s), 1u);
+      ptx::mbar_init(edge_bar(s), 1u);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(tfull_bar(b), 1u);
+      ptx::mbar_init(tempty_bar(b), static_cast<uint32_t>(Cfg::kEpiWarps * Cfg::kCtas));
+    }
+    *abort_flag = 0u;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (Cfg::kTma && threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tmP);
+    ptx::prefetch_tensormap(&tmQ);
+  }
+  if (warp == Cfg::kMmaWarp) {
+    if constexpr (Cfg::kPair) {
+      ptx::tmem_alloc_pair(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
+      ptx::tmem_relinquish();
+    }
+  }
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (warp == Cfg::kEpiWarp0) mm_schedule<Cfg>(p, first, tile_pre, lane);
+  ptx::tc_fence_before_sync();
+  if constexpr (Cfg::kPair) ptx::cluster_sync();  // the peer's barriers are set up too
+  else __syncthreads();
+  ptx::tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_holder;
+  const int32_t tiles = tile_pre[p.G];
+
+  if (Cfg::kTma && warp == 0) {
+    // -------------------------------------------------------------- loads by TMA
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int32_t t = worker; ok && t < tiles; t += workers) {
+        const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
+        if (c.h == 0 || c.len == 0) continue;
+        const int32_t col = c.c0 + static_cast<int32_t>(crank) * 128;
+        const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
+        const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
+        const int32_t boxes = (mine + Cfg::kBoxQ - 1) / Cfg::kBoxQ;
+        const uint32_t bytes =
+            Cfg::kPBytes + static_cast<uint32_t>(boxes * Cfg::kBoxQ * Cfg::kBK * 2);
+        for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+          if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          // pairs: the bytes of both CTAs complete on the leader's barrier.  A stage that ends
+          // between two MMA steps (kGrad) passes through the edge warp of each CTA first.
+          uint32_t bar = Cfg::kPair ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
+          const bool edge = Cfg::kGrad && c.len - k < Cfg::kBK && (c.len & 15) != 0;
+          if (edge) {
+            bar = Cfg::kPair ? ptx::mapa_shared(edge_bar(stage), crank) : edge_bar(stage);
+            ptx::mbar_arrive_expect_tx(edge_bar(stage), bytes);
+          } else if constexpr (Cfg::kPair) {
+            mbar_expect_cluster(bar, bytes);
+          } else {
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+          }
+          const int32_t x = c.k0 + k;
+          const uint32_t dp = s_p + stage * Cfg::kPBytes, dq = s_q + stage * Cfg::kQBytes;
+          auto load2 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b) {
+            if constexpr (Cfg::kPair) ptx::tma_load_2d_pair(dst, m, bar, a, b);
+            else ptx::tma_load_2d(dst, m, bar, a, b);
+          };
+          auto load3 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t g) {
+            if constexpr (Cfg::kPair) ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
+            else ptx::tma_load_3d(dst, m, bar, a, b, g);
+          };
+          if constexpr (Cfg::kMode == Mm::kRows) {
+#pragma unroll
+            for (int i = 0; i < Cfg::kKB; ++i)
+              load3(dp + i * 128 * 128, &tmP, x + 64 * i, col, c.g);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t d = dp + i * Cfg::kMnPiece;
+              if constexpr (Cfg::kGrad) load2(d, &tmP, col + 64 * i, x);
+              else load3(d, &tmP, col + 64 * i, x, c.g);
+            }
+          }
+          if constexpr (Cfg::kQMn) {
+            for (int i = 0; i < boxes; ++i) load2(dq + i * Cfg::kMnPiece, &tmQ, row + 64 * i, x);
+          } else {
+#pragma unroll
+            for (int j = 0; j < Cfg::kKB; ++j)
+              for (int i = 0; i < boxes; ++i)
+                load2(dq + j * Cfg::kQRows * 128 + i * Cfg::kBoxQ * 128, &tmQ, x + 64 * j,
+                      row + Cfg::kBoxQ * i);
+          }
+          if (++stage == Cfg::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // wait until the MMAs have released every stage
+      for (int i = 0; ok && i < Cfg::kStages; ++i) {
+        ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (!Cfg::kTma && warp < 4) {
+    // -------------------------------------------------------------- loads through registers
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int32_t t = worker; ok && t < tiles; t += workers) {
+      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
+      if (c.h == 0 || c.len == 0) continue;
+      const uint16_t* w =
+          Cfg::kGrad ? p.P : p.P + static_cast<int64_t>(c.g) * p.C * p.K;
+      const int64_t ldp = Cfg::kGrad ? p.ldp : (Cfg::kPMn ? p.C : p.K);
+      for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+        if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        // a row of 64 elements along the operand's rows, 16-byte pieces swizzled by the row
+        auto fill = [&](uint32_t dst, const uint16_t* base, int64_t ld, bool mn, int32_t tile,
+                        int32_t at, int32_t end) {
+          // K-major: `tile` rows from `at`, contraction k..; MN-major: contraction rows, `tile`
+          // elements from `at`
+          const int32_t rows = mn ? Cfg::kBK : tile, wide = (mn ? tile : Cfg::kBK) / 64;
+          for (int32_t i = static_cast<int32_t>(threadIdx.x); i < rows * wide * 8; i += 128) {
+            const int32_t ch = i & 7, r = (i >> 3) % rows, piece = (i >> 3) / rows;
+            const int32_t row = mn ? k + r : at + r;
+            const int32_t colm = (mn ? at : k) + piece * 64 + ch * 8;
+            const bool in = row < (mn ? c.len : end);
+            const int32_t left = in ? (mn ? end : c.len) - colm : 0;
+            const int64_t from = static_cast<int64_t>(mn ? c.k0 + row : row) * ld +
+                                 (mn ? colm : c.k0 + colm);
+            const uint4 v = left > 0 ? mm_load8(base + from, left) : make_uint4(0u, 0u, 0u, 0u);
+            ptx::st_shared_v4(dst + static_cast<uint32_t>(piece * rows + r) * 128u +
+                                  (static_cast<uint32_t>(ch ^ (r & 7)) << 4),
+                              v.x, v.y, v.z, v.w);
+          }
+        };
+        fill(s_p + stage * Cfg::kPBytes, w, ldp, Cfg::kPMn, 128, c.c0, p.C);
+        fill(s_q + stage * Cfg::kQBytes, p.Q, p.ldq, Cfg::kQMn, Cfg::kQRows, c.r0,
+             Cfg::kGrad ? p.R : c.r0 + c.valid);
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(full_bar(stage));
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    for (int i = 0; ok && threadIdx.x == 0 && i < Cfg::kStages; ++i) {
+      ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    __syncwarp();
+  } else if (warp == Cfg::kMmaWarp) {
+    // -------------------------------------------------------------- MMAs
+    if (lane == 0 && crank == 0) {
+      int stage = 0;
+      uint32_t phase = 0, used = 0;
+      bool ok = true;
+      const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
+      const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
+      for (int32_t t = worker; ok && t < tiles; t += workers) {
+        const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
+        if (c.h == 0 || c.len == 0) continue;
+        const uint32_t idesc = mm_idesc<Cfg>(p.bf16, c.h);
+        const int b = static_cast<int>(used & 1u);
+        if (!wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                                  p.timeout_ns))
+          break;
+        ++used;
+        ptx::tc_fence_after_sync();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::kTileN);
+        for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+          if (!wait_bar<Cfg::kPair>(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after_sync();
+          const uint32_t p_lo = p_lo0 + static_cast<uint32_t>(stage * (Cfg::kPBytes >> 4));
+          const uint32_t q_lo = q_lo0 + static_cast<uint32_t>(stage * (Cfg::kQBytes >> 4));
+          const int32_t steps = min(Cfg::kBK / 16, (c.len - k + 15) / 16);
+#pragma unroll
+          for (int s = 0; s < Cfg::kBK / 16; ++s) {
+            constexpr uint32_t kMn16 = 16 * 128 / 16;
+            const uint32_t po = Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
+            const uint32_t qo =
+                Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
+            if (s < steps)
+              mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc, (k > 0 || s > 0) ? 1u : 0u);
+          }
+          if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+          else ptx::mma_commit(empty_bar(stage));
+          if (++stage == Cfg::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(b), 0x3);
+        else ptx::mma_commit(tfull_bar(b));
+      }
+    }
+    __syncwarp();
+  } else if (Cfg::kTma && Cfg::kGrad && warp == Cfg::kEdgeWarp) {
+    // -------------------------------------------------------------- ends of experts' rows
+    // The last stage of an expert whose rows do not end with an MMA step of 16: its last step
+    // holds rows of the next expert (or past the buffers).  They are zeroed in both operands (0 x
+    // NaN is NaN): whole 128-byte lines here, since the rows are the operands' lines.
+    int stage = 0;
+    uint32_t parity = 0;  // of each stage's edge barrier, one bit
+    for (int32_t t = worker; t < tiles; t += workers) {
+      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
+      if (c.h == 0 || c.len == 0) continue;
+      const int32_t kbs = (c.len + Cfg::kBK - 1) / Cfg::kBK;
+      const int last = (stage + kbs - 1) % Cfg::kStages;
+      stage = (stage + kbs) % Cfg::kStages;
+      if ((c.len & 15) == 0) continue;
+      const bool ok = wait_bar(edge_bar(last), (parity >> last) & 1u, abort_flag, p.status,
+                               p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      parity ^= 1u << last;
+      const int32_t in = c.len - (kbs - 1) * Cfg::kBK;  // rows of the stage that are the expert's
+      const int32_t lines = ((in + 15) & ~15) - in;
+      const int32_t boxes = (c.h / Cfg::kCtas + 63) / 64;
+      for (int32_t i = static_cast<int32_t>(lane); i < (2 + boxes) * lines * 8; i += 32) {
+        const int32_t line = in + (i >> 3) % lines, piece = (i >> 3) / lines;
+        const uint32_t base = piece < 2 ? s_p + last * Cfg::kPBytes + piece * Cfg::kMnPiece
+                                        : s_q + last * Cfg::kQBytes + (piece - 2) * Cfg::kMnPiece;
+        ptx::st_shared_v4(base + static_cast<uint32_t>(line) * 128u + (i & 7) * 16u, 0u, 0u, 0u,
+                          0u);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (Cfg::kPair) ptx::mbar_arrive_cluster(ptx::mapa_shared(full_bar(last), 0u));
+        else ptx::mbar_arrive(full_bar(last));
+      }
+    }
+  } else if (warp >= Cfg::kEpiWarp0) {
+    // -------------------------------------------------------------- epilogue
+    const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
+    constexpr int kParts = Cfg::kEpiWarps / 4;
+    uint32_t used = 0;
+    for (int32_t t = worker; t < tiles; t += workers) {
+      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
+      if (c.h == 0) continue;
+      const bool any = c.len > 0;  // else the empty sum
+      const uint32_t b = used & 1u;
+      if (any) {
+        const bool ok =
+            wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
+                     p.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        ++used;
+        ptx::tc_fence_after_sync();
+      }
+      const int32_t col = c.c0 + static_cast<int32_t>(crank * 128u + q * 32u + lane);
+      const bool in = col < p.C;
+      const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
+      for (int32_t j0 = static_cast<int32_t>(part) * Cfg::kChunk; j0 < c.valid;
+           j0 += kParts * Cfg::kChunk) {
+        uint32_t v[Cfg::kChunk];
+        if (any) {
+          const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
+                                ((q * 32u) << 16);
+          if constexpr (Cfg::kChunk == 32) ptx::tmem_ld_x32(from, v);
+          else ptx::tmem_ld_x16(from, v);
+          ptx::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < Cfg::kChunk; ++j) v[j] = 0u;
+        }
+        const int64_t at = (row0 + j0) * p.C + col;
+        const int32_t n = in ? c.valid - j0 : 0;
+        if (Cfg::kGrad && p.out32) {
+          float* out = static_cast<float*>(p.out) + at;
+          if (p.add != nullptr) {
+            const float* add = static_cast<const float*>(p.add) + at;
+            float s[Cfg::kChunk];
+#pragma unroll
+            for (int j = 0; j < Cfg::kChunk; ++j)
+              s[j] = j < n ? add[static_cast<int64_t>(j) * p.C] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < Cfg::kChunk; ++j)
+              v[j] = __float_as_uint(s[j] + __uint_as_float(v[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < Cfg::kChunk; ++j)
+            if (j < n) out[static_cast<int64_t>(j) * p.C] = __uint_as_float(v[j]);
+        } else {
+          uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+          if (Cfg::kGrad && p.add != nullptr) {
+            const uint16_t* add = static_cast<const uint16_t*>(p.add) + at;
+            uint16_t s[Cfg::kChunk];
+#pragma unroll
+            for (int j = 0; j < Cfg::kChunk; ++j)
+              s[j] = j < n ? add[static_cast<int64_t>(j) * p.C] : static_cast<uint16_t>(0);
+#pragma unroll
+            for (int j = 0; j < Cfg::kChunk; ++j)
+              v[j] = __float_as_uint(mm_widen(s[j], p.bf16) + __uint_as_float(v[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < Cfg::kChunk; ++j)
+            if (j < n)
+              out[static_cast<int64_t>(j) * p.C] = mm_round16(__uint_as_float(v[j]), p.bf16);
+        }
+      }
+      if (any) {
+        ptx::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (Cfg::kPair && crank != 0)
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(static_cast<int>(b)), 0u));
+          else
+            ptx::mbar_arrive(tempty_bar(static_cast<int>(b)));
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  ptx::tc_fence_before_sync();
+  __syncthreads();
+  bool aborting = *abort_flag != 0u;
+  if constexpr (Cfg::kPair) {
+    // neither CTA leaves while the other may signal its barriers, and both wait out what is in
+    // flight if either gave up
+    ptx::cluster_sync();
+    aborting |= ptx::ld_shared_cluster_u32(
+                    ptx::mapa_shared(ptx::smem_addr(smem + Cfg::kOffMisc + 4), crank ^ 1u)) != 0u;
+    ptx::cluster_sync();
+  }
+  if (aborting) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < 2000000ull) ptx::nanosleep(1000);
+  }
+  if (warp == Cfg::kMmaWarp) {
+    ptx::tc_fence_after_sync();
+    if constexpr (Cfg::kPair) ptx::tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+    else ptx::tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace mslkb

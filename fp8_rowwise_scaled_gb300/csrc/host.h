@@ -2,6 +2,7 @@
 // set-up, error record, profiler ranges, launches with programmatic dependence).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -16,6 +17,19 @@ void record_cuda_error(cudaError_t e);
 
 // Checks the current device (MSLKB_ERR_DEVICE unless sm_103) and returns its SM count.
 mslkb_status device_sms(int* sm_count);
+
+// What a tensor-core launch needs of the current device, checked as device_sms does.
+struct DeviceHandles {
+  int sms;
+  uint32_t* status;      // the device status word
+  uint64_t timeout_ns;   // give-up time of one pipeline wait
+};
+mslkb_status device_handles(DeviceHandles* h);
+
+// A tensor map of 16-bit elements with the 128-byte swizzle and zero fill: `dims` (2 or 3)
+// extents and box sides, innermost first, and the strides in bytes of all but the innermost.
+mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const uint64_t* extent,
+                          const uint64_t* stride, const uint32_t* box);
 
 // NVTX push/pop range of the domain "mslkb" around a launch: `name` and the call's rows.
 struct TraceRange {

@@ -804,6 +804,36 @@ mslkb_status device_sms(int* sm_count) {
   return s;
 }
 
+mslkb_status device_handles(DeviceHandles* h) {
+  DeviceState* st = nullptr;
+  const mslkb_status s = device_state(&st);
+  if (s != MSLKB_OK) return s;
+  h->sms = st->sm_count;
+  h->status = st->status_ptr;
+  h->timeout_ns = g_wait_timeout_ns.load();
+  return MSLKB_OK;
+}
+
+mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const uint64_t* extent,
+                          const uint64_t* stride, const uint32_t* box) {
+  if (g_encode == nullptr) return cuda_fail(cudaErrorNotSupported);
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < dims; ++i) {
+    d[i] = extent[i];
+    b[i] = box[i];
+    if (i + 1 < dims) st[i] = stride[i];
+  }
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(dims),
+                              const_cast<void*>(base), d, st, b, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return MSLKB_OK;
+  t_last_cuda_error = static_cast<int>(r);
+  return MSLKB_ERR_CUDA;
+}
+
 TraceRange::TraceRange(const char* name, int64_t rows) {
   nvtx_init();
   nvtxEventAttributes_t a = {};

@@ -496,6 +496,47 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
                                                    const float *saved_scale, void *dx, int64_t R,
                                                    int64_t W, int32_t dtype, void *stream);
 
+/*
+ * The products by expert in 16 bits (dtype MSLKB_BF16 or MSLKB_FP16; MSLKB_ERR_DTYPE
+ * otherwise), for experts that are kept in 16 bits and for the backward pass.  The experts'
+ * rows are packed as in the stacked layout: expert g owns m_sizes[g] rows after those of the
+ * experts before it, clamped to [0, total_M] as there (MSLKB_DEV_MSIZES_CLAMPED).  Products are
+ * exact, sums fp32.  G is limited to MSLKB_MAX_GROUPS, every other size to 2^30; any size and
+ * alignment is accepted, and rows that start and are spaced by multiples of 16 bytes (ldx, lddy,
+ * the matrices' row lengths and all addresses) take the fast path.
+ *
+ *   out[r, n] = sum over k of x[r, k] * w[g, n, k]      transposed = 0: w [G, N, K]
+ *   out[r, n] = sum over k of x[r, k] * w[g, k, n]      transposed = 1: w [G, K, N]
+ *
+ * for every row r of expert g, rounded once.  The second form takes the forward product's
+ * weights as they lie and gives its input's gradient (x is then the gradient of out).
+ *
+ *   x    device, dtype [total_M, K], rows ldx elements apart
+ *   out  device, dtype [total_M, N]; rows past the last expert's are not written
+ *
+ * K = 0 writes +0.0 to every owned row.
+ */
+MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int64_t *m_sizes,
+                                        void *out, int64_t total_M, int64_t G, int64_t N,
+                                        int64_t K, int64_t ldx, int32_t transposed, int32_t dtype,
+                                        void *stream);
+
+/*
+ * The gradient of each expert's matrix:
+ *
+ *   dw[g, n, k] = add[g, n, k] + sum over expert g's rows r of dy[r, n] * x[r, k]
+ *
+ *   dy   device, dtype [total_M, N], rows lddy apart;  x  device, dtype [total_M, K], rows ldx
+ *        apart.  Rows past the last expert's are not used, whatever they hold
+ *   add  device, [G, N, K] of dw's type: what was accumulated before; NULL: nothing.  May be dw
+ *   dw   device, [G, N, K], fp32 if dw_fp32 is not 0, else dtype; every element is written (an
+ *        expert without rows gets add, or +0.0)
+ */
+MSLKB_API mslkb_status mslkb_grouped_mm_weight_grad(
+    const void *dy, const void *x, const int64_t *m_sizes, const void *add, void *dw,
+    int64_t total_M, int64_t G, int64_t N, int64_t K, int64_t lddy, int64_t ldx, int32_t dtype,
+    int32_t dw_fp32, void *stream);
+
 /* Static description of a status code.  Never NULL. */
 MSLKB_API const char *mslkb_status_string(mslkb_status status);
 

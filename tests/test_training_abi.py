@@ -1,0 +1,44 @@
+"""C entry points for training the experts, without a GPU: argument errors come before any CUDA
+call, empty calls do nothing."""
+import pytest
+
+import fp8_rowwise_scaled_gb300 as fx
+from fp8_rowwise_scaled_gb300 import build as fxbuild
+from fp8_rowwise_scaled_gb300 import moe
+from test_moe_abi import P, call, refused
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fxbuild.build()
+    fx.lib()
+
+
+mm = call(fx.mslkb_grouped_mm, dict(
+    x=P, w=P, m_sizes=P, out=P, total_M=8, G=2, N=64, K=64, ldx=64, transposed=0,
+    dtype=moe.MSLKB_BF16, stream=0))
+weight_grad = call(fx.mslkb_grouped_mm_weight_grad, dict(
+    dy=P, x=P, m_sizes=P, add=P, dw=P, total_M=8, G=2, N=64, K=64, lddy=64, ldx=64,
+    dtype=moe.MSLKB_BF16, dw_fp32=1, stream=0))
+BIG = (1 << 30) + 1
+
+
+def test_products_refuse():
+    refused(mm, fx.MSLKB_ERR_NULL, *({k: None} for k in ("x", "w", "m_sizes", "out")))
+    refused(mm, fx.MSLKB_ERR_SHAPE, {"total_M": -1}, {"G": -1}, {"N": -1}, {"K": -1}, {"ldx": 63},
+            {"G": 1025}, {"total_M": BIG}, {"N": BIG}, {"K": BIG, "ldx": BIG}, {"ldx": 1 << 31})
+    refused(mm, fx.MSLKB_ERR_DTYPE, {"dtype": moe.MSLKB_FP32}, {"dtype": 3}, {"dtype": -1})
+    refused(mm, fx.MSLKB_ERR_ALIGN, {"x": 257}, {"w": 257}, {"out": 257}, {"m_sizes": 260})
+    refused(weight_grad, fx.MSLKB_ERR_NULL, *({k: None} for k in ("dy", "x", "m_sizes", "dw")))
+    refused(weight_grad, fx.MSLKB_ERR_SHAPE, {"total_M": -1}, {"G": -1}, {"N": -1}, {"K": -1},
+            {"ldx": 63}, {"lddy": 63}, {"G": 1025}, {"total_M": BIG}, {"N": BIG, "lddy": BIG},
+            {"K": BIG, "ldx": BIG}, {"ldx": 1 << 31}, {"lddy": 1 << 31})
+    refused(weight_grad, fx.MSLKB_ERR_DTYPE, {"dtype": moe.MSLKB_FP32}, {"dtype": 7})
+    refused(weight_grad, fx.MSLKB_ERR_ALIGN, {"x": 257}, {"dy": 257}, {"dw": 258}, {"add": 258},
+            {"m_sizes": 260}, {"dw_fp32": 0, "dw": 257})
+
+
+def test_products_of_nothing():
+    refused(mm, fx.MSLKB_OK, {"total_M": 0, "x": None, "out": None}, {"G": 0, "m_sizes": None},
+            {"N": 0, "w": None})
+    refused(weight_grad, fx.MSLKB_OK, {"G": 0, "dw": None}, {"N": 0}, {"K": 0, "dw": None})
