@@ -34,11 +34,51 @@ mslkb_status launch(const MmParams& p, const CUtensorMap& tp, const CUtensorMap&
                                       tp, tq));
 }
 
+// Tensor maps of P and Q.  Matrices of experts have three dimensions, so that what lies past one
+// is read as zero and not as the next.
+template <class Cfg>
+mslkb_status maps(const MmParams& p, CUtensorMap* tp, CUtensorMap* tq) {
+  const uint64_t C = p.C, K = p.K, G = p.G, total = p.total, R = p.R;
+  const uint64_t ldp = 2 * p.ldp, ldq = 2 * p.ldq;
+  mslkb_status s;
+  if constexpr (Cfg::kMode == Mm::kRows) {
+    const uint64_t extent[3] = {K, C, G}, stride[2] = {2 * K, 2 * K * C};
+    const uint32_t box[3] = {64, 128, 1};
+    s = encode_map16(tp, p.P, 3, extent, stride, box);
+  } else if constexpr (Cfg::kMode == Mm::kTurned) {
+    const uint64_t extent[3] = {C, K, G}, stride[2] = {2 * C, 2 * K * C};
+    const uint32_t box[3] = {64, Cfg::kBK, 1};
+    s = encode_map16(tp, p.P, 3, extent, stride, box);
+  } else {
+    const uint64_t extent[2] = {C, total};
+    const uint32_t box[2] = {64, Cfg::kBK};
+    s = encode_map16(tp, p.P, 2, extent, &ldp, box);
+  }
+  if (s != MSLKB_OK) return s;
+  const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
+  const uint32_t box[2] = {64, Cfg::kGrad ? Cfg::kBK : Cfg::kBoxQ};
+  return encode_map16(tq, p.Q, 2, extent, &ldq, box);
+}
+
+// Rows that TMA can fetch: 16-byte aligned, and so spaced.
+template <Mm kMode>
+bool by_tma(const MmParams& p) {
+  const int64_t row_p = kMode == Mm::kGrad ? p.ldp : (kMode == Mm::kRows ? p.K : p.C);
+  return aligned_to(p.P, 16) && aligned_to(p.Q, 16) && row_p % 8 == 0 && p.ldq % 8 == 0;
+}
+
 template <Mm kMode>
 mslkb_status run(const MmParams& p, int sms, void* stream) {
   CUtensorMap tp, tq;
   std::memset(&tp, 0, sizeof tp);
   std::memset(&tq, 0, sizeof tq);
+  const bool sums = kMode == Mm::kGrad ? p.total > 0 : p.K > 0;
+  if (sums && by_tma<kMode>(p)) {
+    using Cfg = MmCfg<kMode, true, 2, 256, 1, 6, 8>;
+    const mslkb_status s = maps<Cfg>(p, &tp, &tq);
+    if (s != MSLKB_OK) return s;
+    return launch<Cfg>(p, tp, tq, sms, stream);
+  }
   return launch<MmCfg<kMode, false, 1, 128, 1, 4, 4>>(p, tp, tq, sms, stream);
 }
 
