@@ -88,7 +88,7 @@ struct MmCfg {
   static constexpr int kOffP = 0;
   static constexpr int kOffQ = kStages * kPBytes;
   static constexpr int kOffBar = kOffQ + kStages * kQBytes;
-  static constexpr int kNumBars = 3 * kStages + 4;
+  static constexpr int kNumBars = 4 * kStages + 4;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
   static constexpr int kOffSched = (kOffMisc + 8 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffSched + 2 * 4 * (kMaxGroups + 1) + 1024;
@@ -257,14 +257,6 @@ __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t p_lo, uint32_t q_lo,
         : "memory");
 }
 
-// Arrive, expecting `bytes`, on a barrier of another CTA of the cluster.
-__device__ __forceinline__ void mbar_expect_cluster(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                   cluster_bar),
-               "r"(bytes)
-               : "memory");
-}
-
 __device__ __forceinline__ uint16_t mm_round16(float v, bool bf16) {
   return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
@@ -287,6 +279,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   auto tfull_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + b); };
   auto tempty_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + 2 + b); };
   auto edge_bar = [&](int s) { return s_bar + 8u * (2 * Cfg::kStages + 4 + s); };
+  auto peer_bar = [&](int s) { return s_bar + 8u * (3 * Cfg::kStages + 4 + s); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 4);
   int32_t* first = reinterpret_cast<int32_t*>(smem + Cfg::kOffSched);
@@ -299,10 +292,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
-      // TMA: one arrival of each CTA with its bytes; else the loader's threads
-      ptx::mbar_init(full_bar(s), Cfg::kTma ? static_cast<uint32_t>(Cfg::kCtas) : 128u);
+      ptx::mbar_init(full_bar(s), Cfg::kTma ? 1u : 128u);  // else the loader's threads
       ptx::mbar_init(empty_bar(s), 1u);
       ptx::mbar_init(edge_bar(s), 1u);
+      ptx::mbar_init(peer_bar(s), 1u);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(tfull_bar(b), 1u);
@@ -355,17 +348,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             ok = false;
             break;
           }
-          // pairs: the bytes of both CTAs complete on the leader's barrier.  A stage that ends
-          // between two MMA steps (kGrad) passes through the edge warp of each CTA first.
+          // pairs: the bytes of both CTAs (as many in each) complete on the leader's barrier.  A
+          // stage that ends between two MMA steps (kGrad) passes through the edge warp of each
+          // CTA first.
           uint32_t bar = Cfg::kPair ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
           const bool edge = Cfg::kGrad && c.len - k < Cfg::kBK && (c.len & 15) != 0;
           if (edge) {
             bar = Cfg::kPair ? ptx::mapa_shared(edge_bar(stage), crank) : edge_bar(stage);
             ptx::mbar_arrive_expect_tx(edge_bar(stage), bytes);
-          } else if constexpr (Cfg::kPair) {
-            mbar_expect_cluster(bar, bytes);
-          } else {
-            ptx::mbar_arrive_expect_tx(bar, bytes);
+          } else if (crank == 0) {
+            ptx::mbar_arrive_expect_tx(full_bar(stage), bytes * Cfg::kCtas);
           }
           const int32_t x = c.k0 + k;
           const uint32_t dp = s_p + stage * Cfg::kPBytes, dq = s_q + stage * Cfg::kQBytes;
@@ -489,7 +481,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         ptx::tc_fence_after_sync();
         const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::kTileN);
         for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
-          if (!wait_bar<Cfg::kPair>(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns)) {
+          if (!wait_bar(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -549,9 +541,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (Cfg::kPair) ptx::mbar_arrive_cluster(ptx::mapa_shared(full_bar(last), 0u));
-        else ptx::mbar_arrive(full_bar(last));
+      // pairs: the leader's edge warp hands the stage on when the peer's has done its part
+      if (Cfg::kPair && crank != 0) {
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(peer_bar(last), 0u));
+      } else {
+        if constexpr (Cfg::kPair) {
+          const bool there = wait_bar<true>(peer_bar(last), (parity >> last) & 1u ^ 1u, abort_flag,
+                                            p.status, p.timeout_ns);
+          if (!__all_sync(0xffffffffu, there)) break;
+        }
+        if (lane == 0) ptx::mbar_arrive(full_bar(last));
       }
     }
   } else if (warp >= Cfg::kEpiWarp0) {
