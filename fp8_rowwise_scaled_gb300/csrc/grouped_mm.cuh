@@ -16,7 +16,7 @@
 // is persistent and specialised by warp:
 //   warps 0-3   TMA: warp 0 loads, warp 1 issues the MMAs, warp 2 zeroes what a stage holds past
 //               the end of an expert's rows (kGrad).  Without TMA (rows that are not 16-byte
-//               aligned): all four load, through registers, and warp 4 issues the MMAs.
+//               aligned): warps 0-7 load, through registers, and warp 8 issues the MMAs.
 //   the last 4 or 8 warps: the epilogue, from one of two accumulators while the other fills.
 #pragma once
 
@@ -70,9 +70,10 @@ struct MmCfg {
   static constexpr int kPBytes = 128 * kBK * 2;
   static constexpr int kQBytes = kQRows * kBK * 2;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kMmaWarp = kTma ? 1 : 4;
+  static constexpr int kLoaderWarps = kTma ? 1 : 8;
+  static constexpr int kMmaWarp = kLoaderWarps;
   static constexpr int kEdgeWarp = 2;
-  static constexpr int kEpiWarp0 = kTma ? 4 : 8;
+  static constexpr int kEpiWarp0 = kTma ? 4 : 12;
   static constexpr int kEpiWarps = kEpiWarps_;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kRowStep = 16 * kCtas;      // a tile's rows are rounded up to these
@@ -198,23 +199,29 @@ __device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, i
   }
 }
 
-// Eight 16-bit elements from p on, those at or past `left` as zero.
-__device__ __forceinline__ uint4 mm_load8(const uint16_t* p, int32_t left) {
-  if (left >= 8) {
-    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
-    if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-      return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
-    }
-  }
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < left ? __ldg(p + 2 * i) : 0u;
-    const uint32_t hi = 2 * i + 1 < left ? __ldg(p + 2 * i + 1) : 0u;
-    v[i] = lo | (hi << 16);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
+// A warp's share of 64 consecutive 16-bit elements at an address that is even only: aligned words,
+// each lane one, of which those of a row that starts inside a word are put together by
+// mm_join64.  Elements at or past `left` are zero, and nothing outside [0, left) is read.
+struct MmWords {
+  uint32_t v;      // the lane's aligned word
+  uint32_t last;   // lane 31: element 63, which lies in the next word of such a row
+};
+__device__ __forceinline__ MmWords mm_load64(const uint16_t* p, int32_t left, uint32_t lane) {
+  const int32_t s = static_cast<int32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+  const int32_t e = 2 * static_cast<int32_t>(lane) - s;
+  MmWords w{0u, 0u};
+  if (e >= 0 && e + 1 < left) w.v = __ldg(reinterpret_cast<const uint32_t*>(p + e));
+  else if (e >= 0 && e < left) w.v = __ldg(p + e);
+  else if (e < 0 && e + 1 < left) w.v = static_cast<uint32_t>(__ldg(p + e + 1)) << 16;
+  if (s != 0 && lane == 31 && left > 63) w.last = __ldg(p + 63);
+  return w;
+}
+// Elements 2 * lane and 2 * lane + 1.
+__device__ __forceinline__ uint32_t mm_join64(const uint16_t* p, const MmWords& w, uint32_t lane) {
+  if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) return w.v;  // (the same for the whole warp)
+  uint32_t next = __shfl_down_sync(0xffffffffu, w.v, 1);
+  if (lane == 31) next = w.last;
+  return (w.v >> 16) | (next << 16);
 }
 
 // kind::f16 MMA, fp32 accumulator: D (+)= P * Q^T.  Instruction descriptor: bits 4-5 D format
@@ -264,6 +271,38 @@ __device__ __forceinline__ float mm_widen(uint16_t v, bool bf16) {
   return bf16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
 }
 
+__device__ __forceinline__ void mm_put(float* o, float v, bool) { *o = v; }
+__device__ __forceinline__ void mm_put(uint16_t* o, float v, bool bf16) { *o = mm_round16(v, bf16); }
+__device__ __forceinline__ float mm_get(const float* a, bool) { return *a; }
+__device__ __forceinline__ float mm_get(const uint16_t* a, bool bf16) { return mm_widen(*a, bf16); }
+
+// One column of up to kN output rows, C elements apart: v + add (null: nothing) for the first n.
+// The addresses are one running pointer: computed ahead they would take two registers each.
+template <bool kMayAdd, class T, int kN>
+__device__ __forceinline__ void mm_store(T* out, const T* add, int32_t C, int32_t n,
+                                         uint32_t (&v)[kN], bool bf16) {
+  if (kMayAdd && add != nullptr) {
+    float s[kN];
+    if (n >= kN) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j, add += C) s[j] = mm_get(add, bf16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; ++j, add += C) s[j] = j < n ? mm_get(add, bf16) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = __float_as_uint(s[j] + __uint_as_float(v[j]));
+  }
+  if (n >= kN) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j, out += C) mm_put(out, __uint_as_float(v[j]), bf16);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kN; ++j, out += C)
+      if (j < n) mm_put(out, __uint_as_float(v[j]), bf16);
+  }
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     grouped_mm_kernel(const __grid_constant__ MmParams p, const __grid_constant__ CUtensorMap tmP,
@@ -292,7 +331,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
-      ptx::mbar_init(full_bar(s), Cfg::kTma ? 1u : 128u);  // else the loader's threads
+      ptx::mbar_init(full_bar(s), Cfg::kLoaderWarps);
       ptx::mbar_init(empty_bar(s), 1u);
       ptx::mbar_init(edge_bar(s), 1u);
       ptx::mbar_init(peer_bar(s), 1u);
@@ -406,7 +445,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (!Cfg::kTma && warp < 4) {
+  } else if (!Cfg::kTma && warp < Cfg::kLoaderWarps) {
     // -------------------------------------------------------------- loads through registers
     int stage = 0;
     uint32_t phase = 0;
@@ -418,35 +457,46 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           Cfg::kGrad ? p.P : p.P + static_cast<int64_t>(c.g) * p.C * p.K;
       const int64_t ldp = Cfg::kGrad ? p.ldp : (Cfg::kPMn ? p.C : p.K);
       for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
-        if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
-          ok = false;
-          break;
-        }
-        // a row of 64 elements along the operand's rows, 16-byte pieces swizzled by the row
+        ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                                              p.timeout_ns));
+        if (!ok) break;
+        // 64 elements along the operand's rows at a time, eight such pieces under way per warp;
+        // in shared memory the 16-byte parts of a piece are swizzled by its line.  K-major:
+        // `tile` lines from row `at` on; MN-major: a line per contracted row, `tile` elements
+        // from `at` on
         auto fill = [&](uint32_t dst, const uint16_t* base, int64_t ld, bool mn, int32_t tile,
                         int32_t at, int32_t end) {
-          // K-major: `tile` rows from `at`, contraction k..; MN-major: contraction rows, `tile`
-          // elements from `at`
-          const int32_t rows = mn ? Cfg::kBK : tile, wide = (mn ? tile : Cfg::kBK) / 64;
-          for (int32_t i = static_cast<int32_t>(threadIdx.x); i < rows * wide * 8; i += 128) {
-            const int32_t ch = i & 7, r = (i >> 3) % rows, piece = (i >> 3) / rows;
-            const int32_t row = mn ? k + r : at + r;
-            const int32_t colm = (mn ? at : k) + piece * 64 + ch * 8;
-            const bool in = row < (mn ? c.len : end);
-            const int32_t left = in ? (mn ? end : c.len) - colm : 0;
-            const int64_t from = static_cast<int64_t>(mn ? c.k0 + row : row) * ld +
-                                 (mn ? colm : c.k0 + colm);
-            const uint4 v = left > 0 ? mm_load8(base + from, left) : make_uint4(0u, 0u, 0u, 0u);
-            ptx::st_shared_v4(dst + static_cast<uint32_t>(piece * rows + r) * 128u +
-                                  (static_cast<uint32_t>(ch ^ (r & 7)) << 4),
-                              v.x, v.y, v.z, v.w);
+          const int32_t lines = mn ? Cfg::kBK : tile, pieces = (mn ? tile : Cfg::kBK) / 64;
+          constexpr int kBatch = 8;
+          for (int32_t i0 = static_cast<int32_t>(warp) * kBatch; i0 < lines * pieces;
+               i0 += Cfg::kLoaderWarps * kBatch) {
+            MmWords v[kBatch];
+            const uint16_t* from[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              const int32_t r = (i0 + u) % lines, piece = (i0 + u) / lines;
+              const int32_t row = mn ? k + r : at + r;
+              const int32_t e = (mn ? at : k) + piece * 64;
+              const int32_t left = row < (mn ? c.len : end) ? (mn ? end : c.len) - e : 0;
+              from[u] = base + static_cast<int64_t>(mn ? c.k0 + row : row) * ld +
+                        (mn ? e : c.k0 + e);
+              v[u] = mm_load64(from[u], left, lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              const uint32_t line = static_cast<uint32_t>(i0 + u);
+              ptx::st_shared_u32(dst + line * 128u + (((lane >> 2) ^ (line & 7u)) << 4) +
+                                     (lane & 3u) * 4u,
+                                 mm_join64(from[u], v[u], lane));
+            }
           }
         };
         fill(s_p + stage * Cfg::kPBytes, w, ldp, Cfg::kPMn, 128, c.c0, p.C);
         fill(s_q + stage * Cfg::kQBytes, p.Q, p.ldq, Cfg::kQMn, Cfg::kQRows, c.r0,
              Cfg::kGrad ? p.R : c.r0 + c.valid);
         ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(full_bar(stage));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full_bar(stage));
         if (++stage == Cfg::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -588,38 +638,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int j = 0; j < Cfg::kChunk; ++j) v[j] = 0u;
         }
         const int64_t at = (row0 + j0) * p.C + col;
-        const int32_t n = in ? c.valid - j0 : 0;
-        if (Cfg::kGrad && p.out32) {
-          float* out = static_cast<float*>(p.out) + at;
-          if (p.add != nullptr) {
-            const float* add = static_cast<const float*>(p.add) + at;
-            float s[Cfg::kChunk];
-#pragma unroll
-            for (int j = 0; j < Cfg::kChunk; ++j)
-              s[j] = j < n ? add[static_cast<int64_t>(j) * p.C] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < Cfg::kChunk; ++j)
-              v[j] = __float_as_uint(s[j] + __uint_as_float(v[j]));
-          }
-#pragma unroll
-          for (int j = 0; j < Cfg::kChunk; ++j)
-            if (j < n) out[static_cast<int64_t>(j) * p.C] = __uint_as_float(v[j]);
-        } else {
-          uint16_t* out = static_cast<uint16_t*>(p.out) + at;
-          if (Cfg::kGrad && p.add != nullptr) {
-            const uint16_t* add = static_cast<const uint16_t*>(p.add) + at;
-            uint16_t s[Cfg::kChunk];
-#pragma unroll
-            for (int j = 0; j < Cfg::kChunk; ++j)
-              s[j] = j < n ? add[static_cast<int64_t>(j) * p.C] : static_cast<uint16_t>(0);
-#pragma unroll
-            for (int j = 0; j < Cfg::kChunk; ++j)
-              v[j] = __float_as_uint(mm_widen(s[j], p.bf16) + __uint_as_float(v[j]));
-          }
-#pragma unroll
-          for (int j = 0; j < Cfg::kChunk; ++j)
-            if (j < n)
-              out[static_cast<int64_t>(j) * p.C] = mm_round16(__uint_as_float(v[j]), p.bf16);
+        const int32_t n = c.valid - j0;
+        if (in) {
+          if (Cfg::kGrad && p.out32)
+            mm_store<Cfg::kGrad>(static_cast<float*>(p.out) + at,
+                                 p.add == nullptr ? nullptr : static_cast<const float*>(p.add) + at,
+                                 p.C, n, v, true);
+          else
+            mm_store<Cfg::kGrad>(
+                static_cast<uint16_t*>(p.out) + at,
+                p.add == nullptr ? nullptr : static_cast<const uint16_t*>(p.add) + at, p.C, n, v,
+                p.bf16 != 0);
         }
       }
       if (any) {
