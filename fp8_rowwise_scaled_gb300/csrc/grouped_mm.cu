@@ -47,16 +47,16 @@ mslkb_status maps(const MmParams& p, CUtensorMap* tp, CUtensorMap* tq) {
     s = encode_map16(tp, p.P, 3, extent, stride, box);
   } else if constexpr (Cfg::kMode == Mm::kTurned) {
     const uint64_t extent[3] = {C, K, G}, stride[2] = {2 * C, 2 * K * C};
-    const uint32_t box[3] = {64, Cfg::kBK, 1};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(Cfg::kBK), 1};
     s = encode_map16(tp, p.P, 3, extent, stride, box);
   } else {
     const uint64_t extent[2] = {C, total};
-    const uint32_t box[2] = {64, Cfg::kBK};
+    const uint32_t box[2] = {64, static_cast<uint32_t>(Cfg::kBK)};
     s = encode_map16(tp, p.P, 2, extent, &ldp, box);
   }
   if (s != MSLKB_OK) return s;
   const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
-  const uint32_t box[2] = {64, Cfg::kGrad ? Cfg::kBK : Cfg::kBoxQ};
+  const uint32_t box[2] = {64, static_cast<uint32_t>(Cfg::kGrad ? Cfg::kBK : Cfg::kBoxQ)};
   return encode_map16(tq, p.Q, 2, extent, &ldq, box);
 }
 

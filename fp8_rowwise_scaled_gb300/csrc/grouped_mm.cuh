@@ -16,7 +16,8 @@
 // is persistent and specialised by warp:
 //   warps 0-3   TMA: warp 0 loads, warp 1 issues the MMAs, warp 2 zeroes what a stage holds past
 //               the end of an expert's rows (kGrad).  Without TMA (rows that are not 16-byte
-//               aligned): warps 0-7 load, through registers, and warp 8 issues the MMAs.
+//               aligned): warps 0-15 load, through registers, and warp 16 issues the
+//               MMAs.
 //   the last 4 or 8 warps: the epilogue, from one of two accumulators while the other fills.
 #pragma once
 
@@ -25,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kernel.cuh"
 #include "ptx.cuh"
@@ -70,15 +72,18 @@ struct MmCfg {
   static constexpr int kPBytes = 128 * kBK * 2;
   static constexpr int kQBytes = kQRows * kBK * 2;
   static constexpr int kStageBytes = kPBytes + kQBytes;
-  static constexpr int kLoaderWarps = kTma ? 1 : 8;
+  static constexpr int kLoaderWarps = kTma ? 1 : 16;
+  static constexpr int kWarpLines = 128 * kKB / 8;  // without TMA: of P or Q, by 8 warps each
   static constexpr int kMmaWarp = kLoaderWarps;
   static constexpr int kEdgeWarp = 2;
-  static constexpr int kEpiWarp0 = kTma ? 4 : 12;
+  static constexpr int kTileWarp = kTma ? 3 : 17;  // hands out the tiles
+  static constexpr int kEpiWarp0 = kTma ? 4 : 20;
   static constexpr int kEpiWarps = kEpiWarps_;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kRowStep = 16 * kCtas;      // a tile's rows are rounded up to these
   static constexpr int kTmemCols = 2 * kTileN < 32 ? 32 : 2 * kTileN;
-  static constexpr int kChunk = kTileN < 32 ? kTileN : 32;  // TMEM columns read at a time
+  // TMEM columns read at a time (fewer where the loader's warps leave 80 registers per thread)
+  static constexpr int kChunk = kTileN < 32 || (!kTma && kGrad) ? 16 : 32;
   // rows of tiles that run next to each other: 8 x 9.5 tiles of 256 x 256 on 76 CTA pairs read
   // the fewest bytes between them
   static constexpr int kBand = 8;
@@ -88,20 +93,26 @@ struct MmCfg {
 
   static constexpr int kOffP = 0;
   static constexpr int kOffQ = kStages * kPBytes;
-  static constexpr int kOffBar = kOffQ + kStages * kQBytes;
-  static constexpr int kNumBars = 4 * kStages + 4;
+  static constexpr int kStagePart = 8192;  // the epilogue's rows: 32 x 128 in 16 bits
+  static constexpr int kOffStage = kOffQ + kStages * kQBytes;
+  static constexpr int kOffBar = kOffStage + kEpiWarps / 4 * kStagePart;
+  // the scheduler warp hands tiles to the other roles through a ring
+  static constexpr int kRing = 4;
+  static constexpr int kRingUsers = kLoaderWarps + 1 + (kTma && kGrad ? 1 : 0) + kEpiWarps;
+  static constexpr int kNumBars = 4 * kStages + 4 + 2 * kRing;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
-  static constexpr int kOffSched = (kOffMisc + 8 + 15) / 16 * 16;
+  static constexpr int kOffRing = (kOffMisc + 8 + 15) / 16 * 16;
+  static constexpr int kOffSched = kOffRing + kRing * 32;
   static constexpr int kSmemBytes = kOffSched + 2 * 4 * (kMaxGroups + 1) + 1024;
 
   static_assert(kTileN % 16 == 0 && kTileN <= 256 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(!kQMn || kQRows % 64 == 0, "MN-major pieces of 64");
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(kTma || !kPair, "pairs load by TMA");
+  static_assert(kTma || (!kPair && kTileN == 128 && kKB == 1), "the warps' loader");
 };
 
-// A tile: its group, first output column and row, rows (h: rounded up, valid: real), and the
+// A tile: its group (-1: past the last tile), first output column and row, rows (h: rounded up, valid: real), and the
 // contraction [k0, k0 + len) (kGrad: rows of x and dy).
 struct MmTile {
   int32_t g, c0, r0, h, valid, k0, len;
@@ -199,29 +210,88 @@ __device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, i
   }
 }
 
-// A warp's share of 64 consecutive 16-bit elements at an address that is even only: aligned words,
-// each lane one, of which those of a row that starts inside a word are put together by
-// mm_join64.  Elements at or past `left` are zero, and nothing outside [0, left) is read.
-struct MmWords {
-  uint32_t v;      // the lane's aligned word
-  uint32_t last;   // lane 31: element 63, which lies in the next word of such a row
+// The warps' loader: a warp keeps kLines lines of a stage (64 elements of 16 bits each, at
+// addresses that are even only) in registers, lane l the l-th aligned 32-bit word of each.  Of a
+// line that starts inside a word, elements 2 l and 2 l + 1 lie in the words of lanes l and l + 1;
+// its first and last element, in words that reach out of it, are loaded by themselves, those of
+// all lines at once.  Loads are predicated, not branched around, so that all are under way
+// together (in branches they waited for each other: 16 K cycles a stage).
+template <int kLines>
+struct MmLines {
+  uint32_t v[kLines];
+  uint32_t ends;      // lanes u and 16 + u: elements 63 and 0 of line u, if it starts inside a word
+  uint32_t inside;    // bit u: line u starts inside a word
 };
-__device__ __forceinline__ MmWords mm_load64(const uint16_t* p, int32_t left, uint32_t lane) {
-  const int32_t s = static_cast<int32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
-  const int32_t e = 2 * static_cast<int32_t>(lane) - s;
-  MmWords w{0u, 0u};
-  if (e >= 0 && e + 1 < left) w.v = __ldg(reinterpret_cast<const uint32_t*>(p + e));
-  else if (e >= 0 && e < left) w.v = __ldg(p + e);
-  else if (e < 0 && e + 1 < left) w.v = static_cast<uint32_t>(__ldg(p + e + 1)) << 16;
-  if (s != 0 && lane == 31 && left > 63) w.last = __ldg(p + 63);
-  return w;
+
+__device__ __forceinline__ uint32_t mm_ldg32_if(const uint16_t* p, bool on) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0;\n\t"
+      "@p ld.global.nc.u32 %0, [%1];\n\t}"
+      : "=r"(v)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return v;
 }
-// Elements 2 * lane and 2 * lane + 1.
-__device__ __forceinline__ uint32_t mm_join64(const uint16_t* p, const MmWords& w, uint32_t lane) {
-  if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) return w.v;  // (the same for the whole warp)
-  uint32_t next = __shfl_down_sync(0xffffffffu, w.v, 1);
-  if (lane == 31) next = w.last;
-  return (w.v >> 16) | (next << 16);
+__device__ __forceinline__ uint32_t mm_ldg16_if(const uint16_t* p, bool on) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b16 h;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u16 h, 0;\n\t"
+      "@p ld.global.nc.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+      : "=r"(v)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return v;
+}
+
+// Lines at p, p + ld, ...: elements [0, left) of the first `lines` of them; the rest is zero and
+// nothing else is read.
+template <int kLines>
+__device__ __forceinline__ void mm_load_lines(MmLines<kLines>& w, const uint16_t* p, int64_t ld,
+                                              int32_t lines, int32_t left, uint32_t lane) {
+  static_assert(kLines == 16, "two ends of a line in the lanes of one register");
+  const uint32_t s0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 1u;
+  const uint32_t odd = static_cast<uint32_t>(ld) & 1u;
+  w.inside = 0u;
+#pragma unroll
+  for (int u = 0; u < kLines; ++u) {
+    const uint32_t s = s0 ^ ((u & 1) ? odd : 0u);
+    w.inside |= s << u;
+    const int32_t e = 2 * static_cast<int32_t>(lane) - static_cast<int32_t>(s);
+    w.v[u] = mm_ldg32_if(p + u * ld + e, u < lines && e >= 0 && e + 1 < left);
+  }
+  const int32_t mine = static_cast<int32_t>(lane & 15u);
+  const int32_t end = lane < 16 ? 63 : 0;
+  w.ends = mm_ldg16_if(p + mine * ld + end,
+                       ((w.inside >> mine) & 1u) != 0 && mine < lines && end < left);
+  if (left > 0 && left < 64) {
+    // the last element of a row that ends inside this line: where it is alone in its word
+#pragma unroll
+    for (int u = 0; u < kLines; ++u) {
+      const int32_t s = static_cast<int32_t>((w.inside >> u) & 1u);
+      const int32_t e = 2 * static_cast<int32_t>(lane) - s;
+      const uint32_t alone = mm_ldg16_if(p + u * ld + e, u < lines && e >= 0 && e + 1 == left);
+      w.v[u] |= alone;
+    }
+  }
+}
+
+// The lines into a stage's operand from its line `line0` on, swizzled.
+template <int kLines>
+__device__ __forceinline__ void mm_store_lines(const MmLines<kLines>& w, uint32_t dst,
+                                               uint32_t line0, uint32_t lane) {
+#pragma unroll
+  for (int u = 0; u < kLines; ++u) {
+    uint32_t v = w.v[u];
+    if ((w.inside >> u) & 1u) {  // (the same for the whole warp)
+      uint32_t next = __shfl_down_sync(0xffffffffu, v, 1);
+      const uint32_t end = __shfl_sync(0xffffffffu, w.ends, lane < 31 ? u + 16 : u);
+      if (lane == 31) next = end;
+      const uint32_t lo = lane == 0 ? end : v >> 16;
+      v = lo | (next << 16);
+    }
+    const uint32_t line = line0 + static_cast<uint32_t>(u);
+    ptx::st_shared_u32(dst + line * 128u + (((lane >> 2) ^ (line & 7u)) << 4) + (lane & 3u) * 4u,
+                       v);
+  }
 }
 
 // kind::f16 MMA, fp32 accumulator: D (+)= P * Q^T.  Instruction descriptor: bits 4-5 D format
@@ -271,36 +341,134 @@ __device__ __forceinline__ float mm_widen(uint16_t v, bool bf16) {
   return bf16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
 }
 
-__device__ __forceinline__ void mm_put(float* o, float v, bool) { *o = v; }
-__device__ __forceinline__ void mm_put(uint16_t* o, float v, bool bf16) { *o = mm_round16(v, bf16); }
-__device__ __forceinline__ float mm_get(const float* a, bool) { return *a; }
-__device__ __forceinline__ float mm_get(const uint16_t* a, bool bf16) { return mm_widen(*a, bf16); }
-
-// One column of up to kN output rows, C elements apart: v + add (null: nothing) for the first n.
-// The addresses are one running pointer: computed ahead they would take two registers each.
-template <bool kMayAdd, class T, int kN>
-__device__ __forceinline__ void mm_store(T* out, const T* add, int32_t C, int32_t n,
-                                         uint32_t (&v)[kN], bool bf16) {
-  if (kMayAdd && add != nullptr) {
-    float s[kN];
-    if (n >= kN) {
+// f(row, pointer to it) for rows 0 .. kN - 1, C elements apart.  Four running pointers: computed
+// ahead, addresses would take two registers each, and a single one makes every row wait for the
+// 64-bit addition of the row before.
+template <int kN, class T, class F>
+__device__ __forceinline__ void mm_rows(T* p, int32_t C, F f) {
+  T* r[4];
 #pragma unroll
-      for (int j = 0; j < kN; ++j, add += C) s[j] = mm_get(add, bf16);
-    } else {
+  for (int i = 0; i < 4; ++i) r[i] = p + static_cast<int64_t>(i) * C;
+  const int64_t step = 4 * static_cast<int64_t>(C);
 #pragma unroll
-      for (int j = 0; j < kN; ++j, add += C) s[j] = j < n ? mm_get(add, bf16) : 0.0f;
+  for (int j = 0; j < kN; j += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f(j + i, r[i]);
+      r[i] += step;
     }
-#pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = __float_as_uint(s[j] + __uint_as_float(v[j]));
   }
-  if (n >= kN) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j, out += C) mm_put(out, __uint_as_float(v[j]), bf16);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kN; ++j, out += C)
-      if (j < n) mm_put(out, __uint_as_float(v[j]), bf16);
+}
+
+// The epilogue's chunk of a tile: a warp's 32 output columns (one per lane) of kN output rows, C
+// elements apart, of which n are there.  load_add reads what is added to them, ahead of the
+// sums; store adds it, rounds and stores.
+template <class T, int kN>
+struct MmChunk {
+  T a[kN];
+  __device__ __forceinline__ void load_add(const T* add, int32_t C, int32_t n, bool in) {
+    if (!in) n = 0;
+    mm_rows<kN>(add, C, [&](int j, const T* p) { a[j] = j < n ? *p : T(0); });
   }
+  template <bool kAdd>
+  __device__ __forceinline__ void store(T* out, int32_t C, int32_t n, bool in,
+                                        const uint32_t (&v)[kN], bool bf16, uint32_t) {
+    auto put = [&](int j, T* to) {
+      float f = __uint_as_float(v[j]);
+      if constexpr (sizeof(T) == 4) {
+        if (kAdd) f = a[j] + f;
+        *to = f;
+      } else {
+        if (kAdd) f = mm_widen(a[j], bf16) + f;
+        *to = mm_round16(f, bf16);
+      }
+    };
+    if (!in) return;
+    if (n >= kN) mm_rows<kN>(out, C, put);
+    else mm_rows<kN>(out, C, [&](int j, T* to) { if (j < n) put(j, to); });
+  }
+};
+
+// 16-bit results in rows of whole, aligned eights: four warps put their 128 columns of some rows
+// side by side in shared memory, and each then stores whole rows, 256 bytes at a time.  (A warp by
+// itself has 64 bytes of a row, and a store of half a line costs the L2 what one of a line does:
+// weights' gradient of 256 rows, 32 x 4096 x 7168 bf16 on GB300 524 us so, 3.6 TB/s.)  kAdd: what
+// is added comes the same way, 8 bytes a lane, and the rows lie in shared memory in fp32.
+template <int kN>
+struct MmRows {
+  uint2 a[kN / 4];
+  // `add`: the tile's first row and column; this warp's rows are `which`, `which` + 4, ...
+  __device__ __forceinline__ void load_add(const uint16_t* add, int32_t C, int32_t n, int32_t cols,
+                                           int32_t which, uint32_t lane) {
+    const bool in = static_cast<int32_t>(lane) * 4 < cols;
+    add += static_cast<int64_t>(which) * C + lane * 4u;
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i, add += 4 * static_cast<int64_t>(C))
+      a[i] = in && which + 4 * i < n ? *reinterpret_cast<const uint2*>(add) : make_uint2(0u, 0u);
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi, bool bf16) {
+    if (bf16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  // stage: shared memory of these four warps; bar: their barrier
+  template <bool kAdd>
+  __device__ __forceinline__ void store(uint16_t* out, int32_t C, int32_t n, int32_t cols,
+                                        int32_t which, const uint32_t (&v)[kN], bool bf16,
+                                        uint8_t* stage, uint32_t bar, uint32_t lane) {
+    const uint32_t col = static_cast<uint32_t>(which) * 32u + lane;
+    ptx::named_bar_sync(bar, 128);  // the rows before these have been read
+    if constexpr (kAdd) {
+      float* s = reinterpret_cast<float*>(stage) + col;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) s[j * 128] = __uint_as_float(v[j]);
+    } else {
+      uint16_t* s = reinterpret_cast<uint16_t*>(stage) + col;
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        const uint32_t two = pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), bf16);
+        s[j * 128] = static_cast<uint16_t>(two);
+        s[(j + 1) * 128] = static_cast<uint16_t>(two >> 16);
+      }
+    }
+    ptx::named_bar_sync(bar, 128);
+    if constexpr (kAdd) {
+      out += static_cast<int64_t>(which) * C + lane * 4u;
+      const bool in = static_cast<int32_t>(lane) * 4 < cols;
+#pragma unroll
+      for (int i = 0; i < kN / 4; ++i, out += 4 * static_cast<int64_t>(C)) {
+        const float4 f = reinterpret_cast<const float4*>(stage)[(which + 4 * i) * 32 + lane];
+        auto get = [&](uint32_t w) { return mm_widen(static_cast<uint16_t>(w), bf16); };
+        const uint32_t lo = pack(get(a[i].x) + f.x, get(a[i].x >> 16) + f.y, bf16);
+        const uint32_t hi = pack(get(a[i].y) + f.z, get(a[i].y >> 16) + f.w, bf16);
+        if (in && which + 4 * i < n) *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+      }
+    } else {
+      const int32_t row = which * 2 + static_cast<int32_t>(lane >> 4);
+      out += static_cast<int64_t>(row) * C + (lane & 15u) * 8u;
+      const bool in = static_cast<int32_t>(lane & 15u) * 8 < cols;
+#pragma unroll
+      for (int i = 0; i < kN / 8; ++i, out += 8 * static_cast<int64_t>(C)) {
+        const uint4 w = reinterpret_cast<const uint4*>(stage)[(row + 8 * i) * 16 + (lane & 15u)];
+        if (in && row + 8 * i < n) *reinterpret_cast<uint4*>(out) = w;
+      }
+    }
+  }
+};
+
+// Whether `ok` holds in all 128 threads at a barrier.
+__device__ __forceinline__ bool named_bar_and(uint32_t id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(ok)), "r"(id)
+      : "memory");
+  return all != 0;
 }
 
 template <class Cfg>
@@ -319,6 +487,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   auto tempty_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + 2 + b); };
   auto edge_bar = [&](int s) { return s_bar + 8u * (2 * Cfg::kStages + 4 + s); };
   auto peer_bar = [&](int s) { return s_bar + 8u * (3 * Cfg::kStages + 4 + s); };
+  auto tile_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + i); };
+  auto taken_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + Cfg::kRing + i); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 4);
   int32_t* first = reinterpret_cast<int32_t*>(smem + Cfg::kOffSched);
@@ -339,6 +509,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(tfull_bar(b), 1u);
       ptx::mbar_init(tempty_bar(b), static_cast<uint32_t>(Cfg::kEpiWarps * Cfg::kCtas));
+    }
+    for (int i = 0; i < Cfg::kRing; ++i) {
+      ptx::mbar_init(tile_bar(i), 1u);
+      // (a pair's second CTA issues no MMAs)
+      ptx::mbar_init(taken_bar(i), static_cast<uint32_t>(Cfg::kRingUsers) - (crank != 0 ? 1u : 0u));
     }
     *abort_flag = 0u;
     ptx::fence_mbar_init();
@@ -367,15 +542,31 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
   const int32_t tiles = tile_pre[p.G];
 
+  // Tile i of this CTA (or pair), from the ring: by a whole warp, or by one lane of it.  False past
+  // the last one, or if a wait gave up.
+  int4* ring = reinterpret_cast<int4*>(smem + Cfg::kOffRing);
+  auto take = [&](int32_t i, MmTile& c, bool whole_warp) -> bool {
+    const int slot = i % Cfg::kRing;
+    bool ok = wait_bar(tile_bar(slot), static_cast<uint32_t>(i / Cfg::kRing) & 1u, abort_flag,
+                       p.status, p.timeout_ns);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok) != 0;
+    if (!ok) return false;
+    const int4 a = ring[2 * slot], b = ring[2 * slot + 1];
+    c = MmTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) ptx::mbar_arrive(taken_bar(slot));
+    return c.g >= 0;
+  };
+
   if (Cfg::kTma && warp == 0) {
     // -------------------------------------------------------------- loads by TMA
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int32_t t = worker; ok && t < tiles; t += workers) {
-        const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
-        if (c.h == 0 || c.len == 0) continue;
+      MmTile c;
+      for (int32_t i = 0; ok && take(i, c, false); ++i) {
+        if (c.len == 0) continue;
         const int32_t col = c.c0 + static_cast<int32_t>(crank) * 128;
         const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
         const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
@@ -445,55 +636,56 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (!Cfg::kTma && warp < Cfg::kLoaderWarps) {
+  } else if (!Cfg::kTma && warp < static_cast<uint32_t>(Cfg::kLoaderWarps)) {
     // -------------------------------------------------------------- loads through registers
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int32_t t = worker; ok && t < tiles; t += workers) {
-      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
-      if (c.h == 0 || c.len == 0) continue;
-      const uint16_t* w =
-          Cfg::kGrad ? p.P : p.P + static_cast<int64_t>(c.g) * p.C * p.K;
-      const int64_t ldp = Cfg::kGrad ? p.ldp : (Cfg::kPMn ? p.C : p.K);
-      for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+    if constexpr (!Cfg::kTma) {
+      // Half of the warps for P, half for Q; each loads its lines of the next stage before it
+      // stores those of this one, so that a load's latency passes while others are stored.
+      constexpr int kLines = Cfg::kWarpLines;
+      const bool is_q = warp >= Cfg::kLoaderWarps / 2;
+      const bool mn = is_q ? Cfg::kQMn : Cfg::kPMn;
+      const uint32_t line0 = (warp % (Cfg::kLoaderWarps / 2)) * kLines;
+      MmTile c{};
+      int32_t i = 0, k = 0;
+      auto next_stage = [&]() -> bool {  // the next stage of this tile, or the next tile
+        k += Cfg::kBK;
+        if (k < c.len) return true;
+        k = 0;
+        do {
+          if (!take(i++, c, true)) return false;
+        } while (c.len == 0);
+        return true;
+      };
+      auto load = [&](MmLines<kLines>& w) {
+        // K-major: lines are rows of the operand; MN-major: contracted rows, in pieces of 64
+        const uint16_t* base = is_q ? p.Q : (Cfg::kGrad ? p.P : p.P + static_cast<int64_t>(c.g) *
+                                                                           p.C * p.K);
+        const int64_t ld = is_q ? p.ldq : (Cfg::kGrad ? p.ldp : (Cfg::kPMn ? p.C : p.K));
+        const int32_t from = is_q ? c.r0 : c.c0;
+        const int32_t end = is_q ? (Cfg::kGrad ? p.R : c.r0 + c.valid) : p.C;
+        // (a warp's lines lie one row apart, in one piece)
+        const int32_t l0 = static_cast<int32_t>(line0);
+        const int32_t row = mn ? k + l0 % Cfg::kBK : from + l0;
+        const int32_t e = mn ? from + l0 / Cfg::kBK * 64 : k;
+        mm_load_lines<kLines>(
+            w, base + static_cast<int64_t>(mn ? c.k0 + row : row) * ld + (mn ? e : c.k0 + e), ld,
+            (mn ? c.len : end) - row, (mn ? end : c.len) - e, lane);
+      };
+      const uint32_t dst0 = is_q ? s_q : s_p;
+      const uint32_t bytes = is_q ? Cfg::kQBytes : Cfg::kPBytes;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      MmLines<kLines> now, ahead;
+      bool more = next_stage();
+      if (more) load(now);
+      while (more) {
+        more = next_stage();
+        if (more) load(ahead);
         ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
                                               p.timeout_ns));
         if (!ok) break;
-        // 64 elements along the operand's rows at a time, eight such pieces under way per warp;
-        // in shared memory the 16-byte parts of a piece are swizzled by its line.  K-major:
-        // `tile` lines from row `at` on; MN-major: a line per contracted row, `tile` elements
-        // from `at` on
-        auto fill = [&](uint32_t dst, const uint16_t* base, int64_t ld, bool mn, int32_t tile,
-                        int32_t at, int32_t end) {
-          const int32_t lines = mn ? Cfg::kBK : tile, pieces = (mn ? tile : Cfg::kBK) / 64;
-          constexpr int kBatch = 8;
-          for (int32_t i0 = static_cast<int32_t>(warp) * kBatch; i0 < lines * pieces;
-               i0 += Cfg::kLoaderWarps * kBatch) {
-            MmWords v[kBatch];
-            const uint16_t* from[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              const int32_t r = (i0 + u) % lines, piece = (i0 + u) / lines;
-              const int32_t row = mn ? k + r : at + r;
-              const int32_t e = (mn ? at : k) + piece * 64;
-              const int32_t left = row < (mn ? c.len : end) ? (mn ? end : c.len) - e : 0;
-              from[u] = base + static_cast<int64_t>(mn ? c.k0 + row : row) * ld +
-                        (mn ? e : c.k0 + e);
-              v[u] = mm_load64(from[u], left, lane);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-              const uint32_t line = static_cast<uint32_t>(i0 + u);
-              ptx::st_shared_u32(dst + line * 128u + (((lane >> 2) ^ (line & 7u)) << 4) +
-                                     (lane & 3u) * 4u,
-                                 mm_join64(from[u], v[u], lane));
-            }
-          }
-        };
-        fill(s_p + stage * Cfg::kPBytes, w, ldp, Cfg::kPMn, 128, c.c0, p.C);
-        fill(s_q + stage * Cfg::kQBytes, p.Q, p.ldq, Cfg::kQMn, Cfg::kQRows, c.r0,
-             Cfg::kGrad ? p.R : c.r0 + c.valid);
+        mm_store_lines<kLines>(now, dst0 + static_cast<uint32_t>(stage) * bytes, line0, lane);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(full_bar(stage));
@@ -501,16 +693,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           stage = 0;
           phase ^= 1u;
         }
+        now = ahead;
       }
-    }
-    for (int i = 0; ok && threadIdx.x == 0 && i < Cfg::kStages; ++i) {
-      ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
-      if (++stage == Cfg::kStages) {
-        stage = 0;
-        phase ^= 1u;
+      for (int i = 0; ok && threadIdx.x == 0 && i < Cfg::kStages; ++i) {
+        ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp == Cfg::kMmaWarp) {
     // -------------------------------------------------------------- MMAs
     if (lane == 0 && crank == 0) {
@@ -519,9 +712,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       bool ok = true;
       const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
       const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
-      for (int32_t t = worker; ok && t < tiles; t += workers) {
-        const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
-        if (c.h == 0 || c.len == 0) continue;
+      MmTile c;
+      for (int32_t i = 0; ok && take(i, c, false); ++i) {
+        if (c.len == 0) continue;
         const uint32_t idesc = mm_idesc<Cfg>(p.bf16, c.h);
         const int b = static_cast<int>(used & 1u);
         if (!wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag, p.status,
@@ -568,9 +761,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // NaN is NaN): whole 128-byte lines here, since the rows are the operands' lines.
     int stage = 0;
     uint32_t parity = 0;  // of each stage's edge barrier, one bit
-    for (int32_t t = worker; t < tiles; t += workers) {
-      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
-      if (c.h == 0 || c.len == 0) continue;
+    MmTile c;
+    for (int32_t i = 0; take(i, c, true); ++i) {
+      if (c.len == 0) continue;
       const int32_t kbs = (c.len + Cfg::kBK - 1) / Cfg::kBK;
       const int last = (stage + kbs - 1) % Cfg::kStages;
       stage = (stage + kbs) % Cfg::kStages;
@@ -603,64 +796,133 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(full_bar(last));
       }
     }
+  } else if (warp == static_cast<uint32_t>(Cfg::kTileWarp)) {
+    // -------------------------------------------------------------- tiles
+    // 32 tiles are worked out at a time, one by each lane (a search and four divisions), and
+    // handed on one after the other.
+    int32_t i = 0;
+    bool ok = true;
+    for (int64_t t0 = worker; ok; t0 += 32ll * workers) {
+      const int64_t t = t0 + static_cast<int64_t>(lane) * workers;
+      MmTile c{-1, 0, 0, 0, 0, 0, 0};
+      if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
+      const bool more = t0 + 31ll * workers < tiles;   // (else the last of these says so)
+      // tiles of rounded heights past a group's last row have no rows
+      uint32_t left = __ballot_sync(0xffffffffu, c.g < 0 || c.h > 0);
+      if (!more) left &= (2u << (__ffs(__ballot_sync(0xffffffffu, c.g < 0)) - 1)) - 1u;
+      while (left != 0) {
+        const int src = __ffs(left) - 1;
+        left &= left - 1;
+        const int slot = i % Cfg::kRing;
+        ok = __all_sync(0xffffffffu,
+                        wait_bar(taken_bar(slot), (static_cast<uint32_t>(i / Cfg::kRing) & 1u) ^ 1u,
+                                 abort_flag, p.status, p.timeout_ns)) != 0;
+        if (!ok) break;
+        if (static_cast<int>(lane) == src) {
+          ring[2 * slot] = make_int4(c.g, c.c0, c.r0, c.h);
+          ring[2 * slot + 1] = make_int4(c.valid, c.k0, c.len, 0);
+          ptx::mbar_arrive(tile_bar(slot));
+        }
+        __syncwarp();
+        ++i;
+      }
+      if (!more) break;
+    }
   } else if (warp >= Cfg::kEpiWarp0) {
     // -------------------------------------------------------------- epilogue
     const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
-    constexpr int kParts = Cfg::kEpiWarps / 4;
-    uint32_t used = 0;
-    for (int32_t t = worker; t < tiles; t += workers) {
-      const MmTile c = mm_tile<Cfg>(p, first, tile_pre, t);
-      if (c.h == 0) continue;
-      const bool any = c.len > 0;  // else the empty sum
-      const uint32_t b = used & 1u;
-      if (any) {
-        const bool ok =
-            wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
-                     p.timeout_ns);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        ++used;
-        ptx::tc_fence_after_sync();
-      }
-      const int32_t col = c.c0 + static_cast<int32_t>(crank * 128u + q * 32u + lane);
-      const bool in = col < p.C;
-      const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
-      for (int32_t j0 = static_cast<int32_t>(part) * Cfg::kChunk; j0 < c.valid;
-           j0 += kParts * Cfg::kChunk) {
-        uint32_t v[Cfg::kChunk];
+    uint8_t* stage = smem + Cfg::kOffStage + part * Cfg::kStagePart;
+    const uint32_t bar = 1u + part;  // of this part's four warps
+    auto work = [&](auto chunk, auto* out0, auto may_add, auto rows) {
+      using T = std::remove_pointer_t<decltype(out0)>;
+      constexpr bool kAdd = decltype(may_add)::value;
+      constexpr int kN = decltype(rows)::value, kStep = Cfg::kEpiWarps / 4 * kN;
+      constexpr bool kWhole = std::is_same_v<decltype(chunk), MmRows<kN>>;
+      const T* add0 = static_cast<const T*>(p.add);
+      const bool bf16 = p.bf16 != 0;
+      uint32_t used = 0;
+      MmTile c;
+      for (int32_t i = 0;; ++i) {
+        bool ok = take(i, c, true);
+        const int32_t col0 = c.c0 + static_cast<int32_t>(crank) * 128;
+        const int32_t col = col0 + (kWhole ? 0 : static_cast<int32_t>(q * 32u + lane));
+        const bool in = col < p.C;
+        const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
+        int32_t j0 = static_cast<int32_t>(part) * kN;
+        int64_t at = (row0 + j0) * p.C + col;
+        auto load_add = [&](int64_t from, int32_t n) {
+          if constexpr (kWhole)
+            chunk.load_add(add0 + from, p.C, n, p.C - col0, static_cast<int32_t>(q), lane);
+          else
+            chunk.load_add(add0 + from, p.C, n, in);
+        };
+        if constexpr (kAdd) {
+          if (ok) load_add(at, c.valid - j0);
+        }
+        const bool any = ok && c.len > 0;  // else the empty sum
+        const uint32_t b = used & 1u;
         if (any) {
-          const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
-                                ((q * 32u) << 16);
-          if constexpr (Cfg::kChunk == 32) ptx::tmem_ld_x32(from, v);
-          else ptx::tmem_ld_x16(from, v);
-          ptx::tmem_ld_wait();
-        } else {
+          ok = wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
+                        p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          ++used;
+          ptx::tc_fence_after_sync();
+        }
+        if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
+        if (!ok) break;
+        for (; j0 < c.valid; j0 += kStep, at += static_cast<int64_t>(kStep) * p.C) {
+          uint32_t v[kN];
+          if (any) {
+            const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
+                                  ((q * 32u) << 16);
+            if constexpr (kN == 32) ptx::tmem_ld_x32(from, v);
+            else ptx::tmem_ld_x16(from, v);
+            ptx::tmem_ld_wait();
+          } else {
 #pragma unroll
-          for (int j = 0; j < Cfg::kChunk; ++j) v[j] = 0u;
-        }
-        const int64_t at = (row0 + j0) * p.C + col;
-        const int32_t n = c.valid - j0;
-        if (in) {
-          if (Cfg::kGrad && p.out32)
-            mm_store<Cfg::kGrad>(static_cast<float*>(p.out) + at,
-                                 p.add == nullptr ? nullptr : static_cast<const float*>(p.add) + at,
-                                 p.C, n, v, true);
+            for (int j = 0; j < kN; ++j) v[j] = 0u;
+          }
+          auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
+          const int32_t n = c.valid - j0;
+          if constexpr (kAdd) {
+            if (n > kStep) load_add(at + static_cast<int64_t>(kStep) * p.C, n - kStep);
+          }
+          if constexpr (kWhole)
+            now.template store<kAdd>(out0 + at, p.C, n, p.C - col0, static_cast<int32_t>(q), v,
+                                     bf16, stage, bar, lane);
           else
-            mm_store<Cfg::kGrad>(
-                static_cast<uint16_t*>(p.out) + at,
-                p.add == nullptr ? nullptr : static_cast<const uint16_t*>(p.add) + at, p.C, n, v,
-                p.bf16 != 0);
+            now.template store<kAdd>(out0 + at, p.C, n, in, v, bf16, lane);
+        }
+        if (any) {
+          ptx::tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (Cfg::kPair && crank != 0)
+              ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(static_cast<int>(b)), 0u));
+            else
+              ptx::mbar_arrive(tempty_bar(static_cast<int>(b)));
+          }
         }
       }
-      if (any) {
-        ptx::tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (Cfg::kPair && crank != 0)
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(static_cast<int>(b)), 0u));
-          else
-            ptx::mbar_arrive(tempty_bar(static_cast<int>(b)));
-        }
-      }
+    };
+    auto by_type = [&](auto may_add) {
+      using Rows = std::integral_constant<int, Cfg::kChunk>;
+      constexpr int kWide = decltype(may_add)::value ? 16 : Cfg::kChunk;
+      const bool whole = p.C % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 &&
+                         (reinterpret_cast<uintptr_t>(p.add) & 7) == 0;
+      if (Cfg::kGrad && p.out32)
+        work(MmChunk<float, Cfg::kChunk>{}, static_cast<float*>(p.out), may_add, Rows{});
+      else if (whole)
+        work(MmRows<kWide>{}, static_cast<uint16_t*>(p.out), may_add,
+             std::integral_constant<int, kWide>{});
+      else
+        work(MmChunk<uint16_t, Cfg::kChunk>{}, static_cast<uint16_t*>(p.out), may_add, Rows{});
+    };
+    if constexpr (Cfg::kGrad) {
+      if (p.add != nullptr) by_type(std::true_type{});
+      else by_type(std::false_type{});
+    } else {
+      by_type(std::false_type{});
     }
   }
 
