@@ -418,20 +418,18 @@ struct MmRows {
   template <bool kAdd>
   __device__ __forceinline__ void store(uint16_t* out, int32_t C, int32_t n, int32_t cols,
                                         int32_t which, const uint32_t (&v)[kN], bool bf16,
-                                        uint8_t* stage, uint32_t bar, uint32_t lane) {
+                                        uint32_t stage, uint32_t bar, uint32_t lane) {
     const uint32_t col = static_cast<uint32_t>(which) * 32u + lane;
     ptx::named_bar_sync(bar, 128);  // the rows before these have been read
     if constexpr (kAdd) {
-      float* s = reinterpret_cast<float*>(stage) + col;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) s[j * 128] = __uint_as_float(v[j]);
+      for (int j = 0; j < kN; ++j) ptx::st_shared_u32(stage + col * 4u + j * 512u, v[j]);
     } else {
-      uint16_t* s = reinterpret_cast<uint16_t*>(stage) + col;
 #pragma unroll
       for (int j = 0; j < kN; j += 2) {
         const uint32_t two = pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), bf16);
-        s[j * 128] = static_cast<uint16_t>(two);
-        s[(j + 1) * 128] = static_cast<uint16_t>(two >> 16);
+        ptx::st_shared_u16(stage + col * 2u + j * 256u, static_cast<uint16_t>(two));
+        ptx::st_shared_u16(stage + col * 2u + (j + 1) * 256u, static_cast<uint16_t>(two >> 16));
       }
     }
     ptx::named_bar_sync(bar, 128);
@@ -440,10 +438,12 @@ struct MmRows {
       const bool in = static_cast<int32_t>(lane) * 4 < cols;
 #pragma unroll
       for (int i = 0; i < kN / 4; ++i, out += 4 * static_cast<int64_t>(C)) {
-        const float4 f = reinterpret_cast<const float4*>(stage)[(which + 4 * i) * 32 + lane];
+        const uint4 f = ptx::ld_shared_v4(stage + (which + 4 * i) * 512u + lane * 16u);
         auto get = [&](uint32_t w) { return mm_widen(static_cast<uint16_t>(w), bf16); };
-        const uint32_t lo = pack(get(a[i].x) + f.x, get(a[i].x >> 16) + f.y, bf16);
-        const uint32_t hi = pack(get(a[i].y) + f.z, get(a[i].y >> 16) + f.w, bf16);
+        const uint32_t lo = pack(get(a[i].x) + __uint_as_float(f.x),
+                                 get(a[i].x >> 16) + __uint_as_float(f.y), bf16);
+        const uint32_t hi = pack(get(a[i].y) + __uint_as_float(f.z),
+                                 get(a[i].y >> 16) + __uint_as_float(f.w), bf16);
         if (in && which + 4 * i < n) *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
       }
     } else {
@@ -452,7 +452,7 @@ struct MmRows {
       const bool in = static_cast<int32_t>(lane & 15u) * 8 < cols;
 #pragma unroll
       for (int i = 0; i < kN / 8; ++i, out += 8 * static_cast<int64_t>(C)) {
-        const uint4 w = reinterpret_cast<const uint4*>(stage)[(row + 8 * i) * 16 + (lane & 15u)];
+        const uint4 w = ptx::ld_shared_v4(stage + (row + 8 * i) * 256u + (lane & 15u) * 16u);
         if (in && row + 8 * i < n) *reinterpret_cast<uint4*>(out) = w;
       }
     }
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(tfull_bar(b), 1u);
-      ptx::mbar_init(tempty_bar(b), static_cast<uint32_t>(Cfg::kEpiWarps * Cfg::kCtas));
+      ptx::mbar_init(tempty_bar(b), static_cast<uint32_t>(4 * Cfg::kCtas));
     }
     for (int i = 0; i < Cfg::kRing; ++i) {
       ptx::mbar_init(tile_bar(i), 1u);
@@ -830,13 +830,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     }
   } else if (warp >= Cfg::kEpiWarp0) {
     // -------------------------------------------------------------- epilogue
+    // Four warps for a tile, one for each quarter of the TMEM lanes.  Eight warps take turns: while
+    // four store a tile the others wait for the sums of the next (all eight at one tile: 622 us
+    // where the stores alone are 430, 32 x 64 rows, 4096 x 7168 fp32).
     const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
-    uint8_t* stage = smem + Cfg::kOffStage + part * Cfg::kStagePart;
+    constexpr uint32_t kParts = Cfg::kEpiWarps / 4;
+    const uint32_t stage = ptx::smem_addr(smem + Cfg::kOffStage) + part * Cfg::kStagePart;
     const uint32_t bar = 1u + part;  // of this part's four warps
     auto work = [&](auto chunk, auto* out0, auto may_add, auto rows) {
       using T = std::remove_pointer_t<decltype(out0)>;
       constexpr bool kAdd = decltype(may_add)::value;
-      constexpr int kN = decltype(rows)::value, kStep = Cfg::kEpiWarps / 4 * kN;
+      constexpr int kN = decltype(rows)::value;
       constexpr bool kWhole = std::is_same_v<decltype(chunk), MmRows<kN>>;
       const T* add0 = static_cast<const T*>(p.add);
       const bool bf16 = p.bf16 != 0;
@@ -848,29 +852,31 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col = col0 + (kWhole ? 0 : static_cast<int32_t>(q * 32u + lane));
         const bool in = col < p.C;
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
-        int32_t j0 = static_cast<int32_t>(part) * kN;
-        int64_t at = (row0 + j0) * p.C + col;
+        int32_t j0 = 0;
+        int64_t at = row0 * p.C + col;
         auto load_add = [&](int64_t from, int32_t n) {
           if constexpr (kWhole)
             chunk.load_add(add0 + from, p.C, n, p.C - col0, static_cast<int32_t>(q), lane);
           else
             chunk.load_add(add0 + from, p.C, n, in);
         };
-        if constexpr (kAdd) {
-          if (ok) load_add(at, c.valid - j0);
-        }
         const bool any = ok && c.len > 0;  // else the empty sum
         const uint32_t b = used & 1u;
-        if (any) {
+        const bool mine = kParts == 1 || (any ? b : static_cast<uint32_t>(i) & 1u) == part;
+        if constexpr (kAdd) {
+          if (ok && mine) load_add(at, c.valid);
+        }
+        if (any && mine) {
           ok = wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
                         p.timeout_ns);
           ok = __all_sync(0xffffffffu, ok) != 0;
-          ++used;
           ptx::tc_fence_after_sync();
         }
         if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
         if (!ok) break;
-        for (; j0 < c.valid; j0 += kStep, at += static_cast<int64_t>(kStep) * p.C) {
+        used += any ? 1u : 0u;
+        if (!mine) continue;
+        for (; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
           uint32_t v[kN];
           if (any) {
             const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
@@ -885,7 +891,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
           const int32_t n = c.valid - j0;
           if constexpr (kAdd) {
-            if (n > kStep) load_add(at + static_cast<int64_t>(kStep) * p.C, n - kStep);
+            if (n > kN) load_add(at + static_cast<int64_t>(kN) * p.C, n - kN);
           }
           if constexpr (kWhole)
             now.template store<kAdd>(out0 + at, p.C, n, p.C - col0, static_cast<int32_t>(q), v,
