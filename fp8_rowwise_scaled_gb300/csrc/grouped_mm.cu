@@ -21,8 +21,7 @@ int64_t tiles_bound(const MmParams& p) {
 }
 
 template <class Cfg>
-mslkb_status launch(const MmParams& p, const CUtensorMap& tp, const CUtensorMap& tq, int sms,
-                    void* stream) {
+mslkb_status launch(const MmParams& p, const CUtensorMap (&maps)[3], int sms, void* stream) {
   cudaError_t e = allow_smem<grouped_mm_kernel<Cfg>>();
   if (e != cudaSuccess) return launch_status(e);
   const int64_t tiles = tiles_bound<Cfg>(p);
@@ -31,55 +30,73 @@ mslkb_status launch(const MmParams& p, const CUtensorMap& tp, const CUtensorMap&
   const int64_t grid = (tiles < workers ? tiles : workers) * Cfg::kCtas;
   return launch_status(launch_cluster(grouped_mm_kernel<Cfg>, dim3(static_cast<unsigned>(grid)),
                                       dim3(Cfg::kThreads), Cfg::kSmemBytes, Cfg::kCtas, stream, p,
-                                      tp, tq));
+                                      maps[0], maps[1], maps[2]));
 }
 
-// Tensor maps of P and Q.  Matrices of experts have three dimensions, so that what lies past one
-// is read as zero and not as the next.
+// Tensor maps of P, Q and what is added.  Matrices of experts have three dimensions, so that what
+// lies past one is read as zero and not as the next.
 template <class Cfg>
-mslkb_status maps(const MmParams& p, CUtensorMap* tp, CUtensorMap* tq) {
+mslkb_status encode(const MmParams& p, CUtensorMap (&maps)[3]) {
   const uint64_t C = p.C, K = p.K, G = p.G, total = p.total, R = p.R;
   const uint64_t ldp = 2 * p.ldp, ldq = 2 * p.ldq;
+  const uint32_t kbk = Cfg::kBK;
   mslkb_status s;
   if constexpr (Cfg::kMode == Mm::kRows) {
     const uint64_t extent[3] = {K, C, G}, stride[2] = {2 * K, 2 * K * C};
     const uint32_t box[3] = {64, 128, 1};
-    s = encode_map16(tp, p.P, 3, extent, stride, box);
+    s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
   } else if constexpr (Cfg::kMode == Mm::kTurned) {
     const uint64_t extent[3] = {C, K, G}, stride[2] = {2 * C, 2 * K * C};
-    const uint32_t box[3] = {64, static_cast<uint32_t>(Cfg::kBK), 1};
-    s = encode_map16(tp, p.P, 3, extent, stride, box);
+    const uint32_t box[3] = {64, kbk, 1};
+    s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
   } else {
     const uint64_t extent[2] = {C, total};
-    const uint32_t box[2] = {64, static_cast<uint32_t>(Cfg::kBK)};
-    s = encode_map16(tp, p.P, 2, extent, &ldp, box);
+    const uint32_t box[2] = {64, kbk};
+    s = encode_map16(&maps[0], p.P, 2, extent, &ldp, box);
   }
-  if (s != MSLKB_OK) return s;
-  const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
-  const uint32_t box[2] = {64, static_cast<uint32_t>(Cfg::kGrad ? Cfg::kBK : Cfg::kBoxQ)};
-  return encode_map16(tq, p.Q, 2, extent, &ldq, box);
+  if (s == MSLKB_OK) {
+    const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
+    const uint32_t box[2] = {64, Cfg::kGrad ? kbk : static_cast<uint32_t>(Cfg::kBoxQ)};
+    s = encode_map16(&maps[1], p.Q, 2, extent, &ldq, box);
+  }
+  if (s == MSLKB_OK && Cfg::kAddRing) {
+    const uint64_t bytes = p.out32 ? 4 : 2;
+    const uint64_t extent[3] = {C, R, G}, stride[2] = {bytes * C, bytes * C * R};
+    const uint32_t box[3] = {128, static_cast<uint32_t>(Cfg::kChunk), 1};
+    s = encode_map_plain(&maps[2], p.add, static_cast<int>(bytes), 3, extent, stride, box);
+  }
+  return s;
 }
 
 // Rows that TMA can fetch: 16-byte aligned, and so spaced.
 template <Mm kMode>
 bool by_tma(const MmParams& p) {
   const int64_t row_p = kMode == Mm::kGrad ? p.ldp : (kMode == Mm::kRows ? p.K : p.C);
-  return aligned_to(p.P, 16) && aligned_to(p.Q, 16) && row_p % 8 == 0 && p.ldq % 8 == 0;
+  return aligned_to(p.P, 16) && aligned_to(p.Q, 16) && row_p % 8 == 0 && p.ldq % 8 == 0 &&
+         (p.add == nullptr ||
+          (aligned_to(p.add, 16) && static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2) % 16 == 0));
+}
+
+template <class Cfg>
+mslkb_status run_as(const MmParams& p, int sms, void* stream) {
+  CUtensorMap maps[3];
+  std::memset(maps, 0, sizeof maps);
+  if (Cfg::kTma) {
+    const mslkb_status s = encode<Cfg>(p, maps);
+    if (s != MSLKB_OK) return s;
+  }
+  return launch<Cfg>(p, maps, sms, stream);
 }
 
 template <Mm kMode>
 mslkb_status run(const MmParams& p, int sms, void* stream) {
-  CUtensorMap tp, tq;
-  std::memset(&tp, 0, sizeof tp);
-  std::memset(&tq, 0, sizeof tq);
   const bool sums = kMode == Mm::kGrad ? p.total > 0 : p.K > 0;
-  if (sums && by_tma<kMode>(p)) {
-    using Cfg = MmCfg<kMode, true, 2, 256, 1, 6, 8>;
-    const mslkb_status s = maps<Cfg>(p, &tp, &tq);
-    if (s != MSLKB_OK) return s;
-    return launch<Cfg>(p, tp, tq, sms, stream);
+  if (!sums || !by_tma<kMode>(p)) return run_as<MmCfg<kMode, false, 1, 128, 1, 4, 4>>(p, sms, stream);
+  if constexpr (kMode == Mm::kGrad) {
+    if (p.add != nullptr)
+      return run_as<MmCfg<kMode, true, 2, 256, 1, 4, 8, true>>(p, sms, stream);
   }
-  return launch<MmCfg<kMode, false, 1, 128, 1, 4, 4>>(p, tp, tq, sms, stream);
+  return run_as<MmCfg<kMode, true, 2, 256, 1, 6, 8>>(p, sms, stream);
 }
 
 bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {

@@ -53,7 +53,8 @@ struct MmParams {
   int32_t out32;           // 1: fp32 output, 0: the operands' type
 };
 
-template <Mm kMode_, bool kTma_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_>
+template <Mm kMode_, bool kTma_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_,
+          bool kAdd_ = false>
 struct MmCfg {
   static constexpr Mm kMode = kMode_;
   static constexpr bool kGrad = kMode == Mm::kGrad;
@@ -77,7 +78,13 @@ struct MmCfg {
   static constexpr int kMmaWarp = kLoaderWarps;
   static constexpr int kEdgeWarp = 2;
   static constexpr int kTileWarp = kTma ? 3 : 17;  // hands out the tiles
-  static constexpr int kEpiWarp0 = kTma ? 4 : 20;
+  // kGrad by TMA with something to add: that comes by TMA too, chunk by chunk, through a ring of
+  // its own for each four of the epilogue's warps (loaded by the epilogue's threads themselves,
+  // one or two chunks ahead: 1487 us for 32 x 4096 x 7168 fp32, 1264 bf16)
+  static constexpr bool kAddRing = kAdd_;
+  static constexpr int kAddWarp = 4;
+  static constexpr int kAddBytes = kAddRing ? 32768 : 0;
+  static constexpr int kEpiWarp0 = kTma ? (kAddRing ? 8 : 4) : 20;
   static constexpr int kEpiWarps = kEpiWarps_;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kRowStep = 16 * kCtas;      // a tile's rows are rounded up to these
@@ -95,11 +102,14 @@ struct MmCfg {
   static constexpr int kOffQ = kStages * kPBytes;
   static constexpr int kStagePart = 8192;  // the epilogue's rows: 32 x 128 in 16 bits
   static constexpr int kOffStage = kOffQ + kStages * kQBytes;
-  static constexpr int kOffBar = kOffStage + kEpiWarps / 4 * kStagePart;
+  static constexpr int kOffAdd = kOffStage + kEpiWarps / 4 * kStagePart;
+  static constexpr int kOffBar = kOffAdd + kEpiWarps / 4 * kAddBytes;
   // the scheduler warp hands tiles to the other roles through a ring
   static constexpr int kRing = 4;
-  static constexpr int kRingUsers = kLoaderWarps + 1 + (kTma && kGrad ? 1 : 0) + kEpiWarps;
-  static constexpr int kNumBars = 4 * kStages + 4 + 2 * kRing;
+  static constexpr int kRingUsers =
+      kLoaderWarps + 1 + (kTma && kGrad ? 1 : 0) + (kAddRing ? 1 : 0) + kEpiWarps;
+  static constexpr int kAddSlots = 4;  // at most, of one ring
+  static constexpr int kNumBars = 4 * kStages + 4 + 2 * kRing + (kAddRing ? 4 * kAddSlots : 0);
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
   static constexpr int kOffRing = (kOffMisc + 8 + 15) / 16 * 16;
   static constexpr int kOffSched = kOffRing + kRing * 32;
@@ -109,6 +119,7 @@ struct MmCfg {
   static_assert(!kQMn || kQRows % 64 == 0, "MN-major pieces of 64");
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(!kAddRing || (kTma && kGrad && kEpiWarps == 8 && kChunk == 32), "what is added");
   static_assert(kTma || (!kPair && kTileN == 128 && kKB == 1), "the warps' loader");
 };
 
@@ -389,23 +400,12 @@ struct MmChunk {
   }
 };
 
-// 16-bit results in rows of whole, aligned eights: four warps put their 128 columns of some rows
+// 16-bit results in rows of whole, aligned fours: four warps put their 128 columns of some rows
 // side by side in shared memory, and each then stores whole rows, 256 bytes at a time.  (A warp by
-// itself has 64 bytes of a row, and a store of half a line costs the L2 what one of a line does:
-// weights' gradient of 256 rows, 32 x 4096 x 7168 bf16 on GB300 524 us so, 3.6 TB/s.)  kAdd: what
-// is added comes the same way, 8 bytes a lane, and the rows lie in shared memory in fp32.
+// itself has 64 bytes of a row, and a store of half a line takes as long as one of a line:
+// weights' gradient of 256 rows, 32 x 4096 x 7168 bf16 on GB300 524 us so, 383 by whole rows.)
 template <int kN>
 struct MmRows {
-  uint2 a[kN / 4];
-  // `add`: the tile's first row and column; this warp's rows are `which`, `which` + 4, ...
-  __device__ __forceinline__ void load_add(const uint16_t* add, int32_t C, int32_t n, int32_t cols,
-                                           int32_t which, uint32_t lane) {
-    const bool in = static_cast<int32_t>(lane) * 4 < cols;
-    add += static_cast<int64_t>(which) * C + lane * 4u;
-#pragma unroll
-    for (int i = 0; i < kN / 4; ++i, add += 4 * static_cast<int64_t>(C))
-      a[i] = in && which + 4 * i < n ? *reinterpret_cast<const uint2*>(add) : make_uint2(0u, 0u);
-  }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi, bool bf16) {
     if (bf16) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -414,47 +414,29 @@ struct MmRows {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  // stage: shared memory of these four warps; bar: their barrier
-  template <bool kAdd>
-  __device__ __forceinline__ void store(uint16_t* out, int32_t C, int32_t n, int32_t cols,
-                                        int32_t which, const uint32_t (&v)[kN], bool bf16,
-                                        uint32_t stage, uint32_t bar, uint32_t lane) {
-    const uint32_t col = static_cast<uint32_t>(which) * 32u + lane;
+  // out: the chunk's first row and column; stage: shared memory of these four warps, `bar` their
+  // barrier, `which` of them this is
+  static __device__ __forceinline__ void store(uint16_t* out, int32_t C, int32_t n, int32_t cols,
+                                               uint32_t which, const uint32_t (&v)[kN], bool bf16,
+                                               uint32_t stage, uint32_t bar, uint32_t lane) {
     ptx::named_bar_sync(bar, 128);  // the rows before these have been read
-    if constexpr (kAdd) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) ptx::st_shared_u32(stage + col * 4u + j * 512u, v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        const uint32_t two = pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), bf16);
-        ptx::st_shared_u16(stage + col * 2u + j * 256u, static_cast<uint16_t>(two));
-        ptx::st_shared_u16(stage + col * 2u + (j + 1) * 256u, static_cast<uint16_t>(two >> 16));
-      }
-    }
+    for (int j = 0; j < kN; j += 2)  // rows j and j + 1 in a word
+      ptx::st_shared_u32(stage + (which * 32u + lane) * 4u + j * 256u,
+                         pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), bf16));
     ptx::named_bar_sync(bar, 128);
-    if constexpr (kAdd) {
-      out += static_cast<int64_t>(which) * C + lane * 4u;
-      const bool in = static_cast<int32_t>(lane) * 4 < cols;
+    out += static_cast<int64_t>(2 * which) * C + lane * 4u;
+    const bool in = static_cast<int32_t>(lane) * 4 < cols;
 #pragma unroll
-      for (int i = 0; i < kN / 4; ++i, out += 4 * static_cast<int64_t>(C)) {
-        const uint4 f = ptx::ld_shared_v4(stage + (which + 4 * i) * 512u + lane * 16u);
-        auto get = [&](uint32_t w) { return mm_widen(static_cast<uint16_t>(w), bf16); };
-        const uint32_t lo = pack(get(a[i].x) + __uint_as_float(f.x),
-                                 get(a[i].x >> 16) + __uint_as_float(f.y), bf16);
-        const uint32_t hi = pack(get(a[i].y) + __uint_as_float(f.z),
-                                 get(a[i].y >> 16) + __uint_as_float(f.w), bf16);
-        if (in && which + 4 * i < n) *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
-      }
-    } else {
-      const int32_t row = which * 2 + static_cast<int32_t>(lane >> 4);
-      out += static_cast<int64_t>(row) * C + (lane & 15u) * 8u;
-      const bool in = static_cast<int32_t>(lane & 15u) * 8 < cols;
-#pragma unroll
-      for (int i = 0; i < kN / 8; ++i, out += 8 * static_cast<int64_t>(C)) {
-        const uint4 w = ptx::ld_shared_v4(stage + (row + 8 * i) * 256u + (lane & 15u) * 16u);
-        if (in && row + 8 * i < n) *reinterpret_cast<uint4*>(out) = w;
-      }
+    for (int i = 0; i < kN / 8; ++i, out += 8 * static_cast<int64_t>(C)) {
+      const int32_t row = static_cast<int32_t>(2 * which) + 8 * i;
+      const uint4 w = ptx::ld_shared_v4(stage + row * 256u + lane * 16u);
+      if (in && row < n)
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.z, w.w, 0x5410));
+      if (in && row + 1 < n)
+        *reinterpret_cast<uint2*>(out + C) =
+            make_uint2(__byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x7632));
     }
   }
 };
@@ -474,7 +456,8 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, bool ok) {
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     grouped_mm_kernel(const __grid_constant__ MmParams p, const __grid_constant__ CUtensorMap tmP,
-                      const __grid_constant__ CUtensorMap tmQ) {
+                      const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmAdd) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -489,6 +472,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   auto peer_bar = [&](int s) { return s_bar + 8u * (3 * Cfg::kStages + 4 + s); };
   auto tile_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + i); };
   auto taken_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + Cfg::kRing + i); };
+  // ring of what is added, of the epilogue's warps `part`: slot full, slot free
+  auto add_bar = [&](uint32_t part, uint32_t slot) {
+    return s_bar + 8u * (4 * Cfg::kStages + 4 + 2 * Cfg::kRing + part * 2 * Cfg::kAddSlots + slot);
+  };
+  auto addfree_bar = [&](uint32_t part, uint32_t slot) {
+    return add_bar(part, slot) + 8u * Cfg::kAddSlots;
+  };
+  const uint32_t s_add = ptx::smem_addr(smem + Cfg::kOffAdd);
+  const uint32_t add_chunk = p.out32 ? 16384u : 8192u;      // 32 rows of 128
+  const uint32_t add_slots = Cfg::kAddBytes / add_chunk;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 4);
   int32_t* first = reinterpret_cast<int32_t*>(smem + Cfg::kOffSched);
@@ -515,6 +508,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // (a pair's second CTA issues no MMAs)
       ptx::mbar_init(taken_bar(i), static_cast<uint32_t>(Cfg::kRingUsers) - (crank != 0 ? 1u : 0u));
     }
+    if constexpr (Cfg::kAddRing)
+      for (uint32_t i = 0; i < 2; ++i)
+        for (uint32_t j = 0; j < Cfg::kAddSlots; ++j) {
+          ptx::mbar_init(add_bar(i, j), 1u);
+          ptx::mbar_init(addfree_bar(i, j), 4u);
+        }
     *abort_flag = 0u;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
@@ -796,6 +795,28 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(full_bar(last));
       }
     }
+  } else if (Cfg::kAddRing && warp == Cfg::kAddWarp) {
+    // -------------------------------------------------------------- what is added
+    if (lane == 0) {
+      uint32_t used = 0, count0 = 0, count1 = 0;  // chunks of either ring
+      bool ok = true;
+      MmTile c;
+      for (int32_t i = 0; ok && take(i, c, false); ++i) {
+        // (the same turns as the epilogue's)
+        const uint32_t part = c.len > 0 ? used++ & 1u : static_cast<uint32_t>(i) & 1u;
+        for (int32_t j0 = 0; j0 < c.valid; j0 += Cfg::kChunk) {
+          const uint32_t n = part == 0 ? count0++ : count1++, slot = n % add_slots;
+          ok = wait_bar(addfree_bar(part, slot), ((n / add_slots) & 1u) ^ 1u, abort_flag, p.status,
+                        p.timeout_ns);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
+          ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &tmAdd,
+                           add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * 128,
+                           c.r0 + j0, c.g);
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == static_cast<uint32_t>(Cfg::kTileWarp)) {
     // -------------------------------------------------------------- tiles
     // 32 tiles are worked out at a time, one by each lane (a search and four divisions), and
@@ -837,11 +858,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     constexpr uint32_t kParts = Cfg::kEpiWarps / 4;
     const uint32_t stage = ptx::smem_addr(smem + Cfg::kOffStage) + part * Cfg::kStagePart;
     const uint32_t bar = 1u + part;  // of this part's four warps
-    auto work = [&](auto chunk, auto* out0, auto may_add, auto rows) {
+    uint32_t adds = 0;  // chunks of the ring taken
+    // kWhole: 16-bit results by whole rows; kLoad: what is added is loaded here
+    auto work = [&](auto* out0, auto whole, auto load) {
       using T = std::remove_pointer_t<decltype(out0)>;
-      constexpr bool kAdd = decltype(may_add)::value;
-      constexpr int kN = decltype(rows)::value;
-      constexpr bool kWhole = std::is_same_v<decltype(chunk), MmRows<kN>>;
+      constexpr bool kWhole = decltype(whole)::value, kLoad = decltype(load)::value;
+      constexpr int kN = Cfg::kChunk;
+      MmChunk<T, kN> chunk;
       const T* add0 = static_cast<const T*>(p.add);
       const bool bf16 = p.bf16 != 0;
       uint32_t used = 0;
@@ -849,22 +872,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       for (int32_t i = 0;; ++i) {
         bool ok = take(i, c, true);
         const int32_t col0 = c.c0 + static_cast<int32_t>(crank) * 128;
-        const int32_t col = col0 + (kWhole ? 0 : static_cast<int32_t>(q * 32u + lane));
+        const int32_t col = col0 + static_cast<int32_t>(q * 32u + lane);
         const bool in = col < p.C;
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
-        int32_t j0 = 0;
-        int64_t at = row0 * p.C + col;
-        auto load_add = [&](int64_t from, int32_t n) {
-          if constexpr (kWhole)
-            chunk.load_add(add0 + from, p.C, n, p.C - col0, static_cast<int32_t>(q), lane);
-          else
-            chunk.load_add(add0 + from, p.C, n, in);
-        };
+        int64_t at = row0 * p.C;
         const bool any = ok && c.len > 0;  // else the empty sum
         const uint32_t b = used & 1u;
         const bool mine = kParts == 1 || (any ? b : static_cast<uint32_t>(i) & 1u) == part;
-        if constexpr (kAdd) {
-          if (ok && mine) load_add(at, c.valid);
+        if constexpr (kLoad) {
+          if (ok && mine) chunk.load_add(add0 + at + col, p.C, c.valid, in);
         }
         if (any && mine) {
           ok = wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
@@ -876,7 +892,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (!ok) break;
         used += any ? 1u : 0u;
         if (!mine) continue;
-        for (; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
+        for (int32_t j0 = 0; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
           uint32_t v[kN];
           if (any) {
             const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
@@ -888,16 +904,39 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kN; ++j) v[j] = 0u;
           }
-          auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
           const int32_t n = c.valid - j0;
-          if constexpr (kAdd) {
-            if (n > kN) load_add(at + static_cast<int64_t>(kN) * p.C, n - kN);
+          if constexpr (Cfg::kAddRing) {
+            const uint32_t slot = adds % add_slots;
+            bool got = wait_bar(add_bar(part, slot), (adds / add_slots) & 1u, abort_flag, p.status,
+                                p.timeout_ns);
+            got = __all_sync(0xffffffffu, got) != 0;
+            if constexpr (kWhole) got = named_bar_and(bar, got);
+            if (!got) return;
+            ++adds;
+            const uint32_t from = s_add + part * Cfg::kAddBytes + slot * add_chunk +
+                                  (q * 32u + lane) * sizeof(T);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              float a;
+              if constexpr (sizeof(T) == 4)
+                a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
+              else
+                a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
+              v[j] = __float_as_uint(a + __uint_as_float(v[j]));
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
           }
-          if constexpr (kWhole)
-            now.template store<kAdd>(out0 + at, p.C, n, p.C - col0, static_cast<int32_t>(q), v,
-                                     bf16, stage, bar, lane);
-          else
-            now.template store<kAdd>(out0 + at, p.C, n, in, v, bf16, lane);
+          if constexpr (kWhole) {
+            MmRows<kN>::store(out0 + at + col0, p.C, n, p.C - col0, q, v, bf16, stage, bar, lane);
+          } else {
+            auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
+            if constexpr (kLoad) {
+              if (n > kN)
+                chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
+            }
+            now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16, lane);
+          }
         }
         if (any) {
           ptx::tc_fence_before_sync();
@@ -911,24 +950,23 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
       }
     };
-    auto by_type = [&](auto may_add) {
-      using Rows = std::integral_constant<int, Cfg::kChunk>;
-      constexpr int kWide = decltype(may_add)::value ? 16 : Cfg::kChunk;
-      const bool whole = p.C % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 &&
-                         (reinterpret_cast<uintptr_t>(p.add) & 7) == 0;
-      if (Cfg::kGrad && p.out32)
-        work(MmChunk<float, Cfg::kChunk>{}, static_cast<float*>(p.out), may_add, Rows{});
-      else if (whole)
-        work(MmRows<kWide>{}, static_cast<uint16_t*>(p.out), may_add,
-             std::integral_constant<int, kWide>{});
-      else
-        work(MmChunk<uint16_t, Cfg::kChunk>{}, static_cast<uint16_t*>(p.out), may_add, Rows{});
-    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    uint16_t* out16 = static_cast<uint16_t*>(p.out);
+    const bool rows = p.C % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7) == 0;
     if constexpr (Cfg::kGrad) {
-      if (p.add != nullptr) by_type(std::true_type{});
-      else by_type(std::false_type{});
+      float* out32 = static_cast<float*>(p.out);
+      const bool load = !Cfg::kTma && p.add != nullptr;
+      if constexpr (!Cfg::kTma) {
+        if (load && p.out32) work(out32, no, yes);
+        else if (load) work(out16, no, yes);
+      }
+      if (!load && p.out32) work(out32, no, no);
+      else if (!load && rows) work(out16, yes, no);
+      else if (!load) work(out16, no, no);
     } else {
-      by_type(std::false_type{});
+      if (rows) work(out16, yes, no);
+      else work(out16, no, no);
     }
   }
 

@@ -814,8 +814,10 @@ mslkb_status device_handles(DeviceHandles* h) {
   return MSLKB_OK;
 }
 
-mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const uint64_t* extent,
-                          const uint64_t* stride, const uint32_t* box) {
+namespace {
+mslkb_status encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType type,
+                        CUtensorMapSwizzle swizzle, int dims, const uint64_t* extent,
+                        const uint64_t* stride, const uint32_t* box) {
   if (g_encode == nullptr) return cuda_fail(cudaErrorNotSupported);
   cuuint64_t d[3], st[2];
   cuuint32_t b[3], es[3] = {1, 1, 1};
@@ -824,14 +826,28 @@ mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const ui
     b[i] = box[i];
     if (i + 1 < dims) st[i] = stride[i];
   }
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(dims),
-                              const_cast<void*>(base), d, st, b, es,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = g_encode(map, type, static_cast<cuuint32_t>(dims), const_cast<void*>(base), d,
+                              st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r == CUDA_SUCCESS) return MSLKB_OK;
   t_last_cuda_error = static_cast<int>(r);
   return MSLKB_ERR_CUDA;
+}
+}  // namespace
+
+mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const uint64_t* extent,
+                          const uint64_t* stride, const uint32_t* box) {
+  return encode_map(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B, dims,
+                    extent, stride, box);
+}
+
+mslkb_status encode_map_plain(CUtensorMap* map, const void* base, int bytes, int dims,
+                              const uint64_t* extent, const uint64_t* stride,
+                              const uint32_t* box) {
+  return encode_map(map, base,
+                    bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, dims, extent, stride, box);
 }
 
 TraceRange::TraceRange(const char* name, int64_t rows) {
