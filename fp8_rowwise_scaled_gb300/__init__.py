@@ -15,8 +15,8 @@ include/mslkb.h).  This module only marshals arguments:
 * ``moe`` holds both forms of the operators around the product in a mixture-of-experts
   block (norm with an e4m3 output, expert routing, dispatch and combine, SwiGLU with an
   e4m3 output and checkpoint, and their gradients), re-exported here;
-* ``training`` those for training the experts: their products in 16 bits and the weights'
-  gradients.
+* ``training`` those for training the experts: their products in 16 bits, the weights'
+  gradients, and the gradients' norm and clipping.
 
 There is no fallback: if libmslkb.so is missing or cannot be loaded, every call raises.
 """
@@ -652,4 +652,6 @@ from .moe import (  # noqa: E402 - needs the definitions above
     mslkb_swiglu_quant_backward, route_experts, route_experts_backward, swiglu_quant,
     swiglu_quant_backward)
 from .training import (  # noqa: E402
-    grouped_mm, grouped_mm_weight_grad, mslkb_grouped_mm, mslkb_grouped_mm_weight_grad)
+    ClippedGrads, clip_grad_norm, grad_norm, grouped_mm, grouped_mm_weight_grad,
+    mslkb_clip_grad_norm, mslkb_grad_norm, mslkb_grad_norm_workspace_bytes, mslkb_grouped_mm,
+    mslkb_grouped_mm_weight_grad)

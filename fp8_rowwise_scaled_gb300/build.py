@@ -42,7 +42,8 @@ BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["mslkb.cu", "mslkb_noalloc.cu", "variants_stacked_tma.cu",
            "variants_dynamic_tma.cu", "variants_cpasync.cu", "variants_ragged_n.cu",
            "variants_ragged_k.cu", "variants_blockscale.cu", "variants_blockscale_dynamic.cu",
-           "norm_quant.cu", "route.cu", "dispatch.cu", "swiglu_quant.cu", "grouped_mm.cu"]
+           "norm_quant.cu", "route.cu", "dispatch.cu", "swiglu_quant.cu", "grouped_mm.cu",
+           "grad_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -21,6 +21,7 @@
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "mslkb.h"
 
@@ -513,6 +514,103 @@ PyObject* grouped_mm_weight_grad(PyObject* const* a) {
   });
 }
 
+// A list of gradients: addresses, sizes and types, and the device that all are on.
+struct Gradients {
+  std::vector<const void*> at;
+  std::vector<int64_t> sizes;
+  std::vector<int32_t> types;
+  std::vector<const at::Tensor*> tensors;
+  explicit Gradients(PyObject* o) {
+    if (!PyList_Check(o) && !PyTuple_Check(o))
+      raise(PyExc_TypeError, "grads must be a list or tuple of tensors");
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    at.reserve(n), sizes.reserve(n), types.reserve(n), tensors.reserve(n);
+    const int device = c10::cuda::current_device();
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(o, i), "grads");
+      const at::ScalarType type = t.scalar_type();
+      if (type != at::kBFloat16 && type != at::kHalf && type != at::kFloat)
+        raise(PyExc_TypeError, std::string("grads: dtype ") + c10::toString(type) +
+                                   " is not bfloat16, float16 or float32");
+      if (!t.is_cuda()) raise(PyExc_ValueError, "grads must be CUDA tensors");
+      if (t.get_device() != device)
+        raise(PyExc_ValueError, "grads: a tensor is on another device than the current one");
+      if (!t.is_non_overlapping_and_dense())
+        raise(PyExc_ValueError, "grads must be dense");
+      at.push_back(t.data_ptr());
+      sizes.push_back(t.numel());
+      types.push_back(type == at::kFloat ? MSLKB_FP32
+                                         : (type == at::kHalf ? MSLKB_FP16 : MSLKB_BF16));
+      tensors.push_back(&t);
+    }
+  }
+  int64_t count() const { return static_cast<int64_t>(at.size()); }
+};
+
+// The norm's place: an fp32 tensor of one element on the current device.
+float* norm_place(PyObject* o) {
+  const at::Tensor& t = tensor(o, "norm");
+  if (t.scalar_type() != at::kFloat) raise(PyExc_TypeError, "norm: expected float32");
+  if (t.numel() != 1) raise(PyExc_ValueError, "norm: expected one element");
+  if (!t.is_cuda() || t.get_device() != c10::cuda::current_device())
+    raise(PyExc_ValueError, "norm must be a CUDA tensor on the current device");
+  return static_cast<float*>(t.data_ptr());
+}
+
+// grads, kind, out, stream
+PyObject* grad_norm(PyObject* const* a) {
+  const Gradients g(a[0]);
+  const int32_t kind = static_cast<int32_t>(integer(a[1]));
+  float* norm = norm_place(a[2]);
+  Call c;
+  c.device = c10::cuda::current_device();
+  void* s = c.stream(a[3]);
+  const int64_t bytes = mslkb_grad_norm_workspace_bytes(g.count());
+  const Scratch workspace(bytes, s);
+  return run([&] {
+    return mslkb_grad_norm(g.at.data(), g.sizes.data(), g.types.data(), g.count(), kind, norm,
+                           workspace.p, bytes, s);
+  });
+}
+
+// grads, kind, max_norm, eps, norm, outs, stream
+PyObject* clip_grad_norm(PyObject* const* a) {
+  const Gradients g(a[0]);
+  const int32_t kind = static_cast<int32_t>(integer(a[1]));
+  const double max_norm = number(a[2]), eps = number(a[3]);
+  float* norm = norm_place(a[4]);
+  PyObject* o = a[5];
+  if (!PyList_Check(o) && !PyTuple_Check(o))
+    raise(PyExc_TypeError, "out: expected (norm, list of tensors)");
+  if (PySequence_Fast_GET_SIZE(o) != g.count())
+    raise(PyExc_ValueError, "out: " + std::to_string(g.count()) + " tensors expected, got " +
+                                std::to_string(PySequence_Fast_GET_SIZE(o)));
+  std::vector<void*> outs;
+  outs.reserve(g.at.size());
+  for (int64_t i = 0; i < g.count(); ++i) {
+    const at::Tensor& t = tensor(PySequence_Fast_GET_ITEM(o, i), "out");
+    const at::Tensor& like = *g.tensors[i];
+    if (t.scalar_type() != like.scalar_type())
+      raise(PyExc_TypeError, std::string("out: dtype ") + c10::toString(t.scalar_type()) +
+                                 ", expected " + c10::toString(like.scalar_type()));
+    if (t.sizes() != like.sizes() || t.strides() != like.strides())
+      raise(PyExc_ValueError, "out: shape " + shape_text(t.sizes()) + ", expected " +
+                                  shape_text(like.sizes()) + " with the gradient's strides");
+    if (!t.is_cuda() || t.get_device() != like.get_device())
+      raise(PyExc_ValueError, "out must be CUDA tensors on the same device");
+    outs.push_back(t.data_ptr());
+  }
+  Call c;
+  c.device = c10::cuda::current_device();
+  void* s = c.stream(a[6]);
+  const int64_t bytes = mslkb_grad_norm_workspace_bytes(g.count());
+  const Scratch workspace(bytes, s);
+  return run([&] {
+    return mslkb_clip_grad_norm(g.at.data(), outs.data(), g.sizes.data(), g.types.data(),
+                                g.count(), kind, max_norm, eps, norm, workspace.p, bytes, s);
+  });
+}
+
 // The number of arguments, and no C++ exception past this point.
 template <PyObject* (*kFn)(PyObject* const*), Py_ssize_t kCount>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
@@ -551,6 +649,8 @@ PyMethodDef g_methods[] = {MSLKB_ENTRY(add_rms_norm_quant, 9),
                            MSLKB_ENTRY(swiglu_quant_backward, 5),
                            MSLKB_ENTRY(grouped_mm, 6),
                            MSLKB_ENTRY(grouped_mm_weight_grad, 6),
+                           MSLKB_ENTRY(grad_norm, 4),
+                           MSLKB_ENTRY(clip_grad_norm, 7),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,

@@ -1,7 +1,9 @@
-"""Operators for training the experts: their products in 16 bits, forward and backward.
+"""Operators for training the experts: their products in 16 bits, forward and backward, and what
+follows the backward pass.
 
     grouped_mm(x, w) -> ... -> grouped_mm(dy, w, transposed=True)     the input's gradient
                                grouped_mm_weight_grad(dy, x)          the weights' gradient
+                            -> clip_grad_norm(all gradients)          (or grad_norm alone)
 
 As in moe.py, whose conventions hold here too: ``mslkb_*`` functions mirror the C entry points,
 the others take torch CUDA tensors, run on the current stream or on ``stream``, and put their
@@ -10,20 +12,28 @@ results into ``out`` where it is given.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import fp8_rowwise_scaled_gb300 as _fx
 
 from . import moe as _moe
 
+MSLKB_NORM_2, MSLKB_NORM_INF = range(2)
+MAX_TENSORS = 65536
+
 
 def declare(L: ctypes.CDLL) -> ctypes.CDLL:
     """Argument and result types of this module's entry points on a loaded library."""
-    p, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    p, i64, i32, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double
     for name, args in {
             "mslkb_grouped_mm": [p] * 4 + [i64] * 5 + [i32, i32, p],
-            "mslkb_grouped_mm_weight_grad": [p] * 5 + [i64] * 6 + [i32, i32, p]}.items():
+            "mslkb_grouped_mm_weight_grad": [p] * 5 + [i64] * 6 + [i32, i32, p],
+            "mslkb_grad_norm": [p] * 3 + [i64, i32, p, p, i64, p],
+            "mslkb_clip_grad_norm": [p] * 4 + [i64, i32, f64, f64, p, p, i64, p]}.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
+    L.mslkb_grad_norm_workspace_bytes.argtypes = [i64]
+    L.mslkb_grad_norm_workspace_bytes.restype = i64
     return L
 
 
@@ -40,6 +50,23 @@ def mslkb_grouped_mm_weight_grad(dy, x, m_sizes, add, dw, total_M, G, N, K, lddy
                                  dw_fp32=1, stream=0) -> int:
     return _fx.lib().mslkb_grouped_mm_weight_grad(dy, x, m_sizes, add, dw, total_M, G, N, K, lddy,
                                                   ldx, dtype, dw_fp32, stream)
+
+
+def mslkb_grad_norm_workspace_bytes(count) -> int:
+    return _fx.lib().mslkb_grad_norm_workspace_bytes(count)
+
+
+def mslkb_grad_norm(grads, sizes, dtypes, count, kind, norm, workspace, workspace_bytes,
+                    stream=0) -> int:
+    """grads, sizes, dtypes: host arrays (ctypes arrays or addresses)."""
+    return _fx.lib().mslkb_grad_norm(grads, sizes, dtypes, count, kind, norm, workspace,
+                                     workspace_bytes, stream)
+
+
+def mslkb_clip_grad_norm(grads, outs, sizes, dtypes, count, kind, max_norm, eps, norm, workspace,
+                         workspace_bytes, stream=0) -> int:
+    return _fx.lib().mslkb_clip_grad_norm(grads, outs, sizes, dtypes, count, kind, max_norm, eps,
+                                          norm, workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------------------------------
@@ -98,3 +125,59 @@ def grouped_mm_weight_grad(dy, x, m_sizes, *, add=None, dtype=None, out=None, st
     if s:
         raise _fx.MslkbError(s, "grouped_mm_weight_grad")
     return out
+
+
+class ClippedGrads(NamedTuple):
+    """norm fp32 (of the gradients before they were scaled); grads, the scaled gradients."""
+    norm: object
+    grads: object
+
+
+def _kind(norm_type):
+    if norm_type == 2:
+        return MSLKB_NORM_2
+    if norm_type == float("inf"):
+        return MSLKB_NORM_INF
+    raise ValueError(f"norm_type must be 2 or infinity, not {norm_type!r}")
+
+
+def grad_norm(grads, *, norm_type=2.0, out=None, stream=None):
+    """The norm of all gradients taken together as one vector: the square root of the sum of all
+    squares, or the largest magnitude (``norm_type`` infinity).
+
+    grads: a list or tuple of dense tensors, each bf16, fp16 or fp32 -> fp32 tensor of one
+    element."""
+    b = _binding()
+    kind = _kind(norm_type)
+    if out is None:
+        out = _moe._new(stream, (), _moe._torch.float32)
+    s = b.grad_norm(grads, kind, out, _moe._raw(stream))
+    if s:
+        raise _fx.MslkbError(s, "grad_norm")
+    return out
+
+
+def clip_grad_norm(grads, max_norm, *, norm_type=2.0, eps=1e-6, out=None, stream=None):
+    """grads * min(1, max_norm / (norm + eps)), norm that of grad_norm -> ClippedGrads(norm,
+    grads).
+
+    ``out`` is (norm, tensors of the gradients' types, shapes and strides); the tensors may be the
+    gradients themselves, which are then scaled in place (and not written where nothing
+    changes), but must not overlap otherwise.  Without ``out`` new tensors are made."""
+    b = _binding()
+    kind = _kind(norm_type)
+    if out is None:
+        torch = _moe._torch
+        if not isinstance(grads, (list, tuple)):
+            raise TypeError("grads must be a list or tuple of tensors")
+        if not all(isinstance(g, torch.Tensor) for g in grads):
+            raise TypeError("grads must be a torch.Tensor")
+        with torch.cuda.stream(None if stream is None else _moe._stream(stream)):
+            out = ClippedGrads(torch.empty((), dtype=torch.float32, device="cuda"),
+                               [torch.empty_like(g) for g in grads])
+    elif not isinstance(out, tuple) or len(out) != 2:
+        raise TypeError("out must be a tuple (norm, tensors)")
+    s = b.clip_grad_norm(grads, kind, max_norm, eps, out[0], out[1], _moe._raw(stream))
+    if s:
+        raise _fx.MslkbError(s, "clip_grad_norm")
+    return ClippedGrads(*out)

@@ -537,6 +537,45 @@ MSLKB_API mslkb_status mslkb_grouped_mm_weight_grad(
     int64_t total_M, int64_t G, int64_t N, int64_t K, int64_t lddy, int64_t ldx, int32_t dtype,
     int32_t dw_fp32, void *stream);
 
+/*
+ * The norm of a list of gradients taken together, as one vector:
+ *
+ *   norm = (sum over all elements of g^2)^(1/2)    kind MSLKB_NORM_2
+ *   norm = the largest |g|                         kind MSLKB_NORM_INF
+ *
+ *   grads    host array of `count` device pointers; tensor i has sizes[i] elements (0: none) of
+ *            type dtypes[i] (MSLKB_BF16, MSLKB_FP16 or MSLKB_FP32, which may differ), dense, at
+ *            any address that suits its type.  sizes and dtypes are host arrays.  The arrays may
+ *            be freed when the call returns
+ *   norm     device, fp32: a NaN among the elements makes it NaN, an infinity infinity; else it
+ *            is infinite only past fp32's largest number (squares do not overflow)
+ *   workspace, workspace_bytes: as for the norm's gradient above, of
+ *            mslkb_grad_norm_workspace_bytes(count)
+ */
+#define MSLKB_NORM_2 0
+#define MSLKB_NORM_INF 1
+#define MSLKB_MAX_TENSORS 65536
+MSLKB_API int64_t mslkb_grad_norm_workspace_bytes(int64_t count);
+MSLKB_API mslkb_status mslkb_grad_norm(const void *const *grads, const int64_t *sizes,
+                                       const int32_t *dtypes, int64_t count, int32_t kind,
+                                       float *norm, void *workspace, int64_t workspace_bytes,
+                                       void *stream);
+
+/*
+ * The gradients scaled so that their norm does not exceed max_norm:
+ *
+ *   outs[i] = grads[i] * scale,    scale = min(1, max_norm / (norm + eps))   (NaN if norm is)
+ *
+ * each product rounded once to its tensor's type; norm is that of grads, as above.  outs[i] may
+ * be grads[i] itself (left as it is where scale is 1); otherwise results must not lie over each
+ * other or over gradients (MSLKB_ERR_SHAPE).  max_norm >= 0 (it may be infinite), eps >= 0.
+ */
+MSLKB_API mslkb_status mslkb_clip_grad_norm(const void *const *grads, void *const *outs,
+                                            const int64_t *sizes, const int32_t *dtypes,
+                                            int64_t count, int32_t kind, double max_norm,
+                                            double eps, float *norm, void *workspace,
+                                            int64_t workspace_bytes, void *stream);
+
 /* Static description of a status code.  Never NULL. */
 MSLKB_API const char *mslkb_status_string(mslkb_status status);
 

@@ -1,5 +1,7 @@
 """C entry points for training the experts, without a GPU: argument errors come before any CUDA
 call, empty calls do nothing."""
+import ctypes
+
 import pytest
 
 import fp8_rowwise_scaled_gb300 as fx
@@ -42,3 +44,45 @@ def test_products_of_nothing():
     refused(mm, fx.MSLKB_OK, {"total_M": 0, "x": None, "out": None}, {"G": 0, "m_sizes": None},
             {"N": 0, "w": None})
     refused(weight_grad, fx.MSLKB_OK, {"G": 0, "dw": None}, {"N": 0}, {"K": 0, "dw": None})
+
+
+def array(kind, *values):
+    return (kind * len(values))(*values)
+
+
+GRADS = array(ctypes.c_void_p, 256, 4096)
+OUTS = array(ctypes.c_void_p, 16384, 32768)
+SIZES = array(ctypes.c_int64, 10, 100)
+TYPES = array(ctypes.c_int32, moe.MSLKB_BF16, moe.MSLKB_FP32)
+norm = call(fx.mslkb_grad_norm, dict(
+    grads=GRADS, sizes=SIZES, dtypes=TYPES, count=2, kind=0, norm=P, workspace=P, bytes=1 << 20,
+    stream=0))
+clip = call(fx.mslkb_clip_grad_norm, dict(
+    grads=GRADS, outs=OUTS, sizes=SIZES, dtypes=TYPES, count=2, kind=0, max_norm=1.0, eps=1e-6,
+    norm=P, workspace=P, bytes=1 << 20, stream=0))
+
+
+def test_lists_refuse():
+    bad_size, bad_type = array(ctypes.c_int64, 10, -1), array(ctypes.c_int32, 0, 3)
+    for fn in (norm, clip):
+        refused(fn, fx.MSLKB_ERR_NULL, *({k: None} for k in ("grads", "sizes", "dtypes", "norm")),
+                {"grads": array(ctypes.c_void_p, 256, None)})
+        refused(fn, fx.MSLKB_ERR_SHAPE, {"count": -1}, {"count": 65537}, {"kind": 2}, {"kind": -1},
+                {"sizes": bad_size}, {"sizes": array(ctypes.c_int64, 1 << 41, 1)})
+        refused(fn, fx.MSLKB_ERR_DTYPE, {"dtypes": bad_type})
+        refused(fn, fx.MSLKB_ERR_ALIGN, {"grads": array(ctypes.c_void_p, 257, 4096)},
+                {"grads": array(ctypes.c_void_p, 256, 4098)}, {"norm": 258})
+        refused(fn, fx.MSLKB_ERR_WORKSPACE, {"workspace": None}, {"workspace": 264}, {"bytes": 4095})
+    refused(clip, fx.MSLKB_ERR_NULL, {"outs": None}, {"outs": array(ctypes.c_void_p, 16384, None)})
+    refused(clip, fx.MSLKB_ERR_ALIGN, {"outs": array(ctypes.c_void_p, 16385, 32768)})
+    refused(clip, fx.MSLKB_ERR_SHAPE, {"max_norm": -1.0}, {"max_norm": float("nan")},
+            {"eps": -1.0}, {"eps": float("nan")}, {"eps": float("inf")},
+            # one result over the other, a result over the other's gradient, or beside its own
+            {"outs": array(ctypes.c_void_p, 16384, 16400)},
+            {"outs": array(ctypes.c_void_p, 4096 + 396, 32768)},
+            {"outs": array(ctypes.c_void_p, 258, 32768)})
+
+
+def test_list_workspace():
+    f = fx.mslkb_grad_norm_workspace_bytes
+    assert f(0) == f(1) == f(1024) == 4096 and f(1025) == 8192 and f(-1) == f(65537) == 0
