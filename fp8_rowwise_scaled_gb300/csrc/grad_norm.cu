@@ -19,6 +19,7 @@
 // of Knuth), so that long runs of equal values do not drift; the pairs of the threads and CTAs are
 // added in fp64.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <vector>
@@ -33,18 +34,25 @@ constexpr int kThreads = 512;
 constexpr int kChunkBytes = 4096;
 constexpr int kMaxParts = 512;            // CTAs of a launch, and partial sums of it
 constexpr int kFew = 64, kSome = 256, kMany = 1024;   // tensors of a launch, by the size of its parameters
-constexpr int kCluster = 8;
-constexpr int64_t kSmallBytes = 1 << 19;  // of a list that one cluster takes
+constexpr int kCluster = 16;       // most CTAs of a cluster
+constexpr int kSmallChunks = 512;  // of a list that one cluster takes
 
 // A list of tensors and the chunks before each.
 template <int kMost>
 struct List {
-  const void* in[kMost];
-  void* out[kMost];
-  int64_t size[kMost];        // elements * 4 + type
+  struct Tensor {
+    const void* in;
+    void* out;
+    int64_t size;             // elements * 4 + type
+  } t[kMost];
   uint32_t first[kMost + 1];  // chunks before tensor i
+  uint16_t start[kMaxParts + 1];   // the tensor of run r's first chunk (the last chunk's past it)
   int32_t count;
 };
+
+__host__ __device__ inline uint32_t share(uint32_t total, uint32_t i, uint32_t of) {
+  return static_cast<uint32_t>(static_cast<uint64_t>(total) * i / of);
+}
 
 // A sum in two fp32 numbers.
 struct Pair {
@@ -126,19 +134,26 @@ __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
   return h < n ? h : n;
 }
 
-constexpr int kBatch = 4;  // vectors of a thread under way
+// Vectors of a thread under way.
+template <int kStep>
+constexpr int kBatchOf = kStep == 32 ? 8 : 4;
 
-template <bool kInf, class T>
+// By kStep threads, of which this is `tid`.
+template <bool kInf, int kStep, class T>
 __device__ void sum_run(const T* p, int64_t n, Sums& s, int tid) {
   constexpr int kN = 16 / sizeof(T);
   const int64_t head = head_of(p, n);
   const T* mid = p + head;
-  const int64_t vecs = (n - head) / kN;
+  const int64_t vecs = (n - head) / kN, tail = n - head - vecs * kN;
+  constexpr int kBatch = kBatchOf<kStep>;
+  // the ends, fewer than kN elements each
+  const float edge = tid < head + tail ? to_float(tid < head ? p[tid] : mid[vecs * kN + tid - head])
+                                       : 0.f;
   int64_t i = tid;
-  for (; i + (kBatch - 1) * kThreads < vecs; i += kBatch * kThreads) {
+  for (; i + (kBatch - 1) * kStep < vecs; i += kBatch * kStep) {
     uint4 w[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) w[u] = load16(mid + (i + u * kThreads) * kN);
+    for (int u = 0; u < kBatch; ++u) w[u] = load16(mid + (i + u * kStep) * kN);
     float even = 0.f, odd = 0.f;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -148,22 +163,28 @@ __device__ void sum_run(const T* p, int64_t n, Sums& s, int tid) {
     }
     if (!kInf) s.mid.add(even + odd);
   }
-  for (; i < vecs; i += kThreads) {
-    float v[kN], batch = 0.f;
-    unpack16<T>(load16(mid + i * kN), v);
-    take<kInf>(s, batch, v);
-    if (!kInf) s.mid.add(batch);
+  if (i < vecs) {   // fewer vectors than a batch
+    uint4 w[kBatch - 1];
+#pragma unroll
+    for (int u = 0; u < kBatch - 1; ++u)
+      w[u] = i + u * kStep < vecs ? load16(mid + (i + u * kStep) * kN) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int u = 0; u < kBatch - 1; ++u) {
+      float v[kN], batch = 0.f;
+      unpack16<T>(w[u], v);
+      if (i + u * kStep < vecs) take<kInf>(s, batch, v);
+      if (!kInf) s.mid.add(batch);
+    }
   }
-  // the ends, fewer than kN elements each
-  const int64_t tail = n - head - vecs * kN;
   if (tid < head + tail) {
-    float v[1] = {to_float(tid < head ? p[tid] : mid[vecs * kN + tid - head])}, batch = 0.f;
+    const float v[1] = {edge};
+    float batch = 0.f;
     take<kInf>(s, batch, v);
     if (!kInf) s.mid.add(batch);
   }
 }
 
-template <class T>
+template <int kStep, class T>
 __device__ void scale_run(const T* p, T* o, int64_t n, float f, int tid) {
   constexpr int kN = 16 / sizeof(T);
   // whole vectors where both lie alike, else element by element
@@ -179,39 +200,49 @@ __device__ void scale_run(const T* p, T* o, int64_t n, float f, int tid) {
     for (int j = 0; j < kN; ++j) v[j] *= f;
     __stcs(reinterpret_cast<uint4*>(om + at * kN), pack16<T>(v));
   };
+  constexpr int kBatch = kBatchOf<kStep>;
+  const int64_t tail = n - head - vecs * kN;
+  const bool at_head = alike && tid < head;
+  const float edge = at_head ? to_float(p[tid]) : 0.f;
+  const float last = tid < tail ? to_float(pm[vecs * kN + tid]) : 0.f;
   int64_t i = vecs - 1 - tid;   // from the end: what was read last is in L2
-  for (; i - (kBatch - 1) * kThreads >= 0; i -= kBatch * kThreads) {
+  for (; i - (kBatch - 1) * kStep >= 0; i -= kBatch * kStep) {
     uint4 w[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) w[u] = load16(pm + (i - u * kThreads) * kN);
+    for (int u = 0; u < kBatch; ++u) w[u] = load16(pm + (i - u * kStep) * kN);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) one(i - u * kThreads, w[u]);
+    for (int u = 0; u < kBatch; ++u) one(i - u * kStep, w[u]);
   }
-  for (; i >= 0; i -= kThreads) one(i, load16(pm + i * kN));
-  for (int64_t k = tid; k < head; k += kThreads) o[k] = from_float<T>(to_float(p[k]) * f);
-  const int64_t tail = n - head - vecs * kN;
-  if (tid < tail) om[vecs * kN + tid] = from_float<T>(to_float(pm[vecs * kN + tid]) * f);
+  if (i >= 0) {
+    uint4 w[kBatch - 1];
+#pragma unroll
+    for (int u = 0; u < kBatch - 1; ++u)
+      if (i - u * kStep >= 0) w[u] = load16(pm + (i - u * kStep) * kN);
+#pragma unroll
+    for (int u = 0; u < kBatch - 1; ++u)
+      if (i - u * kStep >= 0) one(i - u * kStep, w[u]);
+  }
+  if (at_head) o[tid] = from_float<T>(edge * f);
+  if (tid < tail) om[vecs * kN + tid] = from_float<T>(last * f);
+  if (!alike)
+    for (int64_t k = tid; k < head; k += kStep) o[k] = from_float<T>(to_float(p[k]) * f);
 }
 
-// The runs of chunks [c0, c1), tensor by tensor: f(i, first element, elements).
+// Run `r` of `of`, tensor by tensor: f(tensor, first element, elements).
 template <bool kBack, class L, class F>
-__device__ __forceinline__ void each_run(const L& l, uint32_t c0, uint32_t c1, F f) {
+__device__ __forceinline__ void each_run(const L& l, uint32_t r, uint32_t of, F f) {
+  const uint32_t total = l.first[l.count];
+  const uint32_t c0 = share(total, r, of), c1 = share(total, r + 1, of);
   if (c0 >= c1) return;
-  const uint32_t start = kBack ? c1 - 1 : c0;
-  int lo = 0, hi = l.count;   // the last tensor with first[i] <= start
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.first[mid] <= start) lo = mid;
-    else hi = mid;
-  }
-  for (int i = lo; i >= 0 && i < l.count; i += kBack ? -1 : 1) {
+  for (int i = l.start[kBack ? r + 1 : r]; i >= 0 && i < l.count; i += kBack ? -1 : 1) {
     const uint32_t a = l.first[i], b = l.first[i + 1];
     if (kBack ? b <= c0 : a >= c1) break;
-    const int64_t size = l.size[i] >> 2;
-    const int64_t each = kChunkBytes / ((l.size[i] & 3) == MSLKB_FP32 ? 4 : 2);
+    const auto& t = l.t[i];
+    const int64_t size = t.size >> 2;
+    const int64_t each = kChunkBytes / ((t.size & 3) == MSLKB_FP32 ? 4 : 2);
     const int64_t e0 = a > c0 ? 0 : static_cast<int64_t>(c0 - a) * each;
     const int64_t e1 = b <= c1 ? size : min(size, static_cast<int64_t>(c1 - a) * each);
-    if (e1 > e0) f(i, e0, e1 - e0);
+    if (a < c1 && e1 > e0) f(t, e0, e1 - e0);
   }
 }
 
@@ -224,27 +255,27 @@ __device__ __forceinline__ void by_type(int64_t size, F f) {
   }
 }
 
-template <bool kInf, class L>
-__device__ __forceinline__ Sums sum_chunks(const L& l, uint32_t c0, uint32_t c1) {
+template <bool kInf, int kStep, class L>
+__device__ __forceinline__ Sums sum_chunks(const L& l, uint32_t r, uint32_t of) {
   Sums s;
-  const int tid = static_cast<int>(threadIdx.x);
-  each_run<false>(l, c0, c1, [&](int i, int64_t e0, int64_t n) {
-    by_type(l.size[i], [&](auto t) {
+  const int tid = static_cast<int>(threadIdx.x) % kStep;
+  each_run<false>(l, r, of, [&](const auto& g, int64_t e0, int64_t n) {
+    by_type(g.size, [&](auto t) {
       using T = decltype(t);
-      sum_run<kInf>(static_cast<const T*>(l.in[i]) + e0, n, s, tid);
+      sum_run<kInf, kStep>(static_cast<const T*>(g.in) + e0, n, s, tid);
     });
   });
   return s;
 }
 
-template <class L>
-__device__ __forceinline__ void scale_chunks(const L& l, uint32_t c0, uint32_t c1, float f) {
-  const int tid = static_cast<int>(threadIdx.x);
-  each_run<true>(l, c0, c1, [&](int i, int64_t e0, int64_t n) {
-    if (f == 1.f && l.in[i] == l.out[i]) return;   // nothing changes
-    by_type(l.size[i], [&](auto t) {
+template <int kStep, class L>
+__device__ __forceinline__ void scale_chunks(const L& l, uint32_t r, uint32_t of, float f) {
+  const int tid = static_cast<int>(threadIdx.x) % kStep;
+  each_run<true>(l, r, of, [&](const auto& g, int64_t e0, int64_t n) {
+    if (f == 1.f && g.in == g.out) return;   // nothing changes
+    by_type(g.size, [&](auto t) {
       using T = decltype(t);
-      scale_run(static_cast<const T*>(l.in[i]) + e0, static_cast<T*>(l.out[i]) + e0, n, f, tid);
+      scale_run<kStep>(static_cast<const T*>(g.in) + e0, static_cast<T*>(g.out) + e0, n, f, tid);
     });
   });
 }
@@ -294,10 +325,6 @@ __device__ __forceinline__ float scale_of(float norm, float max_norm, float eps)
   return f > 1.f ? 1.f : f;   // (a NaN stays)
 }
 
-__device__ __forceinline__ uint32_t share(uint32_t total, uint32_t i, uint32_t of) {
-  return static_cast<uint32_t>(static_cast<uint64_t>(total) * i / of);
-}
-
 struct ClipArgs {
   float* norm;
   double* parts;
@@ -313,9 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ double shared[kThreads / 32];
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const uint32_t total = l.first[l.count];
-  const Sums s = sum_chunks<kInf>(l, share(total, blockIdx.x, gridDim.x),
-                                  share(total, blockIdx.x + 1, gridDim.x));
+  const Sums s = sum_chunks<kInf, kThreads>(l, blockIdx.x, gridDim.x);
   const double d = cta_sum<kInf>(s, shared);
   if (threadIdx.x == 0) a.parts[a.part0 + blockIdx.x] = d;
 }
@@ -354,12 +379,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::griddep_wait();
   const float norm = norm_of(kInf, all_parts<kInf>(a, shared));
   if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-  const uint32_t total = l.first[l.count];
-  scale_chunks(l, share(total, blockIdx.x, gridDim.x), share(total, blockIdx.x + 1, gridDim.x),
-               scale_of(norm, a.max_norm, a.eps));
+  scale_chunks<kThreads>(l, blockIdx.x, gridDim.x, scale_of(norm, a.max_norm, a.eps));
 }
 
-// A short list: one cluster, which sums and, if wanted, scales.
+// A short list: one cluster, which sums and, if wanted, scales.  The runs are the warps', so that
+// the latencies of many small tensors pass together.
 template <bool kInf, bool kClip>
 __global__ void __launch_bounds__(kThreads)
     small_list_kernel(const __grid_constant__ List<kFew> l, const __grid_constant__ ClipArgs a) {
@@ -368,9 +392,9 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   if (gridDim.x > 1) ptx::cluster_arrive();   // (waited for before others' memory is written)
   ptx::griddep_wait();
-  const uint32_t total = l.first[l.count], rank = blockIdx.x, of = gridDim.x;
-  const uint32_t c0 = share(total, rank, of), c1 = share(total, rank + 1, of);
-  const Sums s = sum_chunks<kInf>(l, c0, c1);
+  const uint32_t rank = blockIdx.x, of = gridDim.x;
+  const uint32_t warp = rank * (kThreads / 32) + (threadIdx.x >> 5), warps = of * (kThreads / 32);
+  const Sums s = sum_chunks<kInf, 32>(l, warp, warps);
   const double d = cta_sum<kInf>(s, shared);
   if (of > 1) {
     ptx::cluster_wait();
@@ -392,7 +416,7 @@ __global__ void __launch_bounds__(kThreads)
   for (uint32_t r = 1; r < of; ++r) sum = join(kInf, sum, all[r]);
   const float norm = norm_of(kInf, sum);
   if (rank == 0 && threadIdx.x == 0) *a.norm = norm;
-  if constexpr (kClip) scale_chunks(l, c0, c1, scale_of(norm, a.max_norm, a.eps));
+  if constexpr (kClip) scale_chunks<32>(l, warp, warps, scale_of(norm, a.max_norm, a.eps));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -417,13 +441,26 @@ void fill(List<kMost>* l, const Args& a, int64_t from, int64_t to) {
   l->count = static_cast<int32_t>(to - from);
   for (int64_t i = from; i < to; ++i) {
     const int64_t k = i - from;
-    l->in[k] = a.in[i];
-    l->out[k] = a.out != nullptr ? a.out[i] : nullptr;
-    l->size[k] = a.sizes[i] * 4 + a.types[i];
+    l->t[k] = {a.in[i], a.out != nullptr ? a.out[i] : nullptr, a.sizes[i] * 4 + a.types[i]};
     l->first[k] = chunks;
     chunks += static_cast<uint32_t>(chunks_of(a.sizes[i], a.types[i]));
   }
   l->first[to - from] = chunks;
+}
+
+// Where each of `runs` runs starts, and for those that walk back where it ends: start[r] is the
+// tensor of chunk share(r), start[runs] that of the last chunk (a run that walks back starts at
+// the tensor of the next run's first chunk, and passes over it where that is not its own).
+template <int kMost>
+void cut(List<kMost>* l, int runs) {
+  const uint32_t total = l->first[l->count];
+  int i = 0;
+  for (int r = 0; r <= runs; ++r) {
+    uint32_t c = share(total, static_cast<uint32_t>(r), static_cast<uint32_t>(runs));
+    if (c == total && total > 0) --c;
+    while (i + 1 < l->count && l->first[i + 1] <= c) ++i;
+    l->start[r] = static_cast<uint16_t>(i);
+  }
 }
 
 template <bool kInf, int kMost>
@@ -437,6 +474,7 @@ cudaError_t run_list(const Args& a, ClipArgs c, int sms, void* stream) {
       fill(&l, a, i * kMost, std::min(a.count, (i + 1) * kMost));
       const int grid = static_cast<int>(
           std::min<int64_t>(most, std::max<int64_t>(1, l.first[l.count])));
+      cut(&l, grid);
       const cudaError_t e = f(l, grid, i);
       if (e != cudaSuccess) return e;
       c.part0 += grid;
@@ -457,19 +495,59 @@ cudaError_t run_list(const Args& a, ClipArgs c, int sms, void* stream) {
   });
 }
 
+// CTAs that a cluster of `kKernel` can have on this device: 16, or 8 where 16 do not fit.
+template <auto kKernel>
+cudaError_t most_ctas(int* ctas) {
+  static std::atomic<int8_t> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int8_t>& mine = known[dev & 63];
+  if ((*ctas = mine.load()) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int fit = 0;
+  e = cudaOccupancyMaxActiveClusters(&fit, kKernel, &cfg);
+  if (e != cudaSuccess) return e;
+  *ctas = fit > 0 ? kCluster : 8;
+  mine.store(static_cast<int8_t>(*ctas));
+  return cudaSuccess;
+}
+
+template <bool kInf, bool kClip>
+cudaError_t run_small(List<kFew>& l, const ClipArgs& c, void* stream) {
+  // a chunk per warp, as far as they go: 1, 8 or 16 CTAs
+  const uint32_t chunks = l.first[l.count];
+  int grid = chunks <= kThreads / 32 ? 1 : 8;
+  if (chunks > 8 * kThreads / 32) {
+    const cudaError_t e = most_ctas<small_list_kernel<kInf, kClip>>(&grid);
+    if (e != cudaSuccess) return e;
+  }
+  cut(&l, grid * (kThreads / 32));
+  return launch_cluster(small_list_kernel<kInf, kClip>, dim3(grid), dim3(kThreads), 0, grid,
+                        stream, l, c);
+}
+
 template <bool kInf>
 cudaError_t run(const Args& a, const ClipArgs& c, int sms, void* stream) {
-  int64_t bytes = 0;
-  for (int64_t i = 0; i < a.count; ++i) bytes += a.sizes[i] * dtype_bytes(a.types[i]);
-  if (a.count <= kFew && bytes <= kSmallBytes) {
-    List<kFew> l;
-    fill(&l, a, 0, a.count);
-    const int grid = bytes <= 4 * kChunkBytes ? 1 : kCluster;
-    if (a.out != nullptr)
-      return launch_cluster(small_list_kernel<kInf, true>, dim3(grid), dim3(kThreads), 0, grid,
-                            stream, l, c);
-    return launch_cluster(small_list_kernel<kInf, false>, dim3(grid), dim3(kThreads), 0, grid,
-                          stream, l, c);
+  if (a.count <= kFew) {
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < a.count; ++i) chunks += chunks_of(a.sizes[i], a.types[i]);
+    if (chunks <= kSmallChunks) {
+      List<kFew> l;
+      fill(&l, a, 0, a.count);
+      return a.out != nullptr ? run_small<kInf, true>(l, c, stream)
+                              : run_small<kInf, false>(l, c, stream);
+    }
   }
   if (a.count <= kFew) return run_list<kInf, kFew>(a, c, sms, stream);
   if (a.count <= kSome) return run_list<kInf, kSome>(a, c, sms, stream);
