@@ -62,6 +62,14 @@ struct Pair {
     lo += (hi - (t - b)) + (v - b);
     hi = t;
   }
+  __device__ __forceinline__ void add_lanes() {   // of a warp, all lanes get the sum
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      const float l = __shfl_xor_sync(0xffffffffu, lo, m);
+      add(__shfl_xor_sync(0xffffffffu, hi, m));
+      lo += l;
+    }
+  }
   __device__ __forceinline__ double value() const {
     // (beside an infinite hi, lo is infinity less infinity)
     return isinf(hi) ? static_cast<double>(hi) : static_cast<double>(hi) + static_cast<double>(lo);
@@ -280,33 +288,40 @@ __device__ __forceinline__ void scale_chunks(const L& l, uint32_t r, uint32_t of
   });
 }
 
-// A CTA's sum of squares, or (kInf) largest magnitude, in thread 0, as fp64.
+// The fp64 unit of an SM takes 16 cycles for an operation of a warp, so one warp does those, and
+// the others wait (done by all 16 warps of two CTAs, sums and root took 13 us).
+struct Joined {
+  Pair mid, big, small;
+};
+
+// A CTA's sum of squares, or (kInf) largest magnitude, in the lanes of warp 0, as fp64.
 template <bool kInf>
-__device__ __forceinline__ double cta_sum(const Sums& s, double* shared) {
+__device__ __forceinline__ double cta_sum(Sums s, Joined* shared) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  constexpr uint32_t kWarps = kThreads / 32;
   if constexpr (kInf) {
-    uint32_t* words = reinterpret_cast<uint32_t*>(shared);
     const uint32_t m = __reduce_max_sync(0xffffffffu, s.most);
-    if (lane == 0) words[warp] = m;
+    if (lane == 0) shared[warp].mid.hi = __uint_as_float(m);
     __syncthreads();
-    uint32_t all = 0;
-    if (warp == 0) all = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? words[lane] : 0u);
-    return static_cast<double>(__uint_as_float(all));
+    if (warp != 0) return 0.0;
+    const uint32_t mine = lane < kWarps ? __float_as_uint(shared[lane].mid.hi) : 0u;
+    return static_cast<double>(__uint_as_float(__reduce_max_sync(0xffffffffu, mine)));
   } else {
-    double d = s.mid.value();
-    if (__any_sync(0xffffffffu, s.big.hi != 0.f || s.small.hi != 0.f))
-      d += s.big.value() * 1.3937965749081639e+42 +     // 2^140
-           s.small.value() * 6.2230152778611417e-61;    // 2^-200
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-    if (lane == 0) shared[warp] = d;
-    __syncthreads();
-    d = 0.0;
-    if (warp == 0) {
-      d = lane < kThreads / 32 ? shared[lane] : 0.0;
-#pragma unroll
-      for (int m = 8; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+    s.mid.add_lanes();
+    if (__any_sync(0xffffffffu, s.big.hi != 0.f || s.small.hi != 0.f)) {
+      s.big.add_lanes();
+      s.small.add_lanes();
     }
+    if (lane == 0) shared[warp] = {s.mid, s.big, s.small};
+    __syncthreads();
+    if (warp != 0) return 0.0;
+    const Joined j = lane < kWarps ? shared[lane] : Joined{};
+    double d = j.mid.value();
+    if (__any_sync(0xffffffffu, j.big.hi != 0.f || j.small.hi != 0.f))
+      d += j.big.value() * 1.3937965749081639e+42 +     // 2^140
+           j.small.value() * 6.2230152778611417e-61;    // 2^-200
+#pragma unroll
+    for (int m = kWarps / 2; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
     return d;
   }
 }
@@ -316,8 +331,34 @@ __device__ __forceinline__ double join(bool inf, double a, double b) {
   return a != a || b != b ? a + b : (a > b ? a : b);   // (a NaN stays)
 }
 
-__device__ __forceinline__ float norm_of(bool inf, double total) {
-  return static_cast<float>(inf ? total : sqrt(total));
+// Where partial sums come together.
+struct Together {
+  double part[kThreads];
+  float norm;
+};
+
+// The norm from `count` partial sums, in every thread of the CTA: fetched by all threads at once,
+// added by one warp.
+template <bool kInf>
+__device__ __forceinline__ float norm_of(const double* parts, int count, Together& t) {
+  double d = 0.0;
+  for (int i0 = 0; i0 < count; i0 += kThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    if (i0 > 0) __syncthreads();
+    if (i < count) t.part[threadIdx.x] = parts[i];
+    __syncthreads();
+    if (threadIdx.x < 32)
+      for (int k = static_cast<int>(threadIdx.x); k < min(kThreads, count - i0); k += 32)
+        d = join(kInf, d, t.part[k]);
+  }
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) d = join(kInf, d, __shfl_xor_sync(0xffffffffu, d, m));
+    const float norm = static_cast<float>(kInf ? d : sqrt(d));
+    if (threadIdx.x == 0) t.norm = norm;
+  }
+  __syncthreads();
+  return t.norm;
 }
 
 __device__ __forceinline__ float scale_of(float norm, float max_norm, float eps) {
@@ -337,7 +378,7 @@ struct ClipArgs {
 template <bool kInf, int kMost>
 __global__ void __launch_bounds__(kThreads, 2)
     norm_parts_kernel(const __grid_constant__ List<kMost> l, const __grid_constant__ ClipArgs a) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Joined shared[kThreads / 32];
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const Sums s = sum_chunks<kInf, kThreads>(l, blockIdx.x, gridDim.x);
@@ -345,39 +386,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) a.parts[a.part0 + blockIdx.x] = d;
 }
 
-// All partial sums, the same in every thread of every CTA.
-template <bool kInf>
-__device__ __forceinline__ double all_parts(const ClipArgs& a, double* shared) {
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-  double d = 0.0;
-  for (int i = static_cast<int>(threadIdx.x); i < a.part_count; i += kThreads)
-    d = join(kInf, d, __ldcg(a.parts + i));
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) d = join(kInf, d, __shfl_xor_sync(0xffffffffu, d, m));
-  if (lane == 0) shared[warp] = d;
-  __syncthreads();
-  d = 0.0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) d = join(kInf, d, shared[i]);
-  return d;
-}
-
 template <bool kInf>
 __global__ void __launch_bounds__(kThreads) norm_total_kernel(const __grid_constant__ ClipArgs a) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Together together;
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const double d = all_parts<kInf>(a, shared);
-  if (threadIdx.x == 0) *a.norm = norm_of(kInf, d);
+  const float norm = norm_of<kInf>(a.parts, a.part_count, together);
+  if (threadIdx.x == 0) *a.norm = norm;
 }
 
 template <bool kInf, int kMost>
 __global__ void __launch_bounds__(kThreads, 2)
     clip_kernel(const __grid_constant__ List<kMost> l, const __grid_constant__ ClipArgs a) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Together together;
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const float norm = norm_of(kInf, all_parts<kInf>(a, shared));
+  const float norm = norm_of<kInf>(a.parts, a.part_count, together);
   if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
   scale_chunks<kThreads>(l, blockIdx.x, gridDim.x, scale_of(norm, a.max_norm, a.eps));
 }
@@ -386,8 +410,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 // the latencies of many small tensors pass together.
 template <bool kInf, bool kClip>
 __global__ void __launch_bounds__(kThreads)
-    small_list_kernel(const __grid_constant__ List<kFew> l, const __grid_constant__ ClipArgs a) {
-  __shared__ double shared[kThreads / 32];
+    small_list_kernel(const __grid_constant__ List<kFew> list, const __grid_constant__ ClipArgs a) {
+  // The list in shared memory, fetched while the kernel before this one ends: read where it is
+  // needed, each of its lines would be a miss of the constant cache in its own turn.
+  __shared__ List<kFew> l;
+  static_assert(sizeof(l) % 4 == 0, "copied by words");
+  for (int i = static_cast<int>(threadIdx.x); i < static_cast<int>(sizeof(l) / 4); i += kThreads)
+    reinterpret_cast<uint32_t*>(&l)[i] = reinterpret_cast<const uint32_t*>(&list)[i];
+  __syncthreads();
+  __shared__ Joined shared[kThreads / 32];
   __shared__ double all[kCluster];
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   if (gridDim.x > 1) ptx::cluster_arrive();   // (waited for before others' memory is written)
@@ -412,9 +443,8 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) all[0] = d;
     __syncthreads();
   }
-  double sum = all[0];
-  for (uint32_t r = 1; r < of; ++r) sum = join(kInf, sum, all[r]);
-  const float norm = norm_of(kInf, sum);
+  __shared__ Together together;
+  const float norm = norm_of<kInf>(all, static_cast<int>(of), together);
   if (rank == 0 && threadIdx.x == 0) *a.norm = norm;
   if constexpr (kClip) scale_chunks<32>(l, warp, warps, scale_of(norm, a.max_norm, a.eps));
 }
