@@ -654,4 +654,5 @@ from .moe import (  # noqa: E402 - needs the definitions above
 from .training import (  # noqa: E402
     ClippedGrads, clip_grad_norm, grad_norm, grouped_mm, grouped_mm_weight_grad,
     mslkb_clip_grad_norm, mslkb_grad_norm, mslkb_grad_norm_workspace_bytes, mslkb_grouped_mm,
-    mslkb_grouped_mm_weight_grad)
+    mslkb_grouped_mm_weight_grad, mslkb_grouped_mm_weight_grad_workspace_bytes,
+    mslkb_grouped_mm_workspace_bytes)

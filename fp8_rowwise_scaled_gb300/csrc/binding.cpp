@@ -485,9 +485,11 @@ PyObject* grouped_mm(PyObject* const* a) {
   const void* m_sizes = c.dense(a[2], "m_sizes", at::kLong, {G});
   void* out = c.dense(a[4], "out", c.type, {M, N});
   void* s = c.stream(a[5]);
+  const int64_t bytes = mslkb_grouped_mm_workspace_bytes(xp, wp, M, G, N, K, ldx, turned);
+  const Scratch workspace(bytes, s);
   return run([&] {
     return mslkb_grouped_mm(xp, wp, static_cast<const int64_t*>(m_sizes), out, M, G, N, K, ldx,
-                            turned, c.dtype, s);
+                            turned, c.dtype, workspace.p, bytes, s);
   });
 }
 
@@ -508,9 +510,12 @@ PyObject* grouped_mm_weight_grad(PyObject* const* a) {
   const void* add = c.dense_or_null(a[3], "add", type, {G, N, K});
   void* out = c.dense(a[4], "out", type, {G, N, K});
   void* s = c.stream(a[5]);
+  const int64_t bytes =
+      mslkb_grouped_mm_weight_grad_workspace_bytes(dyp, xp, M, N, K, lddy, ldx);
+  const Scratch workspace(bytes, s);
   return run([&] {
     return mslkb_grouped_mm_weight_grad(dyp, xp, static_cast<const int64_t*>(m_sizes), add, out, M,
-                                        G, N, K, lddy, ldx, c.dtype, fp32, s);
+                                        G, N, K, lddy, ldx, c.dtype, fp32, workspace.p, bytes, s);
   });
 }
 

@@ -40,24 +40,26 @@ mslkb_status encode(const MmParams& p, CUtensorMap (&maps)[3]) {
   const uint64_t C = p.C, K = p.K, G = p.G, total = p.total, R = p.R;
   const uint64_t ldp = 2 * p.ldp, ldq = 2 * p.ldq;
   const uint32_t kbk = Cfg::kBK;
-  mslkb_status s;
-  if constexpr (Cfg::kMode == Mm::kRows) {
-    const uint64_t extent[3] = {K, C, G}, stride[2] = {2 * K, 2 * K * C};
-    const uint32_t box[3] = {64, 128, 1};
-    s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
-  } else if constexpr (Cfg::kMode == Mm::kTurned) {
-    const uint64_t extent[3] = {C, K, G}, stride[2] = {2 * C, 2 * K * C};
-    const uint32_t box[3] = {64, kbk, 1};
-    s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
-  } else {
-    const uint64_t extent[2] = {C, total};
-    const uint32_t box[2] = {64, kbk};
-    s = encode_map16(&maps[0], p.P, 2, extent, &ldp, box);
-  }
-  if (s == MSLKB_OK) {
-    const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
-    const uint32_t box[2] = {64, Cfg::kGrad ? kbk : static_cast<uint32_t>(Cfg::kBoxQ)};
-    s = encode_map16(&maps[1], p.Q, 2, extent, &ldq, box);
+  mslkb_status s = MSLKB_OK;
+  if (p.sums) {
+    if constexpr (Cfg::kMode == Mm::kRows) {
+      const uint64_t extent[3] = {K, C, G}, stride[2] = {ldp, ldp * C};
+      const uint32_t box[3] = {64, 128, 1};
+      s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
+    } else if constexpr (Cfg::kMode == Mm::kTurned) {
+      const uint64_t extent[3] = {C, K, G}, stride[2] = {ldp, ldp * K};
+      const uint32_t box[3] = {64, kbk, 1};
+      s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
+    } else {
+      const uint64_t extent[2] = {C, total};
+      const uint32_t box[2] = {64, kbk};
+      s = encode_map16(&maps[0], p.P, 2, extent, &ldp, box);
+    }
+    if (s == MSLKB_OK) {
+      const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
+      const uint32_t box[2] = {64, Cfg::kGrad ? kbk : static_cast<uint32_t>(Cfg::kBoxQ)};
+      s = encode_map16(&maps[1], p.Q, 2, extent, &ldq, box);
+    }
   }
   if (s == MSLKB_OK && Cfg::kAddRing) {
     const uint64_t bytes = p.out32 ? 4 : 2;
@@ -68,35 +70,22 @@ mslkb_status encode(const MmParams& p, CUtensorMap (&maps)[3]) {
   return s;
 }
 
-// Rows that TMA can fetch: 16-byte aligned, and so spaced.
-template <Mm kMode>
-bool by_tma(const MmParams& p) {
-  const int64_t row_p = kMode == Mm::kGrad ? p.ldp : (kMode == Mm::kRows ? p.K : p.C);
-  return aligned_to(p.P, 16) && aligned_to(p.Q, 16) && row_p % 8 == 0 && p.ldq % 8 == 0 &&
-         (p.add == nullptr ||
-          (aligned_to(p.add, 16) && static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2) % 16 == 0));
-}
-
 template <class Cfg>
 mslkb_status run_as(const MmParams& p, int sms, void* stream) {
   CUtensorMap maps[3];
   std::memset(maps, 0, sizeof maps);
-  if (Cfg::kTma) {
-    const mslkb_status s = encode<Cfg>(p, maps);
-    if (s != MSLKB_OK) return s;
-  }
-  return launch<Cfg>(p, maps, sms, stream);
+  const mslkb_status s = encode<Cfg>(p, maps);
+  return s != MSLKB_OK ? s : launch<Cfg>(p, maps, sms, stream);
 }
 
 template <Mm kMode>
 mslkb_status run(const MmParams& p, int sms, void* stream) {
-  const bool sums = kMode == Mm::kGrad ? p.total > 0 : p.K > 0;
-  if (!sums || !by_tma<kMode>(p)) return run_as<MmCfg<kMode, false, 1, 128, 1, 4, 4>>(p, sms, stream);
   if constexpr (kMode == Mm::kGrad) {
-    if (p.add != nullptr)
-      return run_as<MmCfg<kMode, true, 2, 256, 1, 4, 8, true>>(p, sms, stream);
+    const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
+    if (p.add != nullptr && aligned_to(p.add, 16) && row % 16 == 0)
+      return run_as<MmCfg<kMode, 2, 256, 1, 4, 8, true>>(p, sms, stream);
   }
-  return run_as<MmCfg<kMode, true, 2, 256, 1, 6, 8>>(p, sms, stream);
+  return run_as<MmCfg<kMode, 2, 256, 1, 6, 8>>(p, sms, stream);
 }
 
 bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
@@ -104,14 +93,79 @@ bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
          K <= kMaxSize && G <= kMaxGroups;
 }
 
+// An operand as the call gives it: rows of a matrix, or of all experts' (per_expert rows each).
+struct Operand {
+  const void* at;
+  int64_t rows, cols, ld, per_expert;
+
+  // TMA fetches rows that start on 16 bytes and are spaced by multiples of 16.
+  bool fits() const { return aligned_to(at, 16) && (rows <= 1 || ld % 8 == 0); }
+  int64_t copy_ld() const { return ceil_to(cols, 8) * 8; }
+  int64_t copy_bytes() const {
+    return fits() || rows == 0 || cols == 0 ? 0 : ceil_to(rows * copy_ld() * 2, 256) * 256;
+  }
+};
+
+// The operands as they are, or copied to aligned rows in the workspace.
+mslkb_status align_operands(Operand (&o)[2], const int64_t* m_sizes, void* workspace, int sms,
+                            void* stream) {
+  AlignedCopy c[2] = {};
+  int n = 0;
+  uint8_t* to = static_cast<uint8_t*>(workspace);
+  int64_t units = 0;
+  for (Operand& p : o) {
+    const int64_t bytes = p.copy_bytes();
+    if (bytes == 0) {
+      if (p.rows <= 1) p.ld = p.copy_ld();
+      continue;
+    }
+    c[n++] = {static_cast<const uint16_t*>(p.at), reinterpret_cast<uint16_t*>(to), p.ld,
+              p.copy_ld(), p.rows, static_cast<int32_t>(p.cols),
+              static_cast<int32_t>(p.per_expert)};
+    units += p.rows * ceil_to(p.cols, kCopyCols);
+    p.at = to;
+    p.ld = p.copy_ld();
+    to += bytes;
+  }
+  if (n == 0) return MSLKB_OK;
+  const int64_t ctas = ceil_to(units, kCopyThreads / 32), most = 8 * sms;
+  return launch_status(launch_dependent(
+      aligned_rows_kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+      dim3(kCopyThreads), 0, stream, c[0], c[1], m_sizes));
+}
+
+mslkb_status workspace_status(const Operand (&o)[2], const void* workspace, int64_t bytes) {
+  const int64_t need = o[0].copy_bytes() + o[1].copy_bytes();
+  if (need == 0) return MSLKB_OK;
+  return workspace != nullptr && aligned_to(workspace, 16) && bytes >= need ? MSLKB_OK
+                                                                            : MSLKB_ERR_WORKSPACE;
+}
+
+void mm_operands(Operand (&o)[2], const void* x, const void* w, int64_t total_M, int64_t G,
+                 int64_t N, int64_t K, int64_t ldx, int32_t transposed) {
+  const int64_t rows = transposed ? K : N, cols = transposed ? N : K;
+  o[0] = {w, G * rows, cols, cols, rows};
+  o[1] = {x, total_M, K, ldx, 0};
+}
+
 }  // namespace
 }  // namespace mslkb
 
 extern "C" {
 
+int64_t mslkb_grouped_mm_workspace_bytes(const void* x, const void* w, int64_t total_M, int64_t G,
+                                         int64_t N, int64_t K, int64_t ldx, int32_t transposed) {
+  using namespace mslkb;
+  if (!sizes_ok(total_M, G, N, K) || total_M == 0 || G == 0 || N == 0) return 0;
+  Operand o[2];
+  mm_operands(o, x, w, total_M, G, N, K, ldx, transposed);
+  return o[0].copy_bytes() + o[1].copy_bytes();
+}
+
 mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_sizes, void* out,
                               int64_t total_M, int64_t G, int64_t N, int64_t K, int64_t ldx,
-                              int32_t transposed, int32_t dtype, void* stream) {
+                              int32_t transposed, int32_t dtype, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
   using namespace mslkb;
   if (!sizes_ok(total_M, G, N, K) || ldx < K || ldx > MSLKB_MAX_DIM) return MSLKB_ERR_SHAPE;
   if (dtype != MSLKB_BF16 && dtype != MSLKB_FP16) return MSLKB_ERR_DTYPE;
@@ -120,30 +174,46 @@ mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_siz
     return MSLKB_ERR_NULL;
   if (!aligned_to(x, 2) || !aligned_to(w, 2) || !aligned_to(out, 2) || !aligned_to(m_sizes, 8))
     return MSLKB_ERR_ALIGN;
-  DeviceHandles h;
-  mslkb_status s = device_handles(&h);
+  Operand o[2];
+  mm_operands(o, x, w, total_M, G, N, K, ldx, transposed);
+  mslkb_status s = workspace_status(o, workspace, workspace_bytes);
   if (s != MSLKB_OK) return s;
+  DeviceHandles h;
+  if ((s = device_handles(&h)) != MSLKB_OK) return s;
+  const TraceRange range("grouped_mm", total_M);
+  if ((s = align_operands(o, m_sizes, workspace, h.sms, stream)) != MSLKB_OK) return s;
   MmParams p{};
-  p.P = static_cast<const uint16_t*>(w);
-  p.Q = static_cast<const uint16_t*>(x);
+  p.P = static_cast<const uint16_t*>(o[0].at);
+  p.Q = static_cast<const uint16_t*>(o[1].at);
+  p.ldp = o[0].ld;
+  p.ldq = o[1].ld;
   p.m_sizes = m_sizes;
   p.out = out;
   p.status = h.status;
   p.timeout_ns = h.timeout_ns;
-  p.ldq = ldx;
   p.total = static_cast<int32_t>(total_M);
   p.G = static_cast<int32_t>(G);
   p.C = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
   p.bf16 = dtype == MSLKB_BF16;
-  const TraceRange range("grouped_mm", total_M);
+  p.sums = K > 0;
   return transposed ? run<Mm::kTurned>(p, h.sms, stream) : run<Mm::kRows>(p, h.sms, stream);
+}
+
+int64_t mslkb_grouped_mm_weight_grad_workspace_bytes(const void* dy, const void* x,
+                                                     int64_t total_M, int64_t N, int64_t K,
+                                                     int64_t lddy, int64_t ldx) {
+  using namespace mslkb;
+  if (!sizes_ok(total_M, 0, N, K)) return 0;
+  const Operand o[2] = {{x, total_M, K, ldx, 0}, {dy, total_M, N, lddy, 0}};
+  return o[0].copy_bytes() + o[1].copy_bytes();
 }
 
 mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const int64_t* m_sizes,
                                           const void* add, void* dw, int64_t total_M, int64_t G,
                                           int64_t N, int64_t K, int64_t lddy, int64_t ldx,
-                                          int32_t dtype, int32_t dw_fp32, void* stream) {
+                                          int32_t dtype, int32_t dw_fp32, void* workspace,
+                                          int64_t workspace_bytes, void* stream) {
   using namespace mslkb;
   if (!sizes_ok(total_M, G, N, K) || ldx < K || lddy < N || ldx > MSLKB_MAX_DIM ||
       lddy > MSLKB_MAX_DIM)
@@ -156,26 +226,30 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
   if (!aligned_to(x, 2) || !aligned_to(dy, 2) || !aligned_to(m_sizes, 8) ||
       !aligned_to(dw, wide) || !aligned_to(add, wide))
     return MSLKB_ERR_ALIGN;
-  DeviceHandles h;
-  mslkb_status s = device_handles(&h);
+  Operand o[2] = {{x, total_M, K, ldx, 0}, {dy, total_M, N, lddy, 0}};
+  mslkb_status s = workspace_status(o, workspace, workspace_bytes);
   if (s != MSLKB_OK) return s;
+  DeviceHandles h;
+  if ((s = device_handles(&h)) != MSLKB_OK) return s;
+  const TraceRange range("grouped_mm_weight_grad", total_M);
+  if ((s = align_operands(o, m_sizes, workspace, h.sms, stream)) != MSLKB_OK) return s;
   MmParams p{};
-  p.P = static_cast<const uint16_t*>(x);
-  p.Q = static_cast<const uint16_t*>(dy);
+  p.P = static_cast<const uint16_t*>(o[0].at);
+  p.Q = static_cast<const uint16_t*>(o[1].at);
+  p.ldp = o[0].ld;
+  p.ldq = o[1].ld;
   p.m_sizes = m_sizes;
   p.out = dw;
   p.add = add;
   p.status = h.status;
   p.timeout_ns = h.timeout_ns;
-  p.ldp = ldx;
-  p.ldq = lddy;
   p.total = static_cast<int32_t>(total_M);
   p.G = static_cast<int32_t>(G);
   p.C = static_cast<int32_t>(K);
   p.R = static_cast<int32_t>(N);
   p.bf16 = dtype == MSLKB_BF16;
   p.out32 = dw_fp32 != 0;
-  const TraceRange range("grouped_mm_weight_grad", total_M);
+  p.sums = total_M > 0;
   return run<Mm::kGrad>(p, h.sms, stream);
 }
 

@@ -26,30 +26,43 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
     """Argument and result types of this module's entry points on a loaded library."""
     p, i64, i32, f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double
     for name, args in {
-            "mslkb_grouped_mm": [p] * 4 + [i64] * 5 + [i32, i32, p],
-            "mslkb_grouped_mm_weight_grad": [p] * 5 + [i64] * 6 + [i32, i32, p],
+            "mslkb_grouped_mm": [p] * 4 + [i64] * 5 + [i32, i32, p, i64, p],
+            "mslkb_grouped_mm_weight_grad": [p] * 5 + [i64] * 6 + [i32, i32, p, i64, p],
             "mslkb_grad_norm": [p] * 3 + [i64, i32, p, p, i64, p],
             "mslkb_clip_grad_norm": [p] * 4 + [i64, i32, f64, f64, p, p, i64, p]}.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, ctypes.c_int
-    L.mslkb_grad_norm_workspace_bytes.argtypes = [i64]
-    L.mslkb_grad_norm_workspace_bytes.restype = i64
+    for name, args in {
+            "mslkb_grouped_mm_workspace_bytes": [p] * 2 + [i64] * 5 + [i32],
+            "mslkb_grouped_mm_weight_grad_workspace_bytes": [p] * 2 + [i64] * 5,
+            "mslkb_grad_norm_workspace_bytes": [i64]}.items():
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, i64
     return L
 
 
 # ---------------------------------------------------------------------------------------
 # raw C entry points (integer pointers, None for NULL)
 # ---------------------------------------------------------------------------------------
-def mslkb_grouped_mm(x, w, m_sizes, out, total_M, G, N, K, ldx, transposed, dtype,
-                     stream=0) -> int:
+def mslkb_grouped_mm_workspace_bytes(x, w, total_M, G, N, K, ldx, transposed=0) -> int:
+    return _fx.lib().mslkb_grouped_mm_workspace_bytes(x, w, total_M, G, N, K, ldx, transposed)
+
+
+def mslkb_grouped_mm(x, w, m_sizes, out, total_M, G, N, K, ldx, transposed, dtype, workspace=None,
+                     workspace_bytes=0, stream=0) -> int:
     return _fx.lib().mslkb_grouped_mm(x, w, m_sizes, out, total_M, G, N, K, ldx, transposed,
-                                      dtype, stream)
+                                      dtype, workspace, workspace_bytes, stream)
+
+
+def mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, N, K, lddy, ldx) -> int:
+    return _fx.lib().mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, N, K, lddy, ldx)
 
 
 def mslkb_grouped_mm_weight_grad(dy, x, m_sizes, add, dw, total_M, G, N, K, lddy, ldx, dtype,
-                                 dw_fp32=1, stream=0) -> int:
+                                 dw_fp32=1, workspace=None, workspace_bytes=0, stream=0) -> int:
     return _fx.lib().mslkb_grouped_mm_weight_grad(dy, x, m_sizes, add, dw, total_M, G, N, K, lddy,
-                                                  ldx, dtype, dw_fp32, stream)
+                                                  ldx, dtype, dw_fp32, workspace, workspace_bytes,
+                                                  stream)
 
 
 def mslkb_grad_norm_workspace_bytes(count) -> int:

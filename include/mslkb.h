@@ -501,9 +501,12 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  * otherwise), for experts that are kept in 16 bits and for the backward pass.  The experts'
  * rows are packed as in the stacked layout: expert g owns m_sizes[g] rows after those of the
  * experts before it, clamped to [0, total_M] as there (MSLKB_DEV_MSIZES_CLAMPED).  Products are
- * exact, sums fp32.  G is limited to MSLKB_MAX_GROUPS, every other size to 2^30; any size and
- * alignment is accepted, and rows that start and are spaced by multiples of 16 bytes (ldx, lddy,
- * the matrices' row lengths and all addresses) take the fast path.
+ * exact, sums fp32.  G is limited to MSLKB_MAX_GROUPS, every other size to 2^30.  Any size and
+ * alignment is accepted; an operand whose rows do not start on 16 bytes, or are not spaced by
+ * multiples of 16 (its address, ldx, lddy or the matrices' row length), is first copied to rows
+ * that do, in `workspace` (16-byte aligned, contents need not be initialised, not shared by calls
+ * that may run at the same time) of at least the bytes that the call's *_workspace_bytes function
+ * returns for the same arguments: 0, and then NULL will do, where both operands are aligned.
  *
  *   out[r, n] = sum over k of x[r, k] * w[g, n, k]      transposed = 0: w [G, N, K]
  *   out[r, n] = sum over k of x[r, k] * w[g, k, n]      transposed = 1: w [G, K, N]
@@ -516,10 +519,13 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  *
  * K = 0 writes +0.0 to every owned row.
  */
+MSLKB_API int64_t mslkb_grouped_mm_workspace_bytes(const void *x, const void *w, int64_t total_M,
+                                                   int64_t G, int64_t N, int64_t K, int64_t ldx,
+                                                   int32_t transposed);
 MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int64_t *m_sizes,
                                         void *out, int64_t total_M, int64_t G, int64_t N,
                                         int64_t K, int64_t ldx, int32_t transposed, int32_t dtype,
-                                        void *stream);
+                                        void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * The gradient of each expert's matrix:
@@ -532,10 +538,14 @@ MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int6
  *   dw   device, [G, N, K], fp32 if dw_fp32 is not 0, else dtype; every element is written (an
  *        expert without rows gets add, or +0.0)
  */
+MSLKB_API int64_t mslkb_grouped_mm_weight_grad_workspace_bytes(const void *dy, const void *x,
+                                                               int64_t total_M, int64_t N,
+                                                               int64_t K, int64_t lddy,
+                                                               int64_t ldx);
 MSLKB_API mslkb_status mslkb_grouped_mm_weight_grad(
     const void *dy, const void *x, const int64_t *m_sizes, const void *add, void *dw,
     int64_t total_M, int64_t G, int64_t N, int64_t K, int64_t lddy, int64_t ldx, int32_t dtype,
-    int32_t dw_fp32, void *stream);
+    int32_t dw_fp32, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * The norm of a list of gradients taken together, as one vector:

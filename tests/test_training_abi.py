@@ -18,10 +18,10 @@ def _lib():
 
 mm = call(fx.mslkb_grouped_mm, dict(
     x=P, w=P, m_sizes=P, out=P, total_M=8, G=2, N=64, K=64, ldx=64, transposed=0,
-    dtype=moe.MSLKB_BF16, stream=0))
+    dtype=moe.MSLKB_BF16, workspace=None, bytes=0, stream=0))
 weight_grad = call(fx.mslkb_grouped_mm_weight_grad, dict(
     dy=P, x=P, m_sizes=P, add=P, dw=P, total_M=8, G=2, N=64, K=64, lddy=64, ldx=64,
-    dtype=moe.MSLKB_BF16, dw_fp32=1, stream=0))
+    dtype=moe.MSLKB_BF16, dw_fp32=1, workspace=None, bytes=0, stream=0))
 BIG = (1 << 30) + 1
 
 
@@ -38,6 +38,25 @@ def test_products_refuse():
     refused(weight_grad, fx.MSLKB_ERR_DTYPE, {"dtype": moe.MSLKB_FP32}, {"dtype": 7})
     refused(weight_grad, fx.MSLKB_ERR_ALIGN, {"x": 257}, {"dy": 257}, {"dw": 258}, {"add": 258},
             {"m_sizes": 260}, {"dw_fp32": 0, "dw": 257})
+
+
+def test_products_workspace():
+    """Copies of the operands whose rows are not aligned to 16 bytes."""
+    f = fx.mslkb_grouped_mm_workspace_bytes
+    assert f(P, P, 8, 2, 64, 64, 64, 0) == 0 and f(P, P, 8, 2, 64, 63, 64, 1) == 0
+    assert f(P, P, 8, 2, 64, 63, 64, 0) == 2 * 64 * 64 * 2          # w's rows of 63
+    assert f(P, P, 8, 2, 64, 64, 65, 0) == 8 * 64 * 2               # x's, 65 apart
+    assert f(P + 2, P + 2, 8, 2, 64, 64, 64, 0) == 2 * 64 * 64 * 2 + 8 * 64 * 2
+    assert f(P, P, 1, 1, 1, 64, 65, 0) == 0                         # one row of each
+    assert f(P, P, 0, 2, 64, 63, 63, 0) == f(P, P, 8, 2, 64, -1, 63, 0) == 0
+    refused(mm, fx.MSLKB_ERR_WORKSPACE, {"ldx": 65}, {"x": P + 2},
+            {"ldx": 65, "workspace": P, "bytes": 1023}, {"ldx": 65, "workspace": P + 8,
+                                                         "bytes": 1 << 20})
+    f = fx.mslkb_grouped_mm_weight_grad_workspace_bytes
+    assert f(P, P, 8, 64, 64, 64, 64) == 0 and f(P, P, 8, 64, 64, 65, 64) == 1024
+    assert f(P, P, 8, 64, 64, 64, 65) == 1024 and f(P, P, 0, 64, 64, 65, 65) == 0
+    refused(weight_grad, fx.MSLKB_ERR_WORKSPACE, {"ldx": 65}, {"dy": P + 2},
+            {"lddy": 65, "workspace": P, "bytes": 1023})
 
 
 def test_products_of_nothing():
