@@ -21,7 +21,7 @@ int64_t tiles_bound(const MmParams& p) {
 }
 
 template <class Cfg>
-mslkb_status launch(const MmParams& p, const CUtensorMap (&maps)[3], int sms, void* stream) {
+mslkb_status launch(const MmParams& p, const MmMaps& maps, int sms, void* stream) {
   cudaError_t e = allow_smem<grouped_mm_kernel<Cfg>>();
   if (e != cudaSuccess) return launch_status(e);
   const int64_t tiles = tiles_bound<Cfg>(p);
@@ -30,56 +30,71 @@ mslkb_status launch(const MmParams& p, const CUtensorMap (&maps)[3], int sms, vo
   const int64_t grid = (tiles < workers ? tiles : workers) * Cfg::kCtas;
   return launch_status(launch_cluster(grouped_mm_kernel<Cfg>, dim3(static_cast<unsigned>(grid)),
                                       dim3(Cfg::kThreads), Cfg::kSmemBytes, Cfg::kCtas, stream, p,
-                                      maps[0], maps[1], maps[2]));
+                                      maps));
 }
 
-// Tensor maps of P, Q and what is added.  Matrices of experts have three dimensions, so that what
-// lies past one is read as zero and not as the next.
+// Tensor maps of P, Q and what is added.  Matrices of experts have a dimension of their own, so that
+// what lies past one is read as zero and not as the next.  An MN-major operand lies in shared
+// memory in pieces of 64 elements: where its rows consist of whole pieces these are a dimension
+// too, and one box fetches both pieces of a CTA.
 template <class Cfg>
-mslkb_status encode(const MmParams& p, CUtensorMap (&maps)[3]) {
+mslkb_status encode(MmParams& p, MmMaps* maps) {
   const uint64_t C = p.C, K = p.K, G = p.G, total = p.total, R = p.R;
   const uint64_t ldp = 2 * p.ldp, ldq = 2 * p.ldq;
   const uint32_t kbk = Cfg::kBK;
   mslkb_status s = MSLKB_OK;
   if (p.sums) {
+    p.p_pieces = Cfg::kPMn && C % 64 == 0;
+    p.q_pieces = Cfg::kQMn && R % 64 == 0;
     if constexpr (Cfg::kMode == Mm::kRows) {
       const uint64_t extent[3] = {K, C, G}, stride[2] = {ldp, ldp * C};
       const uint32_t box[3] = {64, 128, 1};
-      s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
+      s = encode_map16(&maps->p, p.P, 3, extent, stride, box);
     } else if constexpr (Cfg::kMode == Mm::kTurned) {
-      const uint64_t extent[3] = {C, K, G}, stride[2] = {ldp, ldp * K};
-      const uint32_t box[3] = {64, kbk, 1};
-      s = encode_map16(&maps[0], p.P, 3, extent, stride, box);
+      const uint64_t extent[4] = {64, K, C / 64, G}, stride[3] = {ldp, 128, ldp * K};
+      const uint32_t box[4] = {64, kbk, 2, 1};
+      const uint64_t extent3[3] = {C, K, G}, stride3[2] = {ldp, ldp * K};
+      const uint32_t box3[3] = {64, kbk, 1};
+      s = p.p_pieces ? encode_map16(&maps->p, p.P, 4, extent, stride, box)
+                     : encode_map16(&maps->p, p.P, 3, extent3, stride3, box3);
     } else {
-      const uint64_t extent[2] = {C, total};
-      const uint32_t box[2] = {64, kbk};
-      s = encode_map16(&maps[0], p.P, 2, extent, &ldp, box);
+      const uint64_t extent[3] = {64, total, C / 64}, stride[2] = {ldp, 128};
+      const uint32_t box[3] = {64, kbk, 2};
+      const uint64_t extent2[2] = {C, total};
+      s = p.p_pieces ? encode_map16(&maps->p, p.P, 3, extent, stride, box)
+                     : encode_map16(&maps->p, p.P, 2, extent2, &ldp, box);
     }
-    if (s == MSLKB_OK) {
-      const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
-      const uint32_t box[2] = {64, Cfg::kGrad ? kbk : static_cast<uint32_t>(Cfg::kBoxQ)};
-      s = encode_map16(&maps[1], p.Q, 2, extent, &ldq, box);
+    const uint64_t extent[2] = {Cfg::kGrad ? R : K, total};
+    const uint32_t box[2] = {64, Cfg::kGrad ? kbk : static_cast<uint32_t>(Cfg::kQRows)};
+    const uint32_t box64[2] = {64, Cfg::kGrad ? kbk : 64u};
+    if (s == MSLKB_OK) s = encode_map16(&maps->q64, p.Q, 2, extent, &ldq, box64);
+    if (s == MSLKB_OK && p.q_pieces) {
+      const uint64_t extent3[3] = {64, total, R / 64}, stride3[2] = {ldq, 128};
+      const uint32_t box3[3] = {64, kbk, 2};
+      s = encode_map16(&maps->q, p.Q, 3, extent3, stride3, box3);
+    } else if (s == MSLKB_OK) {
+      s = encode_map16(&maps->q, p.Q, 2, extent, &ldq, box);
     }
   }
   if (s == MSLKB_OK && Cfg::kAddRing) {
     const uint64_t bytes = p.out32 ? 4 : 2;
     const uint64_t extent[3] = {C, R, G}, stride[2] = {bytes * C, bytes * C * R};
     const uint32_t box[3] = {128, static_cast<uint32_t>(Cfg::kChunk), 1};
-    s = encode_map_plain(&maps[2], p.add, static_cast<int>(bytes), 3, extent, stride, box);
+    s = encode_map_plain(&maps->add, p.add, static_cast<int>(bytes), 3, extent, stride, box);
   }
   return s;
 }
 
 template <class Cfg>
-mslkb_status run_as(const MmParams& p, int sms, void* stream) {
-  CUtensorMap maps[3];
-  std::memset(maps, 0, sizeof maps);
-  const mslkb_status s = encode<Cfg>(p, maps);
+mslkb_status run_as(MmParams& p, int sms, void* stream) {
+  MmMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  const mslkb_status s = encode<Cfg>(p, &maps);
   return s != MSLKB_OK ? s : launch<Cfg>(p, maps, sms, stream);
 }
 
 template <Mm kMode>
-mslkb_status run(const MmParams& p, int sms, void* stream) {
+mslkb_status run(MmParams& p, int sms, void* stream) {
   if constexpr (kMode == Mm::kGrad) {
     const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
     if (p.add != nullptr && aligned_to(p.add, 16) && row % 16 == 0)

@@ -53,7 +53,14 @@ struct MmParams {
   int32_t K;               // contraction length (kGrad: each expert's rows instead)
   int32_t bf16;            // 1: bf16 operands, 0: fp16
   int32_t out32;           // 1: fp32 output, 0: the operands' type
+  int32_t p_pieces, q_pieces;  // an MN-major operand's 64-element pieces in one box (see encode)
   int32_t sums;            // 0: the contraction is empty everywhere, and P and Q are not read
+};
+
+// Tensor maps.  p, q: the operands, by boxes of a CTA's share of a stage; q64: by halves of
+// it, for tiles of few rows; add: what is added (kGrad).
+struct MmMaps {
+  CUtensorMap p, q, q64, add;
 };
 
 template <Mm kMode_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_,
@@ -71,7 +78,7 @@ struct MmCfg {
   static constexpr int kKB = kKB_;
   static constexpr int kStages = kStages_;
   static constexpr int kQRows = kTileN / kCtas;    // of Q in one CTA
-  static constexpr int kBoxQ = kQRows < 64 ? kQRows : 64;
+  static_assert(kQRows == 128 || kQRows == 64, "boxes of Q");
   static constexpr int kPBytes = 128 * kBK * 2;
   static constexpr int kQBytes = kQRows * kBK * 2;
   static constexpr int kStageBytes = kPBytes + kQBytes;
@@ -368,9 +375,7 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, bool ok) {
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
-    grouped_mm_kernel(const __grid_constant__ MmParams p, const __grid_constant__ CUtensorMap tmP,
-                      const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmAdd) {
+    grouped_mm_kernel(const __grid_constant__ MmParams p, const __grid_constant__ MmMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -432,8 +437,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     ptx::fence_proxy_async_smem();
   }
   if (threadIdx.x == 0 && p.sums) {
-    ptx::prefetch_tensormap(&tmP);
-    ptx::prefetch_tensormap(&tmQ);
+    ptx::prefetch_tensormap(&maps.p);
+    ptx::prefetch_tensormap(&maps.q);
+    ptx::prefetch_tensormap(&maps.q64);
   }
   if (warp == Cfg::kMmaWarp) {
     if constexpr (Cfg::kPair) {
@@ -482,9 +488,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col = c.c0 + static_cast<int32_t>(crank) * 128;
         const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
         const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
-        const int32_t boxes = (mine + Cfg::kBoxQ - 1) / Cfg::kBoxQ;
-        const uint32_t bytes =
-            Cfg::kPBytes + static_cast<uint32_t>(boxes * Cfg::kBoxQ * Cfg::kBK * 2);
+        // of Q 64 rows or 128 (of kGrad, columns) are loaded
+        const bool half = mine <= 64;
+        const uint32_t bytes = Cfg::kPBytes + static_cast<uint32_t>((half ? 64 : 128) * Cfg::kBK * 2);
         for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
@@ -511,26 +517,42 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             if constexpr (Cfg::kPair) ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
             else ptx::tma_load_3d(dst, m, bar, a, b, g);
           };
+          auto load4 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t z,
+                           int32_t g) {
+            if constexpr (Cfg::kPair) ptx::tma_load_4d_pair(dst, m, bar, a, b, z, g);
+            else ptx::tma_load_4d(dst, m, bar, a, b, z, g);
+          };
+          // (few, large operations: an SM's loads are limited by their number as well)
           if constexpr (Cfg::kMode == Mm::kRows) {
 #pragma unroll
             for (int i = 0; i < Cfg::kKB; ++i)
-              load3(dp + i * 128 * 128, &tmP, x + 64 * i, col, c.g);
+              load3(dp + i * 128 * 128, &maps.p, x + 64 * i, col, c.g);
+          } else if constexpr (Cfg::kMode == Mm::kTurned) {
+            if (p.p_pieces) {
+              load4(dp, &maps.p, 0, x, col / 64, c.g);
+            } else {
+              load3(dp, &maps.p, col, x, c.g);
+              load3(dp + Cfg::kMnPiece, &maps.p, col + 64, x, c.g);
+            }
           } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t d = dp + i * Cfg::kMnPiece;
-              if constexpr (Cfg::kGrad) load2(d, &tmP, col + 64 * i, x);
-              else load3(d, &tmP, col + 64 * i, x, c.g);
+            if (p.p_pieces) {
+              load3(dp, &maps.p, 0, x, col / 64);
+            } else {
+              load2(dp, &maps.p, col, x);
+              load2(dp + Cfg::kMnPiece, &maps.p, col + 64, x);
             }
           }
           if constexpr (Cfg::kQMn) {
-            for (int i = 0; i < boxes; ++i) load2(dq + i * Cfg::kMnPiece, &tmQ, row + 64 * i, x);
+            if (p.q_pieces && !half && row % 64 == 0) {
+              load3(dq, &maps.q, 0, x, row / 64);
+            } else {
+              load2(dq, &maps.q64, row, x);
+              if (!half) load2(dq + Cfg::kMnPiece, &maps.q64, row + 64, x);
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < Cfg::kKB; ++j)
-              for (int i = 0; i < boxes; ++i)
-                load2(dq + j * Cfg::kQRows * 128 + i * Cfg::kBoxQ * 128, &tmQ, x + 64 * j,
-                      row + Cfg::kBoxQ * i);
+              load2(dq + j * Cfg::kQRows * 128, half ? &maps.q64 : &maps.q, x + 64 * j, row);
           }
           if (++stage == Cfg::kStages) {
             stage = 0;
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       parity ^= 1u << last;
       const int32_t in = c.len - (kbs - 1) * Cfg::kBK;  // rows of the stage that are the expert's
       const int32_t lines = ((in + 15) & ~15) - in;
-      const int32_t boxes = (c.h / Cfg::kCtas + 63) / 64;
+      const int32_t boxes = c.h / Cfg::kCtas <= 64 ? 1 : 2;
       for (int32_t i = static_cast<int32_t>(lane); i < (2 + boxes) * lines * 8; i += 32) {
         const int32_t line = in + (i >> 3) % lines, piece = (i >> 3) / lines;
         const uint32_t base = piece < 2 ? s_p + last * Cfg::kPBytes + piece * Cfg::kMnPiece
@@ -655,7 +677,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         p.timeout_ns);
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
-          ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &tmAdd,
+          ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &maps.add,
                            add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * 128,
                            c.r0 + j0, c.g);
         }

@@ -26,7 +26,7 @@ struct DeviceHandles {
 };
 mslkb_status device_handles(DeviceHandles* h);
 
-// A tensor map with zero fill: `dims` (2 or 3) extents and box sides, innermost first, and the
+// A tensor map with zero fill: `dims` (2 to 4) extents and box sides, innermost first, and the
 // strides in bytes of all but the innermost.  encode_map16: of 16-bit elements, with the 128-byte
 // swizzle; encode_map_plain: of 16- or 32-bit elements, boxes row by row.
 mslkb_status encode_map16(CUtensorMap* map, const void* base, int dims, const uint64_t* extent,

@@ -819,8 +819,8 @@ mslkb_status encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType 
                         CUtensorMapSwizzle swizzle, int dims, const uint64_t* extent,
                         const uint64_t* stride, const uint32_t* box) {
   if (g_encode == nullptr) return cuda_fail(cudaErrorNotSupported);
-  cuuint64_t d[3], st[2];
-  cuuint32_t b[3], es[3] = {1, 1, 1};
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
   for (int i = 0; i < dims; ++i) {
     d[i] = extent[i];
     b[i] = box[i];
