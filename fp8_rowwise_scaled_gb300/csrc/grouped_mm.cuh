@@ -53,6 +53,7 @@ struct MmParams {
   int32_t K;               // contraction length (kGrad: each expert's rows instead)
   int32_t bf16;            // 1: bf16 operands, 0: fp16
   int32_t out32;           // 1: fp32 output, 0: the operands' type
+  int32_t wide;            // output columns of a tile per CTA: 128, or less for kRows
   int32_t p_pieces, q_pieces;  // an MN-major operand's 64-element pieces in one box (see encode)
   int32_t sums;            // 0: the contraction is empty everywhere, and P and Q are not read
 };
@@ -73,7 +74,6 @@ struct MmCfg {
   static constexpr int kCtas = kCtas_;
   static constexpr bool kPair = kCtas == 2;
   static constexpr int kTileN = kTileN_;           // output rows of a tile
-  static constexpr int kTileC = 128 * kCtas;       // output columns of a tile
   static constexpr int kBK = 64 * kKB_;            // contraction per stage: 128-byte pieces
   static constexpr int kKB = kKB_;
   static constexpr int kStages = kStages_;
@@ -133,10 +133,20 @@ struct MmTile {
   int32_t g, c0, r0, h, valid, k0, len;
 };
 
+// Output columns of a tile, and of each CTA.
+template <class Cfg>
+__device__ __forceinline__ int32_t mm_wide(const MmParams& p) {
+  return Cfg::kMode == Mm::kRows ? p.wide : 128;
+}
+template <class Cfg>
+__device__ __forceinline__ int32_t mm_tile_c(const MmParams& p) {
+  return Cfg::kCtas * mm_wide<Cfg>(p);
+}
+
 template <class Cfg>
 __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* first,
                                           const int32_t* tile_pre, int32_t t) {
-  const int32_t ct = (p.C + Cfg::kTileC - 1) / Cfg::kTileC;
+  const int32_t tile_c = mm_tile_c<Cfg>(p), ct = (p.C + tile_c - 1) / tile_c;
   MmTile o;
   int32_t local, rows;
   if constexpr (Cfg::kGrad) {
@@ -159,20 +169,17 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
     o.k0 = 0;
     o.len = p.K;
   }
-  // tiles of equal height, in bands of kBand rows of tiles, column by column of tiles
+  // row tiles in bands of kBand, column by column of tiles
   const int32_t rt = (rows + Cfg::kTileN - 1) / Cfg::kTileN;
-  const int32_t band = local / (Cfg::kBand * ct);
+  const int32_t band = rt <= Cfg::kBand ? 0 : local / (Cfg::kBand * ct);
   const int32_t in = local - band * Cfg::kBand * ct;
   const int32_t deep = min(Cfg::kBand, rt - band * Cfg::kBand);
-  const int32_t c = in / deep;
+  const int32_t c = deep == 1 ? in : (deep == Cfg::kBand ? in / Cfg::kBand : in / deep);
   const int32_t r = band * Cfg::kBand + (in - c * deep);
-  const int32_t each = (rows + rt - 1) / rt;
-  const int32_t h = (each + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
-  o.c0 = c * Cfg::kTileC;
-  const int32_t off = r * h;
-  o.valid = max(0, min(h, rows - off));
-  o.h = o.valid > 0 ? (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep : 0;
-  o.r0 = off + (Cfg::kGrad ? 0 : first[o.g]);
+  o.c0 = c * tile_c;
+  o.valid = min(Cfg::kTileN, rows - r * Cfg::kTileN);
+  o.h = (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
+  o.r0 = r * Cfg::kTileN + (Cfg::kGrad ? 0 : first[o.g]);
   return o;
 }
 
@@ -181,47 +188,60 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
 template <class Cfg>
 __device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, int32_t* tile_pre,
                                             uint32_t lane) {
-  const int32_t G = p.G, per = (G + 31) / 32;
+  // (sums are clamped as they are made, so that 32 bits hold them: total is at most 2^30)
+  const int32_t G = p.G, per = (G + 31) / 32, total = p.total;
   const int32_t g0 = min(G, static_cast<int32_t>(lane) * per), g1 = min(G, g0 + per);
-  const int64_t total = p.total;
+  auto before = [&](int32_t sum) {   // of this lane, clamped
+    int32_t v = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= static_cast<uint32_t>(d)) v = min(total, v + o);
+    }
+    v = __shfl_up_sync(0xffffffffu, v, 1);
+    return lane == 0 ? 0 : v;
+  };
   bool clamped = false;
-  int64_t sum = 0;
+  int32_t sum = 0;
   for (int32_t g = g0; g < g1; ++g) {
     const int64_t m = p.m_sizes[g];
     clamped |= m < 0 || m > total;
-    const int64_t mc = m < 0 ? 0 : (m > total ? total : m);
-    first[g] = static_cast<int32_t>(mc);
-    sum += mc;
+    const int32_t mc = static_cast<int32_t>(m < 0 ? 0 : (m > total ? total : m));
+    first[g] = mc;
+    clamped |= sum + mc > total;
+    sum = min(total, sum + mc);
   }
-  int64_t run = warp_incl_scan(sum, lane) - sum;
+  int32_t run = before(sum);
+  clamped |= run + sum > total;
   for (int32_t g = g0; g < g1; ++g) {
-    const int64_t mc = first[g];
-    first[g] = static_cast<int32_t>(run < total ? run : total);
-    run += mc;
+    const int32_t mc = first[g];
+    first[g] = run;
+    run = min(total, run + mc);
   }
-  if (lane == 31) {
-    clamped |= run > total;
-    first[G] = static_cast<int32_t>(run < total ? run : total);
-  }
+  if (lane == 31) first[G] = run;
   __syncwarp();
   if (__any_sync(0xffffffffu, clamped) && lane == 0 && blockIdx.x == 0)
     atomicOr(p.status, kStatusClamped);
-  const int64_t ct = (p.C + Cfg::kTileC - 1) / Cfg::kTileC;
+  const int32_t ct = (p.C + mm_tile_c<Cfg>(p) - 1) / mm_tile_c<Cfg>(p);
   if constexpr (Cfg::kGrad) {
-    if (lane == 0)
-      tile_pre[G] = static_cast<int32_t>(G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN));
+    if (lane == 0) tile_pre[G] = G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
   } else {
-    auto tiles = [&](int32_t g) {
-      return ct * ((first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN);
-    };
-    int64_t mine = 0;
+    // (row tiles first: there are at most total / kTileN + G of them)
+    auto tiles = [&](int32_t g) { return (first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN; };
+    int32_t mine = 0;
     for (int32_t g = g0; g < g1; ++g) mine += tiles(g);
-    int64_t at = warp_incl_scan(mine, lane) - mine;
+    int32_t at = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= static_cast<uint32_t>(d)) at += o;
+    }
+    at -= mine;
     for (int32_t g = g0; g < g1; ++g) {
-      tile_pre[g] = static_cast<int32_t>(at);
+      tile_pre[g] = at * ct;
       at += tiles(g);
     }
-    if (lane == 31) tile_pre[G] = static_cast<int32_t>(at);
+    if (lane == 31) tile_pre[G] = at * ct;
   }
 }
 
@@ -458,7 +478,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   else __syncthreads();
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
-  const int32_t tiles = tile_pre[p.G];
+  const int32_t tiles = tile_pre[p.G], wide = mm_wide<Cfg>(p);
 
   // Tile i of this CTA (or pair), from the ring: by a whole warp, or by one lane of it.  False past
   // the last one, or if a wait gave up.
@@ -485,12 +505,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       MmTile c;
       for (int32_t i = 0; ok && take(i, c, false); ++i) {
         if (c.len == 0) continue;
-        const int32_t col = c.c0 + static_cast<int32_t>(crank) * 128;
+        const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide;
         const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
         const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
         // of Q 64 rows or 128 (of kGrad, columns) are loaded
         const bool half = mine <= 64;
-        const uint32_t bytes = Cfg::kPBytes + static_cast<uint32_t>((half ? 64 : 128) * Cfg::kBK * 2);
+        const uint32_t bytes =
+            static_cast<uint32_t>((wide + (half ? 64 : 128)) * Cfg::kBK * 2);
         for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
             ok = false;
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (!ok) break;
           ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
           ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &maps.add,
-                           add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * 128,
+                           add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * wide,
                            c.r0 + j0, c.g);
         }
       }
@@ -695,8 +716,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       MmTile c{-1, 0, 0, 0, 0, 0, 0};
       if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
       const bool more = t0 + 31ll * workers < tiles;   // (else the last of these says so)
-      // tiles of rounded heights past a group's last row have no rows
-      uint32_t left = __ballot_sync(0xffffffffu, c.g < 0 || c.h > 0);
+      uint32_t left = 0xffffffffu;
       if (!more) left &= (2u << (__ffs(__ballot_sync(0xffffffffu, c.g < 0)) - 1)) - 1u;
       while (left != 0) {
         const int src = __ffs(left) - 1;
@@ -738,9 +758,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       MmTile c;
       for (int32_t i = 0;; ++i) {
         bool ok = take(i, c, true);
-        const int32_t col0 = c.c0 + static_cast<int32_t>(crank) * 128;
+        const int32_t col0 = c.c0 + static_cast<int32_t>(crank) * wide;
+        const int32_t cols = min(wide, p.C - col0);   // of this CTA
         const int32_t col = col0 + static_cast<int32_t>(q * 32u + lane);
-        const bool in = col < p.C;
+        const bool in = col < col0 + cols;
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
         int64_t at = row0 * p.C;
         const bool any = ok && c.len > 0;  // else the empty sum
@@ -795,7 +816,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
           }
           if constexpr (kWhole) {
-            MmRows<kN>::store(out0 + at + col0, p.C, n, p.C - col0, q, v, bf16, stage, bar, lane);
+            MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
           } else {
             auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
             if constexpr (kLoad) {
@@ -840,17 +861,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   // ---------------------------------------------------------------- teardown
   ptx::tc_fence_before_sync();
-  __syncthreads();
-  bool aborting = *abort_flag != 0u;
   if constexpr (Cfg::kPair) {
     // neither CTA leaves while the other may signal its barriers, and both wait out what is in
     // flight if either gave up
+    if (lane == 0 && *abort_flag != 0u)
+      ptx::st_shared_cluster_u32(
+          ptx::mapa_shared(ptx::smem_addr(smem + Cfg::kOffMisc + 4), crank ^ 1u), 1u);
     ptx::cluster_sync();
-    aborting |= ptx::ld_shared_cluster_u32(
-                    ptx::mapa_shared(ptx::smem_addr(smem + Cfg::kOffMisc + 4), crank ^ 1u)) != 0u;
-    ptx::cluster_sync();
+  } else {
+    __syncthreads();
   }
-  if (aborting) {
+  if (*abort_flag != 0u) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - t0 < 2000000ull) ptx::nanosleep(1000);
   }
