@@ -511,7 +511,7 @@ PyObject* grouped_mm_weight_grad(PyObject* const* a) {
   void* out = c.dense(a[4], "out", type, {G, N, K});
   void* s = c.stream(a[5]);
   const int64_t bytes =
-      mslkb_grouped_mm_weight_grad_workspace_bytes(dyp, xp, M, N, K, lddy, ldx);
+      mslkb_grouped_mm_weight_grad_workspace_bytes(dyp, xp, M, G, N, K, lddy, ldx);
   const Scratch workspace(bytes, s);
   return run([&] {
     return mslkb_grouped_mm_weight_grad(dyp, xp, static_cast<const int64_t*>(m_sizes), add, out, M,

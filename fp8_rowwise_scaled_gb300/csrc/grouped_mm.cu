@@ -24,7 +24,7 @@ template <class Cfg>
 mslkb_status launch(const MmParams& p, const MmMaps& maps, int sms, void* stream) {
   cudaError_t e = allow_smem<grouped_mm_kernel<Cfg>>();
   if (e != cudaSuccess) return launch_status(e);
-  const int64_t tiles = tiles_bound<Cfg>(p);
+  const int64_t tiles = tiles_bound<Cfg>(p) * p.splits;
   if (tiles > INT32_MAX) return MSLKB_ERR_SHAPE;
   const int64_t workers = sms / Cfg::kCtas;
   const int64_t grid = (tiles < workers ? tiles : workers) * Cfg::kCtas;
@@ -90,10 +90,11 @@ mslkb_status encode(MmParams& p, MmMaps* maps) {
 // which the worker of most columns has fewest, if as many experts have rows as can have.  One token
 // on 8 experts of 4096 x 7168 on GB300, 76 pairs: two rounds of 256 columns (128 tiles) 84 us, of
 // 216 (152 tiles) 74.
+// (Split contractions fill the workers by themselves.)
 template <class Cfg>
 int32_t tile_columns(const MmParams& p, int sms) {
   const int64_t experts = p.G < p.total ? p.G : p.total, workers = sms / Cfg::kCtas;
-  if (Cfg::kMode != Mm::kRows || p.total > 128 * experts) return 128;
+  if (Cfg::kMode != Mm::kRows || p.splits > 1 || p.total > 128 * experts) return 128;
   auto columns = [&](int64_t w) {
     return ceil_to(experts * ceil_to(p.C, Cfg::kCtas * w), workers) * w;
   };
@@ -117,7 +118,7 @@ template <Mm kMode>
 mslkb_status run(MmParams& p, int sms, void* stream) {
   if constexpr (kMode == Mm::kGrad) {
     const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
-    if (p.add != nullptr && aligned_to(p.add, 16) && row % 16 == 0)
+    if (p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0)
       return run_as<MmCfg<kMode, 2, 256, 1, 4, 8, true>>(p, sms, stream);
   }
   return run_as<MmCfg<kMode, 2, 256, 1, 6, 8>>(p, sms, stream);
@@ -126,6 +127,73 @@ mslkb_status run(MmParams& p, int sms, void* stream) {
 bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
   return total >= 0 && G >= 0 && N >= 0 && K >= 0 && total <= kMaxSize && N <= kMaxSize &&
          K <= kMaxSize && G <= kMaxGroups;
+}
+
+// Parts of each contraction.  Few tiles leave most pairs without one, and a pair takes some 0.3 us
+// for a stage of 64, however few the rows (of 4096 x 7168, one expert and row: 39 us); so the
+// contractions of up to two rounds of tiles are split, into the number of parts that takes least by
+// this reckoning: rounds of the pairs x (stages of a part, and a tile's ends), and for the
+// slices' sum a launch and their bytes.
+constexpr int kPairs = 76, kMostSplits = 16, kLeastStages = 4;
+int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements) {
+  const int64_t stages = ceil_to(contraction, 64);
+  if (tiles > 2 * kPairs) return 1;
+  int32_t best = 1;
+  double least = 0.0;
+  for (int32_t s = 1; s <= kMostSplits && (s == 1 || s * kLeastStages <= stages); ++s) {
+    const double rounds = static_cast<double>(ceil_to(tiles * s, kPairs));
+    double us = rounds * (0.3 * static_cast<double>(ceil_to(stages, s)) + 1.0);
+    if (s > 1) us += 4.0 + static_cast<double>(elements) * 4.0 * 2.0 * s / 6e6;
+    if (s == 1 || us < least) least = us, best = s;
+  }
+  return best;
+}
+
+int64_t slice_of(int64_t elements) { return ceil_to(elements, 4) * 4; }
+
+int32_t mm_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
+  if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
+  const int64_t row_tiles = total_M / 256 + (G < total_M ? G : total_M);
+  return splits_of(row_tiles * ceil_to(N, 256), K, total_M * N);
+}
+
+int32_t grad_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
+  if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
+  return splits_of(G * ceil_to(N, 256) * ceil_to(K, 256), ceil_to(total_M, G), G * N * K);
+}
+
+// The slices' place in the workspace, behind the operands' copies.
+int64_t slices_bytes(int32_t splits, int64_t elements) {
+  return splits > 1 ? splits * slice_of(elements) * 4 : 0;
+}
+
+// Runs the product into slices, and sums them.
+template <class F>
+mslkb_status run_split(MmParams& p, int64_t elements, bool owned_rows, float* slices, int sms,
+                       void* stream, F run_product) {
+  SliceSum s{};
+  s.slices = slices;
+  s.out = p.out;
+  s.add = p.add;
+  s.m_sizes = owned_rows ? p.m_sizes : nullptr;
+  s.slice = slice_of(elements);
+  s.n = elements;
+  s.splits = p.splits;
+  s.G = p.G;
+  s.total = p.total;
+  s.C = p.C;
+  s.bf16 = p.bf16;
+  s.out32 = p.out32;
+  p.out = slices;
+  p.add = nullptr;
+  p.out32 = 1;
+  p.slice = s.slice;
+  const mslkb_status status = run_product();
+  if (status != MSLKB_OK) return status;
+  const int64_t ctas = ceil_to(elements, 4 * kSumThreads), most = 8 * sms;
+  return launch_status(launch_dependent(slice_sum_kernel,
+                                        dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+                                        dim3(kSumThreads), 0, stream, s));
 }
 
 // An operand as the call gives it: rows of a matrix, or of all experts' (per_expert rows each).
@@ -169,8 +237,9 @@ mslkb_status align_operands(Operand (&o)[2], const int64_t* m_sizes, void* works
       dim3(kCopyThreads), 0, stream, c[0], c[1], m_sizes));
 }
 
-mslkb_status workspace_status(const Operand (&o)[2], const void* workspace, int64_t bytes) {
-  const int64_t need = o[0].copy_bytes() + o[1].copy_bytes();
+int64_t copies_bytes(const Operand (&o)[2]) { return o[0].copy_bytes() + o[1].copy_bytes(); }
+
+mslkb_status workspace_status(int64_t need, const void* workspace, int64_t bytes) {
   if (need == 0) return MSLKB_OK;
   return workspace != nullptr && aligned_to(workspace, 16) && bytes >= need ? MSLKB_OK
                                                                             : MSLKB_ERR_WORKSPACE;
@@ -194,7 +263,7 @@ int64_t mslkb_grouped_mm_workspace_bytes(const void* x, const void* w, int64_t t
   if (!sizes_ok(total_M, G, N, K) || total_M == 0 || G == 0 || N == 0) return 0;
   Operand o[2];
   mm_operands(o, x, w, total_M, G, N, K, ldx, transposed);
-  return o[0].copy_bytes() + o[1].copy_bytes();
+  return copies_bytes(o) + slices_bytes(mm_splits(total_M, G, N, K), total_M * N);
 }
 
 mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_sizes, void* out,
@@ -211,7 +280,10 @@ mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_siz
     return MSLKB_ERR_ALIGN;
   Operand o[2];
   mm_operands(o, x, w, total_M, G, N, K, ldx, transposed);
-  mslkb_status s = workspace_status(o, workspace, workspace_bytes);
+  const int64_t copies = copies_bytes(o);
+  const int32_t splits = mm_splits(total_M, G, N, K);
+  mslkb_status s = workspace_status(copies + slices_bytes(splits, total_M * N), workspace,
+                                    workspace_bytes);
   if (s != MSLKB_OK) return s;
   DeviceHandles h;
   if ((s = device_handles(&h)) != MSLKB_OK) return s;
@@ -232,16 +304,22 @@ mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_siz
   p.K = static_cast<int32_t>(K);
   p.bf16 = dtype == MSLKB_BF16;
   p.sums = K > 0;
-  return transposed ? run<Mm::kTurned>(p, h.sms, stream) : run<Mm::kRows>(p, h.sms, stream);
+  p.splits = splits;
+  auto product = [&] {
+    return transposed ? run<Mm::kTurned>(p, h.sms, stream) : run<Mm::kRows>(p, h.sms, stream);
+  };
+  if (splits == 1) return product();
+  float* slices = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + copies);
+  return run_split(p, total_M * N, true, slices, h.sms, stream, product);
 }
 
 int64_t mslkb_grouped_mm_weight_grad_workspace_bytes(const void* dy, const void* x,
-                                                     int64_t total_M, int64_t N, int64_t K,
-                                                     int64_t lddy, int64_t ldx) {
+                                                     int64_t total_M, int64_t G, int64_t N,
+                                                     int64_t K, int64_t lddy, int64_t ldx) {
   using namespace mslkb;
-  if (!sizes_ok(total_M, 0, N, K)) return 0;
+  if (!sizes_ok(total_M, G, N, K) || G == 0 || N == 0 || K == 0) return 0;
   const Operand o[2] = {{x, total_M, K, ldx, 0}, {dy, total_M, N, lddy, 0}};
-  return o[0].copy_bytes() + o[1].copy_bytes();
+  return copies_bytes(o) + slices_bytes(grad_splits(total_M, G, N, K), G * N * K);
 }
 
 mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const int64_t* m_sizes,
@@ -262,7 +340,10 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
       !aligned_to(dw, wide) || !aligned_to(add, wide))
     return MSLKB_ERR_ALIGN;
   Operand o[2] = {{x, total_M, K, ldx, 0}, {dy, total_M, N, lddy, 0}};
-  mslkb_status s = workspace_status(o, workspace, workspace_bytes);
+  const int64_t copies = copies_bytes(o);
+  const int32_t splits = grad_splits(total_M, G, N, K);
+  mslkb_status s = workspace_status(copies + slices_bytes(splits, G * N * K), workspace,
+                                    workspace_bytes);
   if (s != MSLKB_OK) return s;
   DeviceHandles h;
   if ((s = device_handles(&h)) != MSLKB_OK) return s;
@@ -285,7 +366,11 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
   p.bf16 = dtype == MSLKB_BF16;
   p.out32 = dw_fp32 != 0;
   p.sums = total_M > 0;
-  return run<Mm::kGrad>(p, h.sms, stream);
+  p.splits = splits;
+  if (splits == 1) return run<Mm::kGrad>(p, h.sms, stream);
+  float* slices = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + copies);
+  return run_split(p, G * N * K, false, slices, h.sms, stream,
+                   [&] { return run<Mm::kGrad>(p, h.sms, stream); });
 }
 
 }  // extern "C"

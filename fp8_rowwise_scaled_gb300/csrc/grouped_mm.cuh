@@ -55,6 +55,8 @@ struct MmParams {
   int32_t out32;           // 1: fp32 output, 0: the operands' type
   int32_t wide;            // output columns of a tile per CTA: 128, or less for kRows
   int32_t p_pieces, q_pieces;  // an MN-major operand's 64-element pieces in one box (see encode)
+  int32_t splits;          // parts of each contraction, whose sums go to slices of out (fp32)
+  int64_t slice;           // elements from slice to slice
   int32_t sums;            // 0: the contraction is empty everywhere, and P and Q are not read
 };
 
@@ -128,9 +130,9 @@ struct MmCfg {
 };
 
 // A tile: its group (-1: past the last tile), first output column and row, rows (h: rounded up, valid: real), and the
-// contraction [k0, k0 + len) (kGrad: rows of x and dy).
+// contraction [k0, k0 + len) (kGrad: rows of x and dy), or the part of it that is this tile's.
 struct MmTile {
-  int32_t g, c0, r0, h, valid, k0, len;
+  int32_t g, c0, r0, h, valid, k0, len, part;
 };
 
 // Output columns of a tile, and of each CTA.
@@ -148,6 +150,11 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
                                           const int32_t* tile_pre, int32_t t) {
   const int32_t tile_c = mm_tile_c<Cfg>(p), ct = (p.C + tile_c - 1) / tile_c;
   MmTile o;
+  o.part = 0;
+  if (p.splits > 1) {
+    o.part = t / tile_pre[p.G];
+    t -= o.part * tile_pre[p.G];
+  }
   int32_t local, rows;
   if constexpr (Cfg::kGrad) {
     const int32_t per = ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
@@ -180,6 +187,13 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
   o.valid = min(Cfg::kTileN, rows - r * Cfg::kTileN);
   o.h = (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
   o.r0 = r * Cfg::kTileN + (Cfg::kGrad ? 0 : first[o.g]);
+  if (p.splits > 1) {   // by whole stages
+    const int64_t stages = (o.len + Cfg::kBK - 1) / Cfg::kBK;
+    const int32_t a = static_cast<int32_t>(stages * o.part / p.splits) * Cfg::kBK;
+    const int32_t b = static_cast<int32_t>(stages * (o.part + 1) / p.splits) * Cfg::kBK;
+    o.k0 += a;
+    o.len = min(o.len, b) - a;
+  }
   return o;
 }
 
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   else __syncthreads();
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
-  const int32_t tiles = tile_pre[p.G], wide = mm_wide<Cfg>(p);
+  const int32_t tiles = tile_pre[p.G] * p.splits, wide = mm_wide<Cfg>(p);
 
   // Tile i of this CTA (or pair), from the ring: by a whole warp, or by one lane of it.  False past
   // the last one, or if a wait gave up.
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     if (whole_warp) ok = __all_sync(0xffffffffu, ok) != 0;
     if (!ok) return false;
     const int4 a = ring[2 * slot], b = ring[2 * slot + 1];
-    c = MmTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+    c = MmTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (whole_warp) __syncwarp();
     if (!whole_warp || lane == 0) ptx::mbar_arrive(taken_bar(slot));
     return c.g >= 0;
@@ -713,7 +727,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     bool ok = true;
     for (int64_t t0 = worker; ok; t0 += 32ll * workers) {
       const int64_t t = t0 + static_cast<int64_t>(lane) * workers;
-      MmTile c{-1, 0, 0, 0, 0, 0, 0};
+      MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
       if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
       const bool more = t0 + 31ll * workers < tiles;   // (else the last of these says so)
       uint32_t left = 0xffffffffu;
@@ -728,7 +742,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (!ok) break;
         if (static_cast<int>(lane) == src) {
           ring[2 * slot] = make_int4(c.g, c.c0, c.r0, c.h);
-          ring[2 * slot + 1] = make_int4(c.valid, c.k0, c.len, 0);
+          ring[2 * slot + 1] = make_int4(c.valid, c.k0, c.len, c.part);
           ptx::mbar_arrive(tile_bar(slot));
         }
         __syncwarp();
@@ -763,7 +777,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col = col0 + static_cast<int32_t>(q * 32u + lane);
         const bool in = col < col0 + cols;
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
-        int64_t at = row0 * p.C;
+        int64_t at = row0 * p.C + c.part * p.slice;
         const bool any = ok && c.len > 0;  // else the empty sum
         const uint32_t b = used & 1u;
         const bool mine = kParts == 1 || (any ? b : static_cast<uint32_t>(i) & 1u) == part;
@@ -854,7 +868,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       else if (!load && rows) work(out16, yes, no);
       else if (!load) work(out16, no, no);
     } else {
-      if (rows) work(out16, yes, no);
+      if (p.splits > 1) work(static_cast<float*>(p.out), no, no);
+      else if (rows) work(out16, yes, no);
       else work(out16, no, no);
     }
   }
@@ -970,6 +985,79 @@ __global__ void __launch_bounds__(kCopyThreads)
       if (2 * (lane + 32 * i) < left) to[32 * i] = w;
     }
   }
+}
+
+// The sum of a split contraction's slices (and of what is added to a gradient), rounded.
+struct SliceSum {
+  const float* slices;
+  void* out;
+  const void* add;          // of out's type, or null
+  const int64_t* m_sizes;   // not null: only the experts' rows count, of `total`
+  int64_t slice, n;         // elements from slice to slice; of out
+  int32_t splits, G, total, C, bf16, out32;
+};
+
+constexpr int kSumThreads = 256;
+
+template <class T>
+__device__ __forceinline__ float sum_get(T v, bool bf16) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return mm_widen(v, bf16);
+}
+template <class T>
+__device__ __forceinline__ T sum_put(float v, bool bf16) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return mm_round16(v, bf16);
+}
+
+template <class T>
+__device__ __forceinline__ void sum_slices(const SliceSum& p, int64_t n) {
+  T* out = static_cast<T*>(p.out);
+  const T* add = static_cast<const T*>(p.add);
+  const bool bf16 = p.bf16 != 0;
+  // four elements a thread, their slices' loads under way together
+  for (int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x); i < n;
+       i += 4ll * kSumThreads * gridDim.x) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    const int m = static_cast<int>(min(static_cast<int64_t>(4), n - i));
+    if (add != nullptr) {
+      for (int j = 0; j < 4; ++j)
+        if (j < m) s[j] = sum_get(add[i + j], bf16);
+    }
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {   // (a slice's length is a multiple of four)
+      const float4 v = *reinterpret_cast<const float4*>(p.slices + k * p.slice + i);
+      s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+    }
+    for (int j = 0; j < 4; ++j)
+      if (j < m) out[i + j] = sum_put<T>(s[j], bf16);
+  }
+}
+
+__global__ void __launch_bounds__(kSumThreads)
+    slice_sum_kernel(const __grid_constant__ SliceSum p) {
+  if (threadIdx.x == 0) ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  int64_t n = p.n;
+  if (p.m_sizes != nullptr) {
+    // rows that are experts': counts clamped as the product's
+    __shared__ int32_t warps[kSumThreads / 32];
+    int32_t rows = 0;
+    for (int g = static_cast<int>(threadIdx.x); g < p.G; g += kSumThreads) {
+      const int64_t m = p.m_sizes[g];
+      rows = min(p.total, rows + static_cast<int32_t>(m < 0 ? 0 : (m > p.total ? p.total : m)));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      rows = min(p.total, rows + __shfl_xor_sync(0xffffffffu, rows, d));
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = rows;
+    __syncthreads();
+    rows = 0;
+    for (int w = 0; w < kSumThreads / 32; ++w) rows = min(p.total, rows + warps[w]);
+    n = static_cast<int64_t>(rows) * p.C;
+  }
+  if (p.out32) sum_slices<float>(p, n);
+  else sum_slices<uint16_t>(p, n);
 }
 
 }  // namespace mslkb

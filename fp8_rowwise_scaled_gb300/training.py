@@ -34,7 +34,7 @@ def declare(L: ctypes.CDLL) -> ctypes.CDLL:
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name, args in {
             "mslkb_grouped_mm_workspace_bytes": [p] * 2 + [i64] * 5 + [i32],
-            "mslkb_grouped_mm_weight_grad_workspace_bytes": [p] * 2 + [i64] * 5,
+            "mslkb_grouped_mm_weight_grad_workspace_bytes": [p] * 2 + [i64] * 6,
             "mslkb_grad_norm_workspace_bytes": [i64]}.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, i64
@@ -54,8 +54,9 @@ def mslkb_grouped_mm(x, w, m_sizes, out, total_M, G, N, K, ldx, transposed, dtyp
                                       dtype, workspace, workspace_bytes, stream)
 
 
-def mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, N, K, lddy, ldx) -> int:
-    return _fx.lib().mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, N, K, lddy, ldx)
+def mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, G, N, K, lddy, ldx) -> int:
+    return _fx.lib().mslkb_grouped_mm_weight_grad_workspace_bytes(dy, x, total_M, G, N, K, lddy,
+                                                                  ldx)
 
 
 def mslkb_grouped_mm_weight_grad(dy, x, m_sizes, add, dw, total_M, G, N, K, lddy, ldx, dtype,

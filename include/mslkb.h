@@ -504,9 +504,10 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  * exact, sums fp32.  G is limited to MSLKB_MAX_GROUPS, every other size to 2^30.  Any size and
  * alignment is accepted; an operand whose rows do not start on 16 bytes, or are not spaced by
  * multiples of 16 (its address, ldx, lddy or the matrices' row length), is first copied to rows
- * that do, in `workspace` (16-byte aligned, contents need not be initialised, not shared by calls
- * that may run at the same time) of at least the bytes that the call's *_workspace_bytes function
- * returns for the same arguments: 0, and then NULL will do, where both operands are aligned.
+ * that do, and a contraction with few output tiles is split into parts whose sums are added in a
+ * fixed order.  Both take `workspace` (16-byte aligned, contents need not be initialised, not
+ * shared by calls that may run at the same time) of at least the bytes that the call's
+ * *_workspace_bytes function returns for the same arguments; where that is 0, NULL will do.
  *
  *   out[r, n] = sum over k of x[r, k] * w[g, n, k]      transposed = 0: w [G, N, K]
  *   out[r, n] = sum over k of x[r, k] * w[g, k, n]      transposed = 1: w [G, K, N]
@@ -539,8 +540,8 @@ MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int6
  *        expert without rows gets add, or +0.0)
  */
 MSLKB_API int64_t mslkb_grouped_mm_weight_grad_workspace_bytes(const void *dy, const void *x,
-                                                               int64_t total_M, int64_t N,
-                                                               int64_t K, int64_t lddy,
+                                                               int64_t total_M, int64_t G,
+                                                               int64_t N, int64_t K, int64_t lddy,
                                                                int64_t ldx);
 MSLKB_API mslkb_status mslkb_grouped_mm_weight_grad(
     const void *dy, const void *x, const int64_t *m_sizes, const void *add, void *dw,

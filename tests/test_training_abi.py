@@ -53,8 +53,11 @@ def test_products_workspace():
             {"ldx": 65, "workspace": P, "bytes": 1023}, {"ldx": 65, "workspace": P + 8,
                                                          "bytes": 1 << 20})
     f = fx.mslkb_grouped_mm_weight_grad_workspace_bytes
-    assert f(P, P, 8, 64, 64, 64, 64) == 0 and f(P, P, 8, 64, 64, 65, 64) == 1024
-    assert f(P, P, 8, 64, 64, 64, 65) == 1024 and f(P, P, 0, 64, 64, 65, 65) == 0
+    assert f(P, P, 8, 2, 64, 64, 64, 64) == 0 and f(P, P, 8, 2, 64, 64, 65, 64) == 1024
+    assert f(P, P, 8, 2, 64, 64, 64, 65) == 1024 and f(P, P, 0, 2, 64, 64, 65, 65) == 0
+    # one expert's 64 x 64 sums of many rows: in slices
+    assert f(P, P, 1 << 16, 1, 64, 64, 64, 64) % (64 * 64 * 4) == 0
+    assert f(P, P, 1 << 16, 1, 64, 64, 64, 64) > 64 * 64 * 4
     refused(weight_grad, fx.MSLKB_ERR_WORKSPACE, {"ldx": 65}, {"dy": P + 2},
             {"lddy": 65, "workspace": P, "bytes": 1023})
 
