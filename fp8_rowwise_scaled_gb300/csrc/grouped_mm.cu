@@ -143,7 +143,7 @@ int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements) {
   for (int32_t s = 1; s <= kMostSplits && (s == 1 || s * kLeastStages <= stages); ++s) {
     const double rounds = static_cast<double>(ceil_to(tiles * s, kPairs));
     double us = rounds * (0.3 * static_cast<double>(ceil_to(stages, s)) + 1.0);
-    if (s > 1) us += 4.0 + static_cast<double>(elements) * 4.0 * 2.0 * s / 6e6;
+    if (s > 1) us += 2.5 + static_cast<double>(elements) * 4.0 * 2.0 * s / 6e6;
     if (s == 1 || us < least) least = us, best = s;
   }
   return best;

@@ -184,9 +184,12 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
   const int32_t c = deep == 1 ? in : (deep == Cfg::kBand ? in / Cfg::kBand : in / deep);
   const int32_t r = band * Cfg::kBand + (in - c * deep);
   o.c0 = c * tile_c;
-  o.valid = min(Cfg::kTileN, rows - r * Cfg::kTileN);
+  // (row tiles of one height, rounded up; the last may have fewer rows, or none)
+  const int32_t each = (rows + rt - 1) / rt;
+  const int32_t height = (each + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
+  o.valid = max(0, min(height, rows - r * height));
   o.h = (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
-  o.r0 = r * Cfg::kTileN + (Cfg::kGrad ? 0 : first[o.g]);
+  o.r0 = r * height + (Cfg::kGrad ? 0 : first[o.g]);
   if (p.splits > 1) {   // by whole stages
     const int64_t stages = (o.len + Cfg::kBK - 1) / Cfg::kBK;
     const int32_t a = static_cast<int32_t>(stages * o.part / p.splits) * Cfg::kBK;
@@ -607,51 +610,60 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     __syncwarp();
   } else if (warp == Cfg::kMmaWarp) {
     // -------------------------------------------------------------- MMAs
-    if (lane == 0 && crank == 0) {
+    // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and
+    // one lane issues (by that lane alone, in a branch of its own, a stage took 580 cycles to
+    // issue; the tensor core takes 512 for it).
+    if (crank == 0) {
+      const bool issuer = ptx::elect_one();
       int stage = 0;
       uint32_t phase = 0, used = 0;
       bool ok = true;
       const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
       const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
       MmTile c;
-      for (int32_t i = 0; ok && take(i, c, false); ++i) {
-        if (c.len == 0) continue;
-        const uint32_t idesc = mm_idesc<Cfg>(p.bf16, c.h);
+      for (int32_t i = 0; ok && take(i, c, true); ++i) {
+        const int32_t len = __shfl_sync(0xffffffffu, c.len, 0);
+        if (len == 0) continue;
+        const uint32_t idesc = mm_idesc<Cfg>(p.bf16, __shfl_sync(0xffffffffu, c.h, 0));
         const int b = static_cast<int>(used & 1u);
-        if (!wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag, p.status,
-                                  p.timeout_ns))
-          break;
+        ok = __all_sync(0xffffffffu,
+                        wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
+                                             p.status, p.timeout_ns)) != 0;
+        if (!ok) break;
         ++used;
         ptx::tc_fence_after_sync();
         const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::kTileN);
-        for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
-          if (!wait_bar(full_bar(stage), phase, abort_flag, p.status, p.timeout_ns)) {
-            ok = false;
-            break;
-          }
+        for (int32_t k = 0; k < len; k += Cfg::kBK) {
+          ok = __all_sync(0xffffffffu, wait_bar(full_bar(stage), phase, abort_flag, p.status,
+                                                p.timeout_ns)) != 0;
+          if (!ok) break;
           ptx::tc_fence_after_sync();
           const uint32_t p_lo = p_lo0 + static_cast<uint32_t>(stage * (Cfg::kPBytes >> 4));
           const uint32_t q_lo = q_lo0 + static_cast<uint32_t>(stage * (Cfg::kQBytes >> 4));
-          const int32_t steps = min(Cfg::kBK / 16, (c.len - k + 15) / 16);
+          const int32_t steps = min(Cfg::kBK / 16, (len - k + 15) / 16);
+          if (issuer) {
 #pragma unroll
-          for (int s = 0; s < Cfg::kBK / 16; ++s) {
-            constexpr uint32_t kMn16 = 16 * 128 / 16;
-            const uint32_t po = Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
-            const uint32_t qo =
-                Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
-            if (s < steps)
-              mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc, (k > 0 || s > 0) ? 1u : 0u);
+            for (int s = 0; s < Cfg::kBK / 16; ++s) {
+              constexpr uint32_t kMn16 = 16 * 128 / 16;
+              const uint32_t po = Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
+              const uint32_t qo =
+                  Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
+              if (s < steps)
+                mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc, (k > 0 || s > 0) ? 1u : 0u);
+            }
+            if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+            else ptx::mma_commit(empty_bar(stage));
           }
-          if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
-          else ptx::mma_commit(empty_bar(stage));
           if (++stage == Cfg::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(b), 0x3);
-        else ptx::mma_commit(tfull_bar(b));
+        if (issuer) {
+          if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(b), 0x3);
+          else ptx::mma_commit(tfull_bar(b));
+        }
       }
     }
     __syncwarp();
@@ -721,17 +733,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     __syncwarp();
   } else if (warp == static_cast<uint32_t>(Cfg::kTileWarp)) {
     // -------------------------------------------------------------- tiles
-    // 32 tiles are worked out at a time, one by each lane (a search and four divisions), and
-    // handed on one after the other.
+    // Round n goes over the workers from the n-th on, so that a worker does not get the same row tile
+    // of every column: those of fewer rows take less time, and workers that get ahead of others
+    // read the weights from memory instead of sharing them in L2 (32 experts of 480 rows, 4096 x
+    // 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a time, one by each lane
+    // (a search and up to four divisions), and handed on one after the other.
     int32_t i = 0;
     bool ok = true;
-    for (int64_t t0 = worker; ok; t0 += 32ll * workers) {
-      const int64_t t = t0 + static_cast<int64_t>(lane) * workers;
+    for (int64_t n0 = 0; ok; n0 += 32) {
+      const int64_t n = n0 + lane;
+      const int64_t t = n * workers + (Cfg::kGrad ? worker : (worker + n) % workers);
       MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
       if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
-      const bool more = t0 + 31ll * workers < tiles;   // (else the last of these says so)
-      uint32_t left = 0xffffffffu;
-      if (!more) left &= (2u << (__ffs(__ballot_sync(0xffffffffu, c.g < 0)) - 1)) - 1u;
+      const uint32_t past = __ballot_sync(0xffffffffu, c.g < 0);   // (the first of these says so)
+      const bool more = past == 0u;
+      uint32_t left = more ? 0xffffffffu : (2u << (__ffs(past) - 1)) - 1u;
+      left &= __ballot_sync(0xffffffffu, c.g < 0 || c.h > 0);
       while (left != 0) {
         const int src = __ffs(left) - 1;
         left &= left - 1;
