@@ -129,20 +129,22 @@ bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
          K <= kMaxSize && G <= kMaxGroups;
 }
 
-// Parts of each contraction.  Few tiles leave most pairs without one, and a pair takes some 0.3 us
-// for a stage of 64, however few the rows (of 4096 x 7168, one expert and row: 39 us); so the
+// Parts of each contraction.  Few tiles leave most pairs without one, and a pair takes some 0.2 us
+// for a stage of 64, however few the rows (4096 x 7168, one expert and row: 28 us); so the
 // contractions of up to two rounds of tiles are split, into the number of parts that takes least by
-// this reckoning: rounds of the pairs x (stages of a part, and a tile's ends), and for the
-// slices' sum a launch and their bytes.
+// this reckoning: rounds of the pairs x (stages of a part, and a tile's ends), or the time that the
+// operands take to read; and for the slices' sum a launch and their bytes.
 constexpr int kPairs = 76, kMostSplits = 16, kLeastStages = 4;
-int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements) {
+int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements, int64_t operands) {
   const int64_t stages = ceil_to(contraction, 64);
   if (tiles > 2 * kPairs) return 1;
+  const double read = static_cast<double>(operands) * 2.0 / 6.5e6;
   int32_t best = 1;
   double least = 0.0;
   for (int32_t s = 1; s <= kMostSplits && (s == 1 || s * kLeastStages <= stages); ++s) {
     const double rounds = static_cast<double>(ceil_to(tiles * s, kPairs));
-    double us = rounds * (0.3 * static_cast<double>(ceil_to(stages, s)) + 1.0);
+    double us = rounds * (0.2 * static_cast<double>(ceil_to(stages, s)) + 1.0);
+    if (us < read) us = read;
     if (s > 1) us += 2.5 + static_cast<double>(elements) * 4.0 * 2.0 * s / 6e6;
     if (s == 1 || us < least) least = us, best = s;
   }
@@ -153,13 +155,16 @@ int64_t slice_of(int64_t elements) { return ceil_to(elements, 4) * 4; }
 
 int32_t mm_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
   if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
-  const int64_t row_tiles = total_M / 256 + (G < total_M ? G : total_M);
-  return splits_of(row_tiles * ceil_to(N, 256), K, total_M * N);
+  const int64_t experts = G < total_M ? G : total_M;   // with rows, at most
+  return splits_of((total_M / 256 + experts) * ceil_to(N, 256), K, total_M * N,
+                   experts * N * K + total_M * K);
 }
 
 int32_t grad_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
   if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
-  return splits_of(G * ceil_to(N, 256) * ceil_to(K, 256), ceil_to(total_M, G), G * N * K);
+  // (experts have different numbers of rows: twice as many as they have on average)
+  return splits_of(G * ceil_to(N, 256) * ceil_to(K, 256), ceil_to(2 * total_M, G + 1), G * N * K,
+                   total_M * (N + K));
 }
 
 // The slices' place in the workspace, behind the operands' copies.

@@ -515,25 +515,30 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      MmTile c;
-      for (int32_t i = 0; ok && take(i, c, false); ++i) {
-        if (c.len == 0) continue;
-        const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide;
-        const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
-        const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
-        // of Q 64 rows or 128 (of kGrad, columns) are loaded
-        const bool half = mine <= 64;
-        const uint32_t bytes =
-            static_cast<uint32_t>((wide + (half ? 64 : 128)) * Cfg::kBK * 2);
-        for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
-          if (!wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns)) {
-            ok = false;
-            break;
-          }
+    // (by the whole warp, with one lane issuing, as the MMAs below)
+    const bool issuer = ptx::elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    MmTile taken;
+    for (int32_t i = 0; ok && take(i, taken, true); ++i) {
+      // (the same in every lane, which the compiler is told)
+      auto all = [](int32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const MmTile c{all(taken.g), all(taken.c0), all(taken.r0), all(taken.h), 0, all(taken.k0),
+                     all(taken.len), 0};
+      if (c.len == 0) continue;
+      const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide;
+      const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
+      const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
+      // of Q 64 rows or 128 (of kGrad, columns) are loaded
+      const bool half = mine <= 64;
+      const uint32_t bytes =
+          static_cast<uint32_t>((wide + (half ? 64 : 128)) * Cfg::kBK * 2);
+      for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+        ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag,
+                                              p.status, p.timeout_ns)) != 0;
+        if (!ok) break;
+        if (issuer) {
           // pairs: the bytes of both CTAs (as many in each) complete on the leader's barrier.  A
           // stage that ends between two MMA steps (kGrad) passes through the edge warp of each
           // CTA first.
@@ -592,19 +597,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             for (int j = 0; j < Cfg::kKB; ++j)
               load2(dq + j * Cfg::kQRows * 128, half ? &maps.q64 : &maps.q, x + 64 * j, row);
           }
-          if (++stage == Cfg::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-      }
-      // wait until the MMAs have released every stage
-      for (int i = 0; ok && i < Cfg::kStages; ++i) {
-        ok = wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status, p.timeout_ns);
         if (++stage == Cfg::kStages) {
           stage = 0;
           phase ^= 1u;
         }
+      }
+    }
+    // wait until the MMAs have released every stage
+    for (int i = 0; ok && i < Cfg::kStages; ++i) {
+      ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                                            p.timeout_ns)) != 0;
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
     __syncwarp();
