@@ -1,7 +1,8 @@
 // grad_norm.cu -- the norm of a list of gradients taken together, and the gradients scaled so that
 // it does not exceed a bound.
 //
-//   norm = (sum_i sum_j g_ij^2)^(1/2)  or  max |g_ij|,   out_ij = g_ij * min(1, max_norm / (norm + eps))
+//   norm = (sum_i sum_j g_ij^2)^(1/2)  or  max |g_ij|
+//   out_ij = g_ij * min(1, max_norm / (norm + eps))
 //
 // Bound by memory: everything is read once for the norm, and read again and written once for the
 // clipping.  The list is cut into chunks of kChunkBytes, and every CTA takes an equal run of them
@@ -33,7 +34,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kChunkBytes = 4096;
 constexpr int kMaxParts = 512;            // CTAs of a launch, and partial sums of it
-constexpr int kFew = 64, kSome = 256, kMany = 1024;   // tensors of a launch, by the size of its parameters
+// Tensors of a launch, by the size of its parameters.
+constexpr int kFew = 64, kSome = 256, kMany = 1024;
 constexpr int kCluster = 16;       // most CTAs of a cluster
 constexpr int kSmallChunks = 512;  // of a list that one cluster takes
 
@@ -615,7 +617,8 @@ bool apart(const Args& a) {
 mslkb_status run_checked(const Args& a, int32_t kind, float* norm, double max_norm, double eps,
                          void* workspace, int64_t workspace_bytes, void* stream,
                          const char* name) try {
-  if (a.count < 0 || a.count > MSLKB_MAX_TENSORS || (kind != MSLKB_NORM_2 && kind != MSLKB_NORM_INF))
+  if (a.count < 0 || a.count > MSLKB_MAX_TENSORS ||
+      (kind != MSLKB_NORM_2 && kind != MSLKB_NORM_INF))
     return MSLKB_ERR_SHAPE;
   if (norm == nullptr) return MSLKB_ERR_NULL;
   if (a.count > 0 && (a.in == nullptr || a.sizes == nullptr || a.types == nullptr))

@@ -1,5 +1,6 @@
 // grouped_mm.cu -- 16-bit products by expert: which kernel serves a call, and the entry points.
 // (The kernel, its mathematics and layout: grouped_mm.cuh.)
+#include <atomic>
 #include <cstring>
 
 #include "grouped_mm.cuh"
@@ -24,6 +25,18 @@ template <class Cfg>
 mslkb_status launch(const MmParams& p, const MmMaps& maps, int sms, void* stream) {
   cudaError_t e = allow_smem<grouped_mm_kernel<Cfg>>();
   if (e != cudaSuccess) return launch_status(e);
+  if constexpr (Cfg::kLong) {
+    // a kernel that moves registers between its warps waits for ever if it starts with too few
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+      cudaFuncAttributes a;
+      if ((e = cudaFuncGetAttributes(&a, grouped_mm_kernel<Cfg>)) != cudaSuccess)
+        return launch_status(e);
+      regs.store(a.numRegs);
+    }
+    if (regs.load() * Cfg::kThreads < 128 * Cfg::kRegsFew + 256 * Cfg::kRegsMany)
+      return launch_status(cudaErrorInvalidConfiguration);
+  }
   const int64_t tiles = tiles_bound<Cfg>(p) * p.splits;
   if (tiles > INT32_MAX) return MSLKB_ERR_SHAPE;
   const int64_t workers = sms / Cfg::kCtas;
@@ -33,8 +46,8 @@ mslkb_status launch(const MmParams& p, const MmMaps& maps, int sms, void* stream
                                       maps));
 }
 
-// Tensor maps of P, Q and what is added.  Matrices of experts have a dimension of their own, so that
-// what lies past one is read as zero and not as the next.  An MN-major operand lies in shared
+// Tensor maps of P, Q and what is added.  Matrices of experts have a dimension of their own, so
+// that what lies past one is read as zero and not as the next.  An MN-major operand lies in shared
 // memory in pieces of 64 elements: where its rows consist of whole pieces these are a dimension
 // too, and one box fetches both pieces of a CTA.
 template <class Cfg>
@@ -117,6 +130,11 @@ mslkb_status run_as(MmParams& p, int sms, void* stream) {
 template <Mm kMode>
 mslkb_status run(MmParams& p, int sms, void* stream) {
   if constexpr (kMode == Mm::kGrad) {
+    // fp32 sums of several kSumRows rows in registers, where experts may well have as many (32
+    // experts of 4096 x 7168 on GB300, us in registers / onto the result: 1024 rows each 1404 /
+    // 2235; 256 each 789 / 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280)
+    if (p.out32 && p.total >= 192ll * p.G * p.splits)
+      return run_as<MmCfg<kMode, 2, 256, 1, 6, 8, false, true>>(p, sms, stream);
     const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
     if (p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0)
       return run_as<MmCfg<kMode, 2, 256, 1, 4, 8, true>>(p, sms, stream);

@@ -67,7 +67,7 @@ struct MmMaps {
 };
 
 template <Mm kMode_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_,
-          bool kAdd_ = false>
+          bool kAdd_ = false, bool kLong_ = false>
 struct MmCfg {
   static constexpr Mm kMode = kMode_;
   static constexpr bool kGrad = kMode == Mm::kGrad;
@@ -91,6 +91,14 @@ struct MmCfg {
   // its own for each four of the epilogue's warps (loaded by the epilogue's threads themselves,
   // one or two chunks ahead: 1487 us for 32 x 4096 x 7168 fp32, 1264 bf16)
   static constexpr bool kAddRing = kAdd_;
+  // The tensor core's sums lose what lies below their last bit, always downwards: some 1e-9 of the
+  // result for every row summed (fp32 results of 4096 rows, normal values, were 4.4e-6 off).  So
+  // fp32 gradients are summed there kSumRows rows at a time, and these sums added with rounding
+  // (5e-7).  kLong: for many rows per expert, in registers, which eight warps have for a tile's
+  // 256 rows of sums (and take from the others); else in the result itself.
+  static constexpr bool kLong = kLong_;
+  static constexpr int kSumRows = 512;
+  static constexpr int kRegsFew = 56, kRegsMany = 224;   // of warps 0-3, of the epilogue's
   static constexpr int kAddWarp = 4;
   static constexpr int kAddBytes = kAddRing ? 32768 : 0;
   static constexpr int kEpiWarp0 = kAddRing ? 8 : 4;
@@ -116,7 +124,7 @@ struct MmCfg {
   static constexpr int kRing = 4;
   static constexpr int kRingUsers = 2 + (kGrad ? 1 : 0) + (kAddRing ? 1 : 0) + kEpiWarps;
   static constexpr int kAddSlots = 4;  // at most, of one ring
-  static constexpr int kNumBars = 4 * kStages + 4 + 2 * kRing + (kAddRing ? 4 * kAddSlots : 0);
+  static constexpr int kNumBars = 4 * kStages + 6 + 2 * kRing + (kAddRing ? 4 * kAddSlots : 0);
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
   static constexpr int kOffRing = (kOffMisc + 8 + 15) / 16 * 16;
   static constexpr int kOffSched = kOffRing + kRing * 32;
@@ -126,11 +134,14 @@ struct MmCfg {
   static_assert(!kQMn || kQRows % 64 == 0, "MN-major pieces of 64");
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(!kLong || (kGrad && !kAddRing && kThreads == 384 && kTileN == 256 &&
+                           128 * kRegsFew + 256 * kRegsMany <= 384 * 168), "registers");
   static_assert(!kAddRing || (kGrad && kEpiWarps == 8 && kChunk == 32), "what is added");
 };
 
-// A tile: its group (-1: past the last tile), first output column and row, rows (h: rounded up, valid: real), and the
-// contraction [k0, k0 + len) (kGrad: rows of x and dy), or the part of it that is this tile's.
+// A tile: its group (-1: past the last tile), first output column and row, rows (h: rounded up,
+// valid: real), and the contraction [k0, k0 + len) (kGrad: rows of x and dy), or the part of it that
+// is this tile's.
 struct MmTile {
   int32_t g, c0, r0, h, valid, k0, len, part;
 };
@@ -244,7 +255,9 @@ __device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, i
     if (lane == 0) tile_pre[G] = G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
   } else {
     // (row tiles first: there are at most total / kTileN + G of them)
-    auto tiles = [&](int32_t g) { return (first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN; };
+    auto tiles = [&](int32_t g) {
+      return (first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN;
+    };
     int32_t mine = 0;
     for (int32_t g = g0; g < g1; ++g) mine += tiles(g);
     int32_t at = mine;
@@ -421,15 +434,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const uint32_t s_bar = ptx::smem_addr(smem + Cfg::kOffBar);
   auto full_bar = [&](int s) { return s_bar + 8u * s; };
   auto empty_bar = [&](int s) { return s_bar + 8u * (Cfg::kStages + s); };
-  auto tfull_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + b); };
-  auto tempty_bar = [&](int b) { return s_bar + 8u * (2 * Cfg::kStages + 2 + b); };
-  auto edge_bar = [&](int s) { return s_bar + 8u * (2 * Cfg::kStages + 4 + s); };
-  auto peer_bar = [&](int s) { return s_bar + 8u * (3 * Cfg::kStages + 4 + s); };
-  auto tile_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + i); };
-  auto taken_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 4 + Cfg::kRing + i); };
+  // sums in TMEM buffer b for the epilogue's four warps `part` (each four see all completions of
+  // their own barriers, one after the other, however many sums the others take in between)
+  auto tfull_bar = [&](uint32_t part, uint32_t b) {
+    return s_bar + 8u * (2 * Cfg::kStages + 2 * part + b);
+  };
+  auto tempty_bar = [&](uint32_t b) { return s_bar + 8u * (2 * Cfg::kStages + 4 + b); };
+  auto edge_bar = [&](int s) { return s_bar + 8u * (2 * Cfg::kStages + 6 + s); };
+  auto peer_bar = [&](int s) { return s_bar + 8u * (3 * Cfg::kStages + 6 + s); };
+  auto tile_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 6 + i); };
+  auto taken_bar = [&](int i) { return s_bar + 8u * (4 * Cfg::kStages + 6 + Cfg::kRing + i); };
   // ring of what is added, of the epilogue's warps `part`: slot full, slot free
   auto add_bar = [&](uint32_t part, uint32_t slot) {
-    return s_bar + 8u * (4 * Cfg::kStages + 4 + 2 * Cfg::kRing + part * 2 * Cfg::kAddSlots + slot);
+    return s_bar + 8u * (4 * Cfg::kStages + 6 + 2 * Cfg::kRing + part * 2 * Cfg::kAddSlots + slot);
   };
   auto addfree_bar = [&](uint32_t part, uint32_t slot) {
     return add_bar(part, slot) + 8u * Cfg::kAddSlots;
@@ -455,8 +472,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       ptx::mbar_init(peer_bar(s), 1u);
     }
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(tfull_bar(b), 1u);
-      ptx::mbar_init(tempty_bar(b), static_cast<uint32_t>(4 * Cfg::kCtas));
+      ptx::mbar_init(tfull_bar(0u, b), 1u);
+      ptx::mbar_init(tfull_bar(1u, b), 1u);
+      ptx::mbar_init(tempty_bar(b),
+                     static_cast<uint32_t>((Cfg::kLong ? Cfg::kEpiWarps : 4) * Cfg::kCtas));
     }
     for (int i = 0; i < Cfg::kRing; ++i) {
       ptx::mbar_init(tile_bar(i), 1u);
@@ -513,267 +532,340 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     return c.g >= 0;
   };
 
-  if (warp == 0) {
-    // -------------------------------------------------------------- loads
-    // (by the whole warp, with one lane issuing, as the MMAs below)
-    const bool issuer = ptx::elect_one();
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    MmTile taken;
-    for (int32_t i = 0; ok && take(i, taken, true); ++i) {
-      // (the same in every lane, which the compiler is told)
-      auto all = [](int32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
-      const MmTile c{all(taken.g), all(taken.c0), all(taken.r0), all(taken.h), 0, all(taken.k0),
-                     all(taken.len), 0};
-      if (c.len == 0) continue;
-      const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide;
-      const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
-      const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
-      // of Q 64 rows or 128 (of kGrad, columns) are loaded
-      const bool half = mine <= 64;
-      const uint32_t bytes =
-          static_cast<uint32_t>((wide + (half ? 64 : 128)) * Cfg::kBK * 2);
-      for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
-        ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag,
-                                              p.status, p.timeout_ns)) != 0;
-        if (!ok) break;
-        if (issuer) {
-          // pairs: the bytes of both CTAs (as many in each) complete on the leader's barrier.  A
-          // stage that ends between two MMA steps (kGrad) passes through the edge warp of each
-          // CTA first.
-          uint32_t bar = Cfg::kPair ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
-          const bool edge = Cfg::kGrad && c.len - k < Cfg::kBK && (c.len & 15) != 0;
-          if (edge) {
-            bar = Cfg::kPair ? ptx::mapa_shared(edge_bar(stage), crank) : edge_bar(stage);
-            ptx::mbar_arrive_expect_tx(edge_bar(stage), bytes);
-          } else if (crank == 0) {
-            ptx::mbar_arrive_expect_tx(full_bar(stage), bytes * Cfg::kCtas);
-          }
-          const int32_t x = c.k0 + k;
-          const uint32_t dp = s_p + stage * Cfg::kPBytes, dq = s_q + stage * Cfg::kQBytes;
-          auto load2 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b) {
-            if constexpr (Cfg::kPair) ptx::tma_load_2d_pair(dst, m, bar, a, b);
-            else ptx::tma_load_2d(dst, m, bar, a, b);
-          };
-          auto load3 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t g) {
-            if constexpr (Cfg::kPair) ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
-            else ptx::tma_load_3d(dst, m, bar, a, b, g);
-          };
-          auto load4 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t z,
-                           int32_t g) {
-            if constexpr (Cfg::kPair) ptx::tma_load_4d_pair(dst, m, bar, a, b, z, g);
-            else ptx::tma_load_4d(dst, m, bar, a, b, z, g);
-          };
-          // (few, large operations: an SM's loads are limited by their number as well)
-          if constexpr (Cfg::kMode == Mm::kRows) {
-#pragma unroll
-            for (int i = 0; i < Cfg::kKB; ++i)
-              load3(dp + i * 128 * 128, &maps.p, x + 64 * i, col, c.g);
-          } else if constexpr (Cfg::kMode == Mm::kTurned) {
-            if (p.p_pieces) {
-              load4(dp, &maps.p, 0, x, col / 64, c.g);
-            } else {
-              load3(dp, &maps.p, col, x, c.g);
-              load3(dp + Cfg::kMnPiece, &maps.p, col + 64, x, c.g);
-            }
-          } else {
-            if (p.p_pieces) {
-              load3(dp, &maps.p, 0, x, col / 64);
-            } else {
-              load2(dp, &maps.p, col, x);
-              load2(dp + Cfg::kMnPiece, &maps.p, col + 64, x);
-            }
-          }
-          if constexpr (Cfg::kQMn) {
-            if (p.q_pieces && !half && row % 64 == 0) {
-              load3(dq, &maps.q, 0, x, row / 64);
-            } else {
-              load2(dq, &maps.q64, row, x);
-              if (!half) load2(dq + Cfg::kMnPiece, &maps.q64, row + 64, x);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < Cfg::kKB; ++j)
-              load2(dq + j * Cfg::kQRows * 128, half ? &maps.q64 : &maps.q, x + 64 * j, row);
-          }
-        }
-        if (++stage == Cfg::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // wait until the MMAs have released every stage
-    for (int i = 0; ok && i < Cfg::kStages; ++i) {
-      ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
-                                            p.timeout_ns)) != 0;
-      if (++stage == Cfg::kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    __syncwarp();
-  } else if (warp == Cfg::kMmaWarp) {
-    // -------------------------------------------------------------- MMAs
-    // The whole warp walks the loop, so that stages and descriptors stay in uniform registers, and
-    // one lane issues (by that lane alone, in a branch of its own, a stage took 580 cycles to
-    // issue; the tensor core takes 512 for it).
-    if (crank == 0) {
+  // rows (steps of the contraction) that the tensor core sums
+  const int32_t sum_rows = Cfg::kGrad && p.out32 ? Cfg::kSumRows : 1 << 30;
+  if (warp < static_cast<uint32_t>(Cfg::kEpiWarp0)) {
+    if constexpr (Cfg::kLong) ptx::setmaxnreg_dec<Cfg::kRegsFew>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- loads
+      // (by the whole warp, with one lane issuing, as the MMAs below)
       const bool issuer = ptx::elect_one();
       int stage = 0;
-      uint32_t phase = 0, used = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
-      const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
-      MmTile c;
-      for (int32_t i = 0; ok && take(i, c, true); ++i) {
-        const int32_t len = __shfl_sync(0xffffffffu, c.len, 0);
-        if (len == 0) continue;
-        const uint32_t idesc = mm_idesc<Cfg>(p.bf16, __shfl_sync(0xffffffffu, c.h, 0));
-        const int b = static_cast<int>(used & 1u);
-        ok = __all_sync(0xffffffffu,
-                        wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
-                                             p.status, p.timeout_ns)) != 0;
-        if (!ok) break;
-        ++used;
-        ptx::tc_fence_after_sync();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(b * Cfg::kTileN);
-        for (int32_t k = 0; k < len; k += Cfg::kBK) {
-          ok = __all_sync(0xffffffffu, wait_bar(full_bar(stage), phase, abort_flag, p.status,
-                                                p.timeout_ns)) != 0;
+      MmTile taken;
+      for (int32_t i = 0; ok && take(i, taken, true); ++i) {
+        // (the same in every lane, which the compiler is told)
+        auto all = [](int32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+        const MmTile c{all(taken.g), all(taken.c0), all(taken.r0), all(taken.h), 0, all(taken.k0),
+                       all(taken.len), 0};
+        if (c.len == 0) continue;
+        const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide;
+        const int32_t mine = c.h / Cfg::kCtas;  // rows of Q in this CTA
+        const int32_t row = c.r0 + static_cast<int32_t>(crank) * mine;
+        // of Q 64 rows or 128 (of kGrad, columns) are loaded
+        const bool half = mine <= 64;
+        const uint32_t bytes =
+            static_cast<uint32_t>((wide + (half ? 64 : 128)) * Cfg::kBK * 2);
+        for (int32_t k = 0; k < c.len; k += Cfg::kBK) {
+          ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag,
+                                                p.status, p.timeout_ns)) != 0;
           if (!ok) break;
-          ptx::tc_fence_after_sync();
-          const uint32_t p_lo = p_lo0 + static_cast<uint32_t>(stage * (Cfg::kPBytes >> 4));
-          const uint32_t q_lo = q_lo0 + static_cast<uint32_t>(stage * (Cfg::kQBytes >> 4));
-          const int32_t steps = min(Cfg::kBK / 16, (len - k + 15) / 16);
           if (issuer) {
-#pragma unroll
-            for (int s = 0; s < Cfg::kBK / 16; ++s) {
-              constexpr uint32_t kMn16 = 16 * 128 / 16;
-              const uint32_t po = Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
-              const uint32_t qo =
-                  Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
-              if (s < steps)
-                mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc, (k > 0 || s > 0) ? 1u : 0u);
+            // pairs: the bytes of both CTAs (as many in each) complete on the leader's barrier.  A
+            // stage that ends between two MMA steps (kGrad) passes through the edge warp of each
+            // CTA first.
+            uint32_t bar = Cfg::kPair ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
+            const bool edge = Cfg::kGrad && c.len - k < Cfg::kBK && (c.len & 15) != 0;
+            if (edge) {
+              bar = Cfg::kPair ? ptx::mapa_shared(edge_bar(stage), crank) : edge_bar(stage);
+              ptx::mbar_arrive_expect_tx(edge_bar(stage), bytes);
+            } else if (crank == 0) {
+              ptx::mbar_arrive_expect_tx(full_bar(stage), bytes * Cfg::kCtas);
             }
-            if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
-            else ptx::mma_commit(empty_bar(stage));
+            const int32_t x = c.k0 + k;
+            const uint32_t dp = s_p + stage * Cfg::kPBytes, dq = s_q + stage * Cfg::kQBytes;
+            auto load2 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b) {
+              if constexpr (Cfg::kPair) ptx::tma_load_2d_pair(dst, m, bar, a, b);
+              else ptx::tma_load_2d(dst, m, bar, a, b);
+            };
+            auto load3 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t g) {
+              if constexpr (Cfg::kPair) ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
+              else ptx::tma_load_3d(dst, m, bar, a, b, g);
+            };
+            auto load4 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t z,
+                             int32_t g) {
+              if constexpr (Cfg::kPair) ptx::tma_load_4d_pair(dst, m, bar, a, b, z, g);
+              else ptx::tma_load_4d(dst, m, bar, a, b, z, g);
+            };
+            // (few, large operations: an SM's loads are limited by their number as well)
+            if constexpr (Cfg::kMode == Mm::kRows) {
+#pragma unroll
+              for (int i = 0; i < Cfg::kKB; ++i)
+                load3(dp + i * 128 * 128, &maps.p, x + 64 * i, col, c.g);
+            } else if constexpr (Cfg::kMode == Mm::kTurned) {
+              if (p.p_pieces) {
+                load4(dp, &maps.p, 0, x, col / 64, c.g);
+              } else {
+                load3(dp, &maps.p, col, x, c.g);
+                load3(dp + Cfg::kMnPiece, &maps.p, col + 64, x, c.g);
+              }
+            } else {
+              if (p.p_pieces) {
+                load3(dp, &maps.p, 0, x, col / 64);
+              } else {
+                load2(dp, &maps.p, col, x);
+                load2(dp + Cfg::kMnPiece, &maps.p, col + 64, x);
+              }
+            }
+            if constexpr (Cfg::kQMn) {
+              if (p.q_pieces && !half && row % 64 == 0) {
+                load3(dq, &maps.q, 0, x, row / 64);
+              } else {
+                load2(dq, &maps.q64, row, x);
+                if (!half) load2(dq + Cfg::kMnPiece, &maps.q64, row + 64, x);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < Cfg::kKB; ++j)
+                load2(dq + j * Cfg::kQRows * 128, half ? &maps.q64 : &maps.q, x + 64 * j, row);
+            }
           }
           if (++stage == Cfg::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        if (issuer) {
-          if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(b), 0x3);
-          else ptx::mma_commit(tfull_bar(b));
+      }
+      // wait until the MMAs have released every stage
+      for (int i = 0; ok && i < Cfg::kStages; ++i) {
+        ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                                              p.timeout_ns)) != 0;
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
+      __syncwarp();
+    } else if (warp == Cfg::kMmaWarp) {
+      // -------------------------------------------------------------- MMAs
+      // The whole warp walks the loop, so that stages and descriptors stay in uniform registers,
+      // and one lane issues (by that lane alone, in a branch of its own, a stage took 580 cycles
+      // to issue; the tensor core takes 512 for it).
+      if (crank == 0) {
+        const bool issuer = ptx::elect_one();
+        int stage = 0;
+        uint32_t phase = 0, used = 0, turn = 0;
+        bool ok = true;
+        const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
+        const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
+        MmTile c;
+        for (int32_t i = 0; ok && take(i, c, true); ++i) {
+          const int32_t len = __shfl_sync(0xffffffffu, c.len, 0);
+          if (len == 0) continue;
+          const uint32_t idesc = mm_idesc<Cfg>(p.bf16, __shfl_sync(0xffffffffu, c.h, 0));
+          for (int32_t k = 0; k < len;) {
+            const uint32_t b = used & 1u;
+            ok = __all_sync(0xffffffffu,
+                            wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
+                                                 p.status, p.timeout_ns)) != 0;
+            if (!ok) break;
+            ++used;
+            ptx::tc_fence_after_sync();
+            const uint32_t d = tmem_base + b * Cfg::kTileN;
+            const int32_t from = k, end = len - k > sum_rows ? k + sum_rows : len;
+            for (; k < end; k += Cfg::kBK) {
+              ok = __all_sync(0xffffffffu, wait_bar(full_bar(stage), phase, abort_flag, p.status,
+                                                    p.timeout_ns)) != 0;
+              if (!ok) break;
+              ptx::tc_fence_after_sync();
+              const uint32_t p_lo = p_lo0 + static_cast<uint32_t>(stage * (Cfg::kPBytes >> 4));
+              const uint32_t q_lo = q_lo0 + static_cast<uint32_t>(stage * (Cfg::kQBytes >> 4));
+              const int32_t steps = min(Cfg::kBK / 16, (len - k + 15) / 16);
+              if (issuer) {
+#pragma unroll
+                for (int s = 0; s < Cfg::kBK / 16; ++s) {
+                  constexpr uint32_t kMn16 = 16 * 128 / 16;
+                  const uint32_t po =
+                      Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
+                  const uint32_t qo =
+                      Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
+                  if (s < steps)
+                    mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc,
+                                     (k > from || s > 0) ? 1u : 0u);
+                }
+                if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+                else ptx::mma_commit(empty_bar(stage));
+              }
+              if (++stage == Cfg::kStages) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (!ok) break;
+            if (issuer) {
+              if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(turn, b), 0x3);
+              else ptx::mma_commit(tfull_bar(turn, b));
+            }
+          }
+          if (!Cfg::kLong && Cfg::kEpiWarps == 8) turn ^= 1u;
+        }
+      }
+      __syncwarp();
+    } else if (Cfg::kGrad && warp == Cfg::kEdgeWarp) {
+      // -------------------------------------------------------------- ends of experts' rows
+      // The last stage of an expert whose rows do not end with an MMA step of 16: its last step
+      // holds rows of the next expert (or past the buffers).  They are zeroed in both operands (0 x
+      // NaN is NaN): whole 128-byte lines here, since the rows are the operands' lines.
+      int stage = 0;
+      uint32_t parity = 0;  // of each stage's edge barrier, one bit
+      MmTile c;
+      for (int32_t i = 0; take(i, c, true); ++i) {
+        if (c.len == 0) continue;
+        const int32_t kbs = (c.len + Cfg::kBK - 1) / Cfg::kBK;
+        const int last = (stage + kbs - 1) % Cfg::kStages;
+        stage = (stage + kbs) % Cfg::kStages;
+        if ((c.len & 15) == 0) continue;
+        const bool ok = wait_bar(edge_bar(last), (parity >> last) & 1u, abort_flag, p.status,
+                                 p.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        parity ^= 1u << last;
+        const int32_t in = c.len - (kbs - 1) * Cfg::kBK;  // rows of the stage that are the expert's
+        const int32_t lines = ((in + 15) & ~15) - in;
+        const int32_t boxes = c.h / Cfg::kCtas <= 64 ? 1 : 2;
+        for (int32_t i = static_cast<int32_t>(lane); i < (2 + boxes) * lines * 8; i += 32) {
+          const int32_t line = in + (i >> 3) % lines, piece = (i >> 3) / lines;
+          const uint32_t base = piece < 2 ? s_p + last * Cfg::kPBytes + piece * Cfg::kMnPiece
+                                          : s_q + last * Cfg::kQBytes + (piece - 2) * Cfg::kMnPiece;
+          ptx::st_shared_v4(base + static_cast<uint32_t>(line) * 128u + (i & 7) * 16u, 0u, 0u, 0u,
+                            0u);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        // pairs: the leader's edge warp hands the stage on when the peer's has done its part
+        if (Cfg::kPair && crank != 0) {
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(peer_bar(last), 0u));
+        } else {
+          if constexpr (Cfg::kPair) {
+            const bool there = wait_bar<true>(peer_bar(last), ((parity >> last) & 1u) ^ 1u, abort_flag,
+                                              p.status, p.timeout_ns);
+            if (!__all_sync(0xffffffffu, there)) break;
+          }
+          if (lane == 0) ptx::mbar_arrive(full_bar(last));
+        }
+      }
+    } else if (Cfg::kAddRing && warp == Cfg::kAddWarp) {
+      // -------------------------------------------------------------- what is added
+      if (lane == 0) {
+        uint32_t turn = 0, count0 = 0, count1 = 0;  // chunks of either ring
+        bool ok = true;
+        MmTile c;
+        for (int32_t i = 0; ok && take(i, c, false); ++i) {
+          // (the same turns as the epilogue's)
+          const uint32_t part = (c.len > 0 ? turn++ : static_cast<uint32_t>(i)) & 1u;
+          for (int32_t j0 = 0; j0 < c.valid; j0 += Cfg::kChunk) {
+            const uint32_t n = part == 0 ? count0++ : count1++, slot = n % add_slots;
+            ok = wait_bar(addfree_bar(part, slot), ((n / add_slots) & 1u) ^ 1u, abort_flag,
+                          p.status,
+                          p.timeout_ns);
+            if (!ok) break;
+            ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
+            ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &maps.add,
+                             add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * wide,
+                             c.r0 + j0, c.g);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == static_cast<uint32_t>(Cfg::kTileWarp)) {
+      // -------------------------------------------------------------- tiles
+      // Round n goes over the workers from the n-th on, so that a worker does not get the same row
+      // tile of every column: those of fewer rows take less time, and workers that get ahead of
+      // others read the weights from memory instead of sharing them in L2 (32 experts of 480 rows,
+      // 4096 x 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a
+      // time, one by each lane (a search and up to four divisions), and handed on one by one.
+      int32_t i = 0;
+      bool ok = true;
+      for (int64_t n0 = 0; ok; n0 += 32) {
+        const int64_t n = n0 + lane;
+        const int64_t t = n * workers + (Cfg::kGrad ? worker : (worker + n) % workers);
+        MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
+        if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
+        const uint32_t past = __ballot_sync(0xffffffffu, c.g < 0);   // (the first of these says so)
+        const bool more = past == 0u;
+        uint32_t left = more ? 0xffffffffu : (2u << (__ffs(past) - 1)) - 1u;
+        left &= __ballot_sync(0xffffffffu, c.g < 0 || c.h > 0);
+        while (left != 0) {
+          const int src = __ffs(left) - 1;
+          left &= left - 1;
+          const int slot = i % Cfg::kRing;
+          const uint32_t par = (static_cast<uint32_t>(i / Cfg::kRing) & 1u) ^ 1u;
+          ok = __all_sync(0xffffffffu, wait_bar(taken_bar(slot), par, abort_flag, p.status,
+                                                p.timeout_ns)) != 0;
+          if (!ok) break;
+          if (static_cast<int>(lane) == src) {
+            ring[2 * slot] = make_int4(c.g, c.c0, c.r0, c.h);
+            ring[2 * slot + 1] = make_int4(c.valid, c.k0, c.len, c.part);
+            ptx::mbar_arrive(tile_bar(slot));
+          }
+          __syncwarp();
+          ++i;
+        }
+        if (!more) break;
+      }
     }
-    __syncwarp();
-  } else if (Cfg::kGrad && warp == Cfg::kEdgeWarp) {
-    // -------------------------------------------------------------- ends of experts' rows
-    // The last stage of an expert whose rows do not end with an MMA step of 16: its last step
-    // holds rows of the next expert (or past the buffers).  They are zeroed in both operands (0 x
-    // NaN is NaN): whole 128-byte lines here, since the rows are the operands' lines.
-    int stage = 0;
-    uint32_t parity = 0;  // of each stage's edge barrier, one bit
+  } else if constexpr (Cfg::kLong) {
+    // -------------------------------------------------------------- epilogue, many rows
+    // Eight warps for a tile: one for each quarter of the TMEM lanes and half of the output rows,
+    // whose sums they keep.
+    ptx::setmaxnreg_inc<Cfg::kRegsMany>();
+    constexpr int kHalf = Cfg::kTileN / 2;
+    const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
+    uint32_t used = 0;
     MmTile c;
     for (int32_t i = 0; take(i, c, true); ++i) {
-      if (c.len == 0) continue;
-      const int32_t kbs = (c.len + Cfg::kBK - 1) / Cfg::kBK;
-      const int last = (stage + kbs - 1) % Cfg::kStages;
-      stage = (stage + kbs) % Cfg::kStages;
-      if ((c.len & 15) == 0) continue;
-      const bool ok = wait_bar(edge_bar(last), (parity >> last) & 1u, abort_flag, p.status,
-                               p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      parity ^= 1u << last;
-      const int32_t in = c.len - (kbs - 1) * Cfg::kBK;  // rows of the stage that are the expert's
-      const int32_t lines = ((in + 15) & ~15) - in;
-      const int32_t boxes = c.h / Cfg::kCtas <= 64 ? 1 : 2;
-      for (int32_t i = static_cast<int32_t>(lane); i < (2 + boxes) * lines * 8; i += 32) {
-        const int32_t line = in + (i >> 3) % lines, piece = (i >> 3) / lines;
-        const uint32_t base = piece < 2 ? s_p + last * Cfg::kPBytes + piece * Cfg::kMnPiece
-                                        : s_q + last * Cfg::kQBytes + (piece - 2) * Cfg::kMnPiece;
-        ptx::st_shared_v4(base + static_cast<uint32_t>(line) * 128u + (i & 7) * 16u, 0u, 0u, 0u,
-                          0u);
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      // pairs: the leader's edge warp hands the stage on when the peer's has done its part
-      if (Cfg::kPair && crank != 0) {
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(peer_bar(last), 0u));
+      const int32_t n = min(kHalf, c.valid - static_cast<int32_t>(part) * kHalf);
+      const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide +
+                          static_cast<int32_t>(q * 32u + lane);
+      const bool in = col < p.C;
+      const int64_t at = (static_cast<int64_t>(c.g) * p.R + c.r0 + part * kHalf) * p.C + col +
+                         c.part * p.slice;
+      // what is added comes first: its loads pass while the first rows are summed
+      float sum[kHalf];
+      if (p.add != nullptr) {
+        const int32_t there = in ? n : 0;
+        mm_rows<kHalf>(static_cast<const float*>(p.add) + at, p.C,
+                       [&](int j, const float* a) { sum[j] = j < there ? *a : 0.f; });
       } else {
-        if constexpr (Cfg::kPair) {
-          const bool there = wait_bar<true>(peer_bar(last), (parity >> last) & 1u ^ 1u, abort_flag,
-                                            p.status, p.timeout_ns);
-          if (!__all_sync(0xffffffffu, there)) break;
-        }
-        if (lane == 0) ptx::mbar_arrive(full_bar(last));
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) sum[j] = 0.f;
       }
-    }
-  } else if (Cfg::kAddRing && warp == Cfg::kAddWarp) {
-    // -------------------------------------------------------------- what is added
-    if (lane == 0) {
-      uint32_t used = 0, count0 = 0, count1 = 0;  // chunks of either ring
       bool ok = true;
-      MmTile c;
-      for (int32_t i = 0; ok && take(i, c, false); ++i) {
-        // (the same turns as the epilogue's)
-        const uint32_t part = c.len > 0 ? used++ & 1u : static_cast<uint32_t>(i) & 1u;
-        for (int32_t j0 = 0; j0 < c.valid; j0 += Cfg::kChunk) {
-          const uint32_t n = part == 0 ? count0++ : count1++, slot = n % add_slots;
-          ok = wait_bar(addfree_bar(part, slot), ((n / add_slots) & 1u) ^ 1u, abort_flag, p.status,
-                        p.timeout_ns);
-          if (!ok) break;
-          ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
-          ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &maps.add,
-                           add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * wide,
-                           c.r0 + j0, c.g);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == static_cast<uint32_t>(Cfg::kTileWarp)) {
-    // -------------------------------------------------------------- tiles
-    // Round n goes over the workers from the n-th on, so that a worker does not get the same row tile
-    // of every column: those of fewer rows take less time, and workers that get ahead of others
-    // read the weights from memory instead of sharing them in L2 (32 experts of 480 rows, 4096 x
-    // 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a time, one by each lane
-    // (a search and up to four divisions), and handed on one after the other.
-    int32_t i = 0;
-    bool ok = true;
-    for (int64_t n0 = 0; ok; n0 += 32) {
-      const int64_t n = n0 + lane;
-      const int64_t t = n * workers + (Cfg::kGrad ? worker : (worker + n) % workers);
-      MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
-      if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
-      const uint32_t past = __ballot_sync(0xffffffffu, c.g < 0);   // (the first of these says so)
-      const bool more = past == 0u;
-      uint32_t left = more ? 0xffffffffu : (2u << (__ffs(past) - 1)) - 1u;
-      left &= __ballot_sync(0xffffffffu, c.g < 0 || c.h > 0);
-      while (left != 0) {
-        const int src = __ffs(left) - 1;
-        left &= left - 1;
-        const int slot = i % Cfg::kRing;
-        ok = __all_sync(0xffffffffu,
-                        wait_bar(taken_bar(slot), (static_cast<uint32_t>(i / Cfg::kRing) & 1u) ^ 1u,
-                                 abort_flag, p.status, p.timeout_ns)) != 0;
+      for (int32_t k = 0; k < c.len; k += sum_rows) {
+        const uint32_t b = used & 1u;
+        ok = wait_bar(tfull_bar(0u, b), (used >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok) != 0;
         if (!ok) break;
-        if (static_cast<int>(lane) == src) {
-          ring[2 * slot] = make_int4(c.g, c.c0, c.r0, c.h);
-          ring[2 * slot + 1] = make_int4(c.valid, c.k0, c.len, c.part);
-          ptx::mbar_arrive(tile_bar(slot));
+        ++used;
+        ptx::tc_fence_after_sync();
+#pragma unroll
+        for (int j0 = 0; j0 < kHalf; j0 += 32) {
+          if (j0 < n) {
+            uint32_t v[32];
+            ptx::tmem_ld_x32(tmem_base + b * Cfg::kTileN + part * kHalf + j0 + ((q * 32u) << 16),
+                             v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[j0 + j] += __uint_as_float(v[j]);
+          }
         }
+        ptx::tc_fence_before_sync();
         __syncwarp();
-        ++i;
+        if (lane == 0) {
+          if (Cfg::kPair && crank != 0)
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
+          else
+            ptx::mbar_arrive(tempty_bar(b));
+        }
       }
-      if (!more) break;
+      if (!ok) break;
+      float* out = static_cast<float*>(p.out) + at;
+      if (in && n >= kHalf)
+        mm_rows<kHalf>(out, p.C, [&](int j, float* to) { *to = sum[j]; });
+      else if (in)
+        mm_rows<kHalf>(out, p.C, [&](int j, float* to) { if (j < n) *to = sum[j]; });
     }
-  } else if (warp >= Cfg::kEpiWarp0) {
+  } else {
     // -------------------------------------------------------------- epilogue
     // Four warps for a tile, one for each quarter of the TMEM lanes.  Eight warps take turns: while
     // four store a tile the others wait for the sums of the next (all eight at one tile: 622 us
@@ -791,7 +883,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       MmChunk<T, kN> chunk;
       const T* add0 = static_cast<const T*>(p.add);
       const bool bf16 = p.bf16 != 0;
-      uint32_t used = 0;
+      uint32_t used = 0, turn = 0;
+      uint32_t seen = 0;   // parity of the completions seen, a bit for each buffer
       MmTile c;
       for (int32_t i = 0;; ++i) {
         bool ok = take(i, c, true);
@@ -800,79 +893,94 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int32_t col = col0 + static_cast<int32_t>(q * 32u + lane);
         const bool in = col < col0 + cols;
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
-        int64_t at = row0 * p.C + c.part * p.slice;
+        const int64_t at0 = row0 * p.C + c.part * p.slice;
         const bool any = ok && c.len > 0;  // else the empty sum
-        const uint32_t b = used & 1u;
-        const bool mine = kParts == 1 || (any ? b : static_cast<uint32_t>(i) & 1u) == part;
+        const bool mine = kParts == 1 || ((any ? turn : static_cast<uint32_t>(i)) & 1u) == part;
         if constexpr (kLoad) {
-          if (ok && mine) chunk.load_add(add0 + at + col, p.C, c.valid, in);
+          if (ok && mine) chunk.load_add(add0 + at0 + col, p.C, c.valid, in);
         }
-        if (any && mine) {
-          ok = wait_bar(tfull_bar(static_cast<int>(b)), (used >> 1) & 1u, abort_flag, p.status,
-                        p.timeout_ns);
-          ok = __all_sync(0xffffffffu, ok) != 0;
-          ptx::tc_fence_after_sync();
-        }
-        if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
-        if (!ok) break;
-        used += any ? 1u : 0u;
-        if (!mine) continue;
-        for (int32_t j0 = 0; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
-          uint32_t v[kN];
+        int32_t k = 0;
+        do {   // over the sums of sum_rows rows (16-bit results: of all)
+          const uint32_t b = used & 1u;
+          if (any && mine) {
+            ok = wait_bar(tfull_bar(part, b), (seen >> b) & 1u, abort_flag, p.status,
+                          p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            seen ^= 1u << b;
+            ptx::tc_fence_after_sync();
+          }
+          if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
+          if (!ok) break;
+          used += any ? 1u : 0u;
+          if (!mine) continue;
+          int64_t at = at0;
+          for (int32_t j0 = 0; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
+            uint32_t v[kN];
+            if (any) {
+              const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
+                                    ((q * 32u) << 16);
+              if constexpr (kN == 32) ptx::tmem_ld_x32(from, v);
+              else ptx::tmem_ld_x16(from, v);
+              ptx::tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < kN; ++j) v[j] = 0u;
+            }
+            const int32_t n = c.valid - j0;
+            if constexpr (Cfg::kGrad && sizeof(T) == 4) {
+              if (k > 0) {   // onto the sums so far
+                MmChunk<float, kN> so_far;
+                so_far.load_add(out0 + at + col, p.C, n, in);
+                so_far.template store<true>(out0 + at + col, p.C, n, in, v, bf16, lane);
+                continue;
+              }
+            }
+            if constexpr (Cfg::kAddRing) {
+              const uint32_t slot = adds % add_slots;
+              bool got = wait_bar(add_bar(part, slot), (adds / add_slots) & 1u, abort_flag,
+                                  p.status, p.timeout_ns);
+              got = __all_sync(0xffffffffu, got) != 0;
+              if constexpr (kWhole) got = named_bar_and(bar, got);
+              if (!got) return;
+              ++adds;
+              const uint32_t from = s_add + part * Cfg::kAddBytes + slot * add_chunk +
+                                    (q * 32u + lane) * sizeof(T);
+#pragma unroll
+              for (int j = 0; j < kN; ++j) {
+                float a;
+                if constexpr (sizeof(T) == 4)
+                  a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
+                else
+                  a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
+                v[j] = __float_as_uint(a + __uint_as_float(v[j]));
+              }
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
+            }
+            if constexpr (kWhole) {
+              MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
+            } else {
+              auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
+              if constexpr (kLoad) {
+                if (n > kN)
+                  chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
+              }
+              now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16, lane);
+            }
+          }
           if (any) {
-            const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
-                                  ((q * 32u) << 16);
-            if constexpr (kN == 32) ptx::tmem_ld_x32(from, v);
-            else ptx::tmem_ld_x16(from, v);
-            ptx::tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int j = 0; j < kN; ++j) v[j] = 0u;
-          }
-          const int32_t n = c.valid - j0;
-          if constexpr (Cfg::kAddRing) {
-            const uint32_t slot = adds % add_slots;
-            bool got = wait_bar(add_bar(part, slot), (adds / add_slots) & 1u, abort_flag, p.status,
-                                p.timeout_ns);
-            got = __all_sync(0xffffffffu, got) != 0;
-            if constexpr (kWhole) got = named_bar_and(bar, got);
-            if (!got) return;
-            ++adds;
-            const uint32_t from = s_add + part * Cfg::kAddBytes + slot * add_chunk +
-                                  (q * 32u + lane) * sizeof(T);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-              float a;
-              if constexpr (sizeof(T) == 4)
-                a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
-              else
-                a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
-              v[j] = __float_as_uint(a + __uint_as_float(v[j]));
-            }
+            ptx::tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
-          }
-          if constexpr (kWhole) {
-            MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
-          } else {
-            auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
-            if constexpr (kLoad) {
-              if (n > kN)
-                chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
+            if (lane == 0) {
+              if (Cfg::kPair && crank != 0)
+                ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
+              else
+                ptx::mbar_arrive(tempty_bar(b));
             }
-            now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16, lane);
           }
-        }
-        if (any) {
-          ptx::tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (Cfg::kPair && crank != 0)
-              ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(static_cast<int>(b)), 0u));
-            else
-              ptx::mbar_arrive(tempty_bar(static_cast<int>(b)));
-          }
-        }
+        } while (any && (k += sum_rows) < c.len);
+        if (!ok) break;
+        turn += any ? 1u : 0u;
       }
     };
     const std::true_type yes{};
@@ -1002,7 +1110,8 @@ __global__ void __launch_bounds__(kCopyThreads)
     for (int i = 0; i < kWords; ++i) {
       uint32_t w = v[i];
       if (s != 0) {
-        const uint32_t next = __shfl_sync(0xffffffffu, lane == 0 ? v[i + 1] : v[i], (lane + 1) & 31);
+        const uint32_t next =
+            __shfl_sync(0xffffffffu, lane == 0 ? v[i + 1] : v[i], (lane + 1) & 31);
         w = (w >> 16) | (next << 16);
       }
       if (2 * (lane + 32 * i) < left) to[32 * i] = w;

@@ -118,6 +118,44 @@ def test_weight_grad(shape, dtype, grad):
         check_grad(dw, dy, x, counts, add, f"counts {counts}")
 
 
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("counts", [[1300, 40, 0, 3], [5, 2049, 7, 300, 0, 2], [1024] * 3,
+                                    [4000, 1], [513] * 9])
+@pytest.mark.parametrize("shape", [(200, 264), (512, 512), (77, 130)])
+def test_weight_grad_many_rows(shape, counts, add):
+    """Experts with more rows than the tensor core sums at a time, beside others with few; fp32
+    sums are made 512 rows at a time, so the lost bits do not grow with the rows: 512 * 2^-23 of
+    the magnitudes, and a rounding for each of the sums of 512."""
+    n, k = shape
+    m = sum(counts)
+    dy, x = randn(1, m, n), randn(2, m, k)
+    for grad in (FP32, BF16):
+        before = randn(3, len(counts), n, k, dtype=grad) if add else None
+        dw = fx.grouped_mm_weight_grad(dy, x, sizes(counts), add=before, dtype=grad)
+        check_grad(dw, dy, x, counts, before)
+        if grad is FP32:
+            for g, (a, b) in enumerate(bounds(counts)):
+                want, mag = np64(dy[a:b]).T @ np64(x[a:b]), np.abs(np64(dy[a:b])).T @ np.abs(
+                    np64(x[a:b]))
+                if add:
+                    want, mag = want + np64(before[g]), mag + np.abs(np64(before[g]))
+                close(np64(dw[g]), want, off(512 + (b - a) // 512 + 2, mag, want, FP32),
+                      f"expert {g}")
+
+
+def test_weight_grad_error_does_not_grow():
+    """Sums of 64 to 16384 rows of normal values, as 2-norms: half of the last place that the
+    tensor core loses in each of 512 / 16 steps, downwards, is 32 * 2^-24 at the most."""
+    for rows in (64, 1024, 4096, 16384):
+        for experts in (1, 40):
+            m = rows * experts
+            dy, x = randn(rows, m, 64), randn(rows + 1, m, 128)
+            dw = fx.grouped_mm_weight_grad(dy, x, sizes([rows] * experts))
+            want = dy[-rows:].double().t() @ x[-rows:].double()
+            rel = ((dw[-1].double() - want).norm() / want.norm()).item()
+            assert rel <= 32 * 2.0 ** -24, (rows, experts, rel)
+
+
 def test_weight_grad_in_place():
     counts = [40, 0, 9]
     dy, x = randn(1, 49, 128), randn(2, 49, 256)
