@@ -23,6 +23,12 @@ TYPES = [BF16, FP16, FP32]
 NAN, INF = float("nan"), float("inf")
 
 
+def stream():
+    """A stream of the pool that holds those of high priority: the ordinary pool's 32 go round, and
+    tests that count the workspaces kept by stream take theirs from it."""
+    return torch.cuda.Stream(priority=-1)
+
+
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
     if not torch.cuda.is_available():
@@ -205,7 +211,7 @@ def test_streams_and_graphs():
         grads = grads_of(sizes)
         out = (torch.zeros((), device="cuda"), [torch.zeros_like(g) for g in grads])
         only = torch.zeros((), device="cuda")
-        side = torch.cuda.Stream()
+        side = stream()
         torch.cuda.synchronize()
         fx.clip_grad_norm(grads, 0.25, out=out, stream=side)
         fx.grad_norm(grads, out=only, stream=side.cuda_stream)
@@ -216,7 +222,7 @@ def test_streams_and_graphs():
         with torch.cuda.graph(graph):
             fx.clip_grad_norm(grads, 0.25, out=out)
             fx.grad_norm(grads, out=only)
-        runs.append((graph, grads, out, only, torch.cuda.Stream()))
+        runs.append((graph, grads, out, only, stream()))
     for i, (_, grads, *_) in enumerate(runs):
         for j, g in enumerate(grads):
             g.copy_(randn(100 + 10 * i + j, *g.shape))
