@@ -101,8 +101,8 @@ mslkb_status encode(MmParams& p, MmMaps* maps) {
 // Output columns of a CTA's share of a tile.  With few rows per expert the time is that of reading
 // the weights, and a worker's that of its tiles' columns: of the widths up to 128, the one with
 // which the worker of most columns has fewest, if as many experts have rows as can have.  One token
-// on 8 experts of 4096 x 7168 on GB300, 76 pairs: two rounds of 256 columns (128 tiles) 84 us, of
-// 216 (152 tiles) 74.
+// on 8 experts of 4096 x 7168 on GB300, 76 pairs: two rounds of 256 columns (128 tiles) 83 us, of
+// 216 (152 tiles) 79.
 // (Split contractions fill the workers by themselves.)
 template <class Cfg>
 int32_t tile_columns(const MmParams& p, int sms) {
@@ -134,12 +134,12 @@ mslkb_status run(MmParams& p, int sms, void* stream) {
     // experts of 4096 x 7168 on GB300, us in registers / onto the result: 1024 rows each 1404 /
     // 2235; 256 each 789 / 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280)
     if (p.out32 && p.total >= 192ll * p.G * p.splits)
-      return run_as<MmCfg<kMode, 2, 256, 1, 6, 8, false, true>>(p, sms, stream);
+      return run_as<MmCfg<kMode, false, true>>(p, sms, stream);
     const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
     if (p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0)
-      return run_as<MmCfg<kMode, 2, 256, 1, 4, 8, true>>(p, sms, stream);
+      return run_as<MmCfg<kMode, true>>(p, sms, stream);
   }
-  return run_as<MmCfg<kMode, 2, 256, 1, 6, 8>>(p, sms, stream);
+  return run_as<MmCfg<kMode>>(p, sms, stream);
 }
 
 bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
@@ -362,6 +362,11 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
   if (!aligned_to(x, 2) || !aligned_to(dy, 2) || !aligned_to(m_sizes, 8) ||
       !aligned_to(dw, wide) || !aligned_to(add, wide))
     return MSLKB_ERR_ALIGN;
+  if (add != nullptr && add != dw) {   // (added to what has not been written yet)
+    const uintptr_t a = reinterpret_cast<uintptr_t>(add), b = reinterpret_cast<uintptr_t>(dw);
+    const double bytes = static_cast<double>(G) * N * K * wide;
+    if (static_cast<double>(a < b ? b - a : a - b) < bytes) return MSLKB_ERR_SHAPE;
+  }
   Operand o[2] = {{x, total_M, K, ldx, 0}, {dy, total_M, N, lddy, 0}};
   const int64_t copies = copies_bytes(o);
   const int32_t splits = grad_splits(total_M, G, N, K);

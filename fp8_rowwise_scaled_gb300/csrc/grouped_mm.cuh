@@ -7,20 +7,20 @@
 //
 // All three are D[c, r] = sum_k P[c, k] * Q[r, k] with the output's columns c on the MMA's M side
 // (TMEM lanes) and its rows r on the N side (TMEM columns).  So the rows of an expert, ragged,
-// cost the tensor core what they are, rounded up to 16 (32 on CTA pairs) and not to a tile's 128
-// or 256; and a warp reads 32 neighbouring columns of one output row from TMEM, which it stores as
-// one piece.  P is w or x, Q is x or dy; an operand whose contracted index is its rows (w turned,
-// both operands of kGrad) is read as it lies in memory, "MN-major": the tensor core takes either.
+// cost the tensor core what they are, rounded up to 32, and not to a tile's 128 or 256; and a warp
+// reads 32 neighbouring columns of one output row from TMEM, which it stores as one piece.  P is w
+// or x, Q is x or dy; an operand whose contracted index is its rows (w turned, both operands of
+// kGrad) is read as it lies in memory, "MN-major": the tensor core takes either.
 //
-// A CTA (or a pair of CTAs on two SMs: 256 x 256 tiles, each CTA holding half of either operand)
-// is persistent and specialised by warp:
+// A pair of CTAs on two SMs (tiles of 256 x 256, each CTA holding half of either operand) is
+// persistent and specialised by warp:
 //   warp 0      loads by TMA (operands whose rows do not start on 16 bytes are copied to rows that
 //               do, before: aligned_rows_kernel)
 //   warp 1      issues the MMAs
 //   warp 2      zeroes what a stage holds past the end of an expert's rows (kGrad)
 //   warp 3      works out the tiles and hands them to the other warps
 //   warp 4      loads what is added to a gradient (with three idle ones, only where there is some)
-//   the last 8  the epilogue, four from either accumulator while the other fills.
+//   the last 8  the epilogue: four and four in turns, or all of them where they keep sums.
 #pragma once
 
 #include <cuda.h>
@@ -66,30 +66,26 @@ struct MmMaps {
   CUtensorMap p, q, q64, add;
 };
 
-template <Mm kMode_, int kCtas_, int kTileN_, int kKB_, int kStages_, int kEpiWarps_,
-          bool kAdd_ = false, bool kLong_ = false>
+template <Mm kMode_, bool kAdd_ = false, bool kLong_ = false>
 struct MmCfg {
   static constexpr Mm kMode = kMode_;
   static constexpr bool kGrad = kMode == Mm::kGrad;
   static constexpr bool kPMn = kMode != Mm::kRows;  // the operand's rows are the contraction
   static constexpr bool kQMn = kGrad;
-  static constexpr int kCtas = kCtas_;
-  static constexpr bool kPair = kCtas == 2;
-  static constexpr int kTileN = kTileN_;           // output rows of a tile
-  static constexpr int kBK = 64 * kKB_;            // contraction per stage: 128-byte pieces
-  static constexpr int kKB = kKB_;
-  static constexpr int kStages = kStages_;
+  static constexpr int kCtas = 2;
+  static constexpr int kTileN = 256;               // output rows of a tile
+  static constexpr int kBK = 64;                   // contraction per stage: 128-byte pieces
+  static constexpr int kStages = kAdd_ ? 4 : 6;
   static constexpr int kQRows = kTileN / kCtas;    // of Q in one CTA
-  static_assert(kQRows == 128 || kQRows == 64, "boxes of Q");
   static constexpr int kPBytes = 128 * kBK * 2;
   static constexpr int kQBytes = kQRows * kBK * 2;
   static constexpr int kStageBytes = kPBytes + kQBytes;
   static constexpr int kMmaWarp = 1;
   static constexpr int kEdgeWarp = 2;
   static constexpr int kTileWarp = 3;  // hands out the tiles
-  // kGrad by TMA with something to add: that comes by TMA too, chunk by chunk, through a ring of
-  // its own for each four of the epilogue's warps (loaded by the epilogue's threads themselves,
-  // one or two chunks ahead: 1487 us for 32 x 4096 x 7168 fp32, 1264 bf16)
+  // kGrad with something to add: that comes by TMA too, chunk by chunk, through a ring of its own
+  // for each four of the epilogue's warps (32 experts of 75 rows, 4096 x 7168 on GB300: 1331 us
+  // fp32, 711 bf16; loaded by the epilogue's threads themselves, a chunk ahead, 1541 and 1031)
   static constexpr bool kAddRing = kAdd_;
   // The tensor core's sums lose what lies below their last bit, always downwards: some 1e-9 of the
   // result for every row summed (fp32 results of 4096 rows, normal values, were 4.4e-6 off).  So
@@ -102,24 +98,23 @@ struct MmCfg {
   static constexpr int kAddWarp = 4;
   static constexpr int kAddBytes = kAddRing ? 32768 : 0;
   static constexpr int kEpiWarp0 = kAddRing ? 8 : 4;
-  static constexpr int kEpiWarps = kEpiWarps_;
+  static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   static constexpr int kRowStep = 16 * kCtas;      // a tile's rows are rounded up to these
-  static constexpr int kTmemCols = 2 * kTileN < 32 ? 32 : 2 * kTileN;
-  static constexpr int kChunk = kTileN < 32 ? kTileN : 32;  // TMEM columns read at a time
+  static constexpr int kTmemCols = 2 * kTileN;
+  static constexpr int kChunk = 32;                // TMEM columns read at a time
   // rows of tiles that run next to each other: 8 x 9.5 tiles of 256 x 256 on 76 CTA pairs read
   // the fewest bytes between them
   static constexpr int kBand = 8;
-  // bytes between the 64-element pieces of an MN-major operand, and the step of 16 of the
-  // contraction, in the 16-byte units of a shared-memory descriptor
+  // bytes between the 64-element pieces of an MN-major operand
   static constexpr uint32_t kMnPiece = kBK * 128;
 
   static constexpr int kOffP = 0;
   static constexpr int kOffQ = kStages * kPBytes;
   static constexpr int kStagePart = 8192;  // the epilogue's rows: 32 x 128 in 16 bits
   static constexpr int kOffStage = kOffQ + kStages * kQBytes;
-  static constexpr int kOffAdd = kOffStage + kEpiWarps / 4 * kStagePart;
-  static constexpr int kOffBar = kOffAdd + kEpiWarps / 4 * kAddBytes;
+  static constexpr int kOffAdd = kOffStage + (kLong ? 0 : 2 * kStagePart);
+  static constexpr int kOffBar = kOffAdd + 2 * kAddBytes;
   // the scheduler warp hands tiles to the other roles through a ring
   static constexpr int kRing = 4;
   static constexpr int kRingUsers = 2 + (kGrad ? 1 : 0) + (kAddRing ? 1 : 0) + kEpiWarps;
@@ -130,18 +125,16 @@ struct MmCfg {
   static constexpr int kOffSched = kOffRing + kRing * 32;
   static constexpr int kSmemBytes = kOffSched + 2 * 4 * (kMaxGroups + 1) + 1024;
 
-  static_assert(kTileN % 16 == 0 && kTileN <= 256 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
-  static_assert(!kQMn || kQRows % 64 == 0, "MN-major pieces of 64");
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(!kLong || (kGrad && !kAddRing && kThreads == 384 && kTileN == 256 &&
+  static_assert(!kLong || (kGrad && !kAddRing && kThreads == 384 &&
                            128 * kRegsFew + 256 * kRegsMany <= 384 * 168), "registers");
-  static_assert(!kAddRing || (kGrad && kEpiWarps == 8 && kChunk == 32), "what is added");
+  static_assert(!kAddRing || kGrad, "what is added");
 };
 
 // A tile: its group (-1: past the last tile), first output column and row, rows (h: rounded up,
-// valid: real), and the contraction [k0, k0 + len) (kGrad: rows of x and dy), or the part of it that
-// is this tile's.
+// valid: real), and the contraction [k0, k0 + len) (kGrad: rows of x and dy), or the part of it
+// that is this tile's.
 struct MmTile {
   int32_t g, c0, r0, h, valid, k0, len, part;
 };
@@ -294,25 +287,15 @@ __device__ __forceinline__ uint32_t mm_desc_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | ((kMn ? (kPiece >> 4) : 1u) << 16);
 }
 
-template <bool kPair>
 __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t p_lo, uint32_t q_lo, uint32_t idesc,
                                        uint32_t accumulate) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
-        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
-        "r"(p_lo), "r"(q_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kSw128DescHi)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
-        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
-        "r"(p_lo), "r"(q_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kSw128DescHi)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+      "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d),
+      "r"(p_lo), "r"(q_lo), "r"(idesc), "r"(accumulate), "n"(ptx::kSw128DescHi)
+      : "memory");
 }
 
 __device__ __forceinline__ uint16_t mm_round16(float v, bool bf16) {
@@ -353,7 +336,7 @@ struct MmChunk {
   }
   template <bool kAdd>
   __device__ __forceinline__ void store(T* out, int32_t C, int32_t n, bool in,
-                                        const uint32_t (&v)[kN], bool bf16, uint32_t) {
+                                        const uint32_t (&v)[kN], bool bf16) {
     auto put = [&](int j, T* to) {
       float f = __uint_as_float(v[j]);
       if constexpr (sizeof(T) == 4) {
@@ -460,7 +443,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   int32_t* tile_pre = first + (kMaxGroups + 1);
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-  const uint32_t crank = Cfg::kPair ? ptx::cluster_ctarank() : 0u;
+  const uint32_t crank = ptx::cluster_ctarank();
   const int32_t worker = static_cast<int32_t>(blockIdx.x) / Cfg::kCtas;
   const int32_t workers = static_cast<int32_t>(gridDim.x) / Cfg::kCtas;
 
@@ -498,20 +481,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     ptx::prefetch_tensormap(&maps.q64);
   }
   if (warp == Cfg::kMmaWarp) {
-    if constexpr (Cfg::kPair) {
-      ptx::tmem_alloc_pair(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
-      ptx::tmem_relinquish_pair();
-    } else {
-      ptx::tmem_alloc(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
-      ptx::tmem_relinquish();
-    }
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_holder), Cfg::kTmemCols);
+    ptx::tmem_relinquish_pair();
   }
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (warp == Cfg::kEpiWarp0) mm_schedule<Cfg>(p, first, tile_pre, lane);
   ptx::tc_fence_before_sync();
-  if constexpr (Cfg::kPair) ptx::cluster_sync();  // the peer's barriers are set up too
-  else __syncthreads();
+  ptx::cluster_sync();  // the peer's barriers are set up too
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
   const int32_t tiles = tile_pre[p.G] * p.splits, wide = mm_wide<Cfg>(p);
@@ -562,13 +539,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                                                 p.status, p.timeout_ns)) != 0;
           if (!ok) break;
           if (issuer) {
-            // pairs: the bytes of both CTAs (as many in each) complete on the leader's barrier.  A
-            // stage that ends between two MMA steps (kGrad) passes through the edge warp of each
-            // CTA first.
-            uint32_t bar = Cfg::kPair ? ptx::mapa_shared(full_bar(stage), 0u) : full_bar(stage);
+            // the bytes of both CTAs (as many in each) complete on the leader's barrier.  A stage
+            // that ends between two MMA steps (kGrad) passes through the edge warp of each CTA
+            // first.
+            uint32_t bar = ptx::mapa_shared(full_bar(stage), 0u);
             const bool edge = Cfg::kGrad && c.len - k < Cfg::kBK && (c.len & 15) != 0;
             if (edge) {
-              bar = Cfg::kPair ? ptx::mapa_shared(edge_bar(stage), crank) : edge_bar(stage);
+              bar = ptx::mapa_shared(edge_bar(stage), crank);
               ptx::mbar_arrive_expect_tx(edge_bar(stage), bytes);
             } else if (crank == 0) {
               ptx::mbar_arrive_expect_tx(full_bar(stage), bytes * Cfg::kCtas);
@@ -576,26 +553,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             const int32_t x = c.k0 + k;
             const uint32_t dp = s_p + stage * Cfg::kPBytes, dq = s_q + stage * Cfg::kQBytes;
             auto load2 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b) {
-              if constexpr (Cfg::kPair) ptx::tma_load_2d_pair(dst, m, bar, a, b);
-              else ptx::tma_load_2d(dst, m, bar, a, b);
+              ptx::tma_load_2d_pair(dst, m, bar, a, b);
             };
             auto load3 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t g) {
-              if constexpr (Cfg::kPair) ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
-              else ptx::tma_load_3d(dst, m, bar, a, b, g);
-            };
-            auto load4 = [&](uint32_t dst, const CUtensorMap* m, int32_t a, int32_t b, int32_t z,
-                             int32_t g) {
-              if constexpr (Cfg::kPair) ptx::tma_load_4d_pair(dst, m, bar, a, b, z, g);
-              else ptx::tma_load_4d(dst, m, bar, a, b, z, g);
+              ptx::tma_load_3d_pair(dst, m, bar, a, b, g);
             };
             // (few, large operations: an SM's loads are limited by their number as well)
             if constexpr (Cfg::kMode == Mm::kRows) {
-#pragma unroll
-              for (int i = 0; i < Cfg::kKB; ++i)
-                load3(dp + i * 128 * 128, &maps.p, x + 64 * i, col, c.g);
+              load3(dp, &maps.p, x, col, c.g);
             } else if constexpr (Cfg::kMode == Mm::kTurned) {
               if (p.p_pieces) {
-                load4(dp, &maps.p, 0, x, col / 64, c.g);
+                ptx::tma_load_4d_pair(dp, &maps.p, bar, 0, x, col / 64, c.g);
               } else {
                 load3(dp, &maps.p, col, x, c.g);
                 load3(dp + Cfg::kMnPiece, &maps.p, col + 64, x, c.g);
@@ -616,9 +584,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 if (!half) load2(dq + Cfg::kMnPiece, &maps.q64, row + 64, x);
               }
             } else {
-#pragma unroll
-              for (int j = 0; j < Cfg::kKB; ++j)
-                load2(dq + j * Cfg::kQRows * 128, half ? &maps.q64 : &maps.q, x + 64 * j, row);
+              load2(dq, half ? &maps.q64 : &maps.q, x, row);
             }
           }
           if (++stage == Cfg::kStages) {
@@ -657,7 +623,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int32_t k = 0; k < len;) {
             const uint32_t b = used & 1u;
             ok = __all_sync(0xffffffffu,
-                            wait_bar<Cfg::kPair>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
+                            wait_bar<true>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
                                                  p.status, p.timeout_ns)) != 0;
             if (!ok) break;
             ++used;
@@ -676,16 +642,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < Cfg::kBK / 16; ++s) {
                   constexpr uint32_t kMn16 = 16 * 128 / 16;
-                  const uint32_t po =
-                      Cfg::kPMn ? s * kMn16 : (s / 4) * (128 * 128 / 16) + (s % 4) * 2;
-                  const uint32_t qo =
-                      Cfg::kQMn ? s * kMn16 : (s / 4) * (Cfg::kQRows * 128 / 16) + (s % 4) * 2;
                   if (s < steps)
-                    mm_mma<Cfg::kPair>(d, p_lo + po, q_lo + qo, idesc,
-                                     (k > from || s > 0) ? 1u : 0u);
+                    mm_mma(d, p_lo + s * (Cfg::kPMn ? kMn16 : 2u),
+                           q_lo + s * (Cfg::kQMn ? kMn16 : 2u), idesc,
+                           (k > from || s > 0) ? 1u : 0u);
                 }
-                if constexpr (Cfg::kPair) ptx::mma_commit_pair(empty_bar(stage), 0x3);
-                else ptx::mma_commit(empty_bar(stage));
+                ptx::mma_commit_pair(empty_bar(stage), 0x3);
               }
               if (++stage == Cfg::kStages) {
                 stage = 0;
@@ -693,12 +655,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               }
             }
             if (!ok) break;
-            if (issuer) {
-              if constexpr (Cfg::kPair) ptx::mma_commit_pair(tfull_bar(turn, b), 0x3);
-              else ptx::mma_commit(tfull_bar(turn, b));
-            }
+            if (issuer) ptx::mma_commit_pair(tfull_bar(turn, b), 0x3);
           }
-          if (!Cfg::kLong && Cfg::kEpiWarps == 8) turn ^= 1u;
+          if (!Cfg::kLong) turn ^= 1u;
         }
       }
       __syncwarp();
@@ -732,15 +691,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        // pairs: the leader's edge warp hands the stage on when the peer's has done its part
-        if (Cfg::kPair && crank != 0) {
+        // the leader's edge warp hands the stage on when the peer's has done its part
+        if (crank != 0) {
           if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(peer_bar(last), 0u));
         } else {
-          if constexpr (Cfg::kPair) {
-            const bool there = wait_bar<true>(peer_bar(last), ((parity >> last) & 1u) ^ 1u, abort_flag,
-                                              p.status, p.timeout_ns);
-            if (!__all_sync(0xffffffffu, there)) break;
-          }
+          const bool there = wait_bar<true>(peer_bar(last), ((parity >> last) & 1u) ^ 1u,
+                                            abort_flag, p.status, p.timeout_ns);
+          if (!__all_sync(0xffffffffu, there)) break;
           if (lane == 0) ptx::mbar_arrive(full_bar(last));
         }
       }
@@ -852,7 +809,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         ptx::tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if (Cfg::kPair && crank != 0)
+          if (crank != 0)
             ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
           else
             ptx::mbar_arrive(tempty_bar(b));
@@ -868,10 +825,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   } else {
     // -------------------------------------------------------------- epilogue
     // Four warps for a tile, one for each quarter of the TMEM lanes.  Eight warps take turns: while
-    // four store a tile the others wait for the sums of the next (all eight at one tile: 622 us
-    // where the stores alone are 430, 32 x 64 rows, 4096 x 7168 fp32).
+    // four store a tile the others wait for the sums of the next (weights' gradient of 256 rows, 32
+    // x 4096 x 7168 bf16 on GB300: 417 us; all eight at one tile 599).
     const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
-    constexpr uint32_t kParts = Cfg::kEpiWarps / 4;
     const uint32_t stage = ptx::smem_addr(smem + Cfg::kOffStage) + part * Cfg::kStagePart;
     const uint32_t bar = 1u + part;  // of this part's four warps
     uint32_t adds = 0;  // chunks of the ring taken
@@ -895,7 +851,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
         const int64_t at0 = row0 * p.C + c.part * p.slice;
         const bool any = ok && c.len > 0;  // else the empty sum
-        const bool mine = kParts == 1 || ((any ? turn : static_cast<uint32_t>(i)) & 1u) == part;
+        const bool mine = ((any ? turn : static_cast<uint32_t>(i)) & 1u) == part;
         if constexpr (kLoad) {
           if (ok && mine) chunk.load_add(add0 + at0 + col, p.C, c.valid, in);
         }
@@ -919,8 +875,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             if (any) {
               const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
                                     ((q * 32u) << 16);
-              if constexpr (kN == 32) ptx::tmem_ld_x32(from, v);
-              else ptx::tmem_ld_x16(from, v);
+              ptx::tmem_ld_x32(from, v);
               ptx::tmem_ld_wait();
             } else {
 #pragma unroll
@@ -931,7 +886,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               if (k > 0) {   // onto the sums so far
                 MmChunk<float, kN> so_far;
                 so_far.load_add(out0 + at + col, p.C, n, in);
-                so_far.template store<true>(out0 + at + col, p.C, n, in, v, bf16, lane);
+                so_far.template store<true>(out0 + at + col, p.C, n, in, v, bf16);
                 continue;
               }
             }
@@ -965,14 +920,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 if (n > kN)
                   chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
               }
-              now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16, lane);
+              now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16);
             }
           }
           if (any) {
             ptx::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-              if (Cfg::kPair && crank != 0)
+              if (crank != 0)
                 ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
               else
                 ptx::mbar_arrive(tempty_bar(b));
@@ -1007,33 +962,28 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   // ---------------------------------------------------------------- teardown
   ptx::tc_fence_before_sync();
-  if constexpr (Cfg::kPair) {
-    // neither CTA leaves while the other may signal its barriers, and both wait out what is in
-    // flight if either gave up
-    if (lane == 0 && *abort_flag != 0u)
-      ptx::st_shared_cluster_u32(
-          ptx::mapa_shared(ptx::smem_addr(smem + Cfg::kOffMisc + 4), crank ^ 1u), 1u);
-    ptx::cluster_sync();
-  } else {
-    __syncthreads();
-  }
+  // neither CTA leaves while the other may signal its barriers, and both wait out what is in flight
+  // if either gave up
+  if (lane == 0 && *abort_flag != 0u)
+    ptx::st_shared_cluster_u32(
+        ptx::mapa_shared(ptx::smem_addr(smem + Cfg::kOffMisc + 4), crank ^ 1u), 1u);
+  ptx::cluster_sync();
   if (*abort_flag != 0u) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (ptx::globaltimer_ns() - t0 < 2000000ull) ptx::nanosleep(1000);
   }
   if (warp == Cfg::kMmaWarp) {
     ptx::tc_fence_after_sync();
-    if constexpr (Cfg::kPair) ptx::tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
-    else ptx::tmem_dealloc(tmem_base, Cfg::kTmemCols);
+    ptx::tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
   }
 }
 
 // Rows of 16-bit elements at any even address, copied to rows that start on 16 bytes: up to two
 // matrices, of which one may be the experts' (those without rows are left out).  A warp takes 512
 // elements of a row: words at aligned addresses, lane after lane, put together across lanes where
-// the row starts inside a word; nothing outside the row is read.  Bound by memory; loading such
-// rows straight into the product's stages, through registers, took 2.5 times as long (8 experts x
-// 1001 x 1002, 8000 rows on GB300: 95 us).
+// the row starts inside a word; nothing outside the row is read.  Bound by memory.  (8 experts x
+// 1001 x 1002, 8000 rows on GB300: 31 us for copy and product; loading such rows straight into the
+// product's stages, through registers, 95.)
 struct AlignedCopy {
   const uint16_t* from;
   uint16_t* to;

@@ -122,8 +122,8 @@ def grouped_mm_weight_grad(dy, x, m_sizes, *, add=None, dtype=None, out=None, st
 
     dy [total_M, N], x [total_M, K] bf16 / fp16 (rows may be strided), m_sizes [G] int64 -> dw
     [G, N, K] in ``dtype`` (fp32, the default, or dy's; that of ``add`` where it is given).  ``add``
-    is what was accumulated before and may be ``out`` itself.  Rows past sum(m_sizes) are not used;
-    an expert without rows gets ``add``, or zeros."""
+    is what was accumulated before and may be ``out`` itself (but must not overlap it otherwise).
+    Rows past sum(m_sizes) are not used; an expert without rows gets ``add``, or zeros."""
     b = _binding()
     if out is None:
         torch = _moe._torch
@@ -131,7 +131,7 @@ def grouped_mm_weight_grad(dy, x, m_sizes, *, add=None, dtype=None, out=None, st
         if not isinstance(m_sizes, torch.Tensor):
             raise TypeError("m_sizes must be a torch.Tensor")
         if dtype is None:
-            dtype = torch.float32 if add is None else add.dtype
+            dtype = add.dtype if isinstance(add, torch.Tensor) else torch.float32
         if dtype not in (torch.float32, dy.dtype):
             raise TypeError(f"dtype {dtype} is neither float32 nor dy's")
         out = _moe._new(stream, (m_sizes.numel(), N, K), dtype)

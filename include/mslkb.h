@@ -536,6 +536,7 @@ MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int6
  *   dy   device, dtype [total_M, N], rows lddy apart;  x  device, dtype [total_M, K], rows ldx
  *        apart.  Rows past the last expert's are not used, whatever they hold
  *   add  device, [G, N, K] of dw's type: what was accumulated before; NULL: nothing.  May be dw
+ *        itself, but must not overlap it otherwise (MSLKB_ERR_SHAPE)
  *   dw   device, [G, N, K], fp32 if dw_fp32 is not 0, else dtype; every element is written (an
  *        expert without rows gets add, or +0.0)
  */

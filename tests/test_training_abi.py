@@ -34,7 +34,8 @@ def test_products_refuse():
     refused(weight_grad, fx.MSLKB_ERR_NULL, *({k: None} for k in ("dy", "x", "m_sizes", "dw")))
     refused(weight_grad, fx.MSLKB_ERR_SHAPE, {"total_M": -1}, {"G": -1}, {"N": -1}, {"K": -1},
             {"ldx": 63}, {"lddy": 63}, {"G": 1025}, {"total_M": BIG}, {"N": BIG, "lddy": BIG},
-            {"K": BIG, "ldx": BIG}, {"ldx": 1 << 31}, {"lddy": 1 << 31})
+            {"K": BIG, "ldx": BIG}, {"ldx": 1 << 31}, {"lddy": 1 << 31},
+            {"add": P + 4}, {"dw": P + 4 * 2 * 64 * 64 - 4})        # over a part of each other
     refused(weight_grad, fx.MSLKB_ERR_DTYPE, {"dtype": moe.MSLKB_FP32}, {"dtype": 7})
     refused(weight_grad, fx.MSLKB_ERR_ALIGN, {"x": 257}, {"dy": 257}, {"dw": 258}, {"add": 258},
             {"m_sizes": 260}, {"dw_fp32": 0, "dw": 257})
@@ -94,7 +95,8 @@ def test_lists_refuse():
         refused(fn, fx.MSLKB_ERR_DTYPE, {"dtypes": bad_type})
         refused(fn, fx.MSLKB_ERR_ALIGN, {"grads": array(ctypes.c_void_p, 257, 4096)},
                 {"grads": array(ctypes.c_void_p, 256, 4098)}, {"norm": 258})
-        refused(fn, fx.MSLKB_ERR_WORKSPACE, {"workspace": None}, {"workspace": 264}, {"bytes": 4095})
+        refused(fn, fx.MSLKB_ERR_WORKSPACE, {"workspace": None}, {"workspace": 264},
+                {"bytes": 4095})
     refused(clip, fx.MSLKB_ERR_NULL, {"outs": None}, {"outs": array(ctypes.c_void_p, 16384, None)})
     refused(clip, fx.MSLKB_ERR_ALIGN, {"outs": array(ctypes.c_void_p, 16385, 32768)})
     refused(clip, fx.MSLKB_ERR_SHAPE, {"max_norm": -1.0}, {"max_norm": float("nan")},
