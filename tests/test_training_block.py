@@ -118,3 +118,71 @@ def test_forward_in_16_bits_is_the_products():
     full = fx.grouped_mm(rows, experts.up, d.m_sizes)
     # one rounding to e4m3 of either operand: 5.1 %
     assert off(mb.product(d.x, d.x_scale, w.up, d.m_sizes), np64(full)) < 0.06
+
+
+def test_backward_in_a_graph():
+    """A captured backward pass with clipping, replayed with other gradients of out, gives what the
+    calls give."""
+    mb, w, experts, (x, res, dout, dres) = block(48, 256, 128, 8, 3)
+    _, _, kept = mb.forward(w, x, res, 2)
+
+    def step():
+        grads = mb.backward(w, kept, dout, dres, experts)
+        each = [grads[k] for k in ("norm", "router", "up", "down")]
+        return fx.clip_grad_norm(each, 0.1)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    g = torch.Generator(device="cuda")
+    for seed in range(3):
+        g.manual_seed(seed)
+        dout.copy_(torch.randn(dout.shape, generator=g, device="cuda"))
+        graph.replay()
+        want = step()
+        assert torch.equal(held.norm, want.norm)
+        assert all(torch.equal(a, b) for a, b in zip(held.grads, want.grads))
+    assert fx.device_status() == 0
+
+
+def test_host_threads():
+    """Four host threads, each with products and a clipping of its own on a stream of its own."""
+    import threading
+    cases, errors = [], []
+    for i in range(4):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(i)
+        m, n, k = 150 + 40 * i, 200 + i, 136 + 8 * i     # rows of odd and of aligned lengths
+        cases.append([torch.randn(s, generator=g, device="cuda").bfloat16()
+                      for s in ((m, k), (3, n, k), (m, n))] +
+                     [torch.tensor([m - 100, 0, 90], device="cuda"),
+                      torch.cuda.Stream(priority=-1)])
+
+    def calls(x, w, dy, sizes, stream):
+        out = fx.grouped_mm(x, w, sizes, stream=stream)
+        dx = fx.grouped_mm(dy, w, sizes, transposed=True, stream=stream)
+        dw = fx.grouped_mm_weight_grad(dy, x, sizes, stream=stream)
+        return out, dx, dw, *fx.clip_grad_norm([dw, out, dx], 1.0, stream=stream).grads
+
+    def worker(case, got):
+        try:
+            torch.cuda.set_device(0)
+            for _ in range(20):
+                got.append(calls(*case))
+            case[-1].synchronize()
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(repr(e))
+    want = [calls(*c) for c in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+    threads = [threading.Thread(target=worker, args=a) for a in zip(cases, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    assert not any(t.is_alive() for t in threads) and not errors, errors
+    for one, runs in zip(want, got):
+        assert len(runs) == 20
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(r, one))
+    assert fx.device_status() == 0
