@@ -16,9 +16,8 @@ int64_t ceil_to(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // More tiles than a call can have: every group's last one may be partly filled.
 template <class Cfg>
 int64_t tiles_bound(const MmParams& p) {
-  const int64_t ct = ceil_to(p.C, Cfg::kCtas * p.wide);
-  if (Cfg::kGrad) return p.G * ct * ceil_to(p.R, Cfg::kTileN);
-  return ct * (p.total / Cfg::kTileN + (p.G < p.total ? p.G : p.total));
+  if (Cfg::kGrad) return p.ct * static_cast<int64_t>(p.G) * ceil_to(p.R, Cfg::kTileN);
+  return p.ct * static_cast<int64_t>(p.total / Cfg::kTileN + (p.G < p.total ? p.G : p.total));
 }
 
 template <class Cfg>
@@ -123,6 +122,7 @@ mslkb_status run_as(MmParams& p, int sms, void* stream) {
   MmMaps maps;
   std::memset(&maps, 0, sizeof maps);
   p.wide = tile_columns<Cfg>(p, sms);
+  p.ct = static_cast<int32_t>(ceil_to(p.C, Cfg::kCtas * p.wide));
   const mslkb_status s = encode<Cfg>(p, &maps);
   return s != MSLKB_OK ? s : launch<Cfg>(p, maps, sms, stream);
 }

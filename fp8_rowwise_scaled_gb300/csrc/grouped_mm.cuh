@@ -53,7 +53,7 @@ struct MmParams {
   int32_t K;               // contraction length (kGrad: each expert's rows instead)
   int32_t bf16;            // 1: bf16 operands, 0: fp16
   int32_t out32;           // 1: fp32 output, 0: the operands' type
-  int32_t wide;            // output columns of a tile per CTA: 128, or less for kRows
+  int32_t wide, ct;        // output columns of a tile per CTA: 128, or less for kRows; such tiles
   int32_t p_pieces, q_pieces;  // an MN-major operand's 64-element pieces in one box (see encode)
   int32_t splits;          // parts of each contraction, whose sums go to slices of out (fp32)
   int64_t slice;           // elements from slice to slice
@@ -152,7 +152,7 @@ __device__ __forceinline__ int32_t mm_tile_c(const MmParams& p) {
 template <class Cfg>
 __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* first,
                                           const int32_t* tile_pre, int32_t t) {
-  const int32_t tile_c = mm_tile_c<Cfg>(p), ct = (p.C + tile_c - 1) / tile_c;
+  const int32_t ct = p.ct;
   MmTile o;
   o.part = 0;
   if (p.splits > 1) {
@@ -182,14 +182,17 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
   }
   // row tiles in bands of kBand, column by column of tiles
   const int32_t rt = (rows + Cfg::kTileN - 1) / Cfg::kTileN;
-  const int32_t band = rt <= Cfg::kBand ? 0 : local / (Cfg::kBand * ct);
-  const int32_t in = local - band * Cfg::kBand * ct;
-  const int32_t deep = min(Cfg::kBand, rt - band * Cfg::kBand);
-  const int32_t c = deep == 1 ? in : (deep == Cfg::kBand ? in / Cfg::kBand : in / deep);
-  const int32_t r = band * Cfg::kBand + (in - c * deep);
-  o.c0 = c * tile_c;
-  // (row tiles of one height, rounded up; the last may have fewer rows, or none)
-  const int32_t each = (rows + rt - 1) / rt;
+  int32_t c = local, r = 0, each = rows;
+  if (rt > 1) {
+    const int32_t band = rt <= Cfg::kBand ? 0 : local / (Cfg::kBand * ct);
+    const int32_t in = local - band * Cfg::kBand * ct;
+    const int32_t deep = min(Cfg::kBand, rt - band * Cfg::kBand);
+    c = deep == Cfg::kBand ? in / Cfg::kBand : in / deep;
+    r = band * Cfg::kBand + (in - c * deep);
+    // (row tiles of one height, rounded up; the last may have fewer rows, or none)
+    each = (rows + rt - 1) / rt;
+  }
+  o.c0 = c * mm_tile_c<Cfg>(p);
   const int32_t height = (each + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
   o.valid = max(0, min(height, rows - r * height));
   o.h = (o.valid + Cfg::kRowStep - 1) / Cfg::kRowStep * Cfg::kRowStep;
@@ -243,7 +246,7 @@ __device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, i
   __syncwarp();
   if (__any_sync(0xffffffffu, clamped) && lane == 0 && blockIdx.x == 0)
     atomicOr(p.status, kStatusClamped);
-  const int32_t ct = (p.C + mm_tile_c<Cfg>(p) - 1) / mm_tile_c<Cfg>(p);
+  const int32_t ct = p.ct;
   if constexpr (Cfg::kGrad) {
     if (lane == 0) tile_pre[G] = G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
   } else {
@@ -485,13 +488,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     ptx::tmem_relinquish_pair();
   }
   if (threadIdx.x == 0) ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  if (warp == Cfg::kEpiWarp0) mm_schedule<Cfg>(p, first, tile_pre, lane);
   ptx::tc_fence_before_sync();
   ptx::cluster_sync();  // the peer's barriers are set up too
   ptx::tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
-  const int32_t tiles = tile_pre[p.G] * p.splits, wide = mm_wide<Cfg>(p);
+  const int32_t wide = mm_wide<Cfg>(p);
+  // (all that comes before passes while the kernel before this one ends)
+  ptx::griddep_wait();
 
   // Tile i of this CTA (or pair), from the ring: by a whole warp, or by one lane of it.  False past
   // the last one, or if a wait gave up.
@@ -731,11 +734,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // others read the weights from memory instead of sharing them in L2 (32 experts of 480 rows,
       // 4096 x 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a
       // time, one by each lane (a search and up to four divisions), and handed on one by one.
-      int32_t i = 0;
+      mm_schedule<Cfg>(p, first, tile_pre, lane);
+      __syncwarp();
+      const int32_t tiles = tile_pre[p.G] * p.splits;
+      int32_t i = 0, turn = static_cast<int32_t>(static_cast<uint32_t>(worker + lane) %
+                                                 static_cast<uint32_t>(workers));
       bool ok = true;
       for (int64_t n0 = 0; ok; n0 += 32) {
-        const int64_t n = n0 + lane;
-        const int64_t t = n * workers + (Cfg::kGrad ? worker : (worker + n) % workers);
+        const int64_t t = (n0 + lane) * workers + (Cfg::kGrad ? worker : turn);
+        turn = static_cast<int32_t>(static_cast<uint32_t>(turn + 32) %
+                                    static_cast<uint32_t>(workers));
         MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
         if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
         const uint32_t past = __ballot_sync(0xffffffffu, c.g < 0);   // (the first of these says so)
