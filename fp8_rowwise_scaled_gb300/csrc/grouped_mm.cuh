@@ -151,13 +151,13 @@ __device__ __forceinline__ int32_t mm_tile_c(const MmParams& p) {
 
 template <class Cfg>
 __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* first,
-                                          const int32_t* tile_pre, int32_t t) {
+                                          const int32_t* tile_pre, int32_t tiles, int32_t t) {
   const int32_t ct = p.ct;
   MmTile o;
   o.part = 0;
   if (p.splits > 1) {
-    o.part = t / tile_pre[p.G];
-    t -= o.part * tile_pre[p.G];
+    o.part = t / tiles;
+    t -= o.part * tiles;
   }
   int32_t local, rows;
   if constexpr (Cfg::kGrad) {
@@ -207,68 +207,86 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
   return o;
 }
 
-// One warp: first[g] = rows before group g, clamped to [0, total] (G + 1 entries), and the tiles
-// before it.
-template <class Cfg>
-__device__ __forceinline__ void mm_schedule(const MmParams& p, int32_t* first, int32_t* tile_pre,
-                                            uint32_t lane) {
-  // (sums are clamped as they are made, so that 32 bits hold them: total is at most 2^30)
-  const int32_t G = p.G, per = (G + 31) / 32, total = p.total;
-  const int32_t g0 = min(G, static_cast<int32_t>(lane) * per), g1 = min(G, g0 + per);
-  auto before = [&](int32_t sum) {   // of this lane, clamped
-    int32_t v = sum;
+// v of the lanes up to this one, added up (at most `most`).
+__device__ __forceinline__ int32_t mm_lanes_up_to(int32_t v, int32_t most, uint32_t lane) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= static_cast<uint32_t>(d)) v = min(total, v + o);
-    }
-    v = __shfl_up_sync(0xffffffffu, v, 1);
-    return lane == 0 ? 0 : v;
-  };
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= static_cast<uint32_t>(d)) v = min(most, v + o);
+  }
+  return v;
+}
+
+// One warp: first[g] = rows before group g, clamped to [0, total] (G + 1 entries), and the tiles
+// before it.  Returns all tiles.  Up to 32 groups, one to a lane, stay in registers: the first
+// loads of a call wait for this (16 experts on GB300: 2050 cycles by the general way, 1200 so, of
+// which the counts take 600 to come).
+template <class Cfg>
+__device__ __forceinline__ int32_t mm_schedule(const MmParams& p, int32_t* first,
+                                               int32_t* tile_pre, uint32_t lane) {
+  // (sums are clamped as they are made, so that 32 bits hold them: total is at most 2^30)
+  const int32_t G = p.G, total = p.total, ct = p.ct;
   bool clamped = false;
-  int32_t sum = 0;
-  for (int32_t g = g0; g < g1; ++g) {
+  auto count = [&](int32_t g) {
     const int64_t m = p.m_sizes[g];
     clamped |= m < 0 || m > total;
-    const int32_t mc = static_cast<int32_t>(m < 0 ? 0 : (m > total ? total : m));
-    first[g] = mc;
-    clamped |= sum + mc > total;
-    sum = min(total, sum + mc);
+    return static_cast<int32_t>(m < 0 ? 0 : (m > total ? total : m));
+  };
+  auto tiles_of = [&](int32_t rows) { return (rows + Cfg::kTileN - 1) / Cfg::kTileN; };
+  int32_t tiles = 0;   // (row tiles first: there are at most total / kTileN + G of them)
+  if (G <= 32) {
+    const int32_t g = static_cast<int32_t>(lane);
+    const int32_t mc = g < G ? count(g) : 0;
+    const int32_t end = mm_lanes_up_to(mc, total, lane);
+    int32_t from = __shfl_up_sync(0xffffffffu, end, 1);
+    if (lane == 0) from = 0;
+    clamped |= from + mc > total;
+    if (g < G) first[g + 1] = end;
+    if (lane == 0) first[0] = 0;
+    if constexpr (!Cfg::kGrad) {
+      const int32_t up_to = mm_lanes_up_to(tiles_of(end - from), INT32_MAX, lane);
+      if (g < G) tile_pre[g + 1] = up_to * ct;
+      if (lane == 0) tile_pre[0] = 0;
+      tiles = __shfl_sync(0xffffffffu, up_to, 31) * ct;
+    }
+  } else {
+    const int32_t per = (G + 31) / 32;
+    const int32_t g0 = min(G, static_cast<int32_t>(lane) * per), g1 = min(G, g0 + per);
+    int32_t sum = 0;
+    for (int32_t g = g0; g < g1; ++g) {
+      const int32_t mc = count(g);
+      first[g] = mc;
+      clamped |= sum + mc > total;
+      sum = min(total, sum + mc);
+    }
+    int32_t run = __shfl_up_sync(0xffffffffu, mm_lanes_up_to(sum, total, lane), 1);
+    if (lane == 0) run = 0;
+    clamped |= run + sum > total;
+    for (int32_t g = g0; g < g1; ++g) {
+      const int32_t mc = first[g];
+      first[g] = run;
+      run = min(total, run + mc);
+    }
+    if (lane == 31) first[G] = run;
+    __syncwarp();
+    if constexpr (!Cfg::kGrad) {
+      int32_t mine = 0;
+      for (int32_t g = g0; g < g1; ++g) mine += tiles_of(first[g + 1] - first[g]);
+      const int32_t up_to = mm_lanes_up_to(mine, INT32_MAX, lane);
+      int32_t at = up_to - mine;
+      for (int32_t g = g0; g < g1; ++g) {
+        tile_pre[g] = at * ct;
+        at += tiles_of(first[g + 1] - first[g]);
+      }
+      if (lane == 31) tile_pre[G] = at * ct;
+      tiles = __shfl_sync(0xffffffffu, up_to, 31) * ct;
+    }
   }
-  int32_t run = before(sum);
-  clamped |= run + sum > total;
-  for (int32_t g = g0; g < g1; ++g) {
-    const int32_t mc = first[g];
-    first[g] = run;
-    run = min(total, run + mc);
-  }
-  if (lane == 31) first[G] = run;
-  __syncwarp();
+  if constexpr (Cfg::kGrad) tiles = G * ct * tiles_of(p.R);
   if (__any_sync(0xffffffffu, clamped) && lane == 0 && blockIdx.x == 0)
     atomicOr(p.status, kStatusClamped);
-  const int32_t ct = p.ct;
-  if constexpr (Cfg::kGrad) {
-    if (lane == 0) tile_pre[G] = G * ct * ((p.R + Cfg::kTileN - 1) / Cfg::kTileN);
-  } else {
-    // (row tiles first: there are at most total / kTileN + G of them)
-    auto tiles = [&](int32_t g) {
-      return (first[g + 1] - first[g] + Cfg::kTileN - 1) / Cfg::kTileN;
-    };
-    int32_t mine = 0;
-    for (int32_t g = g0; g < g1; ++g) mine += tiles(g);
-    int32_t at = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t o = __shfl_up_sync(0xffffffffu, at, d);
-      if (lane >= static_cast<uint32_t>(d)) at += o;
-    }
-    at -= mine;
-    for (int32_t g = g0; g < g1; ++g) {
-      tile_pre[g] = at * ct;
-      at += tiles(g);
-    }
-    if (lane == 31) tile_pre[G] = at * ct;
-  }
+  __syncwarp();
+  return tiles;
 }
 
 // kind::f16 MMA, fp32 accumulator: D (+)= P * Q^T.  Instruction descriptor: bits 4-5 D format
@@ -734,9 +752,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // others read the weights from memory instead of sharing them in L2 (32 experts of 480 rows,
       // 4096 x 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a
       // time, one by each lane (a search and up to four divisions), and handed on one by one.
-      mm_schedule<Cfg>(p, first, tile_pre, lane);
-      __syncwarp();
-      const int32_t tiles = tile_pre[p.G] * p.splits;
+      const int32_t part = mm_schedule<Cfg>(p, first, tile_pre, lane);   // of a split product
+      const int32_t tiles = part * p.splits;
       int32_t i = 0, turn = static_cast<int32_t>(static_cast<uint32_t>(worker + lane) %
                                                  static_cast<uint32_t>(workers));
       bool ok = true;
@@ -745,7 +762,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         turn = static_cast<int32_t>(static_cast<uint32_t>(turn + 32) %
                                     static_cast<uint32_t>(workers));
         MmTile c{-1, 0, 0, 0, 0, 0, 0, 0};
-        if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, static_cast<int32_t>(t));
+        if (t < tiles) c = mm_tile<Cfg>(p, first, tile_pre, part, static_cast<int32_t>(t));
         const uint32_t past = __ballot_sync(0xffffffffu, c.g < 0);   // (the first of these says so)
         const bool more = past == 0u;
         uint32_t left = more ? 0xffffffffu : (2u << (__ffs(past) - 1)) - 1u;
