@@ -89,9 +89,9 @@ mslkb_status encode(MmParams& p, MmMaps* maps) {
     }
   }
   if (s == MSLKB_OK && Cfg::kAddRing) {
-    const uint64_t bytes = p.out32 ? 4 : 2;
+    const uint64_t bytes = Cfg::kAdd;
     const uint64_t extent[3] = {C, R, G}, stride[2] = {bytes * C, bytes * C * R};
-    const uint32_t box[3] = {128, static_cast<uint32_t>(Cfg::kChunk), 1};
+    const uint32_t box[3] = {128, static_cast<uint32_t>(Cfg::kAddRows), 1};
     s = encode_map_plain(&maps->add, p.add, static_cast<int>(bytes), 3, extent, stride, box);
   }
   return s;
@@ -130,14 +130,18 @@ mslkb_status run_as(MmParams& p, int sms, void* stream) {
 template <Mm kMode>
 mslkb_status run(MmParams& p, int sms, void* stream) {
   if constexpr (kMode == Mm::kGrad) {
+    const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
+    const bool ring =
+        p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0;
     // fp32 sums of several kSumRows rows in registers, where experts may well have as many (32
     // experts of 4096 x 7168 on GB300, us in registers / onto the result: 1024 rows each 1404 /
-    // 2235; 256 each 789 / 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280)
-    if (p.out32 && p.total >= 192ll * p.G * p.splits)
-      return run_as<MmCfg<kMode, false, true>>(p, sms, stream);
-    const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
-    if (p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0)
-      return run_as<MmCfg<kMode, true>>(p, sms, stream);
+    // 2235; 256 each 789 / 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280; with
+    // something to add 384 each 1544 / 1284, 384 on average 1648 / 1691, 1024 each 1813 / 2609)
+    if (p.out32 && p.total >= (ring ? 384ll : 192ll) * p.G * p.splits)
+      return run_as<MmCfg<kMode, 0, true>>(p, sms, stream);
+    if (ring)
+      return p.out32 ? run_as<MmCfg<kMode, 4>>(p, sms, stream)
+                     : run_as<MmCfg<kMode, 2>>(p, sms, stream);
   }
   return run_as<MmCfg<kMode>>(p, sms, stream);
 }

@@ -66,7 +66,7 @@ struct MmMaps {
   CUtensorMap p, q, q64, add;
 };
 
-template <Mm kMode_, bool kAdd_ = false, bool kLong_ = false>
+template <Mm kMode_, int kAdd_ = 0, bool kLong_ = false>
 struct MmCfg {
   static constexpr Mm kMode = kMode_;
   static constexpr bool kGrad = kMode == Mm::kGrad;
@@ -75,7 +75,8 @@ struct MmCfg {
   static constexpr int kCtas = 2;
   static constexpr int kTileN = 256;               // output rows of a tile
   static constexpr int kBK = 64;                   // contraction per stage: 128-byte pieces
-  static constexpr int kStages = kAdd_ ? 4 : 6;
+  static constexpr int kAdd = kAdd_;               // bytes of an element that is added; 0: none
+  static constexpr int kStages = kAdd == 0 ? 6 : (kAdd == 4 ? 3 : 4);
   static constexpr int kQRows = kTileN / kCtas;    // of Q in one CTA
   static constexpr int kPBytes = 128 * kBK * 2;
   static constexpr int kQBytes = kQRows * kBK * 2;
@@ -83,10 +84,16 @@ struct MmCfg {
   static constexpr int kMmaWarp = 1;
   static constexpr int kEdgeWarp = 2;
   static constexpr int kTileWarp = 3;  // hands out the tiles
-  // kGrad with something to add: that comes by TMA too, chunk by chunk, through a ring of its own
-  // for each four of the epilogue's warps (32 experts of 75 rows, 4096 x 7168 on GB300: 1331 us
-  // fp32, 711 bf16; loaded by the epilogue's threads themselves, a chunk ahead, 1541 and 1031)
-  static constexpr bool kAddRing = kAdd_;
+  // kGrad with something to add: that comes by TMA too, in slots of 8 KB, through a ring of its own
+  // for each four of the epilogue's warps (32 experts of 75 rows, 4096 x 7168 on GB300: 1120 us
+  // fp32, 706 bf16; loaded by the epilogue's threads themselves, a chunk ahead, 1541 and 1031).
+  // Bound by what is on its way: fp32 with four stages and four slots each 1330, three and seven
+  // 1120, two and nine 1180; bf16, whose tiles take half as long, four and four 706, three and
+  // six 750.  (One warp loads for both rings, in the order of the tiles: one each 1122 and 737.)
+  static constexpr bool kAddRing = kAdd > 0;
+  static constexpr int kAddRows = kAdd == 4 ? 16 : 32;   // of 128, in a slot
+  static constexpr int kAddSlot = 8192;
+  static constexpr int kAddSlots = kAdd == 0 ? 0 : (kAdd == 4 ? 7 : 4);
   // The tensor core's sums lose what lies below their last bit, always downwards: some 1e-9 of the
   // result for every row summed (fp32 results of 4096 rows, normal values, were 4.4e-6 off).  So
   // fp32 gradients are summed there kSumRows rows at a time, and these sums added with rounding
@@ -96,7 +103,7 @@ struct MmCfg {
   static constexpr int kSumRows = 512;
   static constexpr int kRegsFew = 56, kRegsMany = 224;   // of warps 0-3, of the epilogue's
   static constexpr int kAddWarp = 4;
-  static constexpr int kAddBytes = kAddRing ? 32768 : 0;
+  static constexpr int kAddBytes = kAddSlots * kAddSlot;
   static constexpr int kEpiWarp0 = kAddRing ? 8 : 4;
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
@@ -113,13 +120,12 @@ struct MmCfg {
   static constexpr int kOffQ = kStages * kPBytes;
   static constexpr int kStagePart = 8192;  // the epilogue's rows: 32 x 128 in 16 bits
   static constexpr int kOffStage = kOffQ + kStages * kQBytes;
-  static constexpr int kOffAdd = kOffStage + (kLong ? 0 : 2 * kStagePart);
+  static constexpr int kOffAdd = kOffStage + (kLong || kAdd == 4 ? 0 : 2 * kStagePart);
   static constexpr int kOffBar = kOffAdd + 2 * kAddBytes;
   // the scheduler warp hands tiles to the other roles through a ring
   static constexpr int kRing = 4;
   static constexpr int kRingUsers = 2 + (kGrad ? 1 : 0) + (kAddRing ? 1 : 0) + kEpiWarps;
-  static constexpr int kAddSlots = 4;  // at most, of one ring
-  static constexpr int kNumBars = 4 * kStages + 6 + 2 * kRing + (kAddRing ? 4 * kAddSlots : 0);
+  static constexpr int kNumBars = 4 * kStages + 6 + 2 * kRing + 4 * kAddSlots;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem address, abort flag
   static constexpr int kOffRing = (kOffMisc + 8 + 15) / 16 * 16;
   static constexpr int kOffSched = kOffRing + kRing * 32;
@@ -456,8 +462,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     return add_bar(part, slot) + 8u * Cfg::kAddSlots;
   };
   const uint32_t s_add = ptx::smem_addr(smem + Cfg::kOffAdd);
-  const uint32_t add_chunk = p.out32 ? 16384u : 8192u;      // 32 rows of 128
-  const uint32_t add_slots = Cfg::kAddBytes / add_chunk;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffMisc + 4);
   int32_t* first = reinterpret_cast<int32_t*>(smem + Cfg::kOffSched);
@@ -725,23 +729,25 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     } else if (Cfg::kAddRing && warp == Cfg::kAddWarp) {
       // -------------------------------------------------------------- what is added
       if (lane == 0) {
-        uint32_t turn = 0, count0 = 0, count1 = 0;  // chunks of either ring
+        uint32_t turn = 0, next[2] = {0, 0}, phase[2] = {0, 0};   // of either ring
         bool ok = true;
         MmTile c;
         for (int32_t i = 0; ok && take(i, c, false); ++i) {
           // (the same turns as the epilogue's)
           const uint32_t part = (c.len > 0 ? turn++ : static_cast<uint32_t>(i)) & 1u;
-          for (int32_t j0 = 0; j0 < c.valid; j0 += Cfg::kChunk) {
-            const uint32_t n = part == 0 ? count0++ : count1++, slot = n % add_slots;
-            ok = wait_bar(addfree_bar(part, slot), ((n / add_slots) & 1u) ^ 1u, abort_flag,
-                          p.status,
+          uint32_t slot = part == 0 ? next[0] : next[1], parity = part == 0 ? phase[0] : phase[1];
+          for (int32_t j0 = 0; j0 < c.valid; j0 += Cfg::kAddRows) {
+            ok = wait_bar(addfree_bar(part, slot), parity ^ 1u, abort_flag, p.status,
                           p.timeout_ns);
             if (!ok) break;
-            ptx::mbar_arrive_expect_tx(add_bar(part, slot), add_chunk);
-            ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * add_chunk, &maps.add,
+            ptx::mbar_arrive_expect_tx(add_bar(part, slot), Cfg::kAddSlot);
+            ptx::tma_load_3d(s_add + part * Cfg::kAddBytes + slot * Cfg::kAddSlot, &maps.add,
                              add_bar(part, slot), c.c0 + static_cast<int32_t>(crank) * wide,
                              c.r0 + j0, c.g);
+            if (++slot == Cfg::kAddSlots) slot = 0, parity ^= 1u;
           }
+          if (part == 0) next[0] = slot, phase[0] = parity;
+          else next[1] = slot, phase[1] = parity;
         }
       }
       __syncwarp();
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
     const uint32_t stage = ptx::smem_addr(smem + Cfg::kOffStage) + part * Cfg::kStagePart;
     const uint32_t bar = 1u + part;  // of this part's four warps
-    uint32_t adds = 0;  // chunks of the ring taken
+    uint32_t slot = 0, parity = 0;   // of the ring
     // kWhole: 16-bit results by whole rows; kLoad: what is added is loaded here
     auto work = [&](auto* out0, auto whole, auto load) {
       using T = std::remove_pointer_t<decltype(out0)>;
@@ -916,26 +922,29 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               }
             }
             if constexpr (Cfg::kAddRing) {
-              const uint32_t slot = adds % add_slots;
-              bool got = wait_bar(add_bar(part, slot), (adds / add_slots) & 1u, abort_flag,
-                                  p.status, p.timeout_ns);
-              got = __all_sync(0xffffffffu, got) != 0;
-              if constexpr (kWhole) got = named_bar_and(bar, got);
-              if (!got) return;
-              ++adds;
-              const uint32_t from = s_add + part * Cfg::kAddBytes + slot * add_chunk +
-                                    (q * 32u + lane) * sizeof(T);
 #pragma unroll
-              for (int j = 0; j < kN; ++j) {
-                float a;
-                if constexpr (sizeof(T) == 4)
-                  a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
-                else
-                  a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
-                v[j] = __float_as_uint(a + __uint_as_float(v[j]));
+              for (int h = 0; h < kN; h += Cfg::kAddRows) {
+                if (h > 0 && n <= h) break;
+                bool got = wait_bar(add_bar(part, slot), parity, abort_flag, p.status,
+                                    p.timeout_ns);
+                got = __all_sync(0xffffffffu, got) != 0;
+                if constexpr (kWhole) got = named_bar_and(bar, got);
+                if (!got) return;
+                const uint32_t from = s_add + part * Cfg::kAddBytes + slot * Cfg::kAddSlot +
+                                      (q * 32u + lane) * Cfg::kAdd;
+#pragma unroll
+                for (int j = 0; j < Cfg::kAddRows; ++j) {
+                  float a;
+                  if constexpr (sizeof(T) == 4)
+                    a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
+                  else
+                    a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
+                  v[h + j] = __float_as_uint(a + __uint_as_float(v[h + j]));
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
+                if (++slot == Cfg::kAddSlots) slot = 0, parity ^= 1u;
               }
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
             }
             if constexpr (kWhole) {
               MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
@@ -975,9 +984,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (load && p.out32) work(out32, no, yes);
         else if (load) work(out16, no, yes);
       }
-      if (!load && p.out32) work(out32, no, no);
-      else if (!load && rows) work(out16, yes, no);
-      else if (!load) work(out16, no, no);
+      if constexpr (Cfg::kAdd != 2)
+        if (!load && p.out32) work(out32, no, no);
+      if constexpr (Cfg::kAdd != 4) {
+        if (!load && !p.out32 && rows) work(out16, yes, no);
+        else if (!load && !p.out32) work(out16, no, no);
+      }
     } else {
       if (p.splits > 1) work(static_cast<float*>(p.out), no, no);
       else if (rows) work(out16, yes, no);

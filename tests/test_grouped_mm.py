@@ -149,6 +149,21 @@ def test_weight_grad_many_rows(shape, counts, add):
                       f"expert {g}")
 
 
+def test_weight_grad_added_by_few_experts_rows():
+    """What is added where most experts have few rows and two have many, in place as well."""
+    counts = [2000, 0, 7, 1041] + [16] * 30
+    n, k = 512, 776
+    m = sum(counts)
+    dy, x = randn(1, m, n), randn(2, m, k)
+    for grad in (FP32, BF16):
+        before = randn(3, len(counts), n, k, dtype=grad)
+        dw = fx.grouped_mm_weight_grad(dy, x, sizes(counts), add=before)
+        check_grad(dw, dy, x, counts, before)
+        held = before.clone()
+        assert fx.grouped_mm_weight_grad(dy, x, sizes(counts), add=held, out=held) is held
+        assert torch.equal(held, dw)
+
+
 def test_weight_grad_error_does_not_grow():
     """Sums of 64 to 16384 rows of normal values, as 2-norms: half of the last place that the
     tensor core loses in each of 512 / 16 steps, downwards, is 32 * 2^-24 at the most."""
