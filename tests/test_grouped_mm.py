@@ -402,7 +402,7 @@ def test_gradients_against_differences():
     slope = (f(0.5) - f(-0.5))
     dx, dw = fx.grouped_mm(g, w, ms, transposed=True), fx.grouped_mm_weight_grad(g, x, ms)
     got = (np64(dx) * u).sum() + (np64(dw) * v).sum()
-    # dx is rounded to bf16 (2^-9 relative), dw is fp32
+    # dx is rounded to bf16 (2^-8 relative), dw is fp32
     tol = 2.0 ** -8 * np.abs(np64(dx) * u).sum() + 2.0 ** -16 * np.abs(np64(dw) * v).sum()
     assert abs(got - slope) <= tol
 
