@@ -204,6 +204,21 @@ def test_bits_do_not_change():
     assert all(torch.equal(fx.grad_norm(grads), first) for _ in range(10))
 
 
+def test_small_tensors_beside_large_ones():
+    """Many small tensors in one CTA's run, before, between and behind large ones."""
+    for types in ([BF16], [FP32], TYPES):
+        sizes = ([1 + 37 * i for i in range(120)] + [3_000_001] +
+                 [8192, 8191, 4097, 2048, 2049] * 8 + [5_000_000] + [7168] * 60)
+        grads = grads_of(sizes, types)
+        r = fx.clip_grad_norm(grads, 0.25)
+        check_norm(r.norm, grads)
+        check_clip(r.grads, grads, grads, 0.25)
+        held = [g.clone() for g in grads]
+        fx.clip_grad_norm(held, 0.25, out=(torch.zeros((), device="cuda"), held))
+        assert all(torch.equal(a, b) for a, b in zip(held, r.grads))
+        assert torch.equal(fx.grad_norm(grads), r.norm)
+
+
 def test_streams_and_graphs():
     """Two graphs of different lists, replayed with new values side by side."""
     runs = []
