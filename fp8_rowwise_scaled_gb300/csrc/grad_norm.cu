@@ -7,11 +7,11 @@
 // Bound by memory: everything is read once for the norm, and read again and written once for the
 // clipping.  The list is cut into chunks of kChunkBytes, and every CTA takes an equal run of them
 // across the tensors' borders (small tensors by its warps in turn), so that many small tensors and
-// a few large ones load the SMs alike;
-// where a tensor starts is looked up in the kernel's parameters (no copy of the list to the
-// device, so that a call can be captured).  Partial sums go to the workspace and are added in a
-// fixed order.  The clipping walks each CTA's run backwards: what the norm read last is still in
-// L2.  A short list is one launch of one cluster, which exchanges its sums through shared memory.
+// a few large ones load the SMs alike; where a tensor starts is looked up in the kernel's
+// parameters (no copy of the list to the device, so that a call can be captured).  Partial sums go
+// to the workspace and are added in a fixed order.  The clipping walks each CTA's run backwards:
+// what the norm read last is still in L2.  A short list is one launch of one cluster, which
+// exchanges its sums through shared memory.
 //
 // Sums.  A square overflows fp32 from 2^64 on and is lost below 2^-63, and a gradient that has run
 // away or died has such elements; so a vector of 16 bytes whose largest magnitude is outside
