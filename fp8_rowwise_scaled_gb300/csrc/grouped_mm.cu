@@ -133,15 +133,22 @@ mslkb_status run(MmParams& p, int sms, void* stream) {
     const int64_t row = static_cast<int64_t>(p.C) * (p.out32 ? 4 : 2);
     const bool ring =
         p.add != nullptr && p.splits == 1 && aligned_to(p.add, 16) && row % 16 == 0;
-    // fp32 sums of several kSumRows rows in registers, where experts may well have as many (32
-    // experts of 4096 x 7168 on GB300, us in registers / onto the result: 1024 rows each 1404 /
-    // 2235; 256 each 789 / 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280; with
-    // something to add 384 each 1544 / 1284, 384 on average 1648 / 1691, 1024 each 1813 / 2609)
-    if (p.out32 && p.total >= (ring ? 384ll : 192ll) * p.G * p.splits)
+    // Sums in registers (kLong) where experts may well have more rows than the tensor core sums.
+    // 32 experts of 4096 x 7168 on GB300, us in registers / in tensor memory: fp32, 256 rows each 803 /
+    // 692, but 256 on average and up to 2000, 4096 x 2048, 246 / 280; 384 each onto something 1544 /
+    // 1284.  16 bits, 700 rows each 1009 / 988, 1024 1152 / 1105, 1500 1798 / 2057; 1024 on average and up
+    // to 9000 1361 / 1466.  (What is added in 16 bits never: loaded by the epilogue's threads it
+    // takes 6600 us for 1024 rows each, 1298 through the ring.)
+    const int64_t rows_from = p.out32 ? (ring ? 384 : 192) : 768;
+    if ((p.out32 || p.add == nullptr) && p.total >= rows_from * p.G * p.splits)
       return run_as<MmCfg<kMode, 0, true>>(p, sms, stream);
     if (ring)
       return p.out32 ? run_as<MmCfg<kMode, 4>>(p, sms, stream)
                      : run_as<MmCfg<kMode, 2>>(p, sms, stream);
+  }
+  if constexpr (kMode != Mm::kGrad) {
+    if (ceil_to(ceil_to(p.K, 64), p.splits) * 64 > kSumLen16)
+      return run_as<MmCfg<kMode, 0, true>>(p, sms, stream);
   }
   return run_as<MmCfg<kMode>>(p, sms, stream);
 }

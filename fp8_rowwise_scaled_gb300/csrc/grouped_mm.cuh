@@ -21,6 +21,15 @@
 //   warp 3      works out the tiles and hands them to the other warps
 //   warp 4      loads what is added to a gradient (with three idle ones, only where there is some)
 //   the last 8  the epilogue: four and four in turns, or all of them where they keep sums.
+//
+// Sums.  The tensor core's fp32 sums lose what lies below their last bit, always towards zero: up
+// to 2^-23 of the sum for each step of 16 terms, some 1e-9 of it for every term (4096 terms of normal
+// values were 4.4e-6 off).  So it sums kSumLen16 or kSumLen32 terms at the most,
+// and these sums are added with rounding:
+//   * kLong, contractions that are longer everywhere, or for most experts: in registers, which eight
+//     warps have for a tile's 256 rows (and take from the others), while the tensor core goes on;
+//   * else, where some experts have more rows than that: in tensor memory, the sum so far in one of
+//     its buffers and the next sum in the other, for which the tensor core has to wait.
 #pragma once
 
 #include <cuda.h>
@@ -66,6 +75,12 @@ struct MmMaps {
   CUtensorMap p, q, q64, add;
 };
 
+// Terms that the tensor core sums at a time, for results in 16 bits and in fp32.  Each sum taken
+// out of tensor memory costs the tensor core some 100 cycles of the 8192 that 1024 terms take
+// (32 experts of 1024 rows, 4096 x 7168 bf16 on GB300: 1127 us with sums of 1024, 1160 of 512, 1106 in
+// one; where normal values add up, results are 1e-6 off, 5e-7 and 7e-6 before they are rounded).
+constexpr int kSumLen16 = 1024, kSumLen32 = 512;
+
 template <Mm kMode_, int kAdd_ = 0, bool kLong_ = false>
 struct MmCfg {
   static constexpr Mm kMode = kMode_;
@@ -94,13 +109,7 @@ struct MmCfg {
   static constexpr int kAddRows = kAdd == 4 ? 16 : 32;   // of 128, in a slot
   static constexpr int kAddSlot = 8192;
   static constexpr int kAddSlots = kAdd == 0 ? 0 : (kAdd == 4 ? 7 : 4);
-  // The tensor core's sums lose what lies below their last bit, always downwards: some 1e-9 of the
-  // result for every row summed (fp32 results of 4096 rows, normal values, were 4.4e-6 off).  So
-  // fp32 gradients are summed there kSumRows rows at a time, and these sums added with rounding
-  // (5e-7).  kLong: for many rows per expert, in registers, which eight warps have for a tile's
-  // 256 rows of sums (and take from the others); else in the result itself.
-  static constexpr bool kLong = kLong_;
-  static constexpr int kSumRows = 512;
+  static constexpr bool kLong = kLong_;   // the tensor core's sums are added in registers
   static constexpr int kRegsFew = 56, kRegsMany = 224;   // of warps 0-3, of the epilogue's
   static constexpr int kAddWarp = 4;
   static constexpr int kAddBytes = kAddSlots * kAddSlot;
@@ -120,7 +129,7 @@ struct MmCfg {
   static constexpr int kOffQ = kStages * kPBytes;
   static constexpr int kStagePart = 8192;  // the epilogue's rows: 32 x 128 in 16 bits
   static constexpr int kOffStage = kOffQ + kStages * kQBytes;
-  static constexpr int kOffAdd = kOffStage + (kLong || kAdd == 4 ? 0 : 2 * kStagePart);
+  static constexpr int kOffAdd = kOffStage + (kAdd == 4 ? 0 : 2 * kStagePart);
   static constexpr int kOffBar = kOffAdd + 2 * kAddBytes;
   // the scheduler warp hands tiles to the other roles through a ring
   static constexpr int kRing = 4;
@@ -133,7 +142,8 @@ struct MmCfg {
 
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzle atoms");
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-  static_assert(!kLong || (kGrad && !kAddRing && kThreads == 384 &&
+  static_assert(kSumLen16 % kBK == 0 && kSumLen32 % kBK == 0, "whole stages");
+  static_assert(!kLong || (!kAddRing && kThreads == 384 &&
                            128 * kRegsFew + 256 * kRegsMany <= 384 * 168), "registers");
   static_assert(!kAddRing || kGrad, "what is added");
 };
@@ -534,8 +544,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     return c.g >= 0;
   };
 
-  // rows (steps of the contraction) that the tensor core sums
-  const int32_t sum_rows = Cfg::kGrad && p.out32 ? Cfg::kSumRows : 1 << 30;
+  const int32_t sum_len = Cfg::kGrad && p.out32 ? kSumLen32 : kSumLen16;
   if (warp < static_cast<uint32_t>(Cfg::kEpiWarp0)) {
     if constexpr (Cfg::kLong) ptx::setmaxnreg_dec<Cfg::kRegsFew>();
     if (warp == 0) {
@@ -636,7 +645,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       if (crank == 0) {
         const bool issuer = ptx::elect_one();
         int stage = 0;
-        uint32_t phase = 0, used = 0, turn = 0;
+        // cur: the buffer of a tile's first sum; used: the parity of either one's uses, a bit each
+        uint32_t phase = 0, cur = 0, used = 0, turn = 0;
         bool ok = true;
         const uint32_t p_lo0 = mm_desc_lo<Cfg::kPMn, Cfg::kMnPiece>(s_p);
         const uint32_t q_lo0 = mm_desc_lo<Cfg::kQMn, Cfg::kMnPiece>(s_q);
@@ -646,15 +656,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (len == 0) continue;
           const uint32_t idesc = mm_idesc<Cfg>(p.bf16, __shfl_sync(0xffffffffu, c.h, 0));
           for (int32_t k = 0; k < len;) {
-            const uint32_t b = used & 1u;
+            const uint32_t b = Cfg::kLong || k == 0 ? cur : cur ^ 1u;
             ok = __all_sync(0xffffffffu,
-                            wait_bar<true>(tempty_bar(b), ((used >> 1) & 1u) ^ 1u, abort_flag,
+                            wait_bar<true>(tempty_bar(b), ((used >> b) & 1u) ^ 1u, abort_flag,
                                                  p.status, p.timeout_ns)) != 0;
             if (!ok) break;
-            ++used;
+            used ^= 1u << b;
             ptx::tc_fence_after_sync();
             const uint32_t d = tmem_base + b * Cfg::kTileN;
-            const int32_t from = k, end = len - k > sum_rows ? k + sum_rows : len;
+            const int32_t from = k, end = len - k > sum_len ? k + sum_len : len;
             for (; k < end; k += Cfg::kBK) {
               ok = __all_sync(0xffffffffu, wait_bar(full_bar(stage), phase, abort_flag, p.status,
                                                     p.timeout_ns)) != 0;
@@ -681,8 +691,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             }
             if (!ok) break;
             if (issuer) ptx::mma_commit_pair(tfull_bar(turn, b), 0x3);
+            if (Cfg::kLong) cur ^= 1u;
           }
-          if (!Cfg::kLong) turn ^= 1u;
+          if (!Cfg::kLong) turn ^= 1u, cur ^= 1u;
         }
       }
       __syncwarp();
@@ -793,66 +804,102 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
     }
   } else if constexpr (Cfg::kLong) {
-    // -------------------------------------------------------------- epilogue, many rows
+    // -------------------------------------------------------------- epilogue, long contractions
     // Eight warps for a tile: one for each quarter of the TMEM lanes and half of the output rows,
     // whose sums they keep.
     ptx::setmaxnreg_inc<Cfg::kRegsMany>();
     constexpr int kHalf = Cfg::kTileN / 2;
     const uint32_t q = warp & 3u, part = (warp - Cfg::kEpiWarp0) >> 2;
-    uint32_t used = 0;
-    MmTile c;
-    for (int32_t i = 0; take(i, c, true); ++i) {
-      const int32_t n = min(kHalf, c.valid - static_cast<int32_t>(part) * kHalf);
-      const int32_t col = c.c0 + static_cast<int32_t>(crank) * wide +
-                          static_cast<int32_t>(q * 32u + lane);
-      const bool in = col < p.C;
-      const int64_t at = (static_cast<int64_t>(c.g) * p.R + c.r0 + part * kHalf) * p.C + col +
-                         c.part * p.slice;
-      // what is added comes first: its loads pass while the first rows are summed
-      float sum[kHalf];
-      if (p.add != nullptr) {
-        const int32_t there = in ? n : 0;
-        mm_rows<kHalf>(static_cast<const float*>(p.add) + at, p.C,
-                       [&](int j, const float* a) { sum[j] = j < there ? *a : 0.f; });
-      } else {
+    const uint32_t stage = ptx::smem_addr(smem + Cfg::kOffStage) + part * Cfg::kStagePart;
+    const uint32_t bar = 1u + part;  // of this half's four warps
+    // kWhole: 16-bit results by whole rows
+    auto work = [&](auto* out0, auto whole) {
+      using T = std::remove_pointer_t<decltype(out0)>;
+      constexpr bool kWhole = decltype(whole)::value;
+      const bool bf16 = p.bf16 != 0;
+      uint32_t used = 0;
+      MmTile c;
+      for (int32_t i = 0;; ++i) {
+        bool ok = take(i, c, true);
+        const int32_t n = min(kHalf, c.valid - static_cast<int32_t>(part) * kHalf);
+        const int32_t col0 = c.c0 + static_cast<int32_t>(crank) * wide;
+        const int32_t cols = min(wide, p.C - col0);   // of this CTA
+        const int32_t col = col0 + static_cast<int32_t>(q * 32u + lane);
+        const bool in = col < col0 + cols;
+        const int64_t row0 = Cfg::kGrad ? static_cast<int64_t>(c.g) * p.R + c.r0 : c.r0;
+        const int64_t at = (row0 + part * kHalf) * p.C + c.part * p.slice;
+        float sum[kHalf];
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) sum[j] = 0.f;
-      }
-      bool ok = true;
-      for (int32_t k = 0; k < c.len; k += sum_rows) {
-        const uint32_t b = used & 1u;
-        ok = wait_bar(tfull_bar(0u, b), (used >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok) != 0;
-        if (!ok) break;
-        ++used;
-        ptx::tc_fence_after_sync();
+        if constexpr (Cfg::kGrad && sizeof(T) == 4) {
+          // what is added comes first: its loads pass while the first rows are summed
+          const int32_t there = in ? n : 0;
+          if (ok && p.add != nullptr)
+            mm_rows<kHalf>(static_cast<const T*>(p.add) + at + col, p.C,
+                           [&](int j, const T* a) { sum[j] = j < there ? *a : 0.f; });
+        }
+        for (int32_t k = 0; ok && k < c.len; k += sum_len) {
+          const uint32_t b = used & 1u;
+          ok = wait_bar(tfull_bar(0u, b), (used >> 1) & 1u, abort_flag, p.status, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          if (!ok) break;
+          ++used;
+          ptx::tc_fence_after_sync();
+          // 64 rows on their way at a time
+          const uint32_t from = tmem_base + b * Cfg::kTileN + part * kHalf + ((q * 32u) << 16);
 #pragma unroll
-        for (int j0 = 0; j0 < kHalf; j0 += 32) {
-          if (j0 < n) {
-            uint32_t v[32];
-            ptx::tmem_ld_x32(tmem_base + b * Cfg::kTileN + part * kHalf + j0 + ((q * 32u) << 16),
-                             v);
-            ptx::tmem_ld_wait();
+          for (int j0 = 0; j0 < kHalf; j0 += 64) {
+            if (j0 < n) {
+              uint32_t v[32], w[32];
+              ptx::tmem_ld_x32(from + j0, v);
+              ptx::tmem_ld_x32(from + j0 + 32, w);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[j0 + j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 32; ++j) {
+                sum[j0 + j] += __uint_as_float(v[j]);
+                sum[j0 + 32 + j] += __uint_as_float(w[j]);
+              }
+            }
+          }
+          ptx::tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (crank != 0)
+              ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
+            else
+              ptx::mbar_arrive(tempty_bar(b));
           }
         }
-        ptx::tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (crank != 0)
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
-          else
-            ptx::mbar_arrive(tempty_bar(b));
+        if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
+        if (!ok) break;
+        if constexpr (kWhole) {
+#pragma unroll
+          for (int j0 = 0; j0 < kHalf; j0 += 32) {
+            if (j0 < n) {
+              uint32_t v[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[j0 + j]);
+              MmRows<32>::store(out0 + at + static_cast<int64_t>(j0) * p.C + col0, p.C, n - j0, cols,
+                                q, v, bf16, stage, bar, lane);
+            }
+          }
+        } else {
+          auto put = [&](int j, T* to) {
+            if constexpr (sizeof(T) == 4) *to = sum[j];
+            else *to = mm_round16(sum[j], bf16);
+          };
+          if (in && n >= kHalf)
+            mm_rows<kHalf>(out0 + at + col, p.C, put);
+          else if (in)
+            mm_rows<kHalf>(out0 + at + col, p.C, [&](int j, T* to) { if (j < n) put(j, to); });
         }
       }
-      if (!ok) break;
-      float* out = static_cast<float*>(p.out) + at;
-      if (in && n >= kHalf)
-        mm_rows<kHalf>(out, p.C, [&](int j, float* to) { *to = sum[j]; });
-      else if (in)
-        mm_rows<kHalf>(out, p.C, [&](int j, float* to) { if (j < n) *to = sum[j]; });
-    }
+    };
+    uint16_t* out16 = static_cast<uint16_t*>(p.out);
+    if (p.out32) work(static_cast<float*>(p.out), std::false_type());
+    else if (p.C % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7) == 0)
+      work(out16, std::true_type());
+    else work(out16, std::false_type());
   } else {
     // -------------------------------------------------------------- epilogue
     // Four warps for a tile, one for each quarter of the TMEM lanes.  Eight warps take turns: while
@@ -870,7 +917,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       MmChunk<T, kN> chunk;
       const T* add0 = static_cast<const T*>(p.add);
       const bool bf16 = p.bf16 != 0;
-      uint32_t used = 0, turn = 0;
+      uint32_t cur = 0, turn = 0;
       uint32_t seen = 0;   // parity of the completions seen, a bit for each buffer
       MmTile c;
       for (int32_t i = 0;; ++i) {
@@ -886,90 +933,92 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if constexpr (kLoad) {
           if (ok && mine) chunk.load_add(add0 + at0 + col, p.C, c.valid, in);
         }
-        int32_t k = 0;
-        do {   // over the sums of sum_rows rows (16-bit results: of all)
-          const uint32_t b = used & 1u;
-          if (any && mine) {
-            ok = wait_bar(tfull_bar(part, b), (seen >> b) & 1u, abort_flag, p.status,
-                          p.timeout_ns);
-            ok = __all_sync(0xffffffffu, ok) != 0;
-            seen ^= 1u << b;
-            ptx::tc_fence_after_sync();
-          }
-          if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
-          if (!ok) break;
-          used += any ? 1u : 0u;
-          if (!mine) continue;
-          int64_t at = at0;
-          for (int32_t j0 = 0; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
-            uint32_t v[kN];
-            if (any) {
-              const uint32_t from = tmem_base + b * Cfg::kTileN + static_cast<uint32_t>(j0) +
-                                    ((q * 32u) << 16);
-              ptx::tmem_ld_x32(from, v);
-              ptx::tmem_ld_wait();
-            } else {
+        auto rows_of = [&](uint32_t buffer, int32_t j0) {
+          return tmem_base + buffer * Cfg::kTileN + static_cast<uint32_t>(j0) + ((q * 32u) << 16);
+        };
+        auto release = [&](uint32_t buffer) {
+          ptx::tc_fence_before_sync();
+          __syncwarp();
+          if (lane != 0) return;
+          if (crank != 0)
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(buffer), 0u));
+          else
+            ptx::mbar_arrive(tempty_bar(buffer));
+        };
+        // the tensor core's sums: the first stays where it is, others are added to it
+        for (int32_t k = 0; ok && any && mine && k < c.len; k += sum_len) {
+          const uint32_t b = k == 0 ? cur : cur ^ 1u;
+          ok = wait_bar(tfull_bar(part, b), (seen >> b) & 1u, abort_flag, p.status, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok) != 0;
+          seen ^= 1u << b;
+          ptx::tc_fence_after_sync();
+          if (!ok || k == 0) continue;
+#pragma unroll 1
+          for (int32_t j0 = 0; j0 < c.valid; j0 += 16) {
+            uint32_t sum[16], v[16];
+            ptx::tmem_ld_x16(rows_of(cur, j0), sum);
+            ptx::tmem_ld_x16(rows_of(b, j0), v);
+            ptx::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < kN; ++j) v[j] = 0u;
-            }
-            const int32_t n = c.valid - j0;
-            if constexpr (Cfg::kGrad && sizeof(T) == 4) {
-              if (k > 0) {   // onto the sums so far
-                MmChunk<float, kN> so_far;
-                so_far.load_add(out0 + at + col, p.C, n, in);
-                so_far.template store<true>(out0 + at + col, p.C, n, in, v, bf16);
-                continue;
-              }
-            }
-            if constexpr (Cfg::kAddRing) {
-#pragma unroll
-              for (int h = 0; h < kN; h += Cfg::kAddRows) {
-                if (h > 0 && n <= h) break;
-                bool got = wait_bar(add_bar(part, slot), parity, abort_flag, p.status,
-                                    p.timeout_ns);
-                got = __all_sync(0xffffffffu, got) != 0;
-                if constexpr (kWhole) got = named_bar_and(bar, got);
-                if (!got) return;
-                const uint32_t from = s_add + part * Cfg::kAddBytes + slot * Cfg::kAddSlot +
-                                      (q * 32u + lane) * Cfg::kAdd;
-#pragma unroll
-                for (int j = 0; j < Cfg::kAddRows; ++j) {
-                  float a;
-                  if constexpr (sizeof(T) == 4)
-                    a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
-                  else
-                    a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
-                  v[h + j] = __float_as_uint(a + __uint_as_float(v[h + j]));
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
-                if (++slot == Cfg::kAddSlots) slot = 0, parity ^= 1u;
-              }
-            }
-            if constexpr (kWhole) {
-              MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
-            } else {
-              auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
-              if constexpr (kLoad) {
-                if (n > kN)
-                  chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
-              }
-              now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16);
-            }
+            for (int j = 0; j < 16; ++j)
+              v[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(v[j]));
+            ptx::tmem_st_x16(rows_of(cur, j0), v);
           }
-          if (any) {
-            ptx::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if (crank != 0)
-                ptx::mbar_arrive_cluster(ptx::mapa_shared(tempty_bar(b), 0u));
-              else
-                ptx::mbar_arrive(tempty_bar(b));
-            }
-          }
-        } while (any && (k += sum_rows) < c.len);
+          ptx::tmem_st_wait();
+          release(b);
+        }
+        if constexpr (kWhole) ok = named_bar_and(bar, ok);  // (they meet at it: leave together)
         if (!ok) break;
-        turn += any ? 1u : 0u;
+        const uint32_t done = cur;
+        if (any) ++turn, cur ^= 1u;
+        if (!mine) continue;
+        int64_t at = at0;
+        for (int32_t j0 = 0; j0 < c.valid; j0 += kN, at += static_cast<int64_t>(kN) * p.C) {
+          uint32_t v[kN];
+          if (any) {
+            ptx::tmem_ld_x32(rows_of(done, j0), v);
+            ptx::tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) v[j] = 0u;
+          }
+          const int32_t n = c.valid - j0;
+          if constexpr (Cfg::kAddRing) {
+#pragma unroll
+            for (int h = 0; h < kN; h += Cfg::kAddRows) {
+              if (h > 0 && n <= h) break;
+              bool got = wait_bar(add_bar(part, slot), parity, abort_flag, p.status, p.timeout_ns);
+              got = __all_sync(0xffffffffu, got) != 0;
+              if constexpr (kWhole) got = named_bar_and(bar, got);
+              if (!got) return;
+              const uint32_t from = s_add + part * Cfg::kAddBytes + slot * Cfg::kAddSlot +
+                                    (q * 32u + lane) * Cfg::kAdd;
+#pragma unroll
+              for (int j = 0; j < Cfg::kAddRows; ++j) {
+                float a;
+                if constexpr (sizeof(T) == 4)
+                  a = __uint_as_float(ptx::ld_shared_u32(from + j * 512u));
+                else
+                  a = mm_widen(ptx::ld_shared_u16(from + j * 256u), bf16);
+                v[h + j] = __float_as_uint(a + __uint_as_float(v[h + j]));
+              }
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(addfree_bar(part, slot));
+              if (++slot == Cfg::kAddSlots) slot = 0, parity ^= 1u;
+            }
+          }
+          if constexpr (kWhole) {
+            MmRows<kN>::store(out0 + at + col0, p.C, n, cols, q, v, bf16, stage, bar, lane);
+          } else {
+            auto now = chunk;  // what is added to these rows; the next ones' is loaded meanwhile
+            if constexpr (kLoad) {
+              if (n > kN)
+                chunk.load_add(add0 + at + col + static_cast<int64_t>(kN) * p.C, p.C, n - kN, in);
+            }
+            now.template store<kLoad>(out0 + at + col, p.C, n, in, v, bf16);
+          }
+        }
+        if (any) release(done);
       }
     };
     const std::true_type yes{};
@@ -991,7 +1040,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         else if (!load && !p.out32) work(out16, no, no);
       }
     } else {
-      if (p.splits > 1) work(static_cast<float*>(p.out), no, no);
+      if (p.out32) work(static_cast<float*>(p.out), no, no);
       else if (rows) work(out16, yes, no);
       else work(out16, no, no);
     }

@@ -501,8 +501,8 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  * otherwise), for experts that are kept in 16 bits and for the backward pass.  The experts'
  * rows are packed as in the stacked layout: expert g owns m_sizes[g] rows after those of the
  * experts before it, clamped to [0, total_M] as there (MSLKB_DEV_MSIZES_CLAMPED).  Products are
- * exact, sums fp32: the tensor core's, which lose some 1e-9 of the result for each term, for
- * results in 16 bits; for fp32 gradients 512 rows of these at a time, added with rounding.
+ * exact, sums fp32: the tensor core's of at most 1024 terms (fp32 gradients: 512), which lose up to
+ * 2^-23 of the sum for each 16 terms, and these added with rounding.
  * G is limited to MSLKB_MAX_GROUPS, every other size to 2^30.  Any size and alignment is
  * accepted; an operand whose rows do not start on 16 bytes, or are not spaced by multiples of 16
  * (its address, ldx, lddy or the matrices' row length), is first copied to rows that do, and a
