@@ -223,12 +223,17 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const int32_t* firs
   return o;
 }
 
+// Rows a and b together, at most `most`: a, b <= most, whose sum 32 bits need not hold.
+__device__ __forceinline__ int32_t mm_add_rows(int32_t a, int32_t b, int32_t most) {
+  return a + min(b, most - a);
+}
+
 // v of the lanes up to this one, added up (at most `most`).
 __device__ __forceinline__ int32_t mm_lanes_up_to(int32_t v, int32_t most, uint32_t lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= static_cast<uint32_t>(d)) v = min(most, v + o);
+    if (lane >= static_cast<uint32_t>(d)) v = mm_add_rows(v, o, most);
   }
   return v;
 }
@@ -240,7 +245,6 @@ __device__ __forceinline__ int32_t mm_lanes_up_to(int32_t v, int32_t most, uint3
 template <class Cfg>
 __device__ __forceinline__ int32_t mm_schedule(const MmParams& p, int32_t* first,
                                                int32_t* tile_pre, uint32_t lane) {
-  // (sums are clamped as they are made, so that 32 bits hold them: total is at most 2^30)
   const int32_t G = p.G, total = p.total, ct = p.ct;
   bool clamped = false;
   auto count = [&](int32_t g) {
@@ -256,7 +260,7 @@ __device__ __forceinline__ int32_t mm_schedule(const MmParams& p, int32_t* first
     const int32_t end = mm_lanes_up_to(mc, total, lane);
     int32_t from = __shfl_up_sync(0xffffffffu, end, 1);
     if (lane == 0) from = 0;
-    clamped |= from + mc > total;
+    clamped |= mc > total - from;
     if (g < G) first[g + 1] = end;
     if (lane == 0) first[0] = 0;
     if constexpr (!Cfg::kGrad) {
@@ -272,16 +276,16 @@ __device__ __forceinline__ int32_t mm_schedule(const MmParams& p, int32_t* first
     for (int32_t g = g0; g < g1; ++g) {
       const int32_t mc = count(g);
       first[g] = mc;
-      clamped |= sum + mc > total;
-      sum = min(total, sum + mc);
+      clamped |= mc > total - sum;
+      sum = mm_add_rows(sum, mc, total);
     }
     int32_t run = __shfl_up_sync(0xffffffffu, mm_lanes_up_to(sum, total, lane), 1);
     if (lane == 0) run = 0;
-    clamped |= run + sum > total;
+    clamped |= sum > total - run;
     for (int32_t g = g0; g < g1; ++g) {
       const int32_t mc = first[g];
       first[g] = run;
-      run = min(total, run + mc);
+      run = mm_add_rows(run, mc, total);
     }
     if (lane == 31) first[G] = run;
     __syncwarp();
@@ -1213,15 +1217,15 @@ __global__ void __launch_bounds__(kSumThreads)
     int32_t rows = 0;
     for (int g = static_cast<int>(threadIdx.x); g < p.G; g += kSumThreads) {
       const int64_t m = p.m_sizes[g];
-      rows = min(p.total, rows + static_cast<int32_t>(m < 0 ? 0 : (m > p.total ? p.total : m)));
+      rows = mm_add_rows(rows, static_cast<int32_t>(m < 0 ? 0 : (m > p.total ? p.total : m)), p.total);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
-      rows = min(p.total, rows + __shfl_xor_sync(0xffffffffu, rows, d));
+      rows = mm_add_rows(rows, __shfl_xor_sync(0xffffffffu, rows, d), p.total);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = rows;
     __syncthreads();
     rows = 0;
-    for (int w = 0; w < kSumThreads / 32; ++w) rows = min(p.total, rows + warps[w]);
+    for (int w = 0; w < kSumThreads / 32; ++w) rows = mm_add_rows(rows, warps[w], p.total);
     n = static_cast<int64_t>(rows) * p.C;
   }
   if (p.out32) sum_slices<float>(p, n);
