@@ -153,9 +153,16 @@ mslkb_status run(MmParams& p, int sms, void* stream) {
   return run_as<MmCfg<kMode>>(p, sms, stream);
 }
 
+// Each size, and the elements of each operand and result: what passes kMaxElements (2 TB in 16 bits)
+// fits no device, and numbers of bytes, with all copies and slices, stay within 64 bits.
+constexpr double kMaxElements = static_cast<double>(1ll << 40);
 bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
-  return total >= 0 && G >= 0 && N >= 0 && K >= 0 && total <= kMaxSize && N <= kMaxSize &&
-         K <= kMaxSize && G <= kMaxGroups;
+  if (!(total >= 0 && G >= 0 && N >= 0 && K >= 0 && total <= kMaxSize && N <= kMaxSize &&
+        K <= kMaxSize && G <= kMaxGroups))
+    return false;
+  const double t = static_cast<double>(total), g = static_cast<double>(G);
+  const double n = static_cast<double>(N), k = static_cast<double>(K);
+  return t * n <= kMaxElements && t * k <= kMaxElements && g * n * k <= kMaxElements;
 }
 
 // Parts of each contraction.  Few tiles leave most pairs without one, and a pair takes some 0.2 us

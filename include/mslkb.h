@@ -503,7 +503,8 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  * experts before it, clamped to [0, total_M] as there (MSLKB_DEV_MSIZES_CLAMPED).  Products are
  * exact, sums fp32: the tensor core's of at most 1024 terms (fp32 gradients: 512), which lose up to
  * 2^-23 of the sum for each 16 terms, and these added with rounding.
- * G is limited to MSLKB_MAX_GROUPS, every other size to 2^30.  Any size and alignment is
+ * G is limited to MSLKB_MAX_GROUPS, every other size to 2^30, and total_M * N, total_M * K and
+ * G * N * K to 2^40 (MSLKB_ERR_SHAPE; a workspace of 0 bytes).  Any size and alignment is
  * accepted; an operand whose rows do not start on 16 bytes, or are not spaced by multiples of 16
  * (its address, ldx, lddy or the matrices' row length), is first copied to rows that do, and a
  * contraction with few output tiles is split into parts whose sums are added in a fixed order.

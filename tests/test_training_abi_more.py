@@ -1,0 +1,49 @@
+"""C entry points for training the experts, without a GPU: calls at the ends of what the sizes may
+be."""
+import pytest
+
+import fp8_rowwise_scaled_gb300 as fx
+from fp8_rowwise_scaled_gb300 import build as fxbuild
+from test_moe_abi import P, refused
+from test_training_abi import mm, weight_grad
+
+MOST = 1 << 30
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fxbuild.build()
+    fx.lib()
+
+
+@pytest.mark.parametrize("total,G,N,K", [
+    (8, 1024, MOST, MOST), (8, 1, MOST, MOST), (MOST, 1, 2048, 8), (MOST, 1, 8, 2048),
+    (8, 1024, 1 << 16, (1 << 14) + 1), (MOST, 1024, MOST, MOST)])
+def test_sizes_whose_products_are_too_large(total, G, N, K):
+    """Refused whatever the workspace, and before it is reckoned with: 64 bits would not hold the
+    bytes of 1024 x 2^30 x 2^30 elements (nor of their rows of one less, copied)."""
+    for workspace, nbytes in ((None, 0), (P, 1 << 62)):
+        for less in (0, 1):
+            kw = dict(total_M=total, G=G, N=N, K=K - less, workspace=workspace, bytes=nbytes)
+            # (one less keeps three of the products above the limit)
+            if total * N <= 1 << 40 and total * (K - less) <= 1 << 40 and \
+                    G * N * (K - less) <= 1 << 40:
+                continue
+            refused(mm, fx.MSLKB_ERR_SHAPE, {**kw, "ldx": K, "transposed": 0},
+                    {**kw, "ldx": K, "transposed": 1})
+            refused(weight_grad, fx.MSLKB_ERR_SHAPE, {**kw, "ldx": K, "lddy": N})
+            for t in (0, 1):
+                assert fx.mslkb_grouped_mm_workspace_bytes(P, P, total, G, N, K - less, K, t) == 0
+            assert fx.mslkb_grouped_mm_weight_grad_workspace_bytes(
+                P, P, total, G, N, K - less, N, K) == 0
+
+
+def test_workspace_of_the_largest_sizes():
+    """Bytes of copies and slices at the limit: positive, and enough."""
+    f = fx.mslkb_grouped_mm_workspace_bytes
+    rows = 1 << 29
+    assert f(P + 2, P + 2, rows, 1, 8, 2048, 2048, 0) >= 2 * rows * 2048
+    assert f(P, P, rows, 1, 8, 2047, 2047, 0) >= 2 * rows * 2048
+    assert f(P + 2, P, 1, 1024, 1 << 15, 1 << 15, 1 << 15, 1) >= 2 * 1 << 15
+    f = fx.mslkb_grouped_mm_weight_grad_workspace_bytes
+    assert f(P + 2, P + 2, MOST, 1, 512, 1024, 512, 1024) >= 2 * MOST * (512 + 1024)
