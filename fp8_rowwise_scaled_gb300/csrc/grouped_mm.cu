@@ -170,10 +170,16 @@ bool sizes_ok(int64_t total, int64_t G, int64_t N, int64_t K) {
 // contractions of up to two rounds of tiles are split, into the number of parts that takes least by
 // this reckoning: rounds of the pairs x (stages of a part, and a tile's ends), or the time that the
 // operands take to read; and for the slices' sum a launch and their bytes.
+// Warps that work once per tile wait for as long as a contraction takes, so that none may come near
+// the time after which a wait gives up (1 s): a part has at most kMostTerms of the `longest` there
+// can be, 0.2 s if every stage comes from memory and all pairs read at once (64 KB each, 0.8 us).
 constexpr int kPairs = 76, kMostSplits = 16, kLeastStages = 4;
-int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements, int64_t operands) {
+constexpr int64_t kMostTerms = 1 << 24;
+int32_t splits_of(int64_t tiles, int64_t contraction, int64_t longest, int64_t elements,
+                  int64_t operands) {
   const int64_t stages = ceil_to(contraction, 64);
-  if (tiles > 2 * kPairs) return 1;
+  const int32_t needed = static_cast<int32_t>(ceil_to(longest, kMostTerms));
+  if (tiles > 2 * kPairs) return needed;
   const double read = static_cast<double>(operands) * 2.0 / 6.5e6;
   int32_t best = 1;
   double least = 0.0;
@@ -184,7 +190,7 @@ int32_t splits_of(int64_t tiles, int64_t contraction, int64_t elements, int64_t 
     if (s > 1) us += 2.5 + static_cast<double>(elements) * 4.0 * 2.0 * s / 6e6;
     if (s == 1 || us < least) least = us, best = s;
   }
-  return best;
+  return best > needed ? best : needed;
 }
 
 int64_t slice_of(int64_t elements) { return ceil_to(elements, 4) * 4; }
@@ -192,15 +198,16 @@ int64_t slice_of(int64_t elements) { return ceil_to(elements, 4) * 4; }
 int32_t mm_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
   if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
   const int64_t experts = G < total_M ? G : total_M;   // with rows, at most
-  return splits_of((total_M / 256 + experts) * ceil_to(N, 256), K, total_M * N,
+  return splits_of((total_M / 256 + experts) * ceil_to(N, 256), K, K, total_M * N,
                    experts * N * K + total_M * K);
 }
 
 int32_t grad_splits(int64_t total_M, int64_t G, int64_t N, int64_t K) {
   if (total_M == 0 || G == 0 || N == 0 || K == 0) return 1;
-  // (experts have different numbers of rows: twice as many as they have on average)
-  return splits_of(G * ceil_to(N, 256) * ceil_to(K, 256), ceil_to(2 * total_M, G + 1), G * N * K,
-                   total_M * (N + K));
+  // (experts have different numbers of rows: twice as many as they have on average, and one at
+  // most all)
+  return splits_of(G * ceil_to(N, 256) * ceil_to(K, 256), ceil_to(2 * total_M, G + 1), total_M,
+                   G * N * K, total_M * (N + K));
 }
 
 // The slices' place in the workspace, behind the operands' copies.

@@ -56,3 +56,39 @@ def test_counts_past_the_largest_number_of_rows(counts, owner):
               f"row {r}")
     out[rows] = 0
     assert not any(out[i:i + (1 << 26)].any() for i in range(0, MOST, 1 << 26))
+
+
+@pytest.mark.parametrize("grad", [FP32, BF16])
+def test_one_expert_with_all_rows(grad):
+    """More tiles than CTA pairs, and one of them with 2^30 rows: in parts, of which none takes as long
+    as a wait of the kernel may.  Sums of ones: exact."""
+    x = torch.ones((MOST, 1), dtype=BF16, device="cuda")
+    dy = torch.ones_like(x)
+    counts = [0] * 1024
+    counts[3], counts[700] = 40, MOST - 40
+    dw = fx.grouped_mm_weight_grad(dy, x, sizes(counts), dtype=grad)
+    assert fx.device_status() == 0
+    want = torch.tensor(counts, dtype=torch.float64).to(grad)
+    assert torch.equal(dw.flatten().cpu(), want)
+
+
+def test_long_rows():
+    """A contraction of 2^25, turned and not, in parts; sums of ones."""
+    k, n, g = 1 << 25, 8, 160
+    x = torch.ones((g, k), dtype=BF16, device="cuda")
+    w = torch.zeros((g, n, k), dtype=BF16, device="cuda")
+    w[:, 3] = 1.0
+    w[7, 5, -1] = 2.0
+    ms = sizes([1] * g)
+    want = torch.zeros((g, n))
+    want[:, 3] = k
+    want[7, 5] = 2.0
+    out = fx.grouped_mm(x, w, ms)
+    assert fx.device_status() == 0
+    assert torch.equal(out.cpu(), want.to(BF16))
+    w = w.view(g, k, n).zero_()
+    w[:, :, 3] = 1.0
+    w[7, -1, 5] = 2.0
+    out = fx.grouped_mm(x, w, ms, transposed=True)
+    assert fx.device_status() == 0
+    assert torch.equal(out.cpu(), want.to(BF16))

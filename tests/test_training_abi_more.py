@@ -47,3 +47,17 @@ def test_workspace_of_the_largest_sizes():
     assert f(P + 2, P, 1, 1024, 1 << 15, 1 << 15, 1 << 15, 1) >= 2 * 1 << 15
     f = fx.mslkb_grouped_mm_weight_grad_workspace_bytes
     assert f(P + 2, P + 2, MOST, 1, 512, 1024, 512, 1024) >= 2 * MOST * (512 + 1024)
+
+
+def test_no_contraction_outlasts_a_wait():
+    """Parts of at most 2^24 terms, whatever the number of tiles: a wait lasts as long as a part."""
+    f = fx.mslkb_grouped_mm_weight_grad_workspace_bytes
+    copies = 2 * MOST * 8 * 2                      # rows of one element, copied to 16 bytes
+    assert f(P, P, MOST, 1024, 1, 1, 1, 1) == copies + 64 * 1024 * 4
+    assert f(P, P, 1 << 25, 1024, 8, 8, 8, 8) == 2 * 1024 * 64 * 4
+    assert f(P, P, (1 << 24) + 1, 1024, 8, 8, 8, 8) == 2 * 1024 * 64 * 4
+    assert f(P, P, 1 << 24, 1024, 8, 8, 8, 8) == 0
+    f = fx.mslkb_grouped_mm_workspace_bytes
+    assert f(P, P, 200, 200, 8, 1 << 26, 1 << 26, 0) == 4 * 200 * 8 * 4
+    assert f(P, P, 200, 200, 8, 1 << 24, 1 << 24, 0) == 0
+    assert f(P, P, 1, 1, 8, MOST, MOST, 0) == 64 * 8 * 4
