@@ -2,7 +2,7 @@
 // it does not exceed a bound.
 //
 //   norm = (sum_i sum_j g_ij^2)^(1/2)  or  max |g_ij|
-//   out_ij = g_ij * min(1, max_norm / (norm + eps))
+//   out_ij = g_ij * (norm + eps <= max_norm ? 1 : max_norm / (norm + eps))
 //
 // Bound by memory: everything is read once for the norm, and read again and written once for the
 // clipping.  The list is cut into chunks of kChunkBytes, and every CTA takes an equal run of them
@@ -386,9 +386,11 @@ __device__ __forceinline__ float norm_of(const double* parts, int count, Togethe
   return t.norm;
 }
 
+// The scale: the quotient is only taken where it is below 1, so that neither an infinite bound over an
+// infinite norm nor 0 / 0 comes into it.  (A NaN stays.)
 __device__ __forceinline__ float scale_of(float norm, float max_norm, float eps) {
-  const float f = max_norm / (norm + eps);
-  return f > 1.f ? 1.f : f;   // (a NaN stays)
+  const float n = norm + eps;
+  return n <= max_norm ? 1.f : max_norm / n;
 }
 
 struct ClipArgs {

@@ -172,8 +172,9 @@ def grad_norm(grads, *, norm_type=2.0, out=None, stream=None):
 
 
 def clip_grad_norm(grads, max_norm, *, norm_type=2.0, eps=1e-6, out=None, stream=None):
-    """grads * min(1, max_norm / (norm + eps)), norm that of grad_norm -> ClippedGrads(norm,
-    grads).
+    """grads * scale -> ClippedGrads(norm, grads): norm is that of grad_norm, scale is 1 where norm +
+    eps <= max_norm (always, unless norm is NaN, if max_norm is infinite), else max_norm / (norm +
+    eps).
 
     ``out`` is (norm, tensors of the gradients' types, shapes and strides); the tensors may be the
     gradients themselves, which are then scaled in place (and not written where nothing

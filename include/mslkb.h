@@ -579,11 +579,15 @@ MSLKB_API mslkb_status mslkb_grad_norm(const void *const *grads, const int64_t *
 /*
  * The gradients scaled so that their norm does not exceed max_norm:
  *
- *   outs[i] = grads[i] * scale,    scale = min(1, max_norm / (norm + eps))   (NaN if norm is)
+ *   outs[i] = grads[i] * scale,    scale = 1 where norm + eps <= max_norm, else
+ *                                          max_norm / (norm + eps)
  *
- * each product rounded once to its tensor's type; norm is that of grads, as above.  outs[i] may
+ * each product rounded once to its tensor's type; norm is that of grads, as above, in fp32.  The
+ * scale is NaN exactly if norm is; an infinite max_norm leaves gradients as they are even if norm
+ * is infinite; a finite one scales them by 0 then (an infinite element becomes NaN).  outs[i] may
  * be grads[i] itself (left as it is where scale is 1); otherwise results must not lie over each
- * other or over gradients (MSLKB_ERR_SHAPE).  max_norm >= 0 (it may be infinite), eps >= 0.
+ * other or over gradients (MSLKB_ERR_SHAPE).  max_norm >= 0 (it may be infinite, and is if fp32
+ * does not hold it), eps >= 0.
  */
 MSLKB_API mslkb_status mslkb_clip_grad_norm(const void *const *grads, void *const *outs,
                                             const int64_t *sizes, const int32_t *dtypes,
