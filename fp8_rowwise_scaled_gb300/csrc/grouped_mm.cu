@@ -257,6 +257,18 @@ struct Operand {
   }
 };
 
+// Whether `bytes` at `to` lie over an element of `rows` rows of `cols` 16-bit elements, ld apart.
+bool lies_over(const void* to, int64_t bytes, const void* from, int64_t rows, int64_t cols,
+               int64_t ld) {
+  if (bytes == 0 || rows == 0 || cols == 0) return false;
+  const int64_t a = static_cast<int64_t>(reinterpret_cast<uintptr_t>(from));
+  const int64_t b = static_cast<int64_t>(reinterpret_cast<uintptr_t>(to));
+  if (b + bytes <= a) return false;
+  // the last row that starts before the end of `to`
+  const int64_t last = (b + bytes - 1 - a) / (2 * ld);
+  return a + 2 * ((last < rows ? last : rows - 1) * ld + cols) > b;
+}
+
 // The operands as they are, or copied to aligned rows in the workspace.
 mslkb_status align_operands(Operand (&o)[2], const int64_t* m_sizes, void* workspace, int sms,
                             void* stream) {
@@ -333,6 +345,9 @@ mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_siz
   mslkb_status s = workspace_status(copies + slices_bytes(splits, total_M * N), workspace,
                                     workspace_bytes);
   if (s != MSLKB_OK) return s;
+  for (const Operand& p : o)   // (what is written must not have been an input of other tiles)
+    if (lies_over(out, 2 * total_M * N, p.at, p.rows, p.cols, p.ld)) return MSLKB_ERR_SHAPE;
+  if (lies_over(out, 2 * total_M * N, m_sizes, 1, 4 * G, 4 * G)) return MSLKB_ERR_SHAPE;
   DeviceHandles h;
   if ((s = device_handles(&h)) != MSLKB_OK) return s;
   const TraceRange range("grouped_mm", total_M);
@@ -398,6 +413,10 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
   mslkb_status s = workspace_status(copies + slices_bytes(splits, G * N * K), workspace,
                                     workspace_bytes);
   if (s != MSLKB_OK) return s;
+  const int64_t dw_bytes = G * N * K * static_cast<int64_t>(wide);
+  for (const Operand& p : o)
+    if (lies_over(dw, dw_bytes, p.at, p.rows, p.cols, p.ld)) return MSLKB_ERR_SHAPE;
+  if (lies_over(dw, dw_bytes, m_sizes, 1, 4 * G, 4 * G)) return MSLKB_ERR_SHAPE;
   DeviceHandles h;
   if ((s = device_handles(&h)) != MSLKB_OK) return s;
   const TraceRange range("grouped_mm_weight_grad", total_M);

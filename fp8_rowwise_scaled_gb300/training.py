@@ -106,7 +106,8 @@ def grouped_mm(x, w, m_sizes, *, transposed=False, out=None, stream=None):
     x [total_M, K] bf16 / fp16 (rows may be strided), packed by expert as moe_dispatch does, w
     [G, N, K] of x's type, or [G, K, N] with ``transposed`` (the forward product's weights as they
     are: the gradient of its input), m_sizes [G] int64 -> out [total_M, N] of x's type.  Rows past
-    sum(m_sizes) are not written: a freshly allocated ``out`` is zeroed first."""
+    sum(m_sizes) are not written: a freshly allocated ``out`` is zeroed first.  ``out`` must not lie
+    over x, w or m_sizes."""
     b = _binding()
     if out is None:
         M, shape = _moe._shape(x, "x")[0], _stack_shape(w, "w")
@@ -123,7 +124,8 @@ def grouped_mm_weight_grad(dy, x, m_sizes, *, add=None, dtype=None, out=None, st
     dy [total_M, N], x [total_M, K] bf16 / fp16 (rows may be strided), m_sizes [G] int64 -> dw
     [G, N, K] in ``dtype`` (fp32, the default, or dy's; that of ``add`` where it is given).  ``add``
     is what was accumulated before and may be ``out`` itself (but must not overlap it otherwise).
-    Rows past sum(m_sizes) are not used; an expert without rows gets ``add``, or zeros."""
+    Rows past sum(m_sizes) are not used; an expert without rows gets ``add``, or zeros.  ``out`` must
+    not lie over dy, x or m_sizes."""
     b = _binding()
     if out is None:
         torch = _moe._torch

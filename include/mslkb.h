@@ -519,7 +519,8 @@ MSLKB_API mslkb_status mslkb_swiglu_quant_backward(const void *dy, const void *s
  * weights as they lie and gives its input's gradient (x is then the gradient of out).
  *
  *   x    device, dtype [total_M, K], rows ldx elements apart
- *   out  device, dtype [total_M, N]; rows past the last expert's are not written
+ *   out  device, dtype [total_M, N]; rows past the last expert's are not written.  Must not lie
+ *        over elements of x or w, or over m_sizes (MSLKB_ERR_SHAPE)
  *
  * K = 0 writes +0.0 to every owned row.
  */
@@ -541,7 +542,8 @@ MSLKB_API mslkb_status mslkb_grouped_mm(const void *x, const void *w, const int6
  *   add  device, [G, N, K] of dw's type: what was accumulated before; NULL: nothing.  May be dw
  *        itself, but must not overlap it otherwise (MSLKB_ERR_SHAPE)
  *   dw   device, [G, N, K], fp32 if dw_fp32 is not 0, else dtype; every element is written (an
- *        expert without rows gets add, or +0.0)
+ *        expert without rows gets add, or +0.0).  Must not lie over elements of dy or x, or over
+ *        m_sizes (MSLKB_ERR_SHAPE)
  */
 MSLKB_API int64_t mslkb_grouped_mm_weight_grad_workspace_bytes(const void *dy, const void *x,
                                                                int64_t total_M, int64_t G,

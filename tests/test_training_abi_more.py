@@ -1,6 +1,7 @@
 """C entry points for training the experts, without a GPU: calls at the ends of what the sizes may
 be."""
 import pytest
+import torch
 
 import fp8_rowwise_scaled_gb300 as fx
 from fp8_rowwise_scaled_gb300 import build as fxbuild
@@ -61,3 +62,43 @@ def test_no_contraction_outlasts_a_wait():
     assert f(P, P, 200, 200, 8, 1 << 26, 1 << 26, 0) == 4 * 200 * 8 * 4
     assert f(P, P, 200, 200, 8, 1 << 24, 1 << 24, 0) == 0
     assert f(P, P, 1, 1, 8, MOST, MOST, 0) == 64 * 8 * 4
+
+
+# addresses far from each other, which no call here follows
+X, W, DY, OUT, COUNTS = ((i + 1) << 40 for i in range(5))
+
+
+def test_products_over_their_inputs():
+    """A result that shares a byte with an element of an input is refused."""
+    kw = dict(total_M=8, G=2, N=64, K=64, ldx=64, x=X, w=W, m_sizes=COUNTS, out=OUT)
+    out = 2 * 8 * 64
+
+    def bad(fn, **more):
+        refused(fn, fx.MSLKB_ERR_SHAPE, {**kw, **more})
+    for t in (0, 1):
+        for at, nbytes in ((X, 8 * 64 * 2), (W, 2 * 64 * 64 * 2), (COUNTS, 16)):
+            for o in (at, at + nbytes - 2, at - out + 2):
+                bad(mm, out=o, transposed=t)
+    kw = dict(total_M=8, G=2, N=64, K=64, ldx=64, lddy=64, x=X, dy=DY, m_sizes=COUNTS, add=None)
+    for wide in (0, 1):
+        dw = 2 * 64 * 64 * (4 if wide else 2)
+        for at, nbytes in ((X, 8 * 64 * 2), (DY, 8 * 64 * 2), (COUNTS, 16)):
+            for o in (at, at + nbytes - 4, at - dw + 4):
+                bad(weight_grad, dw=o, dw_fp32=wide)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="these calls reach the device where there is one")
+def test_products_beside_their_inputs():
+    """Right before and behind them, and between strided rows: taken, as far as the missing device."""
+    other = mm(total_M=8, G=2, N=64, K=64, ldx=64, x=X, w=W, m_sizes=COUNTS, out=OUT)
+    assert other in (fx.MSLKB_ERR_DEVICE, fx.MSLKB_ERR_CUDA)
+    kw = dict(total_M=8, G=2, N=64, K=64, x=X, w=W, m_sizes=COUNTS)
+    out = 2 * 8 * 64
+    ld = 4096
+    refused(mm, other, {**kw, "ldx": 64, "out": X - out}, {**kw, "ldx": 64, "out": X + 2 * 8 * 64},
+            {**kw, "ldx": 64, "out": W - out}, {**kw, "ldx": 64, "out": W + 2 * 2 * 64 * 64},
+            {**kw, "ldx": 64, "out": COUNTS - out}, {**kw, "ldx": 64, "out": COUNTS + 16},
+            {**kw, "ldx": ld, "out": X + 128}, {**kw, "ldx": ld, "out": X + 2 * ld - out},
+            {**kw, "ldx": ld, "out": X + 2 * 7 * ld + 128})
+    refused(mm, fx.MSLKB_ERR_SHAPE, {**kw, "ldx": ld, "out": X + 126},
+            {**kw, "ldx": ld, "out": X + 2 * ld - out + 2}, {**kw, "ldx": ld, "out": X + 2 * 7 * ld})
