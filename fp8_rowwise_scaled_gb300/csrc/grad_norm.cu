@@ -611,8 +611,8 @@ cudaError_t run(const Args& a, const ClipArgs& c, int sms, void* stream) {
   return run_list<kInf, kMany>(a, c, sms, stream);
 }
 
-// Whether no result lies over another, or over a gradient other than its own.
-bool apart(const Args& a) {
+// Whether no result (the norm is one) lies over another, or over a gradient other than its own.
+bool apart(const Args& a, const float* norm) {
   struct Span {
     uintptr_t from, to;
     bool written;
@@ -630,9 +630,11 @@ bool apart(const Args& a) {
   auto before = [](const Span& x, const Span& y) { return x.from < y.from; };
   if (!std::is_sorted(spans.begin(), spans.end(), before))
     std::sort(spans.begin(), spans.end(), before);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
   uintptr_t any = 0, written = 0;   // ends of the spans so far, of those that are written
   for (const Span& s : spans) {
     if (s.from < (s.written ? any : written)) return false;
+    if (at < s.to && s.from < at + sizeof *norm) return false;
     any = std::max(any, s.to);
     if (s.written) written = std::max(written, s.to);
   }
@@ -664,7 +666,7 @@ mslkb_status run_checked(const Args& a, int32_t kind, float* norm, double max_no
   if (workspace == nullptr || !aligned_to(workspace, 16) ||
       workspace_bytes < mslkb_grad_norm_workspace_bytes(a.count))
     return MSLKB_ERR_WORKSPACE;
-  if (a.out != nullptr && !apart(a)) return MSLKB_ERR_SHAPE;
+  if (a.out != nullptr && !apart(a, norm)) return MSLKB_ERR_SHAPE;
   int sms = 0;
   const mslkb_status s = device_sms(&sms);
   if (s != MSLKB_OK) return s;

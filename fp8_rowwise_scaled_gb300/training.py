@@ -180,7 +180,7 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2.0, eps=1e-6, out=None, stream
 
     ``out`` is (norm, tensors of the gradients' types, shapes and strides); the tensors may be the
     gradients themselves, which are then scaled in place (and not written where nothing
-    changes), but must not overlap otherwise.  Without ``out`` new tensors are made."""
+    changes), but must not overlap otherwise, nor the norm lie over them.  Without ``out`` new tensors are made."""
     b = _binding()
     kind = _kind(norm_type)
     if out is None:

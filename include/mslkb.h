@@ -587,8 +587,8 @@ MSLKB_API mslkb_status mslkb_grad_norm(const void *const *grads, const int64_t *
  * each product rounded once to its tensor's type; norm is that of grads, as above, in fp32.  The
  * scale is NaN exactly if norm is; an infinite max_norm leaves gradients as they are even if norm
  * is infinite; a finite one scales them by 0 then (an infinite element becomes NaN).  outs[i] may
- * be grads[i] itself (left as it is where scale is 1); otherwise results must not lie over each
- * other or over gradients (MSLKB_ERR_SHAPE).  max_norm >= 0 (it may be infinite, and is if fp32
+ * be grads[i] itself (left as it is where scale is 1); otherwise results, norm among them, must not
+ * lie over each other or over gradients (MSLKB_ERR_SHAPE).  max_norm >= 0 (it may be infinite, and is if fp32
  * does not hold it), eps >= 0.
  */
 MSLKB_API mslkb_status mslkb_clip_grad_norm(const void *const *grads, void *const *outs,

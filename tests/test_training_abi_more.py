@@ -6,7 +6,7 @@ import torch
 import fp8_rowwise_scaled_gb300 as fx
 from fp8_rowwise_scaled_gb300 import build as fxbuild
 from test_moe_abi import P, refused
-from test_training_abi import mm, weight_grad
+from test_training_abi import GRADS, OUTS, clip, mm, weight_grad
 
 MOST = 1 << 30
 
@@ -102,3 +102,10 @@ def test_products_beside_their_inputs():
             {**kw, "ldx": ld, "out": X + 2 * 7 * ld + 128})
     refused(mm, fx.MSLKB_ERR_SHAPE, {**kw, "ldx": ld, "out": X + 126},
             {**kw, "ldx": ld, "out": X + 2 * ld - out + 2}, {**kw, "ldx": ld, "out": X + 2 * 7 * ld})
+
+
+def test_norm_over_a_list():
+    """The clipping's norm inside a gradient (10 bf16 at 256, 100 fp32 at 4096) or a result."""
+    for at in (256, 272, 4096, 4492, 16384, 16400, 32768, 33164):
+        refused(clip, fx.MSLKB_ERR_SHAPE, {"norm": at})
+        refused(clip, fx.MSLKB_ERR_SHAPE, {"norm": at, "outs": GRADS if at < 8192 else OUTS})
