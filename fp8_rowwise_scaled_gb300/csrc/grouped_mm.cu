@@ -361,6 +361,7 @@ mslkb_status mslkb_grouped_mm(const void* x, const void* w, const int64_t* m_siz
   p.out = out;
   p.status = h.status;
   p.timeout_ns = h.timeout_ns;
+  p.test_stall = h.test_stall;
   p.total = static_cast<int32_t>(total_M);
   p.G = static_cast<int32_t>(G);
   p.C = static_cast<int32_t>(N);
@@ -431,6 +432,7 @@ mslkb_status mslkb_grouped_mm_weight_grad(const void* dy, const void* x, const i
   p.add = add;
   p.status = h.status;
   p.timeout_ns = h.timeout_ns;
+  p.test_stall = h.test_stall;
   p.total = static_cast<int32_t>(total_M);
   p.G = static_cast<int32_t>(G);
   p.C = static_cast<int32_t>(K);

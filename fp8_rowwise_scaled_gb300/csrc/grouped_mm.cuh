@@ -67,6 +67,7 @@ struct MmParams {
   int32_t splits;          // parts of each contraction, whose sums go to slices of out (fp32)
   int64_t slice;           // elements from slice to slice
   int32_t sums;            // 0: the contraction is empty everywhere, and P and Q are not read
+  int32_t test_stall;      // test hook: the first pair withholds its first stage
 };
 
 // Tensor maps.  p, q: the operands, by boxes of a CTA's share of a stage; q64: by halves of
@@ -558,6 +559,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // (test hook: neither CTA arrives or loads, so that the wait for this stage runs out)
+      bool withhold = p.test_stall != 0 && worker == 0;
       MmTile taken;
       for (int32_t i = 0; ok && take(i, taken, true); ++i) {
         // (the same in every lane, which the compiler is told)
@@ -576,7 +579,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           ok = __all_sync(0xffffffffu, wait_bar(empty_bar(stage), phase ^ 1u, abort_flag,
                                                 p.status, p.timeout_ns)) != 0;
           if (!ok) break;
-          if (issuer) {
+          if (issuer && !withhold) {
             // the bytes of both CTAs (as many in each) complete on the leader's barrier.  A stage
             // that ends between two MMA steps (kGrad) passes through the edge warp of each CTA
             // first.
@@ -625,6 +628,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               load2(dq, half ? &maps.q64 : &maps.q, x, row);
             }
           }
+          withhold = false;
           if (++stage == Cfg::kStages) {
             stage = 0;
             phase ^= 1u;

@@ -18,11 +18,13 @@ void record_cuda_error(cudaError_t e);
 // Checks the current device (MSLKB_ERR_DEVICE unless sm_103) and returns its SM count.
 mslkb_status device_sms(int* sm_count);
 
-// What a tensor-core launch needs of the current device, checked as device_sms does.
+// What a tensor-core launch needs of the current device, checked as device_sms does, and of the
+// process (a test's request to stall the next launch is taken up by this).
 struct DeviceHandles {
   int sms;
   uint32_t* status;      // the device status word
   uint64_t timeout_ns;   // give-up time of one pipeline wait
+  int32_t test_stall;    // 1: the launch's first CTAs withhold a stage
 };
 mslkb_status device_handles(DeviceHandles* h);
 

@@ -811,6 +811,7 @@ mslkb_status device_handles(DeviceHandles* h) {
   h->sms = st->sm_count;
   h->status = st->status_ptr;
   h->timeout_ns = g_wait_timeout_ns.load();
+  h->test_stall = g_test_stall.exchange(0);
   return MSLKB_OK;
 }
 

@@ -79,7 +79,7 @@ MSLKB_API mslkb_status mslkb_set_weight_prefetch(int32_t kblocks);
 MSLKB_API mslkb_status mslkb_test_speculate_from_next_launch(const void* meta);
 
 /*
- * Test hook for failure detection: the next launch, through any entry point, has its
+ * Test hook for failure detection: the next launch of a product, through any entry point, has its
  * first CTA (both CTAs of its first pair, on CTA-pair kernels) withhold one pipeline stage,
  * so that a wait of that CTA runs out after the limit set by mslkb_set_wait_timeout_us and
  * the kernel's abort path runs.  That launch's output is incomplete and the status word
