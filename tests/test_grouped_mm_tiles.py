@@ -212,3 +212,17 @@ def test_weight_grad_in_parts(counts, grad, dtype):
     for add in (None, before):
         dw = fx.grouped_mm_weight_grad(dy, x, sizes(counts), add=add, dtype=grad)
         check_grad(dw, dy, x, counts, add)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("n,k", [(1000, 1160), (1001, 2100), (4104, 1032)])
+def test_few_rows_of_many_experts(n, k, transposed, dtype):
+    """Tiles narrower than others, and contractions longer than the tensor core's sums."""
+    counts = [1, 3, 0, 2, 40] * 12
+    x, w = operands(counts, n, k, transposed, dtype, spare=3)
+    out = torch.full((sum(counts) + 3, n), 7.0, dtype=dtype, device="cuda")
+    assert split_of(x, w, counts, n, k, transposed) == 0
+    fx.grouped_mm(x, w, sizes(counts), transposed=transposed, out=out)
+    check_mm(out, x, w, counts, transposed)
+    assert (out[sum(counts):] == 7.0).all()
