@@ -3,8 +3,8 @@
     python -m fp8_rowwise_scaled_gb300.build [--force] [--ptxas-verbose] [--checked]
 
 --checked builds libmslkb_checked.so instead: the same sources compiled with MSLKB_CHECKED,
-whose kernels test every global access against the extents of the call's buffers and
-report an index outside them in the device status word (MSLKB_DEV_BOUNDS) instead of
+whose FP8 product kernels (kernel.cuh) test every global access against the extents of the call's
+buffers and report an index outside them in the device status word (MSLKB_DEV_BOUNDS) instead of
 making the access.  A test build (the stand-in for a memory checker); slower.
 
 Each translation unit in csrc/ compiles in parallel to _build/*.o, then nvcc links them

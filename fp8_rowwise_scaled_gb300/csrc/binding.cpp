@@ -1,12 +1,13 @@
 // binding.cpp -- the Python extension _binding: checks the torch tensors of a call of the
-// operators around the grouped product and passes their addresses to libmslkb.so.  A call of
-// one token takes 3 us on the device; the checks take about 0.1 us here (with Python code and
-// ctypes they took 5).  Nothing is computed here, and nothing allocated but the scratch of the
-// norm's gradient.
+// operators around the grouped product, and of those for training, and passes their addresses to
+// libmslkb.so.  A call of one token takes 3 us on the device; the checks take about 0.1 us here
+// (with Python code and ctypes they took 5).  Nothing is computed here, and nothing allocated but
+// a call's scratch: of the norm's gradient, the 16-bit products and the gradients' norm.
 //
-// Every function takes positional arguments only (moe.py names them) and returns the
-// mslkb_status, or kNoColumns; wrong tensors raise TypeError or ValueError.  `out` is the tuple
-// of results, `stream` None (the current stream) or a cudaStream_t as an integer.
+// Every function takes positional arguments only (moe.py and training.py name them) and returns
+// the mslkb_status, or kNoColumns; wrong tensors raise TypeError or ValueError.  `out` is the
+// tuple of results, or the result of a function that has one (the clipping's: its list), `stream`
+// None (the current stream) or a cudaStream_t as an integer.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

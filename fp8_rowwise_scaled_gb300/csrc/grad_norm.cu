@@ -305,7 +305,9 @@ __device__ __forceinline__ void scale_chunks(const L& l, uint32_t r, uint32_t of
       using T = decltype(t);
       share_out<kStep, T>(n, turn, [&](auto step, int tid) {
         constexpr int kBy = decltype(step)::value;
-        constexpr int kBatch = kBy < kStep ? 4 : kBatchOf<kBy>;   // (as many as registers hold)
+        // (a warp beside others of its CTA: four vectors, not eight; of clip_kernel, which has 64
+        // registers a thread, 112 bytes spill even so)
+        constexpr int kBatch = kBy < kStep ? 4 : kBatchOf<kBy>;
         scale_run<kBy, kBatch>(static_cast<const T*>(g.in) + e0, static_cast<T*>(g.out) + e0, n, f,
                                tid);
       });

@@ -102,7 +102,7 @@ struct MmCfg {
   static constexpr int kTileWarp = 3;  // hands out the tiles
   // kGrad with something to add: that comes by TMA too, in slots of 8 KB, through a ring of its own
   // for each four of the epilogue's warps (32 experts of 75 rows, 4096 x 7168 on GB300: 1120 us
-  // fp32, 706 bf16; loaded by the epilogue's threads themselves, a chunk ahead, 1541 and 1031).
+  // fp32, 710 bf16; loaded by the epilogue's threads themselves, a chunk ahead, 1541 and 1031).
   // Bound by what is on its way: fp32 with four stages and four slots each 1330, three and seven
   // 1120, two and nine 1180; bf16, whose tiles take half as long, four and four 706, three and
   // six 750.  (One warp loads for both rings, in the order of the tiles: one each 1122 and 737.)
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // Round n goes over the workers from the n-th on, so that a worker does not get the same row
       // tile of every column: those of fewer rows take less time, and workers that get ahead of
       // others read the weights from memory instead of sharing them in L2 (32 experts of 480 rows,
-      // 4096 x 7168 on GB300: 673 us without the turn, 594 with it).  32 tiles are worked out at a
+      // 4096 x 7168 on GB300: 630 us without the turn, 558 with it).  32 tiles are worked out at a
       // time, one by each lane (a search and up to four divisions), and handed on one by one.
       const int32_t part = mm_schedule<Cfg>(p, first, tile_pre, lane);   // of a split product
       const int32_t tiles = part * p.splits;

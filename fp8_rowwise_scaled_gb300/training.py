@@ -8,6 +8,10 @@ follows the backward pass.
 As in moe.py, whose conventions hold here too: ``mslkb_*`` functions mirror the C entry points,
 the others take torch CUDA tensors, run on the current stream or on ``stream``, and put their
 results into ``out`` where it is given.
+
+As there, autograd sees none of it: a result of inputs that require a gradient is detached, and
+what is written in place (``out`` over a gradient, or over ``add``) does not raise the tensor's
+version.  A backward pass calls the gradients' functions itself.
 """
 from __future__ import annotations
 
